@@ -284,6 +284,109 @@ int mla_absorb_q(const void* q, const void* w_uk_t, void* q_out, int T, int H, i
 int mla_v_up_proj(const void* attn_out, const void* w_uv, void* out, int T, int H, int V, void* workspace,
                   size_t workspace_bytes, void* stream);
 
+/* ---- Paged 8-bit K/V cache: layers with separate K and V heads.
+ *
+ * The caches are uint8 [NB, HK, 64, D] of float8_e4m3 codes (D = 64 or 128),
+ * 16-byte aligned, one for K and one for V, with one float32 scale per block
+ * of 64 tokens and head, [NB, HK] each; value = code * scale.  They are paged
+ * through block tables like the latent caches above: int32 [R, MB], a row per
+ * request.  A batch is ragged: request r's new tokens are rows
+ * query_start[r] .. query_start[r + 1] - 1 of its token arrays
+ * (query_start int32 [R + 1], non-decreasing), and they are the last of its
+ * seq_lens[r] tokens: row t has position seq_lens[r] - query_start[r + 1] + t.
+ * Rows before query_start[0] or from query_start[R] on belong to no request:
+ * they are not read, and their results are left as they were, so a batch
+ * padded to a fixed T can be captured into a CUDA graph.
+ * At most 8192 requests per call (SMLA_ERR_UNSUPPORTED beyond); NB * HK * 64
+ * must fit in int32.  No kernel of these calls starts before the preceding
+ * work on `stream` has completed. */
+
+/* Block tables, slot maps and positions of a batch from its requests' lengths.
+ * Request r has context_lens[r] tokens cached (negative counts as 0) in the
+ * first ceil(context_lens[r] / 64) blocks of its table row and brings
+ * query_lens[r] new ones.  The blocks that these need are taken from a stack
+ * of free block ids, free_blocks[0 .. free_count - 1], top first, in the order
+ * of requests and blocks.
+ *   context_lens, query_lens int32 [R]; free_blocks int32 [F]; free_count int32 [1]
+ *   block_table      int32 [R, MB]  new entries written, others left as they were
+ *   query_start      int32 [R + 1]  first token of each request; the last: their number.  At most T
+ *   seq_lens         int32 [R]      context_lens + query_lens (saturating)
+ *   req_id_per_token int32 [T]      request of each token; -1 behind the last
+ *   positions        int32 [T]      position in its request; 0 behind the last
+ *   slot_mapping     int64 [T]      cache slot (block * 64 + offset); -1 behind the last, beyond MB
+ *                                   blocks, and where the table has no block inside [0, NB)
+ *   free_count_out   int32 [1]      blocks left on the stack
+ *   missing          int32 [1]      blocks that the stack did not have; their entries are -1
+ * All written.  seq_lens may be context_lens or query_lens, free_count_out may be free_count. */
+int paged_blocks_extend(const int32_t* context_lens, const int32_t* query_lens, int32_t* block_table,
+                        const int32_t* free_blocks, const int32_t* free_count, int32_t* query_start,
+                        int32_t* seq_lens, int32_t* req_id_per_token, int32_t* positions, int64_t* slot_mapping,
+                        int32_t* free_count_out, int32_t* missing, int R, int MB, int NB, int F, int T, void* stream);
+
+/* The blocks of the requests with release[r] != 0 (uint8 [R]) back on the
+ * stack: the entries inside [0, NB) of the first ceil(seq_lens[r] / 64) of
+ * their table rows are pushed in order (beyond F entries: dropped), and
+ *   context_lens   int32 [R]  0 for them, seq_lens for the others (written)
+ *   free_count_out int32 [1]  blocks on the stack (written)
+ * The table is left as it is.  A block belongs to one request: one that two
+ * released rows hold is pushed twice.  context_lens may be seq_lens and
+ * free_count_out may be free_count. */
+int paged_blocks_release(const uint8_t* release, const int32_t* seq_lens, const int32_t* block_table,
+                         int32_t* free_blocks, const int32_t* free_count, int32_t* context_lens,
+                         int32_t* free_count_out, int R, int MB, int NB, int F, void* stream);
+
+/* Quantize-and-store of a batch's new K and V rows into the paged caches.
+ *   k, v   bf16 [T, HK, D], tokens k_stride (v_stride) elements apart (at least HK * D, a multiple of
+ *          8), 16-byte aligned: slices of a fused projection's output can be given as they are
+ *   query_start, seq_lens, block_table: the batch, as above
+ *   k_cache, v_cache, k_scale, v_scale: written, as above
+ * Scale of a block and head: the smallest power of two 2^E, E >= -100, with
+ * amax <= 448 * 2^E over the call's rows of the block (infinities left out).
+ * A block whose first row is stored by the call takes it; one that holds
+ * earlier rows takes the larger of its own and this, and where its own was
+ * smaller its earlier rows' codes become e4m3(code * old / new).  Codes are
+ * x / scale rounded to the nearest e4m3 (ties to even), saturating; a NaN is
+ * stored as 0.  Rows behind the last are left as they were.  A row whose block is
+ * outside [0, NB) or beyond MB is skipped, as is a request with fewer tokens
+ * (seq_lens) than new rows.  A block belongs to one request. */
+int kv_cache_store_fp8(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* query_start,
+                       const int32_t* seq_lens, const int32_t* block_table, uint8_t* k_cache, uint8_t* v_cache,
+                       float* k_scale, float* v_scale, int T, int HK, int D, int R, int MB, int NB, void* stream);
+
+/* Attention of a batch over the paged caches, with H = G * HK query heads
+ * (1 <= G <= 128; head h reads K/V head h / G).
+ *   q       bf16 [T, H, D], tokens q_stride elements apart (at least H * D, a multiple of 8), 16-byte aligned
+ *   out     bf16 [T, H, D], 16-byte aligned; lse fp32 [T, H] (written for the batch's rows)
+ * Token t at position p of request r sees the keys lo <= j < hi of the request:
+ *   hi = min(seq_lens[r], max(p + 1, prefix_lens[r])), without prefix_lens min(seq_lens[r], p + 1):
+ *        causal, but for a prefix that every token sees (prefix_lens = seq_lens: no causal mask)
+ *   lo = max(0, p - window + 1 if window > 0, doc_start[t] if given): a sliding window, and the first
+ *        position of the token's document
+ * with the logits x = sm_scale * q.k, then x = softcap * tanh(x / softcap) if
+ * softcap > 0, then x -= alibi_slopes[h] * |p - j| if given.  A key whose block is
+ * outside [0, NB) or beyond MB is not seen.  A token that sees no key gets out = 0
+ * and lse = -inf.
+ *   alibi_slopes fp32 [H], prefix_lens int32 [R], doc_start int32 [T]: each may be NULL
+ *   max_query_len  an estimate of the most new tokens of a request, for the choice of the work split;
+ *                  any value gives right results
+ * Keys that a token does not see do not reach its result whatever their bytes
+ * and scales hold, with one exception: a NaN code (which kv_cache_store_fp8
+ * never writes) or a NaN or infinite scale at a position that another token of the
+ * same request sees.  The codes enter both products as stored, q as two e4m3
+ * terms (exact but for components below 2^-10 of their row's largest), the
+ * weights as an e4m3 and an e5m2 term (about 8 significant bits); sums in
+ * float32.
+ *   workspace  at least paged_attention_fp8_workspace_bytes(...) bytes, 256-byte aligned; NULL = library-cached */
+int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+                        const float* k_scale, const float* v_scale, const int32_t* block_table,
+                        const int32_t* seq_lens, const int32_t* query_start, float sm_scale, int max_query_len,
+                        int window, float softcap, const float* alibi_slopes, const int32_t* prefix_lens,
+                        const int32_t* doc_start, void* out, float* lse, int T, int H, int HK, int D, int R, int MB,
+                        int NB, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes paged_attention_fp8 needs on the current device (0 for sizes it rejects). */
+size_t paged_attention_fp8_workspace_bytes(int T, int H, int HK, int D, int R, int max_query_len);
+
 /* Reads (and clears) the device status word of a workspace after
  * synchronizing `stream`: 0 = no fault; 1 = a kernel wait ran past its time
  * limit and the kernel unwound (its outputs are not valid).  workspace NULL =

@@ -12,14 +12,19 @@ Entry points (see include/smla.h for layouts and semantics):
   (sparse_mla_prefill_fp8 with its steps sparse_mla_gather_upconvert_fp8 and
   sparse_mla_translate_indices_workspace, and the host-side
   sparse_mla_prefill_chunks), plus workspace-size and status helpers.
+The paged 8-bit K/V cache of layers with separate K and V heads:
+  paged_blocks_extend and paged_blocks_release (block tables and slot maps
+  from request lengths), kv_cache_store_fp8, paged_attention_fp8.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import subprocess
 import threading
 from concurrent.futures import ThreadPoolExecutor
+from typing import Any, NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
@@ -28,7 +33,8 @@ _BUILD = os.path.join(_PKG, "_build")
 LIB_PATH = os.path.join(_PKG, "libsmla.so")
 HEADER = os.path.join(_ROOT, "include", "smla.h")
 
-SOURCES = ["smla_decode.cu", "smla_attn.cu", "smla_wide.cu", "smla_wide8.cu", "smla_store.cu", "smla_nvfp4.cu", "smla_absorb.cu", "smla_api.cu"]
+SOURCES = ["smla_decode.cu", "smla_attn.cu", "smla_wide.cu", "smla_wide8.cu", "smla_store.cu", "smla_nvfp4.cu", "smla_absorb.cu",
+           "smla_blocks.cu", "smla_kvstore.cu", "smla_paged_attn.cu", "smla_api.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17", "-lineinfo",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 
@@ -134,6 +140,18 @@ def lib():
             L.mla_absorb_q.restype = i32
             L.mla_v_up_proj.argtypes = [P, P, P, i32, i32, i32, P, sz, P]
             L.mla_v_up_proj.restype = i32
+            L.paged_blocks_extend.argtypes = [P] * 12 + [i32] * 5 + [P]
+            L.paged_blocks_extend.restype = i32
+            L.paged_blocks_release.argtypes = [P] * 7 + [i32] * 4 + [P]
+            L.paged_blocks_release.restype = i32
+            i64 = ctypes.c_int64
+            L.kv_cache_store_fp8.argtypes = [P, i64, P, i64, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, P]
+            L.kv_cache_store_fp8.restype = i32
+            L.paged_attention_fp8.argtypes = [P, i64, P, P, P, P, P, P, P, f32, i32, i32, f32, P, P, P, P, P,
+                                              i32, i32, i32, i32, i32, i32, i32, P, sz, P]
+            L.paged_attention_fp8.restype = i32
+            L.paged_attention_fp8_workspace_bytes.argtypes = [i32] * 6
+            L.paged_attention_fp8_workspace_bytes.restype = sz
             L.smla_read_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_int), P]
             L.smla_read_noalloc_status.restype = i32
             L.smla_last_error.argtypes = []
@@ -494,6 +512,208 @@ def sparse_mla_translate_indices(indices, block_table, req_id_per_token, num_blo
                                             T, K, R, MB, int(num_blocks), _stream_ptr(stream, dev))
     _check(rc, "sparse_mla_translate_indices")
     return out
+
+
+# ---- paged 8-bit K/V cache
+
+class PagedBatch(NamedTuple):
+    """What paged_blocks_extend makes of a batch's lengths."""
+    query_start: Any       # int32 [R + 1]
+    seq_lens: Any          # int32 [R]
+    req_id_per_token: Any  # int32 [T]
+    positions: Any         # int32 [T]
+    slot_mapping: Any      # int64 [T]
+    free_count: Any        # int32 [1]
+    missing: Any           # int32 [1]
+
+
+@contextlib.contextmanager
+def _on(dev, stream):
+    """The tensors' device current (calls launch on the current device) and,
+    where the caller names a stream, that stream, so that what a call allocates
+    belongs to it."""
+    import torch
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield torch.cuda.current_stream(dev)
+        else:
+            with torch.cuda.stream(stream):
+                yield stream
+
+
+def _rows(t, heads, D, name):
+    """Checks [T, heads, D] bf16 rows that may be slices of longer ones; their
+    distance in elements."""
+    import torch
+    if not t.is_cuda:
+        raise SmlaError("all tensors must be CUDA tensors (there is no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise SmlaError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise SmlaError(f"{name}: shape {tuple(t.shape)}, expected (T, {heads}, {D})")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+        raise SmlaError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+def paged_blocks_extend(context_lens, query_lens, block_table, free_blocks, free_count, num_tokens: int,
+                        num_blocks: int, out=None, stream=None):
+    """Block tables, slot maps and positions of a batch from its requests'
+    lengths (int32 [R] each): the blocks that the new tokens need are taken
+    from the stack free_blocks[:free_count] (int32 [F], [1]) into block_table
+    (int32 [R, MB], modified in place).  num_tokens: rows of the batch, at
+    least the new tokens' number; num_blocks: blocks of the cache.  Returns a
+    PagedBatch (`out`, if given; its seq_lens may be context_lens and its
+    free_count the argument, which are then updated)."""
+    import torch
+    dev = _dev(context_lens, query_lens, block_table, free_blocks, free_count, *(out or ()))
+    R, MB = block_table.shape
+    F, T = free_blocks.numel(), int(num_tokens)
+    i32 = torch.int32
+    _expect(context_lens, i32, (R,), "context_lens")
+    _expect(query_lens, i32, (R,), "query_lens")
+    _expect(block_table, i32, (R, MB), "block_table")
+    _expect(free_blocks, i32, (F,), "free_blocks")
+    _expect(free_count, i32, (1,), "free_count")
+    with _on(dev, stream) as on:
+        if out is None:
+            n = max(T, 0)
+            start, lens, req, pos, left, lack = torch.empty(2 * R + 2 * n + 3, dtype=i32, device=dev).split(
+                [R + 1, R, n, n, 1, 1])
+            out = PagedBatch(start, lens, req, pos, torch.empty(n, dtype=torch.int64, device=dev), left, lack)
+        else:
+            out = PagedBatch(*out)
+            for name, shape in (("query_start", R + 1), ("seq_lens", R), ("req_id_per_token", T), ("positions", T),
+                                ("free_count", 1), ("missing", 1)):
+                _expect(getattr(out, name), i32, (shape,), name)
+            _expect(out.slot_mapping, torch.int64, (T,), "slot_mapping")
+        rc = lib().paged_blocks_extend(
+            _ptr(context_lens), _ptr(query_lens), _ptr(block_table), _ptr(free_blocks), _ptr(free_count),
+            _ptr(out.query_start), _ptr(out.seq_lens), _ptr(out.req_id_per_token), _ptr(out.positions),
+            _ptr(out.slot_mapping), _ptr(out.free_count), _ptr(out.missing), R, MB, int(num_blocks), F, T,
+            ctypes.c_void_p(on.cuda_stream))
+    _check(rc, "paged_blocks_extend")
+    return out
+
+
+def paged_blocks_release(release, seq_lens, block_table, free_blocks, free_count, num_blocks: int, context_lens=None,
+                         free_count_out=None, stream=None):
+    """The blocks of the requests with release set (bool or uint8 [R]) back on
+    the stack (free_blocks modified in place).  Returns (context_lens int32
+    [R]: 0 for them, seq_lens for the others; free_count int32 [1]); both may
+    be written over the arguments of those meanings."""
+    import torch
+    dev = _dev(release, seq_lens, block_table, free_blocks, free_count, context_lens, free_count_out)
+    R, MB = block_table.shape
+    F = free_blocks.numel()
+    if release.dtype not in (torch.bool, torch.uint8):
+        raise SmlaError(f"release: dtype {release.dtype}, expected bool or uint8")
+    _expect(release, release.dtype, (R,), "release")
+    _expect(seq_lens, torch.int32, (R,), "seq_lens")
+    _expect(block_table, torch.int32, (R, MB), "block_table")
+    _expect(free_blocks, torch.int32, (F,), "free_blocks")
+    _expect(free_count, torch.int32, (1,), "free_count")
+    with _on(dev, stream) as on:
+        if context_lens is None:
+            context_lens = torch.empty(R, dtype=torch.int32, device=dev)
+        if free_count_out is None:
+            free_count_out = torch.empty(1, dtype=torch.int32, device=dev)
+        _expect(context_lens, torch.int32, (R,), "context_lens")
+        _expect(free_count_out, torch.int32, (1,), "free_count_out")
+        rc = lib().paged_blocks_release(_ptr(release), _ptr(seq_lens), _ptr(block_table), _ptr(free_blocks),
+                                        _ptr(free_count), _ptr(context_lens), _ptr(free_count_out), R, MB,
+                                        int(num_blocks), F, ctypes.c_void_p(on.cuda_stream))
+    _check(rc, "paged_blocks_release")
+    return context_lens, free_count_out
+
+
+def _paged_cache(k_cache, v_cache, k_scale, v_scale):
+    import torch
+    if k_cache.dim() != 4 or k_cache.shape[2] != 64:
+        raise SmlaError(f"k_cache: shape {tuple(k_cache.shape)}, expected (NB, HK, 64, D)")
+    NB, HK, _, D = k_cache.shape
+    _expect(k_cache, torch.uint8, (NB, HK, 64, D), "k_cache")
+    _expect(v_cache, torch.uint8, (NB, HK, 64, D), "v_cache")
+    _expect(k_scale, torch.float32, (NB, HK), "k_scale")
+    _expect(v_scale, torch.float32, (NB, HK), "v_scale")
+    return NB, HK, D
+
+
+def kv_cache_store_fp8(k, v, query_start, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale, stream=None):
+    """Quantize a batch's new K and V rows (bf16 [T,HK,D], slices of longer
+    rows allowed) into the paged e4m3 caches (uint8 [NB,HK,64,D], scales fp32
+    [NB,HK]), modified in place.  query_start int32 [R+1], seq_lens int32 [R],
+    block_table int32 [R,MB]."""
+    import torch
+    dev = _dev(query_start, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale)
+    NB, HK, D = _paged_cache(k_cache, v_cache, k_scale, v_scale)
+    R, MB = block_table.shape
+    T = k.shape[0]
+    ks, vs = _rows(k, HK, D, "k"), _rows(v, HK, D, "v")
+    if v.shape[0] != T or k.device != dev or v.device != dev:
+        raise SmlaError("k and v must have the same tokens, on the device of the cache")
+    _expect(query_start, torch.int32, (R + 1,), "query_start")
+    _expect(seq_lens, torch.int32, (R,), "seq_lens")
+    _expect(block_table, torch.int32, (R, MB), "block_table")
+    with _on(dev, stream) as on:
+        rc = lib().kv_cache_store_fp8(_ptr(k), ks, _ptr(v), vs, _ptr(query_start), _ptr(seq_lens), _ptr(block_table),
+                                      _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), T, HK, D, R, MB, NB,
+                                      ctypes.c_void_p(on.cuda_stream))
+    _check(rc, "kv_cache_store_fp8")
+    return k_cache, v_cache, k_scale, v_scale
+
+
+def paged_attention_fp8_workspace_bytes(T: int, H: int, HK: int, D: int, R: int, max_query_len: int) -> int:
+    return int(lib().paged_attention_fp8_workspace_bytes(T, H, HK, D, R, max_query_len))
+
+
+def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start, sm_scale: float,
+                        max_query_len=None, window: int = 0, softcap: float = 0.0, alibi_slopes=None,
+                        prefix_lens=None, doc_start=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of a ragged batch over the paged e4m3 caches.  q bf16 [T,H,D]
+    (slices of longer rows allowed); the cache as for kv_cache_store_fp8;
+    causal, with a sliding window, capped scores, distance biases (fp32 [H]), a
+    prefix that all tokens of a request see (int32 [R]) and documents (int32
+    [T]: first position of the token's document) as asked.  max_query_len: an
+    estimate of the most new tokens of a request (default: T - R + 1).  The
+    workspace, if none is given, is allocated for the call.  Returns (out bf16
+    [T,H,D], lse fp32 [T,H]); rows of no request are left as they were."""
+    import torch
+    dev = _dev(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start, alibi_slopes, prefix_lens,
+               doc_start, out, lse, workspace)
+    NB, HK, D = _paged_cache(k_cache, v_cache, k_scale, v_scale)
+    R, MB = block_table.shape
+    T, H = q.shape[0], q.shape[1]
+    stride = _rows(q, H, D, "q")
+    if q.device != dev:
+        raise SmlaError("all tensors must be on the same device")
+    _expect(block_table, torch.int32, (R, MB), "block_table")
+    _expect(seq_lens, torch.int32, (R,), "seq_lens")
+    _expect(query_start, torch.int32, (R + 1,), "query_start")
+    if alibi_slopes is not None:
+        _expect(alibi_slopes, torch.float32, (H,), "alibi_slopes")
+    if prefix_lens is not None:
+        _expect(prefix_lens, torch.int32, (R,), "prefix_lens")
+    if doc_start is not None:
+        _expect(doc_start, torch.int32, (T,), "doc_start")
+    longest = max(1, T - R + 1) if max_query_len is None else int(max_query_len)
+    with _on(dev, stream) as on:
+        if out is None:
+            out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        _expect(out, torch.bfloat16, (T, H, D), "out")
+        _expect(lse, torch.float32, (T, H), "lse")
+        if workspace is None:
+            workspace = torch.empty(paged_attention_fp8_workspace_bytes(T, H, HK, D, R, longest), dtype=torch.uint8,
+                                    device=dev)
+        rc = lib().paged_attention_fp8(
+            _ptr(q), stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+            _ptr(seq_lens), _ptr(query_start), float(sm_scale), longest, int(window), float(softcap),
+            _ptr(alibi_slopes), _ptr(prefix_lens), _ptr(doc_start), _ptr(out), _ptr(lse), T, H, HK, D, R, MB, NB,
+            _ptr(workspace), workspace.numel() * workspace.element_size(), ctypes.c_void_p(on.cuda_stream))
+    _check(rc, "paged_attention_fp8")
+    return out, lse
 
 
 def read_noalloc_status(stream=None) -> int:

@@ -666,6 +666,159 @@ int smla_read_noalloc_status(int* status_out, void* stream) {
   return smla_read_device_status(scratch, status_out, stream);
 }
 
+// ---- paged K/V cache
+
+namespace {
+int check_batch(int T, int R, int MB, int NB) {
+  if (T < 0 || R < 0 || MB <= 0 || NB <= 0)
+    return fail(SMLA_ERR_INVALID_ARG, "bad sizes T=%d R=%d MB=%d NB=%d", T, R, MB, NB);
+  if (R > smla::kMaxPagedRequests)
+    return fail(SMLA_ERR_UNSUPPORTED, "R=%d unsupported: at most %d requests", R, smla::kMaxPagedRequests);
+  if ((int64_t)NB * 64 > INT32_MAX || MB > (1 << 25))
+    return fail(SMLA_ERR_UNSUPPORTED, "NB*64 must fit in int32 and MB be at most 2^25");
+  return SMLA_OK;
+}
+int check_kv_heads(int HK, int D, int NB) {
+  if (HK <= 0) return fail(SMLA_ERR_INVALID_ARG, "bad size HK=%d", HK);
+  if (D != 64 && D != 128) return fail(SMLA_ERR_UNSUPPORTED, "D=%d unsupported: must be 64 or 128", D);
+  if ((int64_t)NB * HK * 64 > INT32_MAX) return fail(SMLA_ERR_UNSUPPORTED, "NB*HK*64 must fit in int32");
+  return SMLA_OK;
+}
+int check_rows(const char* name, const void* p, int64_t stride, int64_t least) {
+  if (!p) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(p)) return fail(SMLA_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (stride < least || stride % 8 != 0)
+    return fail(SMLA_ERR_INVALID_ARG, "%s: stride %lld must be at least %lld and a multiple of 8", name,
+                (long long)stride, (long long)least);
+  return SMLA_OK;
+}
+}  // namespace
+
+int paged_blocks_extend(const int32_t* context_lens, const int32_t* query_lens, int32_t* block_table,
+                        const int32_t* free_blocks, const int32_t* free_count, int32_t* query_start,
+                        int32_t* seq_lens, int32_t* req_id_per_token, int32_t* positions, int64_t* slot_mapping,
+                        int32_t* free_count_out, int32_t* missing, int R, int MB, int NB, int F, int T, void* stream) {
+  int rc = check_batch(T, R, MB, NB);
+  if (rc != SMLA_OK) return rc;
+  if (F < 0) return fail(SMLA_ERR_INVALID_ARG, "bad size F=%d", F);
+  if ((R > 0 && (!context_lens || !query_lens || !block_table || !seq_lens)) || (F > 0 && !free_blocks) ||
+      !free_count || !query_start || !free_count_out || !missing ||
+      (T > 0 && (!req_id_per_token || !positions || !slot_mapping)))
+    return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+  smla::BlocksExtendArgs a{context_lens, query_lens, block_table, free_blocks,    free_count, query_start,
+                           seq_lens,     req_id_per_token, positions, slot_mapping, free_count_out, missing,
+                           R,            MB,         F,           T,              NB};
+  cudaError_t e = smla::launch_blocks_extend(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_blocks_extend launch");
+  return SMLA_OK;
+}
+
+int paged_blocks_release(const uint8_t* release, const int32_t* seq_lens, const int32_t* block_table,
+                         int32_t* free_blocks, const int32_t* free_count, int32_t* context_lens,
+                         int32_t* free_count_out, int R, int MB, int NB, int F, void* stream) {
+  int rc = check_batch(0, R, MB, NB);
+  if (rc != SMLA_OK) return rc;
+  if (F < 0) return fail(SMLA_ERR_INVALID_ARG, "bad size F=%d", F);
+  if ((R > 0 && (!release || !seq_lens || !block_table || !context_lens)) || (F > 0 && !free_blocks) || !free_count ||
+      !free_count_out)
+    return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+  smla::BlocksReleaseArgs a{release, seq_lens, block_table, free_blocks, free_count, context_lens, free_count_out,
+                            R,       MB,       F,           NB};
+  cudaError_t e = smla::launch_blocks_release(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_blocks_release launch");
+  return SMLA_OK;
+}
+
+int kv_cache_store_fp8(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* query_start,
+                       const int32_t* seq_lens, const int32_t* block_table, uint8_t* k_cache, uint8_t* v_cache,
+                       float* k_scale, float* v_scale, int T, int HK, int D, int R, int MB, int NB, void* stream) {
+  int rc = check_batch(T, R, MB, NB);
+  if (rc == SMLA_OK) rc = check_kv_heads(HK, D, NB);
+  if (rc != SMLA_OK) return rc;
+  if (T == 0 || R == 0) return SMLA_OK;
+  rc = check_rows("k", k, k_stride, (int64_t)HK * D);
+  if (rc == SMLA_OK) rc = check_rows("v", v, v_stride, (int64_t)HK * D);
+  if (rc != SMLA_OK) return rc;
+  if (!query_start || !seq_lens || !block_table || !k_cache || !v_cache || !k_scale || !v_scale)
+    return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(k_cache) || !aligned16(v_cache))
+    return fail(SMLA_ERR_INVALID_ARG, "k_cache and v_cache must be 16-byte aligned");
+  smla::KvStoreArgs a{k,       v,       k_stride, v_stride, query_start, seq_lens, block_table, k_cache,
+                      v_cache, k_scale, v_scale,  T,        HK,          D,        R,           MB,
+                      NB};
+  cudaError_t e = smla::launch_kv_store(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_cache_store_fp8 launch");
+  return SMLA_OK;
+}
+
+size_t paged_attention_fp8_workspace_bytes(int T, int H, int HK, int D, int R, int max_query_len) {
+  (void)max_query_len;
+  if (T < 0 || R < 0 || HK <= 0 || H <= 0 || H % HK != 0 || H / HK > 128 || (D != 64 && D != 128)) return 0;
+  return smla::kWsStatusBytes;
+}
+
+int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+                        const float* k_scale, const float* v_scale, const int32_t* block_table,
+                        const int32_t* seq_lens, const int32_t* query_start, float sm_scale, int max_query_len,
+                        int window, float softcap, const float* alibi_slopes, const int32_t* prefix_lens,
+                        const int32_t* doc_start, void* out, float* lse, int T, int H, int HK, int D, int R, int MB,
+                        int NB, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_batch(T, R, MB, NB);
+  if (rc == SMLA_OK) rc = check_kv_heads(HK, D, NB);
+  if (rc != SMLA_OK) return rc;
+  if (H <= 0 || H % HK != 0) return fail(SMLA_ERR_INVALID_ARG, "H=%d must be a positive multiple of HK=%d", H, HK);
+  if (H / HK > 128) return fail(SMLA_ERR_UNSUPPORTED, "H=%d unsupported: at most 128 heads per K/V head", H);
+  if (window < 0 || max_query_len < 0 || !(softcap >= 0.f) || softcap > 3e38f)
+    return fail(SMLA_ERR_INVALID_ARG, "window=%d, max_query_len=%d and softcap=%g must not be negative", window,
+                max_query_len, softcap);
+  if (T == 0 || R == 0) return SMLA_OK;
+  rc = check_rows("q", q, q_stride, (int64_t)H * D);
+  if (rc != SMLA_OK) return rc;
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !query_start || !out || !lse)
+    return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+    return fail(SMLA_ERR_INVALID_ARG, "k_cache, v_cache and out must be 16-byte aligned");
+  const size_t need = paged_attention_fp8_workspace_bytes(T, H, HK, D, R, max_query_len);
+  if (workspace) {
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+      return fail(SMLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (workspace_bytes < need)
+      return fail(SMLA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+  } else {
+    rc = cached_workspace(need, &workspace);
+    if (rc != SMLA_OK) return rc;
+  }
+  smla::PagedAttnArgs a{};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.query_start = query_start;
+  a.alibi_slopes = alibi_slopes;
+  a.prefix_lens = prefix_lens;
+  a.doc_start = doc_start;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.sm_scale = sm_scale;
+  a.softcap = softcap;
+  a.window = window;
+  a.T = T;
+  a.H = H;
+  a.HK = HK;
+  a.D = D;
+  a.R = R;
+  a.MB = MB;
+  a.NB = NB;
+  cudaError_t e = smla::launch_paged_attention(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_attention_fp8 launch");
+  return SMLA_OK;
+}
+
 const char* smla_last_error(void) { return g_err; }
 
 int smla_version(void) { return 100; }

@@ -1,0 +1,252 @@
+// Block tables and slot maps of a batch, built on the GPU from its requests'
+// lengths, with the free cache blocks on a stack in device memory: nothing
+// goes through the host, so a step can be captured into a CUDA graph.
+//
+// extend: request r has c_r tokens cached and brings q_r new ones.
+//   have_r = min(ceil(c_r / 64), MB), want_r = min(ceil((c_r + q_r) / 64), MB)
+//   first_r = sum of (want - have) over the requests before r
+//   block_table[r, j], have_r <= j < want_r, = free_blocks[F - 1 - n], the
+//     n = first_r + j - have_r th new block (F = free_count; -1 once n >= F)
+//   query_start_r = sum of q over the requests before r (at most T)
+//   token t of request r: position c_r + t - query_start_r, its slot
+//     block_table[r, position / 64] * 64 + position % 64
+// release: the blocks of the released requests, in order, back on the stack.
+//
+// Both are bound by latency: a few KB to 1 MB are moved.  One launch of one
+// thread-block cluster: every CTA makes the prefix sums over the requests in
+// its shared memory (redundantly: no exchange through global memory), then
+// the cluster's threads share the tokens and blocks, each finding its request
+// by a binary search in shared memory.  All inputs that a caller may let the
+// outputs overwrite are read before a cluster barrier and written after it.
+#include <cstdint>
+#include <algorithm>
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "smla_common.cuh"
+#include "smla_kernels.h"
+
+namespace cg = cooperative_groups;
+
+namespace smla {
+
+namespace {
+
+constexpr int kMaxThreads = 1024;
+
+// a + b, at most cap (both at most cap <= 2^31 - 1): associative, so a prefix
+// sum can use it in any grouping.
+__device__ __forceinline__ uint32_t add_capped(uint32_t a, uint32_t b, uint32_t cap) { return min(a + b, cap); }
+
+// Exclusive prefix sums of v[0 .. n-1] in place (sums capped), the total in
+// v[n]; all threads of the CTA.
+__device__ void scan_in_place(uint32_t* v, int n, uint32_t cap) {
+  __shared__ uint32_t warp_sum[kMaxThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  const int per = (n + blockDim.x - 1) / blockDim.x;
+  const int beg = min(tid * per, n), end = min(beg + per, n);
+  uint32_t sum = 0;
+  for (int i = beg; i < end; ++i) sum = add_capped(sum, v[i], cap);
+  uint32_t inc = sum;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc = add_capped(inc, u, cap);
+  }
+  uint32_t before = __shfl_up_sync(0xffffffffu, inc, 1);
+  if (lane == 0) before = 0;
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  uint32_t base = 0;
+  for (int w = 0; w < warp; ++w) base = add_capped(base, warp_sum[w], cap);
+  uint32_t run = add_capped(base, before, cap);
+  for (int i = beg; i < end; ++i) {
+    const uint32_t x = v[i];
+    v[i] = run;
+    run = add_capped(run, x, cap);
+  }
+  if (tid == 0) {
+    uint32_t total = 0;
+    for (int w = 0; w < nw; ++w) total = add_capped(total, warp_sum[w], cap);
+    v[n] = total;
+  }
+  __syncthreads();
+}
+
+// The last i in [0, n) with v[i] <= x (v non-decreasing, v[0] <= x).
+__device__ __forceinline__ int last_not_above(const uint32_t* v, int n, uint32_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (v[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int blocks_of(int64_t tokens, int MB) {
+  return (int)min((tokens + kBlock - 1) / kBlock, (int64_t)MB);
+}
+
+__global__ void __launch_bounds__(kMaxThreads) blocks_extend_kernel(const __grid_constant__ BlocksExtendArgs a) {
+  extern __shared__ uint32_t smem_blocks[];
+  const cg::cluster_group cluster = cg::this_cluster();
+  uint32_t* start = smem_blocks;           // [R + 1] first token
+  uint32_t* first = start + a.R + 1;       // [R + 1] first new block
+  uint32_t* ctx = first + a.R + 1;         // [R] cached tokens
+  const int tid = threadIdx.x;
+  const int64_t gid = (int64_t)blockIdx.x * blockDim.x + tid, step = (int64_t)gridDim.x * blockDim.x;
+  const int free_count = max(0, min(__ldg(a.free_count), a.F));
+  for (int r = tid; r < a.R; r += blockDim.x) {
+    const int c = max(0, a.context_lens[r]), q = max(0, a.query_lens[r]);
+    ctx[r] = (uint32_t)c;
+    start[r] = (uint32_t)min(q, a.T);
+    first[r] = (uint32_t)(blocks_of((int64_t)c + q, a.MB) - blocks_of(c, a.MB));
+  }
+  __syncthreads();
+  // The length of request gid, read here because seq_lens may be one of the inputs: the cluster has a
+  // thread for every request (kMaxPagedRequests is 8 CTAs of 1024).
+  int64_t len0 = 0;
+  if (gid < a.R) len0 = (int64_t)max(0, a.context_lens[gid]) + max(0, a.query_lens[gid]);
+  scan_in_place(start, a.R, (uint32_t)a.T);
+  scan_in_place(first, a.R, 0x7fffffffu);
+  const uint32_t used = start[a.R], grown = first[a.R];
+  cluster.sync();
+
+  for (int64_t r = gid; r <= a.R; r += step) {
+    a.query_start[r] = (int32_t)start[r];
+    if (r < a.R) a.seq_lens[r] = (int32_t)min(len0, (int64_t)0x7fffffff);
+  }
+  if (gid == 0) {
+    *a.free_count_out = max(0, free_count - (int)grown);
+    *a.missing = max(0, (int)grown - free_count);
+  }
+  for (int64_t n = gid; n < (int64_t)grown; n += step) {
+    const int r = last_not_above(first, a.R, (uint32_t)n);
+    const int j = blocks_of((int64_t)ctx[r], a.MB) + (int)((uint32_t)n - first[r]);
+    const int64_t at = (int64_t)free_count - 1 - n;
+    a.block_table[(int64_t)r * a.MB + j] = at >= 0 ? __ldg(a.free_blocks + at) : -1;
+  }
+  for (int64_t t = gid; t < a.T; t += step) {
+    int32_t req = -1, pos = 0;
+    int64_t slot = -1;
+    if (t < (int64_t)used) {
+      req = last_not_above(start, a.R, (uint32_t)t);
+      const int64_t p = (int64_t)ctx[req] + (t - start[req]), j = p / kBlock;
+      pos = (int32_t)min(p, (int64_t)0x7fffffff);
+      if (j < a.MB) {
+        const int have = blocks_of((int64_t)ctx[req], a.MB);
+        int64_t b;
+        if (j < have) {
+          b = a.block_table[(int64_t)req * a.MB + j];  // not written by this call
+        } else {
+          const int64_t at = (int64_t)free_count - 1 - ((int64_t)first[req] + (j - have));
+          b = at >= 0 ? __ldg(a.free_blocks + at) : -1;
+        }
+        if (b >= 0 && b < a.NB) slot = b * kBlock + p % kBlock;
+      }
+    }
+    a.req_id_per_token[t] = req;
+    a.positions[t] = pos;
+    a.slot_mapping[t] = slot;
+  }
+}
+
+// A unit is a run of `chunk` table entries of one request; a warp counts the
+// blocks of a unit, and pushes them after the prefix sums over the units.
+__global__ void __launch_bounds__(kMaxThreads) blocks_release_kernel(const __grid_constant__ BlocksReleaseArgs a) {
+  extern __shared__ uint32_t smem_blocks[];
+  cg::cluster_group cluster = cg::this_cluster();
+  uint32_t* count = smem_blocks;  // [units + 1]
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int nw = (int)(gridDim.x * blockDim.x) >> 5, w0 = (int)(blockIdx.x * blockDim.x + tid) >> 5;
+  const int nch = (a.MB + a.chunk - 1) / a.chunk, units = a.R * nch;
+  const int free_count = max(0, min(__ldg(a.free_count), a.F));
+  cluster.sync();  // every CTA of the cluster runs before its shared memory is written
+  auto entries = [&](int u, const int32_t*& row) {  // this unit's entries
+    const int r = u / nch, j0 = (u - r * nch) * a.chunk;
+    row = a.block_table + (int64_t)r * a.MB + j0;
+    if (!a.release[r]) return 0;
+    return max(0, min(a.chunk, blocks_of(max(0, a.seq_lens[r]), a.MB) - j0));
+  };
+  for (int u = w0; u < units; u += nw) {
+    const int32_t* row;
+    const int n = entries(u, row);
+    int got = 0;
+#pragma unroll 4
+    for (int i = lane; i < n; i += 32) {
+      const int b = row[i];
+      got += b >= 0 && b < a.NB;
+    }
+    got = __reduce_add_sync(0xffffffffu, got);
+    if (lane < (int)gridDim.x) cluster.map_shared_rank(count, lane)[u] = (uint32_t)got;
+  }
+  cluster.sync();
+  scan_in_place(count, units, 0x7fffffffu);
+  for (int u = w0; u < units; u += nw) {
+    if (count[u + 1] == count[u]) continue;
+    const int32_t* row;
+    const int n = entries(u, row);
+    int64_t at = (int64_t)free_count + count[u];
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int b = i0 + lane < n ? row[i0 + lane] : -1;
+      const bool ok = b >= 0 && b < a.NB;
+      const uint32_t who = __ballot_sync(0xffffffffu, ok);
+      const int64_t to = at + __popc(who & ((1u << lane) - 1u));
+      if (ok && to < a.F) a.free_blocks[to] = b;
+      at += __popc(who);
+    }
+  }
+  cluster.sync();  // all lengths and the count have been read: context_lens and free_count_out may be the inputs
+  const int step = (int)(gridDim.x * blockDim.x);
+  for (int r = (int)(blockIdx.x * blockDim.x) + tid; r < a.R; r += step)
+    a.context_lens[r] = a.release[r] ? 0 : a.seq_lens[r];
+  if (blockIdx.x == 0 && tid == 0) *a.free_count_out = (int)min((int64_t)a.F, (int64_t)free_count + count[units]);
+}
+
+template <typename Args>
+cudaError_t launch_cluster(void (*kernel)(Args), const Args& a, int ctas, int threads, size_t smem,
+                           cudaStream_t stream) {
+  // set at every launch: it takes well under a microsecond and needs no per-device record
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// CTAs (1, 2, 4 or 8, a portable cluster) and threads for `work` items.
+void size_cluster(int64_t work, int* ctas, int* threads) {
+  *threads = work <= 256 ? 256 : kMaxThreads;
+  *ctas = 1;
+  while (*ctas < 8 && (int64_t)*ctas * *threads < work) *ctas *= 2;
+}
+
+}  // namespace
+
+cudaError_t launch_blocks_extend(const BlocksExtendArgs& a, cudaStream_t stream) {
+  int ctas, threads;
+  size_cluster(std::max<int64_t>((int64_t)a.R + 1, a.T), &ctas, &threads);
+  return launch_cluster(blocks_extend_kernel, a, ctas, threads, (size_t)(3 * (int64_t)a.R + 2) * 4, stream);
+}
+
+cudaError_t launch_blocks_release(BlocksReleaseArgs a, cudaStream_t stream) {
+  a.chunk = 512;
+  while ((int64_t)a.R * ((a.MB + a.chunk - 1) / a.chunk) > kMaxPagedRequests) a.chunk *= 2;
+  const int64_t units = (int64_t)a.R * ((a.MB + a.chunk - 1) / a.chunk);
+  int ctas, threads;
+  size_cluster(32 * units, &ctas, &threads);  // a warp each
+  return launch_cluster(blocks_release_kernel, a, ctas, threads, (size_t)(units + 1) * 4, stream);
+}
+
+}  // namespace smla

@@ -97,6 +97,87 @@ bool nvfp4_native_supported(int H);
 AttnPlan plan_decode_nvfp4(int T, int H, int K, int num_splits, int num_sms);
 cudaError_t launch_decode_nvfp4(const AttnArgs& a, const AttnPlan& plan, cudaStream_t stream);
 
+// ---- paged K/V cache (block size 64, separate K and V heads)
+
+// Requests of one batch: the block-table kernels keep their prefix sums over
+// the requests in shared memory, one thread of an 8-CTA cluster per request.
+constexpr int kMaxPagedRequests = 8192;
+
+// Block tables, slot maps and token positions from request lengths
+// (smla_blocks.cu).
+struct BlocksExtendArgs {
+  const int32_t* context_lens;  // [R]
+  const int32_t* query_lens;    // [R]
+  int32_t* block_table;         // [R, MB], new entries written
+  const int32_t* free_blocks;   // [F] stack, top at free_count - 1
+  const int32_t* free_count;    // [1]
+  int32_t* query_start;         // [R + 1]
+  int32_t* seq_lens;            // [R]
+  int32_t* req_id_per_token;    // [T]
+  int32_t* positions;           // [T]
+  int64_t* slot_mapping;        // [T]
+  int32_t* free_count_out;      // [1]
+  int32_t* missing;             // [1]
+  int R, MB, F, T;
+  int64_t NB;
+};
+struct BlocksReleaseArgs {
+  const uint8_t* release;      // [R], nonzero = release
+  const int32_t* seq_lens;     // [R]
+  const int32_t* block_table;  // [R, MB]
+  int32_t* free_blocks;        // [F] stack
+  const int32_t* free_count;   // [1]
+  int32_t* context_lens;       // [R]
+  int32_t* free_count_out;     // [1]
+  int R, MB, F;
+  int64_t NB;
+  int chunk = 0;               // table entries per unit (set by the launch)
+};
+cudaError_t launch_blocks_extend(const BlocksExtendArgs& a, cudaStream_t stream);
+cudaError_t launch_blocks_release(BlocksReleaseArgs a, cudaStream_t stream);
+
+// Quantize-and-store of new K and V rows, a scale per block and head
+// (smla_kvstore.cu).
+struct KvStoreArgs {
+  const void* k;               // bf16 [T, HK, D], rows k_stride elements apart
+  const void* v;
+  int64_t k_stride, v_stride;
+  const int32_t* query_start;  // [R + 1]
+  const int32_t* seq_lens;     // [R]
+  const int32_t* block_table;  // [R, MB]
+  uint8_t* k_cache;            // [NB, HK, 64, D]
+  uint8_t* v_cache;
+  float* k_scale;              // [NB, HK]
+  float* v_scale;
+  int T, HK, D, R, MB;
+  int64_t NB;
+};
+cudaError_t launch_kv_store(const KvStoreArgs& a, cudaStream_t stream);
+
+// Attention over the paged K/V cache (smla_paged_attn.cu).
+struct PagedAttnArgs {
+  const void* q;               // bf16 [T, H, D], rows q_stride elements apart
+  int64_t q_stride;
+  const uint8_t* k_cache;      // [NB, HK, 64, D]
+  const uint8_t* v_cache;
+  const float* k_scale;        // [NB, HK]
+  const float* v_scale;
+  const int32_t* block_table;  // [R, MB]
+  const int32_t* seq_lens;     // [R]
+  const int32_t* query_start;  // [R + 1]
+  const float* alibi_slopes;   // [H] or null
+  const int32_t* prefix_lens;  // [R] or null
+  const int32_t* doc_start;    // [T] or null
+  void* out;                   // bf16 [T, H, D]
+  float* lse;                  // [T, H]
+  void* workspace;
+  float sm_scale, softcap;
+  int window;
+  int T, H, HK, D, R, MB;
+  int64_t NB;
+};
+cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream);
+
 // Offsets inside the workspace.
 constexpr size_t kWsStatusBytes = 256;
 

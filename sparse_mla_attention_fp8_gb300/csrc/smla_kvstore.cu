@@ -1,0 +1,160 @@
+// Quantize-and-store of new K and V rows into the paged 8-bit K/V cache: e4m3
+// codes [NB, HK, 64, D] with one scale per block of 64 tokens and head.
+//
+// A block's scale is a power of two 2^E, E the smallest (from -100 up) with
+// amax <= 448 * 2^E over the rows it covers, so dividing by it is exact and the
+// only rounding is that to e4m3.  A block whose first row is written by this
+// call takes the new rows' scale.  A block partly filled before keeps the
+// larger of its own and the new rows' scale; where that grows, the codes of
+// its old rows become e4m3(code * old / new), exact but for codes that turn
+// subnormal.  Infinities saturate and are left out of amax; NaN is stored as
+// 0, so that no stored row can spread NaN to a query that does not see it.
+//
+// The new rows of a block are found from the batch's lengths (the tokens of a
+// request are consecutive), not from a slot map: the block's scale needs them
+// together, and this way one warp has them without any exchange or atomics.
+// Unit u of the grid stands for one touched block: request r's units start at
+// floor(query_start_r / 64) + 2 r, which leaves room for every block that its
+// tokens can touch, so a unit finds its request by a search in query_start.
+// A warp per (block, head, K or V) holds the block's new rows in registers
+// (one read of the input), so the kernel moves what it must: bound by HBM for
+// prefill, by latency for single tokens.
+#include <cstdint>
+#include <algorithm>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "sm103_ptx.cuh"
+#include "smla_common.cuh"
+#include "smla_kernels.h"
+#include "smla_paged.cuh"
+
+namespace smla {
+
+namespace {
+
+constexpr int kStoreWarps = 8;
+constexpr uint32_t kAll = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+__device__ __forceinline__ float2 e4m3x2_f32(uint32_t pair) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// |bf16| of both halves of w, 0 for infinities and NaN, into amax.
+__device__ __forceinline__ float finite_amax(float amax, uint32_t w) {
+  const float lo = fabsf(__uint_as_float(w << 16)), hi = fabsf(__uint_as_float(w & 0xffff0000u));
+  if (lo < INFINITY) amax = fmaxf(amax, lo);
+  if (hi < INFINITY) amax = fmaxf(amax, hi);
+  return amax;
+}
+__device__ __forceinline__ float nan_to_0(float x) { return x == x ? x : 0.f; }
+
+// Exponent E of the scale of a group with this amax (finite, >= 0): amax =
+// (1 + f) 2^e, and 448 = 1.75 * 2^8.  Subnormal bf16 have e = -127 here, far
+// below the floor of -100.
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  return max(-100, (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u));
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// The new rows [row0, row0 + n) of one block and head by one warp.  A lane
+// holds 4 values of a row: D / 4 lanes make a row, 128 / D rows an access.
+// kAccesses * 128 / D rows at most.
+template <int D, int kAccesses>
+__device__ __forceinline__ void store_rows(const __nv_bfloat16* __restrict__ src, int64_t stride, int row0, int n,
+                                           uint8_t* __restrict__ page, float* __restrict__ scale) {
+  constexpr int kRowsPer = 128 / D;
+  const int lane = threadIdx.x & 31, sub = lane / (D / 4), col = 4 * (lane % (D / 4));
+  const float old = row0 > 0 ? *scale : 0.f;
+  uint2 v[kAccesses];
+#pragma unroll
+  for (int i = 0; i < kAccesses; ++i) {
+    const int r = i * kRowsPer + sub;
+    v[i] = r < n ? __ldg(reinterpret_cast<const uint2*>(src + r * stride + col)) : make_uint2(0u, 0u);
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kAccesses; ++i) amax = finite_amax(finite_amax(amax, v[i].x), v[i].y);
+  amax = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(amax)));  // non-negative: ordered as its bits
+  const int e = scale_exponent(amax);
+  float s = pow2(e), inv = pow2(-e);
+  if (old > s) {
+    s = old;  // the block's scale stays
+    inv = __frcp_rn(old);
+  } else if (row0 > 0 && old < s) {
+    const float f = old * inv;
+    const int words = row0 * (D / 4);
+    uint32_t* w = reinterpret_cast<uint32_t*>(page);
+#pragma unroll 8
+    for (int i = lane; i < words; i += 32) {
+      const uint32_t c = w[i];
+      const float2 a = e4m3x2_f32(c & 0xffffu), b = e4m3x2_f32(c >> 16);
+      w[i] = e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
+    }
+  }
+  uint8_t* dst = page + (row0 + sub) * D + col;
+#pragma unroll
+  for (int i = 0; i < kAccesses; ++i) {
+    if (i * kRowsPer + sub >= n) break;
+    const float x0 = nan_to_0(__uint_as_float(v[i].x << 16)), x1 = nan_to_0(__uint_as_float(v[i].x & 0xffff0000u));
+    const float x2 = nan_to_0(__uint_as_float(v[i].y << 16)), x3 = nan_to_0(__uint_as_float(v[i].y & 0xffff0000u));
+    *reinterpret_cast<uint32_t*>(dst + i * 128) = e4m3x4(x0 * inv, x1 * inv, x2 * inv, x3 * inv);
+  }
+  if (lane == 0) *scale = s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kStoreWarps) kv_store_kernel(const __grid_constant__ KvStoreArgs a) {
+  const int u = (int)blockIdx.x, warp = threadIdx.x >> 5;
+  const int item = (int)blockIdx.y * kStoreWarps + warp;
+  if (item >= 2 * a.HK) return;
+  // request r's units start at floor(query_start_r / 64) + 2 r
+  const int r = search_units(a.R, u, [&](int i) { return clamp_start(a.query_start, i, a.T) / kBlock + 2 * i; });
+  const int t0 = clamp_start(a.query_start, r, a.T), t1 = clamp_start(a.query_start, r + 1, a.T);
+  const int local = u - (t0 / kBlock + 2 * r);
+  const int64_t len = a.seq_lens[r], ctx = len - (t1 - t0);
+  if (t1 <= t0 || ctx < 0 || local < 0) return;
+  const int64_t j = ctx / kBlock + local;  // logical block
+  if (j * kBlock >= len || j >= a.MB) return;
+  const int b = __ldg(a.block_table + (int64_t)r * a.MB + j);
+  if (b < 0 || b >= a.NB) return;
+  const int64_t p0 = max(ctx, j * kBlock), p1 = min(len, (j + 1) * kBlock);
+  const int row0 = (int)(p0 % kBlock), n = (int)(p1 - p0);
+  const int h = item >> 1;
+  const bool is_v = item & 1;
+  const int64_t bh = (int64_t)b * a.HK + h;
+  const __nv_bfloat16* src = is_v ? static_cast<const __nv_bfloat16*>(a.v) + (t0 + (p0 - ctx)) * a.v_stride
+                                  : static_cast<const __nv_bfloat16*>(a.k) + (t0 + (p0 - ctx)) * a.k_stride;
+  src += (int64_t)h * D;
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  uint8_t* page = (is_v ? a.v_cache : a.k_cache) + bh * (kBlock * D);
+  float* scale = (is_v ? a.v_scale : a.k_scale) + bh;
+  // few rows (single tokens, drafts): a short body, so that a decode step does not fetch and skip the long one
+  if (n * D <= 8 * 128)
+    store_rows<D, 8>(src, stride, row0, n, page, scale);
+  else
+    store_rows<D, kBlock * D / 128>(src, stride, row0, n, page, scale);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_store(const KvStoreArgs& a, cudaStream_t stream) {
+  const dim3 grid((unsigned)(a.T / kBlock + 2 * a.R), (unsigned)((2 * a.HK + kStoreWarps - 1) / kStoreWarps));
+  if (a.D == 128)
+    kv_store_kernel<128><<<grid, 32 * kStoreWarps, 0, stream>>>(a);
+  else
+    kv_store_kernel<64><<<grid, 32 * kStoreWarps, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace smla
