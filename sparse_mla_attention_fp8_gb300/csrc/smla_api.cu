@@ -752,9 +752,11 @@ int kv_cache_store_fp8(const void* k, int64_t k_stride, const void* v, int64_t v
 }
 
 size_t paged_attention_fp8_workspace_bytes(int T, int H, int HK, int D, int R, int max_query_len) {
-  (void)max_query_len;
-  if (T < 0 || R < 0 || HK <= 0 || H <= 0 || H % HK != 0 || H / HK > 128 || (D != 64 && D != 128)) return 0;
-  return smla::kWsStatusBytes;
+  if (T < 0 || R < 0 || HK <= 0 || H <= 0 || H % HK != 0 || H / HK > 128 || (D != 64 && D != 128) || max_query_len < 0)
+    return 0;
+  int sms = 0;
+  if (num_sms(&sms) != SMLA_OK) return 0;
+  return smla::paged_attention_workspace(H / HK, D, max_query_len, sms);
 }
 
 int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
@@ -778,10 +780,16 @@ int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache,
     return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
     return fail(SMLA_ERR_INVALID_ARG, "k_cache, v_cache and out must be 16-byte aligned");
-  const size_t need = paged_attention_fp8_workspace_bytes(T, H, HK, D, R, max_query_len);
+  if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(SMLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  int sms = 0;
+  size_t need = smla::kWsStatusBytes;  // and more, by the device
+  if (!workspace || workspace_bytes >= need) {
+    rc = num_sms(&sms);
+    if (rc != SMLA_OK) return rc;
+    need = smla::paged_attention_workspace(H / HK, D, max_query_len, sms);
+  }
   if (workspace) {
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-      return fail(SMLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     if (workspace_bytes < need)
       return fail(SMLA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
   } else {
@@ -814,7 +822,7 @@ int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache,
   a.R = R;
   a.MB = MB;
   a.NB = NB;
-  cudaError_t e = smla::launch_paged_attention(a, static_cast<cudaStream_t>(stream));
+  cudaError_t e = smla::launch_paged_attention(a, max_query_len, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention_fp8 launch");
   return SMLA_OK;
 }

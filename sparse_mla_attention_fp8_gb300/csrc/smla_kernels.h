@@ -176,7 +176,9 @@ struct PagedAttnArgs {
   int T, H, HK, D, R, MB;
   int64_t NB;
 };
-cudaError_t launch_paged_attention(const PagedAttnArgs& a, cudaStream_t stream);
+// G heads per K/V head; max_query_len an estimate.
+size_t paged_attention_workspace(int G, int D, int max_query_len, int num_sms);
+cudaError_t launch_paged_attention(const PagedAttnArgs& a, int max_query_len, int num_sms, cudaStream_t stream);
 
 // Offsets inside the workspace.
 constexpr size_t kWsStatusBytes = 256;

@@ -387,6 +387,19 @@ def test_attention_nan_query_stays_in_its_row(smla):
     check(b, (out, lse), want)
 
 
+@pytest.mark.parametrize("HK,G,new", [(8, 4, 1), (1, 1, 1), (3, 8, 4), (1, 2, 100)])
+def test_attention_workspace_contents_do_not_matter(smla, HK, G, new):
+    """Few key tiles for many CTAs; a workspace that holds NaN everywhere."""
+    torch = torch_mod()
+    b = ref.Batch(24, HK, G, 128, [1000, 130], [new, 1])
+    n = smla.paged_attention_fp8_workspace_bytes(b.T, HK * G, HK, 128, 2, new)
+    out, lse = smla.paged_attention_fp8(
+        bf16(b.q), *(dev(c) for c in b.caches), *(dev(s) for s in b.scales), i32(b.table), i32(b.lens),
+        i32(b.query_start), b.sm_scale, max_query_len=new,
+        workspace=torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"))
+    check(b, (out.float().cpu().numpy(), lse.cpu().numpy()))
+
+
 def test_attention_is_deterministic(smla):
     b = ref.Batch(23, 2, 8, 128, [3000, 10, 900], [1, 60, 5])
     first = attend(smla, b)
