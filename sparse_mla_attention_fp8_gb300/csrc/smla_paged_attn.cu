@@ -11,24 +11,26 @@
 // a token that sees no key gets out = 0, lse = -inf.  Keys of a block whose
 // table entry is outside [0, NB) are not seen.
 //
-// This kernel takes up to N rows (tokens x heads of one K/V head) per query
-// tile, N = 16 or 32: single tokens and short drafts.  Each key is read once
+// This kernel takes up to C rows (tokens x heads of one K/V head) per query
+// tile, C = 8, 16 or 32: single tokens and short drafts.  Each key is read once
 // and meets few rows, so HBM bounds it, and the design keeps the codes moving
 // from HBM to the tensor cores with no instruction spent on them:
 //  * A key tile is 128 keys, two blocks; TMA copies each block's 64 x D codes
 //    of the head (contiguous in the cache) into a ring of stages.
 //  * Both products run on the codes as stored (tcgen05 kind::f8f6f4), keys or
-//    value columns in the MMA's 128 rows, the query rows in its N columns:
-//      S^T[key, row] = K Q^T, q split into two e4m3 terms, q 2^s = hi + lo
-//        (s puts the row's largest near 448), exact for components down to
-//        2^-10 of it: q has 8 significant bits, and hi leaves at most 4;
-//      O^T[d, row] = V^T P^T per block, P in an e4m3 term and an e5m2 term of
-//        the remainder (about 8 significant bits where P > 2^-14, and down to
-//        2^-23 of the largest weight: many small weights keep their sum).
-//  * Softmax: thread = key, N columns; the block's K scale folds into the
-//    logit.  P = 2^(x - m'), m' a running reference per row that is refreshed
-//    (to put the tile's maximum at 2^6.25) only when a tile exceeds 2^8.75, so
-//    a tile usually costs one vote of the warps instead of N maxima.
+//    value columns in the MMA's 128 rows and the query rows in its N = 2 C
+//    columns, which hold two e4m3 terms of each row's operand, 8 rows' first
+//    terms, then their second ones:
+//      S^T[key, row] = K Q^T, q 2^s = hi + lo (s puts the row's largest near
+//        448): exact for components down to 2^-10 of it, as q has 8
+//        significant bits and hi leaves at most 4;
+//      O^T[d, row] = V^T P^T per block, P = hi + lo / 16: 8 significant bits
+//        where P >= 2^-6, and nothing lost above 2^-14, 2^-19 of the largest
+//        weight or less: many small weights keep their sum.
+//  * Softmax: thread = key, 8 rows; the block's K scale folds into the logit.
+//    P = 2^(x - m'), m' a running reference per row that is refreshed (to put
+//    the tile's maximum at 2^5.25) only when a tile exceeds 2^8.75, so a tile
+//    usually costs one vote of the warps instead of 8 maxima.
 //  * O^T of each tile is read from tensor memory and added, times the block's
 //    V scale, to sums in registers: no rescaling pass, any scales.
 //  * The key tiles of the whole call form one sequence (smla_paged.cuh) that
@@ -36,7 +38,7 @@
 //    several CTAs share is merged by a second kernel.  Lengths are read on the
 //    device only.
 //  * Roles: TMA producer, QK^T issuer, P.V issuer, scheduler (segments ahead,
-//    their Q split and columns), N / 16 groups of 4 softmax warps, 4 warps
+//    their Q split and columns), C / 8 groups of 4 softmax warps, 4 warps
 //    that sum O.
 #include <cstdint>
 #include <algorithm>
@@ -59,11 +61,11 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kTop = 8.75f;      // P = 2^(x - m') <= 2^8.75 < 430 (e4m3: 448)
-constexpr float kRefresh = 6.25f;  // a refreshed m' puts the tile's maximum at 2^6.25
+constexpr float kRefresh = 5.25f;  // a refreshed m' puts the tile's maximum at 2^5.25
 constexpr float kNoMax = -3e38f;   // m' of a row that has seen nothing
 
-__host__ __device__ constexpr uint32_t idesc_f8(uint32_t M, uint32_t N, uint32_t b_e5m2, uint32_t a_mn, uint32_t b_mn) {
-  return (1u << 4) | (b_e5m2 << 10) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
+  return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -96,8 +98,8 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t pair) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// Two weights -> e4m3 codes and e5m2 codes of the remainders (low byte from
-// x0).  The split runs in f16x2: 11 bits, more than the two terms keep.
+// Two weights -> e4m3 codes hi and lo of p ~ hi + lo / 16 (low byte from x0).
+// The split runs in f16x2: 11 bits, more than the two terms keep.
 __device__ __forceinline__ void split_p(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   uint32_t a, d, r;
   uint16_t t;
@@ -106,7 +108,8 @@ __device__ __forceinline__ void split_p(float x0, float x1, uint32_t& hi, uint32
   hi = t;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(t));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(d));
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(t) : "r"(r));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x4c004c00u));  // 16, 16
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(t) : "r"(r));
   lo = t;
 }
 // Offset of 16-byte chunk ch of row r, rows of D bytes under the D-byte swizzle.
@@ -115,64 +118,74 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
   return (uint32_t)(r * D + ((D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4));
 }
 
+// mbar_wait with its slow part out of line: the roles' loops stay small.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* cta_abort, int* status) {
+  return mbar_wait(bar, parity, cta_abort, status, kDevWaitTimeout);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* cta_abort, int* status) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, cta_abort, status);
+}
+
 struct Params {
   PagedAttnArgs a;
-  // Rows of a query tile: tq tokens x up to Gr of the G heads of a K/V head; more than N heads are cut into
+  // Rows of a query tile: tq tokens x up to Gr of the G heads of a K/V head; more than C heads are cut into
   // `cuts` groups, which the sequence of units counts as K/V heads of their own (HV = HK * cuts).
   int G, Gr, cuts, HV, tq;
   int ctas;
   int* status;
   PagedMerge* merge;    // [ctas]
-  float* part_ml;       // [2 ctas][m' | l][N]
-  float* part_o;        // [2 ctas][N][D]
+  float* part_ml;       // [2 ctas][m' | l][C]
+  float* part_o;        // [2 ctas][C][D]
 };
 
-// What a row (column of the MMAs) needs of its own.
-template <int N>
+// What a row needs of its own.
+template <int C>
 struct Columns {
-  float scale[N];  // logit = S * scale * k_scale, in log2 units (natural ones with softcap)
-  float slope[N];  // log2 units per key of distance
-  int pos[N], lo[N], hi[N];
+  float scale[C];  // logit = S * scale * k_scale, in log2 units (natural ones with softcap)
+  float slope[C];  // log2 units per key of distance
+  int pos[C], lo[C], hi[C];
 };
 
-template <int D, int N>
+template <int D, int C>
 struct Lay {
-  static constexpr int kHalves = N / 16;  // softmax groups
-  static constexpr int kWarps = 4 + 4 * kHalves + 4;
+  static constexpr int N = 2 * C;          // MMA columns: two terms of each row
+  static constexpr int kGroups = C / 8;    // softmax groups
+  static constexpr int kWarps = 4 + 4 * kGroups + 4;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kPerSm = N == 16 ? 2 : 1;
+  static constexpr int kPerSm = C <= 16 ? 2 : 1;
   static constexpr int kKTile = kKeyTile * D;
   static constexpr int kStage = 2 * kKTile;
-  static constexpr int kStages = (N == 16 ? 3 : 5) * (128 / D);
-  static constexpr int kMeta = kStages + 2;        // ring of page scales and flags
-  static constexpr int kQTerm = N * D;             // one term of Q
-  static constexpr int kQBuf = 2 * kQTerm;
+  static constexpr int kStages = (C <= 16 ? 3 : 5) * (128 / D);
+  static constexpr int kMeta = kStages + 2;        // ring of block scales and flags
+  static constexpr int kQBuf = N * D;
   static constexpr int kSegs = 2;
-  static constexpr int kP = kKeyTile * 2 * N;
-  static constexpr int kRefs = 4;                  // ring of (m', v scales) towards the summing warps
+  static constexpr int kPBuf = kKeyTile * N;
+  static constexpr int kPBufs = C == 16 ? 1 : 2;   // two where two CTAs still fit an SM
+  static constexpr int kRefs = 4;                  // ring of (factors, v scales) towards the summing warps
   static constexpr int kOffQ = kStages * kStage;
   static constexpr int kOffP = kOffQ + kSegs * kQBuf;
-  static constexpr int kOffCols = kOffP + kP;
-  static constexpr int kOffMeta = kOffCols + kSegs * (int)sizeof(Columns<N>);
+  static constexpr int kOffCols = kOffP + kPBufs * kPBuf;
+  static constexpr int kOffMeta = kOffCols + kSegs * (int)sizeof(Columns<C>);
   static constexpr int kOffRefs = kOffMeta + kMeta * 32;
-  static constexpr int kRef = N * 4 + 16;          // m'[N], v scales, change flag
-  static constexpr int kOffRed = kOffRefs + kRefs * kRef;          // float [halves][4][16]
-  static constexpr int kOffSum = kOffRed + kHalves * 4 * 16 * 4;   // float [halves][4][16]
-  static constexpr int kOffFin = kOffSum + kHalves * 4 * 16 * 4;   // float [2][m' | l][N]
-  static constexpr int kOffSeg = kOffFin + 2 * 2 * N * 4;
+  static constexpr int kRef = C * 4 + 32;          // factor[C], v scales, change flags of the groups
+  static constexpr int kOffRed = kOffRefs + kRefs * kRef;          // float [groups][4][8]
+  static constexpr int kOffSum = kOffRed + kGroups * 4 * 8 * 4;    // float [groups][4][8]
+  static constexpr int kOffFin = kOffSum + kGroups * 4 * 8 * 4;    // float [2][m' | l][C]
+  static constexpr int kOffSeg = kOffFin + 2 * 2 * C * 4;
   static constexpr int kOffBar = (kOffSeg + kSegs * (int)sizeof(Segment) + 7) / 8 * 8;
   enum {
     kKFull = 0, kVFull = kKFull + kStages, kEmpty = kVFull + kStages, kSFull = kEmpty + kStages, kSFree = kSFull + 2,
-    kPFull = kSFree + 2, kPFree, kOFull, kOFree = kOFull + 2, kRefFull = kOFree + 2, kSegFull = kRefFull + kRefs,
-    kSegFree = kSegFull + kSegs, kFinFull = kSegFree + kSegs, kDrainQk = kFinFull + 2, kDrainPv, kNumBars
+    kPFull = kSFree + 2, kPFree = kPFull + kPBufs, kOFull = kPFree + kPBufs, kOFree = kOFull + 2,
+    kRefFull = kOFree + 2, kSegFull = kRefFull + kRefs, kSegFree = kSegFull + kSegs, kFinFull = kSegFree + kSegs,
+    kDrainQk = kFinFull + 2, kDrainPv, kNumBars
   };
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;
   static constexpr int kTmemS = 0, kTmemO = 2 * N;  // S [2][N], O [2][2 blocks][N]
-  static constexpr int kTmemCols = N == 16 ? 128 : 256;
-  static_assert(kTmemO + 4 * N <= kTmemCols, "tensor memory");
+  static constexpr int kTmemCols = 6 * N <= 128 ? 128 : 6 * N <= 256 ? 256 : 512;
+  static_assert(6 * N <= kTmemCols && kPerSm * kTmemCols <= 512, "tensor memory");
   static_assert(kPerSm * (kSmem + 1024) <= 233472, "shared memory of an SM");
-  static_assert(kStage % 1024 == 0 && kQTerm % 512 == 0 && kOffP % 128 == 0 && kOffCols % 16 == 0 &&
+  static_assert(kStage % 1024 == 0 && kQBuf % 1024 == 0 && kOffP % 128 == 0 && kOffCols % 16 == 0 &&
                 kOffRefs % 16 == 0 && kRef % 16 == 0 && kOffFin % 16 == 0 && kOffRed % 16 == 0, "alignment");
   static_assert((kMaxPagedRequests + 1 + kWarps) * 8 <= kStages * kStage, "prefix sums fit the stages");
 };
@@ -220,11 +233,12 @@ __device__ void scan_tiles(int64_t* v, int R) {
   __syncthreads();
 }
 
-template <int D, int N>
-__global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
+template <int D, int C>
+__global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     paged_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map) {
-  using L = Lay<D, N>;
+  using L = Lay<D, C>;
+  constexpr int N = L::N;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   grid_launch_dependents();  // the merge may be launched behind this grid; it waits for the grid's end
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -242,17 +256,19 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[L::kSFull + i], 1);
-      mbar_init(&bars[L::kSFree + i], 4 * L::kHalves);
+      mbar_init(&bars[L::kSFree + i], 4 * L::kGroups);
       mbar_init(&bars[L::kOFull + i], 1);
       mbar_init(&bars[L::kOFree + i], 4);
-      mbar_init(&bars[L::kFinFull + i], L::kHalves);
+      mbar_init(&bars[L::kFinFull + i], L::kGroups);
     }
-    mbar_init(&bars[L::kPFull], 4 * L::kHalves);
-    mbar_init(&bars[L::kPFree], 1);
-    for (int i = 0; i < L::kRefs; ++i) mbar_init(&bars[L::kRefFull + i], L::kHalves);
+    for (int i = 0; i < L::kPBufs; ++i) {
+      mbar_init(&bars[L::kPFull + i], 4 * L::kGroups);
+      mbar_init(&bars[L::kPFree + i], 1);
+    }
+    for (int i = 0; i < L::kRefs; ++i) mbar_init(&bars[L::kRefFull + i], L::kGroups);
     for (int i = 0; i < L::kSegs; ++i) {
       mbar_init(&bars[L::kSegFull + i], 1);
-      mbar_init(&bars[L::kSegFree + i], 1 + 1 + 4 * L::kHalves + 4);
+      mbar_init(&bars[L::kSegFree + i], 1 + 1 + 4 * L::kGroups + 4);
     }
     mbar_init(&bars[L::kDrainQk], 1);
     mbar_init(&bars[L::kDrainPv], 1);
@@ -291,7 +307,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-#define PA_WAIT(idx, parity) mbar_wait(&bars[(idx)], (parity), abort_flag, p.status, kDevWaitTimeout)
+#define PA_WAIT(idx, parity) wait_bar(&bars[(idx)], (parity), abort_flag, p.status)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
@@ -364,7 +380,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- QK^T issuer
     if (lane == 0 && n_local > 0) {
-      constexpr uint32_t id = idesc_f8(128, N, 0, 0, 0);
+      constexpr uint32_t id = idesc_e4m3(128, N, 0, 0);
       constexpr uint32_t lay = D == 128 ? kLayoutSw128 : kLayoutSw64;
       const uint64_t dk0 = make_sdesc(smem_u32(smem), 16, 8 * D, lay);
       const uint64_t dq0 = make_sdesc(smem_u32(smem + L::kOffQ), 16, 8 * D, lay);
@@ -385,11 +401,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
           tc_fence_after();
           const uint64_t dk = dk0 + (uint64_t)((st * L::kStage) >> 4);
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              mma_f8(tmem + L::kTmemS + buf * N, dk + ((32 * k) >> 4), dq + ((term * L::kQTerm + 32 * k) >> 4), id,
-                     term + k > 0 ? 1u : 0u);
+          for (int k = 0; k < D / 32; ++k)
+            mma_f8(tmem + L::kTmemS + buf * N, dk + ((32 * k) >> 4), dq + ((32 * k) >> 4), id, k > 0 ? 1u : 0u);
           mma_commit(&bars[L::kSFull + buf]);
         }
         if (!dead) mma_commit(&bars[L::kSegFree + sb]);  // the segment's Q has been read
@@ -403,30 +416,25 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
   } else if (warp == 3) {
     // ---------------------------------------------------------------- P.V issuer
     if (lane == 0 && n_local > 0) {
-      constexpr uint32_t id_hi = idesc_f8(128, N, 0, 1, 1), id_lo = idesc_f8(128, N, 1, 1, 1);
+      constexpr uint32_t id = idesc_e4m3(128, N, 1, 1);
       // V: rows are keys, D-byte swizzle, read MN-major; at D = 64 the MMA's upper 64 rows read the same
       // columns again (atoms 0 bytes apart) and their results are not used
       const uint64_t dv0 = make_sdesc(smem_u32(smem + L::kKTile), 0, 8 * D, D == 128 ? kLayoutSw128 : kLayoutSw64);
-      // P: blocks of 8 keys x 16 rows, hi blocks then lo blocks of 8 keys
-      const uint64_t dp0 = make_sdesc(smem_u32(smem + L::kOffP), 16 * N, 128, kLayoutNone);
+      // P: core matrices of 8 keys x 16 columns, the N / 16 of 8 keys together
+      const uint64_t dp0 = make_sdesc(smem_u32(smem + L::kOffP), 8 * N, 128, kLayoutNone);
       for (int tl = 0; tl < n_local; ++tl) {
         const int st = tl % L::kStages, buf = tl & 1;
-        if (!PA_WAIT(L::kPFull, tl & 1) || !PA_WAIT(L::kVFull + st, (tl / L::kStages) & 1) ||
+        const int pb = tl % L::kPBufs;
+        if (!PA_WAIT(L::kPFull + pb, (tl / L::kPBufs) & 1) || !PA_WAIT(L::kVFull + st, (tl / L::kStages) & 1) ||
             (tl >= 2 && !PA_WAIT(L::kOFree + buf, ((tl >> 1) + 1) & 1)))
           break;
         tc_fence_after();
-        const uint64_t dv = dv0 + (uint64_t)((st * L::kStage) >> 4);
+        const uint64_t dv = dv0 + (uint64_t)((st * L::kStage) >> 4), dp = dp0 + (uint64_t)((pb * L::kPBuf) >> 4);
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-          for (int term = 0; term < 2; ++term)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int step = 2 * blk + k;  // 32 keys
-              mma_f8(tmem + L::kTmemO + (2 * buf + blk) * N, dv + ((32 * D * step) >> 4),
-                     dp0 + ((64 * N * step + term * 8 * N) >> 4), term ? id_lo : id_hi, term + k > 0 ? 1u : 0u);
-            }
-        mma_commit(&bars[L::kPFree]);
+        for (int step = 0; step < 4; ++step)  // 32 keys; two to a block
+          mma_f8(tmem + L::kTmemO + (2 * buf + (step >> 1)) * N, dv + ((32 * D * step) >> 4), dp + ((32 * N * step) >> 4),
+                 id, step & 1);
+        mma_commit(&bars[L::kPFree + pb]);
         mma_commit(&bars[L::kEmpty + st]);  // the tile's QK^T completed before its P was written
         mma_commit(&bars[L::kOFull + buf]);
       }
@@ -481,9 +489,9 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
             if (seg >= L::kSegs) dead = __any_sync(kAll, !PA_WAIT(L::kSegFree + sb, (seg / L::kSegs + 1) & 1));
             if (dead) break;
             if (lane == 0) *reinterpret_cast<Segment*>(smem + L::kOffSeg + sb * sizeof(Segment)) = s;
-            Columns<N>* cols = reinterpret_cast<Columns<N>*>(smem + L::kOffCols + sb * sizeof(Columns<N>));
+            Columns<C>* cols = reinterpret_cast<Columns<C>*>(smem + L::kOffCols + sb * sizeof(Columns<C>));
             const int rows = s.ntok * s.heads;
-            if (lane < N) {
+            if (lane < C) {
               const int t = min(ta + lane / s.heads, tb - 1), h = s.h0 + lane % s.heads;
               cols->pos[lane] = q.pos(t);
               cols->lo[lane] = lane < rows ? q.lo(a, t) : 0;
@@ -495,7 +503,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
             const uint32_t qd = smem_u32(smem + L::kOffQ + sb * L::kQBuf);
             const int sub = lane / kLanes, c = lane % kLanes;
 #pragma unroll 4
-            for (int i = 0; i < N / kRowsPer; ++i) {
+            for (int i = 0; i < C / kRowsPer; ++i) {
               const int row = i * kRowsPer + sub;
               uint4 v = make_uint4(0u, 0u, 0u, 0u);
               if (row < rows)
@@ -521,9 +529,13 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
                 hi[k >> 1] |= hc << (16 * (k & 1));
                 lo[k >> 1] |= e4m3x2(y0 - back.x, y1 - back.y) << (16 * (k & 1));
               }
-              const uint32_t dst = qd + swz<D>(row, c >> 1) + 8 * (c & 1);
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(hi[0]), "r"(hi[1]) : "memory");
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst + L::kQTerm), "r"(lo[0]), "r"(lo[1]) : "memory");
+              const int op = (row & ~7) + row;  // operand row: 16 b + row % 8, and the second term 8 behind
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op, c >> 1) + 8 * (c & 1)), "r"(hi[0]),
+                           "r"(hi[1])
+                           : "memory");
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op + 8, c >> 1) + 8 * (c & 1)), "r"(lo[0]),
+                           "r"(lo[1])
+                           : "memory");
               if (c == 0) {
                 // a row with an infinity or NaN has no finite result
                 const float back = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
@@ -542,39 +554,43 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
       }
     }
     if (lane == 0) p.merge[blockIdx.x] = mine;
-  } else if (warp < 4 + 4 * L::kHalves) {
-    // ---------------------------------------------------------------- softmax: thread = key, 16 rows per group
-    const int half = (warp - 4) >> 2, quarter = warp & 3;
+  } else if (warp < 4 + 4 * L::kGroups) {
+    // ---------------------------------------------------------------- softmax: thread = key, 8 rows per group
+    const int group = (warp - 4) >> 2, quarter = warp & 3, c0 = 8 * group;
     const int key = 32 * quarter + lane;
-    const uint32_t s_addr = tmem + ((uint32_t)(32 * quarter) << 16) + L::kTmemS + 16 * half;
-    const uint32_t p_addr = smem_u32(smem + L::kOffP) + (key >> 3) * 16 * N + (key & 7) * 16 + half * 128;
-    float* red = reinterpret_cast<float*>(smem + L::kOffRed) + half * 64;
-    float* sums = reinterpret_cast<float*>(smem + L::kOffSum) + half * 64;
-    const int bar = 1 + half;
+    const uint32_t s_addr = tmem + ((uint32_t)(32 * quarter) << 16) + L::kTmemS + 16 * group;
+    const uint32_t p_addr = smem_u32(smem + L::kOffP) + (key >> 3) * 8 * N + (key & 7) * 16 + group * 128;
+    float* red = reinterpret_cast<float*>(smem + L::kOffRed) + group * 32;
+    float* sums = reinterpret_cast<float*>(smem + L::kOffSum) + group * 32;
+    const int bar = 1 + group;
     int tl = 0, seg = 0;
     bool dead = false;
-    auto wait = [&](int idx, uint32_t parity) {  // `dead` stays the same in the whole warp
-      if (!dead) dead = !PA_WAIT(idx, parity);
-      dead = __any_sync(kAll, dead);
+    // `dead` stays the same in the whole warp
+    auto wait = [&](int idx, uint32_t parity) {
+      const bool ok = !dead && PA_WAIT(idx, parity);
+      dead = !__all_sync(kAll, ok);
     };
     while (tl < n_local && !dead) {
       const int sb = seg % L::kSegs;
       wait(L::kSegFull + sb, (seg / L::kSegs) & 1);
       if (dead) break;
       const Segment* sp = reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment));
-      const Columns<N>* cols = reinterpret_cast<const Columns<N>*>(smem + L::kOffCols + sb * sizeof(Columns<N>));
-      const int kt = sp->kt, n = sp->n, lo = sp->lo, hi = sp->hi, all_lo = sp->all_lo, all_hi = sp->all_hi;
-      float m[16], l[16];
+      const Columns<C>* cols = reinterpret_cast<const Columns<C>*>(smem + L::kOffCols + sb * sizeof(Columns<C>));
+      const int kt = sp->kt, n = sp->n;
+      float m[8], l[8];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
+      for (int c = 0; c < 8; ++c) {
         m[c] = kNoMax;
         l[c] = 0.f;
       }
       for (int i = 0; i < n; ++i, ++tl) {
-        const int buf = tl & 1, st = tl % L::kStages;
-        wait(L::kKFull + st, (tl / L::kStages) & 1);  // the tile's scales and flags
-        wait(L::kSFull + buf, (tl >> 1) & 1);
-        if (dead) break;
+        const int buf = tl & 1, st = tl % L::kStages, pb = tl % L::kPBufs;
+        {
+          // the tile's scales and flags (behind its K copies), and its S
+          const bool ok = PA_WAIT(L::kKFull + st, (tl / L::kStages) & 1) && PA_WAIT(L::kSFull + buf, (tl >> 1) & 1);
+          dead = !__all_sync(kAll, ok);
+          if (dead) break;
+        }
         tc_fence_after();
         uint32_t raw[16];
         tmem_ld16_sync(s_addr + buf * N, raw);
@@ -585,81 +601,78 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
         const float ks = meta[key >> 6];
         const int pages = reinterpret_cast<const int*>(meta)[4];
         const int j0 = (kt + i) * kKeyTile, j = j0 + key;
-        float x[16];
+        float x[8];
+        {
+          const float4 f0 = *reinterpret_cast<const float4*>(&cols->scale[c0]);
+          const float4 f1 = *reinterpret_cast<const float4*>(&cols->scale[c0 + 4]);
+          const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          const float4 f = *reinterpret_cast<const float4*>(&cols->scale[16 * half + 4 * c4]);
-          x[4 * c4] = __uint_as_float(raw[4 * c4]) * f.x * ks;
-          x[4 * c4 + 1] = __uint_as_float(raw[4 * c4 + 1]) * f.y * ks;
-          x[4 * c4 + 2] = __uint_as_float(raw[4 * c4 + 2]) * f.z * ks;
-          x[4 * c4 + 3] = __uint_as_float(raw[4 * c4 + 3]) * f.w * ks;
+          for (int c = 0; c < 8; ++c) x[c] = (__uint_as_float(raw[c]) + __uint_as_float(raw[8 + c])) * (f[c] * ks);
         }
         if (a.softcap > 0.f) {
           // cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))), to within a few 2^-23 cap
           const float to = 2.f * kLog2e / a.softcap, cap = a.softcap * kLog2e;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) x[c] = fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(x[c] * to)), cap);
+          for (int c = 0; c < 8; ++c) x[c] = fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(x[c] * to)), cap);
         }
         if (a.alibi_slopes) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            x[c] = fmaf(-cols->slope[16 * half + c], fabsf((float)(cols->pos[16 * half + c] - j)), x[c]);
+          for (int c = 0; c < 8; ++c)
+            x[c] = fmaf(-cols->slope[c0 + c], fabsf((float)(cols->pos[c0 + c] - j)), x[c]);
         }
-        const bool inside = j0 >= all_lo && j0 + kKeyTile <= all_hi && pages == 3;
+        const bool inside = j0 >= sp->all_lo && j0 + kKeyTile <= sp->all_hi && pages == 3;  // every row sees every key
+        bool zero_v = false;
         if (!inside) {
           const bool page_ok = (pages >> (key >> 6)) & 1;
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (!page_ok || j < cols->lo[16 * half + c] || j >= cols->hi[16 * half + c]) x[c] = -INFINITY;
+          for (int c = 0; c < 8; ++c)
+            if (!page_ok || j < cols->lo[c0 + c] || j >= cols->hi[c0 + c]) x[c] = -INFINITY;
+          // keys that no row sees may hold any codes: their V rows become zeros
+          zero_v = group == 0 && (j < sp->lo || j >= sp->hi);
+          if (__any_sync(kAll, zero_v)) wait(L::kVFull + st, (tl / L::kStages) & 1);
         }
         float over = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) over = fmaxf(over, x[c] - m[c]);
+        for (int c = 0; c < 8; ++c) over = fmaxf(over, x[c] - m[c]);
         const bool refresh = bar_any(bar, 128, over > kTop);
+        // the factors go to the summing warps: slot tl % 4 was read before P.V of tile tl - 2 could be issued
+        uint8_t* ref = smem + L::kOffRefs + (tl % L::kRefs) * L::kRef;
+        if (tl >= L::kPBufs) wait(L::kPFree + pb, (tl / L::kPBufs + 1) & 1);  // P.V has read this P buffer
+        if (dead) break;
         if (refresh) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
+          for (int c = 0; c < 8; ++c) {
             const float mx = warp_max(x[c] == x[c] ? x[c] : -INFINITY);
-            if (lane == c) red[quarter * 16 + c] = mx;
+            if (lane == c) red[quarter * 8 + c] = mx;
           }
           named_bar_sync(bar, 128);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float mx = fmaxf(fmaxf(red[c], red[16 + c]), fmaxf(red[32 + c], red[48 + c]));
+          for (int c = 0; c < 8; ++c) {
+            const float mx = fmaxf(fmaxf(red[c], red[8 + c]), fmaxf(red[16 + c], red[24 + c]));
+            float f = 1.f;
             if (mx - m[c] > kTop) {
               const float to = mx - kRefresh;
-              l[c] *= ex2_approx(m[c] - to);
+              f = ex2_approx(m[c] - to);
+              l[c] *= f;
               m[c] = to;
             }
+            if (quarter == 0 && lane == c) reinterpret_cast<float*>(ref)[c0 + c] = f;
           }
         }
-        uint32_t hw[8], lw[8];
+        if (quarter == 0 && lane == 0) {
+          reinterpret_cast<int*>(ref)[C + 2 + group] = refresh;
+          if (group == 0) *reinterpret_cast<float2*>(ref + 4 * C) = make_float2(meta[2], meta[3]);
+        }
+        uint32_t hw[4], lw[4];
 #pragma unroll
-        for (int c2 = 0; c2 < 8; ++c2) {
+        for (int c2 = 0; c2 < 4; ++c2) {
           const float p0 = ex2_approx(x[2 * c2] - m[2 * c2]), p1 = ex2_approx(x[2 * c2 + 1] - m[2 * c2 + 1]);
           l[2 * c2] += p0;
           l[2 * c2 + 1] += p1;
           split_p(p0, p1, hw[c2], lw[c2]);
         }
-        // the references go to the summing warps: slot tl % 4 was read before P.V of tile tl - 2 could be issued
-        uint8_t* ref = smem + L::kOffRefs + (tl % L::kRefs) * L::kRef;
-        if (tl > 0) wait(L::kPFree, (tl + 1) & 1);  // P.V of the previous tile has read P
-        // keys that no row sees may hold any codes: their V rows become zeros
-        const bool zero_v = half == 0 && (j < lo || j >= hi);
-        if (__any_sync(kAll, zero_v)) wait(L::kVFull + st, (tl / L::kStages) & 1);
-        if (dead) break;
-        if (quarter == 0 && lane < 16 && (refresh || i == 0)) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (lane == c) reinterpret_cast<float*>(ref)[16 * half + c] = m[c];
-        }
-        if (quarter == 0 && lane == 0) {
-          reinterpret_cast<int*>(ref)[N + 2 + half] = refresh || i == 0;
-          if (half == 0) *reinterpret_cast<float2*>(ref + 4 * N) = make_float2(meta[2], meta[3]);
-        }
-        st_shared_v4(p_addr, hw[0] | (hw[1] << 16), hw[2] | (hw[3] << 16), hw[4] | (hw[5] << 16), hw[6] | (hw[7] << 16));
-        st_shared_v4(p_addr + 8 * N, lw[0] | (lw[1] << 16), lw[2] | (lw[3] << 16), lw[4] | (lw[5] << 16),
-                     lw[6] | (lw[7] << 16));
+        st_shared_v4(p_addr + pb * L::kPBuf, hw[0] | (hw[1] << 16), hw[2] | (hw[3] << 16), lw[0] | (lw[1] << 16),
+                     lw[2] | (lw[3] << 16));
         if (zero_v) {
           const uint32_t v = smem_u32(smem + st * L::kStage + L::kKTile) + key * D;
 #pragma unroll
@@ -668,27 +681,27 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bars[L::kPFull]);
+          mbar_arrive(&bars[L::kPFull + pb]);
           if (quarter == 0) mbar_arrive(&bars[L::kRefFull + tl % L::kRefs]);
         }
       }
       if (dead) break;
       // the rows' sums over the segment's keys
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
+      for (int c = 0; c < 8; ++c) {
         float v = l[c];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-        if (lane == c) sums[quarter * 16 + c] = v;
+        if (lane == c) sums[quarter * 8 + c] = v;
       }
       named_bar_sync(bar, 128);
       if (quarter == 0) {
-        float* fin = reinterpret_cast<float*>(smem + L::kOffFin + (seg & 1) * 2 * N * 4) + 16 * half;
+        float* fin = reinterpret_cast<float*>(smem + L::kOffFin + (seg & 1) * 2 * C * 4) + c0;
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
+        for (int c = 0; c < 8; ++c)
           if (lane == c) {
             fin[c] = m[c];
-            fin[N + c] = (sums[c] + sums[16 + c]) + (sums[32 + c] + sums[48 + c]);
+            fin[C + c] = (sums[c] + sums[8 + c]) + (sums[16 + c] + sums[24 + c]);
           }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kFinFull + (seg & 1)]);
@@ -697,83 +710,76 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
       ++seg;
     }
   } else {
-    // ---------------------------------------------------------------- sums of O: thread = value column, N rows
+    // ---------------------------------------------------------------- sums of O: thread = value column, C rows
     const int quarter = warp & 3, d = 32 * quarter + lane;
     const uint32_t o_addr = tmem + ((uint32_t)(32 * quarter) << 16) + L::kTmemO;
     int tl = 0, seg = 0;
     bool dead = false;
     auto wait = [&](int idx, uint32_t parity) {
-      if (!dead) dead = !PA_WAIT(idx, parity);
-      dead = __any_sync(kAll, dead);
+      const bool ok = !dead && PA_WAIT(idx, parity);
+      dead = !__all_sync(kAll, ok);
     };
     while (tl < n_local && !dead) {
       const int sb = seg % L::kSegs;
       wait(L::kSegFull + sb, (seg / L::kSegs) & 1);
       if (dead) break;
-      const Segment s = *reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment));
-      float acc[N], m[N];
+      const Segment* sp = reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment));
+      const int n = sp->n;
+      float acc[C];
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
-        acc[c] = 0.f;
-        m[c] = kNoMax;
-      }
-      for (int i = 0; i < s.n; ++i, ++tl) {
+      for (int c = 0; c < C; ++c) acc[c] = 0.f;
+      for (int i = 0; i < n; ++i, ++tl) {
         const int buf = tl & 1;
         wait(L::kRefFull + tl % L::kRefs, (tl / L::kRefs) & 1);
         const uint8_t* ref = smem + L::kOffRefs + (tl % L::kRefs) * L::kRef;
-        const float2 vs = *reinterpret_cast<const float2*>(ref + 4 * N);
+        const float2 vs = *reinterpret_cast<const float2*>(ref + 4 * C);
 #pragma unroll
-        for (int half = 0; half < L::kHalves; ++half)
-          if (reinterpret_cast<const int*>(ref)[N + 2 + half]) {
+        for (int g = 0; g < L::kGroups; ++g)
+          if (reinterpret_cast<const int*>(ref)[C + 2 + g]) {
 #pragma unroll
-            for (int c = 16 * half; c < 16 * half + 16; ++c) {
-              const float to = reinterpret_cast<const float*>(ref)[c];
-              acc[c] *= ex2_approx(m[c] - to);
-              m[c] = to;
-            }
+            for (int c = 8 * g; c < 8 * g + 8; ++c) acc[c] *= reinterpret_cast<const float*>(ref)[c];
           }
         wait(L::kOFull + buf, (tl >> 1) & 1);
         if (dead) break;
         tc_fence_after();
 #pragma unroll
-        for (int half = 0; half < L::kHalves; ++half) {
-          uint32_t o0[16], o1[16];
-          tmem_ld16(o_addr + 2 * buf * N + 16 * half, o0);
-          tmem_ld16(o_addr + (2 * buf + 1) * N + 16 * half, o1);
-          tmem_ld_wait();
-          reg_fence16(o0);
-          reg_fence16(o1);
+        for (int g = 0; g < L::kGroups; ++g)
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            acc[16 * half + c] = fmaf(__uint_as_float(o0[c]), vs.x,
-                                      fmaf(__uint_as_float(o1[c]), vs.y, acc[16 * half + c]));
-        }
+          for (int blk = 0; blk < 2; ++blk) {
+            uint32_t o[16];
+            tmem_ld16_sync(o_addr + (2 * buf + blk) * N + 16 * g, o);
+            const float f = blk ? vs.y : vs.x;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              acc[8 * g + c] = fmaf(fmaf(__uint_as_float(o[8 + c]), 1.f / 16.f, __uint_as_float(o[c])), f, acc[8 * g + c]);
+          }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kOFree + buf]);
       }
       wait(L::kFinFull + (seg & 1), (seg >> 1) & 1);
       if (dead) break;
-      const float* fin = reinterpret_cast<const float*>(smem + L::kOffFin + (seg & 1) * 2 * N * 4);
-      const int rows = s.ntok * s.heads;
-      if (s.slot < 0) {
+      const float* fin = reinterpret_cast<const float*>(smem + L::kOffFin + (seg & 1) * 2 * C * 4);
+      const int heads = sp->heads, rows = sp->ntok * heads;
+      if (sp->slot < 0) {
+        const int t0 = sp->t0, h0 = sp->h0;
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
+        for (int c = 0; c < C; ++c) {
           if (c >= rows) break;
-          const float l = fin[N + c], inv = l == 0.f ? 0.f : 1.f / l;
-          const int64_t row = (int64_t)(s.t0 + c / s.heads) * a.H + s.h0 + c % s.heads;
+          const float l = fin[C + c], inv = l == 0.f ? 0.f : 1.f / l;
+          const int64_t row = (int64_t)(t0 + c / heads) * a.H + h0 + c % heads;
           if (D == 128 || d < D) static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16(acc[c] * inv);
           if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (fin[c] + log2f(l)) * kLn2;
         }
       } else {
-        const int64_t part = 2 * (int64_t)blockIdx.x + s.slot;
-        float* o = p.part_o + part * N * D;
+        const int64_t part = 2 * (int64_t)blockIdx.x + sp->slot;
+        float* o = p.part_o + part * C * D;
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
+        for (int c = 0; c < C; ++c) {
           if (c >= rows) break;
           if (D == 128 || d < D) o[c * D + d] = acc[c];
         }
-        if (d < 2 * N) p.part_ml[part * 2 * N + d] = fin[d];
+        if (d < 2 * C) p.part_ml[part * 2 * C + d] = fin[d];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[L::kSegFree + sb]);
@@ -792,7 +798,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kPerSm)
 // The units that several CTAs share: out = sum_i w_i O_i / sum_i w_i l_i, w_i =
 // 2^(m_i - max m), lse = max m + log2 of the latter sum.  One CTA per CTA that
 // began such a unit and group of rows; thread = value column.
-template <int D, int N>
+template <int D, int C>
 __global__ void __launch_bounds__(D) paged_merge_kernel(const __grid_constant__ Params p) {
   grid_dependency_wait();
   const PagedMerge u = p.merge[blockIdx.x];
@@ -802,14 +808,14 @@ __global__ void __launch_bounds__(D) paged_merge_kernel(const __grid_constant__ 
   auto part = [&](int i) { return i == 0 ? 2 * (int64_t)blockIdx.x + 1 : 2 * ((int64_t)blockIdx.x + i); };
   for (int c = blockIdx.y; c < rows; c += gridDim.y) {
     float top = kNoMax;
-    for (int i = 0; i < u.parts; ++i) top = fmaxf(top, p.part_ml[part(i) * 2 * N + c]);
+    for (int i = 0; i < u.parts; ++i) top = fmaxf(top, p.part_ml[part(i) * 2 * C + c]);
     float sum = 0.f, acc = 0.f;
 #pragma unroll 4
     for (int i = 0; i < u.parts; ++i) {
-      const float* ml = p.part_ml + part(i) * 2 * N + c;
+      const float* ml = p.part_ml + part(i) * 2 * C + c;
       const float w = ex2_approx(ml[0] - top);
-      sum = fmaf(w, ml[N], sum);
-      acc = fmaf(w, p.part_o[part(i) * N * D + c * D + d], acc);
+      sum = fmaf(w, ml[C], sum);
+      acc = fmaf(w, p.part_o[part(i) * C * D + c * D + d], acc);
     }
     const int64_t row = (int64_t)(u.t0 + c / u.heads) * p.a.H + u.h0 + c % u.heads;
     static_cast<__nv_bfloat16*>(p.a.out)[row * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
@@ -855,19 +861,19 @@ struct Sizes {
   int ctas;
   size_t merge, ml, o, bytes;  // offsets in the workspace, and its size
 };
-Sizes sizes(int N, int D, int num_sms) {
+Sizes sizes(int C, int D, int num_sms) {
   Sizes s;
-  s.ctas = num_sms * (N == 16 ? 2 : 1);
+  s.ctas = num_sms * (C <= 16 ? 2 : 1);
   s.merge = kWsStatusBytes;
   s.ml = s.merge + align256(sizeof(PagedMerge) * s.ctas);
-  s.o = s.ml + align256((size_t)2 * s.ctas * 2 * N * 4);
-  s.bytes = s.o + (size_t)2 * s.ctas * N * D * 4;
+  s.o = s.ml + align256((size_t)2 * s.ctas * 2 * C * 4);
+  s.bytes = s.o + (size_t)2 * s.ctas * C * D * 4;
   return s;
 }
 
-template <int D, int N>
+template <int D, int C>
 cudaError_t launch(const PagedAttnArgs& a, const Sizes& sz, cudaStream_t stream) {
-  using L = Lay<D, N>;
+  using L = Lay<D, C>;
   CUtensorMap k_map, v_map;
   const int64_t rows = a.NB * a.HK * kBlock;
   cudaError_t e = cache_map(&k_map, a.k_cache, rows, D);
@@ -877,18 +883,18 @@ cudaError_t launch(const PagedAttnArgs& a, const Sizes& sz, cudaStream_t stream)
   Params p{};
   p.a = a;
   p.G = a.H / a.HK;
-  p.cuts = (p.G + N - 1) / N;
+  p.cuts = (p.G + C - 1) / C;
   p.Gr = (p.G + p.cuts - 1) / p.cuts;
   p.HV = a.HK * p.cuts;
-  p.tq = std::max(1, N / p.Gr);
+  p.tq = std::max(1, C / p.Gr);
   p.ctas = sz.ctas;
   p.status = reinterpret_cast<int*>(ws);
   p.merge = reinterpret_cast<PagedMerge*>(ws + sz.merge);
   p.part_ml = reinterpret_cast<float*>(ws + sz.ml);
   p.part_o = reinterpret_cast<float*>(ws + sz.o);
-  e = cudaFuncSetAttribute(paged_attn_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  e = cudaFuncSetAttribute(paged_attn_kernel<D, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
-  paged_attn_kernel<D, N><<<(unsigned)p.ctas, L::kThreads, L::kSmem, stream>>>(p, k_map, v_map);
+  paged_attn_kernel<D, C><<<(unsigned)p.ctas, L::kThreads, L::kSmem, stream>>>(p, k_map, v_map);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -900,23 +906,27 @@ cudaError_t launch(const PagedAttnArgs& a, const Sizes& sz, cudaStream_t stream)
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, N>, p);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C>, p);
 }
 
 }  // namespace
 
-// N = 32 where 16 rows cannot hold the heads or the estimated tokens of a request: keys are then read
-// once for up to 32 rows.
-static int rows_for(int G, int max_query_len) { return (int64_t)G * std::max(1, max_query_len) <= 16 ? 16 : 32; }
+// Rows per query tile: the fewest that hold the heads of a K/V head and the estimated tokens of a request
+// (fewer rows: less softmax work per key; more: each key read once for all of them).
+static int rows_for(int G, int max_query_len) {
+  const int64_t rows = (int64_t)G * std::max(1, max_query_len);
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
 
 size_t paged_attention_workspace(int G, int D, int max_query_len, int num_sms) {
   return sizes(rows_for(G, max_query_len), D, num_sms).bytes;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int max_query_len, int num_sms, cudaStream_t stream) {
-  const int N = rows_for(a.H / a.HK, max_query_len);
-  const Sizes sz = sizes(N, a.D, num_sms);
-  if (N == 16) return a.D == 128 ? launch<128, 16>(a, sz, stream) : launch<64, 16>(a, sz, stream);
+  const int C = rows_for(a.H / a.HK, max_query_len);
+  const Sizes sz = sizes(C, a.D, num_sms);
+  if (C == 8) return a.D == 128 ? launch<128, 8>(a, sz, stream) : launch<64, 8>(a, sz, stream);
+  if (C == 16) return a.D == 128 ? launch<128, 16>(a, sz, stream) : launch<64, 16>(a, sz, stream);
   return a.D == 128 ? launch<128, 32>(a, sz, stream) : launch<64, 32>(a, sz, stream);
 }
 
