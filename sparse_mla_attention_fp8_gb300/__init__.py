@@ -18,7 +18,6 @@ The paged 8-bit K/V cache of layers with separate K and V heads:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import subprocess
@@ -527,33 +526,72 @@ class PagedBatch(NamedTuple):
     missing: Any           # int32 [1]
 
 
-@contextlib.contextmanager
-def _on(dev, stream):
-    """The tensors' device current (calls launch on the current device) and,
-    where the caller names a stream, that stream, so that what a call allocates
-    belongs to it."""
-    import torch
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield torch.cuda.current_stream(dev)
-        else:
-            with torch.cuda.stream(stream):
-                yield stream
+def _args(*specs):
+    """Checks the (name, tensor, dtype, shape) of a call's contiguous tensors
+    (None: not given); the device they are all on.  One pass, as single-token
+    steps are bound by the host."""
+    dev = -1
+    for name, t, dtype, shape in specs:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise SmlaError("all tensors must be CUDA tensors (there is no CPU path)")
+        if t.dtype != dtype:
+            raise SmlaError(f"{name}: dtype {t.dtype}, expected {dtype}")
+        if t.shape != shape:
+            raise SmlaError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+        if not t.is_contiguous():
+            raise SmlaError("all tensors must be contiguous")
+        d = t.get_device()
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise SmlaError("all tensors must be on the same device")
+    return dev
 
 
-def _rows(t, heads, D, name):
+def _rows(name, t, heads, D, dev):
     """Checks [T, heads, D] bf16 rows that may be slices of longer ones; their
     distance in elements."""
     import torch
     if not t.is_cuda:
         raise SmlaError("all tensors must be CUDA tensors (there is no CPU path)")
+    if t.get_device() != dev:
+        raise SmlaError("all tensors must be on the same device")
     if t.dtype != torch.bfloat16:
         raise SmlaError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
-        raise SmlaError(f"{name}: shape {tuple(t.shape)}, expected (T, {heads}, {D})")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise SmlaError(f"{name}: shape {tuple(shape)}, expected (T, {heads}, {D})")
+    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != D)):
         raise SmlaError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * D
+    return stride[0] if shape[0] > 1 else heads * D
+
+
+def _launch(dev, stream, body):
+    """body(raw stream) with the tensors' device current (the library launches
+    on the current device) and, where the caller names a stream, that stream,
+    so that what the call allocates belongs to it."""
+    import torch
+    if stream is None:
+        if dev == torch.cuda.current_device():
+            return body(torch._C._cuda_getCurrentRawStream(dev))
+        with torch.cuda.device(dev):
+            return body(torch._C._cuda_getCurrentRawStream(dev))
+    if stream.device.index != dev:
+        raise SmlaError("the stream must be on the tensors' device")
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _table_shape(block_table):
+    if block_table.dim() != 2:
+        raise SmlaError(f"block_table: shape {tuple(block_table.shape)}, expected (R, MB)")
+    return block_table.shape
 
 
 def paged_blocks_extend(context_lens, query_lens, block_table, free_blocks, free_count, num_tokens: int,
@@ -566,34 +604,35 @@ def paged_blocks_extend(context_lens, query_lens, block_table, free_blocks, free
     PagedBatch (`out`, if given; its seq_lens may be context_lens and its
     free_count the argument, which are then updated)."""
     import torch
-    dev = _dev(context_lens, query_lens, block_table, free_blocks, free_count, *(out or ()))
-    R, MB = block_table.shape
+    i32, i64 = torch.int32, torch.int64
+    R, MB = _table_shape(block_table)
     F, T = free_blocks.numel(), int(num_tokens)
-    i32 = torch.int32
-    _expect(context_lens, i32, (R,), "context_lens")
-    _expect(query_lens, i32, (R,), "query_lens")
-    _expect(block_table, i32, (R, MB), "block_table")
-    _expect(free_blocks, i32, (F,), "free_blocks")
-    _expect(free_count, i32, (1,), "free_count")
-    with _on(dev, stream) as on:
-        if out is None:
+    dev = _args(("context_lens", context_lens, i32, (R,)), ("query_lens", query_lens, i32, (R,)),
+                ("block_table", block_table, i32, (R, MB)), ("free_blocks", free_blocks, i32, (F,)),
+                ("free_count", free_count, i32, (1,)))
+    if out is not None:
+        out = PagedBatch(*out)
+        if dev != _args(("query_start", out.query_start, i32, (R + 1,)), ("seq_lens", out.seq_lens, i32, (R,)),
+                        ("req_id_per_token", out.req_id_per_token, i32, (T,)), ("positions", out.positions, i32, (T,)),
+                        ("slot_mapping", out.slot_mapping, i64, (T,)), ("free_count", out.free_count, i32, (1,)),
+                        ("missing", out.missing, i32, (1,))):
+            raise SmlaError("all tensors must be on the same device")
+
+    def body(on):
+        b = out
+        if b is None:
             n = max(T, 0)
-            start, lens, req, pos, left, lack = torch.empty(2 * R + 2 * n + 3, dtype=i32, device=dev).split(
+            device = block_table.device
+            start, lens, req, pos, left, lack = torch.empty(2 * R + 2 * n + 3, dtype=i32, device=device).split(
                 [R + 1, R, n, n, 1, 1])
-            out = PagedBatch(start, lens, req, pos, torch.empty(n, dtype=torch.int64, device=dev), left, lack)
-        else:
-            out = PagedBatch(*out)
-            for name, shape in (("query_start", R + 1), ("seq_lens", R), ("req_id_per_token", T), ("positions", T),
-                                ("free_count", 1), ("missing", 1)):
-                _expect(getattr(out, name), i32, (shape,), name)
-            _expect(out.slot_mapping, torch.int64, (T,), "slot_mapping")
-        rc = lib().paged_blocks_extend(
-            _ptr(context_lens), _ptr(query_lens), _ptr(block_table), _ptr(free_blocks), _ptr(free_count),
-            _ptr(out.query_start), _ptr(out.seq_lens), _ptr(out.req_id_per_token), _ptr(out.positions),
-            _ptr(out.slot_mapping), _ptr(out.free_count), _ptr(out.missing), R, MB, int(num_blocks), F, T,
-            ctypes.c_void_p(on.cuda_stream))
-    _check(rc, "paged_blocks_extend")
-    return out
+            b = PagedBatch(start, lens, req, pos, torch.empty(n, dtype=i64, device=device), left, lack)
+        _check(lib().paged_blocks_extend(
+            context_lens.data_ptr(), query_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(),
+            free_count.data_ptr(), b.query_start.data_ptr(), b.seq_lens.data_ptr(), b.req_id_per_token.data_ptr(),
+            b.positions.data_ptr(), b.slot_mapping.data_ptr(), b.free_count.data_ptr(), b.missing.data_ptr(), R, MB,
+            int(num_blocks), F, T, on), "paged_blocks_extend")
+        return b
+    return _launch(dev, stream, body)
 
 
 def paged_blocks_release(release, seq_lens, block_table, free_blocks, free_count, num_blocks: int, context_lens=None,
@@ -603,40 +642,25 @@ def paged_blocks_release(release, seq_lens, block_table, free_blocks, free_count
     [R]: 0 for them, seq_lens for the others; free_count int32 [1]); both may
     be written over the arguments of those meanings."""
     import torch
-    dev = _dev(release, seq_lens, block_table, free_blocks, free_count, context_lens, free_count_out)
-    R, MB = block_table.shape
+    i32 = torch.int32
+    R, MB = _table_shape(block_table)
     F = free_blocks.numel()
     if release.dtype not in (torch.bool, torch.uint8):
         raise SmlaError(f"release: dtype {release.dtype}, expected bool or uint8")
-    _expect(release, release.dtype, (R,), "release")
-    _expect(seq_lens, torch.int32, (R,), "seq_lens")
-    _expect(block_table, torch.int32, (R, MB), "block_table")
-    _expect(free_blocks, torch.int32, (F,), "free_blocks")
-    _expect(free_count, torch.int32, (1,), "free_count")
-    with _on(dev, stream) as on:
-        if context_lens is None:
-            context_lens = torch.empty(R, dtype=torch.int32, device=dev)
-        if free_count_out is None:
-            free_count_out = torch.empty(1, dtype=torch.int32, device=dev)
-        _expect(context_lens, torch.int32, (R,), "context_lens")
-        _expect(free_count_out, torch.int32, (1,), "free_count_out")
-        rc = lib().paged_blocks_release(_ptr(release), _ptr(seq_lens), _ptr(block_table), _ptr(free_blocks),
-                                        _ptr(free_count), _ptr(context_lens), _ptr(free_count_out), R, MB,
-                                        int(num_blocks), F, ctypes.c_void_p(on.cuda_stream))
-    _check(rc, "paged_blocks_release")
-    return context_lens, free_count_out
+    dev = _args(("release", release, release.dtype, (R,)), ("seq_lens", seq_lens, i32, (R,)),
+                ("block_table", block_table, i32, (R, MB)), ("free_blocks", free_blocks, i32, (F,)),
+                ("free_count", free_count, i32, (1,)), ("context_lens", context_lens, i32, (R,)),
+                ("free_count_out", free_count_out, i32, (1,)))
 
-
-def _paged_cache(k_cache, v_cache, k_scale, v_scale):
-    import torch
-    if k_cache.dim() != 4 or k_cache.shape[2] != 64:
-        raise SmlaError(f"k_cache: shape {tuple(k_cache.shape)}, expected (NB, HK, 64, D)")
-    NB, HK, _, D = k_cache.shape
-    _expect(k_cache, torch.uint8, (NB, HK, 64, D), "k_cache")
-    _expect(v_cache, torch.uint8, (NB, HK, 64, D), "v_cache")
-    _expect(k_scale, torch.float32, (NB, HK), "k_scale")
-    _expect(v_scale, torch.float32, (NB, HK), "v_scale")
-    return NB, HK, D
+    def body(on):
+        lens = torch.empty(R, dtype=i32, device=seq_lens.device) if context_lens is None else context_lens
+        left = torch.empty(1, dtype=i32, device=seq_lens.device) if free_count_out is None else free_count_out
+        _check(lib().paged_blocks_release(
+            release.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(),
+            free_count.data_ptr(), lens.data_ptr(), left.data_ptr(), R, MB, int(num_blocks), F, on),
+            "paged_blocks_release")
+        return lens, left
+    return _launch(dev, stream, body)
 
 
 def kv_cache_store_fp8(k, v, query_start, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale, stream=None):
@@ -645,22 +669,32 @@ def kv_cache_store_fp8(k, v, query_start, seq_lens, block_table, k_cache, v_cach
     [NB,HK]), modified in place.  query_start int32 [R+1], seq_lens int32 [R],
     block_table int32 [R,MB]."""
     import torch
-    dev = _dev(query_start, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale)
-    NB, HK, D = _paged_cache(k_cache, v_cache, k_scale, v_scale)
-    R, MB = block_table.shape
+    i32, u8, f32 = torch.int32, torch.uint8, torch.float32
+    R, MB = _table_shape(block_table)
+    NB, HK, D = _cache_shape(k_cache)
+    dev = _args(("query_start", query_start, i32, (R + 1,)), ("seq_lens", seq_lens, i32, (R,)),
+                ("block_table", block_table, i32, (R, MB)), ("k_cache", k_cache, u8, (NB, HK, 64, D)),
+                ("v_cache", v_cache, u8, (NB, HK, 64, D)), ("k_scale", k_scale, f32, (NB, HK)),
+                ("v_scale", v_scale, f32, (NB, HK)))
+    k_stride, v_stride = _rows("k", k, HK, D, dev), _rows("v", v, HK, D, dev)
     T = k.shape[0]
-    ks, vs = _rows(k, HK, D, "k"), _rows(v, HK, D, "v")
-    if v.shape[0] != T or k.device != dev or v.device != dev:
-        raise SmlaError("k and v must have the same tokens, on the device of the cache")
-    _expect(query_start, torch.int32, (R + 1,), "query_start")
-    _expect(seq_lens, torch.int32, (R,), "seq_lens")
-    _expect(block_table, torch.int32, (R, MB), "block_table")
-    with _on(dev, stream) as on:
-        rc = lib().kv_cache_store_fp8(_ptr(k), ks, _ptr(v), vs, _ptr(query_start), _ptr(seq_lens), _ptr(block_table),
-                                      _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), T, HK, D, R, MB, NB,
-                                      ctypes.c_void_p(on.cuda_stream))
-    _check(rc, "kv_cache_store_fp8")
+    if v.shape[0] != T:
+        raise SmlaError(f"k has {T} tokens, v {v.shape[0]}")
+
+    def body(on):
+        _check(lib().kv_cache_store_fp8(
+            k.data_ptr(), k_stride, v.data_ptr(), v_stride, query_start.data_ptr(), seq_lens.data_ptr(),
+            block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), T,
+            HK, D, R, MB, NB, on), "kv_cache_store_fp8")
+    _launch(dev, stream, body)
     return k_cache, v_cache, k_scale, v_scale
+
+
+def _cache_shape(cache):
+    if cache.dim() != 4 or cache.shape[2] != 64:
+        raise SmlaError(f"k_cache: shape {tuple(cache.shape)}, expected (NB, HK, 64, D)")
+    NB, HK, _, D = cache.shape
+    return NB, HK, D
 
 
 def paged_attention_fp8_workspace_bytes(T: int, H: int, HK: int, D: int, R: int, max_query_len: int) -> int:
@@ -679,41 +713,36 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
     workspace, if none is given, is allocated for the call.  Returns (out bf16
     [T,H,D], lse fp32 [T,H]); rows of no request are left as they were."""
     import torch
-    dev = _dev(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start, alibi_slopes, prefix_lens,
-               doc_start, out, lse, workspace)
-    NB, HK, D = _paged_cache(k_cache, v_cache, k_scale, v_scale)
-    R, MB = block_table.shape
+    i32, u8, f32, bf16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
+    R, MB = _table_shape(block_table)
+    NB, HK, D = _cache_shape(k_cache)
     T, H = q.shape[0], q.shape[1]
-    stride = _rows(q, H, D, "q")
-    if q.device != dev:
-        raise SmlaError("all tensors must be on the same device")
-    _expect(block_table, torch.int32, (R, MB), "block_table")
-    _expect(seq_lens, torch.int32, (R,), "seq_lens")
-    _expect(query_start, torch.int32, (R + 1,), "query_start")
-    if alibi_slopes is not None:
-        _expect(alibi_slopes, torch.float32, (H,), "alibi_slopes")
-    if prefix_lens is not None:
-        _expect(prefix_lens, torch.int32, (R,), "prefix_lens")
-    if doc_start is not None:
-        _expect(doc_start, torch.int32, (T,), "doc_start")
+    dev = _args(("k_cache", k_cache, u8, (NB, HK, 64, D)), ("v_cache", v_cache, u8, (NB, HK, 64, D)),
+                ("k_scale", k_scale, f32, (NB, HK)), ("v_scale", v_scale, f32, (NB, HK)),
+                ("block_table", block_table, i32, (R, MB)), ("seq_lens", seq_lens, i32, (R,)),
+                ("query_start", query_start, i32, (R + 1,)), ("alibi_slopes", alibi_slopes, f32, (H,)),
+                ("prefix_lens", prefix_lens, i32, (R,)), ("doc_start", doc_start, i32, (T,)),
+                ("out", out, bf16, (T, H, D)), ("lse", lse, f32, (T, H)))
+    stride = _rows("q", q, H, D, dev)
+    if workspace is not None and (not workspace.is_cuda or workspace.get_device() != dev or
+                                  not workspace.is_contiguous()):
+        raise SmlaError("workspace: must be contiguous, on the tensors' device")
     longest = max(1, T - R + 1) if max_query_len is None else int(max_query_len)
-    with _on(dev, stream) as on:
-        if out is None:
-            out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
-        if lse is None:
-            lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-        _expect(out, torch.bfloat16, (T, H, D), "out")
-        _expect(lse, torch.float32, (T, H), "lse")
-        if workspace is None:
-            workspace = torch.empty(paged_attention_fp8_workspace_bytes(T, H, HK, D, R, longest), dtype=torch.uint8,
-                                    device=dev)
-        rc = lib().paged_attention_fp8(
-            _ptr(q), stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-            _ptr(seq_lens), _ptr(query_start), float(sm_scale), longest, int(window), float(softcap),
-            _ptr(alibi_slopes), _ptr(prefix_lens), _ptr(doc_start), _ptr(out), _ptr(lse), T, H, HK, D, R, MB, NB,
-            _ptr(workspace), workspace.numel() * workspace.element_size(), ctypes.c_void_p(on.cuda_stream))
-    _check(rc, "paged_attention_fp8")
-    return out, lse
+
+    def body(on):
+        o = torch.empty((T, H, D), dtype=bf16, device=q.device) if out is None else out
+        l = torch.empty((T, H), dtype=f32, device=q.device) if lse is None else lse
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(lib().paged_attention_fp8_workspace_bytes(T, H, HK, D, R, longest), dtype=u8,
+                             device=q.device)
+        _check(lib().paged_attention_fp8(
+            q.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), query_start.data_ptr(), sm_scale, longest, window, softcap,
+            _address(alibi_slopes), _address(prefix_lens), _address(doc_start), o.data_ptr(), l.data_ptr(), T, H, HK,
+            D, R, MB, NB, ws.data_ptr(), ws.numel() * ws.element_size(), on), "paged_attention_fp8")
+        return o, l
+    return _launch(dev, stream, body)
 
 
 def read_noalloc_status(stream=None) -> int:

@@ -31,6 +31,8 @@
 //    P = 2^(x - m'), m' a running reference per row that is refreshed (to put
 //    the tile's maximum at 2^5.25) only when a tile exceeds 2^8.75, so a tile
 //    usually costs one vote of the warps instead of 8 maxima.
+//  * A segment's key tiles are taken from the last down: the nearest keys often
+//    weigh most (with distance biases always), so m' settles at once.
 //  * O^T of each tile is read from tensor memory and added, times the block's
 //    V scale, to sums in registers: no rescaling pass, any scales.
 //  * The key tiles of the whole call form one sequence (smla_paged.cuh) that
@@ -320,12 +322,12 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       if (dead) break;
       const Segment s = *reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment));
       const int32_t* row = a.block_table + (int64_t)s.r * a.MB;
-      // lane l holds block base + l of the row: its cache block (-1: none) and scales; the next 32 are
-      // fetched while these are in use
+      // lane l holds block base - l of the row (tiles are taken from the last down): its cache block (-1: none)
+      // and scales; the next 32 are fetched while these are in use
       auto fetch = [&](int page, int& b, float& ks, float& vs) {
         b = -1;
         ks = vs = 0.f;
-        if (page * kBlock < s.hi && (page + 1) * kBlock > s.lo) {
+        if (page >= 0 && page * kBlock < s.hi && (page + 1) * kBlock > s.lo) {
           const int x = __ldg(row + page);
           if (x >= 0 && x < a.NB) {
             b = x;
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       };
       int b, nb;
       float ks, vs, nks, nvs;
-      fetch(2 * s.kt + lane, b, ks, vs);
+      fetch(2 * (s.kt + s.n - 1) + 1 - lane, b, ks, vs);
       for (int i = 0; i < s.n && !dead; ++i, ++tl) {
         const int at = (2 * i) & 31;
         if (at == 0) {
@@ -345,11 +347,11 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
             ks = nks;
             vs = nvs;
           }
-          if (i + 16 < s.n) fetch(2 * (s.kt + i + 16) + lane, nb, nks, nvs);
+          if (i + 16 < s.n) fetch(2 * (s.kt + s.n - 1 - i - 16) + 1 - lane, nb, nks, nvs);
         }
-        const int b0 = __shfl_sync(kAll, b, at), b1 = __shfl_sync(kAll, b, at + 1);
-        const float k0 = __shfl_sync(kAll, ks, at), k1 = __shfl_sync(kAll, ks, at + 1);
-        const float v0 = __shfl_sync(kAll, vs, at), v1 = __shfl_sync(kAll, vs, at + 1);
+        const int b0 = __shfl_sync(kAll, b, at + 1), b1 = __shfl_sync(kAll, b, at);
+        const float k0 = __shfl_sync(kAll, ks, at + 1), k1 = __shfl_sync(kAll, ks, at);
+        const float v0 = __shfl_sync(kAll, vs, at + 1), v1 = __shfl_sync(kAll, vs, at);
         const int st = tl % L::kStages, use = tl / L::kStages;
         if (use > 0) dead = __any_sync(kAll, !PA_WAIT(L::kEmpty + st, (use + 1) & 1));
         if (dead) break;
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         const float* meta = reinterpret_cast<const float*>(smem + L::kOffMeta + (tl % L::kMeta) * 32);
         const float ks = meta[key >> 6];
         const int pages = reinterpret_cast<const int*>(meta)[4];
-        const int j0 = (kt + i) * kKeyTile, j = j0 + key;
+        const int j0 = (kt + n - 1 - i) * kKeyTile, j = j0 + key;
         float x[8];
         {
           const float4 f0 = *reinterpret_cast<const float4*>(&cols->scale[c0]);
@@ -617,8 +619,14 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         }
         if (a.alibi_slopes) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            x[c] = fmaf(-cols->slope[c0 + c], fabsf((float)(cols->pos[c0 + c] - j)), x[c]);
+          for (int c = 0; c < 8; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&cols->slope[c0 + c]);
+            const int4 at = *reinterpret_cast<const int4*>(&cols->pos[c0 + c]);
+            x[c] = fmaf(-f.x, (float)abs(at.x - j), x[c]);
+            x[c + 1] = fmaf(-f.y, (float)abs(at.y - j), x[c + 1]);
+            x[c + 2] = fmaf(-f.z, (float)abs(at.z - j), x[c + 2]);
+            x[c + 3] = fmaf(-f.w, (float)abs(at.w - j), x[c + 3]);
+          }
         }
         const bool inside = j0 >= sp->all_lo && j0 + kKeyTile <= sp->all_hi && pages == 3;  // every row sees every key
         bool zero_v = false;
