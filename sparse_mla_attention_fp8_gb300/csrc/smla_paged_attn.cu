@@ -805,30 +805,52 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
 
 // The units that several CTAs share: out = sum_i w_i O_i / sum_i w_i l_i, w_i =
 // 2^(m_i - max m), lse = max m + log2 of the latter sum.  One CTA per CTA that
-// began such a unit and group of rows; thread = value column.
+// began such a unit (blockIdx.x) and row of it (blockIdx.y); the weights by all
+// threads, then thread = value column (of a half of the parts at D = 64).
+// Bound by latency: three dependent reads, the parts' values in flight together.
+constexpr int kMergeThreads = 128, kMaxParts = 1024;
+
 template <int D, int C>
-__global__ void __launch_bounds__(D) paged_merge_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ Params p) {
+  __shared__ float weight[kMaxParts], red[kMergeThreads / 32], half_acc[D];
   grid_dependency_wait();
   const PagedMerge u = p.merge[blockIdx.x];
-  if (u.parts == 0) return;
-  const int d = threadIdx.x, rows = u.ntok * u.heads;
+  const int c = (int)blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  if (c >= u.ntok * u.heads || u.parts == 0) return;
   // the parts: slot 1 of this CTA, then slot 0 of the following ones
-  auto part = [&](int i) { return i == 0 ? 2 * (int64_t)blockIdx.x + 1 : 2 * ((int64_t)blockIdx.x + i); };
-  for (int c = blockIdx.y; c < rows; c += gridDim.y) {
-    float top = kNoMax;
-    for (int i = 0; i < u.parts; ++i) top = fmaxf(top, p.part_ml[part(i) * 2 * C + c]);
-    float sum = 0.f, acc = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < u.parts; ++i) {
-      const float* ml = p.part_ml + part(i) * 2 * C + c;
-      const float w = ex2_approx(ml[0] - top);
-      sum = fmaf(w, ml[C], sum);
-      acc = fmaf(w, p.part_o[part(i) * C * D + c * D + d], acc);
-    }
-    const int64_t row = (int64_t)(u.t0 + c / u.heads) * p.a.H + u.h0 + c % u.heads;
-    static_cast<__nv_bfloat16*>(p.a.out)[row * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
-    if (d == 0) p.a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  const int64_t first = 2 * (int64_t)blockIdx.x;
+  auto part = [&](int i) { return first + (i == 0 ? 1 : 2 * i); };
+  float top = kNoMax;
+  for (int i = lane; i < u.parts; i += 32) top = fmaxf(top, p.part_ml[part(i) * 2 * C + c]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+  float sum = 0.f;
+  for (int i = tid; i < u.parts; i += kMergeThreads) {
+    const float* ml = p.part_ml + part(i) * 2 * C + c;
+    const float w = ex2_approx(ml[0] - top);
+    weight[i] = w;
+    sum = fmaf(w, ml[C], sum);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  if (lane == 0) red[tid >> 5] = sum;
+  __syncthreads();
+  sum = (red[0] + red[1]) + (red[2] + red[3]);
+  constexpr int kSplit = kMergeThreads / D;
+  const int d = tid % D, half = tid / D;
+  const float* o = p.part_o + c * D + d;
+  float acc = 0.f;
+#pragma unroll 8
+  for (int i = half; i < u.parts; i += kSplit) acc = fmaf(weight[i], o[part(i) * C * D], acc);
+  if (kSplit == 2) {
+    if (half == 1) half_acc[d] = acc;
+    __syncthreads();
+    if (half == 1) return;
+    acc += half_acc[d];
+  }
+  const int64_t row = (int64_t)(u.t0 + c / u.heads) * p.a.H + u.h0 + c % u.heads;
+  static_cast<__nv_bfloat16*>(p.a.out)[row * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
+  if (d == 0) p.a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -871,7 +893,7 @@ struct Sizes {
 };
 Sizes sizes(int C, int D, int num_sms) {
   Sizes s;
-  s.ctas = num_sms * (C <= 16 ? 2 : 1);
+  s.ctas = std::min(num_sms * (C <= 16 ? 2 : 1), kMaxParts);
   s.merge = kWsStatusBytes;
   s.ml = s.merge + align256(sizeof(PagedMerge) * s.ctas);
   s.o = s.ml + align256((size_t)2 * s.ctas * 2 * C * 4);
@@ -909,8 +931,8 @@ cudaError_t launch(const PagedAttnArgs& a, const Sizes& sz, cudaStream_t stream)
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.ctas, 4);
-  cfg.blockDim = dim3(D);
+  cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)C);
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
