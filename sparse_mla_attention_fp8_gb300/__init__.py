@@ -33,7 +33,8 @@ LIB_PATH = os.path.join(_PKG, "libsmla.so")
 HEADER = os.path.join(_ROOT, "include", "smla.h")
 
 SOURCES = ["smla_decode.cu", "smla_attn.cu", "smla_wide.cu", "smla_wide8.cu", "smla_store.cu", "smla_nvfp4.cu", "smla_absorb.cu",
-           "smla_blocks.cu", "smla_kvstore.cu", "smla_paged_attn.cu", "smla_api.cu"]
+           "smla_blocks.cu", "smla_kvstore.cu", "smla_paged_attn.cu", "smla_paged_prefill.cu",
+           "smla_api.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17", "-lineinfo",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 

@@ -176,6 +176,8 @@ struct PagedAttnArgs {
   int T, H, HK, D, R, MB;
   int64_t NB;
 };
+// Many rows per query tile (smla_paged_prefill.cu); called by launch_paged_attention.
+cudaError_t launch_paged_prefill(const PagedAttnArgs& a, int num_sms, cudaStream_t stream);
 // G heads per K/V head; max_query_len an estimate.
 size_t paged_attention_workspace(int G, int D, int max_query_len, int num_sms);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int max_query_len, int num_sms, cudaStream_t stream);

@@ -19,15 +19,6 @@
 // A warp per (block, head, K or V) holds the block's new rows in registers
 // (one read of the input), so the kernel moves what it must: bound by HBM for
 // prefill, by latency for single tokens.
-#include <cstdint>
-#include <algorithm>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-
-#include "sm103_ptx.cuh"
-#include "smla_common.cuh"
-#include "smla_kernels.h"
 #include "smla_paged.cuh"
 
 namespace smla {
@@ -35,18 +26,12 @@ namespace smla {
 namespace {
 
 constexpr int kStoreWarps = 8;
-constexpr uint32_t kAll = 0xffffffffu;
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   uint16_t lo, hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
   return (uint32_t)lo | ((uint32_t)hi << 16);
-}
-__device__ __forceinline__ float2 e4m3x2_f32(uint32_t pair) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // |bf16| of both halves of w, 0 for infinities and NaN, into amax.

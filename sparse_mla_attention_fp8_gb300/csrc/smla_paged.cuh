@@ -3,8 +3,14 @@
 // tiles, and the search from a grid unit to its request.
 #pragma once
 #include <cstdint>
+#include <algorithm>
+#include <mutex>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "sm103_ptx.cuh"
 #include "smla_common.cuh"
 #include "smla_kernels.h"
 
@@ -52,24 +58,17 @@ struct PagedRequest {
   __device__ __forceinline__ int pos(int t) const { return len - t1 + t; }
   // visible keys [lo, hi) of row t
   __device__ __forceinline__ int hi(int t) const { return min(kmax, max(pos(t) + 1, prefix)); }
+  __device__ __forceinline__ int window_lo(const PagedAttnArgs& a, int t) const {
+    return a.window > 0 ? (int)max((int64_t)pos(t) - a.window + 1, (int64_t)0) : 0;
+  }
   __device__ __forceinline__ int lo(const PagedAttnArgs& a, int t) const {
-    int x = a.window > 0 ? max(0, (int)max((int64_t)pos(t) - a.window + 1, (int64_t)0)) : 0;
+    const int x = window_lo(a, t);
     return a.doc_start ? max(x, __ldg(a.doc_start + t)) : x;
   }
-  // Union [lo, hi) of the rows ta .. tb - 1's visible keys, and the keys
-  // [all_lo, all_hi) that all of them see.
-  __device__ __forceinline__ void range(const PagedAttnArgs& a, int ta, int tb, int& lo_, int& hi_, int& all_lo,
-                                        int& all_hi) const {
+  // Union [lo, hi) of the keys that rows ta .. tb - 1 see, documents aside.
+  __device__ __forceinline__ void range(const PagedAttnArgs& a, int ta, int tb, int& lo_, int& hi_) const {
+    lo_ = window_lo(a, ta);
     hi_ = hi(tb - 1);
-    all_hi = hi(ta);
-    lo_ = lo(a, ta);
-    all_lo = lo(a, tb - 1);
-    if (a.doc_start)
-      for (int t = ta; t < tb; ++t) {
-        const int x = lo(a, t);
-        lo_ = min(lo_, x);
-        all_lo = max(all_lo, x);
-      }
   }
 };
 
@@ -83,7 +82,8 @@ __device__ __forceinline__ void key_tiles(int lo, int hi, int& first, int& count
 // each), the K/V heads, the key tiles.  `ctas` CTAs take equal contiguous
 // ranges of it, so a query tile's keys may be split over consecutive CTAs:
 // each then leaves a partial result, and the first of them a record for the
-// merge.
+// merge.  Document starts do not count here (they are per token); a CTA skips
+// the tiles of its range that lie before all its rows' documents.
 __device__ __forceinline__ int64_t range_begin(int64_t c, int64_t total, int ctas) { return c * total / ctas; }
 // The CTA whose range holds tile x.
 __device__ __forceinline__ int range_of(int64_t x, int64_t total, int ctas) {
@@ -92,20 +92,376 @@ __device__ __forceinline__ int range_of(int64_t x, int64_t total, int ctas) {
 
 // One CTA's share of one (query tile, K/V head).
 struct Segment {
-  int r, g;          // request, K/V head
-  int h0, heads;     // query heads
-  int t0, ntok;      // rows
-  int pos0;          // position of row t0
-  int kt, n;         // key tiles kt .. kt + n - 1
-  int lo, hi;        // keys that some row sees
+  int n;               // key tiles; 0: the CTA's range has ended
+  int kt;              // the first of them (they are taken from the last down)
+  int r, g;            // request, K/V head
+  int h0, heads;       // query heads
+  int t0, ntok;        // rows
+  int lo, hi;          // keys that some row sees
   int all_lo, all_hi;  // keys that every row sees
-  int slot;          // partial result to write: 0 (begun by an earlier CTA), 1 (begun here), -1: the whole unit
-  int parts;         // slot 1: CTAs that share the unit
+  int slot;            // partial result to write: 0 (begun by an earlier CTA), 1 (begun here), -1: the whole unit
 };
 
-// A partial result's place: CTA c's slots 2 c and 2 c + 1.
+// A split unit, at the CTA that began it; its partial results are that CTA's
+// slot 1 and the following parts - 1 CTAs' slot 0 (CTA c: slots 2 c, 2 c + 1).
 struct PagedMerge {
   int t0, ntok, h0, heads, parts;  // parts = 0: no unit begun by this CTA is split
 };
+
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kTop = 8.75f;      // P = 2^(x - m') <= 2^8.75 < 430 (e4m3: 448)
+constexpr float kRefresh = 5.25f;  // a refreshed m' puts the tile's maximum at 2^5.25
+constexpr float kNoMax = -3e38f;   // m' of a row that has seen nothing
+
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
+  return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// True in every thread if it is in any of the `n` threads at the named barrier.
+__device__ __forceinline__ bool bar_any(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float warp_max(float x) {  // through an order-preserving map to integers; no NaN
+  int k = __float_as_int(x);
+  k = __reduce_max_sync(kAll, k >= 0 ? k : k ^ 0x7FFFFFFF);
+  return __int_as_float(k >= 0 ? k : k ^ 0x7FFFFFFF);
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_f32(uint32_t pair) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Offset of 16-byte chunk ch of row r, rows of D bytes under the D-byte swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t swz(int r, int ch) {
+  return (uint32_t)(r * D + ((D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4));
+}
+
+// mbar_wait with its slow part out of line: the roles' loops stay small.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* cta_abort, int* status) {
+  return mbar_wait(bar, parity, cta_abort, status, kDevWaitTimeout);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* cta_abort, int* status) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, cta_abort, status);
+}
+
+struct PagedParams {
+  PagedAttnArgs a;
+  // Rows of a query tile: tq tokens x up to Gr of the G heads of a K/V head; more than C heads are cut into
+  // `cuts` groups, which the sequence of units counts as K/V heads of their own (HV = HK * cuts).
+  int G, Gr, cuts, HV, tq;
+  int ctas;
+  int* status;
+  PagedMerge* merge;    // [ctas]
+  float* part_ml;       // [2 ctas][m' | l][C]
+  float* part_o;        // [2 ctas][C][D]
+};
+
+// Tiles of request r (over its query tiles and the K/V heads).
+__device__ __forceinline__ int64_t request_tiles(const PagedParams& p, int r) {
+  PagedRequest q;
+  q.load(p.a, r);
+  int64_t n = 0;
+  for (int t = q.t0; t < q.t1; t += p.tq) {
+    int lo, hi, first, count;
+    q.range(p.a, t, min(t + p.tq, q.t1), lo, hi);
+    key_tiles(lo, hi, first, count);
+    n += count;
+  }
+  return n * p.HV;
+}
+
+// Exclusive prefix sums of v[0 .. R-1] in place, the total in v[R]; all
+// threads.  v has room for a word per warp behind that.
+template <int kThreads>
+__device__ void scan_tiles(int64_t* v, int R) {
+  int64_t* warp_sum = v + R + 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (R + kThreads - 1) / kThreads;
+  const int beg = min(tid * per, R), end = min(beg + per, R);
+  int64_t sum = 0;
+  for (int i = beg; i < end; ++i) sum += v[i];
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(kAll, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int64_t run = inc - sum;
+  for (int w = 0; w < warp; ++w) run += warp_sum[w];
+  for (int i = beg; i < end; ++i) {
+    const int64_t x = v[i];
+    v[i] = run;
+    run += x;
+  }
+  if (tid == kThreads - 1) v[R] = run;
+  __syncthreads();
+}
+
+// This CTA's range of the sequence, and where it begins.
+struct PagedRange {
+  int64_t x0, x1, total, off0;  // off0: tiles of request r0 before x0
+  int ctas, r0;
+};
+
+// By all threads of the CTA; `prefix`: shared memory for R + 1 words and one
+// per warp.  r0 and off0 are valid in warp `walker` only.
+template <int kThreads>
+__device__ __forceinline__ PagedRange paged_range(const PagedParams& p, int64_t* prefix, int walker) {
+  const int R = p.a.R;
+  for (int r = threadIdx.x; r < R; r += kThreads) prefix[r] = request_tiles(p, r);
+  __syncthreads();
+  scan_tiles<kThreads>(prefix, R);
+  PagedRange g{};
+  g.total = prefix[R];
+  // with fewer tiles than CTAs the first CTAs take one each: a unit's parts are consecutive CTAs
+  g.ctas = (int)min((int64_t)p.ctas, g.total);
+  if ((int)blockIdx.x < g.ctas) {
+    g.x0 = range_begin(blockIdx.x, g.total, g.ctas);
+    g.x1 = range_begin((int64_t)blockIdx.x + 1, g.total, g.ctas);
+    if ((int)threadIdx.x >> 5 == walker) {
+      int hi = R;
+      while (hi - g.r0 > 1) {
+        const int mid = (g.r0 + hi) >> 1;
+        if (prefix[mid] <= g.x0) g.r0 = mid;
+        else hi = mid;
+      }
+      g.off0 = g.x0 - prefix[g.r0];
+    }
+  }
+  return g;
+}
+
+// Walks the range by one warp: emit(segment) for each segment in turn, until
+// it returns false.  Returns the record for the merge.
+template <typename F>
+__device__ __forceinline__ PagedMerge walk_segments(const PagedParams& p, const PagedRange& w, F emit) {
+  const PagedAttnArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  PagedMerge mine{0, 0, 0, 0, 0};
+  int64_t x = w.x0, off = w.off0;
+  for (int r = w.r0; x < w.x1 && r < a.R; ++r) {
+    PagedRequest q;
+    q.load(a, r);
+    for (int ta = q.t0; ta < q.t1 && x < w.x1; ta += p.tq) {
+      const int tb = min(ta + p.tq, q.t1);
+      Segment s;
+      q.range(a, ta, tb, s.lo, s.hi);
+      int first, count;
+      key_tiles(s.lo, s.hi, first, count);
+      if (off >= (int64_t)count * p.HV) {
+        off -= (int64_t)count * p.HV;
+        continue;
+      }
+      s.all_lo = q.window_lo(a, tb - 1);
+      s.all_hi = q.hi(ta);
+      if (a.doc_start) {
+        int least = 0x7fffffff, most = 0;
+        for (int t = ta + lane; t < tb; t += 32) {
+          const int y = max(0, q.lo(a, t));
+          least = min(least, y);
+          most = max(most, y);
+        }
+        s.lo = __reduce_min_sync(kAll, least);
+        s.all_lo = __reduce_max_sync(kAll, most);
+      }
+      if (s.hi <= s.lo) s.lo = s.hi = 0;  // nothing is seen: no block is read
+      s.r = r;
+      s.t0 = ta;
+      s.ntok = tb - ta;
+      for (int v = (int)(off / count); v < p.HV && x < w.x1; ++v) {
+        const int skip = (int)(off - (int64_t)v * count);  // tiles of this unit before this CTA's range
+        off = (int64_t)(v + 1) * count;
+        s.g = v / p.cuts;
+        s.h0 = s.g * p.G + v % p.cuts * p.Gr;
+        s.heads = min(p.Gr, p.G - v % p.cuts * p.Gr);
+        s.kt = first + skip;
+        s.n = (int)min((int64_t)(count - skip), w.x1 - x);
+        const bool ends = skip + s.n == count;
+        s.slot = skip == 0 ? (ends ? -1 : 1) : 0;
+        if (s.slot == 1)
+          mine = PagedMerge{ta, s.ntok, s.h0, s.heads,
+                            range_of(x + count - 1, w.total, w.ctas) - (int)blockIdx.x + 1};
+        x += s.n;
+        const int gone = min(s.lo / kKeyTile - s.kt, s.n - 1);  // one tile stays: the result is due
+        if (gone > 0) {
+          s.kt += gone;
+          s.n -= gone;
+        }
+        if (!emit(s)) return mine;
+      }
+      off = 0;
+    }
+  }
+  return mine;
+}
+
+// The units that several CTAs share: out = sum_i w_i O_i / sum_i w_i l_i, w_i =
+// 2^(m_i - max m), lse = max m + log2 of the latter sum.  One CTA per CTA that
+// began such a unit (blockIdx.x) and up to 16 CTAs for its rows; the weights by
+// all threads, then thread = value column (of a half of the parts at D = 64).
+// Bound by latency: three dependent reads, the parts' values in flight together.
+constexpr int kMergeThreads = 128, kMaxParts = 1024, kMergeRows = 16;
+
+template <int D, int C>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedParams p) {
+  __shared__ float weight[kMaxParts], red[kMergeThreads / 32], half_acc[D];
+  grid_dependency_wait();
+  const PagedMerge u = p.merge[blockIdx.x];
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (u.parts == 0) return;
+  // the parts: slot 1 of this CTA, then slot 0 of the following ones
+  const int64_t first = 2 * (int64_t)blockIdx.x;
+  auto part = [&](int i) { return first + (i == 0 ? 1 : 2 * i); };
+  for (int c = (int)blockIdx.y; c < u.ntok * u.heads; c += (int)gridDim.y) {
+    float top = kNoMax;
+    for (int i = lane; i < u.parts; i += 32) top = fmaxf(top, p.part_ml[part(i) * 2 * C + c]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    float sum = 0.f;
+    for (int i = tid; i < u.parts; i += kMergeThreads) {
+      const float* ml = p.part_ml + part(i) * 2 * C + c;
+      const float w = ex2_approx(ml[0] - top);
+      weight[i] = w;
+      sum = fmaf(w, ml[C], sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if (lane == 0) red[tid >> 5] = sum;
+    __syncthreads();
+    sum = (red[0] + red[1]) + (red[2] + red[3]);
+    constexpr int kSplit = kMergeThreads / D;
+    const int d = tid % D, half = tid / D;
+    const float* o = p.part_o + c * D + d;
+    float acc = 0.f;
+#pragma unroll 8
+    for (int i = half; i < u.parts; i += kSplit) acc = fmaf(weight[i], o[part(i) * C * D], acc);
+    if (kSplit == 2) {
+      if (half == 1) half_acc[d] = acc;
+      __syncthreads();
+      if (half == 0) acc += half_acc[d];
+    }
+    const int64_t row = (int64_t)(u.t0 + c / u.heads) * p.a.H + u.h0 + c % u.heads;
+    if (half == 0) static_cast<__nv_bfloat16*>(p.a.out)[row * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
+    if (tid == 0) p.a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    __syncthreads();  // the shared values have been read
+  }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// A cache as rows of D bytes, a box one block of one head, the D-byte swizzle;
+// rows behind the cache read as zeros.
+cudaError_t cache_map(CUtensorMap* m, const void* cache, int64_t rows, int D) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)D};
+  const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)kBlock}, es[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(cache), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The call's workspace: status word, merge records, partial m' and l, partial O.
+struct PagedSizes {
+  int ctas;
+  size_t merge, ml, o, bytes;
+};
+inline PagedSizes paged_sizes(int C, int D, int per_sm, int num_sms) {
+  PagedSizes s;
+  s.ctas = std::min(num_sms * per_sm, kMaxParts);
+  s.merge = kWsStatusBytes;
+  s.ml = s.merge + align256(sizeof(PagedMerge) * s.ctas);
+  s.o = s.ml + align256((size_t)2 * s.ctas * 2 * C * 4);
+  s.bytes = s.o + (size_t)2 * s.ctas * C * D * 4;
+  return s;
+}
+
+// Launches `kernel` (C rows per query tile) over the whole call, then the merge.
+template <int D, int C>
+cudaError_t launch_paged(void (*kernel)(const PagedParams, const CUtensorMap, const CUtensorMap), const PagedAttnArgs& a,
+                         int per_sm, int threads, int smem, int num_sms, cudaStream_t stream) {
+  const PagedSizes sz = paged_sizes(C, D, per_sm, num_sms);
+  CUtensorMap k_map, v_map;
+  const int64_t rows = a.NB * a.HK * kBlock;
+  cudaError_t e = cache_map(&k_map, a.k_cache, rows, D);
+  if (e == cudaSuccess) e = cache_map(&v_map, a.v_cache, rows, D);
+  if (e != cudaSuccess) return e;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  PagedParams p{};
+  p.a = a;
+  p.G = a.H / a.HK;
+  p.cuts = (p.G + C - 1) / C;
+  p.Gr = (p.G + p.cuts - 1) / p.cuts;
+  p.HV = a.HK * p.cuts;
+  p.tq = std::max(1, C / p.Gr);
+  p.ctas = sz.ctas;
+  p.status = reinterpret_cast<int*>(ws);
+  p.merge = reinterpret_cast<PagedMerge*>(ws + sz.merge);
+  p.part_ml = reinterpret_cast<float*>(ws + sz.ml);
+  p.part_o = reinterpret_cast<float*>(ws + sz.o);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, p, k_map, v_map);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)std::min(C, kMergeRows));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C>, p);
+}
+
+}  // namespace
 
 }  // namespace smla

@@ -42,64 +42,12 @@
 //  * Roles: TMA producer, QK^T issuer, P.V issuer, scheduler (segments ahead,
 //    their Q split and columns), C / 8 groups of 4 softmax warps, 4 warps
 //    that sum O.
-#include <cstdint>
-#include <algorithm>
-#include <mutex>
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-
-#include "sm103_ptx.cuh"
-#include "smla_common.cuh"
-#include "smla_kernels.h"
 #include "smla_paged.cuh"
 
 namespace smla {
 
 namespace {
 
-constexpr uint32_t kAll = 0xffffffffu;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kTop = 8.75f;      // P = 2^(x - m') <= 2^8.75 < 430 (e4m3: 448)
-constexpr float kRefresh = 5.25f;  // a refreshed m' puts the tile's maximum at 2^5.25
-constexpr float kNoMax = -3e38f;   // m' of a row that has seen nothing
-
-__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
-  return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// True in every thread if it is in any of the `n` threads at the named barrier.
-__device__ __forceinline__ bool bar_any(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ float warp_max(float x) {  // through an order-preserving map to integers; no NaN
-  int k = __float_as_int(x);
-  k = __reduce_max_sync(kAll, k >= 0 ? k : k ^ 0x7FFFFFFF);
-  return __int_as_float(k >= 0 ? k : k ^ 0x7FFFFFFF);
-}
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 e4m3x2_f32(uint32_t pair) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 // Two weights -> e4m3 codes hi and lo of p ~ hi + lo / 16 (low byte from x0).
 // The split runs in f16x2: 11 bits, more than the two terms keep.
 __device__ __forceinline__ void split_p(float x0, float x1, uint32_t& hi, uint32_t& lo) {
@@ -114,32 +62,6 @@ __device__ __forceinline__ void split_p(float x0, float x1, uint32_t& hi, uint32
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(t) : "r"(r));
   lo = t;
 }
-// Offset of 16-byte chunk ch of row r, rows of D bytes under the D-byte swizzle.
-template <int D>
-__device__ __forceinline__ uint32_t swz(int r, int ch) {
-  return (uint32_t)(r * D + ((D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4));
-}
-
-// mbar_wait with its slow part out of line: the roles' loops stay small.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* cta_abort, int* status) {
-  return mbar_wait(bar, parity, cta_abort, status, kDevWaitTimeout);
-}
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* cta_abort, int* status) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, cta_abort, status);
-}
-
-struct Params {
-  PagedAttnArgs a;
-  // Rows of a query tile: tq tokens x up to Gr of the G heads of a K/V head; more than C heads are cut into
-  // `cuts` groups, which the sequence of units counts as K/V heads of their own (HV = HK * cuts).
-  int G, Gr, cuts, HV, tq;
-  int ctas;
-  int* status;
-  PagedMerge* merge;    // [ctas]
-  float* part_ml;       // [2 ctas][m' | l][C]
-  float* part_o;        // [2 ctas][C][D]
-};
-
 // What a row needs of its own.
 template <int C>
 struct Columns {
@@ -192,52 +114,9 @@ struct Lay {
   static_assert((kMaxPagedRequests + 1 + kWarps) * 8 <= kStages * kStage, "prefix sums fit the stages");
 };
 
-// Tiles of request r (over its query tiles and the K/V heads).
-__device__ __forceinline__ int64_t request_tiles(const Params& p, int r) {
-  PagedRequest q;
-  q.load(p.a, r);
-  int64_t n = 0;
-  for (int t = q.t0; t < q.t1; t += p.tq) {
-    int lo, hi, al, ah, first, count;
-    q.range(p.a, t, min(t + p.tq, q.t1), lo, hi, al, ah);
-    key_tiles(lo, hi, first, count);
-    n += count;
-  }
-  return n * p.HV;
-}
-
-// Exclusive prefix sums of v[0 .. R-1] in place, the total in v[R]; all
-// threads.  v has room for a word per warp behind that.
-template <int kThreads>
-__device__ void scan_tiles(int64_t* v, int R) {
-  int64_t* warp_sum = v + R + 1;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (R + kThreads - 1) / kThreads;
-  const int beg = min(tid * per, R), end = min(beg + per, R);
-  int64_t sum = 0;
-  for (int i = beg; i < end; ++i) sum += v[i];
-  int64_t inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(kAll, inc, o);
-    if (lane >= o) inc += u;
-  }
-  if (lane == 31) warp_sum[warp] = inc;
-  __syncthreads();
-  int64_t run = inc - sum;
-  for (int w = 0; w < warp; ++w) run += warp_sum[w];
-  for (int i = beg; i < end; ++i) {
-    const int64_t x = v[i];
-    v[i] = run;
-    run += x;
-  }
-  if (tid == kThreads - 1) v[R] = run;
-  __syncthreads();
-}
-
 template <int D, int C>
 __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
-    paged_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap k_map,
+    paged_attn_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map) {
   using L = Lay<D, C>;
   constexpr int N = L::N;
@@ -270,7 +149,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     for (int i = 0; i < L::kRefs; ++i) mbar_init(&bars[L::kRefFull + i], L::kGroups);
     for (int i = 0; i < L::kSegs; ++i) {
       mbar_init(&bars[L::kSegFull + i], 1);
-      mbar_init(&bars[L::kSegFree + i], 1 + 1 + 4 * L::kGroups + 4);
+      mbar_init(&bars[L::kSegFree + i], 3 + 4 * L::kGroups + 4);
     }
     mbar_init(&bars[L::kDrainQk], 1);
     mbar_init(&bars[L::kDrainPv], 1);
@@ -281,29 +160,8 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
-  // prefix sums of the requests' tiles, in the stages' memory (before any copy lands there)
-  int64_t* prefix = reinterpret_cast<int64_t*>(smem);
-  for (int r = tid; r < a.R; r += L::kThreads) prefix[r] = request_tiles(p, r);
-  __syncthreads();
-  scan_tiles<L::kThreads>(prefix, a.R);
-  const int64_t total = prefix[a.R];
-  // with fewer tiles than CTAs the first CTAs take one each: a unit's parts are consecutive CTAs
-  const int ctas = (int)min((int64_t)p.ctas, total);
-  const bool idle = (int)blockIdx.x >= ctas;
-  const int64_t x0 = idle ? 0 : range_begin(blockIdx.x, total, ctas);
-  const int64_t x1 = idle ? 0 : range_begin((int64_t)blockIdx.x + 1, total, ctas);
-  const int n_local = (int)(x1 - x0);
-  int r0 = 0;
-  int64_t off0 = 0;
-  if (warp == 2 && n_local > 0) {  // the request of this CTA's first tile
-    int hi = a.R;
-    while (hi - r0 > 1) {
-      const int mid = (r0 + hi) >> 1;
-      if (prefix[mid] <= x0) r0 = mid;
-      else hi = mid;
-    }
-    off0 = x0 - prefix[r0];
-  }
+  grid_dependency_wait();  // everything above may overlap the preceding kernel's end
+  const PagedRange range = paged_range<L::kThreads>(p, reinterpret_cast<int64_t*>(smem), 2);
   fence_proxy_async_smem();  // the copies may overwrite the prefix sums
   tc_fence_before();
   __syncthreads();
@@ -316,11 +174,12 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     const int outside = (int)(a.NB * a.HK * kBlock);  // a row behind the cache: reads as zeros
     int tl = 0, seg = 0;
     bool dead = false;
-    while (tl < n_local && !dead) {
+    while (true) {
       const int sb = seg % L::kSegs;
       dead = __any_sync(kAll, !PA_WAIT(L::kSegFull + sb, (seg / L::kSegs) & 1));
       if (dead) break;
       const Segment s = *reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment));
+      if (s.n == 0) break;
       const int32_t* row = a.block_table + (int64_t)s.r * a.MB;
       // lane l holds block base - l of the row (tiles are taken from the last down): its cache block (-1: none)
       // and scales; the next 32 are fetched while these are in use
@@ -371,7 +230,8 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         }
         __syncwarp();
       }
-      if (lane == 0 && !dead) mbar_arrive(&bars[L::kSegFree + sb]);
+      if (dead) break;
+      if (lane == 0) mbar_arrive(&bars[L::kSegFree + sb]);
       ++seg;
     }
     // no copy may still be landing when the CTA exits
@@ -381,17 +241,18 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- QK^T issuer
-    if (lane == 0 && n_local > 0) {
+    if (lane == 0) {
       constexpr uint32_t id = idesc_e4m3(128, N, 0, 0);
       constexpr uint32_t lay = D == 128 ? kLayoutSw128 : kLayoutSw64;
       const uint64_t dk0 = make_sdesc(smem_u32(smem), 16, 8 * D, lay);
       const uint64_t dq0 = make_sdesc(smem_u32(smem + L::kOffQ), 16, 8 * D, lay);
       int tl = 0, seg = 0;
       bool dead = false;
-      while (tl < n_local && !dead) {
+      while (!dead) {
         const int sb = seg % L::kSegs;
         if (!PA_WAIT(L::kSegFull + sb, (seg / L::kSegs) & 1)) break;
         const int n = reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment))->n;
+        if (n == 0) break;
         const uint64_t dq = dq0 + (uint64_t)((sb * L::kQBuf) >> 4);
         for (int i = 0; i < n; ++i, ++tl) {
           const int st = tl % L::kStages, buf = tl & 1;
@@ -417,14 +278,23 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     __syncwarp();
   } else if (warp == 3) {
     // ---------------------------------------------------------------- P.V issuer
-    if (lane == 0 && n_local > 0) {
+    if (lane == 0) {
       constexpr uint32_t id = idesc_e4m3(128, N, 1, 1);
       // V: rows are keys, D-byte swizzle, read MN-major; at D = 64 the MMA's upper 64 rows read the same
       // columns again (atoms 0 bytes apart) and their results are not used
       const uint64_t dv0 = make_sdesc(smem_u32(smem + L::kKTile), 0, 8 * D, D == 128 ? kLayoutSw128 : kLayoutSw64);
       // P: core matrices of 8 keys x 16 columns, the N / 16 of 8 keys together
       const uint64_t dp0 = make_sdesc(smem_u32(smem + L::kOffP), 8 * N, 128, kLayoutNone);
-      for (int tl = 0; tl < n_local; ++tl) {
+      int tl = 0, seg = 0, left = 0;
+      for (;; ++tl, --left) {
+        if (left == 0) {  // the next segment's tiles
+          const int sb = seg % L::kSegs;
+          if (!PA_WAIT(L::kSegFull + sb, (seg / L::kSegs) & 1)) break;
+          left = reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment))->n;
+          if (left == 0) break;
+          mbar_arrive(&bars[L::kSegFree + sb]);
+          ++seg;
+        }
         const int st = tl % L::kStages, buf = tl & 1;
         const int pb = tl % L::kPBufs;
         if (!PA_WAIT(L::kPFull + pb, (tl / L::kPBufs) & 1) || !PA_WAIT(L::kVFull + st, (tl / L::kStages) & 1) ||
@@ -446,116 +316,83 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     __syncwarp();
   } else if (warp == 2) {
     // ---------------------------------------------------------------- scheduler
-    // Walks this CTA's range; for each segment: the record, the rows' columns
-    // and the two terms of Q.
-    PagedMerge mine{0, 0, 0, 0, 0};
-    if (n_local > 0) {
-      int r = r0, seg = 0;
-      int64_t x = x0, off = off0;
-      bool dead = false;
-      while (x < x1 && r < a.R && !dead) {
+    // For each segment: the record, the rows' columns and the two terms of Q.
+    int seg = 0;
+    bool dead = false;
+    const PagedMerge mine = walk_segments(p, range, [&](const Segment& s) {
+        const int sb = seg % L::kSegs;
+        if (seg >= L::kSegs) dead = __any_sync(kAll, !PA_WAIT(L::kSegFree + sb, (seg / L::kSegs + 1) & 1));
+        if (dead) return false;
+        if (lane == 0) *reinterpret_cast<Segment*>(smem + L::kOffSeg + sb * sizeof(Segment)) = s;
+        Columns<C>* cols = reinterpret_cast<Columns<C>*>(smem + L::kOffCols + sb * sizeof(Columns<C>));
+        const int rows = s.ntok * s.heads;
         PagedRequest q;
-        q.load(a, r);
-        for (int ta = q.t0; ta < q.t1 && x < x1 && !dead; ta += p.tq) {
-          const int tb = min(ta + p.tq, q.t1);
-          Segment s;
-          q.range(a, ta, tb, s.lo, s.hi, s.all_lo, s.all_hi);
-          int first, count;
-          key_tiles(s.lo, s.hi, first, count);
-          if (s.hi <= s.lo) s.lo = s.hi = 0;  // nothing is seen: no block is read
-          if (off >= (int64_t)count * p.HV) {
-            off -= (int64_t)count * p.HV;
-            continue;
-          }
-          s.r = r;
-          s.t0 = ta;
-          s.ntok = tb - ta;
-          s.pos0 = q.pos(ta);
-          for (int g = (int)(off / count); g < p.HV && x < x1; ++g) {
-            const int skip = (int)(off - (int64_t)g * count);  // tiles of this unit before this CTA's range
-            off = (int64_t)(g + 1) * count;
-            s.g = g / p.cuts;
-            s.h0 = s.g * p.G + g % p.cuts * p.Gr;
-            s.heads = min(p.Gr, p.G - g % p.cuts * p.Gr);
-            s.kt = first + skip;
-            s.n = (int)min((int64_t)(count - skip), x1 - x);
-            const bool ends = skip + s.n == count;
-            s.slot = skip == 0 ? (ends ? -1 : 1) : 0;
-            s.parts = 0;
-            if (s.slot == 1) {
-              s.parts = range_of(x + count - 1, total, ctas) - (int)blockIdx.x + 1;
-              mine = PagedMerge{ta, s.ntok, s.h0, s.heads, s.parts};
-            }
-            x += s.n;
-            const int sb = seg % L::kSegs;
-            if (seg >= L::kSegs) dead = __any_sync(kAll, !PA_WAIT(L::kSegFree + sb, (seg / L::kSegs + 1) & 1));
-            if (dead) break;
-            if (lane == 0) *reinterpret_cast<Segment*>(smem + L::kOffSeg + sb * sizeof(Segment)) = s;
-            Columns<C>* cols = reinterpret_cast<Columns<C>*>(smem + L::kOffCols + sb * sizeof(Columns<C>));
-            const int rows = s.ntok * s.heads;
-            if (lane < C) {
-              const int t = min(ta + lane / s.heads, tb - 1), h = s.h0 + lane % s.heads;
-              cols->pos[lane] = q.pos(t);
-              cols->lo[lane] = lane < rows ? q.lo(a, t) : 0;
-              cols->hi[lane] = lane < rows ? q.hi(t) : 0;
-              cols->slope[lane] = a.alibi_slopes && lane < rows ? __ldg(a.alibi_slopes + h) * kLog2e : 0.f;
-            }
-            // D / 8 lanes per row, 8 values each
-            constexpr int kLanes = D / 8, kRowsPer = 32 / kLanes;
-            const uint32_t qd = smem_u32(smem + L::kOffQ + sb * L::kQBuf);
-            const int sub = lane / kLanes, c = lane % kLanes;
-#pragma unroll 4
-            for (int i = 0; i < C / kRowsPer; ++i) {
-              const int row = i * kRowsPer + sub;
-              uint4 v = make_uint4(0u, 0u, 0u, 0u);
-              if (row < rows)
-                v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                         (int64_t)(ta + row / s.heads) * a.q_stride +
-                                                         (int64_t)(s.h0 + row % s.heads) * D) + c);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-              uint32_t amax = 0u;  // of the magnitudes' bits
-#pragma unroll
-              for (int k = 0; k < 4; ++k) amax = max(amax, max((w[k] << 16) & 0x7fffffffu, w[k] & 0x7fff0000u));
-#pragma unroll
-              for (int o = 1; o < kLanes; o <<= 1) amax = max(amax, __shfl_xor_sync(kAll, amax, o));
-              // 2^sh: amax = (1 + f) 2^e to at most 448 = 1.75 * 2^8
-              int sh = 8 - ((int)(amax >> 23) - 127) - ((amax & 0x7fffffu) > 0x600000u);
-              sh = amax == 0u ? 0 : min(sh, 120);
-              const float f = __uint_as_float((uint32_t)(sh + 127) << 23);
-              uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float y0 = __uint_as_float(w[k] << 16) * f, y1 = __uint_as_float(w[k] & 0xffff0000u) * f;
-                const uint32_t hc = e4m3x2(y0, y1);
-                const float2 back = e4m3x2_f32(hc);
-                hi[k >> 1] |= hc << (16 * (k & 1));
-                lo[k >> 1] |= e4m3x2(y0 - back.x, y1 - back.y) << (16 * (k & 1));
-              }
-              const int op = (row & ~7) + row;  // operand row: 16 b + row % 8, and the second term 8 behind
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op, c >> 1) + 8 * (c & 1)), "r"(hi[0]),
-                           "r"(hi[1])
-                           : "memory");
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op + 8, c >> 1) + 8 * (c & 1)), "r"(lo[0]),
-                           "r"(lo[1])
-                           : "memory");
-              if (c == 0) {
-                // a row with an infinity or NaN has no finite result
-                const float back = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
-                                                       : __uint_as_float((uint32_t)(127 - sh) << 23);
-                cols->scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f : kLog2e);
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[L::kSegFull + sb]);
-            ++seg;
-          }
-          off = 0;
+        q.load(a, s.r);
+        if (lane < C) {
+          const int t = s.t0 + min(lane / s.heads, s.ntok - 1), h = s.h0 + lane % s.heads;
+          cols->pos[lane] = q.pos(t);
+          cols->lo[lane] = lane < rows ? q.lo(a, t) : 0;
+          cols->hi[lane] = lane < rows ? q.hi(t) : 0;
+          cols->slope[lane] = a.alibi_slopes && lane < rows ? __ldg(a.alibi_slopes + h) * kLog2e : 0.f;
         }
-        ++r;
-      }
-    }
+        // D / 8 lanes per row, 8 values each
+        constexpr int kLanes = D / 8, kRowsPer = 32 / kLanes;
+        const uint32_t qd = smem_u32(smem + L::kOffQ + sb * L::kQBuf);
+        const int sub = lane / kLanes, c = lane % kLanes;
+#pragma unroll 4
+        for (int i = 0; i < C / kRowsPer; ++i) {
+          const int row = i * kRowsPer + sub;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (row < rows)
+            v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                     (int64_t)(s.t0 + row / s.heads) * a.q_stride +
+                                                     (int64_t)(s.h0 + row % s.heads) * D) + c);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t amax = 0u;  // of the magnitudes' bits
+#pragma unroll
+          for (int k = 0; k < 4; ++k) amax = max(amax, max((w[k] << 16) & 0x7fffffffu, w[k] & 0x7fff0000u));
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) amax = max(amax, __shfl_xor_sync(kAll, amax, o));
+          // 2^sh: amax = (1 + f) 2^e to at most 448 = 1.75 * 2^8
+          int sh = 8 - ((int)(amax >> 23) - 127) - ((amax & 0x7fffffu) > 0x600000u);
+          sh = amax == 0u ? 0 : min(sh, 120);
+          const float f = __uint_as_float((uint32_t)(sh + 127) << 23);
+          uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float y0 = __uint_as_float(w[k] << 16) * f, y1 = __uint_as_float(w[k] & 0xffff0000u) * f;
+            const uint32_t hc = e4m3x2(y0, y1);
+            const float2 back = e4m3x2_f32(hc);
+            hi[k >> 1] |= hc << (16 * (k & 1));
+            lo[k >> 1] |= e4m3x2(y0 - back.x, y1 - back.y) << (16 * (k & 1));
+          }
+          const int op = (row & ~7) + row;  // operand row: 16 b + row % 8, and the second term 8 behind
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op, c >> 1) + 8 * (c & 1)), "r"(hi[0]),
+                       "r"(hi[1])
+                       : "memory");
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op + 8, c >> 1) + 8 * (c & 1)), "r"(lo[0]),
+                       "r"(lo[1])
+                       : "memory");
+          if (c == 0) {
+            // a row with an infinity or NaN has no finite result
+            const float back = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
+                                                   : __uint_as_float((uint32_t)(127 - sh) << 23);
+            cols->scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f : kLog2e);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kSegFull + sb]);
+        ++seg;
+        return true;
+    });
     if (lane == 0) p.merge[blockIdx.x] = mine;
+    const int sb = seg % L::kSegs;
+    if (!dead && seg >= L::kSegs) dead = __any_sync(kAll, !PA_WAIT(L::kSegFree + sb, (seg / L::kSegs + 1) & 1));
+    if (lane == 0 && !dead) {
+      reinterpret_cast<Segment*>(smem + L::kOffSeg + sb * sizeof(Segment))->n = 0;
+      mbar_arrive(&bars[L::kSegFull + sb]);
+    }
   } else if (warp < 4 + 4 * L::kGroups) {
     // ---------------------------------------------------------------- softmax: thread = key, 8 rows per group
     const int group = (warp - 4) >> 2, quarter = warp & 3, c0 = 8 * group;
@@ -567,18 +404,21 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     const int bar = 1 + group;
     int tl = 0, seg = 0;
     bool dead = false;
-    // `dead` stays the same in the whole warp
+    // `dead` stays the same in the whole warp.  After a wait that ran out the loops go on without waiting to
+    // the end of the segment, where the threads of a barrier leave together: none is left behind at one.
     auto wait = [&](int idx, uint32_t parity) {
       const bool ok = !dead && PA_WAIT(idx, parity);
       dead = !__all_sync(kAll, ok);
     };
-    while (tl < n_local && !dead) {
+    while (true) {
       const int sb = seg % L::kSegs;
       wait(L::kSegFull + sb, (seg / L::kSegs) & 1);
+      dead = bar_any(bar, 128, dead);
       if (dead) break;
       const Segment* sp = reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment));
       const Columns<C>* cols = reinterpret_cast<const Columns<C>*>(smem + L::kOffCols + sb * sizeof(Columns<C>));
       const int kt = sp->kt, n = sp->n;
+      if (n == 0) break;
       float m[8], l[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -589,9 +429,9 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         const int buf = tl & 1, st = tl % L::kStages, pb = tl % L::kPBufs;
         {
           // the tile's scales and flags (behind its K copies), and its S
-          const bool ok = PA_WAIT(L::kKFull + st, (tl / L::kStages) & 1) && PA_WAIT(L::kSFull + buf, (tl >> 1) & 1);
+          const bool ok =
+              !dead && PA_WAIT(L::kKFull + st, (tl / L::kStages) & 1) && PA_WAIT(L::kSFull + buf, (tl >> 1) & 1);
           dead = !__all_sync(kAll, ok);
-          if (dead) break;
         }
         tc_fence_after();
         uint32_t raw[16];
@@ -646,7 +486,6 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         // the factors go to the summing warps: slot tl % 4 was read before P.V of tile tl - 2 could be issued
         uint8_t* ref = smem + L::kOffRefs + (tl % L::kRefs) * L::kRef;
         if (tl >= L::kPBufs) wait(L::kPFree + pb, (tl / L::kPBufs + 1) & 1);  // P.V has read this P buffer
-        if (dead) break;
         if (refresh) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -693,7 +532,6 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
           if (quarter == 0) mbar_arrive(&bars[L::kRefFull + tl % L::kRefs]);
         }
       }
-      if (dead) break;
       // the rows' sums over the segment's keys
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -727,12 +565,13 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       const bool ok = !dead && PA_WAIT(idx, parity);
       dead = !__all_sync(kAll, ok);
     };
-    while (tl < n_local && !dead) {
+    while (true) {
       const int sb = seg % L::kSegs;
       wait(L::kSegFull + sb, (seg / L::kSegs) & 1);
       if (dead) break;
       const Segment* sp = reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment));
       const int n = sp->n;
+      if (n == 0) break;
       float acc[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) acc[c] = 0.f;
@@ -803,161 +642,32 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
   }
 }
 
-// The units that several CTAs share: out = sum_i w_i O_i / sum_i w_i l_i, w_i =
-// 2^(m_i - max m), lse = max m + log2 of the latter sum.  One CTA per CTA that
-// began such a unit (blockIdx.x) and row of it (blockIdx.y); the weights by all
-// threads, then thread = value column (of a half of the parts at D = 64).
-// Bound by latency: three dependent reads, the parts' values in flight together.
-constexpr int kMergeThreads = 128, kMaxParts = 1024;
-
 template <int D, int C>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ Params p) {
-  __shared__ float weight[kMaxParts], red[kMergeThreads / 32], half_acc[D];
-  grid_dependency_wait();
-  const PagedMerge u = p.merge[blockIdx.x];
-  const int c = (int)blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-  if (c >= u.ntok * u.heads || u.parts == 0) return;
-  // the parts: slot 1 of this CTA, then slot 0 of the following ones
-  const int64_t first = 2 * (int64_t)blockIdx.x;
-  auto part = [&](int i) { return first + (i == 0 ? 1 : 2 * i); };
-  float top = kNoMax;
-  for (int i = lane; i < u.parts; i += 32) top = fmaxf(top, p.part_ml[part(i) * 2 * C + c]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-  float sum = 0.f;
-  for (int i = tid; i < u.parts; i += kMergeThreads) {
-    const float* ml = p.part_ml + part(i) * 2 * C + c;
-    const float w = ex2_approx(ml[0] - top);
-    weight[i] = w;
-    sum = fmaf(w, ml[C], sum);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-  if (lane == 0) red[tid >> 5] = sum;
-  __syncthreads();
-  sum = (red[0] + red[1]) + (red[2] + red[3]);
-  constexpr int kSplit = kMergeThreads / D;
-  const int d = tid % D, half = tid / D;
-  const float* o = p.part_o + c * D + d;
-  float acc = 0.f;
-#pragma unroll 8
-  for (int i = half; i < u.parts; i += kSplit) acc = fmaf(weight[i], o[part(i) * C * D], acc);
-  if (kSplit == 2) {
-    if (half == 1) half_acc[d] = acc;
-    __syncthreads();
-    if (half == 1) return;
-    acc += half_acc[d];
-  }
-  const int64_t row = (int64_t)(u.t0 + c / u.heads) * p.a.H + u.h0 + c % u.heads;
-  static_cast<__nv_bfloat16*>(p.a.out)[row * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
-  if (d == 0) p.a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
-// A cache as rows of D bytes, a box one block of one head, the D-byte swizzle;
-// rows behind the cache read as zeros.
-cudaError_t cache_map(CUtensorMap* m, const void* cache, int64_t rows, int D) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)D};
-  const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)kBlock}, es[2] = {1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(cache), dims, strides, box, es,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-
-struct Sizes {
-  int ctas;
-  size_t merge, ml, o, bytes;  // offsets in the workspace, and its size
-};
-Sizes sizes(int C, int D, int num_sms) {
-  Sizes s;
-  s.ctas = std::min(num_sms * (C <= 16 ? 2 : 1), kMaxParts);
-  s.merge = kWsStatusBytes;
-  s.ml = s.merge + align256(sizeof(PagedMerge) * s.ctas);
-  s.o = s.ml + align256((size_t)2 * s.ctas * 2 * C * 4);
-  s.bytes = s.o + (size_t)2 * s.ctas * C * D * 4;
-  return s;
-}
-
-template <int D, int C>
-cudaError_t launch(const PagedAttnArgs& a, const Sizes& sz, cudaStream_t stream) {
+cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t stream) {
   using L = Lay<D, C>;
-  CUtensorMap k_map, v_map;
-  const int64_t rows = a.NB * a.HK * kBlock;
-  cudaError_t e = cache_map(&k_map, a.k_cache, rows, D);
-  if (e == cudaSuccess) e = cache_map(&v_map, a.v_cache, rows, D);
-  if (e != cudaSuccess) return e;
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  Params p{};
-  p.a = a;
-  p.G = a.H / a.HK;
-  p.cuts = (p.G + C - 1) / C;
-  p.Gr = (p.G + p.cuts - 1) / p.cuts;
-  p.HV = a.HK * p.cuts;
-  p.tq = std::max(1, C / p.Gr);
-  p.ctas = sz.ctas;
-  p.status = reinterpret_cast<int*>(ws);
-  p.merge = reinterpret_cast<PagedMerge*>(ws + sz.merge);
-  p.part_ml = reinterpret_cast<float*>(ws + sz.ml);
-  p.part_o = reinterpret_cast<float*>(ws + sz.o);
-  e = cudaFuncSetAttribute(paged_attn_kernel<D, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
-  if (e != cudaSuccess) return e;
-  paged_attn_kernel<D, C><<<(unsigned)p.ctas, L::kThreads, L::kSmem, stream>>>(p, k_map, v_map);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)C);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C>, p);
+  return launch_paged<D, C>(paged_attn_kernel<D, C>, a, L::kPerSm, L::kThreads, L::kSmem, num_sms, stream);
+}
+
+// Rows per query tile: the fewest that hold the heads of a K/V head and the estimated tokens of a request
+// (fewer rows: less softmax work per key; more: each key read once for all of them).
+int rows_for(int G, int max_query_len) {
+  const int64_t rows = (int64_t)G * std::max(1, max_query_len);
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
 }
 
 }  // namespace
 
-// Rows per query tile: the fewest that hold the heads of a K/V head and the estimated tokens of a request
-// (fewer rows: less softmax work per key; more: each key read once for all of them).
-static int rows_for(int G, int max_query_len) {
-  const int64_t rows = (int64_t)G * std::max(1, max_query_len);
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-}
-
 size_t paged_attention_workspace(int G, int D, int max_query_len, int num_sms) {
-  return sizes(rows_for(G, max_query_len), D, num_sms).bytes;
+  const int C = rows_for(G, max_query_len);
+  return paged_sizes(C, D, C == 32 ? 1 : 2, num_sms).bytes;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int max_query_len, int num_sms, cudaStream_t stream) {
   const int C = rows_for(a.H / a.HK, max_query_len);
-  const Sizes sz = sizes(C, a.D, num_sms);
-  if (C == 8) return a.D == 128 ? launch<128, 8>(a, sz, stream) : launch<64, 8>(a, sz, stream);
-  if (C == 16) return a.D == 128 ? launch<128, 16>(a, sz, stream) : launch<64, 16>(a, sz, stream);
-  return a.D == 128 ? launch<128, 32>(a, sz, stream) : launch<64, 32>(a, sz, stream);
+  if (C == 128) return launch_paged_prefill(a, num_sms, stream);
+  if (C == 8) return a.D == 128 ? launch<128, 8>(a, num_sms, stream) : launch<64, 8>(a, num_sms, stream);
+  if (C == 16) return a.D == 128 ? launch<128, 16>(a, num_sms, stream) : launch<64, 16>(a, num_sms, stream);
+  return a.D == 128 ? launch<128, 32>(a, num_sms, stream) : launch<64, 32>(a, num_sms, stream);
 }
 
 }  // namespace smla
