@@ -157,9 +157,28 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
   return (uint32_t)(r * D + ((D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4));
 }
 
-// mbar_wait with its slow part out of line: the roles' loops stay small.
+// mbar_wait with its slow part out of line, so that the roles' loops stay
+// small, with a long suspension per probe, so that waiting warps leave the
+// issue slots to the others, and without a look at the (slow) clock before a
+// few probes have run out: the same time limit and abort flag.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* cta_abort, int* status) {
-  return mbar_wait(bar, parity, cta_abort, status, kDevWaitTimeout);
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok) return true;
+    if (*cta_abort) return false;
+    if (i < 16) continue;
+    if (i == 16) t0 = globaltimer_ns();
+    else if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+  }
+  *cta_abort = 1;
+  atomicCAS(status, 0, kDevWaitTimeout);
+  return false;
 }
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* cta_abort, int* status) {
   return mbar_try_wait(bar, parity) || wait_slow(bar, parity, cta_abort, status);
@@ -319,55 +338,62 @@ __device__ __forceinline__ PagedMerge walk_segments(const PagedParams& p, const 
 }
 
 // The units that several CTAs share: out = sum_i w_i O_i / sum_i w_i l_i, w_i =
-// 2^(m_i - max m), lse = max m + log2 of the latter sum.  One CTA per CTA that
-// began such a unit (blockIdx.x) and up to 16 CTAs for its rows; the weights by
-// all threads, then thread = value column (of a half of the parts at D = 64).
-// Bound by latency: three dependent reads, the parts' values in flight together.
-constexpr int kMergeThreads = 128, kMaxParts = 1024, kMergeRows = 16;
+// 2^(m_i - max m), lse = max m + log2 of the latter sum.  A warp per row of a
+// unit, D / 32 value columns a lane; blockIdx.x: the CTA that began the unit.
+// Bound by latency: two dependent reads, with the parts' values in flight
+// together and no exchange between warps.
+constexpr int kMergeThreads = 128, kMaxParts = 1024;
 
 template <int D, int C>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedParams p) {
-  __shared__ float weight[kMaxParts], red[kMergeThreads / 32], half_acc[D];
   grid_dependency_wait();
   const PagedMerge u = p.merge[blockIdx.x];
-  const int tid = threadIdx.x, lane = tid & 31;
-  if (u.parts == 0) return;
+  const int lane = threadIdx.x & 31, c = (int)blockIdx.y * (kMergeThreads / 32) + ((int)threadIdx.x >> 5);
+  if (c >= u.ntok * u.heads || u.parts == 0) return;
   // the parts: slot 1 of this CTA, then slot 0 of the following ones
   const int64_t first = 2 * (int64_t)blockIdx.x;
   auto part = [&](int i) { return first + (i == 0 ? 1 : 2 * i); };
-  for (int c = (int)blockIdx.y; c < u.ntok * u.heads; c += (int)gridDim.y) {
-    float top = kNoMax;
-    for (int i = lane; i < u.parts; i += 32) top = fmaxf(top, p.part_ml[part(i) * 2 * C + c]);
+  float top = kNoMax;
+  for (int i = lane; i < u.parts; i += 32) top = fmaxf(top, p.part_ml[part(i) * 2 * C + c]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    float sum = 0.f;
-    for (int i = tid; i < u.parts; i += kMergeThreads) {
-      const float* ml = p.part_ml + part(i) * 2 * C + c;
-      const float w = ex2_approx(ml[0] - top);
-      weight[i] = w;
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+  constexpr int kPer = D / 32;
+  float sum = 0.f, acc[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+  for (int base = 0; base < u.parts; base += 32) {
+    float w = 0.f;
+    if (base + lane < u.parts) {
+      const float* ml = p.part_ml + part(base + lane) * 2 * C + c;
+      w = ex2_approx(ml[0] - top);
       sum = fmaf(w, ml[C], sum);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (lane == 0) red[tid >> 5] = sum;
-    __syncthreads();
-    sum = (red[0] + red[1]) + (red[2] + red[3]);
-    constexpr int kSplit = kMergeThreads / D;
-    const int d = tid % D, half = tid / D;
-    const float* o = p.part_o + c * D + d;
-    float acc = 0.f;
+    const int n = min(32, u.parts - base);
 #pragma unroll 8
-    for (int i = half; i < u.parts; i += kSplit) acc = fmaf(weight[i], o[part(i) * C * D], acc);
-    if (kSplit == 2) {
-      if (half == 1) half_acc[d] = acc;
-      __syncthreads();
-      if (half == 0) acc += half_acc[d];
+    for (int j = 0; j < n; ++j) {
+      const float f = __shfl_sync(kAll, w, j);
+      const float* o = p.part_o + (part(base + j) * C + c) * D + kPer * lane;
+      if (kPer == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(o);
+        acc[0] = fmaf(f, v.x, acc[0]);
+        acc[1] = fmaf(f, v.y, acc[1]);
+        acc[kPer - 2] = fmaf(f, v.z, acc[kPer - 2]);
+        acc[kPer - 1] = fmaf(f, v.w, acc[kPer - 1]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(o);
+        acc[0] = fmaf(f, v.x, acc[0]);
+        acc[1] = fmaf(f, v.y, acc[1]);
+      }
     }
-    const int64_t row = (int64_t)(u.t0 + c / u.heads) * p.a.H + u.h0 + c % u.heads;
-    if (half == 0) static_cast<__nv_bfloat16*>(p.a.out)[row * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
-    if (tid == 0) p.a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-    __syncthreads();  // the shared values have been read
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t row = (int64_t)(u.t0 + c / u.heads) * p.a.H + u.h0 + c % u.heads;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.a.out) + row * D + kPer * lane);
+#pragma unroll
+  for (int k = 0; k < kPer / 2; ++k) dst[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  if (lane == 0) p.a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -436,7 +462,8 @@ cudaError_t launch_paged(void (*kernel)(const PagedParams, const CUtensorMap, co
   p.cuts = (p.G + C - 1) / C;
   p.Gr = (p.G + p.cuts - 1) / p.cuts;
   p.HV = a.HK * p.cuts;
-  p.tq = std::max(1, C / p.Gr);
+  // 256 rows are two halves of whole tokens
+  p.tq = C == 256 ? 2 * (128 / p.Gr) : std::max(1, C / p.Gr);
   p.ctas = sz.ctas;
   p.status = reinterpret_cast<int*>(ws);
   p.merge = reinterpret_cast<PagedMerge*>(ws + sz.merge);
@@ -456,7 +483,7 @@ cudaError_t launch_paged(void (*kernel)(const PagedParams, const CUtensorMap, co
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kernel, p, k_map, v_map);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)std::min(C, kMergeRows));
+  cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)(C / (kMergeThreads / 32)));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C>, p);

@@ -473,8 +473,8 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         if (!inside) {
           const bool page_ok = (pages >> (key >> 6)) & 1;
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (!page_ok || j < cols->lo[c0 + c] || j >= cols->hi[c0 + c]) x[c] = -INFINITY;
+          for (int c = 0; c < 8; ++c)  // (no branches)
+            x[c] = page_ok & (j >= cols->lo[c0 + c]) & (j < cols->hi[c0 + c]) ? x[c] : -INFINITY;
           // keys that no row sees may hold any codes: their V rows become zeros
           zero_v = group == 0 && (j < sp->lo || j >= sp->hi);
           if (__any_sync(kAll, zero_v)) wait(L::kVFull + st, (tl / L::kStages) & 1);
@@ -652,19 +652,19 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t stream) {
 // (fewer rows: less softmax work per key; more: each key read once for all of them).
 int rows_for(int G, int max_query_len) {
   const int64_t rows = (int64_t)G * std::max(1, max_query_len);
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 256;
 }
 
 }  // namespace
 
 size_t paged_attention_workspace(int G, int D, int max_query_len, int num_sms) {
   const int C = rows_for(G, max_query_len);
-  return paged_sizes(C, D, C == 32 ? 1 : 2, num_sms).bytes;
+  return paged_sizes(C, D, C <= 16 ? 2 : 1, num_sms).bytes;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int max_query_len, int num_sms, cudaStream_t stream) {
   const int C = rows_for(a.H / a.HK, max_query_len);
-  if (C == 128) return launch_paged_prefill(a, num_sms, stream);
+  if (C == 256) return launch_paged_prefill(a, num_sms, stream);
   if (C == 8) return a.D == 128 ? launch<128, 8>(a, num_sms, stream) : launch<64, 8>(a, num_sms, stream);
   if (C == 16) return a.D == 128 ? launch<128, 16>(a, num_sms, stream) : launch<64, 16>(a, num_sms, stream);
   return a.D == 128 ? launch<128, 32>(a, num_sms, stream) : launch<64, 32>(a, num_sms, stream);

@@ -162,24 +162,23 @@ def attention(q, kc, vc, ks, vs, table, lens, query_start, sm_scale, window=0, s
             for g in range(HK):
                 K = E4M3[kc[b, g, j % BLOCK]] * ks[b, g].astype(np.float64)[:, None]
                 V = E4M3[vc[b, g, j % BLOCK]] * vs[b, g].astype(np.float64)[:, None]
-                for h in range(g * G, g * G + G):
-                    qh = q[t, h].astype(np.float64)
-                    x = (K @ qh) * sm_scale
-                    if softcap:
-                        x = softcap * np.tanh(x / softcap)
-                    if slopes is not None:
-                        x = x - float(slopes[h]) * np.abs(pos - j)
-                    m = x.max()
-                    w = np.exp(x - m)
-                    total = w.sum()
-                    out[t, h] = w @ V / total
-                    lse[t, h] = m + np.log(total)
-                    dx = sm_scale * np.abs(qh).max() * np.abs(K).sum(1).max() * (2.0 ** -18 + 2.0 ** -16)
-                    dx += 2.0 ** -20 * (abs(m) + softcap + 32)
-                    big = np.abs(V).max(0)
-                    tol[t, h] = (2.0 ** -7 * (w @ np.abs(V)) / total + len(j) * 2.0 ** -24 * np.abs(V).max() / total
-                                 + 2.0 ** -8 * np.abs(out[t, h]) + 2 * dx * big)
-                    ltol[t, h] = dx
+                h = slice(g * G, g * G + G)
+                qh = q[t, h].astype(np.float64)
+                x = (qh @ K.T) * sm_scale
+                if softcap:
+                    x = softcap * np.tanh(x / softcap)
+                if slopes is not None:
+                    x = x - slopes[h].astype(np.float64)[:, None] * np.abs(pos - j)
+                m = x.max(1, keepdims=True)
+                w = np.exp(x - m)
+                total = w.sum(1, keepdims=True)
+                out[t, h] = w @ V / total
+                lse[t, h] = (m + np.log(total))[:, 0]
+                dx = sm_scale * np.abs(qh).max(1, keepdims=True) * np.abs(K).sum(1).max() * (2.0 ** -18 + 2.0 ** -16)
+                dx = dx + 2.0 ** -20 * (np.abs(m) + softcap + 32)
+                tol[t, h] = (2.0 ** -7 * (w @ np.abs(V)) / total + len(j) * 2.0 ** -24 * np.abs(V).max() / total
+                             + 2.0 ** -8 * np.abs(out[t, h]) + 2 * dx * np.abs(V).max(0))
+                ltol[t, h] = dx[:, 0]
     return out, lse, tol, ltol
 
 

@@ -284,6 +284,9 @@ ATTENTION = [
     (1, 12, 128, [100, 0], [60, 90], dict(alibi=True, softcap=10.0)),
     (1, 2, 128, [0, 50, 3], [150, 100, 2], dict(prefix=[100, 150, 0])),
     (2, 2, 64, [0, 130], [60, 3], dict(prefix=[60, 500], window=20, alibi=True)),
+    # many segments a CTA, with one and with two filled halves of a query tile, in turn
+    (60, 12, 64, [0, 400] * 4, [9, 30, 11, 1, 25, 4, 5, 40], {}),
+    (48, 8, 128, [300, 0, 900] * 3, [16, 17, 33, 1, 32, 15, 40, 2, 20], dict(softcap=30.0)),
 ]
 
 
