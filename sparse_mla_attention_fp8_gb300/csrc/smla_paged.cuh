@@ -79,10 +79,11 @@ __device__ __forceinline__ void key_tiles(int lo, int hi, int& first, int& count
 }
 
 // The sequence of key tiles of a call: requests, their query tiles (tq tokens
-// each), the K/V heads, the key tiles.  `ctas` CTAs take equal contiguous
-// ranges of it, so a query tile's keys may be split over consecutive CTAs:
-// each then leaves a partial result, and the first of them a record for the
-// merge.  Document starts do not count here (they are per token); a CTA skips
+// each), the K/V heads, the key tiles, each unit's (query tile's and head's)
+// behind unit_cost places that stand for its start and end.  `ctas` CTAs take
+// equal contiguous ranges of it, so a unit's keys may be split over consecutive
+// CTAs: each then leaves a partial result, and the first of them a record for
+// the merge.  Document starts do not count here (they are per token); a CTA skips
 // the tiles of its range that lie before all its rows' documents.
 __device__ __forceinline__ int64_t range_begin(int64_t c, int64_t total, int ctas) { return c * total / ctas; }
 // The CTA whose range holds tile x.
@@ -157,6 +158,26 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
   return (uint32_t)(r * D + ((D == 128 ? ch ^ (r & 7) : ch ^ ((r >> 1) & 3)) << 4));
 }
 
+// 8 bf16 values of a row whose largest magnitude has the bits amax, in two
+// e4m3 terms of q 2^s: s puts amax = (1 + f) 2^e to at most 448 = 1.75 * 2^8.
+// back = 2^-s, NaN for a row with an infinity or NaN: it has no finite result.
+__device__ __forceinline__ void split_q8(const uint32_t (&w)[4], uint32_t amax, uint32_t (&hi)[2], uint32_t (&lo)[2],
+                                         float& back) {
+  int s = 8 - ((int)(amax >> 23) - 127) - ((amax & 0x7fffffu) > 0x600000u);
+  s = amax == 0u ? 0 : min(s, 120);
+  const float f = __uint_as_float((uint32_t)(s + 127) << 23);
+  back = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - s) << 23);
+  hi[0] = hi[1] = lo[0] = lo[1] = 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float y0 = __uint_as_float(w[k] << 16) * f, y1 = __uint_as_float(w[k] & 0xffff0000u) * f;
+    const uint32_t c = e4m3x2(y0, y1);
+    const float2 d = e4m3x2_f32(c);
+    hi[k >> 1] |= c << (16 * (k & 1));
+    lo[k >> 1] |= e4m3x2(y0 - d.x, y1 - d.y) << (16 * (k & 1));
+  }
+}
+
 // mbar_wait with its slow part out of line, so that the roles' loops stay
 // small, with a long suspension per probe, so that waiting warps leave the
 // issue slots to the others, and without a look at the (slow) clock before a
@@ -190,13 +211,15 @@ struct PagedParams {
   // `cuts` groups, which the sequence of units counts as K/V heads of their own (HV = HK * cuts).
   int G, Gr, cuts, HV, tq;
   int ctas;
+  int unit_cost;        // what a segment costs beyond its tiles, in tiles
   int* status;
   PagedMerge* merge;    // [ctas]
   float* part_ml;       // [2 ctas][m' | l][C]
   float* part_o;        // [2 ctas][C][D]
+  float* q_scale;       // [T, H], of a q split beforehand
 };
 
-// Tiles of request r (over its query tiles and the K/V heads).
+// Places of request r in the sequence (over its query tiles and the K/V heads).
 __device__ __forceinline__ int64_t request_tiles(const PagedParams& p, int r) {
   PagedRequest q;
   q.load(p.a, r);
@@ -205,7 +228,7 @@ __device__ __forceinline__ int64_t request_tiles(const PagedParams& p, int r) {
     int lo, hi, first, count;
     q.range(p.a, t, min(t + p.tq, q.t1), lo, hi);
     key_tiles(lo, hi, first, count);
-    n += count;
+    n += count + p.unit_cost;
   }
   return n * p.HV;
 }
@@ -290,8 +313,9 @@ __device__ __forceinline__ PagedMerge walk_segments(const PagedParams& p, const 
       q.range(a, ta, tb, s.lo, s.hi);
       int first, count;
       key_tiles(s.lo, s.hi, first, count);
-      if (off >= (int64_t)count * p.HV) {
-        off -= (int64_t)count * p.HV;
+      const int len = count + p.unit_cost;  // places of a unit
+      if (off >= (int64_t)len * p.HV) {
+        off -= (int64_t)len * p.HV;
         continue;
       }
       s.all_lo = q.window_lo(a, tb - 1);
@@ -310,20 +334,22 @@ __device__ __forceinline__ PagedMerge walk_segments(const PagedParams& p, const 
       s.r = r;
       s.t0 = ta;
       s.ntok = tb - ta;
-      for (int v = (int)(off / count); v < p.HV && x < w.x1; ++v) {
-        const int skip = (int)(off - (int64_t)v * count);  // tiles of this unit before this CTA's range
-        off = (int64_t)(v + 1) * count;
+      for (int v = (int)(off / len); v < p.HV && x < w.x1; ++v) {
+        const int skip = (int)(off - (int64_t)v * len);  // places of this unit before this CTA's range
+        off = (int64_t)(v + 1) * len;
+        const int take = (int)min((int64_t)(len - skip), w.x1 - x);
+        const int64_t last = x + (len - skip) - 1;  // the unit's last place
+        x += take;
+        const int beg = max(0, skip - p.unit_cost), end = max(0, skip + take - p.unit_cost);  // tiles
+        if (beg == end) continue;
         s.g = v / p.cuts;
         s.h0 = s.g * p.G + v % p.cuts * p.Gr;
         s.heads = min(p.Gr, p.G - v % p.cuts * p.Gr);
-        s.kt = first + skip;
-        s.n = (int)min((int64_t)(count - skip), w.x1 - x);
-        const bool ends = skip + s.n == count;
-        s.slot = skip == 0 ? (ends ? -1 : 1) : 0;
+        s.kt = first + beg;
+        s.n = end - beg;
+        s.slot = beg == 0 ? (end == count ? -1 : 1) : 0;
         if (s.slot == 1)
-          mine = PagedMerge{ta, s.ntok, s.h0, s.heads,
-                            range_of(x + count - 1, w.total, w.ctas) - (int)blockIdx.x + 1};
-        x += s.n;
+          mine = PagedMerge{ta, s.ntok, s.h0, s.heads, range_of(last, w.total, w.ctas) - (int)blockIdx.x + 1};
         const int gone = min(s.lo / kKeyTile - s.kt, s.n - 1);  // one tile stays: the result is due
         if (gone > 0) {
           s.kt += gone;
@@ -445,16 +471,10 @@ inline PagedSizes paged_sizes(int C, int D, int per_sm, int num_sms) {
   return s;
 }
 
-// Launches `kernel` (C rows per query tile) over the whole call, then the merge.
-template <int D, int C>
-cudaError_t launch_paged(void (*kernel)(const PagedParams, const CUtensorMap, const CUtensorMap), const PagedAttnArgs& a,
-                         int per_sm, int threads, int smem, int num_sms, cudaStream_t stream) {
-  const PagedSizes sz = paged_sizes(C, D, per_sm, num_sms);
-  CUtensorMap k_map, v_map;
-  const int64_t rows = a.NB * a.HK * kBlock;
-  cudaError_t e = cache_map(&k_map, a.k_cache, rows, D);
-  if (e == cudaSuccess) e = cache_map(&v_map, a.v_cache, rows, D);
-  if (e != cudaSuccess) return e;
+// The parameters of a call with C rows per query tile, without those of a
+// split q; per_sm CTAs an SM.
+template <int C>
+PagedParams paged_params(const PagedAttnArgs& a, const PagedSizes& sz, int unit_cost) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   PagedParams p{};
   p.a = a;
@@ -465,28 +485,46 @@ cudaError_t launch_paged(void (*kernel)(const PagedParams, const CUtensorMap, co
   // 256 rows are two halves of whole tokens
   p.tq = C == 256 ? 2 * (128 / p.Gr) : std::max(1, C / p.Gr);
   p.ctas = sz.ctas;
+  p.unit_cost = unit_cost;
   p.status = reinterpret_cast<int*>(ws);
   p.merge = reinterpret_cast<PagedMerge*>(ws + sz.merge);
   p.part_ml = reinterpret_cast<float*>(ws + sz.ml);
   p.part_o = reinterpret_cast<float*>(ws + sz.o);
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  return p;
+}
+
+// A launch that may overlap the preceding kernel's end (the kernels wait for it
+// before they touch global memory).
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                              const Args&... args) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, p, k_map, v_map);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)(C / (kMergeThreads / 32)));
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, int C>
+cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
+  return launch_overlapped(paged_merge_kernel<D, C>, dim3((unsigned)p.ctas, (unsigned)(C / (kMergeThreads / 32))),
+                           kMergeThreads, 0, stream, p);
+}
+
+cudaError_t cache_maps(const PagedAttnArgs& a, CUtensorMap* k_map, CUtensorMap* v_map) {
+  const int64_t rows = a.NB * a.HK * kBlock;
+  const cudaError_t e = cache_map(k_map, a.k_cache, rows, a.D);
+  return e == cudaSuccess ? cache_map(v_map, a.v_cache, rows, a.D) : e;
 }
 
 }  // namespace

@@ -353,19 +353,9 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
           for (int k = 0; k < 4; ++k) amax = max(amax, max((w[k] << 16) & 0x7fffffffu, w[k] & 0x7fff0000u));
 #pragma unroll
           for (int o = 1; o < kLanes; o <<= 1) amax = max(amax, __shfl_xor_sync(kAll, amax, o));
-          // 2^sh: amax = (1 + f) 2^e to at most 448 = 1.75 * 2^8
-          int sh = 8 - ((int)(amax >> 23) - 127) - ((amax & 0x7fffffu) > 0x600000u);
-          sh = amax == 0u ? 0 : min(sh, 120);
-          const float f = __uint_as_float((uint32_t)(sh + 127) << 23);
-          uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float y0 = __uint_as_float(w[k] << 16) * f, y1 = __uint_as_float(w[k] & 0xffff0000u) * f;
-            const uint32_t hc = e4m3x2(y0, y1);
-            const float2 back = e4m3x2_f32(hc);
-            hi[k >> 1] |= hc << (16 * (k & 1));
-            lo[k >> 1] |= e4m3x2(y0 - back.x, y1 - back.y) << (16 * (k & 1));
-          }
+          uint32_t hi[2], lo[2];
+          float back;
+          split_q8(w, amax, hi, lo, back);
           const int op = (row & ~7) + row;  // operand row: 16 b + row % 8, and the second term 8 behind
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op, c >> 1) + 8 * (c & 1)), "r"(hi[0]),
                        "r"(hi[1])
@@ -373,12 +363,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op + 8, c >> 1) + 8 * (c & 1)), "r"(lo[0]),
                        "r"(lo[1])
                        : "memory");
-          if (c == 0) {
-            // a row with an infinity or NaN has no finite result
-            const float back = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
-                                                   : __uint_as_float((uint32_t)(127 - sh) << 23);
-            cols->scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f : kLog2e);
-          }
+          if (c == 0) cols->scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f : kLog2e);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -642,10 +627,18 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
   }
 }
 
+// Places of a unit beside its tiles: about what its start and end take.
+constexpr int kUnitCost = 1;
+
 template <int D, int C>
 cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t stream) {
   using L = Lay<D, C>;
-  return launch_paged<D, C>(paged_attn_kernel<D, C>, a, L::kPerSm, L::kThreads, L::kSmem, num_sms, stream);
+  CUtensorMap k_map, v_map;
+  cudaError_t e = cache_maps(a, &k_map, &v_map);
+  if (e != cudaSuccess) return e;
+  const PagedParams p = paged_params<C>(a, paged_sizes(C, D, L::kPerSm, num_sms), kUnitCost);
+  e = launch_overlapped(paged_attn_kernel<D, C>, dim3((unsigned)p.ctas), L::kThreads, L::kSmem, stream, p, k_map, v_map);
+  return e == cudaSuccess ? launch_merge<D, C>(p, stream) : e;
 }
 
 // Rows per query tile: the fewest that hold the heads of a K/V head and the estimated tokens of a request
@@ -657,9 +650,9 @@ int rows_for(int G, int max_query_len) {
 
 }  // namespace
 
-size_t paged_attention_workspace(int G, int D, int max_query_len, int num_sms) {
-  const int C = rows_for(G, max_query_len);
-  return paged_sizes(C, D, C <= 16 ? 2 : 1, num_sms).bytes;
+size_t paged_attention_workspace(int T, int H, int HK, int D, int max_query_len, int num_sms) {
+  const int C = rows_for(H / HK, max_query_len);
+  return C == 256 ? paged_prefill_workspace(T, H, D, num_sms) : paged_sizes(C, D, C <= 16 ? 2 : 1, num_sms).bytes;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int max_query_len, int num_sms, cudaStream_t stream) {

@@ -18,12 +18,15 @@
 //    2^-25.
 //  * Softmax: thread pair = row, each thread the keys of one block (one K
 //    scale).  P = 2^(x - m') with the row's running reference m', computed in one
-//    pass over S into registers; only if some weight passes 2^15 is m' refreshed
-//    (to put the tile's largest at 2^2), O scaled in tensor memory and the pass
-//    repeated.
+//    pass over S into registers.  m' starts at 0 and stays there while the row's
+//    logits lie where f16 is exact enough; only if some weight passes 2^15, or a
+//    row's first keys all lie below 2^-6, is it refreshed (to put the tile's
+//    largest at 2^2), O scaled in tensor memory and the pass repeated.
 //  * P overwrites S in tensor memory and enters P V from there.
+//  * q is split by a kernel beforehand, so that a segment's Q is one copy that
+//    overlaps the end of the segment before.
 //  * Roles: TMA producer, MMA issuer, scheduler, 4 warps converting V, 8 softmax
-//    warps per half, which also split Q and write the results.
+//    warps per half, which also write the results.
 #include "smla_paged.cuh"
 
 namespace smla {
@@ -33,6 +36,9 @@ namespace {
 constexpr int kRows = 128;          // rows of a half
 constexpr float kTop16 = 15.f;      // P = 2^(x - m') <= 2^15 (f16: 65504)
 constexpr float kRefresh16 = 2.f;   // a refreshed m' puts the tile's maximum at 2^2
+constexpr float kLow16 = -6.f;      // a row that begins below 2^-6 is refreshed
+// Places of a unit beside its tiles: about what its start and end take.
+constexpr int kUnitCost = 3;
 
 // (a.x, a.y) * (b.x, b.y) + (c.x, c.y) and sums, two at a time.
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
@@ -76,28 +82,65 @@ struct PreLay {
   static constexpr int kOffQ = kOffV16 + 2 * kV16;
   static constexpr int kOffMeta = kOffQ + 2 * kQHalf;
   static constexpr int kOffRed = kOffMeta + kMeta * 32;            // float [2 halves][2][128] maxima
-  static constexpr int kOffSum = kOffRed + 4 * kRows * 4;          // float [2 halves][2][128] sums, and Q's maxima
+  static constexpr int kOffSum = kOffRed + 4 * kRows * 4;          // float [2 halves][2][128] sums
   static constexpr int kOffRef = kOffSum + 4 * kRows * 4;          // float [segs] largest v scale
   static constexpr int kOffSeg = kOffRef + 16;
   static constexpr int kOffBar = (kOffSeg + kSegs * (int)sizeof(Segment) + 7) / 8 * 8;
   enum {
     kKFull = 0, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages, kVEmpty = kVFull + kVStages,
     kMetaFull = kVEmpty + kVStages, kV16Full = kMetaFull + kMeta, kV16Empty = kV16Full + 2, kSFull = kV16Empty + 2,
-    kPFull = kSFull + 2, kPvDone = kPFull + 2, kQFull = kPvDone + 2, kSegFull = kQFull + 2,
+    kPFull = kSFull + 2, kPvDone = kPFull + 2, kQFull = kPvDone + 2, kQEmpty = kQFull + 2, kOFree = kQEmpty + 2,
+    kSegFull = kOFree + 2,
     kSegFree = kSegFull + kSegs, kDrain = kSegFree + kSegs, kNumBars
   };
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;
   static constexpr int kTmemS = 0, kTmemO = 256, kTmemCols = 512;  // S of the halves, O of the halves: 128 columns each
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert((kMaxPagedRequests + 1 + kWarps) * 8 <= kOffMeta, "prefix sums fit the operands' memory");
+  static_assert((kMaxPagedRequests + 1 + kWarps) * 8 <= kOffQ, "prefix sums fit the memory before Q");
   static_assert(kKTile % 1024 == 0 && kV16 % 1024 == 0 && kQTerm % 1024 == 0, "operand alignment");
 };
+
+// q in two e4m3 terms per (token, head): q 2^s = hi + lo, s such that the row's
+// largest comes near 448.  terms [2][T, H, D]; scale [T, H] = what turns a
+// product with K codes into a logit, but for the block's K scale.  D / 8 lanes
+// per row, 8 values each; bound by HBM.
+constexpr int kSplitThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kSplitThreads)
+    paged_split_q_kernel(const __grid_constant__ PagedAttnArgs a, uint8_t* __restrict__ terms, float* __restrict__ scale) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  constexpr int kLanes = D / 8;
+  const int64_t rows = (int64_t)a.T * a.H, row0 = (int64_t)clamp_start(a.query_start, 0, a.T) * a.H;
+  const int64_t row1 = (int64_t)clamp_start(a.query_start, a.R, a.T) * a.H;
+  const int64_t row = ((int64_t)blockIdx.x * kSplitThreads + threadIdx.x) / kLanes;
+  const int c = threadIdx.x % kLanes;
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  const bool mine = row >= row0 && row < row1;
+  if (mine)
+    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row / a.H * a.q_stride +
+                                             row % a.H * D) + c);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t amax = 0u;  // of the magnitudes' bits
+#pragma unroll
+  for (int k = 0; k < 4; ++k) amax = max(amax, max((w[k] << 16) & 0x7fffffffu, w[k] & 0x7fff0000u));
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) amax = max(amax, __shfl_xor_sync(kAll, amax, o));
+  if (!mine) return;
+  float back;
+  uint32_t hi[2], lo[2];
+  split_q8(w, amax, hi, lo, back);
+  *reinterpret_cast<uint2*>(terms + row * D + 8 * c) = make_uint2(hi[0], hi[1]);
+  *reinterpret_cast<uint2*>(terms + (rows + row) * D + 8 * c) = make_uint2(lo[0], lo[1]);
+  if (c == 0) scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f : kLog2e);
+}
 
 template <int D>
 __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
     paged_prefill_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap k_map,
-                         const __grid_constant__ CUtensorMap v_map) {
+                         const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map) {
   using L = PreLay<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   grid_launch_dependents();  // the merge may be launched behind this grid; it waits for the grid's end
@@ -125,7 +168,9 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
       mbar_init(&bars[L::kSFull + i], 1);
       mbar_init(&bars[L::kPFull + i], 8);
       mbar_init(&bars[L::kPvDone + i], 1);
-      mbar_init(&bars[L::kQFull + i], 8);
+      mbar_init(&bars[L::kQFull + i], 1);
+      mbar_init(&bars[L::kQEmpty + i], 1);
+      mbar_init(&bars[L::kOFree + i], 8);
     }
     for (int i = 0; i < L::kSegs; ++i) {
       mbar_init(&bars[L::kSegFull + i], 1);
@@ -139,9 +184,12 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
     tmem_alloc(tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
+  // the rows behind a tile's last stay zero: the copies of Q write the rows of its tokens only
+  for (int i = tid; i < 2 * L::kQHalf / 16; i += L::kThreads)
+    *reinterpret_cast<uint4*>(smem + L::kOffQ + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
   grid_dependency_wait();  // everything above may overlap the preceding kernel's end
   const PagedRange range = paged_range<L::kThreads>(p, reinterpret_cast<int64_t*>(smem), 2);
-  fence_proxy_async_smem();  // the copies may overwrite the prefix sums
+  fence_proxy_async_smem();  // the copies may overwrite the prefix sums, the tensor cores read the zeros
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -151,7 +199,8 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
     const int outside = (int)(a.NB * a.HK * kBlock);  // a row behind the cache: reads as zeros
-    int tl = 0, seg = 0;
+    const uint32_t q_bytes = (uint32_t)(p.Gr * half_tokens * D);  // of a half's term
+    int tl = 0, seg = 0, filled[2] = {0, 0};
     bool dead = false;
     while (true) {
       const int sb = seg % L::kSegs;
@@ -160,6 +209,19 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
       const Segment s = *reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment));
       if (s.n == 0) break;
       const int32_t* row = a.block_table + (int64_t)s.r * a.MB;
+      for (int h = 0; h < (s.ntok > half_tokens ? 2 : 1); ++h) {
+        if (filled[h] > 0) dead = __any_sync(kAll, !PA_WAIT(L::kQEmpty + h, (filled[h] + 1) & 1));
+        if (dead) break;
+        ++filled[h];
+        if (lane == 0) {
+          const uint32_t qd = smem_u32(smem + L::kOffQ + h * L::kQHalf);
+          mbar_arrive_expect_tx(&bars[L::kQFull + h], 2 * q_bytes);
+          tma_load_3d(qd, &q_map, 0, s.h0, s.t0 + h * half_tokens, &bars[L::kQFull + h]);
+          tma_load_3d(qd + L::kQTerm, &q_map, 0, s.h0, a.T + s.t0 + h * half_tokens, &bars[L::kQFull + h]);
+        }
+        __syncwarp();
+      }
+      if (dead) break;
       // lane l holds block base - l of the row (tiles are taken from the last down): its cache block (-1: none)
       // and scales; the next 32 are fetched while these are in use
       auto fetch = [&](int page, int& b, float& ks, float& vs) {
@@ -225,6 +287,8 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
       ++seg;
     }
     // no copy may still be landing when the CTA exits
+    for (int h = 0; h < 2; ++h)
+      if (filled[h] > 0) mbar_wait_drain(&bars[L::kQFull + h], (filled[h] + 1) & 1);
     for (int j = max(0, tl - L::kStages); j < tl; ++j) mbar_wait_drain(&bars[L::kKFull + j % L::kStages], (j / L::kStages) & 1);
     for (int j = max(0, tl - L::kVStages); j < tl; ++j)
       mbar_wait_drain(&bars[L::kVFull + j % L::kVStages], (j / L::kVStages) & 1);
@@ -245,7 +309,7 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         if (!dead) dead = !PA_WAIT(idx, parity);
         return !dead;
       };
-      auto qk = [&](int h, int t, bool last) {
+      auto qk = [&](int h, int t, bool last, bool ends) {
         const int st = t % L::kStages;
         if (!wait(L::kKFull + st, (t / L::kStages) & 1)) return;
         if (done[h] > 0 && !wait(L::kPvDone + h, (done[h] + 1) & 1)) return;
@@ -259,9 +323,12 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
                    term + k > 0 ? 1u : 0u);
         mma_commit(&bars[L::kSFull + h]);
         if (last) mma_commit(&bars[L::kKEmpty + st]);
+        if (ends) mma_commit(&bars[L::kQEmpty + h]);
       };
       auto pv = [&](int h, int t, bool first, bool last) {
         const int vb = t & 1;
+        // a segment's first product overwrites O, which the segment before has to have been read out of
+        if (first && filled[h] > 1 && !wait(L::kOFree + h, filled[h] & 1)) return;
         if (!wait(L::kPFull + h, done[h] & 1) || !wait(L::kV16Full + vb, (t >> 1) & 1)) return;
         tc_fence_after();
         const uint64_t dv = dv0 + (uint64_t)((vb * L::kV16) >> 4);
@@ -280,13 +347,14 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         const int n = sp->n, halves = sp->ntok > half_tokens ? 2 : 1;
         if (n == 0) break;
         mbar_arrive(&bars[L::kSegFree + sb]);
-        // the halves' Q is split, and their O of the segment before has been read
-        for (int h = 0; h < halves; ++h) wait(L::kQFull + h, filled[h]++ & 1);
-        for (int h = 0; h < halves; ++h) qk(h, tl, h == halves - 1);
+        for (int h = 0; h < halves; ++h) {
+          wait(L::kQFull + h, filled[h]++ & 1);
+          qk(h, tl, h == halves - 1, n == 1);
+        }
         for (int i = 0; i < n && !dead; ++i, ++tl)
           for (int h = 0; h < halves; ++h) {
             pv(h, tl, i == 0, h == halves - 1);
-            if (i + 1 < n) qk(h, tl + 1, h == halves - 1);
+            if (i + 1 < n) qk(h, tl + 1, h == halves - 1, i + 2 == n);
           }
         if (dead) break;
         ++seg;
@@ -333,9 +401,12 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
   } else if (warp >= L::kConvWarp0 && warp < L::kSoftWarp0) {
     // ---------------------------------------------------------------- V to f16, times v_scale / R; unseen keys zero
     const int w = warp - L::kConvWarp0;
-    constexpr int kChunks = D / 16;            // 16-byte chunks of a key's codes
-    constexpr int kKeysPer = 32 / kChunks;     // keys that a warp converts at a time
-    const int ch = lane % kChunks, sub = lane / kChunks;
+    // A warp converts its 32 keys in steps of kKeysPer.  8 lanes (what one shared-memory access
+    // serves at a time) take 4 chunks of two keys whose numbers differ in bits 0 and 2, so that under the
+    // swizzles neither the reads nor the writes meet in a bank.
+    constexpr int kHalves = D / 64, kKeysPer = 8 / kHalves;  // 64-column halves of a key; keys a step
+    const int ch = (lane & 3) + (D == 128 ? 4 * ((lane >> 3) & 1) : 0);
+    const int pair = lane >> (D == 128 ? 4 : 3);              // which two keys of the step's
     int tl = 0, seg = 0;
     bool dead = false;
     while (true) {
@@ -360,7 +431,8 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         const uint32_t src = smem_u32(smem + L::kOffV + sv * L::kKTile), dst = smem_u32(smem + L::kOffV16 + vb * L::kV16);
 #pragma unroll
         for (int it = 0; it < 32 / kKeysPer; ++it) {
-          const int r = 32 * w + it * kKeysPer + sub, j = j0 + r;
+          const int first = (it * kKeysPer % 8) / 2 + pair;  // of 8 keys, pairs (0, 5), (1, 4), (2, 7), (3, 6)
+          const int r = 32 * w + it * kKeysPer / 8 * 8 + ((lane & 4) ? first ^ 5 : first), j = j0 + r;
           uint32_t c[4], o[8];
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
@@ -426,67 +498,20 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         continue;
       }
       int pos = 0, lo = 0, hi = 0;
-      float slope = 0.f, f_row;
+      float slope = 0.f, f_row = 0.f;
       int64_t out_row = -1;
-      {
-        // this row, and this thread's half of its Q in two terms
-        const uint4* src = nullptr;
-        if (row < ntok * heads) {
-          PagedRequest q;
-          q.load(a, sp->r);
-          const int t = sp->t0 + half * half_tokens + row / heads, h = sp->h0 + row % heads;
-          pos = q.pos(t);
-          lo = q.lo(a, t);
-          hi = q.hi(t);
-          if (a.alibi_slopes) slope = __ldg(a.alibi_slopes + h) * kLog2e;
-          out_row = (int64_t)t * a.H + h;
-          src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (int64_t)t * a.q_stride +
-                                               (int64_t)h * D + blk * (D / 2));
-        }
-        uint4 v[D / 16];
-        uint32_t amax = 0u;  // of the magnitudes' bits
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          v[i] = src ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) amax = max(amax, max((w[k] << 16) & 0x7fffffffu, w[k] & 0x7fff0000u));
-        }
-        reinterpret_cast<uint32_t*>(red)[blk * kRows + row] = amax;
-        named_bar_sync(bar, 64);
-        amax = max(amax, reinterpret_cast<const uint32_t*>(red)[(1 - blk) * kRows + row]);
-        named_bar_sync(bar, 64);
-        // 2^sh: amax = (1 + f) 2^e to at most 448 = 1.75 * 2^8
-        int sh = 8 - ((int)(amax >> 23) - 127) - ((amax & 0x7fffffu) > 0x600000u);
-        sh = amax == 0u ? 0 : min(sh, 120);
-        const float f = __uint_as_float((uint32_t)(sh + 127) << 23);
-        // a row with an infinity or NaN has no finite result
-        f_row = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - sh) << 23);
-        f_row *= a.sm_scale * (a.softcap > 0.f ? 1.f : kLog2e);
-        const uint32_t qd = smem_u32(smem + L::kOffQ + half * L::kQHalf);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {  // 16 codes each
-          const uint32_t w[8] = {v[2 * i].x,     v[2 * i].y,     v[2 * i].z,     v[2 * i].w,
-                                 v[2 * i + 1].x, v[2 * i + 1].y, v[2 * i + 1].z, v[2 * i + 1].w};
-          uint32_t hc[4] = {0u, 0u, 0u, 0u}, lc[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float y0 = __uint_as_float(w[k] << 16) * f, y1 = __uint_as_float(w[k] & 0xffff0000u) * f;
-            const uint32_t c = e4m3x2(y0, y1);
-            const float2 back = e4m3x2_f32(c);
-            hc[k >> 1] |= c << (16 * (k & 1));
-            lc[k >> 1] |= e4m3x2(y0 - back.x, y1 - back.y) << (16 * (k & 1));
-          }
-          const uint32_t dst = qd + swz<D>(row, blk * (D / 32) + i);
-          st_shared_v4(dst, hc[0], hc[1], hc[2], hc[3]);
-          st_shared_v4(dst + L::kQTerm, lc[0], lc[1], lc[2], lc[3]);
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();  // O of the segment before has been read
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::kQFull + half]);
+      if (row < ntok * heads) {
+        PagedRequest q;
+        q.load(a, sp->r);
+        const int t = sp->t0 + half * half_tokens + row / heads, h = sp->h0 + row % heads;
+        pos = q.pos(t);
+        lo = q.lo(a, t);
+        hi = q.hi(t);
+        if (a.alibi_slopes) slope = __ldg(a.alibi_slopes + h) * kLog2e;
+        out_row = (int64_t)t * a.H + h;
+        f_row = p.q_scale[out_row];
       }
-      float m = kNoMax, l = 0.f;
+      float m = 0.f, l = 0.f;
       for (int i = 0; i < n; ++i, ++tl, ++done) {
         {
           // S first: a half that skipped segments may be phases of the meta ring behind until then
@@ -500,46 +525,32 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         const int pages = reinterpret_cast<const int*>(meta)[4];
         const int j0 = (kt + n - 1 - i) * kKeyTile, jb = j0 + 64 * blk;  // first keys of the tile and of this block
         const bool inside = j0 >= sp->all_lo && j0 + kKeyTile <= sp->all_hi && pages == 3;  // no mask
-        const bool plain = inside && !a.alibi_slopes && !(a.softcap > 0.f);
-        // visible keys of the block for this row: lo_k <= k < lo_k + n_k
-        const int lo_k = max(lo - jb, 0), n_k = (pages >> blk) & 1 ? max(min(hi - jb, 64) - lo_k, 0) : 0;
+        const bool changed = a.alibi_slopes || a.softcap > 0.f;
+        // the block's keys that this row sees, a bit each
+        uint64_t seen = 0ull;
+        if (!inside && ((pages >> blk) & 1)) {
+          const int lo_k = min(max(lo - jb, 0), 64), hi_k = min(max(hi - jb, 0), 64);
+          if (hi_k > lo_k) seen = (~0ull >> (64 - (hi_k - lo_k))) << lo_k;
+        }
         uint32_t pw[32];  // the weights, f16 pairs
         float part;
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
-          const float base = m == kNoMax ? 0.f : m;
-          float top = -INFINITY;  // the largest x - base
+          float top = -INFINITY;  // the largest x - m'
           uint64_t sum2 = 0ull;
-          // weights of the 16 keys x - base; two sums and the largest besides
-          auto weigh = [&](const uint32_t (&x)[16], int c) {
+          const uint64_t f2 = pack2(f, f), m2 = pack2(-m, -m);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float x0 = __uint_as_float(x[2 * k]), x1 = __uint_as_float(x[2 * k + 1]);
-              top = fmaxf(top, fmaxf(x0, x1));
-              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-              sum2 = add2(sum2, pack2(p0, p1));
-              pw[8 * c + k] = pack_f16x2(p0, p1);
-            }
-          };
-          if (plain) {
-            const uint64_t f2 = pack2(f, f), m2 = pack2(-base, -base);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t x[16];
-              tmem_ld16_sync(s_addr + 16 * c, x);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[16];
+            tmem_ld16_sync(s_addr + 16 * c, x);
+            if (!changed) {
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, m2));
                 x[2 * k] = __float_as_uint(y.x);
                 x[2 * k + 1] = __float_as_uint(y.y);
               }
-              weigh(x, c);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t x[16];
-              tmem_ld16_sync(s_addr + 16 * c, x);
+            } else {
 #pragma unroll
               for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
               if (a.softcap > 0.f) {
@@ -551,37 +562,46 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
               }
               if (a.alibi_slopes) {
                 float away = (float)(pos - jb - 16 * c);
-                asm volatile("" : "+f"(away));  // as lo_c below
+                asm volatile("" : "+f"(away));  // as bits below
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
                   x[k] = __float_as_uint(fmaf(-slope, fabsf(away - (float)k), __uint_as_float(x[k])));
               }
-              if (!inside) {
-                // (opaque: otherwise the 64 comparisons move out of the pass loop and run for every tile)
-                int lo_c = 16 * c - lo_k;
-                asm volatile("" : "+r"(lo_c));
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  x[k] = (uint32_t)(lo_c + k) < (uint32_t)n_k ? x[k] : 0xff800000u;  // -infinity
-              }
+              for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) - m);
+            }
+            if (!inside) {
+              // (opaque: otherwise the 64 tests move out of the pass loop and run for every tile)
+              uint32_t bits = (uint32_t)(seen >> (16 * c));
+              asm volatile("" : "+r"(bits));
 #pragma unroll
-              for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) - base);
-              weigh(x, c);
+              for (int k = 0; k < 16; ++k) x[k] = (bits >> k) & 1u ? x[k] : 0xff800000u;  // -infinity
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float x0 = __uint_as_float(x[2 * k]), x1 = __uint_as_float(x[2 * k + 1]);
+              top = fmaxf(top, fmaxf(x0, x1));
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              sum2 = add2(sum2, pack2(p0, p1));
+              pw[8 * c + k] = pack_f16x2(p0, p1);
             }
           }
           const float2 s2 = unpack2(sum2);
           part = s2.x + s2.y;
-          if (pass == 1 || !bar_any(bar, 64, top + (base - m) > kTop16)) break;
-          // a weight too large for f16, or a row's first key: refresh the row's reference
-          red[blk * kRows + row] = top == top ? top + base : -INFINITY;
+          const bool low = l == 0.f && top < kLow16 && top > -INFINITY;
+          if (pass == 1 || !bar_any(bar, 64, top > kTop16 || low)) break;
+          red[blk * kRows + row] = top;
+          sums[blk * kRows + row] = l;
           named_bar_sync(bar, 64);
           top = fmaxf(red[row], red[kRows + row]);
           float g = 1.f;
-          if (top - m > kTop16) {
-            const float to = top - kRefresh16;
-            g = ex2_approx(m - to);
+          if (top > kTop16) {
+            const float up = top - kRefresh16;
+            g = ex2_approx(-up);
             l *= g;
-            m = to;
+            m += up;
+          } else if (top < kLow16 && top > -INFINITY && sums[row] + sums[kRows + row] == 0.f) {
+            m += top - kRefresh16;  // (O is 0 so far)
           }
           // P V of the tiles before is complete: S of this tile was issued behind it
           if (i > 0 && __any_sync(kAll, g != 1.f)) {
@@ -612,6 +632,7 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         if (lane == 0) mbar_arrive(&bars[L::kPFull + half]);
       }
       // the results: O R / l, or the partial O R with m' and l
+      named_bar_sync(bar, 64);
       sums[blk * kRows + row] = l;
       named_bar_sync(bar, 64);
       l += sums[(1 - blk) * kRows + row];
@@ -642,16 +663,20 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
                                  __uint_as_float(o[4 * k + 2]) * g, __uint_as_float(o[4 * k + 3]) * g);
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars[L::kOFree + half]);
+        mbar_arrive(&bars[L::kSegFree + sb]);
+      }
       if (blk == 0 && out_row >= 0 && !dead) {
         if (slot < 0) {
           a.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         } else {
-          p.part_ml[part_at * 512 + c_row] = m;
+          p.part_ml[part_at * 512 + c_row] = l == 0.f ? kNoMax : m;
           p.part_ml[part_at * 512 + 256 + c_row] = l;
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[L::kSegFree + sb]);
       ++seg;
     }
   }
@@ -664,13 +689,51 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
   }
 }
 
+// Workspace: what every call has, then the two terms of q and its scales.
+size_t terms_offset(const PagedSizes& sz) { return align256(sz.bytes); }
+size_t scales_offset(const PagedSizes& sz, int T, int H, int D) {
+  return terms_offset(sz) + align256((size_t)2 * T * H * D);
+}
+
+// A term of q as [2 T, H, D] bytes (both terms), a box the rows of half a query tile.
+cudaError_t term_map(CUtensorMap* m, void* terms, int T, int H, int D, int heads, int tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)2 * T};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)H * D};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)heads, (cuuint32_t)tokens}, es[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, terms, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int D>
 cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t stream) {
   using L = PreLay<D>;
-  return launch_paged<D, 2 * kRows>(paged_prefill_kernel<D>, a, L::kPerSm, L::kThreads, L::kSmem, num_sms, stream);
+  constexpr int C = 2 * kRows;
+  const PagedSizes sz = paged_sizes(C, D, L::kPerSm, num_sms);
+  uint8_t* terms = static_cast<uint8_t*>(a.workspace) + terms_offset(sz);
+  PagedParams p = paged_params<C>(a, sz, kUnitCost);
+  p.q_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + scales_offset(sz, a.T, a.H, D));
+  CUtensorMap k_map, v_map, q_map;
+  cudaError_t e = cache_maps(a, &k_map, &v_map);
+  if (e == cudaSuccess) e = term_map(&q_map, terms, a.T, a.H, D, p.Gr, p.tq / 2);
+  if (e != cudaSuccess) return e;
+  const int64_t threads = (int64_t)a.T * a.H * (D / 8);
+  e = launch_overlapped(paged_split_q_kernel<D>, dim3((unsigned)((threads + kSplitThreads - 1) / kSplitThreads)),
+                        kSplitThreads, 0, stream, a, terms, p.q_scale);
+  if (e == cudaSuccess)
+    e = launch_overlapped(paged_prefill_kernel<D>, dim3((unsigned)p.ctas), L::kThreads, L::kSmem, stream, p, k_map, v_map,
+                          q_map);
+  return e == cudaSuccess ? launch_merge<D, C>(p, stream) : e;
 }
 
 }  // namespace
+
+size_t paged_prefill_workspace(int T, int H, int D, int num_sms) {
+  return scales_offset(paged_sizes(2 * kRows, D, 1, num_sms), T, H, D) + align256((size_t)T * H * 4);
+}
 
 cudaError_t launch_paged_prefill(const PagedAttnArgs& a, int num_sms, cudaStream_t stream) {
   return a.D == 128 ? launch<128>(a, num_sms, stream) : launch<64>(a, num_sms, stream);
