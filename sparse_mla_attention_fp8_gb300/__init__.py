@@ -624,9 +624,13 @@ def paged_blocks_extend(context_lens, query_lens, block_table, free_blocks, free
         if b is None:
             n = max(T, 0)
             device = block_table.device
-            start, lens, req, pos, left, lack = torch.empty(
-                2 * R + 2 * n + 3, dtype=i32, device=device).split_with_sizes((R + 1, R, n, n, 1, 1))
-            b = PagedBatch(start, lens, req, pos, torch.empty(n, dtype=i64, device=device), left, lack)
+            ints = torch.empty(2 * R + 2 * n + 3, dtype=i32, device=device)
+            parts, at = [], 0
+            for size in (R + 1, R, n, n, 1, 1):
+                parts.append(ints.as_strided((size,), (1,), at))
+                at += size
+            parts.insert(4, torch.empty(n, dtype=i64, device=device))
+            b = PagedBatch(*parts)
         _check(lib().paged_blocks_extend(
             context_lens.data_ptr(), query_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(),
             free_count.data_ptr(), b.query_start.data_ptr(), b.seq_lens.data_ptr(), b.req_id_per_token.data_ptr(),

@@ -16,9 +16,9 @@
 // Unit u of the grid stands for one touched block: request r's units start at
 // floor(query_start_r / 64) + 2 r, which leaves room for every block that its
 // tokens can touch, so a unit finds its request by a search in query_start.
-// A warp per (block, head, K or V) holds the block's new rows in registers
-// (one read of the input), so the kernel moves what it must: bound by HBM for
-// prefill, by latency for single tokens.
+// One warp or four per (block, head, K or V); the new rows are read once, so the
+// kernel moves what it must: bound by HBM for prefill, by latency for single
+// tokens.
 #include "smla_paged.cuh"
 
 namespace smla {
@@ -52,56 +52,90 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// The new rows [row0, row0 + n) of one block and head by one warp.  A lane
-// holds 4 values of a row: D / 4 lanes make a row, 128 / D rows an access.
-// kAccesses * 128 / D rows at most.
-template <int D, int kAccesses>
-__device__ __forceinline__ void store_rows(const __nv_bfloat16* __restrict__ src, int64_t stride, int row0, int n,
-                                           uint8_t* __restrict__ page, float* __restrict__ scale) {
-  constexpr int kRowsPer = 128 / D;
-  const int lane = threadIdx.x & 31, sub = lane / (D / 4), col = 4 * (lane % (D / 4));
-  const float old = row0 > 0 ? *scale : 0.f;
-  uint2 v[kAccesses];
-#pragma unroll
-  for (int i = 0; i < kAccesses; ++i) {
-    const int r = i * kRowsPer + sub;
-    v[i] = r < n ? __ldg(reinterpret_cast<const uint2*>(src + r * stride + col)) : make_uint2(0u, 0u);
-  }
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kAccesses; ++i) amax = finite_amax(finite_amax(amax, v[i].x), v[i].y);
-  amax = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(amax)));  // non-negative: ordered as its bits
-  const int e = scale_exponent(amax);
-  float s = pow2(e), inv = pow2(-e);
+// The scale of a block and head, and 1 / scale: `old` is its scale before (0
+// where no earlier row counts), amax its new rows'.
+__device__ __forceinline__ void block_scale(float old, uint32_t amax, float& s, float& inv) {
+  const int e = scale_exponent(__uint_as_float(amax));
+  s = pow2(e);
+  inv = pow2(-e);
   if (old > s) {
-    s = old;  // the block's scale stays
+    s = old;
     inv = __frcp_rn(old);
-  } else if (row0 > 0 && old < s) {
-    const float f = old * inv;
-    const int words = row0 * (D / 4);
-    uint32_t* w = reinterpret_cast<uint32_t*>(page);
-#pragma unroll 8
-    for (int i = lane; i < words; i += 32) {
-      const uint32_t c = w[i];
-      const float2 a = e4m3x2_f32(c & 0xffffu), b = e4m3x2_f32(c >> 16);
-      w[i] = e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
-    }
   }
-  uint8_t* dst = page + (row0 + sub) * D + col;
-#pragma unroll
-  for (int i = 0; i < kAccesses; ++i) {
-    if (i * kRowsPer + sub >= n) break;
-    const float x0 = nan_to_0(__uint_as_float(v[i].x << 16)), x1 = nan_to_0(__uint_as_float(v[i].x & 0xffff0000u));
-    const float x2 = nan_to_0(__uint_as_float(v[i].y << 16)), x3 = nan_to_0(__uint_as_float(v[i].y & 0xffff0000u));
-    *reinterpret_cast<uint32_t*>(dst + i * 128) = e4m3x4(x0 * inv, x1 * inv, x2 * inv, x3 * inv);
-  }
-  if (lane == 0) *scale = s;
 }
 
-template <int D>
+// Codes of the earlier rows (words of them, by `threads` threads) under a
+// scale that has grown from old = f * the new one.
+__device__ __forceinline__ void rescale_codes(uint32_t* __restrict__ w, int words, float f, int thread, int threads) {
+#pragma unroll 8
+  for (int i = thread; i < words; i += threads) {
+    const uint32_t c = w[i];
+    const float2 a = e4m3x2_f32(c & 0xffffu), b = e4m3x2_f32(c >> 16);
+    w[i] = e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
+  }
+}
+
+__device__ __forceinline__ uint32_t codes_of(uint2 v, float inv) {
+  return e4m3x4(nan_to_0(__uint_as_float(v.x << 16)) * inv, nan_to_0(__uint_as_float(v.x & 0xffff0000u)) * inv,
+                nan_to_0(__uint_as_float(v.y << 16)) * inv, nan_to_0(__uint_as_float(v.y & 0xffff0000u)) * inv);
+}
+
+// The new rows [row0, row0 + n) of one block and head, by one warp (kGroup = 1)
+// or four (kGroup = 4, thread `t` of 128).  A lane holds 4 values of a row: D / 4
+// lanes make a row, 128 / D rows an access.  Four warps hold up to 64 rows in
+// registers: one read, many loads in flight.  One warp, for the few rows of
+// single tokens and drafts, holds 8 accesses; where there are more it reads
+// them twice.
+template <int D, int kGroup>
+__device__ __forceinline__ void store_rows(const __nv_bfloat16* __restrict__ src, int64_t stride, int row0, int n,
+                                           uint8_t* __restrict__ page, float* __restrict__ scale, int t, int bar,
+                                           uint32_t* __restrict__ shared_max) {
+  constexpr int kRowsPer = 128 / D;
+  constexpr int kHeld = kGroup == 4 ? kBlock / 4 / kRowsPer : 8;  // accesses
+  const int lane = t & 31, warp = t >> 5, sub = lane / (D / 4), col = 4 * (lane % (D / 4));
+  const float old = row0 > 0 ? *scale : 0.f;
+  const int first = warp * kHeld * kRowsPer;  // this warp's first row
+  uint2 v[kHeld];
+  uint32_t top = 0u;
+  for (int base = first; base < n; base += kGroup == 4 ? kBlock : kHeld * kRowsPer) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int r = base + i * kRowsPer + sub;
+      v[i] = r < n ? __ldg(reinterpret_cast<const uint2*>(src + r * stride + col)) : make_uint2(0u, 0u);
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) amax = finite_amax(finite_amax(amax, v[i].x), v[i].y);
+    top = max(top, __float_as_uint(amax));  // non-negative: ordered as its bits
+  }
+  top = __reduce_max_sync(kAll, top);
+  if (kGroup == 4) {
+    if (lane == 0) shared_max[warp] = top;
+    named_bar_sync(bar, 128);  // and every warp has read the old scale
+    top = max(max(shared_max[0], shared_max[1]), max(shared_max[2], shared_max[3]));
+  }
+  float s, inv;
+  block_scale(old, top, s, inv);
+  if (row0 > 0 && old < s) rescale_codes(reinterpret_cast<uint32_t*>(page), row0 * (D / 4), old * inv, t, 32 * kGroup);
+  uint8_t* dst = page + (row0 + sub) * D + col;
+  const bool again = kGroup == 1 && n > kHeld * kRowsPer;
+  for (int base = first; base < n; base += kGroup == 4 ? kBlock : kHeld * kRowsPer) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int r = base + i * kRowsPer + sub;
+      if (r >= n) break;
+      if (again) v[i] = __ldg(reinterpret_cast<const uint2*>(src + r * stride + col));
+      *reinterpret_cast<uint32_t*>(dst + (base + i * kRowsPer) * D) = codes_of(v[i], inv);
+    }
+  }
+  if (t == 0) *scale = s;
+}
+
+template <int D, int kGroup>
 __global__ void __launch_bounds__(32 * kStoreWarps) kv_store_kernel(const __grid_constant__ KvStoreArgs a) {
-  const int u = (int)blockIdx.x, warp = threadIdx.x >> 5;
-  const int item = (int)blockIdx.y * kStoreWarps + warp;
+  __shared__ uint32_t group_max[kStoreWarps];
+  const int u = (int)blockIdx.x, group = (int)threadIdx.x / (32 * kGroup), t = (int)threadIdx.x % (32 * kGroup);
+  const int item = (int)blockIdx.y * (kStoreWarps / kGroup) + group;
   if (item >= 2 * a.HK) return;
   // request r's units start at floor(query_start_r / 64) + 2 r
   const int r = search_units(a.R, u, [&](int i) { return clamp_start(a.query_start, i, a.T) / kBlock + 2 * i; });
@@ -124,21 +158,25 @@ __global__ void __launch_bounds__(32 * kStoreWarps) kv_store_kernel(const __grid
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
   uint8_t* page = (is_v ? a.v_cache : a.k_cache) + bh * (kBlock * D);
   float* scale = (is_v ? a.v_scale : a.k_scale) + bh;
-  // few rows (single tokens, drafts): a short body, so that a decode step does not fetch and skip the long one
-  if (n * D <= 8 * 128)
-    store_rows<D, 8>(src, stride, row0, n, page, scale);
-  else
-    store_rows<D, kBlock * D / 128>(src, stride, row0, n, page, scale);
+  store_rows<D, kGroup>(src, stride, row0, n, page, scale, t, 1 + group, group_max + 4 * group);
 }
 
 }  // namespace
 
+template <int D, int kGroup>
+static void launch(const KvStoreArgs& a, cudaStream_t stream) {
+  constexpr int kItems = kStoreWarps / kGroup;
+  const dim3 grid((unsigned)(a.T / kBlock + 2 * a.R), (unsigned)((2 * a.HK + kItems - 1) / kItems));
+  kv_store_kernel<D, kGroup><<<grid, 32 * kStoreWarps, 0, stream>>>(a);
+}
+
 cudaError_t launch_kv_store(const KvStoreArgs& a, cudaStream_t stream) {
-  const dim3 grid((unsigned)(a.T / kBlock + 2 * a.R), (unsigned)((2 * a.HK + kStoreWarps - 1) / kStoreWarps));
+  // four warps a block and head where a request brings 16 rows or more on average
+  const bool many = a.T / 16 >= a.R;
   if (a.D == 128)
-    kv_store_kernel<128><<<grid, 32 * kStoreWarps, 0, stream>>>(a);
+    many ? launch<128, 4>(a, stream) : launch<128, 1>(a, stream);
   else
-    kv_store_kernel<64><<<grid, 32 * kStoreWarps, 0, stream>>>(a);
+    many ? launch<64, 4>(a, stream) : launch<64, 1>(a, stream);
   return cudaGetLastError();
 }
 

@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
 }
 
 // Places of a unit beside its tiles: about what its start and end take.
-constexpr int kUnitCost = 1;
+constexpr int kUnitCost = 4;
 
 template <int D, int C>
 cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t stream) {
