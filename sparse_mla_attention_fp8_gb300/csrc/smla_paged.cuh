@@ -205,6 +205,20 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   return mbar_try_wait(bar, parity) || wait_slow(bar, parity, cta_abort, status);
 }
 
+// Place in a ring of N slots with a barrier each: index and the parity of its
+// phase (no divisions in the roles' loops).
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 struct PagedParams {
   PagedAttnArgs a;
   // Rows of a query tile: tq tokens x up to Gr of the G heads of a K/V head; more than C heads are cut into

@@ -80,7 +80,7 @@ struct Lay {
   static constexpr int kKTile = kKeyTile * D;
   static constexpr int kStage = 2 * kKTile;
   static constexpr int kStages = (C <= 16 ? 3 : 5) * (128 / D);
-  static constexpr int kMeta = kStages + 2;        // ring of block scales and flags
+  static constexpr int kMeta = kStages <= 6 ? 8 : 16;  // ring of block scales and flags
   static constexpr int kQBuf = N * D;
   static constexpr int kSegs = 2;
   static constexpr int kPBuf = kKeyTile * N;
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
+    Ring<L::kStages> ring;
     const int outside = (int)(a.NB * a.HK * kBlock);  // a row behind the cache: reads as zeros
     int tl = 0, seg = 0;
     bool dead = false;
@@ -211,9 +212,10 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         const int b0 = __shfl_sync(kAll, b, at + 1), b1 = __shfl_sync(kAll, b, at);
         const float k0 = __shfl_sync(kAll, ks, at + 1), k1 = __shfl_sync(kAll, ks, at);
         const float v0 = __shfl_sync(kAll, vs, at + 1), v1 = __shfl_sync(kAll, vs, at);
-        const int st = tl % L::kStages, use = tl / L::kStages;
-        if (use > 0) dead = __any_sync(kAll, !PA_WAIT(L::kEmpty + st, (use + 1) & 1));
+        const int st = ring.i;
+        dead = __any_sync(kAll, !PA_WAIT(L::kEmpty + st, ring.phase ^ 1u));  // (true at once in the first lap)
         if (dead) break;
+        ring.next();
         if (lane == 0) {
           float* meta = reinterpret_cast<float*>(smem + L::kOffMeta + (tl % L::kMeta) * 32);
           *reinterpret_cast<float4*>(meta) = make_float4(k0, k1, v0, v1);
@@ -246,6 +248,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       constexpr uint32_t lay = D == 128 ? kLayoutSw128 : kLayoutSw64;
       const uint64_t dk0 = make_sdesc(smem_u32(smem), 16, 8 * D, lay);
       const uint64_t dq0 = make_sdesc(smem_u32(smem + L::kOffQ), 16, 8 * D, lay);
+      Ring<L::kStages> ring;
       int tl = 0, seg = 0;
       bool dead = false;
       while (!dead) {
@@ -255,12 +258,12 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         if (n == 0) break;
         const uint64_t dq = dq0 + (uint64_t)((sb * L::kQBuf) >> 4);
         for (int i = 0; i < n; ++i, ++tl) {
-          const int st = tl % L::kStages, buf = tl & 1;
-          if ((tl >= 2 && !PA_WAIT(L::kSFree + buf, ((tl >> 1) + 1) & 1)) ||
-              !PA_WAIT(L::kKFull + st, (tl / L::kStages) & 1)) {
+          const int st = ring.i, buf = tl & 1;
+          if (!PA_WAIT(L::kSFree + buf, ((tl >> 1) + 1) & 1) || !PA_WAIT(L::kKFull + st, ring.phase)) {
             dead = true;
             break;
           }
+          ring.next();
           tc_fence_after();
           const uint64_t dk = dk0 + (uint64_t)((st * L::kStage) >> 4);
 #pragma unroll
@@ -285,6 +288,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       const uint64_t dv0 = make_sdesc(smem_u32(smem + L::kKTile), 0, 8 * D, D == 128 ? kLayoutSw128 : kLayoutSw64);
       // P: core matrices of 8 keys x 16 columns, the N / 16 of 8 keys together
       const uint64_t dp0 = make_sdesc(smem_u32(smem + L::kOffP), 8 * N, 128, kLayoutNone);
+      Ring<L::kStages> ring;
       int tl = 0, seg = 0, left = 0;
       for (;; ++tl, --left) {
         if (left == 0) {  // the next segment's tiles
@@ -295,11 +299,12 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
           mbar_arrive(&bars[L::kSegFree + sb]);
           ++seg;
         }
-        const int st = tl % L::kStages, buf = tl & 1;
+        const int st = ring.i, buf = tl & 1;
         const int pb = tl % L::kPBufs;
-        if (!PA_WAIT(L::kPFull + pb, (tl / L::kPBufs) & 1) || !PA_WAIT(L::kVFull + st, (tl / L::kStages) & 1) ||
-            (tl >= 2 && !PA_WAIT(L::kOFree + buf, ((tl >> 1) + 1) & 1)))
+        if (!PA_WAIT(L::kPFull + pb, (tl / L::kPBufs) & 1) || !PA_WAIT(L::kVFull + st, ring.phase) ||
+            !PA_WAIT(L::kOFree + buf, ((tl >> 1) + 1) & 1))
           break;
+        ring.next();
         tc_fence_after();
         const uint64_t dv = dv0 + (uint64_t)((st * L::kStage) >> 4), dp = dp0 + (uint64_t)((pb * L::kPBuf) >> 4);
 #pragma unroll
@@ -387,6 +392,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     float* red = reinterpret_cast<float*>(smem + L::kOffRed) + group * 32;
     float* sums = reinterpret_cast<float*>(smem + L::kOffSum) + group * 32;
     const int bar = 1 + group;
+    Ring<L::kStages> ring;
     int tl = 0, seg = 0;
     bool dead = false;
     // `dead` stays the same in the whole warp.  After a wait that ran out the loops go on without waiting to
@@ -410,12 +416,12 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         m[c] = kNoMax;
         l[c] = 0.f;
       }
-      for (int i = 0; i < n; ++i, ++tl) {
-        const int buf = tl & 1, st = tl % L::kStages, pb = tl % L::kPBufs;
+      for (int i = 0; i < n; ++i, ++tl, ring.next()) {
+        const int buf = tl & 1, st = ring.i, pb = tl % L::kPBufs;
         {
           // the tile's scales and flags (behind its K copies), and its S
           const bool ok =
-              !dead && PA_WAIT(L::kKFull + st, (tl / L::kStages) & 1) && PA_WAIT(L::kSFull + buf, (tl >> 1) & 1);
+              !dead && PA_WAIT(L::kKFull + st, ring.phase) && PA_WAIT(L::kSFull + buf, (tl >> 1) & 1);
           dead = !__all_sync(kAll, ok);
         }
         tc_fence_after();
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
             x[c] = page_ok & (j >= cols->lo[c0 + c]) & (j < cols->hi[c0 + c]) ? x[c] : -INFINITY;
           // keys that no row sees may hold any codes: their V rows become zeros
           zero_v = group == 0 && (j < sp->lo || j >= sp->hi);
-          if (__any_sync(kAll, zero_v)) wait(L::kVFull + st, (tl / L::kStages) & 1);
+          if (__any_sync(kAll, zero_v)) wait(L::kVFull + st, ring.phase);
         }
         float over = -INFINITY;
 #pragma unroll
@@ -470,7 +476,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         const bool refresh = bar_any(bar, 128, over > kTop);
         // the factors go to the summing warps: slot tl % 4 was read before P.V of tile tl - 2 could be issued
         uint8_t* ref = smem + L::kOffRefs + (tl % L::kRefs) * L::kRef;
-        if (tl >= L::kPBufs) wait(L::kPFree + pb, (tl / L::kPBufs + 1) & 1);  // P.V has read this P buffer
+        wait(L::kPFree + pb, (tl / L::kPBufs + 1) & 1);  // P.V has read this P buffer
         if (refresh) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {

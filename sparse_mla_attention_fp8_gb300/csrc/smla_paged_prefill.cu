@@ -74,7 +74,7 @@ struct PreLay {
   static constexpr int kKTile = kKeyTile * D;               // codes of a tile: K's, V's
   static constexpr int kStages = 3 * (128 / D), kVStages = 2 * (128 / D);
   static constexpr int kV16 = kKeyTile * D * 2;             // converted V: D / 64 panels of 128 keys x 128 bytes
-  static constexpr int kMeta = 2 * kStages;                 // ring of block scales and flags
+  static constexpr int kMeta = kStages <= 3 ? 8 : 16;       // ring of block scales and flags
   static constexpr int kQTerm = kRows * D, kQHalf = 2 * kQTerm;
   static constexpr int kSegs = 2;
   static constexpr int kOffV = kStages * kKTile;
@@ -200,6 +200,8 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
     // ---------------------------------------------------------------- TMA producer
     const int outside = (int)(a.NB * a.HK * kBlock);  // a row behind the cache: reads as zeros
     const uint32_t q_bytes = (uint32_t)(p.Gr * half_tokens * D);  // of a half's term
+    Ring<L::kStages> ring;
+    Ring<L::kVStages> v_ring;
     int tl = 0, seg = 0, filled[2] = {0, 0};
     bool dead = false;
     while (true) {
@@ -252,8 +254,9 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         const int b0 = __shfl_sync(kAll, b, at + 1), b1 = __shfl_sync(kAll, b, at);
         const float k0 = __shfl_sync(kAll, ks, at + 1), k1 = __shfl_sync(kAll, ks, at);
         const float v0 = __shfl_sync(kAll, vs, at + 1), v1 = __shfl_sync(kAll, vs, at);
-        const int st = tl % L::kStages, use = tl / L::kStages, sv = tl % L::kVStages, vuse = tl / L::kVStages;
-        if (use > 0) dead = __any_sync(kAll, !PA_WAIT(L::kKEmpty + st, (use + 1) & 1));
+        const int st = ring.i, sv = v_ring.i;
+        const uint32_t k_phase = ring.phase;
+        dead = __any_sync(kAll, !PA_WAIT(L::kKEmpty + st, k_phase ^ 1u));  // (true at once in the first lap)
         if (dead) break;
         const int y0 = b0 >= 0 ? (b0 * a.HK + s.g) * kBlock : outside;
         const int y1 = b1 >= 0 ? (b1 * a.HK + s.g) * kBlock : outside;
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
           tma_load_2d(kd + kBlock * D, &k_map, 0, y1, &bars[L::kKFull + st]);
         }
         __syncwarp();
-        if (vuse > 0) dead = __any_sync(kAll, !PA_WAIT(L::kVEmpty + sv, (vuse + 1) & 1));
+        dead = __any_sync(kAll, !PA_WAIT(L::kVEmpty + sv, v_ring.phase ^ 1u));
         if (lane == 0 && !dead) {
           const uint32_t vd = smem_u32(smem + L::kOffV + sv * L::kKTile);
           mbar_arrive_expect_tx(&bars[L::kVFull + sv], L::kKTile);
@@ -278,9 +281,11 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         }
         __syncwarp();
         if (dead) {  // this tile's K copies are in flight, its V copies are not
-          mbar_wait_drain(&bars[L::kKFull + st], use & 1);
+          mbar_wait_drain(&bars[L::kKFull + st], k_phase);
           break;
         }
+        ring.next();
+        v_ring.next();
       }
       if (dead) break;
       if (lane == 0) mbar_arrive(&bars[L::kSegFree + sb]);
@@ -309,9 +314,10 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         if (!dead) dead = !PA_WAIT(idx, parity);
         return !dead;
       };
-      auto qk = [&](int h, int t, bool last, bool ends) {
-        const int st = t % L::kStages;
-        if (!wait(L::kKFull + st, (t / L::kStages) & 1)) return;
+      Ring<L::kStages> ring;  // the K tile that the next first half takes
+      auto qk = [&](int h, bool last, bool ends) {
+        const int st = ring.i;
+        if (!wait(L::kKFull + st, ring.phase)) return;
         if (done[h] > 0 && !wait(L::kPvDone + h, (done[h] + 1) & 1)) return;
         tc_fence_after();
         const uint64_t dk = dk0 + (uint64_t)((st * L::kKTile) >> 4), dq = dq0 + (uint64_t)((h * L::kQHalf) >> 4);
@@ -322,7 +328,10 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
             mma_f8(tmem + L::kTmemS + 128 * h, dq + ((term * L::kQTerm + 32 * k) >> 4), dk + ((32 * k) >> 4), id_qk,
                    term + k > 0 ? 1u : 0u);
         mma_commit(&bars[L::kSFull + h]);
-        if (last) mma_commit(&bars[L::kKEmpty + st]);
+        if (last) {
+          mma_commit(&bars[L::kKEmpty + st]);
+          ring.next();
+        }
         if (ends) mma_commit(&bars[L::kQEmpty + h]);
       };
       auto pv = [&](int h, int t, bool first, bool last) {
@@ -349,12 +358,12 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         mbar_arrive(&bars[L::kSegFree + sb]);
         for (int h = 0; h < halves; ++h) {
           wait(L::kQFull + h, filled[h]++ & 1);
-          qk(h, tl, h == halves - 1, n == 1);
+          qk(h, h == halves - 1, n == 1);
         }
         for (int i = 0; i < n && !dead; ++i, ++tl)
           for (int h = 0; h < halves; ++h) {
             pv(h, tl, i == 0, h == halves - 1);
-            if (i + 1 < n) qk(h, tl + 1, h == halves - 1, i + 2 == n);
+            if (i + 1 < n) qk(h, h == halves - 1, i + 2 == n);
           }
         if (dead) break;
         ++seg;
@@ -407,6 +416,7 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
     constexpr int kHalves = D / 64, kKeysPer = 8 / kHalves;  // 64-column halves of a key; keys a step
     const int ch = (lane & 3) + (D == 128 ? 4 * ((lane >> 3) & 1) : 0);
     const int pair = lane >> (D == 128 ? 4 : 3);              // which two keys of the step's
+    Ring<L::kVStages> ring;
     int tl = 0, seg = 0;
     bool dead = false;
     while (true) {
@@ -417,11 +427,11 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
       const int kt = sp->kt, n = sp->n, lo = sp->lo, hi = sp->hi;
       if (n == 0) break;
       const float v_ref = reinterpret_cast<const float*>(smem + L::kOffRef)[sb];
-      for (int i = 0; i < n; ++i, ++tl) {
-        const int sv = tl % L::kVStages, vb = tl & 1;
-        const bool ok = (tl < 2 || PA_WAIT(L::kV16Empty + vb, ((tl >> 1) + 1) & 1)) &&
+      for (int i = 0; i < n; ++i, ++tl, ring.next()) {
+        const int sv = ring.i, vb = tl & 1;
+        const bool ok = PA_WAIT(L::kV16Empty + vb, ((tl >> 1) + 1) & 1) &&
                         PA_WAIT(L::kMetaFull + tl % L::kMeta, (tl / L::kMeta) & 1) &&
-                        PA_WAIT(L::kVFull + sv, (tl / L::kVStages) & 1);
+                        PA_WAIT(L::kVFull + sv, ring.phase);
         dead = !__all_sync(kAll, ok);
         if (dead) break;
         const float* meta = reinterpret_cast<const float*>(smem + L::kOffMeta + (tl % L::kMeta) * 32);
