@@ -115,7 +115,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kTop = 8.75f;      // P = 2^(x - m') <= 2^8.75 < 430 (e4m3: 448)
-constexpr float kRefresh = 5.25f;  // a refreshed m' puts the tile's maximum at 2^5.25
+constexpr float kRefresh = 4.25f;  // a refreshed m' puts the tile's maximum at 2^4.25
 constexpr float kNoMax = -3e38f;   // m' of a row that has seen nothing
 
 __host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
@@ -137,10 +137,10 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool v) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ float warp_max(float x) {  // through an order-preserving map to integers; no NaN
-  int k = __float_as_int(x);
-  k = __reduce_max_sync(kAll, k >= 0 ? k : k ^ 0x7FFFFFFF);
-  return __int_as_float(k >= 0 ? k : k ^ 0x7FFFFFFF);
+__device__ __forceinline__ float warp_max(float x) {  // NaN only if all are
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;

@@ -24,17 +24,18 @@
 //      S^T[key, row] = K Q^T, q 2^s = hi + lo (s puts the row's largest near
 //        448): exact for components down to 2^-10 of it, as q has 8
 //        significant bits and hi leaves at most 4;
-//      O^T[d, row] = V^T P^T per block, P = hi + lo / 16: 8 significant bits
-//        where P >= 2^-6, and nothing lost above 2^-14, 2^-19 of the largest
-//        weight or less: many small weights keep their sum.
+//      O^T[d, row] = V^T P^T, P = 2^(x - m') v_scale / R = hi + lo / 16, R the
+//        larger v_scale of the tile's two blocks: 8 significant bits where P >=
+//        2^-6, and nothing lost above 2^-14, 2^-18 of the largest weight or
+//        less: many small weights keep their sum.
 //  * Softmax: thread = key, 8 rows; the block's K scale folds into the logit.
-//    P = 2^(x - m'), m' a running reference per row that is refreshed (to put
-//    the tile's maximum at 2^5.25) only when a tile exceeds 2^8.75, so a tile
-//    usually costs one vote of the warps instead of 8 maxima.
+//    m' is a running reference per row that is refreshed (to put the tile's
+//    maximum at 2^4.25) only when a weight exceeds 2^8.75, so a tile usually
+//    costs one vote of the warps instead of 8 maxima.
 //  * A segment's key tiles are taken from the last down: the nearest keys often
 //    weigh most (with distance biases always), so m' settles at once.
-//  * O^T of each tile is read from tensor memory and added, times the block's
-//    V scale, to sums in registers: no rescaling pass, any scales.
+//  * O^T of each tile is read from tensor memory and added, times R, to sums in
+//    registers: no rescaling pass, any scales.
 //  * The key tiles of the whole call form one sequence (smla_paged.cuh) that
 //    the persistent CTAs share equally, whatever the lengths; a unit that
 //    several CTAs share is merged by a second kernel.  Lengths are read on the
@@ -91,7 +92,7 @@ struct Lay {
   static constexpr int kOffCols = kOffP + kPBufs * kPBuf;
   static constexpr int kOffMeta = kOffCols + kSegs * (int)sizeof(Columns<C>);
   static constexpr int kOffRefs = kOffMeta + kMeta * 32;
-  static constexpr int kRef = C * 4 + 32;          // factor[C], v scales, change flags of the groups
+  static constexpr int kRef = C * 4 + 32;          // factor[C], R, change flags of the groups
   static constexpr int kOffRed = kOffRefs + kRefs * kRef;          // float [groups][4][8]
   static constexpr int kOffSum = kOffRed + kGroups * 4 * 8 * 4;    // float [groups][4][8]
   static constexpr int kOffFin = kOffSum + kGroups * 4 * 8 * 4;    // float [2][m' | l][C]
@@ -105,9 +106,9 @@ struct Lay {
   };
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;
-  static constexpr int kTmemS = 0, kTmemO = 2 * N;  // S [2][N], O [2][2 blocks][N]
-  static constexpr int kTmemCols = 6 * N <= 128 ? 128 : 6 * N <= 256 ? 256 : 512;
-  static_assert(6 * N <= kTmemCols && kPerSm * kTmemCols <= 512, "tensor memory");
+  static constexpr int kTmemS = 0, kTmemO = 2 * N;  // S [2][N], O [2][N]
+  static constexpr int kTmemCols = 4 * N;
+  static_assert(kTmemCols >= 32 && kPerSm * kTmemCols <= 512, "tensor memory");
   static_assert(kPerSm * (kSmem + 1024) <= 233472, "shared memory of an SM");
   static_assert(kStage % 1024 == 0 && kQBuf % 1024 == 0 && kOffP % 128 == 0 && kOffCols % 16 == 0 &&
                 kOffRefs % 16 == 0 && kRef % 16 == 0 && kOffFin % 16 == 0 && kOffRed % 16 == 0, "alignment");
@@ -308,9 +309,9 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         tc_fence_after();
         const uint64_t dv = dv0 + (uint64_t)((st * L::kStage) >> 4), dp = dp0 + (uint64_t)((pb * L::kPBuf) >> 4);
 #pragma unroll
-        for (int step = 0; step < 4; ++step)  // 32 keys; two to a block
-          mma_f8(tmem + L::kTmemO + (2 * buf + (step >> 1)) * N, dv + ((32 * D * step) >> 4), dp + ((32 * N * step) >> 4),
-                 id, step & 1);
+        for (int step = 0; step < 4; ++step)  // 32 keys
+          mma_f8(tmem + L::kTmemO + buf * N, dv + ((32 * D * step) >> 4), dp + ((32 * N * step) >> 4), id,
+                 step > 0 ? 1u : 0u);
         mma_commit(&bars[L::kPFree + pb]);
         mma_commit(&bars[L::kEmpty + st]);  // the tile's QK^T completed before its P was written
         mma_commit(&bars[L::kOFull + buf]);
@@ -431,7 +432,8 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kSFree + buf]);
         const float* meta = reinterpret_cast<const float*>(smem + L::kOffMeta + (tl % L::kMeta) * 32);
-        const float ks = meta[key >> 6];
+        const float ks = meta[key >> 6], ref_v = fmaxf(fabsf(meta[2]), fabsf(meta[3]));
+        const float vf = ref_v > 0.f ? __fdividef(meta[2 + (key >> 6)], ref_v) : 0.f;
         const int pages = reinterpret_cast<const int*>(meta)[4];
         const int j0 = (kt + n - 1 - i) * kKeyTile, j = j0 + key;
         float x[8];
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         if (refresh) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const float mx = warp_max(x[c] == x[c] ? x[c] : -INFINITY);
+            const float mx = warp_max(x[c]);
             if (lane == c) red[quarter * 8 + c] = mx;
           }
           named_bar_sync(bar, 128);
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         }
         if (quarter == 0 && lane == 0) {
           reinterpret_cast<int*>(ref)[C + 2 + group] = refresh;
-          if (group == 0) *reinterpret_cast<float2*>(ref + 4 * C) = make_float2(meta[2], meta[3]);
+          if (group == 0) *reinterpret_cast<float*>(ref + 4 * C) = ref_v;
         }
         uint32_t hw[4], lw[4];
 #pragma unroll
@@ -507,7 +509,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
           const float p0 = ex2_approx(x[2 * c2] - m[2 * c2]), p1 = ex2_approx(x[2 * c2 + 1] - m[2 * c2 + 1]);
           l[2 * c2] += p0;
           l[2 * c2 + 1] += p1;
-          split_p(p0, p1, hw[c2], lw[c2]);
+          split_p(p0 * vf, p1 * vf, hw[c2], lw[c2]);
         }
         st_shared_v4(p_addr + pb * L::kPBuf, hw[0] | (hw[1] << 16), hw[2] | (hw[3] << 16), lw[0] | (lw[1] << 16),
                      lw[2] | (lw[3] << 16));
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         const int buf = tl & 1;
         wait(L::kRefFull + tl % L::kRefs, (tl / L::kRefs) & 1);
         const uint8_t* ref = smem + L::kOffRefs + (tl % L::kRefs) * L::kRef;
-        const float2 vs = *reinterpret_cast<const float2*>(ref + 4 * C);
+        const float ref_v = *reinterpret_cast<const float*>(ref + 4 * C);
 #pragma unroll
         for (int g = 0; g < L::kGroups; ++g)
           if (reinterpret_cast<const int*>(ref)[C + 2 + g]) {
@@ -581,16 +583,14 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         if (dead) break;
         tc_fence_after();
 #pragma unroll
-        for (int g = 0; g < L::kGroups; ++g)
+        for (int g = 0; g < L::kGroups; ++g) {
+          uint32_t o[16];
+          tmem_ld16_sync(o_addr + buf * N + 16 * g, o);
 #pragma unroll
-          for (int blk = 0; blk < 2; ++blk) {
-            uint32_t o[16];
-            tmem_ld16_sync(o_addr + (2 * buf + blk) * N + 16 * g, o);
-            const float f = blk ? vs.y : vs.x;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              acc[8 * g + c] = fmaf(fmaf(__uint_as_float(o[8 + c]), 1.f / 16.f, __uint_as_float(o[c])), f, acc[8 * g + c]);
-          }
+          for (int c = 0; c < 8; ++c)
+            acc[8 * g + c] =
+                fmaf(fmaf(__uint_as_float(o[8 + c]), 1.f / 16.f, __uint_as_float(o[c])), ref_v, acc[8 * g + c]);
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kOFree + buf]);
