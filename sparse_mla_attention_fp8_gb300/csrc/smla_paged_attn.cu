@@ -28,10 +28,11 @@
 //        larger v_scale of the tile's two blocks: 8 significant bits where P >=
 //        2^-6, and nothing lost above 2^-14, 2^-18 of the largest weight or
 //        less: many small weights keep their sum.
-//  * Softmax: thread = key, 8 rows; the block's K scale folds into the logit.
-//    m' is a running reference per row that is refreshed (to put the tile's
-//    maximum at 2^4.25) only when a weight exceeds 2^8.75, so a tile usually
-//    costs one vote of the warps instead of 8 maxima.
+//  * Softmax: thread = key, 8 or 16 rows; the block's K scale folds into the
+//    logit.  m' is a running reference per row that is set by the row's first
+//    tile (to put its maximum at 2^4.25) and afterwards only when a weight
+//    exceeds 2^8.75, so a tile usually costs one vote of the warps instead of a
+//    maximum per row.
 //  * A segment's key tiles are taken from the last down: the nearest keys often
 //    weigh most (with distance biases always), so m' settles at once.
 //  * O^T of each tile is read from tensor memory and added, times R, to sums in
@@ -41,8 +42,8 @@
 //    several CTAs share is merged by a second kernel.  Lengths are read on the
 //    device only.
 //  * Roles: TMA producer, QK^T issuer, P.V issuer, scheduler (segments ahead,
-//    their Q split and columns), C / 8 groups of 4 softmax warps, 4 warps
-//    that sum O.
+//    their Q split and columns), 4 softmax warps per 16 rows, 4 warps that sum
+//    O.
 #include "smla_paged.cuh"
 
 namespace smla {
@@ -74,7 +75,8 @@ struct Columns {
 template <int D, int C>
 struct Lay {
   static constexpr int N = 2 * C;          // MMA columns: two terms of each row
-  static constexpr int kGroups = C / 8;    // softmax groups
+  static constexpr int kCols = C == 8 ? 8 : 16;  // rows of a softmax group
+  static constexpr int kGroups = C / kCols;      // softmax groups
   static constexpr int kWarps = 4 + 4 * kGroups + 4;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPerSm = C <= 16 ? 2 : 1;
@@ -93,9 +95,10 @@ struct Lay {
   static constexpr int kOffMeta = kOffCols + kSegs * (int)sizeof(Columns<C>);
   static constexpr int kOffRefs = kOffMeta + kMeta * 32;
   static constexpr int kRef = C * 4 + 32;          // factor[C], R, change flags of the groups
-  static constexpr int kOffRed = kOffRefs + kRefs * kRef;          // float [groups][4][8]
-  static constexpr int kOffSum = kOffRed + kGroups * 4 * 8 * 4;    // float [groups][4][8]
-  static constexpr int kOffFin = kOffSum + kGroups * 4 * 8 * 4;    // float [2][m' | l][C]
+  static constexpr int kOffRed = kOffRefs + kRefs * kRef;          // float [groups][4][kCols] maxima
+  static constexpr int kOffSum = kOffRed + 4 * C * 4;              // float [groups][4][kCols] sums
+  static constexpr int kOffM = kOffSum + 4 * C * 4;                // float [C] m'
+  static constexpr int kOffFin = kOffM + C * 4;                    // float [2][m' | l][C]
   static constexpr int kOffSeg = kOffFin + 2 * 2 * C * 4;
   static constexpr int kOffBar = (kOffSeg + kSegs * (int)sizeof(Segment) + 7) / 8 * 8;
   enum {
@@ -385,14 +388,17 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       mbar_arrive(&bars[L::kSegFull + sb]);
     }
   } else if (warp < 4 + 4 * L::kGroups) {
-    // ---------------------------------------------------------------- softmax: thread = key, 8 rows per group
-    const int group = (warp - 4) >> 2, quarter = warp & 3, c0 = 8 * group;
+    // ---------------------------------------------------------------- softmax: thread = key, kCols rows per group
+    constexpr int kCols = L::kCols, kSub = kCols / 8;
+    const int group = (warp - 4) >> 2, quarter = warp & 3, c0 = kCols * group;
     const int key = 32 * quarter + lane;
-    const uint32_t s_addr = tmem + ((uint32_t)(32 * quarter) << 16) + L::kTmemS + 16 * group;
-    const uint32_t p_addr = smem_u32(smem + L::kOffP) + (key >> 3) * 8 * N + (key & 7) * 16 + group * 128;
-    float* red = reinterpret_cast<float*>(smem + L::kOffRed) + group * 32;
-    float* sums = reinterpret_cast<float*>(smem + L::kOffSum) + group * 32;
+    const uint32_t s_addr = tmem + ((uint32_t)(32 * quarter) << 16) + L::kTmemS + 2 * c0;
+    const uint32_t p_addr = smem_u32(smem + L::kOffP) + (key >> 3) * 8 * N + (key & 7) * 16 + group * kSub * 128;
+    float* red = reinterpret_cast<float*>(smem + L::kOffRed) + 4 * c0;
+    float* sums = reinterpret_cast<float*>(smem + L::kOffSum) + 4 * c0;
+    float* m_ref = reinterpret_cast<float*>(smem + L::kOffM) + c0;
     const int bar = 1 + group;
+    constexpr uint32_t kAllSeen = (1u << kCols) - 1u;
     Ring<L::kStages> ring;
     int tl = 0, seg = 0;
     bool dead = false;
@@ -405,60 +411,66 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     while (true) {
       const int sb = seg % L::kSegs;
       wait(L::kSegFull + sb, (seg / L::kSegs) & 1);
+      if (quarter == 0 && lane < kCols) m_ref[lane] = 0.f;
       dead = bar_any(bar, 128, dead);
       if (dead) break;
       const Segment* sp = reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment));
       const Columns<C>* cols = reinterpret_cast<const Columns<C>*>(smem + L::kOffCols + sb * sizeof(Columns<C>));
       const int kt = sp->kt, n = sp->n;
       if (n == 0) break;
-      float m[8], l[8];
+      uint32_t seen = 0u;  // rows that have met a key they see (the same in every thread of the group)
+      uint64_t l2[kCols / 2];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        m[c] = kNoMax;
-        l[c] = 0.f;
-      }
+      for (int c = 0; c < kCols / 2; ++c) l2[c] = 0ull;
       for (int i = 0; i < n; ++i, ++tl, ring.next()) {
         const int buf = tl & 1, st = ring.i, pb = tl % L::kPBufs;
         {
           // the tile's scales and flags (behind its K copies), and its S
-          const bool ok =
-              !dead && PA_WAIT(L::kKFull + st, ring.phase) && PA_WAIT(L::kSFull + buf, (tl >> 1) & 1);
+          const bool ok = !dead && PA_WAIT(L::kKFull + st, ring.phase) && PA_WAIT(L::kSFull + buf, (tl >> 1) & 1);
           dead = !__all_sync(kAll, ok);
         }
         tc_fence_after();
-        uint32_t raw[16];
-        tmem_ld16_sync(s_addr + buf * N, raw);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::kSFree + buf]);
         const float* meta = reinterpret_cast<const float*>(smem + L::kOffMeta + (tl % L::kMeta) * 32);
         const float ks = meta[key >> 6], ref_v = fmaxf(fabsf(meta[2]), fabsf(meta[3]));
         const float vf = ref_v > 0.f ? __fdividef(meta[2 + (key >> 6)], ref_v) : 0.f;
         const int pages = reinterpret_cast<const int*>(meta)[4];
         const int j0 = (kt + n - 1 - i) * kKeyTile, j = j0 + key;
-        float x[8];
+        float y[kCols];  // logits, then logits - m'
         {
-          const float4 f0 = *reinterpret_cast<const float4*>(&cols->scale[c0]);
-          const float4 f1 = *reinterpret_cast<const float4*>(&cols->scale[c0 + 4]);
-          const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+          const uint64_t ks2 = pack2(ks, ks);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] = (__uint_as_float(raw[c]) + __uint_as_float(raw[8 + c])) * (f[c] * ks);
+          for (int b = 0; b < kSub; ++b) {
+            uint32_t raw[16];
+            tmem_ld16_sync(s_addr + buf * N + 16 * b, raw);
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+              const float2 f = *reinterpret_cast<const float2*>(&cols->scale[c0 + 8 * b + c]);
+              const float2 v = unpack2(mul2(add2(pack2(__uint_as_float(raw[c]), __uint_as_float(raw[c + 1])),
+                                                 pack2(__uint_as_float(raw[8 + c]), __uint_as_float(raw[9 + c]))),
+                                            mul2(pack2(f.x, f.y), ks2)));
+              y[8 * b + c] = v.x;
+              y[8 * b + c + 1] = v.y;
+            }
+          }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kSFree + buf]);
         if (a.softcap > 0.f) {
           // cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))), to within a few 2^-23 cap
           const float to = 2.f * kLog2e / a.softcap, cap = a.softcap * kLog2e;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] = fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(x[c] * to)), cap);
+          for (int c = 0; c < kCols; ++c) y[c] = fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(y[c] * to)), cap);
         }
         if (a.alibi_slopes) {
 #pragma unroll
-          for (int c = 0; c < 8; c += 4) {
+          for (int c = 0; c < kCols; c += 4) {
             const float4 f = *reinterpret_cast<const float4*>(&cols->slope[c0 + c]);
             const int4 at = *reinterpret_cast<const int4*>(&cols->pos[c0 + c]);
-            x[c] = fmaf(-f.x, (float)abs(at.x - j), x[c]);
-            x[c + 1] = fmaf(-f.y, (float)abs(at.y - j), x[c + 1]);
-            x[c + 2] = fmaf(-f.z, (float)abs(at.z - j), x[c + 2]);
-            x[c + 3] = fmaf(-f.w, (float)abs(at.w - j), x[c + 3]);
+            y[c] = fmaf(-f.x, (float)abs(at.x - j), y[c]);
+            y[c + 1] = fmaf(-f.y, (float)abs(at.y - j), y[c + 1]);
+            y[c + 2] = fmaf(-f.z, (float)abs(at.z - j), y[c + 2]);
+            y[c + 3] = fmaf(-f.w, (float)abs(at.w - j), y[c + 3]);
           }
         }
         const bool inside = j0 >= sp->all_lo && j0 + kKeyTile <= sp->all_hi && pages == 3;  // every row sees every key
@@ -466,53 +478,73 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         if (!inside) {
           const bool page_ok = (pages >> (key >> 6)) & 1;
 #pragma unroll
-          for (int c = 0; c < 8; ++c)  // (no branches)
-            x[c] = page_ok & (j >= cols->lo[c0 + c]) & (j < cols->hi[c0 + c]) ? x[c] : -INFINITY;
+          for (int c = 0; c < kCols; ++c)  // (no branches)
+            y[c] = page_ok & (j >= cols->lo[c0 + c]) & (j < cols->hi[c0 + c]) ? y[c] : -INFINITY;
           // keys that no row sees may hold any codes: their V rows become zeros
           zero_v = group == 0 && (j < sp->lo || j >= sp->hi);
           if (__any_sync(kAll, zero_v)) wait(L::kVFull + st, ring.phase);
         }
         float over = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) over = fmaxf(over, x[c] - m[c]);
-        const bool refresh = bar_any(bar, 128, over > kTop);
+        for (int c = 0; c < kCols; c += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(&m_ref[c]);
+          y[c] -= m.x;
+          y[c + 1] -= m.y;
+          y[c + 2] -= m.z;
+          y[c + 3] -= m.w;
+          over = fmaxf(over, fmaxf(fmaxf(y[c], y[c + 1]), fmaxf(y[c + 2], y[c + 3])));
+        }
+        const bool refresh = bar_any(bar, 128, over > kTop) || seen != kAllSeen;
         // the factors go to the summing warps: slot tl % 4 was read before P.V of tile tl - 2 could be issued
         uint8_t* ref = smem + L::kOffRefs + (tl % L::kRefs) * L::kRef;
         wait(L::kPFree + pb, (tl / L::kPBufs + 1) & 1);  // P.V has read this P buffer
         if (refresh) {
+          // lane c (mod kCols): row c's maximum, the change of its reference, and the factor of its sums
+          float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float mx = warp_max(x[c]);
-            if (lane == c) red[quarter * 8 + c] = mx;
+          for (int c = 0; c < kCols; ++c) {
+            const float v = warp_max(y[c]);
+            if ((lane & (kCols - 1)) == c) mx = v;
           }
+          if (lane < kCols) red[quarter * kCols + lane] = mx;
           named_bar_sync(bar, 128);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const float mx = fmaxf(fmaxf(red[c], red[8 + c]), fmaxf(red[16 + c], red[24 + c]));
-            float f = 1.f;
-            if (mx - m[c] > kTop) {
-              const float to = mx - kRefresh;
-              f = ex2_approx(m[c] - to);
-              l[c] *= f;
-              m[c] = to;
-            }
-            if (quarter == 0 && lane == c) reinterpret_cast<float*>(ref)[c0 + c] = f;
+          const int c1 = lane & (kCols - 1);
+          mx = fmaxf(fmaxf(red[c1], red[kCols + c1]), fmaxf(red[2 * kCols + c1], red[3 * kCols + c1]));
+          const bool first = !((seen >> c1) & 1u);
+          const bool set = first ? mx > -INFINITY : mx > kTop;
+          const float up = set ? mx - kRefresh : 0.f, factor = set && !first ? ex2_approx(-up) : 1.f;
+          seen |= __ballot_sync(kAll, set) & kAllSeen;
+          if (quarter == 0 && lane < kCols) {
+            m_ref[lane] += up;
+            reinterpret_cast<float*>(ref)[c0 + lane] = factor;
           }
+#pragma unroll
+          for (int c = 0; c < kCols; c += 2) {
+            y[c] -= __shfl_sync(kAll, up, c);
+            y[c + 1] -= __shfl_sync(kAll, up, c + 1);
+            l2[c / 2] = mul2(l2[c / 2], pack2(__shfl_sync(kAll, factor, c), __shfl_sync(kAll, factor, c + 1)));
+          }
+          named_bar_sync(bar, 128);  // m_ref and red are in order for the next tile
         }
         if (quarter == 0 && lane == 0) {
           reinterpret_cast<int*>(ref)[C + 2 + group] = refresh;
           if (group == 0) *reinterpret_cast<float*>(ref + 4 * C) = ref_v;
         }
-        uint32_t hw[4], lw[4];
+        const uint64_t vf2 = pack2(vf, vf);
 #pragma unroll
-        for (int c2 = 0; c2 < 4; ++c2) {
-          const float p0 = ex2_approx(x[2 * c2] - m[2 * c2]), p1 = ex2_approx(x[2 * c2 + 1] - m[2 * c2 + 1]);
-          l[2 * c2] += p0;
-          l[2 * c2 + 1] += p1;
-          split_p(p0 * vf, p1 * vf, hw[c2], lw[c2]);
+        for (int b = 0; b < kSub; ++b) {
+          uint32_t hw[4], lw[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int at = 8 * b + 2 * c;
+            const uint64_t p2 = pack2(ex2_approx(y[at]), ex2_approx(y[at + 1]));
+            l2[at / 2] = add2(l2[at / 2], p2);
+            const float2 pv = unpack2(mul2(p2, vf2));
+            split_p(pv.x, pv.y, hw[c], lw[c]);
+          }
+          st_shared_v4(p_addr + pb * L::kPBuf + 128 * b, hw[0] | (hw[1] << 16), hw[2] | (hw[3] << 16),
+                       lw[0] | (lw[1] << 16), lw[2] | (lw[3] << 16));
         }
-        st_shared_v4(p_addr + pb * L::kPBuf, hw[0] | (hw[1] << 16), hw[2] | (hw[3] << 16), lw[0] | (lw[1] << 16),
-                     lw[2] | (lw[3] << 16));
         if (zero_v) {
           const uint32_t v = smem_u32(smem + st * L::kStage + L::kKTile) + key * D;
 #pragma unroll
@@ -527,21 +559,21 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       }
       // the rows' sums over the segment's keys
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        float v = l[c];
+      for (int c = 0; c < kCols; ++c) {
+        const float2 pair = unpack2(l2[c / 2]);
+        float v = c & 1 ? pair.y : pair.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-        if (lane == c) sums[quarter * 8 + c] = v;
+        if (lane == c) sums[quarter * kCols + c] = v;
       }
       named_bar_sync(bar, 128);
       if (quarter == 0) {
         float* fin = reinterpret_cast<float*>(smem + L::kOffFin + (seg & 1) * 2 * C * 4) + c0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (lane == c) {
-            fin[c] = m[c];
-            fin[C + c] = (sums[c] + sums[8 + c]) + (sums[16 + c] + sums[24 + c]);
-          }
+        if (lane < kCols) {
+          const float l = (sums[lane] + sums[kCols + lane]) + (sums[2 * kCols + lane] + sums[3 * kCols + lane]);
+          fin[lane] = l == 0.f ? kNoMax : m_ref[lane];
+          fin[C + lane] = l;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kFinFull + (seg & 1)]);
       }
@@ -577,19 +609,19 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         for (int g = 0; g < L::kGroups; ++g)
           if (reinterpret_cast<const int*>(ref)[C + 2 + g]) {
 #pragma unroll
-            for (int c = 8 * g; c < 8 * g + 8; ++c) acc[c] *= reinterpret_cast<const float*>(ref)[c];
+            for (int c = L::kCols * g; c < L::kCols * (g + 1); ++c) acc[c] *= reinterpret_cast<const float*>(ref)[c];
           }
         wait(L::kOFull + buf, (tl >> 1) & 1);
         if (dead) break;
         tc_fence_after();
 #pragma unroll
-        for (int g = 0; g < L::kGroups; ++g) {
+        for (int b = 0; b < C / 8; ++b) {
           uint32_t o[16];
-          tmem_ld16_sync(o_addr + buf * N + 16 * g, o);
+          tmem_ld16_sync(o_addr + buf * N + 16 * b, o);
 #pragma unroll
           for (int c = 0; c < 8; ++c)
-            acc[8 * g + c] =
-                fmaf(fmaf(__uint_as_float(o[8 + c]), 1.f / 16.f, __uint_as_float(o[c])), ref_v, acc[8 * g + c]);
+            acc[8 * b + c] =
+                fmaf(fmaf(__uint_as_float(o[8 + c]), 1.f / 16.f, __uint_as_float(o[c])), ref_v, acc[8 * b + c]);
         }
         tc_fence_before();
         __syncwarp();
