@@ -2,8 +2,9 @@
 
 Thin Python binding of the C-ABI library ``libsmla.so`` (declared in
 ``include/smla.h``).  Every function here only marshals torch tensors into
-pointers and sizes and calls the same-named C entry point; all the work runs
-in the library's CUDA kernels.  There is no CPU fallback: if the library has
+pointers and sizes and calls the same-named C entry point (the paged operators
+through a compiled module, csrc/smla_binding.cpp); all the work runs in the
+library's CUDA kernels.  There is no CPU fallback: if the library has
 not been built, or a tensor is not on a CUDA device, the call raises.
 
 Entry points (see include/smla.h for layouts and semantics):
@@ -31,6 +32,7 @@ _CSRC = os.path.join(_PKG, "csrc")
 _BUILD = os.path.join(_PKG, "_build")
 LIB_PATH = os.path.join(_PKG, "libsmla.so")
 HEADER = os.path.join(_ROOT, "include", "smla.h")
+BINDING_PATH = os.path.join(_PKG, "_binding.so")
 
 SOURCES = ["smla_decode.cu", "smla_attn.cu", "smla_wide.cu", "smla_wide8.cu", "smla_store.cu", "smla_nvfp4.cu", "smla_absorb.cu",
            "smla_blocks.cu", "smla_kvstore.cu", "smla_paged_attn.cu", "smla_paged_prefill.cu",
@@ -41,6 +43,7 @@ NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17",
 SMLA_OK = 0
 _lock = threading.Lock()
 _lib = None
+_binding = None
 
 
 class SmlaError(RuntimeError):
@@ -71,23 +74,46 @@ def build(force: bool = False, verbose: bool = False) -> str:
         obj = os.path.join(_BUILD, s.replace(".cu", ".o"))
         if force or _stale(obj, src):
             jobs.append([nvcc, *NVCC_FLAGS, "-c", src, "-o", obj])
+    objs = [os.path.join(_BUILD, s.replace(".cu", ".o")) for s in SOURCES]
+    link = force or bool(jobs) or not os.path.exists(LIB_PATH)
+    tmp_binding = BINDING_PATH + f".tmp{os.getpid()}"
+    bind = force or _stale(BINDING_PATH, os.path.join(_CSRC, "smla_binding.cpp"))
+    if bind:
+        jobs.append(_binding_command(tmp_binding))
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise SmlaError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise SmlaError(f"{cmd[0]} failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose:
             print(r.stdout + r.stderr)
 
     if jobs:
         with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             list(ex.map(run, jobs))
-    objs = [os.path.join(_BUILD, s.replace(".cu", ".o")) for s in SOURCES]
-    if force or jobs or not os.path.exists(LIB_PATH):
+    if bind:
+        os.replace(tmp_binding, BINDING_PATH)
+    if link:
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         run([nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", *objs, "-o", tmp])
         os.replace(tmp, LIB_PATH)
     return LIB_PATH
+
+
+def _binding_command(out: str) -> list:
+    """The compiler call for the Python binding of the paged operators (host
+    code only, against the installed torch's headers)."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            "-I" + sysconfig.get_path("include"), "-isystem", os.path.join(root, "include"), "-isystem",
+            os.path.join(root, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+            os.path.join(_CSRC, "smla_binding.cpp"), "-o", out, "-L" + os.path.join(root, "lib"),
+            "-Wl,-rpath," + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def lib():
@@ -527,72 +553,36 @@ class PagedBatch(NamedTuple):
     missing: Any           # int32 [1]
 
 
-def _args(*specs):
-    """Checks the (name, tensor, dtype, shape) of a call's contiguous tensors
-    (None: not given); the device they are all on.  One pass, as single-token
-    steps are bound by the host."""
-    dev = -1
-    for name, t, dtype, shape in specs:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise SmlaError("all tensors must be CUDA tensors (there is no CPU path)")
-        if t.dtype != dtype:
-            raise SmlaError(f"{name}: dtype {t.dtype}, expected {dtype}")
-        if t.shape != shape:
-            raise SmlaError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-        if not t.is_contiguous():
-            raise SmlaError("all tensors must be contiguous")
-        d = t.get_device()
-        if dev < 0:
-            dev = d
-        elif d != dev:
-            raise SmlaError("all tensors must be on the same device")
-    return dev
+def _bound():
+    """The compiled binding of the paged operators, on the loaded library."""
+    global _binding
+    if _binding is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries first)
+        L = lib()
+        with _lock:
+            if _binding is None:
+                if not os.path.exists(BINDING_PATH):
+                    raise SmlaError(f"{BINDING_PATH} is missing: run sparse_mla_attention_fp8_gb300.build() first")
+                spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                module.init(SmlaError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+                    "paged_blocks_extend", "paged_blocks_release", "kv_cache_store_fp8", "paged_attention_fp8",
+                    "paged_attention_fp8_workspace_bytes", "smla_last_error")))
+                _binding = module
+    return _binding
 
 
-def _rows(name, t, heads, D, dev):
-    """Checks [T, heads, D] bf16 rows that may be slices of longer ones; their
-    distance in elements."""
+def _on(stream, tensor, call, *args):
+    """call(*args) on a stream that the caller names: it is made current, so
+    that what the call allocates belongs to it."""
     import torch
-    if not t.is_cuda:
-        raise SmlaError("all tensors must be CUDA tensors (there is no CPU path)")
-    if t.get_device() != dev:
-        raise SmlaError("all tensors must be on the same device")
-    if t.dtype != torch.bfloat16:
-        raise SmlaError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
-        raise SmlaError(f"{name}: shape {tuple(shape)}, expected (T, {heads}, {D})")
-    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != D)):
-        raise SmlaError(f"{name}: the heads of a token must be contiguous")
-    return stride[0] if shape[0] > 1 else heads * D
-
-
-def _launch(dev, stream, body):
-    """body(raw stream) with the tensors' device current (the library launches
-    on the current device) and, where the caller names a stream, that stream,
-    so that what the call allocates belongs to it."""
-    import torch
-    if stream is None:
-        if dev == torch.cuda.current_device():
-            return body(torch._C._cuda_getCurrentRawStream(dev))
-        with torch.cuda.device(dev):
-            return body(torch._C._cuda_getCurrentRawStream(dev))
-    if stream.device.index != dev:
+    if tensor.is_cuda and stream.device != tensor.device:
         raise SmlaError("the stream must be on the tensors' device")
     with torch.cuda.stream(stream):
-        return body(stream.cuda_stream)
-
-
-def _address(t):
-    return None if t is None else t.data_ptr()
-
-
-def _table_shape(block_table):
-    if block_table.dim() != 2:
-        raise SmlaError(f"block_table: shape {tuple(block_table.shape)}, expected (R, MB)")
-    return block_table.shape
+        return call(*args)
 
 
 def paged_blocks_extend(context_lens, query_lens, block_table, free_blocks, free_count, num_tokens: int,
@@ -604,40 +594,10 @@ def paged_blocks_extend(context_lens, query_lens, block_table, free_blocks, free
     least the new tokens' number; num_blocks: blocks of the cache.  Returns a
     PagedBatch (`out`, if given; its seq_lens may be context_lens and its
     free_count the argument, which are then updated)."""
-    import torch
-    i32, i64 = torch.int32, torch.int64
-    R, MB = _table_shape(block_table)
-    F, T = free_blocks.numel(), int(num_tokens)
-    dev = _args(("context_lens", context_lens, i32, (R,)), ("query_lens", query_lens, i32, (R,)),
-                ("block_table", block_table, i32, (R, MB)), ("free_blocks", free_blocks, i32, (F,)),
-                ("free_count", free_count, i32, (1,)))
-    if out is not None:
-        out = PagedBatch(*out)
-        if dev != _args(("query_start", out.query_start, i32, (R + 1,)), ("seq_lens", out.seq_lens, i32, (R,)),
-                        ("req_id_per_token", out.req_id_per_token, i32, (T,)), ("positions", out.positions, i32, (T,)),
-                        ("slot_mapping", out.slot_mapping, i64, (T,)), ("free_count", out.free_count, i32, (1,)),
-                        ("missing", out.missing, i32, (1,))):
-            raise SmlaError("all tensors must be on the same device")
-
-    def body(on):
-        b = out
-        if b is None:
-            n = max(T, 0)
-            device = block_table.device
-            ints = torch.empty(2 * R + 2 * n + 3, dtype=i32, device=device)
-            parts, at = [], 0
-            for size in (R + 1, R, n, n, 1, 1):
-                parts.append(ints.as_strided((size,), (1,), at))
-                at += size
-            parts.insert(4, torch.empty(n, dtype=i64, device=device))
-            b = PagedBatch(*parts)
-        _check(lib().paged_blocks_extend(
-            context_lens.data_ptr(), query_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(),
-            free_count.data_ptr(), b.query_start.data_ptr(), b.seq_lens.data_ptr(), b.req_id_per_token.data_ptr(),
-            b.positions.data_ptr(), b.slot_mapping.data_ptr(), b.free_count.data_ptr(), b.missing.data_ptr(), R, MB,
-            int(num_blocks), F, T, on), "paged_blocks_extend")
-        return b
-    return _launch(dev, stream, body)
+    args = (context_lens, query_lens, block_table, free_blocks, free_count, num_tokens, num_blocks, out)
+    call = (_binding or _bound()).extend
+    made = call(*args) if stream is None else _on(stream, block_table, call, *args)
+    return made if type(made) is PagedBatch else PagedBatch._make(made)
 
 
 def paged_blocks_release(release, seq_lens, block_table, free_blocks, free_count, num_blocks: int, context_lens=None,
@@ -646,26 +606,9 @@ def paged_blocks_release(release, seq_lens, block_table, free_blocks, free_count
     the stack (free_blocks modified in place).  Returns (context_lens int32
     [R]: 0 for them, seq_lens for the others; free_count int32 [1]); both may
     be written over the arguments of those meanings."""
-    import torch
-    i32 = torch.int32
-    R, MB = _table_shape(block_table)
-    F = free_blocks.numel()
-    if release.dtype not in (torch.bool, torch.uint8):
-        raise SmlaError(f"release: dtype {release.dtype}, expected bool or uint8")
-    dev = _args(("release", release, release.dtype, (R,)), ("seq_lens", seq_lens, i32, (R,)),
-                ("block_table", block_table, i32, (R, MB)), ("free_blocks", free_blocks, i32, (F,)),
-                ("free_count", free_count, i32, (1,)), ("context_lens", context_lens, i32, (R,)),
-                ("free_count_out", free_count_out, i32, (1,)))
-
-    def body(on):
-        lens = torch.empty(R, dtype=i32, device=seq_lens.device) if context_lens is None else context_lens
-        left = torch.empty(1, dtype=i32, device=seq_lens.device) if free_count_out is None else free_count_out
-        _check(lib().paged_blocks_release(
-            release.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(),
-            free_count.data_ptr(), lens.data_ptr(), left.data_ptr(), R, MB, int(num_blocks), F, on),
-            "paged_blocks_release")
-        return lens, left
-    return _launch(dev, stream, body)
+    args = (release, seq_lens, block_table, free_blocks, free_count, num_blocks, context_lens, free_count_out)
+    call = (_binding or _bound()).release
+    return call(*args) if stream is None else _on(stream, block_table, call, *args)
 
 
 def kv_cache_store_fp8(k, v, query_start, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale, stream=None):
@@ -673,33 +616,10 @@ def kv_cache_store_fp8(k, v, query_start, seq_lens, block_table, k_cache, v_cach
     rows allowed) into the paged e4m3 caches (uint8 [NB,HK,64,D], scales fp32
     [NB,HK]), modified in place.  query_start int32 [R+1], seq_lens int32 [R],
     block_table int32 [R,MB]."""
-    import torch
-    i32, u8, f32 = torch.int32, torch.uint8, torch.float32
-    R, MB = _table_shape(block_table)
-    NB, HK, D = _cache_shape(k_cache)
-    dev = _args(("query_start", query_start, i32, (R + 1,)), ("seq_lens", seq_lens, i32, (R,)),
-                ("block_table", block_table, i32, (R, MB)), ("k_cache", k_cache, u8, (NB, HK, 64, D)),
-                ("v_cache", v_cache, u8, (NB, HK, 64, D)), ("k_scale", k_scale, f32, (NB, HK)),
-                ("v_scale", v_scale, f32, (NB, HK)))
-    k_stride, v_stride = _rows("k", k, HK, D, dev), _rows("v", v, HK, D, dev)
-    T = k.shape[0]
-    if v.shape[0] != T:
-        raise SmlaError(f"k has {T} tokens, v {v.shape[0]}")
-
-    def body(on):
-        _check(lib().kv_cache_store_fp8(
-            k.data_ptr(), k_stride, v.data_ptr(), v_stride, query_start.data_ptr(), seq_lens.data_ptr(),
-            block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), T,
-            HK, D, R, MB, NB, on), "kv_cache_store_fp8")
-    _launch(dev, stream, body)
+    args = (k, v, query_start, seq_lens, block_table, k_cache, v_cache, k_scale, v_scale)
+    call = (_binding or _bound()).store
+    call(*args) if stream is None else _on(stream, block_table, call, *args)
     return k_cache, v_cache, k_scale, v_scale
-
-
-def _cache_shape(cache):
-    if cache.dim() != 4 or cache.shape[2] != 64:
-        raise SmlaError(f"k_cache: shape {tuple(cache.shape)}, expected (NB, HK, 64, D)")
-    NB, HK, _, D = cache.shape
-    return NB, HK, D
 
 
 def paged_attention_fp8_workspace_bytes(T: int, H: int, HK: int, D: int, R: int, max_query_len: int) -> int:
@@ -717,37 +637,10 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
     estimate of the most new tokens of a request (default: T - R + 1).  The
     workspace, if none is given, is allocated for the call.  Returns (out bf16
     [T,H,D], lse fp32 [T,H]); rows of no request are left as they were."""
-    import torch
-    i32, u8, f32, bf16 = torch.int32, torch.uint8, torch.float32, torch.bfloat16
-    R, MB = _table_shape(block_table)
-    NB, HK, D = _cache_shape(k_cache)
-    T, H = q.shape[0], q.shape[1]
-    dev = _args(("k_cache", k_cache, u8, (NB, HK, 64, D)), ("v_cache", v_cache, u8, (NB, HK, 64, D)),
-                ("k_scale", k_scale, f32, (NB, HK)), ("v_scale", v_scale, f32, (NB, HK)),
-                ("block_table", block_table, i32, (R, MB)), ("seq_lens", seq_lens, i32, (R,)),
-                ("query_start", query_start, i32, (R + 1,)), ("alibi_slopes", alibi_slopes, f32, (H,)),
-                ("prefix_lens", prefix_lens, i32, (R,)), ("doc_start", doc_start, i32, (T,)),
-                ("out", out, bf16, (T, H, D)), ("lse", lse, f32, (T, H)))
-    stride = _rows("q", q, H, D, dev)
-    if workspace is not None and (not workspace.is_cuda or workspace.get_device() != dev or
-                                  not workspace.is_contiguous()):
-        raise SmlaError("workspace: must be contiguous, on the tensors' device")
-    longest = max(1, T - R + 1) if max_query_len is None else int(max_query_len)
-
-    def body(on):
-        o = torch.empty((T, H, D), dtype=bf16, device=q.device) if out is None else out
-        l = torch.empty((T, H), dtype=f32, device=q.device) if lse is None else lse
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(lib().paged_attention_fp8_workspace_bytes(T, H, HK, D, R, longest), dtype=u8,
-                             device=q.device)
-        _check(lib().paged_attention_fp8(
-            q.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            block_table.data_ptr(), seq_lens.data_ptr(), query_start.data_ptr(), sm_scale, longest, window, softcap,
-            _address(alibi_slopes), _address(prefix_lens), _address(doc_start), o.data_ptr(), l.data_ptr(), T, H, HK,
-            D, R, MB, NB, ws.data_ptr(), ws.numel() * ws.element_size(), on), "paged_attention_fp8")
-        return o, l
-    return _launch(dev, stream, body)
+    args = (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start, sm_scale, max_query_len, window,
+            softcap, alibi_slopes, prefix_lens, doc_start, out, lse, workspace)
+    call = (_binding or _bound()).attention
+    return call(*args) if stream is None else _on(stream, block_table, call, *args)
 
 
 def read_noalloc_status(stream=None) -> int:
