@@ -126,28 +126,56 @@ __global__ void __launch_bounds__(kMaxThreads) blocks_extend_kernel(const __grid
     const int64_t at = (int64_t)free_count - 1 - n;
     a.block_table[(int64_t)r * a.MB + j] = at >= 0 ? __ldg(a.free_blocks + at) : -1;
   }
-  for (int64_t t = gid; t < a.T; t += step) {
-    int32_t req = -1, pos = 0;
-    int64_t slot = -1;
-    if (t < (int64_t)used) {
-      req = last_not_above(start, a.R, (uint32_t)t);
-      const int64_t p = (int64_t)ctx[req] + (t - start[req]), j = p / kBlock;
-      pos = (int32_t)min(p, (int64_t)0x7fffffff);
-      if (j < a.MB) {
-        const int have = blocks_of((int64_t)ctx[req], a.MB);
-        int64_t b;
-        if (j < have) {
-          b = a.block_table[(int64_t)req * a.MB + j];  // not written by this call
-        } else {
-          const int64_t at = (int64_t)free_count - 1 - ((int64_t)first[req] + (j - have));
-          b = at >= 0 ? __ldg(a.free_blocks + at) : -1;
+  // four tokens a thread: mostly of one request and block, so one search and one table read
+  const bool whole = ((reinterpret_cast<uintptr_t>(a.req_id_per_token) | reinterpret_cast<uintptr_t>(a.positions) |
+                       reinterpret_cast<uintptr_t>(a.slot_mapping)) & 15u) == 0;  // 16-byte stores
+  for (int64_t t0 = 4 * gid; t0 < a.T; t0 += 4 * step) {
+    int32_t req[4], pos[4];
+    int64_t slot[4];
+    int r = -1, have = 0;
+    int64_t j_at = -1, b = -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t t = t0 + k;
+      req[k] = -1;
+      pos[k] = 0;
+      slot[k] = -1;
+      if (t < (int64_t)used) {
+        if (r < 0 || (uint32_t)t >= start[r + 1]) {
+          r = last_not_above(start, a.R, (uint32_t)t);
+          have = blocks_of((int64_t)ctx[r], a.MB);
+          j_at = -1;
         }
-        if (b >= 0 && b < a.NB) slot = b * kBlock + p % kBlock;
+        const int64_t p = (int64_t)ctx[r] + (t - start[r]), j = p / kBlock;
+        if (j != j_at) {
+          j_at = j;
+          b = -1;
+          if (j < have) {
+            b = a.block_table[(int64_t)r * a.MB + j];  // not written by this call
+          } else if (j < a.MB) {
+            const int64_t at = (int64_t)free_count - 1 - ((int64_t)first[r] + (j - have));
+            if (at >= 0) b = __ldg(a.free_blocks + at);
+          }
+        }
+        req[k] = r;
+        pos[k] = (int32_t)min(p, (int64_t)0x7fffffff);
+        if (b >= 0 && b < a.NB) slot[k] = b * kBlock + p % kBlock;
       }
     }
-    a.req_id_per_token[t] = req;
-    a.positions[t] = pos;
-    a.slot_mapping[t] = slot;
+    if (whole && t0 + 4 <= a.T) {
+      *reinterpret_cast<int4*>(a.req_id_per_token + t0) = make_int4(req[0], req[1], req[2], req[3]);
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<longlong2*>(a.slot_mapping + t0) = make_longlong2(slot[0], slot[1]);
+      *reinterpret_cast<longlong2*>(a.slot_mapping + t0 + 2) = make_longlong2(slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (t0 + k < a.T) {
+          a.req_id_per_token[t0 + k] = req[k];
+          a.positions[t0 + k] = pos[k];
+          a.slot_mapping[t0 + k] = slot[k];
+        }
+    }
   }
 }
 
@@ -156,26 +184,31 @@ __global__ void __launch_bounds__(kMaxThreads) blocks_extend_kernel(const __grid
 __global__ void __launch_bounds__(kMaxThreads) blocks_release_kernel(const __grid_constant__ BlocksReleaseArgs a) {
   extern __shared__ uint32_t smem_blocks[];
   cg::cluster_group cluster = cg::this_cluster();
-  uint32_t* count = smem_blocks;  // [units + 1]
   const int tid = threadIdx.x, lane = tid & 31;
   const int nw = (int)(gridDim.x * blockDim.x) >> 5, w0 = (int)(blockIdx.x * blockDim.x + tid) >> 5;
   const int nch = (a.MB + a.chunk - 1) / a.chunk, units = a.R * nch;
+  uint32_t* count = smem_blocks;       // [units + 1]
+  uint32_t* held = count + units + 1;  // [R] table entries to look at
   const int free_count = max(0, min(__ldg(a.free_count), a.F));
+  for (int r = tid; r < a.R; r += blockDim.x) held[r] = a.release[r] ? blocks_of(max(0, a.seq_lens[r]), a.MB) : 0;
   cluster.sync();  // every CTA of the cluster runs before its shared memory is written
-  auto entries = [&](int u, const int32_t*& row) {  // this unit's entries
+  // entries of unit u: the first of them, and their number
+  auto entries = [&](int u, const int32_t*& row) {
     const int r = u / nch, j0 = (u - r * nch) * a.chunk;
     row = a.block_table + (int64_t)r * a.MB + j0;
-    if (!a.release[r]) return 0;
-    return max(0, min(a.chunk, blocks_of(max(0, a.seq_lens[r]), a.MB) - j0));
+    return max(0, min(a.chunk, (int)held[r] - j0));
   };
+  constexpr int kAhead = 8;  // reads in flight a lane
   for (int u = w0; u < units; u += nw) {
     const int32_t* row;
     const int n = entries(u, row);
     int got = 0;
-#pragma unroll 4
-    for (int i = lane; i < n; i += 32) {
-      const int b = row[i];
-      got += b >= 0 && b < a.NB;
+    for (int i0 = 0; i0 < n; i0 += 32 * kAhead) {
+      int b[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) b[k] = i0 + 32 * k + lane < n ? row[i0 + 32 * k + lane] : -1;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) got += b[k] >= 0 && b[k] < a.NB;
     }
     got = __reduce_add_sync(0xffffffffu, got);
     if (lane < (int)gridDim.x) cluster.map_shared_rank(count, lane)[u] = (uint32_t)got;
@@ -187,13 +220,18 @@ __global__ void __launch_bounds__(kMaxThreads) blocks_release_kernel(const __gri
     const int32_t* row;
     const int n = entries(u, row);
     int64_t at = (int64_t)free_count + count[u];
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int b = i0 + lane < n ? row[i0 + lane] : -1;
-      const bool ok = b >= 0 && b < a.NB;
-      const uint32_t who = __ballot_sync(0xffffffffu, ok);
-      const int64_t to = at + __popc(who & ((1u << lane) - 1u));
-      if (ok && to < a.F) a.free_blocks[to] = b;
-      at += __popc(who);
+    for (int i0 = 0; i0 < n; i0 += 32 * kAhead) {
+      int b[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) b[k] = i0 + 32 * k + lane < n ? row[i0 + 32 * k + lane] : -1;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const bool ok = b[k] >= 0 && b[k] < a.NB;
+        const uint32_t who = __ballot_sync(0xffffffffu, ok);
+        const int64_t to = at + __popc(who & ((1u << lane) - 1u));
+        if (ok && to < a.F) a.free_blocks[to] = b[k];
+        at += __popc(who);
+      }
     }
   }
   cluster.sync();  // all lengths and the count have been read: context_lens and free_count_out may be the inputs
@@ -236,7 +274,7 @@ void size_cluster(int64_t work, int* ctas, int* threads) {
 
 cudaError_t launch_blocks_extend(const BlocksExtendArgs& a, cudaStream_t stream) {
   int ctas, threads;
-  size_cluster(std::max<int64_t>((int64_t)a.R + 1, a.T), &ctas, &threads);
+  size_cluster(std::max<int64_t>((int64_t)a.R + 1, (a.T + 3) / 4), &ctas, &threads);
   return launch_cluster(blocks_extend_kernel, a, ctas, threads, (size_t)(3 * (int64_t)a.R + 2) * 4, stream);
 }
 
@@ -246,7 +284,7 @@ cudaError_t launch_blocks_release(BlocksReleaseArgs a, cudaStream_t stream) {
   const int64_t units = (int64_t)a.R * ((a.MB + a.chunk - 1) / a.chunk);
   int ctas, threads;
   size_cluster(32 * units, &ctas, &threads);  // a warp each
-  return launch_cluster(blocks_release_kernel, a, ctas, threads, (size_t)(units + 1) * 4, stream);
+  return launch_cluster(blocks_release_kernel, a, ctas, threads, (size_t)(units + 1 + a.R) * 4, stream);
 }
 
 }  // namespace smla
