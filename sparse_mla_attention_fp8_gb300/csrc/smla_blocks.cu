@@ -12,12 +12,13 @@
 //     block_table[r, position / 64] * 64 + position % 64
 // release: the blocks of the released requests, in order, back on the stack.
 //
-// Both are bound by latency: a few KB to 1 MB are moved.  One launch of one
-// thread-block cluster: every CTA makes the prefix sums over the requests in
-// its shared memory (redundantly: no exchange through global memory), then
-// the cluster's threads share the tokens and blocks, each finding its request
-// by a binary search in shared memory.  All inputs that a caller may let the
-// outputs overwrite are read before a cluster barrier and written after it.
+// Both are bound by latency: a few KB to 1 MB are moved.  One launch: every CTA
+// makes the prefix sums over the requests in its shared memory (redundantly: no
+// exchange through global memory), then all threads share the tokens and blocks,
+// each finding its request by a binary search in shared memory.  Where an output
+// may overwrite an input (release always counts across CTAs, too) the CTAs form
+// one thread-block cluster, and inputs are read before a cluster barrier and
+// written after it; extend otherwise takes as many CTAs as the tokens fill.
 #include <cstdint>
 #include <algorithm>
 #include <cooperative_groups.h>
@@ -191,17 +192,22 @@ __global__ void __launch_bounds__(kMaxThreads) blocks_release_kernel(const __gri
   uint32_t* held = count + units + 1;  // [R] table entries to look at
   const int free_count = max(0, min(__ldg(a.free_count), a.F));
   for (int r = tid; r < a.R; r += blockDim.x) held[r] = a.release[r] ? blocks_of(max(0, a.seq_lens[r]), a.MB) : 0;
-  cluster.sync();  // every CTA of the cluster runs before its shared memory is written
+  // this thread's request (the cluster has a thread for each): its length may be overwritten below
+  const int mine = (int)(blockIdx.x * blockDim.x) + tid;
+  const int left = mine < a.R && !a.release[mine] ? a.seq_lens[mine] : 0;
+  for (int u = tid; u < units; u += blockDim.x) count[u] = 0u;
+  cluster.sync();  // every CTA's counts are 0 before others' arrive
   // entries of unit u: the first of them, and their number
   auto entries = [&](int u, const int32_t*& row) {
     const int r = u / nch, j0 = (u - r * nch) * a.chunk;
     row = a.block_table + (int64_t)r * a.MB + j0;
     return max(0, min(a.chunk, (int)held[r] - j0));
   };
-  constexpr int kAhead = 8;  // reads in flight a lane
+  constexpr int kAhead = 4;  // reads in flight a lane
   for (int u = w0; u < units; u += nw) {
     const int32_t* row;
     const int n = entries(u, row);
+    if (n == 0) continue;
     int got = 0;
     for (int i0 = 0; i0 < n; i0 += 32 * kAhead) {
       int b[kAhead];
@@ -211,7 +217,7 @@ __global__ void __launch_bounds__(kMaxThreads) blocks_release_kernel(const __gri
       for (int k = 0; k < kAhead; ++k) got += b[k] >= 0 && b[k] < a.NB;
     }
     got = __reduce_add_sync(0xffffffffu, got);
-    if (lane < (int)gridDim.x) cluster.map_shared_rank(count, lane)[u] = (uint32_t)got;
+    if (got > 0 && lane < (int)gridDim.x) cluster.map_shared_rank(count, lane)[u] = (uint32_t)got;
   }
   cluster.sync();
   scan_in_place(count, units, 0x7fffffffu);
@@ -235,14 +241,12 @@ __global__ void __launch_bounds__(kMaxThreads) blocks_release_kernel(const __gri
     }
   }
   cluster.sync();  // all lengths and the count have been read: context_lens and free_count_out may be the inputs
-  const int step = (int)(gridDim.x * blockDim.x);
-  for (int r = (int)(blockIdx.x * blockDim.x) + tid; r < a.R; r += step)
-    a.context_lens[r] = a.release[r] ? 0 : a.seq_lens[r];
+  if (mine < a.R) a.context_lens[mine] = left;
   if (blockIdx.x == 0 && tid == 0) *a.free_count_out = (int)min((int64_t)a.F, (int64_t)free_count + count[units]);
 }
 
 template <typename Args>
-cudaError_t launch_cluster(void (*kernel)(Args), const Args& a, int ctas, int threads, size_t smem,
+cudaError_t launch_cluster(void (*kernel)(Args), const Args& a, int ctas, int cluster, int threads, size_t smem,
                            cudaStream_t stream) {
   // set at every launch: it takes well under a microsecond and needs no per-device record
   cudaError_t e = cudaSuccess;
@@ -251,7 +255,7 @@ cudaError_t launch_cluster(void (*kernel)(Args), const Args& a, int ctas, int th
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas);
@@ -272,10 +276,24 @@ void size_cluster(int64_t work, int* ctas, int* threads) {
 
 }  // namespace
 
+static bool overlap(const void* a, const void* b, size_t a_bytes, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 cudaError_t launch_blocks_extend(const BlocksExtendArgs& a, cudaStream_t stream) {
+  const int64_t work = std::max<int64_t>((int64_t)a.R + 1, (a.T + 3) / 4);
+  const size_t smem = (size_t)(3 * (int64_t)a.R + 2) * 4, lens = (size_t)a.R * 4;
   int ctas, threads;
-  size_cluster(std::max<int64_t>((int64_t)a.R + 1, (a.T + 3) / 4), &ctas, &threads);
-  return launch_cluster(blocks_extend_kernel, a, ctas, threads, (size_t)(3 * (int64_t)a.R + 2) * 4, stream);
+  size_cluster(work, &ctas, &threads);
+  const bool in_place = overlap(a.seq_lens, a.context_lens, lens, lens) || overlap(a.seq_lens, a.query_lens, lens, lens) ||
+                        overlap(a.free_count_out, a.free_count, 4, 4);
+  if (in_place || ctas == 1) return launch_cluster(blocks_extend_kernel, a, ctas, ctas, threads, smem, stream);
+  // Separate outputs: CTAs of 512 threads, one four-token item a thread, at most 64 of them (each makes the
+  // prefix sums); 95 K tokens of 500 requests take 16.5 us in one cluster
+  constexpr int kThreads = 512;
+  ctas = (int)std::min<int64_t>(64, (work + kThreads - 1) / kThreads);
+  return launch_cluster(blocks_extend_kernel, a, ctas, 1, kThreads, smem, stream);
 }
 
 cudaError_t launch_blocks_release(BlocksReleaseArgs a, cudaStream_t stream) {
@@ -283,8 +301,8 @@ cudaError_t launch_blocks_release(BlocksReleaseArgs a, cudaStream_t stream) {
   while ((int64_t)a.R * ((a.MB + a.chunk - 1) / a.chunk) > kMaxPagedRequests) a.chunk *= 2;
   const int64_t units = (int64_t)a.R * ((a.MB + a.chunk - 1) / a.chunk);
   int ctas, threads;
-  size_cluster(32 * units, &ctas, &threads);  // a warp each
-  return launch_cluster(blocks_release_kernel, a, ctas, threads, (size_t)(units + 1 + a.R) * 4, stream);
+  size_cluster(std::max<int64_t>(32 * units, a.R), &ctas, &threads);  // a warp a unit
+  return launch_cluster(blocks_release_kernel, a, ctas, ctas, threads, (size_t)(units + 1 + a.R) * 4, stream);
 }
 
 }  // namespace smla

@@ -104,7 +104,8 @@ struct Lay {
   enum {
     kKFull = 0, kVFull = kKFull + kStages, kEmpty = kVFull + kStages, kSFull = kEmpty + kStages, kSFree = kSFull + 2,
     kPFull = kSFree + 2, kPFree = kPFull + kPBufs, kOFull = kPFree + kPBufs, kOFree = kOFull + 2,
-    kRefFull = kOFree + 2, kSegFull = kRefFull + kRefs, kSegFree = kSegFull + kSegs, kFinFull = kSegFree + kSegs,
+    kRefFull = kOFree + 2, kSegFull = kRefFull + kRefs, kQFull = kSegFull + kSegs, kSegFree = kQFull + kSegs,
+    kFinFull = kSegFree + kSegs,
     kDrainQk = kFinFull + 2, kDrainPv, kNumBars
   };
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
 
   if (tid == 0) {
     for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(&bars[L::kKFull + i], 1);
+      mbar_init(&bars[L::kKFull + i], 2);  // the copies, the block's scales
       mbar_init(&bars[L::kVFull + i], 1);
       mbar_init(&bars[L::kEmpty + i], 1);
     }
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     for (int i = 0; i < L::kRefs; ++i) mbar_init(&bars[L::kRefFull + i], L::kGroups);
     for (int i = 0; i < L::kSegs; ++i) {
       mbar_init(&bars[L::kSegFull + i], 1);
+      mbar_init(&bars[L::kQFull + i], 1);
       mbar_init(&bars[L::kSegFree + i], 3 + 4 * L::kGroups + 4);
     }
     mbar_init(&bars[L::kDrainQk], 1);
@@ -214,16 +216,11 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
           if (i + 16 < s.n) fetch(2 * (s.kt + s.n - 1 - i - 16) + 1 - lane, nb, nks, nvs);
         }
         const int b0 = __shfl_sync(kAll, b, at + 1), b1 = __shfl_sync(kAll, b, at);
-        const float k0 = __shfl_sync(kAll, ks, at + 1), k1 = __shfl_sync(kAll, ks, at);
-        const float v0 = __shfl_sync(kAll, vs, at + 1), v1 = __shfl_sync(kAll, vs, at);
         const int st = ring.i;
         dead = __any_sync(kAll, !PA_WAIT(L::kEmpty + st, ring.phase ^ 1u));  // (true at once in the first lap)
         if (dead) break;
         ring.next();
         if (lane == 0) {
-          float* meta = reinterpret_cast<float*>(smem + L::kOffMeta + (tl % L::kMeta) * 32);
-          *reinterpret_cast<float4*>(meta) = make_float4(k0, k1, v0, v1);
-          reinterpret_cast<int*>(meta)[4] = (b0 >= 0 ? 1 : 0) | (b1 >= 0 ? 2 : 0);
           const int y0 = b0 >= 0 ? (b0 * a.HK + s.g) * kBlock : outside;
           const int y1 = b1 >= 0 ? (b1 * a.HK + s.g) * kBlock : outside;
           const uint32_t kd = smem_u32(smem + st * L::kStage), vd = kd + L::kKTile;
@@ -233,6 +230,15 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
           mbar_arrive_expect_tx(&bars[L::kVFull + st], L::kKTile);
           tma_load_2d(vd, &v_map, 0, y0, &bars[L::kVFull + st]);
           tma_load_2d(vd + kBlock * D, &v_map, 0, y1, &bars[L::kVFull + st]);
+        }
+        // the scales arrive while the copies are under way
+        const float k0 = __shfl_sync(kAll, ks, at + 1), k1 = __shfl_sync(kAll, ks, at);
+        const float v0 = __shfl_sync(kAll, vs, at + 1), v1 = __shfl_sync(kAll, vs, at);
+        if (lane == 0) {
+          float* meta = reinterpret_cast<float*>(smem + L::kOffMeta + (tl % L::kMeta) * 32);
+          *reinterpret_cast<float4*>(meta) = make_float4(k0, k1, v0, v1);
+          reinterpret_cast<int*>(meta)[4] = (b0 >= 0 ? 1 : 0) | (b1 >= 0 ? 2 : 0);
+          mbar_arrive(&bars[L::kKFull + st]);
         }
         __syncwarp();
       }
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       bool dead = false;
       while (!dead) {
         const int sb = seg % L::kSegs;
-        if (!PA_WAIT(L::kSegFull + sb, (seg / L::kSegs) & 1)) break;
+        if (!PA_WAIT(L::kQFull + sb, (seg / L::kSegs) & 1)) break;
         const int n = reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment))->n;
         if (n == 0) break;
         const uint64_t dq = dq0 + (uint64_t)((sb * L::kQBuf) >> 4);
@@ -332,7 +338,10 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         const int sb = seg % L::kSegs;
         if (seg >= L::kSegs) dead = __any_sync(kAll, !PA_WAIT(L::kSegFree + sb, (seg / L::kSegs + 1) & 1));
         if (dead) return false;
-        if (lane == 0) *reinterpret_cast<Segment*>(smem + L::kOffSeg + sb * sizeof(Segment)) = s;
+        if (lane == 0) {
+          *reinterpret_cast<Segment*>(smem + L::kOffSeg + sb * sizeof(Segment)) = s;
+          mbar_arrive(&bars[L::kSegFull + sb]);  // the copies may begin
+        }
         Columns<C>* cols = reinterpret_cast<Columns<C>*>(smem + L::kOffCols + sb * sizeof(Columns<C>));
         const int rows = s.ntok * s.heads;
         PagedRequest q;
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::kSegFull + sb]);
+        if (lane == 0) mbar_arrive(&bars[L::kQFull + sb]);
         ++seg;
         return true;
     });
@@ -386,6 +395,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     if (lane == 0 && !dead) {
       reinterpret_cast<Segment*>(smem + L::kOffSeg + sb * sizeof(Segment))->n = 0;
       mbar_arrive(&bars[L::kSegFull + sb]);
+      mbar_arrive(&bars[L::kQFull + sb]);
     }
   } else if (warp < 4 + 4 * L::kGroups) {
     // ---------------------------------------------------------------- softmax: thread = key, kCols rows per group
@@ -410,7 +420,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     };
     while (true) {
       const int sb = seg % L::kSegs;
-      wait(L::kSegFull + sb, (seg / L::kSegs) & 1);
+      wait(L::kQFull + sb, (seg / L::kSegs) & 1);
       if (quarter == 0 && lane < kCols) m_ref[lane] = 0.f;
       dead = bar_any(bar, 128, dead);
       if (dead) break;

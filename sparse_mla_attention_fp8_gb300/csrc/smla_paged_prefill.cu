@@ -231,8 +231,6 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
           if (i + 16 < s.n) fetch(2 * (s.kt + s.n - 1 - i - 16) + 1 - lane, nb, nks, nvs);
         }
         const int b0 = __shfl_sync(kAll, b, at + 1), b1 = __shfl_sync(kAll, b, at);
-        const float k0 = __shfl_sync(kAll, ks, at + 1), k1 = __shfl_sync(kAll, ks, at);
-        const float v0 = __shfl_sync(kAll, vs, at + 1), v1 = __shfl_sync(kAll, vs, at);
         const int st = ring.i, sv = v_ring.i;
         const uint32_t k_phase = ring.phase;
         dead = __any_sync(kAll, !PA_WAIT(L::kKEmpty + st, k_phase ^ 1u));  // (true at once in the first lap)
@@ -240,11 +238,6 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         const int y0 = b0 >= 0 ? (b0 * a.HK + s.g) * kBlock : outside;
         const int y1 = b1 >= 0 ? (b1 * a.HK + s.g) * kBlock : outside;
         if (lane == 0) {
-          // slot tl % kMeta: its tile before had its S read before the K stage was free twice
-          float* meta = reinterpret_cast<float*>(smem + L::kOffMeta + (tl % L::kMeta) * 32);
-          *reinterpret_cast<float4*>(meta) = make_float4(k0, k1, v0, v1);
-          reinterpret_cast<int*>(meta)[4] = (b0 >= 0 ? 1 : 0) | (b1 >= 0 ? 2 : 0);
-          mbar_arrive(&bars[L::kMetaFull + tl % L::kMeta]);
           const uint32_t kd = smem_u32(smem + st * L::kKTile);
           mbar_arrive_expect_tx(&bars[L::kKFull + st], L::kKTile);
           tma_load_2d(kd, &k_map, 0, y0, &bars[L::kKFull + st]);
@@ -263,6 +256,17 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
           mbar_wait_drain(&bars[L::kKFull + st], k_phase);
           break;
         }
+        // The scales arrive while the copies are under way.  Slot tl % kMeta: its tile before had its S read
+        // before its K stage was free again.
+        const float k0 = __shfl_sync(kAll, ks, at + 1), k1 = __shfl_sync(kAll, ks, at);
+        const float v0 = __shfl_sync(kAll, vs, at + 1), v1 = __shfl_sync(kAll, vs, at);
+        if (lane == 0) {
+          float* meta = reinterpret_cast<float*>(smem + L::kOffMeta + (tl % L::kMeta) * 32);
+          *reinterpret_cast<float4*>(meta) = make_float4(k0, k1, v0, v1);
+          reinterpret_cast<int*>(meta)[4] = (b0 >= 0 ? 1 : 0) | (b1 >= 0 ? 2 : 0);
+          mbar_arrive(&bars[L::kMetaFull + tl % L::kMeta]);
+        }
+        __syncwarp();
         ring.next();
         v_ring.next();
       }
