@@ -14,14 +14,13 @@
 //    8-bit terms need five, and V is converted once for the 256 rows.  The
 //    conversion also applies v_scale / R (R the largest v_scale of the segment:
 //    at most 1) and zeroes the keys that no row sees, whose codes may be
-//    anything.  P <= 2^15 keeps 11 bits down to 2^-14 and loses nothing above
-//    2^-25.
+//    anything.  P keeps 11 bits down to 2^-14 and loses nothing above 2^-25.
 //  * Softmax: thread pair = row, each thread the keys of one block (one K
 //    scale).  P = 2^(x - m') with the row's running reference m', computed in one
 //    pass over S into registers.  m' starts at 0 and stays there while the row's
-//    logits lie where f16 is exact enough; only if some weight passes 2^15, or a
-//    row's first keys all lie below 2^-6, is it refreshed (to put the tile's
-//    largest at 2^2), O scaled in tensor memory and the pass repeated.
+//    logits lie where f16 is exact enough; only if a thread's weights add up to
+//    65000, or a row's first keys to less than 2^-6, is it refreshed (to put the
+//    tile's largest at 2^2), O scaled in tensor memory and the pass repeated.
 //  * P overwrites S in tensor memory and enters P V from there.
 //  * q is split by a kernel beforehand, so that a segment's Q is one copy that
 //    overlaps the end of the segment before.
@@ -34,9 +33,9 @@ namespace smla {
 namespace {
 
 constexpr int kRows = 128;          // rows of a half
-constexpr float kTop16 = 15.f;      // P = 2^(x - m') <= 2^15 (f16: 65504)
+constexpr float kTop16 = 65000.f;   // largest sum of a thread's weights P = 2^(x - m') (f16: 65504)
 constexpr float kRefresh16 = 2.f;   // a refreshed m' puts the tile's maximum at 2^2
-constexpr float kLow16 = -6.f;      // a row that begins below 2^-6 is refreshed
+constexpr float kLow16 = 0x1p-6f;   // a row whose first keys weigh less is refreshed
 // Places of a unit beside its tiles: about what its start and end take.
 constexpr int kUnitCost = 3;
 
@@ -421,6 +420,7 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         const float vs = __fdividef(meta[2 + (w >> 1)], v_ref);  // warp w: keys 32 w .. 32 w + 31 of the tile
         const uint32_t f = pack_f16x2(vs, vs);
         const int j0 = (kt + n - 1 - i) * kKeyTile;
+        const bool inside = j0 >= lo && j0 + kKeyTile <= hi;  // some row sees each key
         const uint32_t src = smem_u32(smem + L::kOffV + sv * L::kKTile), dst = smem_u32(smem + L::kOffV16 + vb * L::kV16);
 #pragma unroll
         for (int it = 0; it < 32 / kKeysPer; ++it) {
@@ -431,12 +431,15 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
                        : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
                        : "r"(src + swz<D>(r, ch))
                        : "memory");
-          const bool seen = j >= lo && j < hi;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             uint32_t x;
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"((uint16_t)(c[k >> 1] >> (16 * (k & 1)))));
-            o[k] = seen ? mul_f16x2(x, f) : 0u;
+            o[k] = mul_f16x2(x, f);
+          }
+          if (!inside && (j < lo || j >= hi)) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = 0u;
           }
           // columns 16 ch .. 16 ch + 15 of the key: chunks 2 (ch % 4), + 1 of panel ch / 4, 128-byte swizzle
           const uint32_t base = dst + (uint32_t)(ch >> 2) * (kKeyTile * 128) + r * 128;
@@ -525,75 +528,85 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
           const int lo_k = min(max(lo - jb, 0), 64), hi_k = min(max(hi - jb, 0), 64);
           if (hi_k > lo_k) seen = (~0ull >> (64 - (hi_k - lo_k))) << lo_k;
         }
+        // logits - m' of keys 16 c .. 16 c + 15 of the block
+        auto logits = [&](int c, uint32_t (&x)[16]) {
+          tmem_ld16_sync(s_addr + 16 * c, x);
+          if (!changed) {
+            const uint64_t f2 = pack2(f, f), m2 = pack2(-m, -m);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, m2));
+              x[2 * k] = __float_as_uint(y.x);
+              x[2 * k + 1] = __float_as_uint(y.y);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+            if (a.softcap > 0.f) {
+              // cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))), to within a few 2^-23 cap
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                x[k] = __float_as_uint(
+                    fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(__uint_as_float(x[k]) * cap_to)), cap));
+            }
+            if (a.alibi_slopes) {
+              float away = (float)(pos - jb - 16 * c);
+              asm volatile("" : "+f"(away));  // as bits below
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                x[k] = __float_as_uint(fmaf(-slope, fabsf(away - (float)k), __uint_as_float(x[k])));
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) - m);
+          }
+          if (!inside) {
+            // (opaque: otherwise the tests move out of the loops and run for every tile)
+            uint32_t bits = (uint32_t)(seen >> (16 * c));
+            asm volatile("" : "+r"(bits));
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = (bits >> k) & 1u ? x[k] : 0xff800000u;  // -infinity
+          }
+        };
         uint32_t pw[32];  // the weights, f16 pairs
         float part;
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
-          float top = -INFINITY;  // the largest x - m'
           uint64_t sum2 = 0ull;
-          const uint64_t f2 = pack2(f, f), m2 = pack2(-m, -m);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t x[16];
-            tmem_ld16_sync(s_addr + 16 * c, x);
-            if (!changed) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, m2));
-                x[2 * k] = __float_as_uint(y.x);
-                x[2 * k + 1] = __float_as_uint(y.y);
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-              if (a.softcap > 0.f) {
-                // cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))), to within a few 2^-23 cap
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  x[k] = __float_as_uint(
-                      fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(__uint_as_float(x[k]) * cap_to)), cap));
-              }
-              if (a.alibi_slopes) {
-                float away = (float)(pos - jb - 16 * c);
-                asm volatile("" : "+f"(away));  // as bits below
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  x[k] = __float_as_uint(fmaf(-slope, fabsf(away - (float)k), __uint_as_float(x[k])));
-              }
-#pragma unroll
-              for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) - m);
-            }
-            if (!inside) {
-              // (opaque: otherwise the 64 tests move out of the pass loop and run for every tile)
-              uint32_t bits = (uint32_t)(seen >> (16 * c));
-              asm volatile("" : "+r"(bits));
-#pragma unroll
-              for (int k = 0; k < 16; ++k) x[k] = (bits >> k) & 1u ? x[k] : 0xff800000u;  // -infinity
-            }
+            logits(c, x);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const float x0 = __uint_as_float(x[2 * k]), x1 = __uint_as_float(x[2 * k + 1]);
-              top = fmaxf(top, fmaxf(x0, x1));
-              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              const float p0 = ex2_approx(__uint_as_float(x[2 * k])), p1 = ex2_approx(__uint_as_float(x[2 * k + 1]));
               sum2 = add2(sum2, pack2(p0, p1));
               pw[8 * c + k] = pack_f16x2(p0, p1);
             }
           }
           const float2 s2 = unpack2(sum2);
           part = s2.x + s2.y;
-          const bool low = l == 0.f && top < kLow16 && top > -INFINITY;
-          if (pass == 1 || !bar_any(bar, 64, top > kTop16 || low)) break;
+          // The sum tells whether some weight may be too large for f16, or a row's first keys too small for it
+          // (a sum of 0 with keys to see: below what a float holds).
+          const bool low = l == 0.f && part < kLow16 && (inside || seen != 0ull);
+          if (pass == 1 || !bar_any(bar, 64, part > kTop16 || low)) break;
+          float top = -INFINITY;  // the largest logit - m'
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[16];
+            logits(c, x);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) top = fmaxf(top, __uint_as_float(x[k]));
+          }
           red[blk * kRows + row] = top;
           sums[blk * kRows + row] = l;
           named_bar_sync(bar, 64);
           top = fmaxf(red[row], red[kRows + row]);
           float g = 1.f;
-          if (top > kTop16) {
-            const float up = top - kRefresh16;
-            g = ex2_approx(-up);
+          if (top > kRefresh16 && top < INFINITY) {
+            g = ex2_approx(kRefresh16 - top);
             l *= g;
-            m += up;
-          } else if (top < kLow16 && top > -INFINITY && sums[row] + sums[kRows + row] == 0.f) {
+            m += top - kRefresh16;
+          } else if (top > -INFINITY && sums[row] + sums[kRows + row] == 0.f) {
             m += top - kRefresh16;  // (O is 0 so far)
           }
           // P V of the tiles before is complete: S of this tile was issued behind it
