@@ -756,7 +756,7 @@ size_t paged_attention_fp8_workspace_bytes(int T, int H, int HK, int D, int R, i
     return 0;
   int sms = 0;
   if (num_sms(&sms) != SMLA_OK) return 0;
-  return smla::paged_attention_workspace(T, H, HK, D, max_query_len, sms);
+  return smla::paged_attention_workspace(T, H, HK, D, R, max_query_len, sms);
 }
 
 int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
@@ -787,7 +787,7 @@ int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache,
   if (!workspace || workspace_bytes >= need) {
     rc = num_sms(&sms);
     if (rc != SMLA_OK) return rc;
-    need = smla::paged_attention_workspace(T, H, HK, D, max_query_len, sms);
+    need = smla::paged_attention_workspace(T, H, HK, D, R, max_query_len, sms);
   }
   if (workspace) {
     if (workspace_bytes < need)

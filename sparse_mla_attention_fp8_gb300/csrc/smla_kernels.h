@@ -177,10 +177,10 @@ struct PagedAttnArgs {
   int64_t NB;
 };
 // Many rows per query tile (smla_paged_prefill.cu); called by launch_paged_attention.
-size_t paged_prefill_workspace(int T, int H, int D, int num_sms);
+size_t paged_prefill_workspace(int T, int H, int D, int R, int num_sms);
 cudaError_t launch_paged_prefill(const PagedAttnArgs& a, int num_sms, cudaStream_t stream);
 // max_query_len: an estimate.
-size_t paged_attention_workspace(int T, int H, int HK, int D, int max_query_len, int num_sms);
+size_t paged_attention_workspace(int T, int H, int HK, int D, int R, int max_query_len, int num_sms);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int max_query_len, int num_sms, cudaStream_t stream);
 
 // Offsets inside the workspace.

@@ -65,11 +65,6 @@ struct PagedRequest {
     const int x = window_lo(a, t);
     return a.doc_start ? max(x, __ldg(a.doc_start + t)) : x;
   }
-  // Union [lo, hi) of the keys that rows ta .. tb - 1 see, documents aside.
-  __device__ __forceinline__ void range(const PagedAttnArgs& a, int ta, int tb, int& lo_, int& hi_) const {
-    lo_ = window_lo(a, ta);
-    hi_ = hi(tb - 1);
-  }
 };
 
 // Key tiles [first, first + count) of a query tile; one (of no visible key) where nothing is seen.
@@ -83,8 +78,7 @@ __device__ __forceinline__ void key_tiles(int lo, int hi, int& first, int& count
 // behind unit_cost places that stand for its start and end.  `ctas` CTAs take
 // equal contiguous ranges of it, so a unit's keys may be split over consecutive
 // CTAs: each then leaves a partial result, and the first of them a record for
-// the merge.  Document starts do not count here (they are per token); a CTA skips
-// the tiles of its range that lie before all its rows' documents.
+// the merge.
 __device__ __forceinline__ int64_t range_begin(int64_t c, int64_t total, int ctas) { return c * total / ctas; }
 // The CTA whose range holds tile x.
 __device__ __forceinline__ int range_of(int64_t x, int64_t total, int ctas) {
@@ -257,7 +251,28 @@ struct PagedParams {
   float* part_ml;       // [2 ctas][m' | l][C]
   float* part_o;        // [2 ctas][C][D]
   float* q_scale;       // [T, H], of a q split beforehand
+  const int32_t* tile_doc;  // first document start of each query tile, if found beforehand (see tile_slot)
 };
+
+// Query tile (ta - t0) / tq of request r among those of the batch, with room
+// for every request's: request r's begin at floor(t0 / tq) + r.
+__device__ __forceinline__ int tile_slot(const PagedParams& p, int r, int t0, int ta) {
+  return t0 / p.tq + r + (ta - t0) / p.tq;
+}
+// Keys [lo, hi) that hold all that rows ta .. tb - 1 see.
+__device__ __forceinline__ void tile_range(const PagedParams& p, const PagedRequest& q, int r, int ta, int tb, int& lo,
+                                           int& hi) {
+  lo = q.window_lo(p.a, ta);
+  hi = q.hi(tb - 1);
+  if (p.a.doc_start) {
+    int doc = 0x7fffffff;
+    if (p.tile_doc)
+      doc = p.tile_doc[tile_slot(p, r, q.t0, ta)];
+    else
+      for (int t = ta; t < tb; ++t) doc = min(doc, __ldg(p.a.doc_start + t));
+    lo = max(lo, doc);
+  }
+}
 
 // Places of request r in the sequence (over its query tiles and the K/V heads).
 __device__ __forceinline__ int64_t request_tiles(const PagedParams& p, int r) {
@@ -266,7 +281,7 @@ __device__ __forceinline__ int64_t request_tiles(const PagedParams& p, int r) {
   int64_t n = 0;
   for (int t = q.t0; t < q.t1; t += p.tq) {
     int lo, hi, first, count;
-    q.range(p.a, t, min(t + p.tq, q.t1), lo, hi);
+    tile_range(p, q, r, t, min(t + p.tq, q.t1), lo, hi);
     key_tiles(lo, hi, first, count);
     n += count + p.unit_cost;
   }
@@ -350,7 +365,7 @@ __device__ __forceinline__ PagedMerge walk_segments(const PagedParams& p, const 
     for (int ta = q.t0; ta < q.t1 && x < w.x1; ta += p.tq) {
       const int tb = min(ta + p.tq, q.t1);
       Segment s;
-      q.range(a, ta, tb, s.lo, s.hi);
+      tile_range(p, q, r, ta, tb, s.lo, s.hi);
       int first, count;
       key_tiles(s.lo, s.hi, first, count);
       const int len = count + p.unit_cost;  // places of a unit

@@ -698,9 +698,9 @@ int rows_for(int G, int max_query_len) {
 
 }  // namespace
 
-size_t paged_attention_workspace(int T, int H, int HK, int D, int max_query_len, int num_sms) {
+size_t paged_attention_workspace(int T, int H, int HK, int D, int R, int max_query_len, int num_sms) {
   const int C = rows_for(H / HK, max_query_len);
-  return C == 256 ? paged_prefill_workspace(T, H, D, num_sms) : paged_sizes(C, D, C <= 16 ? 2 : 1, num_sms).bytes;
+  return C == 256 ? paged_prefill_workspace(T, H, D, R, num_sms) : paged_sizes(C, D, C <= 16 ? 2 : 1, num_sms).bytes;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int max_query_len, int num_sms, cudaStream_t stream) {

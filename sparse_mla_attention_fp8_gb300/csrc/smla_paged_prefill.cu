@@ -115,7 +115,42 @@ __global__ void __launch_bounds__(kSplitThreads)
   if (c == 0) scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f : kLog2e);
 }
 
-template <int D>
+// First document start of each query tile, a warp each: the shares of the CTAs
+// go by the keys that tiles really meet.
+__global__ void __launch_bounds__(kSplitThreads)
+    paged_tile_doc_kernel(const __grid_constant__ PagedParams p, int32_t* __restrict__ tile_doc, int slots) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int u = ((int)blockIdx.x * kSplitThreads + (int)threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  if (u >= slots) return;
+  const PagedAttnArgs& a = p.a;
+  const int r = search_units(a.R, u, [&](int i) { return clamp_start(a.query_start, i, a.T) / p.tq + i; });
+  const int t0 = clamp_start(a.query_start, r, a.T), t1 = clamp_start(a.query_start, r + 1, a.T);
+  const int64_t ta = t0 + (int64_t)(u - (t0 / p.tq + r)) * p.tq;
+  int doc = 0x7fffffff;
+  if (ta >= t0)
+    for (int64_t t = ta + lane; t < min(ta + p.tq, (int64_t)t1); t += 32) doc = min(doc, __ldg(a.doc_start + t));
+  doc = __reduce_min_sync(kAll, doc);
+  if (lane == 0) tile_doc[u] = doc;
+}
+
+// log2(e) tanh(u) / u as a polynomial of s = u^2 <= 0.75: the one of degree 5 through
+// the Chebyshev points of [0, 0.75], to within 2 x 2^-23 of the value.  Caps are wide as
+// a rule, so that most keys need no exponential and no reciprocal for theirs: those
+// two and the weight's exponential are 3 of the 16 a clock that an SM has, 6144
+// clocks of a tile (256 rows, 128 keys) whose products take 2048.
+constexpr float kTanhTop = 0.866f;  // of |u|
+__device__ __forceinline__ uint64_t tanh_ratio2(uint64_t s) {
+  const auto two = [](float c) { return pack2(c * kLog2e, c * kLog2e); };
+  uint64_t y = fma2(two(-3.89344e-3f), s, two(1.83672e-2f));
+  y = fma2(y, s, two(-5.271812e-2f));
+  y = fma2(y, s, two(1.3312319e-1f));
+  y = fma2(y, s, two(-3.333201e-1f));
+  return fma2(y, s, two(0.9999999f));
+}
+
+// kBent: with a softcap or slopes.
+template <int D, bool kBent>
 __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
     paged_prefill_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap k_map,
                          const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map) {
@@ -469,6 +504,7 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
     float* sums = reinterpret_cast<float*>(smem + L::kOffSum) + half * 2 * kRows;
     const int bar = 1 + 4 * half + quarter;  // the 64 threads of 32 rows
     const float cap_to = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f, cap = a.softcap * kLog2e;
+    const float cap_poly = kTanhTop * a.softcap;
     int tl = 0, seg = 0, done = 0;  // tiles before the segment; tiles of this half
     bool dead = false;
     // After a wait that ran out the loops go on without waiting to the end of the segment, where the
@@ -521,7 +557,6 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         const int pages = reinterpret_cast<const int*>(meta)[4];
         const int j0 = (kt + n - 1 - i) * kKeyTile, jb = j0 + 64 * blk;  // first keys of the tile and of this block
         const bool inside = j0 >= sp->all_lo && j0 + kKeyTile <= sp->all_hi && pages == 3;  // no mask
-        const bool changed = a.alibi_slopes || a.softcap > 0.f;
         // the block's keys that this row sees, a bit each
         uint64_t seen = 0ull;
         if (!inside && ((pages >> blk) & 1)) {
@@ -531,33 +566,47 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         // logits - m' of keys 16 c .. 16 c + 15 of the block
         auto logits = [&](int c, uint32_t (&x)[16]) {
           tmem_ld16_sync(s_addr + 16 * c, x);
-          if (!changed) {
-            const uint64_t f2 = pack2(f, f), m2 = pack2(-m, -m);
+          const uint64_t f2 = pack2(f, f), m2 = pack2(-m, -m);
+          if (kBent && a.softcap > 0.f) {
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float2 y = unpack2(mul2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2));
+              top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
+              x[2 * k] = __float_as_uint(y.x);
+              x[2 * k + 1] = __float_as_uint(y.y);
+            }
+            if (__any_sync(kAll, top > cap_poly)) {
+              // cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))), to within a few 2^-23 cap
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                x[k] = __float_as_uint(
+                    fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(__uint_as_float(x[k]) * cap_to)), cap) - m);
+            } else {
+              const uint64_t u2 = pack2(0.5f * kLn2 * cap_to, 0.5f * kLn2 * cap_to);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint64_t y = pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+                const uint64_t u = mul2(y, u2);
+                const float2 z = unpack2(fma2(y, tanh_ratio2(mul2(u, u)), m2));
+                x[2 * k] = __float_as_uint(z.x);
+                x[2 * k + 1] = __float_as_uint(z.y);
+              }
+            }
+          } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, m2));
               x[2 * k] = __float_as_uint(y.x);
               x[2 * k + 1] = __float_as_uint(y.y);
             }
-          } else {
+          }
+          if (kBent && a.alibi_slopes) {
+            float away = (float)(pos - jb - 16 * c);
+            asm volatile("" : "+f"(away));  // as bits below
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-            if (a.softcap > 0.f) {
-              // cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))), to within a few 2^-23 cap
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                x[k] = __float_as_uint(
-                    fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(__uint_as_float(x[k]) * cap_to)), cap));
-            }
-            if (a.alibi_slopes) {
-              float away = (float)(pos - jb - 16 * c);
-              asm volatile("" : "+f"(away));  // as bits below
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                x[k] = __float_as_uint(fmaf(-slope, fabsf(away - (float)k), __uint_as_float(x[k])));
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) - m);
+            for (int k = 0; k < 16; ++k)
+              x[k] = __float_as_uint(fmaf(-slope, fabsf(away - (float)k), __uint_as_float(x[k])));
           }
           if (!inside) {
             // (opaque: otherwise the tests move out of the loops and run for every tile)
@@ -695,10 +744,14 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
   }
 }
 
-// Workspace: what every call has, then the two terms of q and its scales.
+// Workspace: what every call has, then the two terms of q, its scales, and the query tiles' document starts.
 size_t terms_offset(const PagedSizes& sz) { return align256(sz.bytes); }
 size_t scales_offset(const PagedSizes& sz, int T, int H, int D) {
   return terms_offset(sz) + align256((size_t)2 * T * H * D);
+}
+
+size_t docs_offset(const PagedSizes& sz, int T, int H, int D) {
+  return scales_offset(sz, T, H, D) + align256((size_t)T * H * 4);
 }
 
 // A term of q as [2 T, H, D] bytes (both terms), a box the rows of half a query tile.
@@ -729,16 +782,23 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t stream) {
   const int64_t threads = (int64_t)a.T * a.H * (D / 8);
   e = launch_overlapped(paged_split_q_kernel<D>, dim3((unsigned)((threads + kSplitThreads - 1) / kSplitThreads)),
                         kSplitThreads, 0, stream, a, terms, p.q_scale);
+  if (e == cudaSuccess && a.doc_start) {
+    int32_t* docs = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) + docs_offset(sz, a.T, a.H, D));
+    const int slots = a.T / p.tq + a.R;
+    e = launch_overlapped(paged_tile_doc_kernel, dim3((unsigned)((slots + kSplitThreads / 32 - 1) / (kSplitThreads / 32))),
+                          kSplitThreads, 0, stream, p, docs, slots);
+    p.tile_doc = docs;
+  }
   if (e == cudaSuccess)
-    e = launch_overlapped(paged_prefill_kernel<D>, dim3((unsigned)p.ctas), L::kThreads, L::kSmem, stream, p, k_map, v_map,
-                          q_map);
+    e = launch_overlapped(a.softcap > 0.f || a.alibi_slopes ? paged_prefill_kernel<D, true> : paged_prefill_kernel<D, false>,
+                          dim3((unsigned)p.ctas), L::kThreads, L::kSmem, stream, p, k_map, v_map, q_map);
   return e == cudaSuccess ? launch_merge<D, C>(p, stream) : e;
 }
 
 }  // namespace
 
-size_t paged_prefill_workspace(int T, int H, int D, int num_sms) {
-  return scales_offset(paged_sizes(2 * kRows, D, 1, num_sms), T, H, D) + align256((size_t)T * H * 4);
+size_t paged_prefill_workspace(int T, int H, int D, int R, int num_sms) {
+  return docs_offset(paged_sizes(2 * kRows, D, 1, num_sms), T, H, D) + ((size_t)T + R) * 4;
 }
 
 cudaError_t launch_paged_prefill(const PagedAttnArgs& a, int num_sms, cudaStream_t stream) {
