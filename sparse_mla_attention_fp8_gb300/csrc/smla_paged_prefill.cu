@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   split_q8(w, amax, hi, lo, back);
   *reinterpret_cast<uint2*>(terms + row * D + 8 * c) = make_uint2(hi[0], hi[1]);
   *reinterpret_cast<uint2*>(terms + (rows + row) * D + 8 * c) = make_uint2(lo[0], lo[1]);
-  if (c == 0) scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f : kLog2e);
+  if (c == 0) scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f / a.softcap : kLog2e);
 }
 
 // First document start of each query tile, a warp each: the shares of the CTAs
@@ -134,20 +134,13 @@ __global__ void __launch_bounds__(kSplitThreads)
   if (lane == 0) tile_doc[u] = doc;
 }
 
-// log2(e) tanh(u) / u as a polynomial of s = u^2 <= 0.75: the one of degree 5 through
-// the Chebyshev points of [0, 0.75], to within 2 x 2^-23 of the value.  Caps are wide as
-// a rule, so that most keys need no exponential and no reciprocal for theirs: those
-// two and the weight's exponential are 3 of the 16 a clock that an SM has, 6144
-// clocks of a tile (256 rows, 128 keys) whose products take 2048.
-constexpr float kTanhTop = 0.866f;  // of |u|
-__device__ __forceinline__ uint64_t tanh_ratio2(uint64_t s) {
-  const auto two = [](float c) { return pack2(c * kLog2e, c * kLog2e); };
-  uint64_t y = fma2(two(-3.89344e-3f), s, two(1.83672e-2f));
-  y = fma2(y, s, two(-5.271812e-2f));
-  y = fma2(y, s, two(1.3312319e-1f));
-  y = fma2(y, s, two(-3.333201e-1f));
-  return fma2(y, s, two(0.9999999f));
-}
+// tanh(u) / u as a polynomial of u^2 <= 0.5: the one of degree 4 through the Chebyshev
+// points of [0, 0.5], to within 4 x 2^-23 of the value.  Caps are wide as a rule, so
+// that most keys need no exponential and no reciprocal for theirs: those two and the
+// weight's exponential are 3 of the 16 a clock that an SM has, 6144 clocks of a tile
+// (256 rows, 128 keys) whose products take 2048.
+constexpr float kTanhTop = 0.5f;  // of u^2
+__device__ constexpr float kTanh[5] = {0.99999964f, -0.33329946f, 0.13277967f, -0.05072029f, 0.01364212f};
 
 // kBent: with a softcap or slopes.
 template <int D, bool kBent>
@@ -503,8 +496,7 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
     float* red = reinterpret_cast<float*>(smem + L::kOffRed) + half * 2 * kRows;
     float* sums = reinterpret_cast<float*>(smem + L::kOffSum) + half * 2 * kRows;
     const int bar = 1 + 4 * half + quarter;  // the 64 threads of 32 rows
-    const float cap_to = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f, cap = a.softcap * kLog2e;
-    const float cap_poly = kTanhTop * a.softcap;
+    const float cap = a.softcap * kLog2e;
     int tl = 0, seg = 0, done = 0;  // tiles before the segment; tiles of this half
     bool dead = false;
     // After a wait that ran out the loops go on without waiting to the end of the segment, where the
@@ -553,7 +545,6 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         }
         tc_fence_after();
         const float* meta = reinterpret_cast<const float*>(smem + L::kOffMeta + (tl % L::kMeta) * 32);
-        const float f = f_row * meta[blk];
         const int pages = reinterpret_cast<const int*>(meta)[4];
         const int j0 = (kt + n - 1 - i) * kKeyTile, jb = j0 + 64 * blk;  // first keys of the tile and of this block
         const bool inside = j0 >= sp->all_lo && j0 + kKeyTile <= sp->all_hi && pages == 3;  // no mask
@@ -563,57 +554,72 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
           const int lo_k = min(max(lo - jb, 0), 64), hi_k = min(max(hi - jb, 0), 64);
           if (hi_k > lo_k) seen = (~0ull >> (64 - (hi_k - lo_k))) << lo_k;
         }
+        float f = f_row * meta[blk];  // (with a cap: over the cap)
+        // Where S takes more than a factor, its logits take its place first (in a loop of their own: unrolled into
+        // the pass below, the code ran out of the instruction caches).
+        if (kBent || !inside) {
+          const uint64_t f2 = pack2(f, f);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[16];
+            tmem_ld16_sync(s_addr + 16 * c, x);
+            // x f, with a cap u = x f / cap
+            uint64_t squares = 0ull;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint64_t u2 = mul2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2);
+              if (kBent) squares = fma2(u2, u2, squares);
+              const float2 u = unpack2(u2);
+              x[2 * k] = __float_as_uint(u.x);
+              x[2 * k + 1] = __float_as_uint(u.y);
+            }
+            if (kBent && a.softcap > 0.f) {
+              const float2 sq = unpack2(squares);
+              if (__all_sync(kAll, sq.x <= kTanhTop && sq.y <= kTanhTop)) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const uint64_t u = pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+                  const uint64_t u2 = mul2(u, u);
+                  uint64_t y = pack2(cap * kTanh[4], cap * kTanh[4]);
+#pragma unroll
+                  for (int d = 3; d >= 0; --d) y = fma2(y, u2, pack2(cap * kTanh[d], cap * kTanh[d]));
+                  const float2 z = unpack2(mul2(u, y));
+                  x[2 * k] = __float_as_uint(z.x);
+                  x[2 * k + 1] = __float_as_uint(z.y);
+                }
+              } else {
+                // tanh(u) = 1 - 2 / (1 + e^(2 u)), to within a few 2^-23
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  x[k] = __float_as_uint(
+                      fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(__uint_as_float(x[k]) * (2.f * kLog2e))), cap));
+              }
+            }
+            if (kBent && a.alibi_slopes) {
+              const float away = (float)(pos - jb - 16 * c);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                x[k] = __float_as_uint(fmaf(-slope, fabsf(away - (float)k), __uint_as_float(x[k])));
+            }
+            if (!inside) {
+              const uint32_t bits = (uint32_t)(seen >> (16 * c));
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x[k] = (bits >> k) & 1u ? x[k] : 0xff800000u;  // -infinity
+            }
+            tmem_st16(s_addr + 16 * c, x);
+          }
+          tmem_st_wait();
+          f = 1.f;
+        }
         // logits - m' of keys 16 c .. 16 c + 15 of the block
         auto logits = [&](int c, uint32_t (&x)[16]) {
           tmem_ld16_sync(s_addr + 16 * c, x);
           const uint64_t f2 = pack2(f, f), m2 = pack2(-m, -m);
-          if (kBent && a.softcap > 0.f) {
-            float top = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float2 y = unpack2(mul2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2));
-              top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
-              x[2 * k] = __float_as_uint(y.x);
-              x[2 * k + 1] = __float_as_uint(y.y);
-            }
-            if (__any_sync(kAll, top > cap_poly)) {
-              // cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))), to within a few 2^-23 cap
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                x[k] = __float_as_uint(
-                    fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(__uint_as_float(x[k]) * cap_to)), cap) - m);
-            } else {
-              const uint64_t u2 = pack2(0.5f * kLn2 * cap_to, 0.5f * kLn2 * cap_to);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint64_t y = pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
-                const uint64_t u = mul2(y, u2);
-                const float2 z = unpack2(fma2(y, tanh_ratio2(mul2(u, u)), m2));
-                x[2 * k] = __float_as_uint(z.x);
-                x[2 * k + 1] = __float_as_uint(z.y);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, m2));
-              x[2 * k] = __float_as_uint(y.x);
-              x[2 * k + 1] = __float_as_uint(y.y);
-            }
-          }
-          if (kBent && a.alibi_slopes) {
-            float away = (float)(pos - jb - 16 * c);
-            asm volatile("" : "+f"(away));  // as bits below
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              x[k] = __float_as_uint(fmaf(-slope, fabsf(away - (float)k), __uint_as_float(x[k])));
-          }
-          if (!inside) {
-            // (opaque: otherwise the tests move out of the loops and run for every tile)
-            uint32_t bits = (uint32_t)(seen >> (16 * c));
-            asm volatile("" : "+r"(bits));
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = (bits >> k) & 1u ? x[k] : 0xff800000u;  // -infinity
+          for (int k = 0; k < 8; ++k) {
+            const float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, m2));
+            x[2 * k] = __float_as_uint(y.x);
+            x[2 * k + 1] = __float_as_uint(y.y);
           }
         };
         uint32_t pw[32];  // the weights, f16 pairs
