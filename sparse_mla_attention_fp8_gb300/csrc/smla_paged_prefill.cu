@@ -37,7 +37,7 @@ constexpr float kTop16 = 65000.f;   // largest sum of a thread's weights P = 2^(
 constexpr float kRefresh16 = 2.f;   // a refreshed m' puts the tile's maximum at 2^2
 constexpr float kLow16 = 0x1p-6f;   // a row whose first keys weigh less is refreshed
 // Places of a unit beside its tiles: about what its start and end take.
-constexpr int kUnitCost = 3;
+constexpr int kUnitCost = 2;
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -559,6 +559,14 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         // the pass below, the code ran out of the instruction caches).
         if (kBent || !inside) {
           const uint64_t f2 = pack2(f, f);
+          uint64_t bend[5];  // cap log2(e) tanh(u) / u by powers of u^2
+          if (kBent) {
+#pragma unroll
+            for (int d = 0; d < 5; ++d) {
+              bend[d] = pack2(cap * kTanh[d], cap * kTanh[d]);
+              asm volatile("" : "+l"(bend[d]));  // in registers: not made anew at each use
+            }
+          }
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t x[16];
@@ -580,9 +588,9 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
                 for (int k = 0; k < 8; ++k) {
                   const uint64_t u = pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
                   const uint64_t u2 = mul2(u, u);
-                  uint64_t y = pack2(cap * kTanh[4], cap * kTanh[4]);
+                  uint64_t y = bend[4];
 #pragma unroll
-                  for (int d = 3; d >= 0; --d) y = fma2(y, u2, pack2(cap * kTanh[d], cap * kTanh[d]));
+                  for (int d = 3; d >= 0; --d) y = fma2(y, u2, bend[d]);
                   const float2 z = unpack2(mul2(u, y));
                   x[2 * k] = __float_as_uint(z.x);
                   x[2 * k + 1] = __float_as_uint(z.y);
