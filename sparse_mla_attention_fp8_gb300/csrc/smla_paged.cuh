@@ -351,7 +351,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, int64_t*
   return g;
 }
 
-// Walks the range by one warp: emit(segment) for each segment in turn, until
+// Walks the range by one warp: emit(segment, its request) for each segment in turn, until
 // it returns false.  Returns the record for the merge.
 template <typename F>
 __device__ __forceinline__ PagedMerge walk_segments(const PagedParams& p, const PagedRange& w, F emit) {
@@ -410,7 +410,7 @@ __device__ __forceinline__ PagedMerge walk_segments(const PagedParams& p, const 
           s.kt += gone;
           s.n -= gone;
         }
-        if (!emit(s)) return mine;
+        if (!emit(s, q)) return mine;
       }
       off = 0;
     }

@@ -64,6 +64,12 @@ __device__ __forceinline__ void split_p(float x0, float x1, uint32_t& hi, uint32
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(t) : "r"(r));
   lo = t;
 }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // What a row needs of its own.
 template <int C>
 struct Columns {
@@ -75,38 +81,35 @@ struct Columns {
 template <int D, int C>
 struct Lay {
   static constexpr int N = 2 * C;          // MMA columns: two terms of each row
-  static constexpr int kCols = C == 8 ? 8 : 16;  // rows of a softmax group
-  static constexpr int kGroups = C / kCols;      // softmax groups
-  static constexpr int kWarps = 4 + 4 * kGroups + 4;
+  static constexpr int kWarps = 12;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kPerSm = C <= 16 ? 2 : 1;
+  static constexpr int kPerSm = 2;
   static constexpr int kKTile = kKeyTile * D;
   static constexpr int kStage = 2 * kKTile;
-  static constexpr int kStages = (C <= 16 ? 3 : 5) * (128 / D);
-  static constexpr int kMeta = kStages <= 6 ? 8 : 16;  // ring of block scales and flags
+  static constexpr int kStages = 3 * (128 / D);
+  static constexpr int kMeta = 8;          // ring of block scales and flags
   static constexpr int kQBuf = N * D;
-  static constexpr int kSegs = 2;
+  static constexpr int kSegs = 4, kQs = 2;  // segments ahead; their Q and columns
   static constexpr int kPBuf = kKeyTile * N;
   static constexpr int kPBufs = C == 16 ? 1 : 2;   // two where two CTAs still fit an SM
   static constexpr int kRefs = 4;                  // ring of (factors, v scales) towards the summing warps
   static constexpr int kOffQ = kStages * kStage;
-  static constexpr int kOffP = kOffQ + kSegs * kQBuf;
+  static constexpr int kOffP = kOffQ + kQs * kQBuf;
   static constexpr int kOffCols = kOffP + kPBufs * kPBuf;
-  static constexpr int kOffMeta = kOffCols + kSegs * (int)sizeof(Columns<C>);
+  static constexpr int kOffMeta = kOffCols + kQs * (int)sizeof(Columns<C>);
   static constexpr int kOffRefs = kOffMeta + kMeta * 32;
-  static constexpr int kRef = C * 4 + 32;          // factor[C], R, change flags of the groups
-  static constexpr int kOffRed = kOffRefs + kRefs * kRef;          // float [groups][4][kCols] maxima
-  static constexpr int kOffSum = kOffRed + 4 * C * 4;              // float [groups][4][kCols] sums
+  static constexpr int kRef = C * 4 + 16;          // factor[C], R, whether a factor is not 1
+  static constexpr int kOffRed = kOffRefs + kRefs * kRef;          // float [4][C] maxima
+  static constexpr int kOffSum = kOffRed + 4 * C * 4;              // float [4][C] sums
   static constexpr int kOffM = kOffSum + 4 * C * 4;                // float [C] m'
-  static constexpr int kOffFin = kOffM + C * 4;                    // float [2][m' | l][C]
-  static constexpr int kOffSeg = kOffFin + 2 * 2 * C * 4;
+  static constexpr int kOffFin = kOffM + C * 4;                    // float [segments][m' | l][C]
+  static constexpr int kOffSeg = kOffFin + kSegs * 2 * C * 4;
   static constexpr int kOffBar = (kOffSeg + kSegs * (int)sizeof(Segment) + 7) / 8 * 8;
   enum {
     kKFull = 0, kVFull = kKFull + kStages, kEmpty = kVFull + kStages, kSFull = kEmpty + kStages, kSFree = kSFull + 2,
     kPFull = kSFree + 2, kPFree = kPFull + kPBufs, kOFull = kPFree + kPBufs, kOFree = kOFull + 2,
-    kRefFull = kOFree + 2, kSegFull = kRefFull + kRefs, kQFull = kSegFull + kSegs, kSegFree = kQFull + kSegs,
-    kFinFull = kSegFree + kSegs,
-    kDrainQk = kFinFull + 2, kDrainPv, kNumBars
+    kRefFull = kOFree + 2, kSegFull = kRefFull + kRefs, kSegFree = kSegFull + kSegs, kQFull = kSegFree + kSegs,
+    kQFree = kQFull + kQs, kFinFull = kQFree + kQs, kDrainQk = kFinFull + kSegs, kDrainPv, kNumBars
   };
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmem = kOffMisc + 16 + 1024;
@@ -142,20 +145,21 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[L::kSFull + i], 1);
-      mbar_init(&bars[L::kSFree + i], 4 * L::kGroups);
+      mbar_init(&bars[L::kSFree + i], 4);
       mbar_init(&bars[L::kOFull + i], 1);
       mbar_init(&bars[L::kOFree + i], 4);
-      mbar_init(&bars[L::kFinFull + i], L::kGroups);
+      mbar_init(&bars[L::kQFull + i], 1);
+      mbar_init(&bars[L::kQFree + i], 1 + 4);
     }
     for (int i = 0; i < L::kPBufs; ++i) {
-      mbar_init(&bars[L::kPFull + i], 4 * L::kGroups);
+      mbar_init(&bars[L::kPFull + i], 4);
       mbar_init(&bars[L::kPFree + i], 1);
     }
-    for (int i = 0; i < L::kRefs; ++i) mbar_init(&bars[L::kRefFull + i], L::kGroups);
+    for (int i = 0; i < L::kRefs; ++i) mbar_init(&bars[L::kRefFull + i], 1);
     for (int i = 0; i < L::kSegs; ++i) {
       mbar_init(&bars[L::kSegFull + i], 1);
-      mbar_init(&bars[L::kQFull + i], 1);
-      mbar_init(&bars[L::kSegFree + i], 3 + 4 * L::kGroups + 4);
+      mbar_init(&bars[L::kSegFree + i], 3 + 4 + 4);
+      mbar_init(&bars[L::kFinFull + i], 1);
     }
     mbar_init(&bars[L::kDrainQk], 1);
     mbar_init(&bars[L::kDrainPv], 1);
@@ -262,11 +266,12 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       int tl = 0, seg = 0;
       bool dead = false;
       while (!dead) {
-        const int sb = seg % L::kSegs;
-        if (!PA_WAIT(L::kQFull + sb, (seg / L::kSegs) & 1)) break;
+        const int sb = seg % L::kSegs, qb = seg % L::kQs;
+        if (!PA_WAIT(L::kQFull + qb, (seg / L::kQs) & 1)) break;
         const int n = reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment))->n;
         if (n == 0) break;
-        const uint64_t dq = dq0 + (uint64_t)((sb * L::kQBuf) >> 4);
+        mbar_arrive(&bars[L::kSegFree + sb]);
+        const uint64_t dq = dq0 + (uint64_t)((qb * L::kQBuf) >> 4);
         for (int i = 0; i < n; ++i, ++tl) {
           const int st = ring.i, buf = tl & 1;
           if (!PA_WAIT(L::kSFree + buf, ((tl >> 1) + 1) & 1) || !PA_WAIT(L::kKFull + st, ring.phase)) {
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
             mma_f8(tmem + L::kTmemS + buf * N, dk + ((32 * k) >> 4), dq + ((32 * k) >> 4), id, k > 0 ? 1u : 0u);
           mma_commit(&bars[L::kSFull + buf]);
         }
-        if (!dead) mma_commit(&bars[L::kSegFree + sb]);  // the segment's Q has been read
+        if (!dead) mma_commit(&bars[L::kQFree + qb]);  // the segment's Q has been read
         ++seg;
       }
       // every issued operation completes before tensor memory is released
@@ -334,81 +339,94 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     // For each segment: the record, the rows' columns and the two terms of Q.
     int seg = 0;
     bool dead = false;
-    const PagedMerge mine = walk_segments(p, range, [&](const Segment& s) {
-        const int sb = seg % L::kSegs;
-        if (seg >= L::kSegs) dead = __any_sync(kAll, !PA_WAIT(L::kSegFree + sb, (seg / L::kSegs + 1) & 1));
-        if (dead) return false;
-        if (lane == 0) {
-          *reinterpret_cast<Segment*>(smem + L::kOffSeg + sb * sizeof(Segment)) = s;
-          mbar_arrive(&bars[L::kSegFull + sb]);  // the copies may begin
-        }
-        Columns<C>* cols = reinterpret_cast<Columns<C>*>(smem + L::kOffCols + sb * sizeof(Columns<C>));
-        const int rows = s.ntok * s.heads;
-        PagedRequest q;
-        q.load(a, s.r);
-        if (lane < C) {
-          const int t = s.t0 + min(lane / s.heads, s.ntok - 1), h = s.h0 + lane % s.heads;
-          cols->pos[lane] = q.pos(t);
-          cols->lo[lane] = lane < rows ? q.lo(a, t) : 0;
-          cols->hi[lane] = lane < rows ? q.hi(t) : 0;
-          cols->slope[lane] = a.alibi_slopes && lane < rows ? __ldg(a.alibi_slopes + h) * kLog2e : 0.f;
-        }
-        // D / 8 lanes per row, 8 values each
-        constexpr int kLanes = D / 8, kRowsPer = 32 / kLanes;
-        const uint32_t qd = smem_u32(smem + L::kOffQ + sb * L::kQBuf);
-        const int sub = lane / kLanes, c = lane % kLanes;
-#pragma unroll 4
-        for (int i = 0; i < C / kRowsPer; ++i) {
-          const int row = i * kRowsPer + sub;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    const PagedMerge mine = walk_segments(p, range, [&](const Segment& s, const PagedRequest& q) {
+      // what the rows need is under way before the waits: D / 8 lanes per row, 8 values of q each
+      constexpr int kLanes = D / 8, kRowsPer = 32 / kLanes;
+      const int rows = s.ntok * s.heads, sub = lane / kLanes, c = lane % kLanes;
+      const int tok = lane < rows ? lane / s.heads : 0, head = lane < rows ? lane - tok * s.heads : 0;  // of row `lane`
+      constexpr int kSteps = C / kRowsPer, kAhead = kSteps < 4 ? kSteps : 4;
+      uint4 v[kAhead];
+      auto fetch = [&](int step) {  // steps step .. step + kAhead - 1
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int row = (step + i) * kRowsPer + sub;
+          const int tr = __shfl_sync(kAll, tok, row), hr = __shfl_sync(kAll, head, row);
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
           if (row < rows)
-            v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                     (int64_t)(s.t0 + row / s.heads) * a.q_stride +
-                                                     (int64_t)(s.h0 + row % s.heads) * D) + c);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t amax = 0u;  // of the magnitudes' bits
+            v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                        (int64_t)(s.t0 + tr) * a.q_stride + (int64_t)(s.h0 + hr) * D) + c);
+        }
+      };
+      fetch(0);
+      const int t = s.t0 + tok, lo = lane < rows ? q.lo(a, t) : 0, hi = lane < rows ? q.hi(t) : 0;
+      const float slope = a.alibi_slopes && lane < rows ? __ldg(a.alibi_slopes + s.h0 + head) * kLog2e : 0.f;
+      const int sb = seg % L::kSegs, qb = seg % L::kQs;
+      if (seg >= L::kSegs) dead = __any_sync(kAll, !PA_WAIT(L::kSegFree + sb, (seg / L::kSegs + 1) & 1));
+      if (dead) return false;
+      if (lane == 0) {
+        *reinterpret_cast<Segment*>(smem + L::kOffSeg + sb * sizeof(Segment)) = s;
+        mbar_arrive(&bars[L::kSegFull + sb]);  // the copies may begin
+      }
+      if (seg >= L::kQs) dead = __any_sync(kAll, !PA_WAIT(L::kQFree + qb, (seg / L::kQs + 1) & 1));
+      if (dead) return false;
+      Columns<C>* cols = reinterpret_cast<Columns<C>*>(smem + L::kOffCols + qb * sizeof(Columns<C>));
+      if (lane < C) {
+        cols->pos[lane] = q.pos(t);
+        cols->lo[lane] = lo;
+        cols->hi[lane] = hi;
+        cols->slope[lane] = slope;
+      }
+      const uint32_t qd = smem_u32(smem + L::kOffQ + qb * L::kQBuf);
+#pragma unroll 1
+      for (int step = 0; step < kSteps; step += kAhead) {
+        if (step > 0) fetch(step);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) amax = max(amax, max((w[k] << 16) & 0x7fffffffu, w[k] & 0x7fff0000u));
+        for (int i = 0; i < kAhead; ++i) {
+          const int row = (step + i) * kRowsPer + sub;
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t top = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                   max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
 #pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) amax = max(amax, __shfl_xor_sync(kAll, amax, o));
-          uint32_t hi[2], lo[2];
+          for (int o = 1; o < kLanes; o <<= 1) top = max_u16x2(top, __shfl_xor_sync(kAll, top, o));
+          const uint32_t amax = max(top << 16, top & 0xffff0000u);  // the largest magnitude's bits
+          uint32_t h[2], l[2];
           float back;
-          split_q8(w, amax, hi, lo, back);
+          split_q8(w, amax, h, l, back);
           const int op = (row & ~7) + row;  // operand row: 16 b + row % 8, and the second term 8 behind
-          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op, c >> 1) + 8 * (c & 1)), "r"(hi[0]),
-                       "r"(hi[1])
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op, c >> 1) + 8 * (c & 1)), "r"(h[0]), "r"(h[1])
                        : "memory");
-          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op + 8, c >> 1) + 8 * (c & 1)), "r"(lo[0]),
-                       "r"(lo[1])
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op + 8, c >> 1) + 8 * (c & 1)), "r"(l[0]),
+                       "r"(l[1])
                        : "memory");
           if (c == 0) cols->scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f : kLog2e);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::kQFull + sb]);
-        ++seg;
-        return true;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[L::kQFull + qb]);
+      ++seg;
+      return true;
     });
     if (lane == 0) p.merge[blockIdx.x] = mine;
-    const int sb = seg % L::kSegs;
+    const int sb = seg % L::kSegs, qb = seg % L::kQs;
     if (!dead && seg >= L::kSegs) dead = __any_sync(kAll, !PA_WAIT(L::kSegFree + sb, (seg / L::kSegs + 1) & 1));
+    if (!dead && seg >= L::kQs) dead = __any_sync(kAll, !PA_WAIT(L::kQFree + qb, (seg / L::kQs + 1) & 1));
     if (lane == 0 && !dead) {
       reinterpret_cast<Segment*>(smem + L::kOffSeg + sb * sizeof(Segment))->n = 0;
       mbar_arrive(&bars[L::kSegFull + sb]);
-      mbar_arrive(&bars[L::kQFull + sb]);
+      mbar_arrive(&bars[L::kQFull + qb]);
     }
-  } else if (warp < 4 + 4 * L::kGroups) {
-    // ---------------------------------------------------------------- softmax: thread = key, kCols rows per group
-    constexpr int kCols = L::kCols, kSub = kCols / 8;
-    const int group = (warp - 4) >> 2, quarter = warp & 3, c0 = kCols * group;
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- softmax: thread = key, C rows
+    const int quarter = warp & 3;
     const int key = 32 * quarter + lane;
-    const uint32_t s_addr = tmem + ((uint32_t)(32 * quarter) << 16) + L::kTmemS + 2 * c0;
-    const uint32_t p_addr = smem_u32(smem + L::kOffP) + (key >> 3) * 8 * N + (key & 7) * 16 + group * kSub * 128;
-    float* red = reinterpret_cast<float*>(smem + L::kOffRed) + 4 * c0;
-    float* sums = reinterpret_cast<float*>(smem + L::kOffSum) + 4 * c0;
-    float* m_ref = reinterpret_cast<float*>(smem + L::kOffM) + c0;
-    const int bar = 1 + group;
-    constexpr uint32_t kAllSeen = (1u << kCols) - 1u;
+    const uint32_t s_addr = tmem + ((uint32_t)(32 * quarter) << 16) + L::kTmemS;
+    const uint32_t p_addr = smem_u32(smem + L::kOffP) + (key >> 3) * 8 * N + (key & 7) * 16;
+    float* red = reinterpret_cast<float*>(smem + L::kOffRed);
+    float* sums = reinterpret_cast<float*>(smem + L::kOffSum);
+    float* m_ref = reinterpret_cast<float*>(smem + L::kOffM);
+    constexpr int bar = 1;
+    constexpr uint32_t kAllSeen = (1u << C) - 1u;
     Ring<L::kStages> ring;
     int tl = 0, seg = 0;
     bool dead = false;
@@ -419,19 +437,19 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       dead = !__all_sync(kAll, ok);
     };
     while (true) {
-      const int sb = seg % L::kSegs;
-      wait(L::kQFull + sb, (seg / L::kSegs) & 1);
-      if (quarter == 0 && lane < kCols) m_ref[lane] = 0.f;
+      const int sb = seg % L::kSegs, qb = seg % L::kQs;
+      wait(L::kQFull + qb, (seg / L::kQs) & 1);
+      if (quarter == 0 && lane < C) m_ref[lane] = 0.f;
       dead = bar_any(bar, 128, dead);
       if (dead) break;
       const Segment* sp = reinterpret_cast<const Segment*>(smem + L::kOffSeg + sb * sizeof(Segment));
-      const Columns<C>* cols = reinterpret_cast<const Columns<C>*>(smem + L::kOffCols + sb * sizeof(Columns<C>));
+      const Columns<C>* cols = reinterpret_cast<const Columns<C>*>(smem + L::kOffCols + qb * sizeof(Columns<C>));
       const int kt = sp->kt, n = sp->n;
       if (n == 0) break;
       uint32_t seen = 0u;  // rows that have met a key they see (the same in every thread of the group)
-      uint64_t l2[kCols / 2];
+      uint64_t l2[C / 2];
 #pragma unroll
-      for (int c = 0; c < kCols / 2; ++c) l2[c] = 0ull;
+      for (int c = 0; c < C / 2; ++c) l2[c] = 0ull;
       for (int i = 0; i < n; ++i, ++tl, ring.next()) {
         const int buf = tl & 1, st = ring.i, pb = tl % L::kPBufs;
         {
@@ -445,16 +463,16 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         const float vf = ref_v > 0.f ? __fdividef(meta[2 + (key >> 6)], ref_v) : 0.f;
         const int pages = reinterpret_cast<const int*>(meta)[4];
         const int j0 = (kt + n - 1 - i) * kKeyTile, j = j0 + key;
-        float y[kCols];  // logits, then logits - m'
+        float y[C];  // logits, then logits - m'
         {
           const uint64_t ks2 = pack2(ks, ks);
 #pragma unroll
-          for (int b = 0; b < kSub; ++b) {
+          for (int b = 0; b < C / 8; ++b) {
             uint32_t raw[16];
             tmem_ld16_sync(s_addr + buf * N + 16 * b, raw);
 #pragma unroll
             for (int c = 0; c < 8; c += 2) {
-              const float2 f = *reinterpret_cast<const float2*>(&cols->scale[c0 + 8 * b + c]);
+              const float2 f = *reinterpret_cast<const float2*>(&cols->scale[8 * b + c]);
               const float2 v = unpack2(mul2(add2(pack2(__uint_as_float(raw[c]), __uint_as_float(raw[c + 1])),
                                                  pack2(__uint_as_float(raw[8 + c]), __uint_as_float(raw[9 + c]))),
                                             mul2(pack2(f.x, f.y), ks2)));
@@ -470,13 +488,13 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
           // cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))), to within a few 2^-23 cap
           const float to = 2.f * kLog2e / a.softcap, cap = a.softcap * kLog2e;
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) y[c] = fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(y[c] * to)), cap);
+          for (int c = 0; c < C; ++c) y[c] = fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(y[c] * to)), cap);
         }
         if (a.alibi_slopes) {
 #pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&cols->slope[c0 + c]);
-            const int4 at = *reinterpret_cast<const int4*>(&cols->pos[c0 + c]);
+          for (int c = 0; c < C; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&cols->slope[c]);
+            const int4 at = *reinterpret_cast<const int4*>(&cols->pos[c]);
             y[c] = fmaf(-f.x, (float)abs(at.x - j), y[c]);
             y[c + 1] = fmaf(-f.y, (float)abs(at.y - j), y[c + 1]);
             y[c + 2] = fmaf(-f.z, (float)abs(at.z - j), y[c + 2]);
@@ -488,15 +506,15 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         if (!inside) {
           const bool page_ok = (pages >> (key >> 6)) & 1;
 #pragma unroll
-          for (int c = 0; c < kCols; ++c)  // (no branches)
-            y[c] = page_ok & (j >= cols->lo[c0 + c]) & (j < cols->hi[c0 + c]) ? y[c] : -INFINITY;
+          for (int c = 0; c < C; ++c)  // (no branches)
+            y[c] = page_ok & (j >= cols->lo[c]) & (j < cols->hi[c]) ? y[c] : -INFINITY;
           // keys that no row sees may hold any codes: their V rows become zeros
-          zero_v = group == 0 && (j < sp->lo || j >= sp->hi);
+          zero_v = j < sp->lo || j >= sp->hi;
           if (__any_sync(kAll, zero_v)) wait(L::kVFull + st, ring.phase);
         }
         float over = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < kCols; c += 4) {
+        for (int c = 0; c < C; c += 4) {
           const float4 m = *reinterpret_cast<const float4*>(&m_ref[c]);
           y[c] -= m.x;
           y[c + 1] -= m.y;
@@ -509,27 +527,27 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         uint8_t* ref = smem + L::kOffRefs + (tl % L::kRefs) * L::kRef;
         wait(L::kPFree + pb, (tl / L::kPBufs + 1) & 1);  // P.V has read this P buffer
         if (refresh) {
-          // lane c (mod kCols): row c's maximum, the change of its reference, and the factor of its sums
+          // lane c (mod C): row c's maximum, the change of its reference, and the factor of its sums
           float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
+          for (int c = 0; c < C; ++c) {
             const float v = warp_max(y[c]);
-            if ((lane & (kCols - 1)) == c) mx = v;
+            if ((lane & (C - 1)) == c) mx = v;
           }
-          if (lane < kCols) red[quarter * kCols + lane] = mx;
+          if (lane < C) red[quarter * C + lane] = mx;
           named_bar_sync(bar, 128);
-          const int c1 = lane & (kCols - 1);
-          mx = fmaxf(fmaxf(red[c1], red[kCols + c1]), fmaxf(red[2 * kCols + c1], red[3 * kCols + c1]));
+          const int c1 = lane & (C - 1);
+          mx = fmaxf(fmaxf(red[c1], red[C + c1]), fmaxf(red[2 * C + c1], red[3 * C + c1]));
           const bool first = !((seen >> c1) & 1u);
           const bool set = first ? mx > -INFINITY : mx > kTop;
           const float up = set ? mx - kRefresh : 0.f, factor = set && !first ? ex2_approx(-up) : 1.f;
           seen |= __ballot_sync(kAll, set) & kAllSeen;
-          if (quarter == 0 && lane < kCols) {
+          if (quarter == 0 && lane < C) {
             m_ref[lane] += up;
-            reinterpret_cast<float*>(ref)[c0 + lane] = factor;
+            reinterpret_cast<float*>(ref)[lane] = factor;
           }
 #pragma unroll
-          for (int c = 0; c < kCols; c += 2) {
+          for (int c = 0; c < C; c += 2) {
             y[c] -= __shfl_sync(kAll, up, c);
             y[c + 1] -= __shfl_sync(kAll, up, c + 1);
             l2[c / 2] = mul2(l2[c / 2], pack2(__shfl_sync(kAll, factor, c), __shfl_sync(kAll, factor, c + 1)));
@@ -537,12 +555,12 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
           named_bar_sync(bar, 128);  // m_ref and red are in order for the next tile
         }
         if (quarter == 0 && lane == 0) {
-          reinterpret_cast<int*>(ref)[C + 2 + group] = refresh;
-          if (group == 0) *reinterpret_cast<float*>(ref + 4 * C) = ref_v;
+          reinterpret_cast<float*>(ref)[C] = ref_v;
+          reinterpret_cast<int*>(ref)[C + 1] = refresh;
         }
         const uint64_t vf2 = pack2(vf, vf);
 #pragma unroll
-        for (int b = 0; b < kSub; ++b) {
+        for (int b = 0; b < C / 8; ++b) {
           uint32_t hw[4], lw[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -569,25 +587,28 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       }
       // the rows' sums over the segment's keys
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
+      for (int c = 0; c < C; ++c) {
         const float2 pair = unpack2(l2[c / 2]);
         float v = c & 1 ? pair.y : pair.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-        if (lane == c) sums[quarter * kCols + c] = v;
+        if (lane == c) sums[quarter * C + c] = v;
       }
       named_bar_sync(bar, 128);
       if (quarter == 0) {
-        float* fin = reinterpret_cast<float*>(smem + L::kOffFin + (seg & 1) * 2 * C * 4) + c0;
-        if (lane < kCols) {
-          const float l = (sums[lane] + sums[kCols + lane]) + (sums[2 * kCols + lane] + sums[3 * kCols + lane]);
+        float* fin = reinterpret_cast<float*>(smem + L::kOffFin + sb * 2 * C * 4);
+        if (lane < C) {
+          const float l = (sums[lane] + sums[C + lane]) + (sums[2 * C + lane] + sums[3 * C + lane]);
           fin[lane] = l == 0.f ? kNoMax : m_ref[lane];
           fin[C + lane] = l;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[L::kFinFull + (seg & 1)]);
+        if (lane == 0) mbar_arrive(&bars[L::kFinFull + sb]);
       }
-      if (lane == 0) mbar_arrive(&bars[L::kSegFree + sb]);
+      if (lane == 0) {
+        mbar_arrive(&bars[L::kQFree + qb]);
+        mbar_arrive(&bars[L::kSegFree + sb]);
+      }
       ++seg;
     }
   } else {
@@ -614,13 +635,11 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         const int buf = tl & 1;
         wait(L::kRefFull + tl % L::kRefs, (tl / L::kRefs) & 1);
         const uint8_t* ref = smem + L::kOffRefs + (tl % L::kRefs) * L::kRef;
-        const float ref_v = *reinterpret_cast<const float*>(ref + 4 * C);
+        const float ref_v = reinterpret_cast<const float*>(ref)[C];
+        if (reinterpret_cast<const int*>(ref)[C + 1]) {
 #pragma unroll
-        for (int g = 0; g < L::kGroups; ++g)
-          if (reinterpret_cast<const int*>(ref)[C + 2 + g]) {
-#pragma unroll
-            for (int c = L::kCols * g; c < L::kCols * (g + 1); ++c) acc[c] *= reinterpret_cast<const float*>(ref)[c];
-          }
+          for (int c = 0; c < C; ++c) acc[c] *= reinterpret_cast<const float*>(ref)[c];
+        }
         wait(L::kOFull + buf, (tl >> 1) & 1);
         if (dead) break;
         tc_fence_after();
@@ -637,19 +656,24 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kOFree + buf]);
       }
-      wait(L::kFinFull + (seg & 1), (seg >> 1) & 1);
+      wait(L::kFinFull + sb, (seg / L::kSegs) & 1);
       if (dead) break;
-      const float* fin = reinterpret_cast<const float*>(smem + L::kOffFin + (seg & 1) * 2 * C * 4);
+      const float* fin = reinterpret_cast<const float*>(smem + L::kOffFin + sb * 2 * C * 4);
       const int heads = sp->heads, rows = sp->ntok * heads;
       if (sp->slot < 0) {
-        const int t0 = sp->t0, h0 = sp->h0;
+        // lane c: row c's place and 1 / l
+        const int64_t first = (int64_t)sp->t0 * a.H + sp->h0;
+        const float l = lane < C ? fin[C + lane] : 0.f, inv = l == 0.f ? 0.f : 1.f / l;
+        const int at = lane / heads * a.H + lane % heads;
+        if (quarter == 0 && lane < rows) a.lse[first + at] = l == 0.f ? -INFINITY : (fin[lane] + log2f(l)) * kLn2;
+        if (32 * quarter < D) {
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + first * D + d;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (c >= rows) break;
-          const float l = fin[C + c], inv = l == 0.f ? 0.f : 1.f / l;
-          const int64_t row = (int64_t)(t0 + c / heads) * a.H + h0 + c % heads;
-          if (D == 128 || d < D) static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16(acc[c] * inv);
-          if (d == 0) a.lse[row] = l == 0.f ? -INFINITY : (fin[c] + log2f(l)) * kLn2;
+          for (int c = 0; c < C; ++c) {
+            const int64_t to = __shfl_sync(kAll, at, c);
+            const float f = __shfl_sync(kAll, inv, c);
+            if (c < rows) out[to * D] = __float2bfloat16(acc[c] * f);
+          }
         }
       } else {
         const int64_t part = 2 * (int64_t)blockIdx.x + sp->slot;
@@ -693,22 +717,21 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t stream) {
 // (fewer rows: less softmax work per key; more: each key read once for all of them).
 int rows_for(int G, int max_query_len) {
   const int64_t rows = (int64_t)G * std::max(1, max_query_len);
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 256;
+  return rows <= 8 ? 8 : rows <= 32 ? 16 : 256;
 }
 
 }  // namespace
 
 size_t paged_attention_workspace(int T, int H, int HK, int D, int R, int max_query_len, int num_sms) {
   const int C = rows_for(H / HK, max_query_len);
-  return C == 256 ? paged_prefill_workspace(T, H, D, R, num_sms) : paged_sizes(C, D, C <= 16 ? 2 : 1, num_sms).bytes;
+  return C == 256 ? paged_prefill_workspace(T, H, D, R, num_sms) : paged_sizes(C, D, 2, num_sms).bytes;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int max_query_len, int num_sms, cudaStream_t stream) {
   const int C = rows_for(a.H / a.HK, max_query_len);
   if (C == 256) return launch_paged_prefill(a, num_sms, stream);
   if (C == 8) return a.D == 128 ? launch<128, 8>(a, num_sms, stream) : launch<64, 8>(a, num_sms, stream);
-  if (C == 16) return a.D == 128 ? launch<128, 16>(a, num_sms, stream) : launch<64, 16>(a, num_sms, stream);
-  return a.D == 128 ? launch<128, 32>(a, num_sms, stream) : launch<64, 32>(a, num_sms, stream);
+  return a.D == 128 ? launch<128, 16>(a, num_sms, stream) : launch<64, 16>(a, num_sms, stream);
 }
 
 }  // namespace smla

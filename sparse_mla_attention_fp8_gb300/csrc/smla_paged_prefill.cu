@@ -134,11 +134,19 @@ __global__ void __launch_bounds__(kSplitThreads)
   if (lane == 0) tile_doc[u] = doc;
 }
 
+// A 3-D tiled TMA load of one box, as tma_load_2d.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // tanh(u) / u as a polynomial of u^2 <= 0.5: the one of degree 4 through the Chebyshev
 // points of [0, 0.5], to within 4 x 2^-23 of the value.  Caps are wide as a rule, so
-// that most keys need no exponential and no reciprocal for theirs: those two and the
-// weight's exponential are 3 of the 16 a clock that an SM has, 6144 clocks of a tile
-// (256 rows, 128 keys) whose products take 2048.
+// that most keys need no exponential and no reciprocal for theirs (five prompts of up
+// to 1300 tokens, G = 12, D = 64, cap 50, packed documents: 94 us, without it 100).
 constexpr float kTanhTop = 0.5f;  // of u^2
 __device__ constexpr float kTanh[5] = {0.99999964f, -0.33329946f, 0.13277967f, -0.05072029f, 0.01364212f};
 
@@ -388,7 +396,7 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
     // For each segment: the record, and the largest V scale of its blocks.
     int seg = 0;
     bool dead = false;
-    const PagedMerge mine = walk_segments(p, range, [&](const Segment& s) {
+    const PagedMerge mine = walk_segments(p, range, [&](const Segment& s, const PagedRequest&) {
       uint32_t most = 0u;
       const int32_t* row = a.block_table + (int64_t)s.r * a.MB;
       const int page0 = max(2 * s.kt, s.lo / kBlock), page1 = min(2 * (s.kt + s.n), (s.hi + kBlock - 1) / kBlock);
