@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       constexpr int kLanes = D / 8, kRowsPer = 32 / kLanes;
       const int rows = s.ntok * s.heads, sub = lane / kLanes, c = lane % kLanes;
       const int tok = lane < rows ? lane / s.heads : 0, head = lane < rows ? lane - tok * s.heads : 0;  // of row `lane`
-      constexpr int kSteps = C / kRowsPer, kAhead = kSteps < 4 ? kSteps : 4;
+      constexpr int kSteps = C / kRowsPer, kAhead = kSteps < 2 ? kSteps : 2;
       uint4 v[kAhead];
       auto fetch = [&](int step) {  // steps step .. step + kAhead - 1
 #pragma unroll
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
       uint64_t l2[C / 2];
 #pragma unroll
       for (int c = 0; c < C / 2; ++c) l2[c] = 0ull;
-      for (int i = 0; i < n; ++i, ++tl, ring.next()) {
+      for (int i = n - 1; i >= 0; --i, ++tl, ring.next()) {
         const int buf = tl & 1, st = ring.i, pb = tl % L::kPBufs;
         {
           // the tile's scales and flags (behind its K copies), and its S
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         const float ks = meta[key >> 6], ref_v = fmaxf(fabsf(meta[2]), fabsf(meta[3]));
         const float vf = ref_v > 0.f ? __fdividef(meta[2 + (key >> 6)], ref_v) : 0.f;
         const int pages = reinterpret_cast<const int*>(meta)[4];
-        const int j0 = (kt + n - 1 - i) * kKeyTile, j = j0 + key;
+        const int j0 = (kt + i) * kKeyTile, j = j0 + key;
         float y[C];  // logits, then logits - m'
         {
           const uint64_t ks2 = pack2(ks, ks);
@@ -713,11 +713,14 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t stream) {
   return e == cudaSuccess ? launch_merge<D, C>(p, stream) : e;
 }
 
-// Rows per query tile: the fewest that hold the heads of a K/V head and the estimated tokens of a request
-// (fewer rows: less softmax work per key; more: each key read once for all of them).
+// Rows per query tile, by those of a request and K/V head (its heads times the estimated tokens).  Fewer
+// rows cost less softmax work per key, more let a key read once meet them all; tiles of 256 rows take the
+// same for few as for many.  128 requests of up to 8000 tokens, 4 K/V heads, D = 128 (300 of up to 2000, 8 K/V
+// heads), tiles of 8 | 16 | 256: 16 rows 133 (185) | 112 (206) | 231 (300) us; 32 rows 205 (310) | 149 (302) | 232
+// (306); 48 rows 272 (442) | 187 (417) | 234 (311); 64 rows 357 (543) | 241 (504) | 236 (321).
 int rows_for(int G, int max_query_len) {
   const int64_t rows = (int64_t)G * std::max(1, max_query_len);
-  return rows <= 8 ? 8 : rows <= 32 ? 16 : 256;
+  return rows <= 8 ? 8 : rows <= 48 ? 16 : 256;
 }
 
 }  // namespace
