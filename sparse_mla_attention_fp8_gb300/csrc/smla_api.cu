@@ -769,6 +769,7 @@ int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache,
   if (rc == SMLA_OK) rc = check_kv_heads(HK, D, NB);
   if (rc != SMLA_OK) return rc;
   if (H <= 0 || H % HK != 0) return fail(SMLA_ERR_INVALID_ARG, "H=%d must be a positive multiple of HK=%d", H, HK);
+  if (MB > (1 << 24)) return fail(SMLA_ERR_UNSUPPORTED, "MB=%d unsupported: at most 2^24", MB);
   if (H / HK > 128) return fail(SMLA_ERR_UNSUPPORTED, "H=%d unsupported: at most 128 heads per K/V head", H);
   if (window < 0 || max_query_len < 0 || !(softcap >= 0.f) || softcap > 3e38f)
     return fail(SMLA_ERR_INVALID_ARG, "window=%d, max_query_len=%d and softcap=%g must not be negative", window,

@@ -274,17 +274,19 @@ __device__ __forceinline__ void tile_range(const PagedParams& p, const PagedRequ
   }
 }
 
-// Places of request r in the sequence (over its query tiles and the K/V heads).
-__device__ __forceinline__ int64_t request_tiles(const PagedParams& p, int r) {
+// Places of a unit of request r whose first row is t.
+__device__ __forceinline__ int unit_places(const PagedParams& p, const PagedRequest& q, int r, int t) {
+  int lo, hi, first, count;
+  tile_range(p, q, r, t, min(t + p.tq, q.t1), lo, hi);
+  key_tiles(lo, hi, first, count);
+  return count + p.unit_cost;
+}
+// Places of request r in the sequence (over its query tiles begin, begin + step, ... and the K/V heads).
+__device__ __forceinline__ int64_t request_places(const PagedParams& p, int r, int begin, int step) {
   PagedRequest q;
   q.load(p.a, r);
   int64_t n = 0;
-  for (int t = q.t0; t < q.t1; t += p.tq) {
-    int lo, hi, first, count;
-    tile_range(p, q, r, t, min(t + p.tq, q.t1), lo, hi);
-    key_tiles(lo, hi, first, count);
-    n += count + p.unit_cost;
-  }
+  for (int64_t t = q.t0 + (int64_t)begin * p.tq; t < q.t1; t += (int64_t)step * p.tq) n += unit_places(p, q, r, (int)t);
   return n * p.HV;
 }
 
@@ -328,7 +330,17 @@ struct PagedRange {
 template <int kThreads>
 __device__ __forceinline__ PagedRange paged_range(const PagedParams& p, int64_t* prefix, int walker) {
   const int R = p.a.R;
-  for (int r = threadIdx.x; r < R; r += kThreads) prefix[r] = request_tiles(p, r);
+  // as many lanes a request as there are threads for: a long prompt has many query tiles
+  int per = 1;
+  while (per < 32 && 2 * per * R <= kThreads) per *= 2;
+  if (per == 1) {
+    for (int r = threadIdx.x; r < R; r += kThreads) prefix[r] = request_places(p, r, 0, 1);
+  } else {
+    const int r = threadIdx.x / per, sub = threadIdx.x & (per - 1);
+    int64_t n = r < R ? request_places(p, r, sub, per) : 0;
+    for (int o = 1; o < per; o <<= 1) n += __shfl_xor_sync(kAll, n, o);
+    if (r < R && sub == 0) prefix[r] = n;
+  }
   __syncthreads();
   scan_tiles<kThreads>(prefix, R);
   PagedRange g{};
@@ -362,17 +374,31 @@ __device__ __forceinline__ PagedMerge walk_segments(const PagedParams& p, const 
   for (int r = w.r0; x < w.x1 && r < a.R; ++r) {
     PagedRequest q;
     q.load(a, r);
-    for (int ta = q.t0; ta < q.t1 && x < w.x1; ta += p.tq) {
+    // the query tile in which the range begins, 32 tiles at a time
+    int ta = q.t0;
+    while (off > 0 && ta < q.t1 - p.tq) {
+      const int64_t t = ta + (int64_t)lane * p.tq;
+      const int n = t < q.t1 ? unit_places(p, q, r, (int)t) : 0;
+      int64_t inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t before = __shfl_up_sync(kAll, inc, o);
+        if (lane >= o) inc += before;
+      }
+      const uint32_t reach = __ballot_sync(kAll, off < inc * p.HV);
+      const int k = reach ? __ffs((int)reach) - 1 : 31;
+      const int64_t upto = __shfl_sync(kAll, reach ? inc - n : inc, k);
+      off -= upto * p.HV;
+      ta = (int)min(ta + (int64_t)(reach ? k : 32) * p.tq, (int64_t)q.t1);
+      if (reach) break;
+    }
+    for (; ta < q.t1 && x < w.x1; ta += p.tq) {
       const int tb = min(ta + p.tq, q.t1);
       Segment s;
       tile_range(p, q, r, ta, tb, s.lo, s.hi);
       int first, count;
       key_tiles(s.lo, s.hi, first, count);
       const int len = count + p.unit_cost;  // places of a unit
-      if (off >= (int64_t)len * p.HV) {
-        off -= (int64_t)len * p.HV;
-        continue;
-      }
       s.all_lo = q.window_lo(a, tb - 1);
       s.all_hi = q.hi(ta);
       if (a.doc_start) {
