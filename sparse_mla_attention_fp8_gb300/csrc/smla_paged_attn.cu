@@ -26,8 +26,9 @@
 //        significant bits and hi leaves at most 4;
 //      O^T[d, row] = V^T P^T, P = 2^(x - m') v_scale / R = hi + lo / 16, R the
 //        larger v_scale of the tile's two blocks: 8 significant bits where P >=
-//        2^-6, and nothing lost above 2^-14, 2^-18 of the largest weight or
-//        less: many small weights keep their sum.
+//        2^-6, below that multiples of 2^-13 (2^-17 of the largest weight or
+//        less), rounded with a dither that differs between a tile's 128 keys,
+//        so that many equal small weights keep their sum: within 2^-13 a tile.
 //  * Softmax: thread = key, 8 or 16 rows; the block's K scale folds into the
 //    logit.  m' is a running reference per row that is set by the row's first
 //    tile (to put its maximum at 2^4.25) and afterwards only when a weight
@@ -51,8 +52,9 @@ namespace smla {
 namespace {
 
 // Two weights -> e4m3 codes hi and lo of p ~ hi + lo / 16 (low byte from x0).
-// The split runs in f16x2: 11 bits, more than the two terms keep.
-__device__ __forceinline__ void split_p(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+// The split runs in f16x2: 11 bits, more than the two terms keep.  `dither`, f16x2,
+// is added to 16 lo: a thread's share of the steps in which lo counts small weights.
+__device__ __forceinline__ void split_p(float x0, float x1, uint32_t dither, uint32_t& hi, uint32_t& lo) {
   uint32_t a, d, r;
   uint16_t t;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(x1), "f"(x0));
@@ -60,7 +62,7 @@ __device__ __forceinline__ void split_p(float x0, float x1, uint32_t& hi, uint32
   hi = t;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(t));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(d));
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x4c004c00u));  // 16, 16
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(r), "r"(0x4c004c00u), "r"(dither));  // 16, 16
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(t) : "r"(r));
   lo = t;
 }
@@ -420,6 +422,9 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     // ---------------------------------------------------------------- softmax: thread = key, C rows
     const int quarter = warp & 3;
     const int key = 32 * quarter + lane;
+    // (2 k + 1 - 128) 2^-17, k the key's bits in reverse: evenly over half a step of lo to either side
+    const float dither_f = (float)(2 * (int)(__brev((uint32_t)key) >> 25) - 127) * 0x1p-17f;
+    const uint32_t dither = pack_f16x2(dither_f, dither_f);
     const uint32_t s_addr = tmem + ((uint32_t)(32 * quarter) << 16) + L::kTmemS;
     const uint32_t p_addr = smem_u32(smem + L::kOffP) + (key >> 3) * 8 * N + (key & 7) * 16;
     float* red = reinterpret_cast<float*>(smem + L::kOffRed);
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
             const uint64_t p2 = pack2(ex2_approx(y[at]), ex2_approx(y[at + 1]));
             l2[at / 2] = add2(l2[at / 2], p2);
             const float2 pv = unpack2(mul2(p2, vf2));
-            split_p(pv.x, pv.y, hw[c], lw[c]);
+            split_p(pv.x, pv.y, dither, hw[c], lw[c]);
           }
           st_shared_v4(p_addr + pb * L::kPBuf + 128 * b, hw[0] | (hw[1] << 16), hw[2] | (hw[3] << 16),
                        lw[0] | (lw[1] << 16), lw[2] | (lw[3] << 16));

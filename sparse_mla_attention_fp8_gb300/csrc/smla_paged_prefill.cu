@@ -19,7 +19,7 @@
 //    scale).  P = 2^(x - m') with the row's running reference m', computed in one
 //    pass over S into registers.  m' starts at 0 and stays there while the row's
 //    logits lie where f16 is exact enough; only if a thread's weights add up to
-//    65000, or a row's first keys to less than 2^-6, is it refreshed (to put the
+//    65000, or a row's first keys to less than 2^-3, is it refreshed (to put the
 //    tile's largest at 2^2), O scaled in tensor memory and the pass repeated.
 //  * P overwrites S in tensor memory and enters P V from there.
 //  * q is split by a kernel beforehand, so that a segment's Q is one copy that
@@ -35,7 +35,7 @@ namespace {
 constexpr int kRows = 128;          // rows of a half
 constexpr float kTop16 = 65000.f;   // largest sum of a thread's weights P = 2^(x - m') (f16: 65504)
 constexpr float kRefresh16 = 2.f;   // a refreshed m' puts the tile's maximum at 2^2
-constexpr float kLow16 = 0x1p-6f;   // a row whose first keys weigh less is refreshed
+constexpr float kLow16 = 0x1p-3f;   // a row whose first keys weigh less is refreshed
 // Places of a unit beside its tiles: about what its start and end take.
 constexpr int kUnitCost = 2;
 

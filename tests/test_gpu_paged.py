@@ -371,6 +371,125 @@ def test_attention_many_small_weights(smla):
     check(b, attend(smla, b))
 
 
+@pytest.mark.parametrize("top,rest", [(0, -13.6), (0, -15.4), (0, -17), (0, -18.3), (16, 0), (100, 84.5), (-5, -21.6),
+                                      (-12, -23.4), (-40, -52.3)])
+@pytest.mark.parametrize("HK,G,new", [(80, 1, 1), (40, 12, 1), (16, 16, 20)])
+def test_attention_equal_small_weights(smla, HK, G, new, top, rest):
+    """The newest block's keys weigh 2^top each, the 8000 before them 2^rest:
+    rounding may not shift these to one side.  With V = 1 there and 0 in the
+    newest block the result is their share of the sum.  Tolerance: weights
+    within 2^-7 of their value, equal small ones within 2^-24 of the largest
+    on average; in tiles of 256 rows within 2^-25, the sum being at least 2^-3
+    (a sum below it is scaled up); the logits, as float32 products of magnitude
+    |x|, within 2^-20 |x|; the bf16 result."""
+    torch = torch_mod()
+    R, D, n = 4, 64, 8000
+    MB = n // 64 + 1
+    NB = R * MB
+    k = torch.full((NB, HK, 64, D), 0x38, dtype=torch.uint8, device="cuda")  # 1.0
+    v = k.clone()
+    table = torch.randperm(NB, device="cuda").to(torch.int32).view(R, MB)
+    v[table[:, -1].long()] = 0
+    ks = torch.full((NB, HK), rest / D * np.log(2), device="cuda")
+    ks[table[:, -1].long()] = top / D * np.log(2)
+    vs = torch.ones((NB, HK), device="cuda")
+    lens = i32([n + 64] * R)
+    out, lse = smla.paged_attention_fp8(
+        torch.ones((R * new, HK * G, D), dtype=torch.bfloat16, device="cuda"), k, v, ks, vs, table, lens,
+        i32(np.arange(R + 1) * new), 1.0, max_query_len=new, prefix_lens=lens)
+    a, b = 64.0, n * 2.0 ** (rest - top)
+    want, want_lse = b / (a + b), top * np.log(2) + np.log(a + b)
+    dx = 2.0 ** -20 * max(abs(top), abs(rest))
+    tol = (2.0 ** -7 + 2.0 ** -8 + 2 * dx) * want + n * 2.0 ** -24 / (a + b) + (n * 2.0 ** -22 if G * new > 48 else 0)
+    assert (out.double() - want).abs().max().item() <= tol
+    assert (lse.double() - want_lse).abs().max().item() <= dx + 2.0 ** -20 * abs(want_lse)
+
+
+@pytest.mark.parametrize("HK,G,D,ctx,new,opt", [
+    (1, 32, 64, [20, 3], [500, 90], dict(window=100)),
+    (1, 128, 128, [0], [100], {}),
+    (2, 16, 64, [0, 77], [400, 1], dict(doc=True)),
+])
+@pytest.mark.parametrize("most", [None, 1])
+def test_attention_many_query_tiles(smla, HK, G, D, ctx, new, opt, most):
+    """More than 32 query tiles a request, by either kernel."""
+    if "doc" in opt:
+        opt = dict(doc=[p - p % 90 for c, n in zip(ctx, new) for p in range(c, c + n)])
+    b = ref.Batch(25, HK, G, D, ctx, new, **opt)
+    check(b, attend(smla, b, max_query_len=most))
+
+
+@pytest.mark.parametrize("G,new", [(2, [5, 9]), (16, [30, 5])])
+def test_attention_fewer_tokens_than_rows(smla, G, new):
+    """seq_lens below the number of new rows: the first of them have no position and see nothing."""
+    b = ref.Batch(26, 1, G, 64, [0, 0], new)
+    b.lens[:] = [3, 0]
+    got = attend(smla, b)
+    assert np.isneginf(got[1][:new[0] - 3]).all() and np.isneginf(got[1][new[0]:]).all()
+    check(b, got)
+
+
+@pytest.mark.parametrize("most", [1, 1000])
+def test_attention_many_requests(smla, most):
+    """8192 requests of a few tokens, some with a prefill chunk."""
+    rng = np.random.default_rng(27)
+    ctx, new = rng.integers(0, 140, 8192), np.where(rng.random(8192) < 0.01, rng.integers(0, 30, 8192), 1)
+    b = ref.Batch(28, 1, 2, 64, ctx.tolist(), new.tolist())
+    check(b, attend(smla, b, max_query_len=most))
+
+
+@pytest.mark.parametrize("new", [[1, 1], [70, 1]])
+def test_caches_beyond_32_bit_offsets(smla, new):
+    """Store and attention in the last blocks of caches of 4.6 GB each."""
+    torch = torch_mod()
+    HK, G, D, NB = 8, 4, 128, 70000
+    T = sum(new)
+    k, v, q = (torch.randn((T, n, D), device="cuda").to(torch.bfloat16) for n in (HK, HK, HK * G))
+    start = i32(np.cumsum([0] + new))
+    got = []
+    for first in (0, NB - 4):
+        table = i32(first + np.array([[3, 1], [0, 2]]))
+        cache = [torch.zeros((NB, HK, 64, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scale = [torch.zeros((NB, HK), device="cuda") for _ in range(2)]
+        smla.kv_cache_store_fp8(k, v, start, i32(new), table, *cache, *scale)
+        out, lse = smla.paged_attention_fp8(q, *cache, *scale, table, i32(new), start, 0.1, max_query_len=max(new))
+        got.append([out, lse] + [x[first:first + 4].clone() for x in cache + scale])
+        assert not cache[0][:NB - 4].any() or first == 0
+        del cache, scale
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert got[0][2].any()
+
+
+def test_graphs_in_turn(smla):
+    """A prompt's and a decode step's attention, captured apart and replayed
+    in turn and on two streams at once, on inputs that change in between."""
+    torch = torch_mod()
+    prep = []
+    for seed, ctx, new, most in ((60, [30, 0], [90, 120], 120), (61, [900, 40, 3], [1, 1, 1], 1)):
+        bs = [ref.Batch(seed + 10 * i, 2, 4, 128, ctx, new) for i in range(2)]
+        ins = [[bf16(b.q), *(dev(c) for c in b.caches), *(dev(s) for s in b.scales), i32(b.table)] for b in bs]
+        args = [x.clone() for x in ins[0]]
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        rest = (i32(bs[0].lens), i32(bs[0].query_start), bs[0].sm_scale)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            out = smla.paged_attention_fp8(*args, *rest, max_query_len=most)
+        prep.append((bs, ins, args, graph, stream, out, rest))
+    for i in (0, 1, 0):
+        for bs, ins, args, *_ in prep:
+            for a, x in zip(args, ins[i]):
+                a.copy_(x)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for p in prep:
+                with torch.cuda.stream(p[4]):
+                    p[3].replay()
+        torch.cuda.synchronize()
+        for bs, _, _, _, _, (out, lse), _ in prep:
+            check(bs[i], (out.float().cpu().numpy(), lse.cpu().numpy()))
+
+
 def test_attention_query_slices(smla):
     torch = torch_mod()
     b = ref.Batch(21, 2, 2, 64, [30, 200], [40, 1])

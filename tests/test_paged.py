@@ -119,7 +119,7 @@ def test_store_refuses(L, kw, rc):
 
 
 @pytest.mark.parametrize("kw,rc", [
-    (dict(T=-1), -1), (dict(H=0), -1), (dict(H=5), -1), (dict(H=258, qs=258 * 128), -2), (dict(D=192), -2),
+    (dict(T=-1), -1), (dict(H=0), -1), (dict(H=5), -1), (dict(H=258, qs=258 * 128), -2), (dict(D=192), -2), (dict(MB=(1 << 24) + 1), -2),
     (dict(win=-1), -1), (dict(mq=-1), -1), (dict(cap=-1.0), -1), (dict(cap=float("nan")), -1),
     (dict(cap=float("inf")), -1), (dict(q=None), -1), (dict(q=ODD), -1), (dict(qs=504), -1), (dict(qs=516), -1),
     (dict(out=ODD), -1), (dict(lse=None), -1), (dict(ksc=None), -1), (dict(ws=ctypes.c_void_p(0x10010)), -1),
