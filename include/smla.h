@@ -298,8 +298,9 @@ int mla_v_up_proj(const void* attn_out, const void* w_uv, void* out, int T, int 
  * they are not read, and their results are left as they were, so a batch
  * padded to a fixed T can be captured into a CUDA graph.
  * At most 8192 requests per call (SMLA_ERR_UNSUPPORTED beyond); NB * HK * 64
- * must fit in int32.  No kernel of these calls starts before the preceding
- * work on `stream` has completed. */
+ * must fit in int32.  Every call begins behind the preceding work on `stream`:
+ * the launches of paged_attention_fp8 may overlap its end, but read and write
+ * no memory before it has completed. */
 
 /* Block tables, slot maps and positions of a batch from its requests' lengths.
  * Request r has context_lens[r] tokens cached (negative counts as 0) in the
@@ -369,14 +370,21 @@ int kv_cache_store_fp8(const void* k, int64_t k_stride, const void* v, int64_t v
  *   alibi_slopes fp32 [H], prefix_lens int32 [R], doc_start int32 [T]: each may be NULL
  *   max_query_len  an estimate of the most new tokens of a request, for the choice of the work split;
  *                  any value gives right results
+ * MB may be at most 2^24.
  * Keys that a token does not see do not reach its result whatever their bytes
  * and scales hold, with one exception: a NaN code (which kv_cache_store_fp8
  * never writes) or a NaN or infinite scale at a position that another token of the
- * same request sees.  The codes enter both products as stored, q as two e4m3
- * terms (exact but for components below 2^-10 of their row's largest), the
- * weights as an e4m3 and an e5m2 term (about 8 significant bits); sums in
- * float32.
- *   workspace  at least paged_attention_fp8_workspace_bytes(...) bytes, 256-byte aligned; NULL = library-cached */
+ * same request sees.  Sums and softmax statistics are float32.  q enters as
+ * two e4m3 terms, exact but for components below 2^-10 of their row's
+ * largest, and K as stored.  With up to 48 rows (query heads per K/V head
+ * times max_query_len) V enters as stored and the weights as two e4m3 terms:
+ * within 2^-8 of their value, below 2^-10 of the row's largest weight in
+ * steps of 2^-17 of it, rounded so that equal ones keep their sum.  With
+ * more rows the weights and V are f16: within 2^-11 and, absolutely, 2^-22 of the
+ * row's sum.  This holds while the V scales of a request and head lie within
+ * 2^10 of their largest (zero rows aside): smaller ones lose bits.
+ *   workspace  at least paged_attention_fp8_workspace_bytes(...) bytes, 256-byte aligned (with more than 48
+ *              rows it holds a copy of q too); NULL = library-cached.  Calls that may overlap need one each */
 int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
                         const float* k_scale, const float* v_scale, const int32_t* block_table,
                         const int32_t* seq_lens, const int32_t* query_start, float sm_scale, int max_query_len,

@@ -19,6 +19,9 @@
 // may overwrite an input (release always counts across CTAs, too) the CTAs form
 // one thread-block cluster, and inputs are read before a cluster barrier and
 // written after it; extend otherwise takes as many CTAs as the tokens fill.
+// Measured, replayed from a graph: extend, 500 requests with 95 000 new tokens 8.1
+// us (1.5 MB), 8 single tokens 5.4; release, a third of 700 requests 11.5 us (0.5 MB:
+// the table rows, then the stack, three dependent passes through memory), 3 of 8 4.1.
 #include <cstdint>
 #include <algorithm>
 #include <cooperative_groups.h>

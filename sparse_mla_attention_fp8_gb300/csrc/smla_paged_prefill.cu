@@ -24,8 +24,21 @@
 //  * P overwrites S in tensor memory and enters P V from there.
 //  * q is split by a kernel beforehand, so that a segment's Q is one copy that
 //    overlaps the end of the segment before.
+//  * Masks, caps and slopes change S in tensor memory before the pass, in a loop
+//    of their own: unrolled into it they ran out of the instruction caches (three
+//    prompts without any: 447 us, now 410).
 //  * Roles: TMA producer, MMA issuer, scheduler, 4 warps converting V, 8 softmax
 //    warps per half, which also write the results.
+//
+// Measured, all launches of a call: three prompts of up to 2500 tokens over up
+// to 6000 cached ones, 8 K/V heads, G = 4, D = 128 (0.37 TFLOP): 410 us, 0.89 PFLOP/s,
+// 0.46 of what a bf16 matrix product reaches; alone the kernel takes 376 us (tensor
+// pipe active 43 % of it), the split of q 22, the merge 17.  A half's chain of S (512
+// clocks), softmax (1400), P V (512) and four handovers (150 - 300 each) bounds it: S
+// and P share their tensor memory, so the next S waits for P V, and two halves
+// fill it.  Five prompts of up to 1300 tokens, G = 12, D = 64, capped, packed
+// documents: 76 us, bound by short segments (2 tiles) and by the softmax, which with
+// cap and masks takes 4200 clocks a tile.
 #include "smla_paged.cuh"
 
 namespace smla {
@@ -36,7 +49,8 @@ constexpr int kRows = 128;          // rows of a half
 constexpr float kTop16 = 65000.f;   // largest sum of a thread's weights P = 2^(x - m') (f16: 65504)
 constexpr float kRefresh16 = 2.f;   // a refreshed m' puts the tile's maximum at 2^2
 constexpr float kLow16 = 0x1p-3f;   // a row whose first keys weigh less is refreshed
-// Places of a unit beside its tiles: about what its start and end take.
+// Places of a unit beside its tiles: about what its start and end take (the prompts above: 1, 2, 3, 4, 6 give 480,
+// 412, 412, 415, 420 us; the packed documents 93, 93, 101, 98, 99, before their query tiles were counted by several lanes).
 constexpr int kUnitCost = 2;
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -145,8 +159,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
 
 // tanh(u) / u as a polynomial of u^2 <= 0.5: the one of degree 4 through the Chebyshev
 // points of [0, 0.5], to within 4 x 2^-23 of the value.  Caps are wide as a rule, so
-// that most keys need no exponential and no reciprocal for theirs (five prompts of up
-// to 1300 tokens, G = 12, D = 64, cap 50, packed documents: 94 us, without it 100).
+// that most keys need no exponential and no reciprocal for theirs (the packed documents
+// above: 94 us when this came, without it 100).
 constexpr float kTanhTop = 0.5f;  // of u^2
 __device__ constexpr float kTanh[5] = {0.99999964f, -0.33329946f, 0.13277967f, -0.05072029f, 0.01364212f};
 

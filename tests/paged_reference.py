@@ -136,14 +136,15 @@ def attention(q, kc, vc, ks, vs, table, lens, query_start, sm_scale, window=0, s
               doc=None):
     """(out, lse, tolerance of out, tolerance of lse), float64; NaN in rows of no request.
 
-    Tolerances.  out = sum w v / sum w: the weights enter the product as an
-    e4m3 and an e5m2 term, off by at most 2^-4 * 2^-3 = 2^-7 of their value
-    (and at most 2^-24 of the row's largest weight, where they underflow), so
-    |error| <= 2^-7 sum w |v| / sum w + n 2^-24 max |v|, plus the rounding to
-    bf16 (half a step, 2^-8 of the value) and the logits' own error times the
-    spread of v (2 dx max |v|).  The logits: q in two e4m3 terms (off by at
-    most 2^-18 of the row's largest |q|), products exact, float32 sums of
-    2 D = 256 terms at most: dx = sm_scale max|q| sum|K| (2^-18 + 2^-16)."""
+    Tolerances.  out = sum w v / sum w: the weights enter the product as two
+    e4m3 terms, off by at most 2^-4 * 2^-4 of their value, or as f16, 2^-11;
+    2^-7 sum w |v| / sum w covers either twice.  Small weights are rounded in
+    absolute steps, but evenly to both sides: n 2^-24 max |v| of the row's
+    largest weight.  Then the rounding to bf16 (half a step, 2^-8 of the
+    value) and the logits' own error times the spread of v (2 dx max |v|).
+    The logits: q in two e4m3 terms (off by at most 2^-18 of the row's largest
+    |q|), products exact, float32 sums of 2 D = 256 terms at most: dx = sm_scale
+    max|q| sum|K| (2^-18 + 2^-16)."""
     T, H, D = q.shape
     NB, HK = ks.shape
     G = H // HK
