@@ -379,10 +379,11 @@ int kv_cache_store_fp8(const void* k, int64_t k_stride, const void* v, int64_t v
  * largest, and K as stored.  With up to 48 rows (query heads per K/V head
  * times max_query_len) V enters as stored and the weights as two e4m3 terms:
  * within 2^-8 of their value, below 2^-10 of the row's largest weight in
- * steps of 2^-17 of it, rounded so that equal ones keep their sum.  With
- * more rows the weights and V are f16: within 2^-11 and, absolutely, 2^-22 of the
- * row's sum.  This holds while the V scales of a request and head lie within
- * 2^10 of their largest (zero rows aside): smaller ones lose bits.
+ * steps of 2^-17 of it, rounded so that equal ones keep their sum; where one
+ * of two neighbouring blocks has a smaller V scale, its weights have these
+ * limits higher by the ratio.  With more rows the weights and V are f16: within
+ * 2^-11 and, absolutely, 2^-22 of the row's sum; V scales below 2^-15 of the
+ * largest that the request's tokens see lose bits.
  *   workspace  at least paged_attention_fp8_workspace_bytes(...) bytes, 256-byte aligned (with more than 48
  *              rows it holds a copy of q too); NULL = library-cached.  Calls that may overlap need one each */
 int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,

@@ -371,6 +371,16 @@ def test_attention_many_small_weights(smla):
     check(b, attend(smla, b))
 
 
+@pytest.mark.parametrize("new", [[1, 1], [30, 70]])
+def test_attention_any_scales(smla, new):
+    """Scales of either sign and of zero."""
+    b = ref.Batch(29, 2, 4, 128, [700, 130], new)
+    rng = np.random.default_rng(29)
+    for s in b.scales:
+        s *= rng.choice([-1.0, 1.0, 0.0], s.shape, p=[0.45, 0.45, 0.1]).astype(np.float32)
+    check(b, attend(smla, b))
+
+
 @pytest.mark.parametrize("top,rest", [(0, -13.6), (0, -15.4), (0, -17), (0, -18.3), (16, 0), (100, 84.5), (-5, -21.6),
                                       (-12, -23.4), (-40, -52.3)])
 @pytest.mark.parametrize("HK,G,new", [(80, 1, 1), (40, 12, 1), (16, 16, 20)])
