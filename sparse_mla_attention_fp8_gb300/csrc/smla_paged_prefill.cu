@@ -341,16 +341,33 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
       // converted V, read MN-major: panels of 64 columns
       const uint64_t dv0 = make_sdesc(smem_u32(smem + L::kOffV16), kKeyTile * 128, 1024, kLayoutSw128);
       int tl = 0, seg = 0, done[2] = {0, 0}, filled[2] = {0, 0};  // by half: products P V issued, segments begun
+      int was = 0;  // halves of the segment before
       bool dead = false;
       auto wait = [&](int idx, uint32_t parity) {
         if (!dead) dead = !PA_WAIT(idx, parity);
         return !dead;
       };
       Ring<L::kStages> ring;  // the K tile that the next first half takes
+      // What a product that is seen to have ended leaves free: P V of half 0 its tile's K (both halves' S came
+      // before it), that of the last half its V.  (An arrival here is cheaper than a commit of its own.)
+      Ring<L::kStages> k_ring;
+      int k_due = 0, v_due = -1;
+      auto ended = [&](int h, bool last) {
+        if (h == 0 && k_due) {
+          mbar_arrive(&bars[L::kKEmpty + k_ring.i]);
+          k_ring.next();
+          k_due = 0;
+        }
+        if (last && v_due >= 0) {
+          mbar_arrive(&bars[L::kV16Empty + v_due]);
+          v_due = -1;
+        }
+      };
       auto qk = [&](int h, bool last, bool ends) {
         const int st = ring.i;
         if (!wait(L::kKFull + st, ring.phase)) return;
         if (done[h] > 0 && !wait(L::kPvDone + h, (done[h] + 1) & 1)) return;
+        ended(h, last);
         tc_fence_after();
         const uint64_t dk = dk0 + (uint64_t)((st * L::kKTile) >> 4), dq = dq0 + (uint64_t)((h * L::kQHalf) >> 4);
 #pragma unroll
@@ -360,10 +377,7 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
             mma_f8(tmem + L::kTmemS + 128 * h, dq + ((term * L::kQTerm + 32 * k) >> 4), dk + ((32 * k) >> 4), id_qk,
                    term + k > 0 ? 1u : 0u);
         mma_commit(&bars[L::kSFull + h]);
-        if (last) {
-          mma_commit(&bars[L::kKEmpty + st]);
-          ring.next();
-        }
+        if (last) ring.next();
         if (ends) mma_commit(&bars[L::kQEmpty + h]);
       };
       auto pv = [&](int h, int t, bool first, bool last) {
@@ -378,7 +392,8 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
           mma_ts(tmem + L::kTmemO + 128 * h, tmem + L::kTmemS + 128 * h + 64 * (k >> 2) + 8 * (k & 3),
                  dv + ((2048 * k) >> 4), id_pv, (!first || k > 0) ? 1u : 0u);
         mma_commit(&bars[L::kPvDone + h]);
-        if (last) mma_commit(&bars[L::kV16Empty + vb]);
+        if (h == 0) k_due = 1;
+        if (last) v_due = vb;
         ++done[h];
       };
       while (true) {
@@ -388,15 +403,24 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
         const int n = sp->n, halves = sp->ntok > half_tokens ? 2 : 1;
         if (n == 0) break;
         mbar_arrive(&bars[L::kSegFree + sb]);
-        for (int h = 0; h < halves; ++h) {
+        // (the segment before may have had another number of halves)
+        if (done[0] > 0 && wait(L::kPvDone, (done[0] + 1) & 1)) ended(0, was == 1);
+        if (done[1] > 0 && wait(L::kPvDone + 1, (done[1] + 1) & 1)) ended(1, true);
+        was = halves;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h >= halves) break;
           wait(L::kQFull + h, filled[h]++ & 1);
           qk(h, h == halves - 1, n == 1);
         }
-        for (int i = 0; i < n && !dead; ++i, ++tl)
-          for (int h = 0; h < halves; ++h) {
+        for (int i = 0; i < n && !dead; ++i, ++tl) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h >= halves) break;
             pv(h, tl, i == 0, h == halves - 1);
             if (i + 1 < n) qk(h, h == halves - 1, i + 2 == n);
           }
+        }
         if (dead) break;
         ++seg;
       }
