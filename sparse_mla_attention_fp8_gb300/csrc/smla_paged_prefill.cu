@@ -26,14 +26,14 @@
 //    overlaps the end of the segment before.
 //  * Masks, caps and slopes change S in tensor memory before the pass, in a loop
 //    of their own: unrolled into it they ran out of the instruction caches (three
-//    prompts without any: 447 us, now 410).
+//    prompts without any: 447 us, then 413).
 //  * Roles: TMA producer, MMA issuer, scheduler, 4 warps converting V, 8 softmax
 //    warps per half, which also write the results.
 //
 // Measured, all launches of a call: three prompts of up to 2500 tokens over up
-// to 6000 cached ones, 8 K/V heads, G = 4, D = 128 (0.37 TFLOP): 410 us, 0.89 PFLOP/s,
-// 0.46 of what a bf16 matrix product reaches; alone the kernel takes 376 us (tensor
-// pipe active 43 % of it), the split of q 22, the merge 17.  A half's chain of S (512
+// to 6000 cached ones, 8 K/V heads, G = 4, D = 128 (0.37 TFLOP): 399 us, 0.92 PFLOP/s,
+// 0.47 of what a bf16 matrix product reaches; alone the kernel takes 373 us (tensor
+// pipe active 44 % of it), the split of q 21, the merge 17.  A half's chain of S (512
 // clocks), softmax (1400), P V (512) and four handovers (150 - 300 each) bounds it: S
 // and P share their tensor memory, so the next S waits for P V, and two halves
 // fill it.  Five prompts of up to 1300 tokens, G = 12, D = 64, capped, packed
