@@ -472,19 +472,24 @@ __device__ __forceinline__ PagedMerge walk_segments(const PagedParams& p, const 
 }
 
 // The units that several CTAs share: out = sum_i w_i O_i / sum_i w_i l_i, w_i =
-// 2^(m_i - max m), lse = max m + log2 of the latter sum.  A warp per row of a
-// unit, D / 32 value columns a lane; blockIdx.x: the CTA that began the unit.
-// Bound by latency: two dependent reads, with the parts' values in flight
-// together and no exchange between warps: 8 us behind 64 requests' decode, 17 us
-// behind three prompts of up to 2500 tokens (19 MB of parts).
-constexpr int kMergeThreads = 128, kMaxParts = 1024;
+// 2^(m_i - max m), lse = max m + log2 of the latter sum.  blockIdx.x: the CTA that
+// began the unit.  D / 32 value columns a lane, kWarps warps a row, whose sums meet
+// in shared memory.  Bound by latency: two dependent reads, with the parts' values
+// in flight together.  8 us behind 64 requests' decode, 17 us behind three prompts of up to
+// 2500 tokens (19 MB of parts).
+constexpr int kMaxParts = 1024;
+template <int C>
+constexpr int kMergeThreads = C == 256 ? 256 : 128;  // (a prompt of 300 tokens: 23.2 us with 256, 24.4 with 128)
 
-template <int D, int C>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedParams p) {
+template <int D, int C, int kWarps>
+__global__ void __launch_bounds__(kMergeThreads<C>) paged_merge_kernel(const __grid_constant__ PagedParams p) {
+  constexpr int kPer = D / 32;
+  __shared__ float warp_acc[kWarps][D], warp_sum[kWarps];
   grid_dependency_wait();
   const PagedMerge u = p.merge[blockIdx.x];
-  const int lane = threadIdx.x & 31, c = (int)blockIdx.y * (kMergeThreads / 32) + ((int)threadIdx.x >> 5);
-  if (c >= u.ntok * u.heads || u.parts == 0) return;
+  const int lane = threadIdx.x & 31, warp = (int)threadIdx.x >> 5, share = warp % kWarps;
+  const int c = (int)blockIdx.y * (kMergeThreads<C> / 32 / kWarps) + warp / kWarps;
+  if (c >= u.ntok * u.heads || u.parts == 0) return;  // (the same for the warps of a row)
   // the parts: slot 1 of this CTA, then slot 0 of the following ones
   const int64_t first = 2 * (int64_t)blockIdx.x;
   auto part = [&](int i) { return first + (i == 0 ? 1 : 2 * i); };
@@ -492,22 +497,21 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
   for (int i = lane; i < u.parts; i += 32) top = fmaxf(top, p.part_ml[part(i) * 2 * C + c]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-  constexpr int kPer = D / 32;
   float sum = 0.f, acc[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-  for (int base = 0; base < u.parts; base += 32) {
+  for (int base = share; base < u.parts; base += 32 * kWarps) {  // this warp's: base, base + kWarps, ...
     float w = 0.f;
-    if (base + lane < u.parts) {
-      const float* ml = p.part_ml + part(base + lane) * 2 * C + c;
+    if (base + kWarps * lane < u.parts) {
+      const float* ml = p.part_ml + part(base + kWarps * lane) * 2 * C + c;
       w = ex2_approx(ml[0] - top);
       sum = fmaf(w, ml[C], sum);
     }
-    const int n = min(32, u.parts - base);
+    const int n = min(32, (u.parts - base + kWarps - 1) / kWarps);
 #pragma unroll 8
     for (int j = 0; j < n; ++j) {
       const float f = __shfl_sync(kAll, w, j);
-      const float* o = p.part_o + (part(base + j) * C + c) * D + kPer * lane;
+      const float* o = p.part_o + (part(base + kWarps * j) * C + c) * D + kPer * lane;
       if (kPer == 4) {
         const float4 v = *reinterpret_cast<const float4*>(o);
         acc[0] = fmaf(f, v.x, acc[0]);
@@ -523,6 +527,19 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  if (kWarps > 1) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) warp_acc[share][kPer * lane + k] = acc[k];
+    if (lane == 0) warp_sum[share] = sum;
+    __syncthreads();
+    if (share > 0) return;
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) {
+      sum += warp_sum[i];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] += warp_acc[i][kPer * lane + k];
+    }
+  }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t row = (int64_t)(u.t0 + c / u.heads) * p.a.H + u.h0 + c % u.heads;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.a.out) + row * D + kPer * lane);
@@ -624,10 +641,20 @@ cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+template <int D, int C, int kWarps>
+cudaError_t launch_merge_warps(const PagedParams& p, cudaStream_t stream) {
+  return launch_overlapped(paged_merge_kernel<D, C, kWarps>,
+                           dim3((unsigned)p.ctas, (unsigned)(C * kWarps / (kMergeThreads<C> / 32))), kMergeThreads<C>, 0,
+                           stream, p);
+}
+// Four warps a row where a unit may have 16 parts or more (few units, long tables): one request of up to 8000 tokens
+// 14.8 us, 19.2 with one warp; of 1000 tokens 11.3 and 10.6; 64 of up to 16 000 177.7 and 176.0.
 template <int D, int C>
 cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
-  return launch_overlapped(paged_merge_kernel<D, C>, dim3((unsigned)p.ctas, (unsigned)(C / (kMergeThreads / 32))),
-                           kMergeThreads, 0, stream, p);
+  const int64_t tiles = std::max<int64_t>(((int64_t)p.a.T + p.tq - 1) / p.tq, std::min(p.a.R, p.a.T));
+  const int64_t parts = std::min<int64_t>(p.ctas / (tiles * p.HV), p.a.MB / 2 + 1);
+  if (C <= 16 && parts >= 16) return launch_merge_warps<D, C, C <= 16 ? 4 : 1>(p, stream);
+  return launch_merge_warps<D, C, 1>(p, stream);
 }
 
 cudaError_t cache_maps(const PagedAttnArgs& a, CUtensorMap* k_map, CUtensorMap* v_map) {
