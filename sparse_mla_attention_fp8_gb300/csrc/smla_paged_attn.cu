@@ -48,7 +48,7 @@
 // Measured, all launches of a call, D = 128 unless stated, shares of the copy
 // bandwidth 6.79 TB/s: 64 requests of up to 16 000 tokens, 8 K/V heads, G = 8
 // (1.14 GB) 176 us, 0.95; 3 of up to 260 000, 4 heads, G = 7, distance biases (0.56
-// GB) 99 us, 0.83; 200 of up to 500, 8 heads, G = 8 (0.13 GB) 57 us, 0.33: a segment's
+// GB) 95 us, 0.86; 200 of up to 500, 8 heads, G = 8 (0.13 GB) 57 us, 0.33: a segment's
 // start and end take what 4 of its tiles do; 100 windows of 4096, 5 tokens each, 5
 // heads, G = 3, D = 64, capped (0.23 GB) 84 us, 0.40: the chain S, softmax, P V of a
 // 16 KB tile takes 1.7 us and one tile per CTA is in its softmax at a time.
