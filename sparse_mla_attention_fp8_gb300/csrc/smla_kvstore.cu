@@ -43,7 +43,12 @@ __device__ __forceinline__ float finite_amax(float amax, uint32_t w) {
   if (hi < INFINITY) amax = fmaxf(amax, hi);
   return amax;
 }
-__device__ __forceinline__ float nan_to_0(float x) { return x == x ? x : 0.f; }
+// Both halves of w, NaN as 0.
+__device__ __forceinline__ uint32_t nan_to_0(uint32_t w) {
+  if ((w & 0x7fffu) > 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7fff0000u) > 0x7f800000u) w &= 0xffffu;
+  return w;
+}
 
 // Exponent E of the scale of a group with this amax (finite, >= 0): amax =
 // (1 + f) 2^e, and 448 = 1.75 * 2^8.  Subnormal bf16 have e = -127 here, far
@@ -78,8 +83,8 @@ __device__ __forceinline__ void rescale_codes(uint32_t* __restrict__ w, int word
 }
 
 __device__ __forceinline__ uint32_t codes_of(uint2 v, float inv) {
-  return e4m3x4(nan_to_0(__uint_as_float(v.x << 16)) * inv, nan_to_0(__uint_as_float(v.x & 0xffff0000u)) * inv,
-                nan_to_0(__uint_as_float(v.y << 16)) * inv, nan_to_0(__uint_as_float(v.y & 0xffff0000u)) * inv);
+  return e4m3x4(__uint_as_float(v.x << 16) * inv, __uint_as_float(v.x & 0xffff0000u) * inv,
+                __uint_as_float(v.y << 16) * inv, __uint_as_float(v.y & 0xffff0000u) * inv);
 }
 
 // The new rows [row0, row0 + n) of one block and head, by one warp (kGroup = 1)
@@ -98,23 +103,45 @@ __device__ __forceinline__ void store_rows(const __nv_bfloat16* __restrict__ src
   const float old = row0 > 0 ? *scale : 0.f;
   const int first = warp * kHeld * kRowsPer;  // this warp's first row
   uint2 v[kHeld];
-  uint32_t top = 0u;
-  for (int base = first; base < n; base += kGroup == 4 ? kBlock : kHeld * kRowsPer) {
+  // The largest magnitude's bits: as integers, and again without infinities and NaN where there are any (`special`,
+  // the same for the group: most blocks need neither that nor NaN made 0, a third of the work).
+  auto amax = [&](bool finite) {
+    uint32_t top = 0u;
+    for (int base = first; base < n; base += kGroup == 4 ? kBlock : kHeld * kRowsPer) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int r = base + i * kRowsPer + sub;
-      v[i] = r < n ? __ldg(reinterpret_cast<const uint2*>(src + r * stride + col)) : make_uint2(0u, 0u);
+      for (int i = 0; i < kHeld; ++i) {
+        const int r = base + i * kRowsPer + sub;
+        if (kGroup == 4 && finite) break;  // (held)
+        v[i] = r < n ? __ldg(reinterpret_cast<const uint2*>(src + r * stride + col)) : make_uint2(0u, 0u);
+      }
+      if (finite) {
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+          most = finite_amax(finite_amax(most, v[i].x), v[i].y);
+          v[i] = make_uint2(nan_to_0(v[i].x), nan_to_0(v[i].y));
+        }
+        top = max(top, __float_as_uint(most));  // non-negative: ordered as its bits
+      } else {
+        uint32_t pair = 0u;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) pair = max_u16x2(pair, max_u16x2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu));
+        top = max(top, max(pair << 16, pair & 0xffff0000u));
+      }
     }
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) amax = finite_amax(finite_amax(amax, v[i].x), v[i].y);
-    top = max(top, __float_as_uint(amax));  // non-negative: ordered as its bits
-  }
-  top = __reduce_max_sync(kAll, top);
-  if (kGroup == 4) {
-    if (lane == 0) shared_max[warp] = top;
-    named_bar_sync(bar, 128);  // and every warp has read the old scale
-    top = max(max(shared_max[0], shared_max[1]), max(shared_max[2], shared_max[3]));
+    top = __reduce_max_sync(kAll, top);
+    if (kGroup == 4) {
+      if (lane == 0) shared_max[warp] = top;
+      named_bar_sync(bar, 128);  // and every warp has read the old scale
+      top = max(max(shared_max[0], shared_max[1]), max(shared_max[2], shared_max[3]));
+    }
+    return top;
+  };
+  uint32_t top = amax(false);
+  const bool special = top >= 0x7f800000u;
+  if (special) {
+    if (kGroup == 4) named_bar_sync(bar, 128);  // shared_max has been read
+    top = amax(true);
   }
   float s, inv;
   block_scale(old, top, s, inv);
@@ -127,6 +154,7 @@ __device__ __forceinline__ void store_rows(const __nv_bfloat16* __restrict__ src
       const int r = base + i * kRowsPer + sub;
       if (r >= n) break;
       if (again) v[i] = __ldg(reinterpret_cast<const uint2*>(src + r * stride + col));
+      if (again && special) v[i] = make_uint2(nan_to_0(v[i].x), nan_to_0(v[i].y));
       *reinterpret_cast<uint32_t*>(dst + (base + i * kRowsPer) * D) = codes_of(v[i], inv);
     }
   }
@@ -134,7 +162,7 @@ __device__ __forceinline__ void store_rows(const __nv_bfloat16* __restrict__ src
 }
 
 template <int D, int kGroup>
-__global__ void __launch_bounds__(32 * kStoreWarps) kv_store_kernel(const __grid_constant__ KvStoreArgs a) {
+__global__ void __launch_bounds__(32 * kStoreWarps, 4) kv_store_kernel(const __grid_constant__ KvStoreArgs a) {
   __shared__ uint32_t group_max[kStoreWarps];
   const int u = (int)blockIdx.x, group = (int)threadIdx.x / (32 * kGroup), t = (int)threadIdx.x % (32 * kGroup);
   const int item = (int)blockIdx.y * (kStoreWarps / kGroup) + group;

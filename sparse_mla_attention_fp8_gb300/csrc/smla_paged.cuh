@@ -172,6 +172,11 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t pair) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // Offset of 16-byte chunk ch of row r, rows of D bytes under the D-byte swizzle.
 template <int D>
 __device__ __forceinline__ uint32_t swz(int r, int ch) {

@@ -73,12 +73,6 @@ __device__ __forceinline__ void split_p(float x0, float x1, uint32_t dither, uin
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(t) : "r"(r));
   lo = t;
 }
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // What a row needs of its own.
 template <int C>
 struct Columns {

@@ -191,6 +191,19 @@ def test_store_special_values(smla):
     run_store(smla, lens, start, table, x, cache, scale)
 
 
+@pytest.mark.parametrize("HK,D,ctx,new", [(3, 128, [5, 0], [130, 64]), (2, 64, [9, 0], [150, 30]),
+                                          (2, 128, [3] + [40] * 5, [45] + [1] * 5), (2, 64, [0] * 6, [60, 1, 1, 1, 1, 1])])
+def test_store_scattered_special_values(smla, HK, D, ctx, new):
+    """Infinities and NaN in some blocks and heads and not in others, by one warp and by four."""
+    lens, start, table, _, x, cache, scale = store_inputs(HK, D, ctx, new, 7)
+    rng = np.random.default_rng(7)
+    for y in x:
+        where = (rng.random(y.shape) < 0.002) & (rng.random((1, HK, 1)) < 0.7)
+        y[where] = rng.choice([np.inf, -np.inf, np.nan], where.sum())
+        assert not np.isfinite(y).all()
+    run_store(smla, lens, start, table, x, cache, scale)
+
+
 def test_store_skips_what_has_no_block(smla):
     lens, start, table, NB, x, cache, scale = store_inputs(2, 128, [0, 100, 5, 64], [70, 40, 3, 9], 6)
     table[0, 1], table[1, 1], table[2, 0] = -1, NB, -5
