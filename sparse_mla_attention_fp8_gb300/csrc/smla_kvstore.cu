@@ -18,9 +18,8 @@
 // tokens can touch, so a unit finds its request by a search in query_start.
 // One warp or four per (block, head, K or V); the new rows are read once, so the
 // kernel moves what it must: bound by HBM for prefill, by latency for single
-// tokens.  Measured at 8 heads, D = 128: 9 requests of up to 3500 tokens (148 MB) 34
-// us, 4.3 TB/s, 0.64 of the copy bandwidth (issue slots 63 % busy: the rounding); 64
-// single tokens 3.2 us replayed from a graph.
+// tokens.  Measured at 8 heads, D = 128, replayed from a graph: 9 requests of up to
+// 3500 tokens (148 MB) 25.8 us, 5.7 TB/s, 0.84 of the copy bandwidth; 64 single tokens 2.9 us.
 #include "smla_paged.cuh"
 
 namespace smla {
@@ -201,7 +200,7 @@ static void launch(const KvStoreArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_store(const KvStoreArgs& a, cudaStream_t stream) {
-  // Four warps a block and head where a request brings 16 rows or more on average: one warp | four take 3.2 | 6.0 us
+  // Four warps a block and head where a request brings 16 rows or more on average: one warp | four took 3.2 | 6.0 us
   // for 64 requests of one row, 14.7 | 15.2 for 200 of 9 on average, 25 | 12 for 64 of up to 300.
   const bool many = a.T / 16 >= a.R;
   if (a.D == 128)
