@@ -76,7 +76,7 @@ __device__ __forceinline__ void split_p(float x0, float x1, uint32_t dither, uin
 // What a row needs of its own.
 template <int C>
 struct Columns {
-  float scale[C];  // logit = S * scale * k_scale, in log2 units (natural ones with softcap)
+  float scale[C];  // logit = S * scale * k_scale, in log2 units (in caps with softcap)
   float slope[C];  // log2 units per key of distance
   int pos[C], lo[C], hi[C];
 };
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op + 8, c >> 1) + 8 * (c & 1)), "r"(l[0]),
                        "r"(l[1])
                        : "memory");
-          if (c == 0) cols->scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f : kLog2e);
+          if (c == 0) cols->scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f / a.softcap : kLog2e);
         }
       }
       fence_proxy_async_smem();
@@ -491,10 +491,26 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kSFree + buf]);
         if (a.softcap > 0.f) {
-          // cap tanh(x / cap) = cap (1 - 2 / (1 + e^(2 x / cap))), to within a few 2^-23 cap
-          const float to = 2.f * kLog2e / a.softcap, cap = a.softcap * kLog2e;
+          // y is x / cap.  The polynomial alone where it holds for all, else each by its own size.
+          const float cap = a.softcap * kLog2e;
+          float most = 0.f;
 #pragma unroll
-          for (int c = 0; c < C; ++c) y[c] = fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(y[c] * to)), cap);
+          for (int c = 0; c < C; ++c) most = fmaxf(most, fabsf(y[c]));
+          if (__all_sync(kAll, most * most <= kTanhTop)) {
+#pragma unroll
+            for (int c = 0; c < C; c += 2) {
+              const uint64_t u = pack2(y[c], y[c + 1]), u2 = mul2(u, u);
+              uint64_t t = pack2(cap * kTanh[4], cap * kTanh[4]);
+#pragma unroll
+              for (int d = 3; d >= 0; --d) t = fma2(t, u2, pack2(cap * kTanh[d], cap * kTanh[d]));
+              const float2 v = unpack2(mul2(u, t));
+              y[c] = v.x;
+              y[c + 1] = v.y;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) y[c] = cap * tanh_any(y[c]);
+          }
         }
         if (a.alibi_slopes) {
 #pragma unroll

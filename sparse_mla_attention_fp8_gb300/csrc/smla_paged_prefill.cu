@@ -157,13 +157,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int x
       : "memory");
 }
 
-// tanh(u) / u as a polynomial of u^2 <= 0.5: the one of degree 4 through the Chebyshev
-// points of [0, 0.5], to within 4 x 2^-23 of the value.  Caps are wide as a rule, so
-// that most keys need no exponential and no reciprocal for theirs (the packed documents
-// above: 94 us when this came, without it 100).
-constexpr float kTanhTop = 0.5f;  // of u^2
-__device__ constexpr float kTanh[5] = {0.99999964f, -0.33329946f, 0.13277967f, -0.05072029f, 0.01364212f};
-
 // kBent: with a softcap or slopes.
 template <int D, bool kBent>
 __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
@@ -642,11 +635,9 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
                   x[2 * k + 1] = __float_as_uint(z.y);
                 }
               } else {
-                // tanh(u) = 1 - 2 / (1 + e^(2 u)), to within a few 2^-23
+                // (each by its own size: another row may have reached its cap, or unseen codes be anything)
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  x[k] = __float_as_uint(
-                      fmaf(-2.f * cap, __fdividef(1.f, 1.f + ex2_approx(__uint_as_float(x[k]) * (2.f * kLog2e))), cap));
+                for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(cap * tanh_any(__uint_as_float(x[k])));
               }
             }
             if (kBent && a.alibi_slopes) {
