@@ -364,7 +364,7 @@ int kv_cache_store_fp8(const void* k, int64_t k_stride, const void* v, int64_t v
  *   lo = max(0, p - window + 1 if window > 0, doc_start[t] if given): a sliding window, and the first
  *        position of the token's document
  * with the logits x = sm_scale * q.k, then x = softcap * tanh(x / softcap) if
- * softcap > 0, then x -= alibi_slopes[h] * |p - j| if given.  A key whose block is
+ * softcap > 0 (from 1e-20 to 1e30: others are refused), then x -= alibi_slopes[h] * |p - j| if given.  A key whose block is
  * outside [0, NB) or beyond MB is not seen.  A token that sees no key gets out = 0
  * and lse = -inf.
  *   alibi_slopes fp32 [H], prefix_lens int32 [R], doc_start int32 [T]: each may be NULL

@@ -771,9 +771,10 @@ int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache,
   if (H <= 0 || H % HK != 0) return fail(SMLA_ERR_INVALID_ARG, "H=%d must be a positive multiple of HK=%d", H, HK);
   if (MB > (1 << 24)) return fail(SMLA_ERR_UNSUPPORTED, "MB=%d unsupported: at most 2^24", MB);
   if (H / HK > 128) return fail(SMLA_ERR_UNSUPPORTED, "H=%d unsupported: at most 128 heads per K/V head", H);
-  if (window < 0 || max_query_len < 0 || !(softcap >= 0.f) || softcap > 3e38f)
-    return fail(SMLA_ERR_INVALID_ARG, "window=%d, max_query_len=%d and softcap=%g must not be negative", window,
-                max_query_len, softcap);
+  if (window < 0 || max_query_len < 0)
+    return fail(SMLA_ERR_INVALID_ARG, "window=%d and max_query_len=%d must not be negative", window, max_query_len);
+  if (softcap != 0.f && !(softcap >= 1e-20f && softcap <= 1e30f))
+    return fail(SMLA_ERR_INVALID_ARG, "softcap=%g must be 0 or from 1e-20 to 1e30", softcap);
   if (T == 0 || R == 0) return SMLA_OK;
   rc = check_rows("q", q, q_stride, (int64_t)H * D);
   if (rc != SMLA_OK) return rc;
