@@ -399,8 +399,17 @@ size_t paged_attention_fp8_workspace_bytes(int T, int H, int HK, int D, int R, i
 /* Reads (and clears) the device status word of a workspace after
  * synchronizing `stream`: 0 = no fault; 1 = a kernel wait ran past its time
  * limit and the kernel unwound (its outputs are not valid).  workspace NULL =
- * the library-cached workspace of the current device. */
+ * the library-cached workspace of the current device, and every call of
+ * paged_attention_fp8 on that device since the last such read, whichever
+ * workspace it had.  A workspace's status word is its first 4 bytes: what
+ * they hold before the first call is read as it is, so zero them once. */
 int smla_read_device_status(void* workspace, int* status_out, void* stream);
+
+/* Runs one device thread that waits for what never comes until the kernels'
+ * time limit (2 s), and reports that as paged_attention_fp8 does in its
+ * kernel for few rows (many_rows = 0) or for many: for tests of a caller's
+ * failure handling.  workspace: at least 256 bytes, 256-byte aligned. */
+int smla_paged_wait_check(int many_rows, void* workspace, void* stream);
 
 /* smla_read_device_status for the fixed scratch of
  * sparse_mla_decode_fp8_noalloc on the current device: synchronizes

@@ -178,6 +178,8 @@ def lib():
             L.paged_attention_fp8.restype = i32
             L.paged_attention_fp8_workspace_bytes.argtypes = [i32] * 6
             L.paged_attention_fp8_workspace_bytes.restype = sz
+            L.smla_paged_wait_check.argtypes = [i32, P, P]
+            L.smla_paged_wait_check.restype = i32
             L.smla_read_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_int), P]
             L.smla_read_noalloc_status.restype = i32
             L.smla_last_error.argtypes = []
@@ -635,8 +637,9 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
     prefix that all tokens of a request see (int32 [R]) and documents (int32
     [T]: first position of the token's document) as asked.  max_query_len: an
     estimate of the most new tokens of a request (default: T - R + 1).  The
-    workspace, if none is given, is allocated for the call.  Returns (out bf16
-    [T,H,D], lse fp32 [T,H]); rows of no request are left as they were."""
+    workspace, if none is given, is allocated for the call; read_device_status()
+    tells whether a call has failed, with either.  Returns (out bf16 [T,H,D],
+    lse fp32 [T,H]); rows of no request are left as they were."""
     args = (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start, sm_scale, max_query_len, window,
             softcap, alibi_slopes, prefix_lens, doc_start, out, lse, workspace)
     call = (_binding or _bound()).attention
@@ -653,8 +656,24 @@ def read_noalloc_status(stream=None) -> int:
     return int(st.value)
 
 
+def paged_wait_check(workspace, many_rows: bool = False, stream=None) -> None:
+    """Let one device thread wait in vain until the kernels' time limit (2 s)
+    and report it as paged_attention_fp8 does (in its kernel for few or for
+    many rows): for tests of a caller's failure handling."""
+    import torch
+    dev = _dev(workspace)
+    if workspace.nbytes < 256:
+        raise SmlaError(f"workspace has {workspace.nbytes} bytes, 256 needed")
+    with torch.cuda.device(dev):
+        _check(lib().smla_paged_wait_check(int(many_rows), _ptr(workspace), _stream_ptr(stream, dev)),
+               "smla_paged_wait_check")
+
+
 def read_device_status(workspace=None, stream=None) -> int:
-    """Synchronize and read/clear the kernels' device status word (0 = ok)."""
+    """Synchronize and read/clear the kernels' device status word (0 = ok).
+    Without a workspace: that of the library's own workspace on the current
+    device, and whether a paged_attention_fp8 call on it has failed, whichever
+    workspace it had."""
     import torch
     st = ctypes.c_int(0)
     dev = workspace.device if workspace is not None else torch.device("cuda", torch.cuda.current_device())

@@ -582,31 +582,58 @@ int sparse_mla_translate_indices(const int32_t* indices, const int32_t* block_ta
   return SMLA_OK;
 }
 
+namespace {
+// Reads and clears a device word; into *out if it is set.
+int take_status(void* word, int* out) {
+  int v = 0;
+  cudaError_t e = cudaMemcpy(&v, word, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(status)");
+  if (v != 0) {
+    e = cudaMemset(word, 0, sizeof(int));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(status)");
+    *out = v;
+  }
+  return SMLA_OK;
+}
+}  // namespace
+
 int smla_read_device_status(void* workspace, int* status_out, void* stream) {
   if (!status_out) return fail(SMLA_ERR_INVALID_ARG, "null status_out");
+  // without a workspace: the library-cached one, and what the paged attention's calls report for the device
+  void* words[3] = {workspace, nullptr, nullptr};
   if (!workspace) {
     int dev;
     int rc = current_device(&dev);
     if (rc != SMLA_OK) return rc;
-    std::lock_guard<std::mutex> lk(g_mu);
-    workspace = g_dev[dev].ws;
+    {
+      std::lock_guard<std::mutex> lk(g_mu);
+      words[0] = g_dev[dev].ws;
+    }
+    int* paged[2] = {nullptr, nullptr};
+    cudaError_t e = smla::paged_attn_timed_out(&paged[0]);
+    if (e == cudaSuccess) e = smla::paged_prefill_timed_out(&paged[1]);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetSymbolAddress(status)");
+    words[1] = paged[0];
+    words[2] = paged[1];
   }
-  if (!workspace) {
-    *status_out = 0;
-    return SMLA_OK;
-  }
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaStreamSynchronize(s);
+  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-  int v = 0;
-  e = cudaMemcpy(&v, workspace, sizeof(int), cudaMemcpyDeviceToHost);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(status)");
-  if (v != 0) {
-    e = cudaMemset(workspace, 0, sizeof(int));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(status)");
+  *status_out = 0;
+  for (void* word : words) {
+    const int rc = word ? take_status(word, status_out) : SMLA_OK;
+    if (rc != SMLA_OK) return rc;
   }
-  *status_out = v;
   return SMLA_OK;
+}
+
+int smla_paged_wait_check(int many_rows, void* workspace, void* stream) {
+  if (!workspace) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(SMLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  int* status = static_cast<int*>(workspace);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = many_rows ? smla::paged_prefill_wait_check(status, s) : smla::paged_attn_wait_check(status, s);
+  return e == cudaSuccess ? SMLA_OK : cuda_fail(e, "smla_paged_wait_check launch");
 }
 
 // ---- MLA weight absorption

@@ -182,6 +182,12 @@ cudaError_t launch_paged_prefill(const PagedAttnArgs& a, int num_sms, cudaStream
 // max_query_len: an estimate.
 size_t paged_attention_workspace(int T, int H, int HK, int D, int R, int max_query_len, int num_sms);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int max_query_len, int num_sms, cudaStream_t stream);
+// The current device's words that a wait which ran out in the kernels of either file sets, and a kernel of each
+// file whose only wait runs out.
+cudaError_t paged_attn_timed_out(int** word);
+cudaError_t paged_prefill_timed_out(int** word);
+cudaError_t paged_attn_wait_check(int* status, cudaStream_t stream);
+cudaError_t paged_prefill_wait_check(int* status, cudaStream_t stream);
 
 // Offsets inside the workspace.
 constexpr size_t kWsStatusBytes = 256;

@@ -220,6 +220,10 @@ __device__ __forceinline__ void split_q8(const uint32_t (&w)[4], uint32_t amax, 
   }
 }
 
+// Set when a wait of any call on the device runs out, whichever workspace the call had: one that is
+// allocated for a call is gone when its caller asks.  One word per file that includes this.
+__device__ int g_timed_out;
+
 // mbar_wait with its slow part out of line, so that the roles' loops stay
 // small, with a long suspension per probe, so that waiting warps leave the
 // issue slots to the others, and without a look at the (slow) clock before a
@@ -240,12 +244,28 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile 
     else if (globaltimer_ns() - t0 > kWaitLimitNs) break;
   }
   *cta_abort = 1;
-  atomicCAS(status, 0, kDevWaitTimeout);
+  atomicExch(status, kDevWaitTimeout);  // (whatever an uninitialised workspace held)
+  atomicExch(&g_timed_out, kDevWaitTimeout);
   return false;
 }
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* cta_abort, int* status) {
   return mbar_try_wait(bar, parity) || wait_slow(bar, parity, cta_abort, status);
 }
+
+// One thread that waits for what never comes, and so reports a wait that ran out.
+__global__ void paged_wait_check_kernel(int* status) {
+  __shared__ uint64_t bar;
+  __shared__ int abort_flag;
+  abort_flag = 0;
+  mbar_init(&bar, 1);
+  mbar_fence_init();
+  wait_bar(&bar, 0, &abort_flag, status);
+}
+cudaError_t wait_check(int* status, cudaStream_t stream) {
+  paged_wait_check_kernel<<<1, 1, 0, stream>>>(status);
+  return cudaGetLastError();
+}
+cudaError_t timed_out_word(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_timed_out); }
 
 // Place in a ring of N slots with a barrier each: index and the parity of its
 // phase (no divisions in the roles' loops).

@@ -760,4 +760,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, int max_query_len, in
   return a.D == 128 ? launch<128, 16>(a, num_sms, stream) : launch<64, 16>(a, num_sms, stream);
 }
 
+cudaError_t paged_attn_timed_out(int** word) { return timed_out_word(word); }
+cudaError_t paged_attn_wait_check(int* status, cudaStream_t stream) { return wait_check(status, stream); }
+
 }  // namespace smla

@@ -856,4 +856,7 @@ cudaError_t launch_paged_prefill(const PagedAttnArgs& a, int num_sms, cudaStream
   return a.D == 128 ? launch<128>(a, num_sms, stream) : launch<64>(a, num_sms, stream);
 }
 
+cudaError_t paged_prefill_timed_out(int** word) { return timed_out_word(word); }
+cudaError_t paged_prefill_wait_check(int* status, cudaStream_t stream) { return wait_check(status, stream); }
+
 }  // namespace smla

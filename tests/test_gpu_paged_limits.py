@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 import paged_reference as ref
+from helpers import torch_mod
 from test_gpu_paged import attend, check, smla  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -36,3 +37,21 @@ def test_wide_caps_beside_rows_that_reach_them(smla, G, D, new, cap):  # noqa: F
     b.q[:, 0] *= np.float32(cap / 4)
     b.q = ref.bf16_round(b.q)
     check(b, attend(smla, b), capped(b))
+
+
+# ---------------------------------------------------------------- failed calls
+
+@pytest.mark.parametrize("many_rows", [False, True])
+def test_a_wait_that_runs_out_is_reported_whatever_the_workspace(smla, many_rows):  # noqa: F811
+    """A device thread waits in vain, and reports it as the attention's kernels do, into a workspace that nothing
+    has cleared (as the ones that calls allocate for themselves): the device's status says so once."""
+    torch = torch_mod()
+    workspace = torch.full((256,), 0xFF, dtype=torch.uint8, device="cuda")
+    smla.read_device_status()
+    assert smla.read_device_status() == 0
+    smla.paged_wait_check(workspace, many_rows=many_rows)
+    assert smla.read_device_status(workspace) == 1
+    assert smla.read_device_status(workspace) == 0
+    del workspace
+    assert smla.read_device_status() == 1
+    assert smla.read_device_status() == 0
