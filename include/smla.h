@@ -364,9 +364,9 @@ int kv_cache_store_fp8(const void* k, int64_t k_stride, const void* v, int64_t v
  *   lo = max(0, p - window + 1 if window > 0, doc_start[t] if given): a sliding window, and the first
  *        position of the token's document
  * with the logits x = sm_scale * q.k, then x = softcap * tanh(x / softcap) if
- * softcap > 0 (from 1e-20 to 1e30: others are refused), then x -= alibi_slopes[h] * |p - j| if given.  A key whose block is
- * outside [0, NB) or beyond MB is not seen.  A token that sees no key gets out = 0
- * and lse = -inf.
+ * softcap > 0 (from 1e-20 to 1e30: others are refused), then
+ * x -= alibi_slopes[h] * |p - j| if given.  A key whose block is outside [0, NB)
+ * or beyond MB is not seen.  A token that sees no key gets out = 0 and lse = -inf.
  *   alibi_slopes fp32 [H], prefix_lens int32 [R], doc_start int32 [T]: each may be NULL
  *   max_query_len  an estimate of the most new tokens of a request, for the choice of the work split;
  *                  any value gives right results
@@ -382,8 +382,9 @@ int kv_cache_store_fp8(const void* k, int64_t k_stride, const void* v, int64_t v
  * steps of 2^-17 of it, rounded so that equal ones keep their sum; where one
  * of two neighbouring blocks has a smaller V scale, its weights have these
  * limits higher by the ratio.  With more rows the weights and V are f16: within
- * 2^-11 and, absolutely, 2^-22 of the row's sum; V scales below 2^-15 of the
- * largest that the request's tokens see lose bits.
+ * 2^-11 and, absolutely, 2^-29 of the row's sum for each key (2^-22 for the
+ * 512 nearest), which add up over the keys of a long context; V scales below
+ * 2^-15 of the largest that the request's tokens see lose bits.
  *   workspace  at least paged_attention_fp8_workspace_bytes(...) bytes, 256-byte aligned (with more than 48
  *              rows it holds a copy of q too); NULL = library-cached.  Calls that may overlap need one each */
 int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,

@@ -14,13 +14,14 @@
 //    8-bit terms need five, and V is converted once for the 256 rows.  The
 //    conversion also applies v_scale / R (R the largest v_scale of the segment:
 //    at most 1) and zeroes the keys that no row sees, whose codes may be
-//    anything.  P keeps 11 bits down to 2^-14 and loses nothing above 2^-25.
+//    anything.  P keeps 11 bits down to 2^-14, below that multiples of 2^-24.
 //  * Softmax: thread pair = row, each thread the keys of one block (one K
 //    scale).  P = 2^(x - m') with the row's running reference m', computed in one
 //    pass over S into registers.  m' starts at 0 and stays there while the row's
 //    logits lie where f16 is exact enough; only if a thread's weights add up to
-//    65000, or a row's first keys to less than 2^-3, is it refreshed (to put the
-//    tile's largest at 2^2), O scaled in tensor memory and the pass repeated.
+//    65000, a row's first keys to less than 2^-3 or its first 512 to less than 2^4
+//    is it refreshed (to put the tile's largest, or in the last case the sum, at
+//    2^4), O scaled in tensor memory and the pass repeated.
 //  * P overwrites S in tensor memory and enters P V from there.
 //  * q is split by a kernel beforehand, so that a segment's Q is one copy that
 //    overlaps the end of the segment before.
@@ -47,8 +48,13 @@ namespace {
 
 constexpr int kRows = 128;          // rows of a half
 constexpr float kTop16 = 65000.f;   // largest sum of a thread's weights P = 2^(x - m') (f16: 65504)
-constexpr float kRefresh16 = 2.f;   // a refreshed m' puts the tile's maximum at 2^2
+constexpr float kRefresh16 = 4.f;   // a refreshed m' puts the tile's maximum (or the row's sum) at 2^4
 constexpr float kLow16 = 0x1p-3f;   // a row whose first keys weigh less is refreshed
+// A row that weighs less than kThin16 with kThinAt more tiles has its sum put there (the tile's largest weight to 2^9 at
+// most): of any later key at most 2^-25 is lost to f16, 2^-29 of the sum, and these add up over long contexts.  Not
+// at the first tile, in which the diagonal leaves many rows a few keys.
+constexpr float kThin16 = 0x1p4f;
+constexpr int kThinAt = 3;
 // Places of a unit beside its tiles: about what its start and end take (the prompts above: 1, 2, 3, 4, 6 give 480,
 // 412, 412, 415, 420 us; the packed documents 93, 93, 101, 98, 99, before their query tiles were counted by several lanes).
 constexpr int kUnitCost = 2;
@@ -685,9 +691,10 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
           }
           const float2 s2 = unpack2(sum2);
           part = s2.x + s2.y;
-          // The sum tells whether some weight may be too large for f16, or a row's first keys too small for it
+          // The sum tells whether some weight may be too large for f16, or a row's keys so far too small for it
           // (a sum of 0 with keys to see: below what a float holds).
-          const bool low = l == 0.f && part < kLow16 && (inside || seen != 0ull);
+          const float least = i == kThinAt ? kThin16 : l == 0.f ? kLow16 : 0.f;
+          const bool low = l + part < least && (inside || seen != 0ull);
           if (pass == 1 || !bar_any(bar, 64, part > kTop16 || low)) break;
           float top = -INFINITY;  // the largest logit - m'
 #pragma unroll 1
@@ -701,14 +708,17 @@ __global__ void __launch_bounds__(PreLay<D>::kThreads, PreLay<D>::kPerSm)
           sums[blk * kRows + row] = l;
           named_bar_sync(bar, 64);
           top = fmaxf(red[row], red[kRows + row]);
-          float g = 1.f;
-          if (top > kRefresh16 && top < INFINITY) {
-            g = ex2_approx(kRefresh16 - top);
-            l *= g;
-            m += top - kRefresh16;
-          } else if (top > -INFINITY && sums[row] + sums[kRows + row] == 0.f) {
-            m += top - kRefresh16;  // (O is 0 so far)
-          }
+          const float before = sums[row] + sums[kRows + row];
+          float up = 0.f;
+          if (top > kRefresh16 && top < INFINITY)
+            up = top - kRefresh16;
+          else if (before == 0.f)
+            up = top > -INFINITY ? top - kRefresh16 : 0.f;  // (O and l are 0 so far)
+          else if (i == kThinAt && before < kThin16)
+            up = fmaxf(__log2f(before) - kRefresh16, top - 9.f);
+          const float g = before == 0.f ? 1.f : ex2_approx(-up);
+          l *= g;
+          m += up;
           // P V of the tiles before is complete: S of this tile was issued behind it
           if (i > 0 && __any_sync(kAll, g != 1.f)) {
 #pragma unroll

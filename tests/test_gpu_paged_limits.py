@@ -5,7 +5,7 @@ import pytest
 
 import paged_reference as ref
 from helpers import torch_mod
-from test_gpu_paged import attend, check, smla  # noqa: F401
+from test_gpu_paged import attend, check, i32, smla  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -37,6 +37,60 @@ def test_wide_caps_beside_rows_that_reach_them(smla, G, D, new, cap):  # noqa: F
     b.q[:, 0] *= np.float32(cap / 4)
     b.q = ref.bf16_round(b.q)
     check(b, attend(smla, b), capped(b))
+
+
+# ---------------------------------------------------------------- small weights
+
+def small_weights(smla, HK, G, new, top, rest, n, R=4):  # noqa: F811
+    """Four requests of n keys that weigh 2^rest each behind a newest block of 64 that weigh 2^top each: (the
+    old keys' share of the sum from the kernel, the right one)."""
+    torch = torch_mod()
+    D, MB = 64, n // 64 + 1
+    NB = R * MB
+    k = torch.full((NB, HK, 64, D), 0x38, dtype=torch.uint8, device="cuda")  # 1.0
+    v = k.clone()
+    table = torch.randperm(NB, device="cuda").to(torch.int32).view(R, MB)
+    v[table[:, -1].long()] = 0
+    ks = torch.full((NB, HK), rest / D * np.log(2), device="cuda")
+    ks[table[:, -1].long()] = top / D * np.log(2)
+    vs = torch.ones((NB, HK), device="cuda")
+    lens = i32([n + 64] * R)
+    out, _ = smla.paged_attention_fp8(
+        torch.ones((R * new, HK * G, D), dtype=torch.bfloat16, device="cuda"), k, v, ks, vs, table, lens,
+        i32(np.arange(R + 1) * new), 1.0, max_query_len=new, prefix_lens=lens)
+    a, b = 64.0, n * 2.0 ** (rest - top)
+    return out.double(), b / (a + b)
+
+
+@pytest.mark.parametrize("top,rest", [(0, -13.6), (0, -15.4), (0, -17), (0, -18.3), (16, 0), (100, 84.5), (-5, -21.6),
+                                      (-12, -23.4), (-40, -52.3)])
+@pytest.mark.parametrize("HK,G,new", [(80, 1, 1), (40, 12, 1), (16, 16, 20)])
+def test_small_weights_are_not_dropped(smla, HK, G, new, top, rest):  # noqa: F811
+    """A tolerance that a result without the small weights misses.  Few rows: equal weights within 2^-24 of the
+    largest on average.  Tiles of 256 rows: within 2^-25 of a sum that is kept at 2^4 or more once 512 keys are
+    in it, and at 2 here before; the rounding to f16 or two e4m3 terms 2^-7 of the value, to bf16 2^-8, the
+    logits' 2^-20 |x|."""
+    n = 8000
+    out, want = small_weights(smla, HK, G, new, top, rest, n)
+    dx = 2.0 ** -20 * max(abs(top), abs(rest))
+    steps = n * 2.0 ** -24 / 64 if G * new <= 48 else 512 * 2.0 ** -25 / 2 + n * 2.0 ** -25 / 16
+    tol = (2.0 ** -7 + 2.0 ** -8 + 2 * dx) * want + steps
+    assert tol < want / 2
+    assert (out - want).abs().max().item() <= tol
+
+
+@pytest.mark.parametrize("HK,G,new", [(80, 64, 1), (80, 1, 60)])
+@pytest.mark.parametrize("top,rest", [(-8, -25.1), (-8.9, -25.3), (-7, -24.6)])
+def test_many_small_weights_behind_a_weak_start(smla, HK, G, new, top, rest):  # noqa: F811
+    """The newest block, alone in its tile of keys, weighs 2^top x 64 (between 2^-3 and 1/2); each of the 25 000
+    keys before it less than what f16 holds beside the reference 0.  Within 2^-25 of 2^4 each, the first 512
+    within 2^-25 of 64 x 2^top."""
+    n = 25088  # the tiles have 128 keys: the newest block shares its tile with none
+    out, want = small_weights(smla, HK, G, new, top, rest, n)
+    dx = 2.0 ** -20 * max(abs(top), abs(rest))
+    tol = (2.0 ** -7 + 2.0 ** -8 + 2 * dx) * want + 512 * 2.0 ** -25 / (64 * 2.0 ** top) + n * 2.0 ** -25 / 16
+    assert tol < want / 2
+    assert (out - want).abs().max().item() <= tol
 
 
 # ---------------------------------------------------------------- failed calls
