@@ -7,7 +7,8 @@
 // call takes the new rows' scale.  A block partly filled before keeps the
 // larger of its own and the new rows' scale; where that grows, the codes of
 // its old rows become e4m3(code * old / new), exact but for codes that turn
-// subnormal.  Infinities saturate and are left out of amax; NaN is stored as
+// subnormal.  A block that another program has begun may have any scale: it
+// goes a way of its own, in which quotients and products are rounded once too.  Infinities saturate and are left out of amax; NaN is stored as
 // 0, so that no stored row can spread NaN to a query that does not see it.
 //
 // The new rows of a block are found from the batch's lengths (the tokens of a
@@ -86,6 +87,58 @@ __device__ __forceinline__ uint32_t codes_of(uint2 v, float inv) {
                 __uint_as_float(v.y << 16) * inv, __uint_as_float(v.y & 0xffff0000u) * inv);
 }
 
+// x, where `r` tells on which side of it the exact value lies that it was rounded from: that value rounded to the
+// odd one of the float32 beside it, from which a further rounding to fewer bits goes as from the value itself.
+__device__ __forceinline__ float to_odd(float x, float r) {
+  if (r == 0.f || !(fabsf(x) > 0x1p-30f && fabsf(x) < INFINITY)) return x;
+  const uint32_t b = __float_as_uint(x);
+  return __uint_as_float(((r < 0.f) != (x < 0.f) ? b - 1u : b) | 1u);
+}
+__device__ __forceinline__ float product(float x, float f) {
+  const float p = x * f;
+  return to_odd(p, fmaf(x, f, -p));
+}
+__device__ __forceinline__ float quotient(float x, float m) {
+  const float q = __fdiv_rn(x, m);
+  return q == q ? to_odd(q, fmaf(-q, m, x)) : 0.f;  // (NaN: infinity under an infinite scale)
+}
+
+// store_rows (below) in a block whose scale is no power of two, out of line and as simple as that.
+template <int D, int kGroup>
+__device__ __noinline__ void store_rows_any(const __nv_bfloat16* src, int64_t stride, int row0, int n, uint8_t* page,
+                                            float* scale, float old, int t, int bar, uint32_t* shared_max) {
+  constexpr int kThreads = 32 * kGroup;
+  auto at = [&](int i) { return __ldg(reinterpret_cast<const uint2*>(src + i / (D / 4) * stride + 4 * (i % (D / 4)))); };
+  float most = 0.f;
+  for (int i = t; i < n * (D / 4); i += kThreads) most = finite_amax(finite_amax(most, at(i).x), at(i).y);
+  uint32_t top = __reduce_max_sync(kAll, __float_as_uint(most));
+  if (kGroup == 4) {
+    if ((t & 31) == 0) shared_max[t >> 5] = top;
+    named_bar_sync(bar, 128);  // and every warp has read the old scale
+    top = max(max(shared_max[0], shared_max[1]), max(shared_max[2], shared_max[3]));
+  }
+  const float need = pow2(scale_exponent(__uint_as_float(top)));
+  const float s = fmaxf(old, need);
+  if (old < s) {
+    const float f = old * pow2(-scale_exponent(__uint_as_float(top)));
+    uint32_t* w = reinterpret_cast<uint32_t*>(page);
+    for (int i = t; i < row0 * (D / 4); i += kThreads) {
+      const uint32_t c = w[i];
+      const float2 a = e4m3x2_f32(c & 0xffffu), b = e4m3x2_f32(c >> 16);
+      w[i] = e4m3x4(product(a.x, f), product(a.y, f), product(b.x, f), product(b.y, f));
+    }
+  }
+  // x / s = (x 2^-e) / m, s = m 2^e: nothing in between leaves the range of float32
+  const float to = pow2(-min((int)(__float_as_uint(s) >> 23) - 127, 126)), m = s * to;
+  for (int i = t; i < n * (D / 4); i += kThreads) {
+    const uint2 v = make_uint2(nan_to_0(at(i).x), nan_to_0(at(i).y));
+    reinterpret_cast<uint32_t*>(page + row0 * D)[i] =
+        e4m3x4(quotient(__uint_as_float(v.x << 16) * to, m), quotient(__uint_as_float(v.x & 0xffff0000u) * to, m),
+               quotient(__uint_as_float(v.y << 16) * to, m), quotient(__uint_as_float(v.y & 0xffff0000u) * to, m));
+  }
+  if (t == 0) *scale = s;
+}
+
 // The new rows [row0, row0 + n) of one block and head, by one warp (kGroup = 1)
 // or four (kGroup = 4, thread `t` of 128).  A lane holds 4 values of a row: D / 4
 // lanes make a row, 128 / D rows an access.  Four warps hold up to 64 rows in
@@ -100,6 +153,10 @@ __device__ __forceinline__ void store_rows(const __nv_bfloat16* __restrict__ src
   constexpr int kHeld = kGroup == 4 ? kBlock / 4 / kRowsPer : 8;  // accesses
   const int lane = t & 31, warp = t >> 5, sub = lane / (D / 4), col = 4 * (lane % (D / 4));
   const float old = row0 > 0 ? *scale : 0.f;
+  if ((__float_as_uint(old) & 0x7fffffu) != 0u || old == INFINITY) {  // (the same for the group)
+    store_rows_any<D, kGroup>(src, stride, row0, n, page, scale, old, t, bar, shared_max);
+    return;
+  }
   const int first = warp * kHeld * kRowsPer;  // this warp's first row
   uint2 v[kHeld];
   // The largest magnitude's bits: as integers, and again without infinities and NaN where there are any (`special`,

@@ -5,7 +5,7 @@ import pytest
 
 import paged_reference as ref
 from helpers import torch_mod
-from test_gpu_paged import attend, check, i32, smla  # noqa: F401
+from test_gpu_paged import attend, check, i32, run_store, smla, store_inputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -91,6 +91,41 @@ def test_many_small_weights_behind_a_weak_start(smla, HK, G, new, top, rest):  #
     tol = (2.0 ** -7 + 2.0 ** -8 + 2 * dx) * want + 512 * 2.0 ** -25 / (64 * 2.0 ** top) + n * 2.0 ** -25 / 16
     assert tol < want / 2
     assert (out - want).abs().max().item() <= tol
+
+
+# ---------------------------------------------------------------- store
+
+@pytest.mark.parametrize("HK,D,ctx,new", [(2, 128, [9, 40], [1, 1]), (3, 64, [5, 60], [40, 30]), (2, 128, [33, 1], [31, 70])])
+def test_store_under_scales_that_are_no_powers_of_two(smla, HK, D, ctx, new):  # noqa: F811
+    """A block that another program has begun may have any scale: the codes of the new rows are the quotients'
+    nearest, ties to even, and those of the old rows too where the scale grows."""
+    lens, start, table, _, x, cache, scale = store_inputs(HK, D, ctx, new, 80)
+    rng = np.random.default_rng(81)
+    for i in range(2):
+        # scales around which products with the rounded reciprocal go wrong, and any others
+        scale[i][:] = rng.choice(np.array([3.0, 0.75, 7.0, 0.3, 1.1, 5.0 / 3.0], np.float32), scale[i].shape)
+        scale[i][::3] *= rng.uniform(0.5, 2.0, scale[i][::3].shape).astype(np.float32)
+        # values half-way between two codes under the scale of their block, as near as bf16 comes to them
+        half = (ref.E4M3[8:120] + ref.E4M3[9:121]) / 2
+        tie = rng.choice(half, x[i].shape) * rng.choice([-1.0, 1.0], x[i].shape)
+        for r in range(len(ctx)):
+            b = table[r, ctx[r] // 64]
+            t = slice(start[r], start[r + 1])
+            x[i][t] = ref.bf16_round(tie[t] * scale[i][b][None, :, None])
+        x[i][start[0], 0, 0] = ref.bf16_round(np.array([5000.0]))[0]  # makes one block's scale grow
+        x[i][start[1], 0, 1:4] = [np.nan, np.inf, -np.inf]
+    run_store(smla, lens, start, table, x, cache, scale)
+
+
+@pytest.mark.parametrize("old", [14447047.0 * 2 ** -24, 1.9, 0.3])
+def test_store_rescales_old_codes_to_the_nearest(smla, old):  # noqa: F811
+    """Every finite code under an odd scale that grows to a power of two: 9 x 14447047 lies just below
+    half-way between two codes, where its float32 product lies on it."""
+    lens, start = np.array([63], np.int32), np.array([0, 1], np.int32)
+    codes = np.resize(np.array([c for c in range(256) if c & 127 != 127], np.uint8), (1, 1, 64, 64))
+    cache, scale = [codes.copy(), codes.copy()], [np.full((1, 1), old, np.float32) for _ in range(2)]
+    x = [np.full((1, 1, 64), 448.0 * 2 ** e, np.float32) for e in (1, 3)]
+    run_store(smla, lens, start, np.zeros((1, 1), np.int32), x, cache, scale)
 
 
 # ---------------------------------------------------------------- failed calls
