@@ -336,6 +336,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws = tensor(a[17], "workspace");
       if (!ws.is_contiguous()) refuse("all tensors must be contiguous");
       dev.same(ws);
+      if (ws.numel() == 0) refuse("workspace: must not be empty");  // (its address, null, would ask for the library's)
     }
     check(g_attention(q.data_ptr(), stride, c.k, c.v, c.k_scale, c.v_scale, data<int32_t>(bt), lens, start, number(a[8]),
                       longest, integer(a[10], "window"), number(a[11]), slopes, prefix, doc, out.data_ptr(),

@@ -4,8 +4,8 @@ import numpy as np
 import pytest
 
 import paged_reference as ref
-from helpers import torch_mod
-from test_gpu_paged import attend, check, i32, run_store, smla, store_inputs  # noqa: F401
+from helpers import dev, torch_mod
+from test_gpu_paged import attend, bf16, check, i32, run_store, smla, store_inputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -126,6 +126,18 @@ def test_store_rescales_old_codes_to_the_nearest(smla, old):  # noqa: F811
     cache, scale = [codes.copy(), codes.copy()], [np.full((1, 1), old, np.float32) for _ in range(2)]
     x = [np.full((1, 1, 64), 448.0 * 2 ** e, np.float32) for e in (1, 3)]
     run_store(smla, lens, start, np.zeros((1, 1), np.int32), x, cache, scale)
+
+
+# ---------------------------------------------------------------- workspaces
+
+def test_an_empty_workspace_is_refused(smla):  # noqa: F811
+    """And not taken for none."""
+    torch = torch_mod()
+    b = ref.Batch(50, 2, 2, 64, [3], [2])
+    with pytest.raises(smla.SmlaError, match="workspace"):
+        smla.paged_attention_fp8(bf16(b.q), *(dev(c) for c in b.caches), *(dev(s) for s in b.scales), i32(b.table),
+                                 i32(b.lens), i32(b.query_start), 0.1,
+                                 workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
 
 
 # ---------------------------------------------------------------- failed calls
