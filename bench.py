@@ -83,6 +83,8 @@ PREFILL_FP8_TRAFFIC_BY_SOURCE = {
     # re-keyed: the quantize-and-store kernel of the same file changed; this step's kernels did not
     "a6a9548cdc5f94ae": (10_755_584 + 33_576_704 + 180_224 + 672_449_536 + 528_017_920 + 37_842_176 + 112_640,
                          "gather + up-convert, translation, attention kernel, combine"),
+    "e842d79167309662": (10_755_584 + 33_576_704 + 180_224 + 672_449_536 + 528_017_920 + 37_842_176 + 112_640,
+                         "gather + up-convert, translation, attention kernel, combine"),  # re-keyed: the same again
 }
 ABSORB_TRAFFIC_SOURCES = ("smla_absorb.cu", "sm103_ptx.cuh")
 ABSORB_TRAFFIC_BY_SOURCE = {

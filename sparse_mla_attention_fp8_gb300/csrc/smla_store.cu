@@ -48,7 +48,10 @@ __global__ void __launch_bounds__(256) quantize_store_kernel(const uint4* __rest
   const int lane = threadIdx.x & 31;
   if (token >= T) return;
   const int64_t slot = slot_mapping[token];
-  if (slot < 0 || slot >= NB * kBlock) return;  // skipped token
+  if (slot < 0 || slot >= NB * kBlock) {  // skipped token
+    grid_dependency_wait();  // a grid whose tokens are all skipped ends behind the preceding one, too
+    return;
+  }
   const uint4* src = kv_new + (int64_t)token * (kDqk * 2 / 16);  // 72 chunks of 16 bytes per row
   const uint4 a = __ldg(src + 2 * lane);
   const uint4 b = __ldg(src + 2 * lane + 1);

@@ -156,3 +156,46 @@ def test_a_wait_that_runs_out_is_reported_whatever_the_workspace(smla, many_rows
     del workspace
     assert smla.read_device_status() == 1
     assert smla.read_device_status() == 0
+
+
+# ---------------------------------------------------------------- launch order
+
+def test_calls_behind_a_store_that_skips_all(smla):  # noqa: F811
+    """A decode, a store whose tokens are all skipped, and the paged attention in the workspace that the decode
+    uses: the store ends behind the decode, so the attention begins behind it, too."""
+    import ctypes
+
+    import smla_inputs as inp
+    from helpers import bf16_dev, oracle_cache
+    torch = torch_mod()
+    case = inp.memory_bound_decode(seed=5, R=9, ctx_lo=300, ctx_hi=2500, K=200, H=16)
+    cache = dev(oracle_cache(case))
+    args = (bf16_dev(case.q), cache, dev(case.indices), dev(case.block_table), dev(case.req_id_per_token), case.sm_scale)
+    b = ref.Batch(90, 2, 4, 128, [2000, 30, 700], [1, 1, 1])
+    q, rest = bf16(b.q), [dev(x) for x in b.caches + b.scales + [b.table, b.lens, b.query_start]]
+    rows, skip = torch.zeros((9, 576), dtype=torch.bfloat16, device="cuda"), torch.full((9,), -1, device="cuda")
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    want = smla.sparse_mla_decode_fp8(*args)
+
+    def p(t):
+        return ctypes.c_void_p(t.data_ptr())
+
+    def attend_in_the_librarys_workspace():
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        rc = smla.lib().paged_attention_fp8(p(q), 8 * 128, *(p(x) for x in rest), b.sm_scale, 1, 0, 0.0, None, None, None,
+                                            p(out), p(lse), 3, 8, 2, 128, 3, b.table.shape[1], b.NB, None, 0, stream)
+        assert rc == 0, smla.lib().smla_last_error()
+        return out, lse
+
+    attend_in_the_librarys_workspace()  # (the workspace grows)
+    torch.cuda.synchronize()
+    expected = b.expected()
+    got = []
+    for _ in range(20):
+        decoded = smla.sparse_mla_decode_fp8(*args)
+        smla.mla_cache_store_fp8(rows, skip, cache)
+        got.append((decoded, attend_in_the_librarys_workspace()))
+    torch.cuda.synchronize()
+    for decoded, (out, lse) in got:
+        assert torch.equal(decoded[0], want[0]) and torch.equal(decoded[1], want[1])
+        check(b, (out.float().cpu().numpy(), lse.cpu().numpy()), expected)
