@@ -66,7 +66,7 @@ extern "C" {
  * attention kernels do; ordinary kernels do not), the decode's index translation and Q split may read
  * q, indices, block_table and req_id_per_token before it has finished.  Everything that reads kv_cache
  * or writes out, lse or the workspace waits for it.  So write those four inputs with other kernels,
- * not with a kernel of this library launched directly before the call. */
+ * not with a kernel of this library (but paged_blocks_extend) launched directly before the call. */
 int sparse_mla_decode_fp8(const void* q, const uint8_t* kv_cache, const int32_t* indices,
                           const int32_t* block_table, const int32_t* req_id_per_token, float sm_scale,
                           int num_splits, void* out, float* lse, int T, int H, int K, int R, int MB, int NB,
@@ -254,7 +254,7 @@ int sparse_mla_attention_plan(int fp8, int T, int H, int K, int num_splits, int*
  * completed, so a decode running before it still reads the old rows.  If that kernel signals its
  * dependents early (this library's decode and attention kernels do; ordinary kernels do not),
  * kv_new and slot_mapping may be read before it has finished: write those two with other kernels,
- * not with a kernel of this library launched directly before the call. */
+ * not with a kernel of this library (but paged_blocks_extend) launched directly before the call. */
 int mla_cache_store_fp8(const void* kv_new, const int64_t* slot_mapping, uint8_t* kv_cache, int T, int NB,
                         void* stream);
 
@@ -318,7 +318,9 @@ int mla_v_up_proj(const void* attn_out, const void* w_uv, void* out, int T, int 
  *                                   blocks, and where the table has no block inside [0, NB)
  *   free_count_out   int32 [1]      blocks left on the stack
  *   missing          int32 [1]      blocks that the stack did not have; their entries are -1
- * All written.  seq_lens may be context_lens or query_lens, free_count_out may be free_count. */
+ * All written.  seq_lens may be context_lens or query_lens, free_count_out may be free_count.
+ * mla_cache_store_fp8 and sparse_mla_decode_fp8 may follow directly: the kernel does not signal its
+ * dependents early, and what it writes is visible on the device before its blocks end. */
 int paged_blocks_extend(const int32_t* context_lens, const int32_t* query_lens, int32_t* block_table,
                         const int32_t* free_blocks, const int32_t* free_count, int32_t* query_start,
                         int32_t* seq_lens, int32_t* req_id_per_token, int32_t* positions, int64_t* slot_mapping,

@@ -181,6 +181,9 @@ __global__ void __launch_bounds__(kMaxThreads) blocks_extend_kernel(const __grid
         }
     }
   }
+  // The latent cache's store and decode read these results before they wait for this grid: they begin when its CTAs
+  // have ended, and by then the results are there for all.
+  __threadfence();
 }
 
 // A unit is a run of `chunk` table entries of one request; a warp counts the

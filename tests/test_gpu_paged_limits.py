@@ -199,3 +199,34 @@ def test_calls_behind_a_store_that_skips_all(smla):  # noqa: F811
     for decoded, (out, lse) in got:
         assert torch.equal(decoded[0], want[0]) and torch.equal(decoded[1], want[1])
         check(b, (out.float().cpu().numpy(), lse.cpu().numpy()), expected)
+
+
+def test_latent_store_directly_behind_the_tables(smla):  # noqa: F811
+    """Step after step into the same tables and slot map, each read by the store launched behind it."""
+    import oracle
+    torch = torch_mod()
+    rng = np.random.default_rng(91)
+    R, MB, NB, T, steps = 5, 9, 45, 400, 12
+    table = torch.full((R, MB), -1, dtype=torch.int32, device="cuda")
+    stack, ctx, count = i32(rng.permutation(NB)), i32([0] * R), i32([NB])
+
+    def e(n, t=torch.int32):
+        return torch.full((n,), -7, dtype=t, device="cuda")
+
+    out = smla.PagedBatch(e(R + 1), ctx, e(T), e(T), e(T, torch.int64), count, e(1))
+    cache = torch.zeros((NB, 64, 656), dtype=torch.uint8, device="cuda")
+    news = [rng.integers(0, 60, R) for _ in range(steps)]
+    rows = [bf16(rng.standard_normal((T, 576))) for _ in range(steps)]
+    d_news = [i32(n) for n in news]
+    torch.cuda.synchronize()
+    for new, x in zip(d_news, rows):
+        smla.paged_blocks_extend(ctx, new, table, stack, count, T, NB, out=out)
+        smla.mla_cache_store_fp8(x, out.slot_mapping, cache)
+    torch.cuda.synchronize()
+    want, w_ctx, w_count = np.zeros((NB, 64, 656), np.uint8), np.zeros(R, np.int32), NB
+    w_table = np.full((R, MB), -1, np.int32)
+    for new, x in zip(news, rows):
+        w_table, _, w_ctx, _, _, slot, w_count, _ = ref.extend(w_ctx, new, w_table, stack.cpu().numpy(), w_count, T, NB)
+        oracle.quantize_store(x.cpu().view(torch.int16).numpy().view(np.uint16), slot.astype(np.int64), want)
+    assert np.array_equal(table.cpu().numpy(), w_table) and int(count) == w_count
+    assert np.array_equal(cache.cpu().numpy(), want)
