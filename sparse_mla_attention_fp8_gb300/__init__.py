@@ -33,6 +33,7 @@ _BUILD = os.path.join(_PKG, "_build")
 LIB_PATH = os.path.join(_PKG, "libsmla.so")
 HEADER = os.path.join(_ROOT, "include", "smla.h")
 BINDING_PATH = os.path.join(_PKG, "_binding.so")
+_BINDING_STAMP = os.path.join(_BUILD, "binding.txt")  # what it was compiled against
 
 SOURCES = ["smla_decode.cu", "smla_attn.cu", "smla_wide.cu", "smla_wide8.cu", "smla_store.cu", "smla_nvfp4.cu", "smla_absorb.cu",
            "smla_blocks.cu", "smla_kvstore.cu", "smla_paged_attn.cu", "smla_paged_prefill.cu",
@@ -65,21 +66,11 @@ def _stale(obj: str, src: str) -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the CUDA sources for sm_103a (in parallel) and link libsmla.so
-    in place.  Works without a GPU (nvcc cross-compiles)."""
+    in place, and the Python binding of the paged operators where torch is
+    installed (the library itself needs nvcc alone).  Works without a GPU
+    (nvcc cross-compiles)."""
     os.makedirs(_BUILD, exist_ok=True)
     nvcc = _nvcc()
-    jobs = []
-    for s in SOURCES:
-        src = os.path.join(_CSRC, s)
-        obj = os.path.join(_BUILD, s.replace(".cu", ".o"))
-        if force or _stale(obj, src):
-            jobs.append([nvcc, *NVCC_FLAGS, "-c", src, "-o", obj])
-    objs = [os.path.join(_BUILD, s.replace(".cu", ".o")) for s in SOURCES]
-    link = force or bool(jobs) or not os.path.exists(LIB_PATH)
-    tmp_binding = BINDING_PATH + f".tmp{os.getpid()}"
-    bind = force or _stale(BINDING_PATH, os.path.join(_CSRC, "smla_binding.cpp"))
-    if bind:
-        jobs.append(_binding_command(tmp_binding))
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -88,32 +79,65 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             print(r.stdout + r.stderr)
 
-    if jobs:
-        with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-            list(ex.map(run, jobs))
-    if bind:
-        os.replace(tmp_binding, BINDING_PATH)
-    if link:
-        tmp = LIB_PATH + f".tmp{os.getpid()}"
-        run([nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", *objs, "-o", tmp])
-        os.replace(tmp, LIB_PATH)
+    def bind():
+        tmp = BINDING_PATH + f".tmp{os.getpid()}"
+        run(_binding_command(tmp))
+        os.replace(tmp, BINDING_PATH)
+        with open(_BINDING_STAMP, "w") as f:
+            f.write(stamp)
+
+    objs, jobs = [], []
+    for s in SOURCES:
+        src = os.path.join(_CSRC, s)
+        objs.append(os.path.join(_BUILD, s.replace(".cu", ".o")))
+        if force or _stale(objs[-1], src):
+            jobs.append([nvcc, *NVCC_FLAGS, "-c", src, "-o", objs[-1]])
+    stamp = _binding_stamp()
+    binds = stamp is not None and (force or _binding_stale(stamp))
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        binding = ex.submit(bind) if binds else None
+        list(ex.map(run, jobs))
+        if force or jobs or not os.path.exists(LIB_PATH):
+            tmp = LIB_PATH + f".tmp{os.getpid()}"
+            run([nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", *objs, "-o", tmp])
+            os.replace(tmp, LIB_PATH)
+        if binding is not None:
+            binding.result()  # raises what went wrong there, the library being in place
     return LIB_PATH
+
+
+def _binding_stamp():
+    """What the Python binding is compiled against; None without torch."""
+    import importlib.util
+    import sys
+    from importlib import metadata
+    if importlib.util.find_spec("torch") is None:
+        return None
+    return f"torch {metadata.version('torch')}, python {sys.version}"
+
+
+def _binding_stale(stamp: str) -> bool:
+    if _stale(BINDING_PATH, os.path.join(_CSRC, "smla_binding.cpp")) or not os.path.exists(_BINDING_STAMP):
+        return True
+    with open(_BINDING_STAMP) as f:
+        return f.read() != stamp
 
 
 def _binding_command(out: str) -> list:
     """The compiler call for the Python binding of the paged operators (host
-    code only, against the installed torch's headers)."""
+    code only, by the host compiler that nvcc finds, against the installed
+    torch's headers)."""
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
-    cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    return [_nvcc(), "-shared", "-O2", "-std=c++17", "-cudart", "none", "-Xcompiler", "-fPIC,-Wall",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
             "-I" + sysconfig.get_path("include"), "-isystem", os.path.join(root, "include"), "-isystem",
-            os.path.join(root, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+            os.path.join(root, "include", "torch", "csrc", "api", "include"),
             os.path.join(_CSRC, "smla_binding.cpp"), "-o", out, "-L" + os.path.join(root, "lib"),
-            "-Wl,-rpath," + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            "-Xlinker", "-rpath", "-Xlinker", os.path.join(root, "lib"),
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def lib():
