@@ -125,7 +125,8 @@ struct Lay {
   static_assert((kMaxPagedRequests + 1 + kWarps) * 8 <= kStages * kStage, "prefix sums fit the stages");
 };
 
-template <int D, int C>
+// kCap: may have a softcap.
+template <int D, int C, bool kCap>
 __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
     paged_attn_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap k_map,
                       const __grid_constant__ CUtensorMap v_map) {
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(qd + swz<D>(op + 8, c >> 1) + 8 * (c & 1)), "r"(l[0]),
                        "r"(l[1])
                        : "memory");
-          if (c == 0) cols->scale[row] = a.sm_scale * back * (a.softcap > 0.f ? 1.f / a.softcap : kLog2e);
+          if (c == 0) cols->scale[row] = a.sm_scale * back * (kCap && a.softcap > 0.f ? 1.f / a.softcap : kLog2e);
         }
       }
       fence_proxy_async_smem();
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(Lay<D, C>::kThreads, Lay<D, C>::kPerSm)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kSFree + buf]);
-        if (a.softcap > 0.f) {
+        if (kCap && a.softcap > 0.f) {
           // y is x / cap.  The polynomial alone where it holds for all, else each by its own size.
           const float cap = a.softcap * kLog2e;
           float most = 0.f;
@@ -732,7 +733,10 @@ cudaError_t launch(const PagedAttnArgs& a, int num_sms, cudaStream_t stream) {
   cudaError_t e = cache_maps(a, &k_map, &v_map);
   if (e != cudaSuccess) return e;
   const PagedParams p = paged_params<C>(a, paged_sizes(C, D, L::kPerSm, num_sms), kUnitCost);
-  e = launch_overlapped(paged_attn_kernel<D, C>, dim3((unsigned)p.ctas), L::kThreads, L::kSmem, stream, p, k_map, v_map);
+  // 16 rows: a kernel without the cap's code where there is none (32 requests of 5 tokens, G = 4: 76.9 us, 81.5 with
+  // it); 8 rows: one for both (64 long requests 175 us, with two of its registers spilled 178).
+  e = launch_overlapped(C == 8 || a.softcap > 0.f ? paged_attn_kernel<D, C, true> : paged_attn_kernel<D, C, C == 8>,
+                        dim3((unsigned)p.ctas), L::kThreads, L::kSmem, stream, p, k_map, v_map);
   return e == cudaSuccess ? launch_merge<D, C>(p, stream) : e;
 }
 
