@@ -310,7 +310,9 @@ int mla_v_up_proj(const void* attn_out, const void* w_uv, void* out, int T, int 
  * of requests and blocks.
  *   context_lens, query_lens int32 [R]; free_blocks int32 [F]; free_count int32 [1]
  *   block_table      int32 [R, MB]  new entries written, others left as they were
- *   query_start      int32 [R + 1]  first token of each request; the last: their number.  At most T
+ *   query_start      int32 [R + 1]  first token of each request; the last: their number.  At most T: give T at
+ *                                   least their sum, as store and attention take the rows of a request that T
+ *                                   cuts off for its last tokens
  *   seq_lens         int32 [R]      context_lens + query_lens (saturating)
  *   req_id_per_token int32 [T]      request of each token; -1 behind the last
  *   positions        int32 [T]      position in its request; 0 behind the last
@@ -362,7 +364,9 @@ int kv_cache_store_fp8(const void* k, int64_t k_stride, const void* v, int64_t v
  *   out     bf16 [T, H, D], 16-byte aligned; lse fp32 [T, H] (written for the batch's rows)
  * Token t at position p of request r sees the keys lo <= j < hi of the request:
  *   hi = min(seq_lens[r], max(p + 1, prefix_lens[r])), without prefix_lens min(seq_lens[r], p + 1):
- *        causal, but for a prefix that every token sees (prefix_lens = seq_lens: no causal mask)
+ *        causal, but for a prefix that every token sees (prefix_lens = seq_lens: no causal mask).  The prefix
+ *        is the request's, whatever its documents: with doc_start too, a token sees the keys of later documents
+ *        as far as the prefix goes, so a batch with a prefix per document passes its documents as requests
  *   lo = max(0, p - window + 1 if window > 0, doc_start[t] if given): a sliding window, and the first
  *        position of the token's document
  * with the logits x = sm_scale * q.k, then x = softcap * tanh(x / softcap) if
@@ -371,13 +375,13 @@ int kv_cache_store_fp8(const void* k, int64_t k_stride, const void* v, int64_t v
  * or beyond MB is not seen.  A token that sees no key gets out = 0 and lse = -inf.
  *   alibi_slopes fp32 [H], prefix_lens int32 [R], doc_start int32 [T]: each may be NULL
  *   max_query_len  an estimate of the most new tokens of a request, for the choice of the work split;
- *                  any value gives right results
+ *                  any value gives right results, up to the roundings below
  * MB may be at most 2^24.
  * Keys that a token does not see do not reach its result whatever their bytes
  * and scales hold, with one exception: a NaN code (which kv_cache_store_fp8
  * never writes) or a NaN or infinite scale at a position that another token of the
  * same request sees.  Sums and softmax statistics are float32.  q enters as
- * two e4m3 terms, exact but for components below 2^-10 of their row's
+ * two e4m3 terms, exact but for components below 2^-9 of their row's
  * largest, and K as stored.  With up to 48 rows (query heads per K/V head
  * times max_query_len) V enters as stored and the weights as two e4m3 terms:
  * within 2^-8 of their value, below 2^-10 of the row's largest weight in

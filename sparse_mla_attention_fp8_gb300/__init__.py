@@ -657,10 +657,12 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
                         prefix_lens=None, doc_start=None, out=None, lse=None, workspace=None, stream=None):
     """Attention of a ragged batch over the paged e4m3 caches.  q bf16 [T,H,D]
     (slices of longer rows allowed); the cache as for kv_cache_store_fp8;
-    causal, with a sliding window, capped scores, distance biases (fp32 [H]), a
-    prefix that all tokens of a request see (int32 [R]) and documents (int32
-    [T]: first position of the token's document) as asked.  max_query_len: an
-    estimate of the most new tokens of a request (default: T - R + 1).  The
+    causal, with a sliding window, capped scores (softcap 0 or from 1e-20 to
+    1e30), distance biases (fp32 [H]), a prefix that all tokens of a request
+    see, in whichever document (int32 [R]), and documents (int32 [T]: first
+    position of the token's document) as asked.  max_query_len: an estimate of
+    the most new tokens of a request (default: T - R + 1, which takes the
+    padding rows of a batch for tokens of one: give it there).  The
     workspace, if none is given, is allocated for the call; read_device_status()
     tells whether a call has failed, with either.  Returns (out bf16 [T,H,D],
     lse fp32 [T,H]); rows of no request are left as they were."""

@@ -19,8 +19,8 @@
 // may overwrite an input (release always counts across CTAs, too) the CTAs form
 // one thread-block cluster, and inputs are read before a cluster barrier and
 // written after it; extend otherwise takes as many CTAs as the tokens fill.
-// Measured, replayed from a graph: extend, 500 requests with 95 000 new tokens 8.1
-// us (1.5 MB), 8 single tokens 5.4; release, a third of 700 requests 11.5 us (0.5 MB:
+// Measured, replayed from a graph: extend, 500 requests with 90 000 new tokens 8.4
+// us (1.5 MB), 8 single tokens 5.5; release, a third of 700 requests 11.5 us (0.5 MB:
 // the table rows, then the stack, three dependent passes through memory), 3 of 8 4.1.
 #include <cstdint>
 #include <algorithm>
@@ -296,7 +296,7 @@ cudaError_t launch_blocks_extend(const BlocksExtendArgs& a, cudaStream_t stream)
                         overlap(a.free_count_out, a.free_count, 4, 4);
   if (in_place || ctas == 1) return launch_cluster(blocks_extend_kernel, a, ctas, ctas, threads, smem, stream);
   // Separate outputs: CTAs of 512 threads, one four-token item a thread, at most 64 of them (each makes the
-  // prefix sums); 95 K tokens of 500 requests take 16.5 us in one cluster
+  // prefix sums); 90 K tokens of 500 requests take 16.5 us in one cluster
   constexpr int kThreads = 512;
   ctas = (int)std::min<int64_t>(64, (work + kThreads - 1) / kThreads);
   return launch_cluster(blocks_extend_kernel, a, ctas, 1, kThreads, smem, stream);

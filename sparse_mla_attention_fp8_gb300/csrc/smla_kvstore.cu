@@ -262,8 +262,9 @@ static void launch(const KvStoreArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_store(const KvStoreArgs& a, cudaStream_t stream) {
-  // Four warps a block and head where a request brings 16 rows or more on average: one warp | four took 3.2 | 6.0 us
-  // for 64 requests of one row, 14.7 | 15.2 for 200 of 9 on average, 25 | 12 for 64 of up to 300.
+  // Four warps a block and head where a request brings 16 rows or more on average: one warp | four take 2.9 | 5.2 us
+  // for 64 requests of one row, 14.1 | 12.6 for 200 of 9 on average (38 of them of 20 to 60), 21.2 | 7.6 for 64 of 34
+  // on average (8 heads, D = 128).
   const bool many = a.T / 16 >= a.R;
   if (a.D == 128)
     many ? launch<128, 4>(a, stream) : launch<128, 1>(a, stream);

@@ -108,7 +108,7 @@ namespace {
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kTop = 8.75f;      // P = 2^(x - m') <= 2^8.75 < 430 (e4m3: 448)
+constexpr float kTop = 8.75f;      // P = 2^(x - m') <= 2^8.75 < 431 (e4m3: 448)
 constexpr float kRefresh = 4.25f;  // a refreshed m' puts the tile's maximum at 2^4.25
 constexpr float kNoMax = -3e38f;   // m' of a row that has seen nothing
 

@@ -12,8 +12,8 @@
 // table entry is outside [0, NB) are not seen.
 //
 // This kernel takes up to C rows (tokens x heads of one K/V head) per query
-// tile, C = 8 or 16: single tokens and short drafts.  Each key is read once
-// and meets few rows, so HBM bounds it, and the design keeps the codes moving
+// tile, C = 8 or 16: single tokens and short drafts.  A key is read once for up
+// to C rows (17 to 48 rows of a request are two or three tiles), so HBM bounds it, and the design keeps the codes moving
 // from HBM to the tensor cores with no instruction spent on them:
 //  * A key tile is 128 keys, two blocks; TMA copies each block's 64 x D codes
 //    of the head (contiguous in the cache) into a ring of stages.
@@ -22,7 +22,7 @@
 //    columns, which hold two e4m3 terms of each row's operand, 8 rows' first
 //    terms, then their second ones:
 //      S^T[key, row] = K Q^T, q 2^s = hi + lo (s puts the row's largest near
-//        448): exact for components down to 2^-10 of it, as q has 8
+//        448): exact for components down to 2^-9 of it, as q has 8
 //        significant bits and hi leaves at most 4;
 //      O^T[d, row] = V^T P^T, P = 2^(x - m') v_scale / R = hi + lo / 16, R the
 //        larger v_scale of the tile's two blocks: 8 significant bits where P >=
@@ -48,9 +48,9 @@
 // Measured, all launches of a call, D = 128 unless stated, shares of the copy
 // bandwidth 6.79 TB/s: 64 requests of up to 16 000 tokens, 8 K/V heads, G = 8
 // (1.14 GB) 176 us, 0.95; 3 of up to 260 000, 4 heads, G = 7, distance biases (0.56
-// GB) 95 us, 0.86; 200 of up to 500, 8 heads, G = 8 (0.13 GB) 57 us, 0.33: a segment's
+// GB) 95 us, 0.87; 200 of up to 500, 8 heads, G = 8 (0.13 GB) 54 us, 0.34: a segment's
 // start and end take what 4 of its tiles do; 100 windows of 4096, 5 tokens each, 5
-// heads, G = 3, D = 64, capped (0.23 GB) 84 us, 0.40: the chain S, softmax, P V of a
+// heads, G = 3, D = 64, capped (0.23 GB) 86 us, 0.39: the chain S, softmax, P V of a
 // 16 KB tile takes 1.7 us and one tile per CTA is in its softmax at a time.
 #include "smla_paged.cuh"
 

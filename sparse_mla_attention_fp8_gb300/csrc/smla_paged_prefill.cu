@@ -7,7 +7,7 @@
 // tensor cores bound it, with the softmax and the shared memory that feeds the
 // products close behind.  One half's softmax runs under the other's products.
 //  * S [row][key] = Q K^T on the codes as stored (kind::f8f6f4), q in two e4m3
-//    terms (exact but for components below 2^-10 of their row's largest): two
+//    terms (exact but for components below 2^-9 of their row's largest): two
 //    passes at the 8-bit rate cost what one at the 16-bit rate would, without
 //    converting K.
 //  * O += P V in f16 (kind::f16): P then needs one conversion per pair, where two
@@ -32,13 +32,13 @@
 //    warps per half, which also write the results.
 //
 // Measured, all launches of a call: three prompts of up to 2500 tokens over up
-// to 6000 cached ones, 8 K/V heads, G = 4, D = 128 (0.37 TFLOP): 399 us, 0.92 PFLOP/s,
-// 0.47 of what a bf16 matrix product reaches; alone the kernel takes 373 us (tensor
-// pipe active 44 % of it), the split of q 21, the merge 17.  A half's chain of S (512
+// to 6000 cached ones, 8 K/V heads, G = 4, D = 128 (0.37 TFLOP): 396 us, 0.93 PFLOP/s,
+// 0.48 of what a bf16 matrix product reaches; alone the kernel takes 373 us (tensor
+// pipe active 44 % of it), the split of q 21, the merge 18.  A half's chain of S (512
 // clocks), softmax (1400), P V (512) and four handovers (150 - 300 each) bounds it: S
 // and P share their tensor memory, so the next S waits for P V, and two halves
 // fill it.  Five prompts of up to 1300 tokens, G = 12, D = 64, capped, packed
-// documents: 76 us, bound by short segments (2 tiles) and by the softmax, which with
+// documents: 77 us, bound by short segments (2 tiles) and by the softmax, which with
 // cap and masks takes 4200 clocks a tile.
 #include "smla_paged.cuh"
 
