@@ -113,7 +113,12 @@ def _binding_stamp():
     from importlib import metadata
     if importlib.util.find_spec("torch") is None:
         return None
-    return f"torch {metadata.version('torch')}, python {sys.version}"
+    try:
+        version = metadata.version("torch")
+    except metadata.PackageNotFoundError:  # a source tree on the path
+        import torch
+        version = torch.__version__
+    return f"torch {version}, python {sys.version}"
 
 
 def _binding_stale(stamp: str) -> bool:

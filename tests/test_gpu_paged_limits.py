@@ -128,6 +128,17 @@ def test_store_rescales_old_codes_to_the_nearest(smla, old):  # noqa: F811
     run_store(smla, lens, start, np.zeros((1, 1), np.int32), x, cache, scale)
 
 
+@pytest.mark.parametrize("old", [np.inf, -3.0, -2.0, 1e-40, 3e38])
+@pytest.mark.parametrize("n", [1, 40])
+def test_store_into_blocks_of_odd_scales(smla, old, n):  # noqa: F811
+    """An infinite scale stays and takes codes of 0, a negative or tiny one is replaced; no NaN code is written."""
+    rng = np.random.default_rng(82)
+    cache = [ref.e4m3_encode(rng.standard_normal((2, 2, 64, 128)) * 100) for _ in range(2)]
+    scale = [np.full((2, 2), old, np.float32) for _ in range(2)]
+    x = [ref.bf16_round(rng.standard_normal((n, 2, 128))) for _ in range(2)]
+    run_store(smla, np.array([20 + n], np.int32), np.array([0, n], np.int32), np.array([[1, 0]], np.int32), x, cache, scale)
+
+
 # ---------------------------------------------------------------- workspaces
 
 def test_an_empty_workspace_is_refused(smla):  # noqa: F811
