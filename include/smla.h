@@ -403,12 +403,107 @@ int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache,
 /* Workspace bytes paged_attention_fp8 needs on the current device (0 for sizes it rejects). */
 size_t paged_attention_fp8_workspace_bytes(int T, int H, int HK, int D, int R, int max_query_len);
 
+/* ---- MXFP8 operators: what a decoder layer does around its attention, in 8 bits.
+ *
+ * A matrix [rows, K] (K a multiple of 32) is held as uint8 codes [rows, K] of
+ * float8_e4m3, 16-byte aligned, and uint8 scales [rows, K / 32]: the byte E + 127
+ * stands for the scale 2^E of 32 consecutive values of a row; value = code * 2^E.
+ * Scale rows lie a multiple of 4 bytes apart, 4-byte aligned (up to 3 bytes
+ * behind a row's end are read and count for nothing).  What quantizes takes the
+ * smallest E, E >= -100, with amax <= 448 * 2^E over the group's finite values,
+ * and codes that are value / 2^E rounded to the nearest e4m3 (ties to even);
+ * infinities saturate, a NaN becomes e4m3's NaN.
+ * Rows of activations may be slices of longer ones: their distance (stride) is
+ * given in elements, and with it every row must be aligned as the first.
+ * Every call begins behind the preceding work on `stream`: the launches may
+ * overlap its end, but read and write no memory before it has completed; and no
+ * call of these signals its dependents early.  A wait in the products that runs
+ * past its time limit is reported by smla_read_device_status(NULL, ...). */
+
+#define SMLA_BF16 0
+#define SMLA_F32 1
+
+/* codes, scales = MXFP8 of x [T, K] (x_type: SMLA_BF16 or SMLA_F32; 16-byte aligned rows). */
+int mxfp8_quantize(const void* x, int x_type, int64_t x_stride, uint8_t* codes, uint8_t* scales,
+                   int64_t scale_stride, int T, int K, void* stream);
+
+/* RMS norm behind the residual's addition, quantized:
+ *   h = bf16(x + residual)                          (h = x without residual)
+ *   y = h * (1 / sqrt(mean over K of h^2 + eps)) * weight   (float32)
+ *   x, residual   bf16 [T, K], 16-byte aligned rows; residual may be NULL
+ *   weight        weight_type [K], 16-byte aligned, or NULL (1)
+ *   codes, scales MXFP8 of y, or both NULL
+ *   normed        bf16 [T, K] = y rounded, or NULL
+ *   residual_out  bf16 [T, K] = h, or NULL; may be x or residual where that is contiguous
+ * K: a multiple of 32, at most 65536.  Sums in float32. */
+int rms_norm_mxfp8(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                   const void* weight, int weight_type, float eps, uint8_t* codes, uint8_t* scales,
+                   int64_t scale_stride, void* normed, void* residual_out, int T, int K, void* stream);
+
+/* Linear product with its epilogue: with z = x W^T + bias in float32,
+ *   y = act(z) + residual                        w [N, K], bias [N]
+ *   y = silu(z[:, 0:N]) * z[:, N:2N] + residual  SMLA_ACT_SWIGLU: w [2 N, K], bias [2 N]; rows 0 .. N - 1 are
+ *                                                the gate's, the others the up projection's
+ * act: identity, relu, silu(z) = z / (1 + e^-z), gelu (by erf), or its approximation by tanh.
+ *   x, x_scale   MXFP8 [T, K], rows of codes x_stride bytes apart (a multiple of 16)
+ *   w, w_scale   MXFP8, codes contiguous
+ *   bias         bias_type, or NULL;  residual  bf16 [T, N] or NULL
+ *   out          bf16 [T, N]; or NULL, and codes, scales = MXFP8 of y (N a multiple of 32; 4-byte aligned)
+ * out may be residual.  The products are exact and summed in float32. */
+#define SMLA_ACT_NONE 0
+#define SMLA_ACT_RELU 1
+#define SMLA_ACT_SILU 2
+#define SMLA_ACT_GELU 3
+#define SMLA_ACT_GELU_TANH 4
+#define SMLA_ACT_SWIGLU 5
+int linear_mxfp8(const uint8_t* x, int64_t x_stride, const uint8_t* x_scale, int64_t x_scale_stride,
+                 const uint8_t* w, const uint8_t* w_scale, int64_t w_scale_stride, const void* bias, int bias_type,
+                 int activation, const void* residual, int64_t residual_stride, void* out, uint8_t* codes,
+                 uint8_t* scales, int64_t scale_stride, int T, int N, int K, void* stream);
+
+/* The experts of each token from its router logits (logits_type [T, E]):
+ *   s = softmax over the E logits, or sigmoid of each
+ *   the topk experts with the largest s + bias are taken, in that order, equal ones by their index; with
+ *   num_groups > 1 only those of the topk_groups groups (of E / num_groups consecutive experts, 2 or more)
+ *   whose two largest s + bias have the largest sums, equal ones by their index
+ *   ids     int32 [T, topk]
+ *   weights fp32 [T, topk]: s of each, divided by their sum if renormalize, times scale
+ * bias (fp32 [E], finite) may be NULL.  Without bias and groups experts are ordered by their logits.  A logit
+ * of -infinity or NaN masks its expert; a token that has fewer than topk experts left gets id -1 and weight 0
+ * behind them.  E at most 512, topk at most 32 and E (with groups: those kept). */
+#define SMLA_SCORE_SOFTMAX 0
+#define SMLA_SCORE_SIGMOID 1
+int moe_route(const void* logits, int logits_type, const float* bias, int scoring, int renormalize, float scale,
+              int num_groups, int topk_groups, int32_t* ids, float* weights, int T, int E, int topk, void* stream);
+
+/* Mixture-of-experts layer of a batch of few tokens:
+ *   out[t] = residual[t] + sum over the token's experts e of W2[e] q(g_te * silu(W1[e] x_t) * (W3[e] x_t))
+ * with g_te the sum of the token's weights for e, and q the rounding to MXFP8 (groups of 32 of the F features).
+ *   x, x_scale      MXFP8 [T, K] as for linear_mxfp8
+ *   topk_ids int32, topk_weights fp32 [T, topk]; ids outside [0, E) are skipped
+ *   w13, w13_scale  MXFP8 [E, 2 F, K]: an expert's F rows of W1, then its F rows of W3
+ *   w2, w2_scale    MXFP8 [E, K, F]; all experts' scale rows are one stride apart
+ *   residual        bf16 [T, K] or NULL;  out bf16 [T, K], may be residual
+ * K and F multiples of 32; E at most 1024; topk at most 32.  The products are exact and summed in float32, over
+ * all of a token's experts.  A NaN in an expert's weights reaches the tokens of its tile that do not go to it
+ * (tiles of up to 96 tokens); weights of experts that no token of a tile goes to are not read.
+ *   workspace  at least moe_mxfp8_workspace_bytes(...) bytes, 256-byte aligned; NULL = library-cached.  Calls
+ *              that may overlap need one each */
+int moe_mxfp8(const uint8_t* x, int64_t x_stride, const uint8_t* x_scale, int64_t x_scale_stride,
+              const int32_t* topk_ids, const float* topk_weights, const uint8_t* w13, const uint8_t* w13_scale,
+              int64_t w13_scale_stride, const uint8_t* w2, const uint8_t* w2_scale, int64_t w2_scale_stride,
+              const void* residual, int64_t residual_stride, void* out, int T, int E, int topk, int K, int F,
+              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes moe_mxfp8 needs (0 for sizes it rejects). */
+size_t moe_mxfp8_workspace_bytes(int T, int E, int topk, int F);
+
 /* Reads (and clears) the device status word of a workspace after
  * synchronizing `stream`: 0 = no fault; 1 = a kernel wait ran past its time
  * limit and the kernel unwound (its outputs are not valid).  workspace NULL =
  * the library-cached workspace of the current device, and every call of
- * paged_attention_fp8 on that device since the last such read, whichever
- * workspace it had.  A workspace's status word is its first 4 bytes: what
+ * paged_attention_fp8, linear_mxfp8 and moe_mxfp8 on that device since the last
+ * such read, whichever workspace it had.  A workspace's status word is its first 4 bytes: what
  * they hold before the first call is read as it is, so zero them once. */
 int smla_read_device_status(void* workspace, int* status_out, void* stream);
 

@@ -2,8 +2,8 @@
 
 Thin Python binding of the C-ABI library ``libsmla.so`` (declared in
 ``include/smla.h``).  Every function here only marshals torch tensors into
-pointers and sizes and calls the same-named C entry point (the paged operators
-through a compiled module, csrc/smla_binding.cpp); all the work runs in the
+pointers and sizes and calls the same-named C entry point (the paged and MXFP8
+operators through a compiled module, csrc/smla_binding.cpp); all the work runs in the
 library's CUDA kernels.  There is no CPU fallback: if the library has
 not been built, or a tensor is not on a CUDA device, the call raises.
 
@@ -16,6 +16,11 @@ Entry points (see include/smla.h for layouts and semantics):
 The paged 8-bit K/V cache of layers with separate K and V heads:
   paged_blocks_extend and paged_blocks_release (block tables and slot maps
   from request lengths), kv_cache_store_fp8, paged_attention_fp8.
+What a decoder layer does around its attention, in MXFP8 (e4m3 codes with a
+power-of-two scale per 32 values):
+  mxfp8_quantize, rms_norm_mxfp8 (with the residual's addition), linear_mxfp8
+  (with bias, activation, residual), moe_route and moe_mxfp8 (mixture of
+  experts for few tokens).
 """
 from __future__ import annotations
 
@@ -37,7 +42,7 @@ _BINDING_STAMP = os.path.join(_BUILD, "binding.txt")  # what it was compiled aga
 
 SOURCES = ["smla_decode.cu", "smla_attn.cu", "smla_wide.cu", "smla_wide8.cu", "smla_store.cu", "smla_nvfp4.cu", "smla_absorb.cu",
            "smla_blocks.cu", "smla_kvstore.cu", "smla_paged_attn.cu", "smla_paged_prefill.cu",
-           "smla_api.cu"]
+           "smla_mxnorm.cu", "smla_linear.cu", "smla_moe.cu", "smla_route.cu", "smla_api.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17", "-lineinfo",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
 
@@ -66,7 +71,7 @@ def _stale(obj: str, src: str) -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile the CUDA sources for sm_103a (in parallel) and link libsmla.so
-    in place, and the Python binding of the paged operators where torch is
+    in place, and the Python binding of the paged and MXFP8 operators where torch is
     installed (the library itself needs nvcc alone).  Works without a GPU
     (nvcc cross-compiles)."""
     os.makedirs(_BUILD, exist_ok=True)
@@ -129,7 +134,7 @@ def _binding_stale(stamp: str) -> bool:
 
 
 def _binding_command(out: str) -> list:
-    """The compiler call for the Python binding of the paged operators (host
+    """The compiler call for the Python binding of the paged and MXFP8 operators (host
     code only, by the host compiler that nvcc finds, against the installed
     torch's headers)."""
     import sysconfig
@@ -207,6 +212,19 @@ def lib():
             L.paged_attention_fp8.restype = i32
             L.paged_attention_fp8_workspace_bytes.argtypes = [i32] * 6
             L.paged_attention_fp8_workspace_bytes.restype = sz
+            L.mxfp8_quantize.argtypes = [P, i32, i64, P, P, i64, i32, i32, P]
+            L.mxfp8_quantize.restype = i32
+            L.rms_norm_mxfp8.argtypes = [P, i64, P, i64, P, i32, f32, P, P, i64, P, P, i32, i32, P]
+            L.rms_norm_mxfp8.restype = i32
+            L.linear_mxfp8.argtypes = [P, i64, P, i64, P, P, i64, P, i32, i32, P, i64, P, P, P, i64, i32, i32, i32, P]
+            L.linear_mxfp8.restype = i32
+            L.moe_route.argtypes = [P, i32, P, i32, i32, f32, i32, i32, P, P, i32, i32, i32, P]
+            L.moe_route.restype = i32
+            L.moe_mxfp8.argtypes = [P, i64, P, i64, P, P, P, P, i64, P, P, i64, P, i64, P, i32, i32, i32, i32, i32, P,
+                                    sz, P]
+            L.moe_mxfp8.restype = i32
+            L.moe_mxfp8_workspace_bytes.argtypes = [i32] * 4
+            L.moe_mxfp8_workspace_bytes.restype = sz
             L.smla_paged_wait_check.argtypes = [i32, P, P]
             L.smla_paged_wait_check.restype = i32
             L.smla_read_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_int), P]
@@ -585,7 +603,7 @@ class PagedBatch(NamedTuple):
 
 
 def _bound():
-    """The compiled binding of the paged operators, on the loaded library."""
+    """The compiled binding of the paged and the MXFP8 operators, on the loaded library."""
     global _binding
     if _binding is None:
         import importlib.util
@@ -601,7 +619,8 @@ def _bound():
                 spec.loader.exec_module(module)
                 module.init(SmlaError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
                     "paged_blocks_extend", "paged_blocks_release", "kv_cache_store_fp8", "paged_attention_fp8",
-                    "paged_attention_fp8_workspace_bytes", "smla_last_error")))
+                    "paged_attention_fp8_workspace_bytes", "smla_last_error", "mxfp8_quantize", "rms_norm_mxfp8",
+                    "linear_mxfp8", "moe_route", "moe_mxfp8", "moe_mxfp8_workspace_bytes")))
                 _binding = module
     return _binding
 
@@ -677,6 +696,96 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
     return call(*args) if stream is None else _on(stream, block_table, call, *args)
 
 
+# ---- MXFP8 operators
+
+class MxNorm(NamedTuple):
+    """What rms_norm_mxfp8 makes; None for what was not asked for."""
+    codes: Any     # uint8 [T, K]
+    scales: Any    # uint8 [T, K / 32]
+    normed: Any    # bf16 [T, K]
+    residual: Any  # bf16 [T, K]
+
+
+_ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5}
+_SCORINGS = {"softmax": 0, "sigmoid": 1}
+
+
+def _choice(table: dict, name: str, what: str) -> int:
+    if name not in table:
+        raise SmlaError(f"{what}: {name!r} is none of {', '.join(table)}")
+    return table[name]
+
+
+def mxfp8_quantize(x, codes=None, scales=None, stream=None):
+    """MXFP8 of x (bf16 or float32 [T,K], slices of longer rows allowed; K a
+    multiple of 32): (codes uint8 [T,K] of float8_e4m3, scales uint8 [T,K/32],
+    the byte E + 127 for the scale 2^E of 32 values, in rows a multiple of 4
+    bytes apart).  The form in which the other MXFP8 operators take activations
+    and weights, as uint8 or viewed as float8_e4m3fn and float8_e8m0fnu."""
+    args = (x, codes, scales)
+    call = (_binding or _bound()).quantize
+    return call(*args) if stream is None else _on(stream, x, call, *args)
+
+
+def rms_norm_mxfp8(x, weight=None, eps: float = 1e-6, residual=None, normed=False, quantized: bool = True,
+                   residual_out=None, codes=None, scales=None, stream=None):
+    """RMS norm of h = x + residual (bf16 [T,K], slices of longer rows allowed)
+    with a weight (bf16 or float32 [K]), quantized from its float32 values.
+    Returns an MxNorm: codes and scales as mxfp8_quantize's (if `quantized`);
+    the norm in bf16, if `normed` is True or a tensor for it; and h rounded to
+    bf16, if a residual is given (in `residual_out`, which may be the residual
+    itself, or a new tensor)."""
+    args = (x, weight, eps, residual, normed, quantized, residual_out, codes, scales)
+    call = (_binding or _bound()).norm
+    return MxNorm._make(call(*args) if stream is None else _on(stream, x, call, *args))
+
+
+def linear_mxfp8(x, x_scale, weight, weight_scale, bias=None, activation: str = "none", residual=None,
+                 quantized: bool = False, out=None, out_scale=None, stream=None):
+    """y = act(x W^T + bias) + residual on MXFP8 operands: x [T,K] (slices of
+    longer rows allowed), weight [N,K], bias bf16 or float32 [N], residual bf16
+    [T,N].  activation: "none", "relu", "silu", "gelu", "gelu_tanh", or "swiglu":
+    silu(first half) * second half of a product with 2 N rows.  Returns y in bf16
+    [T,N], or, if `quantized` (N a multiple of 32, no residual), its codes and
+    scales as mxfp8_quantize's.  out may be the residual."""
+    args = (x, x_scale, weight, weight_scale, bias, _choice(_ACTIVATIONS, activation, "activation"), residual, quantized,
+            out, out_scale)
+    call = (_binding or _bound()).linear
+    return call(*args) if stream is None else _on(stream, x, call, *args)
+
+
+def moe_route(logits, topk: int, scoring: str = "softmax", bias=None, renormalize: bool = True, scale: float = 1.0,
+              num_groups: int = 1, topk_groups: int = 1, ids=None, weights=None, stream=None):
+    """The topk experts of each token from its router logits (bf16 or float32
+    [T,E]): the largest scores ("softmax" over the logits, or "sigmoid" of each)
+    plus bias (fp32 [E]), with num_groups > 1 among the topk_groups groups of
+    experts whose two largest have the largest sums; ties go to the lowest index.
+    Returns (ids int32 [T,topk], weights fp32 [T,topk]: the scores, divided by
+    their sum if `renormalize`, times scale).  Logits of -infinity mask an
+    expert; where too few are left, id -1 with weight 0."""
+    args = (logits, topk, _choice(_SCORINGS, scoring, "scoring"), bias, renormalize, scale, num_groups, topk_groups, ids,
+            weights)
+    call = (_binding or _bound()).route
+    return call(*args) if stream is None else _on(stream, logits, call, *args)
+
+
+def moe_mxfp8_workspace_bytes(T: int, E: int, topk: int, F: int) -> int:
+    return int(lib().moe_mxfp8_workspace_bytes(T, E, topk, F))
+
+
+def moe_mxfp8(x, x_scale, topk_ids, topk_weights, w13, w13_scale, w2, w2_scale, residual=None, out=None,
+              workspace=None, stream=None):
+    """Mixture-of-experts layer of a batch of few tokens: each token's experts
+    (int32 [T,topk], ids outside [0,E) skipped) with their weights (fp32
+    [T,topk]); w13 [E,2F,K]: an expert's gate and up projections, w2 [E,K,F], all
+    MXFP8.  The weighted silu(gate) * up is rounded to MXFP8 between the
+    products.  Returns bf16 [T,K], with the residual (bf16 [T,K]) added if given;
+    out may be the residual."""
+    args = (x, x_scale, topk_ids, topk_weights, w13, w13_scale, w2, w2_scale, residual, out, workspace)
+    call = (_binding or _bound()).moe
+    return call(*args) if stream is None else _on(stream, x, call, *args)
+
+
 def read_noalloc_status(stream=None) -> int:
     """Synchronize and read/clear the status word of the allocation-free
     decode's fixed scratch on the current device (0 = ok)."""
@@ -703,8 +812,8 @@ def paged_wait_check(workspace, many_rows: bool = False, stream=None) -> None:
 def read_device_status(workspace=None, stream=None) -> int:
     """Synchronize and read/clear the kernels' device status word (0 = ok).
     Without a workspace: that of the library's own workspace on the current
-    device, and whether a paged_attention_fp8 call on it has failed, whichever
-    workspace it had."""
+    device, and whether a paged_attention_fp8, linear_mxfp8 or moe_mxfp8 call on
+    it has failed, whichever workspace it had."""
     import torch
     st = ctypes.c_int(0)
     dev = workspace.device if workspace is not None else torch.device("cuda", torch.cuda.current_device())

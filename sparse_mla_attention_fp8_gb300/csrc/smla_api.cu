@@ -599,8 +599,9 @@ int take_status(void* word, int* out) {
 
 int smla_read_device_status(void* workspace, int* status_out, void* stream) {
   if (!status_out) return fail(SMLA_ERR_INVALID_ARG, "null status_out");
-  // without a workspace: the library-cached one, and what the paged attention's calls report for the device
-  void* words[3] = {workspace, nullptr, nullptr};
+  // without a workspace: the library-cached one, and what the paged attention's and the MXFP8 products' calls
+  // report for the device
+  void* words[5] = {workspace, nullptr, nullptr, nullptr, nullptr};
   if (!workspace) {
     int dev;
     int rc = current_device(&dev);
@@ -609,12 +610,13 @@ int smla_read_device_status(void* workspace, int* status_out, void* stream) {
       std::lock_guard<std::mutex> lk(g_mu);
       words[0] = g_dev[dev].ws;
     }
-    int* paged[2] = {nullptr, nullptr};
-    cudaError_t e = smla::paged_attn_timed_out(&paged[0]);
-    if (e == cudaSuccess) e = smla::paged_prefill_timed_out(&paged[1]);
+    int* reported[4] = {nullptr, nullptr, nullptr, nullptr};
+    cudaError_t e = smla::paged_attn_timed_out(&reported[0]);
+    if (e == cudaSuccess) e = smla::paged_prefill_timed_out(&reported[1]);
+    if (e == cudaSuccess) e = smla::mx_linear_timed_out(&reported[2]);
+    if (e == cudaSuccess) e = smla::moe_timed_out(&reported[3]);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetSymbolAddress(status)");
-    words[1] = paged[0];
-    words[2] = paged[1];
+    for (int i = 0; i < 4; ++i) words[1 + i] = reported[i];
   }
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
@@ -853,6 +855,249 @@ int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache,
   a.NB = NB;
   cudaError_t e = smla::launch_paged_attention(a, max_query_len, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention_fp8 launch");
+  return SMLA_OK;
+}
+
+// ---- MXFP8 operators
+
+namespace {
+int check_type(const char* name, int type) {
+  if (type != SMLA_BF16 && type != SMLA_F32)
+    return fail(SMLA_ERR_INVALID_ARG, "%s: %d is no type (SMLA_BF16 or SMLA_F32)", name, type);
+  return SMLA_OK;
+}
+int check_groups(const char* name, int v) {
+  if (v <= 0 || v % 32 != 0) return fail(SMLA_ERR_INVALID_ARG, "%s=%d must be a positive multiple of 32", name, v);
+  return SMLA_OK;
+}
+// Rows of `least` elements, 16-byte aligned, `size` bytes an element.
+int check_aligned_rows(const char* name, const void* p, int64_t stride, int64_t least, int size) {
+  if (!p) return fail(SMLA_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (!aligned16(p) || stride * size % 16 != 0)
+    return fail(SMLA_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", name);
+  if (stride < least)
+    return fail(SMLA_ERR_INVALID_ARG, "%s: stride %lld must be at least %lld", name, (long long)stride, (long long)least);
+  return SMLA_OK;
+}
+int check_scales(const char* name, const void* p, int64_t stride, int64_t K) {
+  if (!p) return fail(SMLA_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0 || stride % 4 != 0 || stride < (K / 32 + 3) / 4 * 4)
+    return fail(SMLA_ERR_INVALID_ARG, "%s: rows must be 4-byte aligned, and their distance %lld at least %lld", name,
+                (long long)stride, (long long)((K / 32 + 3) / 4 * 4));
+  return SMLA_OK;
+}
+int check_codes(const char* name, const void* p) {
+  if (!p) return fail(SMLA_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (!aligned16(p)) return fail(SMLA_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  return SMLA_OK;
+}
+// bf16 [T, N], element-aligned.
+int check_bf16(const char* name, const void* p, int64_t stride, int64_t least) {
+  if ((reinterpret_cast<uintptr_t>(p) & 1u) != 0 || stride < least)
+    return fail(SMLA_ERR_INVALID_ARG, "%s: misaligned, or its stride %lld less than %lld", name, (long long)stride,
+                (long long)least);
+  return SMLA_OK;
+}
+}  // namespace
+
+int mxfp8_quantize(const void* x, int x_type, int64_t x_stride, uint8_t* codes, uint8_t* scales,
+                   int64_t scale_stride, int T, int K, void* stream) {
+  if (T < 0) return fail(SMLA_ERR_INVALID_ARG, "bad size T=%d", T);
+  int rc = check_groups("K", K);
+  if (rc == SMLA_OK) rc = check_type("x_type", x_type);
+  if (rc != SMLA_OK || T == 0) return rc;
+  rc = check_aligned_rows("x", x, x_stride, K, x_type == SMLA_F32 ? 4 : 2);
+  if (rc == SMLA_OK) rc = check_codes("codes", codes);
+  if (rc == SMLA_OK) rc = check_scales("scales", scales, scale_stride, K);
+  if (rc != SMLA_OK) return rc;
+  const smla::MxQuantizeArgs a{x, x_stride, x_type == SMLA_F32, codes, scales, scale_stride, T, K};
+  cudaError_t e = smla::launch_mx_quantize(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mxfp8_quantize launch");
+  return SMLA_OK;
+}
+
+int rms_norm_mxfp8(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                   const void* weight, int weight_type, float eps, uint8_t* codes, uint8_t* scales,
+                   int64_t scale_stride, void* normed, void* residual_out, int T, int K, void* stream) {
+  if (T < 0) return fail(SMLA_ERR_INVALID_ARG, "bad size T=%d", T);
+  int rc = check_groups("K", K);
+  if (rc == SMLA_OK) rc = check_type("weight_type", weight_type);
+  if (rc != SMLA_OK) return rc;
+  if (K > smla::kMaxNormK) return fail(SMLA_ERR_UNSUPPORTED, "K=%d unsupported: at most %d", K, smla::kMaxNormK);
+  if (!(eps >= 0.f)) return fail(SMLA_ERR_INVALID_ARG, "eps=%g must not be negative", eps);
+  if (!codes != !scales) return fail(SMLA_ERR_INVALID_ARG, "codes and scales must be given together");
+  if (T == 0) return SMLA_OK;
+  rc = check_aligned_rows("x", x, x_stride, K, 2);
+  if (rc == SMLA_OK && residual) rc = check_aligned_rows("residual", residual, residual_stride, K, 2);
+  if (rc == SMLA_OK && codes) rc = check_codes("codes", codes);
+  if (rc == SMLA_OK && codes) rc = check_scales("scales", scales, scale_stride, K);
+  if (rc != SMLA_OK) return rc;
+  if (!aligned16(weight) || !aligned16(normed) || !aligned16(residual_out))
+    return fail(SMLA_ERR_INVALID_ARG, "weight, normed and residual_out must be 16-byte aligned");
+  if (!codes && !normed && !residual_out) return fail(SMLA_ERR_INVALID_ARG, "no output is asked for");
+  const smla::MxNormArgs a{x,     x_stride, residual,     residual_stride, weight, weight_type == SMLA_F32, eps, codes,
+                           scales, scale_stride, normed, residual_out,    T,      K};
+  cudaError_t e = smla::launch_mx_norm(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rms_norm_mxfp8 launch");
+  return SMLA_OK;
+}
+
+int linear_mxfp8(const uint8_t* x, int64_t x_stride, const uint8_t* x_scale, int64_t x_scale_stride,
+                 const uint8_t* w, const uint8_t* w_scale, int64_t w_scale_stride, const void* bias, int bias_type,
+                 int activation, const void* residual, int64_t residual_stride, void* out, uint8_t* codes,
+                 uint8_t* scales, int64_t scale_stride, int T, int N, int K, void* stream) {
+  if (T < 0 || N <= 0) return fail(SMLA_ERR_INVALID_ARG, "bad sizes T=%d N=%d", T, N);
+  int rc = check_groups("K", K);
+  if (rc == SMLA_OK) rc = check_type("bias_type", bias_type);
+  if (rc != SMLA_OK) return rc;
+  if (activation < SMLA_ACT_NONE || activation > SMLA_ACT_SWIGLU)
+    return fail(SMLA_ERR_INVALID_ARG, "activation %d is none of SMLA_ACT_*", activation);
+  if (out && (codes || scales)) return fail(SMLA_ERR_INVALID_ARG, "out, or codes and scales: not both");
+  if (!out && N % 32 != 0) return fail(SMLA_ERR_INVALID_ARG, "N=%d must be a multiple of 32 for MXFP8 results", N);
+  if (!out && residual) return fail(SMLA_ERR_UNSUPPORTED, "a residual with MXFP8 results is unsupported");
+  if (N > INT32_MAX / 2 - 128) return fail(SMLA_ERR_UNSUPPORTED, "N=%d unsupported", N);
+  if (T == 0) return SMLA_OK;
+  rc = check_aligned_rows("x", x, x_stride, K, 1);
+  if (rc == SMLA_OK) rc = check_scales("x_scale", x_scale, x_scale_stride, K);
+  if (rc == SMLA_OK) rc = check_codes("w", w);
+  if (rc == SMLA_OK) rc = check_scales("w_scale", w_scale, w_scale_stride, K);
+  if (rc == SMLA_OK && !out && (reinterpret_cast<uintptr_t>(codes) & 3u) != 0)
+    rc = fail(SMLA_ERR_INVALID_ARG, "codes must be 4-byte aligned");
+  if (rc == SMLA_OK && !out && !codes) rc = fail(SMLA_ERR_INVALID_ARG, "out: null pointer argument");
+  if (rc == SMLA_OK && !out) rc = check_scales("scales", scales, scale_stride, N);
+  if (rc == SMLA_OK && out) rc = check_bf16("out", out, N, N);
+  if (rc == SMLA_OK && residual) rc = check_bf16("residual", residual, residual_stride, N);
+  if (rc == SMLA_OK && bias && (reinterpret_cast<uintptr_t>(bias) & (bias_type == SMLA_F32 ? 3u : 1u)) != 0)
+    rc = fail(SMLA_ERR_INVALID_ARG, "bias is misaligned");
+  int sms = 0;
+  if (rc == SMLA_OK) rc = num_sms(&sms);
+  if (rc != SMLA_OK) return rc;
+  smla::MxLinearArgs a{};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.x_scale = x_scale;
+  a.x_scale_stride = x_scale_stride;
+  a.w = w;
+  a.w_scale = w_scale;
+  a.w_scale_stride = w_scale_stride;
+  a.to.bias = bias;
+  a.to.bias_f32 = bias_type == SMLA_F32;
+  a.to.activation = activation;
+  a.to.residual = residual;
+  a.to.residual_stride = residual_stride;
+  a.to.out = out;
+  a.to.codes = codes;
+  a.to.scales = scales;
+  a.to.scale_stride = scale_stride;
+  a.T = T;
+  a.N = N;
+  a.K = K;
+  cudaError_t e = smla::launch_mx_linear(a, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "linear_mxfp8 launch");
+  return SMLA_OK;
+}
+
+int moe_route(const void* logits, int logits_type, const float* bias, int scoring, int renormalize, float scale,
+              int num_groups, int topk_groups, int32_t* ids, float* weights, int T, int E, int topk, void* stream) {
+  if (T < 0 || E <= 0 || topk <= 0 || num_groups <= 0 || topk_groups <= 0)
+    return fail(SMLA_ERR_INVALID_ARG, "bad sizes T=%d E=%d topk=%d num_groups=%d topk_groups=%d", T, E, topk, num_groups,
+                topk_groups);
+  const int rc = check_type("logits_type", logits_type);
+  if (rc != SMLA_OK) return rc;
+  if (scoring != SMLA_SCORE_SOFTMAX && scoring != SMLA_SCORE_SIGMOID)
+    return fail(SMLA_ERR_INVALID_ARG, "scoring %d is none of SMLA_SCORE_*", scoring);
+  if (E > smla::kMaxRouteExperts || topk > smla::kMaxTopk)
+    return fail(SMLA_ERR_UNSUPPORTED, "E=%d, topk=%d unsupported: at most %d and %d", E, topk, smla::kMaxRouteExperts,
+                smla::kMaxTopk);
+  if (topk_groups > num_groups || (num_groups > 1 && (num_groups > 32 || E % num_groups != 0 || E / num_groups < 2)))
+    return fail(SMLA_ERR_INVALID_ARG, "E=%d in %d groups, %d kept: at most 32 groups, of equal sizes from 2 on", E,
+                num_groups, topk_groups);
+  if (topk > E / num_groups * topk_groups)
+    return fail(SMLA_ERR_INVALID_ARG, "topk=%d of %d experts", topk, E / num_groups * topk_groups);
+  if (T == 0) return SMLA_OK;
+  if (!logits || !ids || !weights) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+  const smla::MoeRouteArgs a{logits,     logits_type == SMLA_F32, bias, scoring == SMLA_SCORE_SIGMOID, renormalize != 0, scale,
+                             num_groups, topk_groups,             ids,  weights,                       T,                E,
+                             topk};
+  cudaError_t e = smla::launch_moe_route(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "moe_route launch");
+  return SMLA_OK;
+}
+
+namespace {
+int check_moe(int T, int E, int topk, int F) {
+  if (T < 0 || E <= 0 || topk <= 0) return fail(SMLA_ERR_INVALID_ARG, "bad sizes T=%d E=%d topk=%d", T, E, topk);
+  const int rc = check_groups("F", F);
+  if (rc != SMLA_OK) return rc;
+  if (E > 1024 || topk > smla::kMaxTopk)
+    return fail(SMLA_ERR_UNSUPPORTED, "E=%d, topk=%d unsupported: at most 1024 and %d", E, topk, smla::kMaxTopk);
+  return SMLA_OK;
+}
+}  // namespace
+
+size_t moe_mxfp8_workspace_bytes(int T, int E, int topk, int F) {
+  return check_moe(T, E, topk, F) == SMLA_OK ? smla::moe_workspace(T, E, topk, F) : 0;
+}
+
+int moe_mxfp8(const uint8_t* x, int64_t x_stride, const uint8_t* x_scale, int64_t x_scale_stride,
+              const int32_t* topk_ids, const float* topk_weights, const uint8_t* w13, const uint8_t* w13_scale,
+              int64_t w13_scale_stride, const uint8_t* w2, const uint8_t* w2_scale, int64_t w2_scale_stride,
+              const void* residual, int64_t residual_stride, void* out, int T, int E, int topk, int K, int F,
+              void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_moe(T, E, topk, F);
+  if (rc == SMLA_OK) rc = check_groups("K", K);
+  if (rc != SMLA_OK) return rc;
+  if ((int64_t)E * (K + 128) > INT32_MAX || (int64_t)E * 2 * (F + 128) > INT32_MAX)
+    return fail(SMLA_ERR_UNSUPPORTED, "E=%d times K=%d or 2 F=%d rows must fit in int32", E, K, 2 * F);
+  if (T == 0) return SMLA_OK;
+  if (!topk_ids || !topk_weights) return fail(SMLA_ERR_INVALID_ARG, "null pointer argument");
+  rc = check_aligned_rows("x", x, x_stride, K, 1);
+  if (rc == SMLA_OK) rc = check_scales("x_scale", x_scale, x_scale_stride, K);
+  if (rc == SMLA_OK) rc = check_codes("w13", w13);
+  if (rc == SMLA_OK) rc = check_scales("w13_scale", w13_scale, w13_scale_stride, K);
+  if (rc == SMLA_OK) rc = check_codes("w2", w2);
+  if (rc == SMLA_OK) rc = check_scales("w2_scale", w2_scale, w2_scale_stride, F);
+  if (rc == SMLA_OK && !out) rc = fail(SMLA_ERR_INVALID_ARG, "out: null pointer argument");
+  if (rc == SMLA_OK) rc = check_bf16("out", out, K, K);
+  if (rc == SMLA_OK && residual) rc = check_bf16("residual", residual, residual_stride, K);
+  if (rc != SMLA_OK) return rc;
+  const size_t need = smla::moe_workspace(T, E, topk, F);
+  if (workspace) {
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+      return fail(SMLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (workspace_bytes < need)
+      return fail(SMLA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+  } else {
+    rc = cached_workspace(need, &workspace);
+    if (rc != SMLA_OK) return rc;
+  }
+  int sms = 0;
+  rc = num_sms(&sms);
+  if (rc != SMLA_OK) return rc;
+  smla::MoeArgs a{};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.x_scale = x_scale;
+  a.x_scale_stride = x_scale_stride;
+  a.ids = topk_ids;
+  a.weights = topk_weights;
+  a.w13 = w13;
+  a.w13_scale = w13_scale;
+  a.w13_scale_stride = w13_scale_stride;
+  a.w2 = w2;
+  a.w2_scale = w2_scale;
+  a.w2_scale_stride = w2_scale_stride;
+  a.residual = residual;
+  a.residual_stride = residual_stride;
+  a.out = out;
+  a.workspace = workspace;
+  a.T = T;
+  a.E = E;
+  a.topk = topk;
+  a.K = K;
+  a.F = F;
+  cudaError_t e = smla::launch_moe(a, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "moe_mxfp8 launch");
   return SMLA_OK;
 }
 

@@ -1,4 +1,4 @@
-// Python entry to the paged K/V cache operators: checks the tensors' device,
+// Python entry to the paged K/V cache and the MXFP8 operators: checks the tensors' device,
 // type, shape and strides, allocates what the caller did not give, and calls
 // the C entry points (whose addresses the package passes to init).  Single-token
 // steps are bound by the host, and this takes a third to a half of what the same
@@ -27,6 +27,12 @@ decltype(&kv_cache_store_fp8) g_store;
 decltype(&paged_attention_fp8) g_attention;
 decltype(&paged_attention_fp8_workspace_bytes) g_workspace_bytes;
 decltype(&smla_last_error) g_last_error;
+decltype(&mxfp8_quantize) g_quantize;
+decltype(&rms_norm_mxfp8) g_norm;
+decltype(&linear_mxfp8) g_linear;
+decltype(&moe_route) g_route;
+decltype(&moe_mxfp8) g_moe;
+decltype(&moe_mxfp8_workspace_bytes) g_moe_workspace_bytes;
 PyObject* g_error;
 
 // Thrown once the Python error is set.
@@ -347,14 +353,289 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ---- MXFP8 operators
+
+// A matrix [rows, K] whose rows may be slices of longer ones; their distance in elements.
+struct Matrix {
+  const at::Tensor* t;
+  int rows, K;
+  int64_t stride;
+};
+Matrix matrix(PyObject* o, const char* name, Device& dev) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.dim() != 2) {
+    char is[128];
+    print_shape(is, sizeof(is), t.sizes());
+    refuse("%s: shape %s, expected (rows, K)", name, is);
+  }
+  dev.same(t);
+  const int rows = size(t.size(0), name), K = size(t.size(1), name);
+  if (rows > 0 && K > 1 && t.stride(1) != 1) refuse("%s: the values of a row must be contiguous", name);
+  return {&t, rows, K, rows > 1 ? t.stride(0) : (K + 15) / 16 * 16};
+}
+Matrix matrix_of(PyObject* o, const char* name, at::ScalarType type, int rows, int K, Device& dev) {
+  const at::Tensor& t = tensor(o, name);
+  check_type(t, type, name);
+  check_shape(t, {2, {rows, K}}, name);
+  return matrix(o, name, dev);
+}
+
+// Codes as bytes or as e4m3 values, scales as bytes or as e8m0 values.
+void check_code_type(const at::Tensor& t, const char* name) {
+  if (t.scalar_type() != at::kByte && t.scalar_type() != at::kFloat8_e4m3fn)
+    refuse("%s: dtype %s, expected uint8 or float8_e4m3fn", name, c10::toString(t.scalar_type()));
+}
+Matrix code_rows(PyObject* o, const char* name, Device& dev) {
+  check_code_type(tensor(o, name), name);
+  return matrix(o, name, dev);
+}
+uint8_t* codes(PyObject* o, const char* name, const Shape& shape, Device& dev) {
+  const at::Tensor& t = tensor(o, name);
+  check_code_type(t, name);
+  return static_cast<uint8_t*>(arg(o, name, t.scalar_type(), shape, dev).data_ptr());
+}
+struct Scales {
+  uint8_t* p;
+  int64_t stride;
+};
+// [rows, K / 32], or [E, rows / E, K / 32] with all rows one distance apart.
+Scales scales(PyObject* o, const char* name, int64_t E, int64_t rows, int64_t K, Device& dev) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.scalar_type() != at::kByte && t.scalar_type() != at::kFloat8_e8m0fnu)
+    refuse("%s: dtype %s, expected uint8 or float8_e8m0fnu", name, c10::toString(t.scalar_type()));
+  const int64_t n = K / 32;
+  check_shape(t, E ? Shape{3, {E, rows, n}} : Shape{2, {rows, n}}, name);
+  dev.same(t);
+  const int d = E ? 1 : 0;
+  const int64_t padded = (n + 3) / 4 * 4, stride = rows > 1 ? t.stride(d) : E > 1 ? t.stride(0) : padded;
+  if (rows > 0 && n > 1 && t.stride(d + 1) != 1) refuse("%s: the scales of a row must be contiguous", name);
+  if (E > 1 && rows > 1 && t.stride(0) != rows * stride) refuse("%s: all rows must be one distance apart", name);
+  return {static_cast<uint8_t*>(t.data_ptr()), stride};
+}
+at::Tensor made_scales(int64_t rows, int64_t K, const Device& dev) {
+  const int64_t n = K / 32, padded = (n + 3) / 4 * 4;
+  const at::Tensor t = made({rows, padded}, at::kByte, dev);
+  return padded == n ? t : t.narrow(1, 0, n);
+}
+// Where quantized results go: what the caller gave, or new tensors.
+struct Quantized {
+  at::Tensor codes, scales;
+  uint8_t *c, *s;
+  int64_t stride;
+};
+Quantized quantized(PyObject* c, PyObject* s, const char* cname, const char* sname, int rows, int K, Device& dev) {
+  if (K <= 0 || K % 32 != 0) refuse("%d values a row: must be a positive multiple of 32", K);
+  Quantized q;
+  if (c == Py_None) {
+    q.codes = made({rows, K}, at::kByte, dev);
+    q.c = data<uint8_t>(q.codes);
+  } else {
+    q.c = codes(c, cname, {2, {rows, K}}, dev);
+    q.codes = THPVariable_Unpack(c);
+  }
+  q.scales = s == Py_None ? made_scales(rows, K, dev) : tensor(s, sname);
+  if (s == Py_None) {
+    q.s = data<uint8_t>(q.scales);
+    q.stride = (K / 32 + 3) / 4 * 4;
+  } else {
+    const Scales given = scales(s, sname, 0, rows, K, dev);
+    q.s = given.p;
+    q.stride = given.stride;
+  }
+  return q;
+}
+// bf16 or float32
+int float_type(const at::Tensor& t, const char* name) {
+  if (t.scalar_type() == at::kBFloat16) return SMLA_BF16;
+  if (t.scalar_type() == at::kFloat) return SMLA_F32;
+  refuse("%s: dtype %s, expected bfloat16 or float32", name, c10::toString(t.scalar_type()));
+}
+void* stream_of(const Device& dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream(); }
+
+// (x, codes or None, scales or None)
+PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n, 3);
+    Device dev;
+    const Matrix x = matrix(a[0], "x", dev);
+    const int type = float_type(*x.t, "x");
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index);
+    const Quantized q = quantized(a[1], a[2], "codes", "scales", x.rows, x.K, dev);
+    check(g_quantize(x.t->data_ptr(), type, x.stride, q.c, q.s, q.stride, x.rows, x.K, stream_of(dev)), "mxfp8_quantize");
+    return pack({q.codes, q.scales});
+  });
+}
+
+// What the caller gave or, for True, a new bf16 [T, K]; undefined for None and False.
+at::Tensor wanted(PyObject* o, const char* name, int T, int K, Device& dev) {
+  if (o == Py_None || o == Py_False) return {};
+  return o == Py_True ? made({T, K}, at::kBFloat16, dev) : arg(o, name, at::kBFloat16, {2, {T, K}}, dev);
+}
+PyObject* or_none(const at::Tensor& t) {
+  if (t.defined()) {
+    PyObject* o = THPVariable_Wrap(t);
+    if (!o) throw Refused();
+    return o;
+  }
+  Py_RETURN_NONE;
+}
+
+// (x, weight or None, eps, residual or None, normed, quantized, residual_out or None, codes or None, scales or None)
+PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n, 9);
+    Device dev;
+    const Matrix x = matrix(a[0], "x", dev);
+    check_type(*x.t, at::kBFloat16, "x");
+    const int T = x.rows, K = x.K;
+    const void* weight = nullptr;
+    int type = SMLA_BF16;
+    if (a[1] != Py_None) {
+      const at::Tensor& w = tensor(a[1], "weight");
+      type = float_type(w, "weight");
+      weight = arg(a[1], "weight", w.scalar_type(), {1, {K}}, dev).data_ptr();
+    }
+    Matrix res{};
+    if (a[3] != Py_None) res = matrix_of(a[3], "residual", at::kBFloat16, T, K, dev);
+    const bool codes_too = PyObject_IsTrue(a[5]) == 1;
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index);
+    Quantized q{};
+    if (codes_too) q = quantized(a[7], a[8], "codes", "scales", T, K, dev);
+    const at::Tensor normed = wanted(a[4], "normed", T, K, dev);
+    const at::Tensor h = wanted(a[6] == Py_None && res.t ? Py_True : a[6], "residual_out", T, K, dev);
+    check(g_norm(x.t->data_ptr(), x.stride, res.t ? res.t->data_ptr() : nullptr, res.stride, weight, type, number(a[2]), q.c,
+                 q.s, q.stride, normed.defined() ? normed.data_ptr() : nullptr, h.defined() ? h.data_ptr() : nullptr, T, K,
+                 stream_of(dev)),
+          "rms_norm_mxfp8");
+    PyObject* r = PyTuple_New(4);
+    if (!r) throw Refused();
+    const at::Tensor* all[4] = {&q.codes, &q.scales, &normed, &h};
+    for (int i = 0; i < 4; ++i) {
+      try {
+        PyTuple_SET_ITEM(r, i, or_none(*all[i]));
+      } catch (...) {
+        Py_DECREF(r);
+        throw;
+      }
+    }
+    return r;
+  });
+}
+
+// (x, x_scale, weight, weight_scale, bias or None, activation, residual or None, quantized, out or None, out_scale or None)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n, 10);
+    Device dev;
+    const Matrix x = code_rows(a[0], "x", dev);
+    const int T = x.rows, K = x.K, act = integer(a[5], "activation");
+    const Scales xs = scales(a[1], "x_scale", 0, T, K, dev);
+    const Matrix w = code_rows(a[2], "weight", dev);
+    if (w.K != K) refuse("weight: shape (%d, %d), expected (N, %d)", w.rows, w.K, K);
+    if (!w.t->is_contiguous()) refuse("all tensors must be contiguous");
+    if (act == SMLA_ACT_SWIGLU && w.rows % 2 != 0) refuse("weight: %d rows, which must be even for swiglu", w.rows);
+    const int N = act == SMLA_ACT_SWIGLU ? w.rows / 2 : w.rows;
+    const Scales ws = scales(a[3], "weight_scale", 0, w.rows, K, dev);
+    const void* bias = nullptr;
+    int type = SMLA_BF16;
+    if (a[4] != Py_None) {
+      const at::Tensor& b = tensor(a[4], "bias");
+      type = float_type(b, "bias");
+      bias = arg(a[4], "bias", b.scalar_type(), {1, {w.rows}}, dev).data_ptr();
+    }
+    Matrix res{};
+    if (a[6] != Py_None) {
+      res = matrix_of(a[6], "residual", at::kBFloat16, T, N, dev);
+      if (T <= 1) res.stride = N;
+    }
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index);
+    Quantized q{};
+    at::Tensor out;
+    const bool coded = PyObject_IsTrue(a[7]) == 1;
+    if (coded)
+      q = quantized(a[8], a[9], "out", "out_scale", T, N, dev);
+    else
+      out = a[8] == Py_None ? made({T, N}, at::kBFloat16, dev) : arg(a[8], "out", at::kBFloat16, {2, {T, N}}, dev);
+    check(g_linear(data<uint8_t>(*x.t), x.stride, xs.p, xs.stride, data<uint8_t>(*w.t), ws.p, ws.stride, bias, type, act,
+                   res.t ? res.t->data_ptr() : nullptr, res.stride, coded ? nullptr : out.data_ptr(), q.c, q.s, q.stride, T,
+                   N, K, stream_of(dev)),
+          "linear_mxfp8");
+    return coded ? pack({q.codes, q.scales}) : or_none(out);
+  });
+}
+
+// (logits, topk, scoring, bias or None, renormalize, scale, num_groups, topk_groups, ids or None, weights or None)
+PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n, 10);
+    Device dev;
+    const at::Tensor& x = tensor(a[0], "logits");
+    if (x.dim() != 2) refuse("logits: must be [T, E]");
+    const int T = size(x.size(0), "T"), E = size(x.size(1), "E"), topk = integer(a[1], "topk");
+    const int type = float_type(x, "logits");
+    arg(a[0], "logits", x.scalar_type(), {2, {T, E}}, dev);
+    const float* bias = optional<float>(a[3], "bias", at::kFloat, {1, {E}}, dev);
+    if (topk <= 0) refuse("topk: %d must be positive", topk);
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index);
+    const at::Tensor ids = a[8] == Py_None ? made({T, topk}, at::kInt, dev) : arg(a[8], "ids", at::kInt, {2, {T, topk}}, dev);
+    const at::Tensor w =
+        a[9] == Py_None ? made({T, topk}, at::kFloat, dev) : arg(a[9], "weights", at::kFloat, {2, {T, topk}}, dev);
+    check(g_route(x.data_ptr(), type, bias, integer(a[2], "scoring"), PyObject_IsTrue(a[4]) == 1, number(a[5]),
+                  integer(a[6], "num_groups"), integer(a[7], "topk_groups"), data<int32_t>(ids), data<float>(w), T, E, topk,
+                  stream_of(dev)),
+          "moe_route");
+    return pack({ids, w});
+  });
+}
+
+// (x, x_scale, topk_ids, topk_weights, w13, w13_scale, w2, w2_scale, residual, out, workspace: each or None)
+PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n, 11);
+    Device dev;
+    const Matrix x = code_rows(a[0], "x", dev);
+    const int T = x.rows, K = x.K;
+    const Scales xs = scales(a[1], "x_scale", 0, T, K, dev);
+    const at::Tensor &ids = tensor(a[2], "topk_ids"), &w13 = tensor(a[4], "w13");
+    if (ids.dim() != 2) refuse("topk_ids: must be [T, topk]");
+    if (w13.dim() != 3 || w13.size(1) % 2 != 0) refuse("w13: must be [E, 2 F, K]");
+    const int topk = size(ids.size(1), "topk"), E = size(w13.size(0), "E"), F = size(w13.size(1) / 2, "F");
+    arg(a[2], "topk_ids", at::kInt, {2, {T, topk}}, dev);
+    const float* weights = data<float>(arg(a[3], "topk_weights", at::kFloat, {2, {T, topk}}, dev));
+    const uint8_t* up = codes(a[4], "w13", {3, {E, 2 * (int64_t)F, K}}, dev);
+    const Scales ups = scales(a[5], "w13_scale", E, 2 * (int64_t)F, K, dev);
+    const uint8_t* down = codes(a[6], "w2", {3, {E, K, F}}, dev);
+    const Scales downs = scales(a[7], "w2_scale", E, K, F, dev);
+    Matrix res{};
+    if (a[8] != Py_None) res = matrix_of(a[8], "residual", at::kBFloat16, T, K, dev);
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index);
+    const at::Tensor out = a[9] == Py_None ? made({T, K}, at::kBFloat16, dev) : arg(a[9], "out", at::kBFloat16, {2, {T, K}}, dev);
+    at::Tensor ws;
+    if (a[10] == Py_None) {
+      ws = made({(int64_t)g_moe_workspace_bytes(T, E, topk, F)}, at::kByte, dev);
+    } else {
+      ws = tensor(a[10], "workspace");
+      if (!ws.is_contiguous()) refuse("all tensors must be contiguous");
+      dev.same(ws);
+      if (ws.numel() == 0) refuse("workspace: must not be empty");  // (its address, null, would ask for the library's)
+    }
+    check(g_moe(data<uint8_t>(*x.t), x.stride, xs.p, xs.stride, data<int32_t>(ids), weights, up, ups.p, ups.stride, down,
+                downs.p, downs.stride, res.t ? res.t->data_ptr() : nullptr, res.stride, out.data_ptr(), T, E, topk, K, F,
+                ws.data_ptr(), (size_t)ws.nbytes(), stream_of(dev)),
+          "moe_mxfp8");
+    return or_none(out);
+  });
+}
+
 // (error class, addresses of the entry points)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "init: 7 arguments expected");
+  constexpr int kEntries = 12;
+  if (n != 1 + kEntries) {
+    PyErr_Format(PyExc_TypeError, "init: %d arguments expected", 1 + kEntries);
     return nullptr;
   }
-  void* p[6];
-  for (int i = 0; i < 6; ++i) {
+  void* p[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i + 1]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "init: null address");
@@ -369,6 +650,12 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_attention = reinterpret_cast<decltype(g_attention)>(p[3]);
   g_workspace_bytes = reinterpret_cast<decltype(g_workspace_bytes)>(p[4]);
   g_last_error = reinterpret_cast<decltype(g_last_error)>(p[5]);
+  g_quantize = reinterpret_cast<decltype(g_quantize)>(p[6]);
+  g_norm = reinterpret_cast<decltype(g_norm)>(p[7]);
+  g_linear = reinterpret_cast<decltype(g_linear)>(p[8]);
+  g_route = reinterpret_cast<decltype(g_route)>(p[9]);
+  g_moe = reinterpret_cast<decltype(g_moe)>(p[10]);
+  g_moe_workspace_bytes = reinterpret_cast<decltype(g_moe_workspace_bytes)>(p[11]);
   Py_RETURN_NONE;
 }
 
@@ -378,6 +665,11 @@ PyMethodDef kMethods[] = {{"init", FAST(init), METH_FASTCALL, nullptr},
                           {"release", FAST(release), METH_FASTCALL, nullptr},
                           {"store", FAST(store), METH_FASTCALL, nullptr},
                           {"attention", FAST(attention), METH_FASTCALL, nullptr},
+                          {"quantize", FAST(quantize), METH_FASTCALL, nullptr},
+                          {"norm", FAST(norm), METH_FASTCALL, nullptr},
+                          {"linear", FAST(linear), METH_FASTCALL, nullptr},
+                          {"route", FAST(route), METH_FASTCALL, nullptr},
+                          {"moe", FAST(moe), METH_FASTCALL, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -189,6 +189,104 @@ cudaError_t paged_prefill_timed_out(int** word);
 cudaError_t paged_attn_wait_check(int* status, cudaStream_t stream);
 cudaError_t paged_prefill_wait_check(int* status, cudaStream_t stream);
 
+// ---- MXFP8 operators: e4m3 codes with a scale exponent per 32 values
+
+struct MxQuantizeArgs {
+  const void* x;  // bf16 or float32 [T, K], rows x_stride elements apart
+  int64_t x_stride;
+  bool x_f32;
+  uint8_t* codes;   // [T, K]
+  uint8_t* scales;  // [T, K / 32], rows scale_stride bytes apart
+  int64_t scale_stride;
+  int T, K;
+};
+struct MxNormArgs {
+  const void* x;         // bf16 [T, K], rows x_stride elements apart
+  int64_t x_stride;
+  const void* residual;  // the same, or null
+  int64_t residual_stride;
+  const void* weight;    // bf16 or float32 [K], or null
+  bool weight_f32;
+  float eps;
+  uint8_t* codes;        // [T, K] or null
+  uint8_t* scales;       // [T, K / 32], rows scale_stride bytes apart
+  int64_t scale_stride;
+  void* normed;          // bf16 [T, K] or null
+  void* residual_out;    // bf16 [T, K] or null
+  int T, K;
+};
+constexpr int kMaxNormK = 65536;  // a row is held in one CTA's registers
+// (smla_mxnorm.cu)
+cudaError_t launch_mx_quantize(const MxQuantizeArgs& a, cudaStream_t stream);
+cudaError_t launch_mx_norm(const MxNormArgs& a, cudaStream_t stream);
+
+// What a product's results go through and where they go.
+struct MxEpilogue {
+  const void* bias;      // bf16 or float32 [rows of W], or null
+  bool bias_f32;
+  int activation;        // SMLA_ACT_*
+  const void* residual;  // bf16 [T, N], rows residual_stride elements apart, or null
+  int64_t residual_stride;
+  void* out;             // bf16 [T, N], or null where the results are quantized
+  uint8_t* codes;        // [T, N]
+  uint8_t* scales;       // [T, N / 32], rows scale_stride bytes apart
+  int64_t scale_stride;
+};
+struct MxLinearArgs {
+  const uint8_t* x;        // [T, K], rows x_stride bytes apart
+  int64_t x_stride;
+  const uint8_t* x_scale;  // [T, K / 32], rows x_scale_stride bytes apart
+  int64_t x_scale_stride;
+  const uint8_t* w;        // [N or 2 N, K]
+  const uint8_t* w_scale;
+  int64_t w_scale_stride;
+  MxEpilogue to;
+  int T, N, K;
+};
+// (smla_linear.cu)
+cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t mx_linear_timed_out(int** word);
+
+struct MoeRouteArgs {
+  const void* logits;  // bf16 or float32 [T, E]
+  bool logits_f32;
+  const float* bias;   // [E] or null
+  bool sigmoid, renormalize;
+  float scale;
+  int groups, topk_groups;
+  int32_t* ids;        // [T, topk]
+  float* weights;      // [T, topk]
+  int T, E, topk;
+};
+constexpr int kMaxRouteExperts = 512;
+constexpr int kMaxTopk = 32;
+// (smla_route.cu)
+cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t stream);
+
+struct MoeArgs {
+  const uint8_t* x;  // [T, K] as for the linear product
+  int64_t x_stride;
+  const uint8_t* x_scale;
+  int64_t x_scale_stride;
+  const int32_t* ids;    // [T, topk]
+  const float* weights;  // [T, topk]
+  const uint8_t* w13;    // [E, 2 F, K]
+  const uint8_t* w13_scale;
+  int64_t w13_scale_stride;
+  const uint8_t* w2;     // [E, K, F]
+  const uint8_t* w2_scale;
+  int64_t w2_scale_stride;
+  const void* residual;  // bf16 [T, K] or null
+  int64_t residual_stride;
+  void* out;             // bf16 [T, K]
+  void* workspace;
+  int T, E, topk, K, F;
+};
+// (smla_moe.cu)
+size_t moe_workspace(int T, int E, int topk, int F);
+cudaError_t launch_moe(const MoeArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t moe_timed_out(int** word);
+
 // Offsets inside the workspace.
 constexpr size_t kWsStatusBytes = 256;
 

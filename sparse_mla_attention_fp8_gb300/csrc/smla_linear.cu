@@ -1,0 +1,49 @@
+// Linear product on MXFP8 operands with its epilogue: y = act(x W^T + b) +
+// residual, or silu(x Wg^T + bg) * (x Wu^T + bu), in bf16 or MXFP8.
+#include "smla_mxgemm.cuh"
+
+namespace smla {
+
+namespace {
+
+template <int NA, int NT>
+cudaError_t launch_tiles(const MxLinearArgs& a, const MxParams& p, int num_sms, cudaStream_t stream) {
+  CUtensorMap a_map, b_map;
+  cudaError_t e = code_map(&a_map, a.w, (int64_t)NA * a.N, a.K, a.K, kTileRows);
+  if (e == cudaSuccess) e = code_map(&b_map, a.x, a.T, a.K, a.x_stride, NT);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = ((int64_t)a.N + kTileRows - 1) / kTileRows, tokens = ((int64_t)a.T + NT - 1) / NT;
+  const int parts = split_k(rows * tokens, (a.K + kStepK - 1) / kStepK, num_sms);
+  return launch_mx<kLinear, NA, NT>(p, parts, rows, tokens, 1, a_map, b_map, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t stream) {
+  MxParams p{};
+  p.a_scale = a.w_scale;
+  p.a_scale_stride = a.w_scale_stride;
+  p.b_scale = a.x_scale;
+  p.b_scale_stride = a.x_scale_stride;
+  p.rows = a.N;
+  p.T = a.T;
+  p.K = a.K;
+  p.to = a.to;
+  p.ld = a.N;
+  const auto even = [](const void* q, int64_t stride) { return stride % 2 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0; };
+  p.pairs = even(a.to.out, a.N) && (!a.to.residual || even(a.to.residual, a.to.residual_stride));
+  if (a.to.activation == SMLA_ACT_SWIGLU) {
+    if (a.T <= 16) return launch_tiles<2, 16>(a, p, num_sms, stream);
+    if (a.T <= 32) return launch_tiles<2, 32>(a, p, num_sms, stream);
+    if (a.T <= 64) return launch_tiles<2, 64>(a, p, num_sms, stream);
+    return launch_tiles<2, 96>(a, p, num_sms, stream);
+  }
+  if (a.T <= 16) return launch_tiles<1, 16>(a, p, num_sms, stream);
+  if (a.T <= 32) return launch_tiles<1, 32>(a, p, num_sms, stream);
+  if (a.T <= 64) return launch_tiles<1, 64>(a, p, num_sms, stream);
+  return launch_tiles<1, 128>(a, p, num_sms, stream);
+}
+
+cudaError_t mx_linear_timed_out(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_mx_timed_out); }
+
+}  // namespace smla

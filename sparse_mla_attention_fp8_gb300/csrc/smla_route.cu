@@ -1,0 +1,243 @@
+// The experts of each token from its router logits: scores by softmax or
+// sigmoid, a selection bias, groups of experts of which the best are kept, the
+// topk largest, and their weights.
+//
+// One warp per token; what it ranks by lies in registers, expert 32 i + l in
+// lane l, and a round of the selection is a maximum over the warp of ordered
+// bits, then the lowest index that has it.  Without bias and groups the logits
+// themselves are ranked, so float32 decides exactly.  With them what is ranked is
+// computed, and near ties could fall either way: where two neighbours of the
+// ranking, or the last taken and the first left, are nearer than the computation's
+// error, the token is ranked again in 64 bits.  (All of them in 64 bits would take
+// an exponential of 64 bits per expert, at a sixtieth of the rate.)  The call is
+// bound by its launch for decode batches and by reading the logits beyond.
+#include <algorithm>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "sm103_ptx.cuh"
+#include "smla_kernels.h"
+
+namespace smla {
+
+namespace {
+
+constexpr uint32_t kLanes = 0xffffffffu;
+constexpr int kRouteWarps = 4;
+
+// Bits ordered as the values are, above 0; 0 for NaN and -infinity, which are
+// never taken, and for what has been taken.
+__device__ __forceinline__ uint32_t order_bits(float x) {
+  if (!(x > -INFINITY)) return 0u;
+  const uint32_t b = __float_as_uint(x + 0.f);  // (-0 is 0)
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t order_bits(double x) {
+  if (!(x > -INFINITY)) return 0u;
+  const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
+  return b >> 63 ? ~b : b | (1ull << 63);
+}
+__device__ __forceinline__ float value_of(uint32_t b) { return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b); }
+__device__ __forceinline__ double value_of(uint64_t b) {
+  return __longlong_as_double((long long)(b >> 63 ? b & ~(1ull << 63) : ~b));
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kLanes, v); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+  const uint32_t hi = __reduce_max_sync(kLanes, (uint32_t)(v >> 32));
+  const uint32_t lo = __reduce_max_sync(kLanes, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+__device__ __forceinline__ float score_of(bool sigmoid, float x, float top, float inv_sum) {
+  return sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) * inv_sum;
+}
+
+// How far a float32 score plus bias may be from the exact one, in units of 2^-24:
+// of the score (at most 1) 2 for the exponential, 1 for its argument's rounding
+// (s |x - top| < 1/2), up to 21 for the sum of 512 of them and 1 for the quotient;
+// and half of one of the sum with the bias.  32 are taken.
+__device__ __forceinline__ float slack(float x) { return 0x1p-19f * (1.f + fabsf(x)); }
+
+// Ranks a token's experts (keys[i]: of expert 32 i + lane) and takes topk of
+// them, lane k the k-th (-1: there was none).  `near_tie` reports two neighbours
+// nearer than their error.  `scratch`: E keys of shared memory, used with groups.
+template <int R, typename Bits>
+__device__ __forceinline__ int take(const MoeRouteArgs& a, Bits (&keys)[R], Bits* scratch, bool check, bool& near_tie) {
+  const int lane = threadIdx.x & 31;
+  near_tie = false;
+  if (a.groups > 1) {
+    const int size = a.E / a.groups;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (32 * i + lane < a.E) scratch[32 * i + lane] = keys[i];
+    __syncwarp();
+    // lane g: group g's two largest; their sum's key
+    Bits group = 0;
+    if (lane < a.groups) {
+      Bits first = 0, second = 0;
+      for (int i = 0; i < size; ++i) {
+        const Bits k = scratch[lane * size + i];
+        second = k > first ? first : k > second ? k : second;
+        first = k > first ? k : first;
+      }
+      if (second) group = order_bits(value_of(first) + value_of(second));
+    }
+    __syncwarp();
+    uint32_t kept = 0u;
+    Bits last = 0;
+    for (int r = 0; r <= a.topk_groups; ++r) {  // one more, to see how near it is
+      const Bits top = warp_max(group);
+      if (check && r == a.topk_groups && top) {
+        const float lo = (float)value_of(top), hi = (float)value_of(last);
+        near_tie |= hi - lo <= 2.f * (slack(lo) + slack(hi));
+      }
+      if (r == a.topk_groups || !top) break;
+      const int g = __ffs(__ballot_sync(kLanes, group == top)) - 1;
+      kept |= 1u << g;
+      if (lane == g) group = 0;
+      last = top;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (32 * i + lane < a.E && !(kept >> ((32 * i + lane) / size) & 1u)) keys[i] = 0;
+  }
+  int mine = -1;
+  Bits last = 0;
+  for (int r = 0; r <= a.topk; ++r) {
+    Bits best = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) best = keys[i] > best ? keys[i] : best;
+    const Bits top = warp_max(best);
+    if (check && r > 0 && top) {
+      const float lo = (float)value_of(top), hi = (float)value_of(last);
+      near_tie |= hi - lo <= slack(lo) + slack(hi);
+    }
+    if (r == a.topk || !top) break;
+    uint32_t at = 0xffffffffu;
+#pragma unroll
+    for (int i = R - 1; i >= 0; --i)
+      if (keys[i] == top) at = (uint32_t)(32 * i + lane);
+    const int e = (int)__reduce_min_sync(kLanes, at);
+    if (lane == r) mine = e;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (32 * i + lane == e) keys[i] = 0;
+    last = top;
+  }
+  return mine;
+}
+
+// The same in 64 bits, from the logits on.
+template <int R, typename X>
+__device__ __noinline__ int take_64(const MoeRouteArgs& a, const X* logits, uint64_t* scratch) {
+  const int lane = threadIdx.x & 31;
+  uint64_t keys[R];
+  double x[R], top = -INFINITY, sum = 0.;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    x[i] = 32 * i + lane < a.E ? (double)(float)logits[32 * i + lane] : -INFINITY;
+    if (x[i] > top) top = x[i];
+  }
+  if (!a.sigmoid) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmax(top, __shfl_xor_sync(kLanes, top, d));
+#pragma unroll
+    for (int i = 0; i < R; ++i) sum += 32 * i + lane < a.E ? exp(x[i] - top) : 0.;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kLanes, sum, d);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int e = 32 * i + lane;
+    keys[i] = 0;
+    if (e < a.E && x[i] > -INFINITY)
+      keys[i] = order_bits((a.sigmoid ? 1. / (1. + exp(-x[i])) : exp(x[i] - top) / sum) + (a.bias ? (double)a.bias[e] : 0.));
+  }
+  bool unused;
+  return take<R, uint64_t>(a, keys, scratch, false, unused);
+}
+
+template <int R, typename X>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_constant__ MoeRouteArgs a) {
+  __shared__ uint64_t scratch[kRouteWarps][32 * R];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+  grid_dependency_wait();
+  if (t >= a.T) return;
+  const X* logits = static_cast<const X*>(a.logits) + t * a.E;
+  float x[R], top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < R; ++i) x[i] = 32 * i + lane < a.E ? (float)logits[32 * i + lane] : -INFINITY;
+#pragma unroll
+  for (int i = 0; i < R; ++i) top = fmaxf(top, x[i]);
+  const bool computed = a.bias != nullptr || a.groups > 1;  // what is ranked
+  float sum = 0.f, inv = 1.f;
+  if (!a.sigmoid) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kLanes, top, d));
+    if (computed || !a.renormalize) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) sum += x[i] > -INFINITY ? expf(x[i] - top) : 0.f;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kLanes, sum, d);
+      inv = 1.f / sum;
+    }
+  }
+  uint32_t keys[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int e = 32 * i + lane;
+    float rank = x[i];
+    if (computed && x[i] > -INFINITY) rank = score_of(a.sigmoid, x[i], top, inv) + (a.bias && e < a.E ? __ldg(a.bias + e) : 0.f);
+    keys[i] = e < a.E && x[i] > -INFINITY ? order_bits(rank) : 0u;
+  }
+  bool near_tie;
+  int id = take<R, uint32_t>(a, keys, reinterpret_cast<uint32_t*>(scratch[warp]), computed, near_tie);
+  if (near_tie) {
+    __syncwarp();
+    id = take_64<R, X>(a, logits, scratch[warp]);
+  }
+  // lane k: the k-th expert's weight
+  float w = id >= 0 ? score_of(a.sigmoid, (float)logits[id], top, inv) : 0.f;
+  if (a.renormalize) {
+    float all = w;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(kLanes, all, d);
+    w = all > 0.f ? w / all : id >= 0 ? w : 0.f;
+  }
+  if (lane < a.topk) {
+    a.ids[t * a.topk + lane] = id;
+    a.weights[t * a.topk + lane] = id >= 0 ? w * a.scale : 0.f;
+  }
+}
+
+template <int R, typename X>
+cudaError_t launch_route(const MoeRouteArgs& a, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(((int64_t)a.T + kRouteWarps - 1) / kRouteWarps));
+  cfg.blockDim = dim3(32 * kRouteWarps);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, route_kernel<R, X>, a);
+}
+
+template <typename X>
+cudaError_t launch_experts(const MoeRouteArgs& a, cudaStream_t stream) {
+  if (a.E <= 64) return launch_route<2, X>(a, stream);
+  if (a.E <= 128) return launch_route<4, X>(a, stream);
+  if (a.E <= 256) return launch_route<8, X>(a, stream);
+  return launch_route<16, X>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t stream) {
+  return a.logits_f32 ? launch_experts<float>(a, stream) : launch_experts<__nv_bfloat16>(a, stream);
+}
+
+}  // namespace smla
