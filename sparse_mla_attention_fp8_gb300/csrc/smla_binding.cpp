@@ -412,8 +412,10 @@ Scales scales(PyObject* o, const char* name, int64_t E, int64_t rows, int64_t K,
   if (E > 1 && rows > 1 && t.stride(0) != rows * stride) refuse("%s: all rows must be one distance apart", name);
   return {static_cast<uint8_t*>(t.data_ptr()), stride};
 }
+// 16 bytes, not 4: rows on 16-byte boundaries can be copied by TMA (the linear product's kernel for many tokens).
+int64_t made_scale_stride(int64_t K) { return (K / 32 + 15) / 16 * 16; }
 at::Tensor made_scales(int64_t rows, int64_t K, const Device& dev) {
-  const int64_t n = K / 32, padded = (n + 3) / 4 * 4;
+  const int64_t n = K / 32, padded = made_scale_stride(K);
   const at::Tensor t = made({rows, padded}, at::kByte, dev);
   return padded == n ? t : t.narrow(1, 0, n);
 }
@@ -436,7 +438,7 @@ Quantized quantized(PyObject* c, PyObject* s, const char* cname, const char* sna
   q.scales = s == Py_None ? made_scales(rows, K, dev) : tensor(s, sname);
   if (s == Py_None) {
     q.s = data<uint8_t>(q.scales);
-    q.stride = (K / 32 + 3) / 4 * 4;
+    q.stride = made_scale_stride(K);
   } else {
     const Scales given = scales(s, sname, 0, rows, K, dev);
     q.s = given.p;

@@ -1,6 +1,7 @@
 // Linear product on MXFP8 operands with its epilogue: y = act(x W^T + b) +
 // residual, or silu(x Wg^T + bg) * (x Wu^T + bu), in bf16 or MXFP8.
 #include "smla_mxgemm.cuh"
+#include "smla_mxpair.cuh"
 
 namespace smla {
 
@@ -32,6 +33,16 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t st
   p.ld = a.N;
   const auto even = [](const void* q, int64_t stride) { return stride % 2 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0; };
   p.pairs = even(a.to.out, a.N) && (!a.to.residual || even(a.to.residual, a.to.residual_stride));
+  if (a.T > 256 && pair_takes(a)) {
+    switch (a.to.activation) {
+      case SMLA_ACT_NONE: return launch_pair<SMLA_ACT_NONE>(a, p, num_sms, stream);
+      case SMLA_ACT_RELU: return launch_pair<SMLA_ACT_RELU>(a, p, num_sms, stream);
+      case SMLA_ACT_SILU: return launch_pair<SMLA_ACT_SILU>(a, p, num_sms, stream);
+      case SMLA_ACT_GELU: return launch_pair<SMLA_ACT_GELU>(a, p, num_sms, stream);
+      case SMLA_ACT_GELU_TANH: return launch_pair<SMLA_ACT_GELU_TANH>(a, p, num_sms, stream);
+      default: return launch_pair<SMLA_ACT_SWIGLU>(a, p, num_sms, stream);
+    }
+  }
   if (a.to.activation == SMLA_ACT_SWIGLU) {
     if (a.T <= 16) return launch_tiles<2, 16>(a, p, num_sms, stream);
     if (a.T <= 32) return launch_tiles<2, 32>(a, p, num_sms, stream);

@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -143,14 +144,21 @@ __device__ __forceinline__ float bias_at(const MxEpilogue& to, int64_t i) {
                      : __bfloat162float(static_cast<const __nv_bfloat16*>(to.bias)[i]);
 }
 
-// Four tokens (t .. t + 3, those below t_end) of this lane's feature f: `group`
-// is the warp's first feature, the lanes of the warp hold 32 consecutive ones.
-// Row `out_row + i` of the output is token t + i's.
+// Where results go: MXFP8 codes, bf16 two features an access, bf16 one at a time.
+enum MxOut { kOutCodes, kOutPairs, kOutSingle };
+__device__ __forceinline__ MxOut out_kind(const MxParams& p) {
+  return p.to.out == nullptr ? kOutCodes : p.pairs ? kOutPairs : kOutSingle;
+}
+
+// Four tokens' results of this lane's feature f; the lanes of the warp hold 32
+// consecutive features from `group` on.  They go to rows out_row .. of the output,
+// the first n of them.
+template <MxOut kOut>
 __device__ __forceinline__ void write_out(const MxParams& p, float (&v)[4], int f, int group, int64_t out_row, int n) {
   const MxEpilogue& to = p.to;
   const int lane = threadIdx.x & 31;
-  if (to.out == nullptr) {
-    // quantized: N is a multiple of 32, so the warp's group is whole or not there
+  if (kOut == kOutCodes) {
+    // N is a multiple of 32, so the warp's group is whole or not there
     if (group >= p.rows) return;
     int e[4];
 #pragma unroll
@@ -174,7 +182,7 @@ __device__ __forceinline__ void write_out(const MxParams& p, float (&v)[4], int 
   }
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(to.out);
   const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(to.residual);
-  if (p.pairs) {
+  if (kOut == kOutPairs) {
     // two features of one token a lane: even lanes take the even token of a pair
     const int even = f & ~1;
 #pragma unroll
@@ -200,6 +208,12 @@ __device__ __forceinline__ void write_out(const MxParams& p, float (&v)[4], int 
     if (res) v[i] += __bfloat162float(res[(out_row + i) * to.residual_stride + f]);
     out[(out_row + i) * p.ld + f] = __float2bfloat16_rn(v[i]);
   }
+}
+__device__ __forceinline__ void write_out(MxOut kind, const MxParams& p, float (&v)[4], int f, int group, int64_t out_row,
+                                          int n) {
+  if (kind == kOutCodes) write_out<kOutCodes>(p, v, f, group, out_row, n);
+  else if (kind == kOutPairs) write_out<kOutPairs>(p, v, f, group, out_row, n);
+  else write_out<kOutSingle>(p, v, f, group, out_row, n);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -414,6 +428,7 @@ __global__ void __launch_bounds__(kMxThreads, 2)
 
   // ---------------------------------------------------------------- results
   const int q = warp & 3, f = n0 + 32 * q + lane;
+  const MxOut out = out_kind(p);
   float bias[NA];
   if (warp >= 2)
 #pragma unroll
@@ -429,7 +444,7 @@ __global__ void __launch_bounds__(kMxThreads, 2)
       if (MODE == kMoeUp) y[i] = c + i < ntok && m.routed[c + i] ? y[i] * m.share[c + i] : 0.f;
     }
     const int64_t row = MODE == kMoeUp ? (int64_t)slot0 * NT + c : t0 + c;
-    write_out(p, y, f, n0 + 32 * q, row, ntok - c);
+    write_out(out, p, y, f, n0 + 32 * q, row, ntok - c);
   };
   const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
   if (MODE == kMoeUp && total == 0) {
@@ -520,18 +535,23 @@ MxEncodeFn mx_encode_fn() {
   return fn;
 }
 
-// Codes [rows, K], rows `stride` bytes apart (a multiple of 16), in boxes of 128
-// bytes of box_rows rows; what lies outside reads as zeros.
-cudaError_t code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t stride, int box_rows) {
+// Bytes [rows, cols], rows `stride` bytes apart (a multiple of 16), in boxes; what
+// lies outside reads as zeros.
+cudaError_t byte_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t stride, int box_cols,
+                     int box_rows, CUtensorMapSwizzle swizzle) {
   MxEncodeFn enc = mx_encode_fn();
   if (!enc) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)stride};
-  const cuuint32_t box[2] = {(cuuint32_t)kStepK, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, es[2] = {1, 1};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// Codes [rows, K] in boxes of 128 bytes of box_rows rows.
+cudaError_t code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t stride, int box_rows) {
+  return byte_map(map, base, rows, K, stride, kStepK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int MODE, int NA, int NT>

@@ -1,0 +1,356 @@
+// The same product for many tokens: tiles of 256 features by 256 tokens (gated:
+// 256 by 128, gate and up part) by pairs of CTAs, whose MMAs (cta_group::2,
+// M = 256) read each CTA's 128 features from its own shared memory and half of the
+// tokens from each, so that an SM loads and reads half the tokens' bytes.  The
+// pairs are persistent; a tile's accumulator (256 columns) is emptied into
+// registers at once, and while its results are written the next tile's MMAs run.
+//
+// Scales: rows of 32 bytes (8 steps of K) of the tile's 384 scale rows come by TMA;
+// four warps, one for each quarter of the lanes of tensor memory, hold a step's
+// words of all of them and store them there, a set of columns per stage.  (Through
+// shared memory and tcgen05.cp, the copies stood between the MMAs: 2501 x 5120 x
+// 13824 took 166 us against 140 without any scales.)  What one CTA tells the other
+// by an arrival lies in tensor memory or has been read, not in memory: the arrivals
+// are relaxed.  (One that releases at cluster scope waits for the SM's stores in
+// flight: 301 us against 153.)
+//
+// Warp roles: 0 TMA of the codes (each CTA loads its halves, both count on the
+// first one's barriers), 1 MMA issuer (in the first CTA), 2 TMA of the scales,
+// 4..7 scales, 8..15 results.
+#pragma once
+#include "smla_mxgemm.cuh"
+
+namespace smla {
+
+namespace {
+
+// ---------------------------------------------------------------- instructions
+
+__device__ __forceinline__ void pair_alloc(uint32_t* slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// Arrives on the barrier at this place in both CTAs when all MMAs so far have completed.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// tma_load_2d into this CTA, counted on a barrier of either CTA of the pair (cluster address).
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// ---------------------------------------------------------------- layout
+
+template <int NA>
+struct PairLay {
+  static constexpr int kTokens = 256 / NA;             // of a tile: the accumulator's 256 columns
+  static constexpr int kBTile = kTokens / 2 * kStepK;  // a CTA's half of the tokens
+  static constexpr int kStage = NA * kTileRows * kStepK + kBTile;
+  static constexpr int kBlocks = NA + kTokens / 128;   // of 128 scale rows: of the features, then of the tokens
+  static constexpr int kStages = NA == 1 ? 6 : 5;
+  static constexpr int kRawBlock = 128 * 32, kRaw = kBlocks * kRawBlock;
+  static constexpr int kOffRaw = kStages * kStage;
+  static constexpr int kOffMisc = kOffRaw + 2 * kRaw;
+  static constexpr int kSmem = kOffMisc + 256 + 1024;
+  static constexpr int kAcc = 256, kScaleCols = 4 * kBlocks;
+  static constexpr int kCols = 512;
+  static_assert(kSmem <= 232448 && kStage % 1024 == 0 && kAcc + kStages * kScaleCols <= kCols, "limits");
+};
+struct PairMisc {
+  uint64_t full[6], empty[6], raw_full[2], raw_empty[2], acc_full, acc_empty;
+  uint32_t tmem;
+  int abort_flag;
+};
+static_assert(sizeof(PairMisc) <= 256, "misc");
+
+constexpr int kPairThreads = 512;
+// Registers a thread by warpgroup, of 128 at launch: 64 + 96 + 2 * 176 = 4 * 128.
+constexpr int kRoleRegs = 64, kScaleRegs = 96, kResultRegs = 176;
+
+// ---------------------------------------------------------------- the kernel
+
+template <int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    mx_pair_kernel(const __grid_constant__ MxParams p, const __grid_constant__ CUtensorMap a_map,
+                   const __grid_constant__ CUtensorMap b_map, const __grid_constant__ CUtensorMap a_scale_map,
+                   const __grid_constant__ CUtensorMap b_scale_map) {
+  constexpr int NA = ACT == SMLA_ACT_SWIGLU ? 2 : 1;
+  using L = PairLay<NA>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  PairMisc& m = *reinterpret_cast<PairMisc*>(smem + L::kOffMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_ctarank();
+  volatile int* abort_flag = &m.abort_flag;
+
+  if (tid == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&m.full[s], 9);  // the first CTA's producer, four warps' scales in each
+      mbar_init(&m.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&m.raw_full[b], 1);
+      mbar_init(&m.raw_empty[b], 4);
+    }
+    mbar_init(&m.acc_full, 1);
+    mbar_init(&m.acc_empty, 16);
+    m.abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) pair_alloc(&m.tmem, L::kCols);
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = m.tmem;
+  grid_dependency_wait();
+
+  const int steps = (p.K + kStepK - 1) / kStepK;
+  const int token_tiles = (p.T + L::kTokens - 1) / L::kTokens, row_tiles = (p.rows + 2 * kTileRows - 1) / (2 * kTileRows);
+  const int tiles = token_tiles * row_tiles, first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
+  auto token0 = [&](int tile) { return tile % token_tiles * L::kTokens; };
+  auto row0 = [&](int tile) { return tile / token_tiles * (2 * kTileRows) + rank * kTileRows; };
+
+#define PAIR_WAIT(bar, parity) mbar_wait(&(bar), (parity), abort_flag, &g_mx_timed_out, kDevWaitTimeout)
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------------- codes
+      int i = 0;
+      bool ok = true;
+      for (int tile = first; tile < tiles && ok; tile += stride) {
+        const int y = row0(tile), t = token0(tile) + rank * (L::kTokens / 2);
+        for (int k = 0; k < steps; ++k, ++i) {
+          const int s = i % L::kStages, use = i / L::kStages;
+          if (use > 0 && !(ok = PAIR_WAIT(m.empty[s], (use + 1) & 1))) break;
+          const uint32_t stage = smem_u32(smem + s * L::kStage), bar = mapa_shared(smem_u32(&m.full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&m.full[s], 2u * L::kStage);
+#pragma unroll
+          for (int a = 0; a < NA; ++a)
+            pair_load_2d(stage + a * kTileRows * kStepK, &a_map, k * kStepK, y + a * p.rows, bar);
+          pair_load_2d(stage + NA * kTileRows * kStepK, &b_map, k * kStepK, t, bar);
+        }
+      }
+      // after an abort no copy may still be landing when the CTAs exit
+      if (!ok && rank == 0)
+        for (int j = max(0, i - L::kStages); j < i; ++j) mbar_wait_drain(&m.full[j % L::kStages], (j / L::kStages) & 1);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // -------------------------------------------------------------- MMA issuer
+      int i = 0, n = 0;
+      bool ok = true;
+      for (int tile = first; tile < tiles && ok; tile += stride, ++n) {
+        if (n > 0 && !(ok = PAIR_WAIT(m.acc_empty, (n + 1) & 1))) break;
+        tc_fence_after();
+        for (int k = 0; k < steps; ++k, ++i) {
+          const int s = i % L::kStages;
+          if (!(ok = PAIR_WAIT(m.full[s], (i / L::kStages) & 1))) break;
+          tc_fence_after();
+          const uint32_t stage = smem_u32(smem + s * L::kStage), sf = tmem + L::kAcc + s * L::kScaleCols;
+#pragma unroll
+          for (int kk = 0; kk < kStepK / 32; ++kk)
+#pragma unroll
+            for (int a = 0; a < NA; ++a)
+              pair_mma(tmem + a * L::kTokens, make_sdesc(stage + a * kTileRows * kStepK + 32 * kk, 16, 1024, kLayoutSw128),
+                       make_sdesc(stage + NA * kTileRows * kStepK + 32 * kk, 16, 1024, kLayoutSw128),
+                       idesc_mx(2 * kTileRows, L::kTokens, kk), sf + 4 * a, sf + 4 * NA, (k > 0 || kk > 0) ? 1u : 0u);
+          pair_commit(&m.empty[s]);
+        }
+        pair_commit(&m.acc_full);  // (after an abort: nothing is in flight behind it)
+      }
+      if (!ok && n > 0) mbar_wait_drain(&m.acc_full, (n - 1) & 1);
+    } else if (warp == 2 && lane == 0) {
+      // -------------------------------------------------------------- scales' bytes
+      int i = 0;
+      bool ok = true;
+      for (int tile = first; tile < tiles && ok; tile += stride) {
+        const int y = row0(tile), t = token0(tile);
+        for (int k = 0; k < steps; k += 8, ++i) {
+          const int b = i & 1;
+          if (i >= 2 && !(ok = PAIR_WAIT(m.raw_empty[b], ((i >> 1) + 1) & 1))) break;
+          const uint32_t raw = smem_u32(smem + L::kOffRaw + b * L::kRaw);
+          mbar_arrive_expect_tx(&m.raw_full[b], (uint32_t)L::kRaw);
+#pragma unroll
+          for (int j = 0; j < L::kBlocks; ++j)
+            tma_load_2d(raw + j * L::kRawBlock, j < NA ? &a_scale_map : &b_scale_map, 4 * k,
+                        j < NA ? y + j * p.rows : t + 128 * (j - NA), &m.raw_full[b]);
+        }
+      }
+      if (!ok)
+        for (int j = max(0, i - 2); j < i; ++j) mbar_wait_drain(&m.raw_full[j & 1], (j >> 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- scales
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kScaleRegs));
+    const uint32_t to = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + L::kAcc;
+    int i = 0, g = 0;
+    bool dead = false;
+    for (int tile = first; tile < tiles && !dead; tile += stride) {
+      for (int k0 = 0; k0 < steps && !dead; k0 += 8, ++g) {
+        const int b = g & 1;
+        dead = __any_sync(kAllLanes, !PAIR_WAIT(m.raw_full[b], (g >> 1) & 1));
+        if (dead) break;
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+          if (k0 + h >= steps || dead) break;
+          // lane l: four steps' words of rows l, l + 32, l + 64, l + 96 of each block
+          uint4 w[L::kBlocks][4];
+#pragma unroll
+          for (int j = 0; j < L::kBlocks; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              w[j][c] = *reinterpret_cast<const uint4*>(smem + L::kOffRaw + b * L::kRaw + j * L::kRawBlock +
+                                                        (32 * c + lane) * 32 + 4 * h);
+          if (h == 4 || k0 + 4 >= steps) {  // the buffer has been read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.raw_empty[b]);
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if (k0 + h + x >= steps) break;
+            const int s = i % L::kStages;
+            if (i >= L::kStages) dead = __any_sync(kAllLanes, !PAIR_WAIT(m.empty[s], ((i / L::kStages) + 1) & 1));
+            if (dead) break;
+            ++i;
+            tc_fence_after();
+            auto word = [&](const uint4& v) { return x == 0 ? v.x : x == 1 ? v.y : x == 2 ? v.z : v.w; };
+#pragma unroll
+            for (int j = 0; j < L::kBlocks; ++j)
+              tmem_st4(to + s * L::kScaleCols + 4 * j, word(w[j][0]), word(w[j][1]), word(w[j][2]), word(w[j][3]));
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&m.full[s]), 0));
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- results
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kResultRegs));
+    const int q = warp & 3, half = (warp - 8) >> 2;
+    constexpr int kMine = L::kTokens / 2;  // tokens of this warp
+    const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + half * kMine;
+    const uint32_t empty = mapa_shared(smem_u32(&m.acc_empty), 0);
+    const MxOut kind = out_kind(p);
+    int n = 0;
+    for (int tile = first; tile < tiles; tile += stride, ++n) {
+      const int group = row0(tile) + 32 * q, f = group + lane, t = token0(tile) + half * kMine, ntok = p.T - t;
+      float bias[NA];
+#pragma unroll
+      for (int a = 0; a < NA; ++a) bias[a] = p.to.bias && f < p.rows ? bias_at(p.to, (int64_t)a * p.rows + f) : 0.f;
+      if (__any_sync(kAllLanes, !PAIR_WAIT(m.acc_full, n & 1))) break;
+      tc_fence_after();
+      uint32_t w[NA * kMine];
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (int c = 0; c < kMine; c += 32) tmem_ld32(acc + a * L::kTokens + c, w + a * kMine + c);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < NA * kMine; ++i) asm volatile("" : "+r"(w[i]));
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(empty);
+      auto all = [&](auto out) {
+#pragma unroll
+        for (int c = 0; c < kMine; c += 4) {
+          if (c >= ntok) break;
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[i] = __uint_as_float(w[c + i]) + bias[0];
+            if (NA == 2) y[i] = silu(y[i]) * (__uint_as_float(w[(NA - 1) * kMine + c + i]) + bias[NA - 1]);
+            else y[i] = activate(ACT, y[i]);
+          }
+          write_out<decltype(out)::value>(p, y, f, group, t + c, ntok - c);
+        }
+      };
+      if (kind == kOutCodes) all(std::integral_constant<MxOut, kOutCodes>{});
+      else if (kind == kOutPairs) all(std::integral_constant<MxOut, kOutPairs>{});
+      else all(std::integral_constant<MxOut, kOutSingle>{});
+    }
+  }
+#undef PAIR_WAIT
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    pair_dealloc(tmem, L::kCols);
+  }
+}
+
+// Scales [rows, n] in boxes of 8 steps' bytes of 128 rows.
+cudaError_t scale_map(CUtensorMap* map, const void* base, int64_t rows, int64_t n, int64_t stride) {
+  return byte_map(map, base, rows, n, stride, 32, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+// Whether scale rows can be copied by TMA: on 16-byte boundaries.
+bool pair_takes(const MxLinearArgs& a) {
+  const auto rows16 = [](const uint8_t* q, int64_t stride) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && stride % 16 == 0; };
+  return rows16(a.x_scale, a.x_scale_stride) && rows16(a.w_scale, a.w_scale_stride);
+}
+
+template <int ACT>
+cudaError_t launch_pair(const MxLinearArgs& a, const MxParams& p, int num_sms, cudaStream_t stream) {
+  constexpr int NA = ACT == SMLA_ACT_SWIGLU ? 2 : 1;
+  using L = PairLay<NA>;
+  CUtensorMap a_map, b_map;
+  cudaError_t e = code_map(&a_map, a.w, (int64_t)NA * a.N, a.K, a.K, kTileRows);
+  if (e == cudaSuccess) e = code_map(&b_map, a.x, a.T, a.K, a.x_stride, L::kTokens / 2);
+  CUtensorMap a_scale_map, b_scale_map;
+  if (e == cudaSuccess) e = scale_map(&a_scale_map, a.w_scale, (int64_t)NA * a.N, a.K / kMxGroup, a.w_scale_stride);
+  if (e == cudaSuccess) e = scale_map(&b_scale_map, a.x_scale, a.T, a.K / kMxGroup, a.x_scale_stride);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (((int64_t)a.T + L::kTokens - 1) / L::kTokens) * (((int64_t)a.N + 2 * kTileRows - 1) / (2 * kTileRows));
+  if (tiles > INT32_MAX / 4) return cudaErrorInvalidValue;
+  e = cudaFuncSetAttribute(mx_pair_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, num_sms / 2)));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mx_pair_kernel<ACT>, p, a_map, b_map, a_scale_map, b_scale_map);
+}
+
+}  // namespace
+
+}  // namespace smla

@@ -226,6 +226,23 @@ def test_linear_quantized(smla, T, N, K, act):
     check_linear(smla, T, N, K, act=act, quantized=True)
 
 
+@pytest.mark.parametrize("T,N,K", [(257, 32, 32), (300, 256, 128), (383, 130, 4096), (512, 257, 96), (640, 1000, 256),
+                                   (257, 1, 544), (1111, 2080, 1056), (2000, 4096, 512), (5000, 96, 128), (1024, 5120, 64)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_linear_many_tokens(smla, T, N, K, act):
+    check_linear(smla, T, N, K, act=act)
+    if N % 32 == 0:
+        check_linear(smla, T, N, K, act=act, quantized=True)
+    else:
+        check_linear(smla, T, N, K, act=act, bias=torch.bfloat16, residual=True)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh", "swiglu"])
+@pytest.mark.parametrize("out", ["bf16", "residual", "mxfp8"])
+def test_linear_epilogues_many_tokens(smla, act, out):
+    check_linear(smla, 500, 352, 384, act=act, bias=torch.float32, residual=out == "residual", quantized=out == "mxfp8")
+
+
 def test_linear_many_tiles(smla):
     check_linear(smla, 1100, 1300, 640, act="gelu", bias=torch.float32)
     check_linear(smla, 1000, 1056, 640, act="swiglu", quantized=True)
