@@ -1029,8 +1029,8 @@ int check_moe(int T, int E, int topk, int F) {
   if (T < 0 || E <= 0 || topk <= 0) return fail(SMLA_ERR_INVALID_ARG, "bad sizes T=%d E=%d topk=%d", T, E, topk);
   const int rc = check_groups("F", F);
   if (rc != SMLA_OK) return rc;
-  if (E > 1024 || topk > smla::kMaxTopk)
-    return fail(SMLA_ERR_UNSUPPORTED, "E=%d, topk=%d unsupported: at most 1024 and %d", E, topk, smla::kMaxTopk);
+  if (E > 512 || topk > smla::kMaxTopk)
+    return fail(SMLA_ERR_UNSUPPORTED, "E=%d, topk=%d unsupported: at most 512 and %d", E, topk, smla::kMaxTopk);
   return SMLA_OK;
 }
 }  // namespace

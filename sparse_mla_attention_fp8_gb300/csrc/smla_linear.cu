@@ -7,15 +7,23 @@ namespace smla {
 
 namespace {
 
-template <int NA, int NT>
+template <int MODE, int NT>
 cudaError_t launch_tiles(const MxLinearArgs& a, const MxParams& p, int num_sms, cudaStream_t stream) {
+  constexpr int kGate = MODE == kGated ? 2 : 1;
   CUtensorMap a_map, b_map;
-  cudaError_t e = code_map(&a_map, a.w, (int64_t)NA * a.N, a.K, a.K, kTileRows);
+  cudaError_t e = code_map(&a_map, a.w, (int64_t)kGate * a.N, a.K, a.K, kTileRows / kGate);
   if (e == cudaSuccess) e = code_map(&b_map, a.x, a.T, a.K, a.x_stride, NT);
   if (e != cudaSuccess) return e;
-  const int64_t rows = ((int64_t)a.N + kTileRows - 1) / kTileRows, tokens = ((int64_t)a.T + NT - 1) / NT;
+  const int64_t rows = ((int64_t)a.N * kGate + kTileRows - 1) / kTileRows, tokens = ((int64_t)a.T + NT - 1) / NT;
   const int parts = split_k(rows * tokens, (a.K + kStepK - 1) / kStepK, num_sms);
-  return launch_mx<kLinear, NA, NT>(p, parts, rows, tokens, 1, a_map, b_map, stream);
+  return launch_mx<MODE, NT>(p, parts, rows, tokens, 1, a_map, b_map, stream);
+}
+template <int MODE>
+cudaError_t launch_few(const MxLinearArgs& a, const MxParams& p, int num_sms, cudaStream_t stream) {
+  if (a.T <= 16) return launch_tiles<MODE, 16>(a, p, num_sms, stream);
+  if (a.T <= 32) return launch_tiles<MODE, 32>(a, p, num_sms, stream);
+  if (a.T <= 64) return launch_tiles<MODE, 64>(a, p, num_sms, stream);
+  return launch_tiles<MODE, 128>(a, p, num_sms, stream);
 }
 
 }  // namespace
@@ -33,7 +41,8 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t st
   p.ld = a.N;
   const auto even = [](const void* q, int64_t stride) { return stride % 2 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0; };
   p.pairs = even(a.to.out, a.N) && (!a.to.residual || even(a.to.residual, a.to.residual_stride));
-  if (a.T > 256 && pair_takes(a)) {
+  p.wide_scales = rows16(a.x_scale, a.x_scale_stride) && rows16(a.w_scale, a.w_scale_stride);
+  if (a.T > (getenv("PAIRT") ? atoi(getenv("PAIRT")) : 256) && p.wide_scales) {  // (scale rows that TMA can copy)
     switch (a.to.activation) {
       case SMLA_ACT_NONE: return launch_pair<SMLA_ACT_NONE>(a, p, num_sms, stream);
       case SMLA_ACT_RELU: return launch_pair<SMLA_ACT_RELU>(a, p, num_sms, stream);
@@ -43,16 +52,8 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t st
       default: return launch_pair<SMLA_ACT_SWIGLU>(a, p, num_sms, stream);
     }
   }
-  if (a.to.activation == SMLA_ACT_SWIGLU) {
-    if (a.T <= 16) return launch_tiles<2, 16>(a, p, num_sms, stream);
-    if (a.T <= 32) return launch_tiles<2, 32>(a, p, num_sms, stream);
-    if (a.T <= 64) return launch_tiles<2, 64>(a, p, num_sms, stream);
-    return launch_tiles<2, 96>(a, p, num_sms, stream);
-  }
-  if (a.T <= 16) return launch_tiles<1, 16>(a, p, num_sms, stream);
-  if (a.T <= 32) return launch_tiles<1, 32>(a, p, num_sms, stream);
-  if (a.T <= 64) return launch_tiles<1, 64>(a, p, num_sms, stream);
-  return launch_tiles<1, 128>(a, p, num_sms, stream);
+  return a.to.activation == SMLA_ACT_SWIGLU ? launch_few<kGated>(a, p, num_sms, stream)
+                                            : launch_few<kLinear>(a, p, num_sms, stream);
 }
 
 cudaError_t mx_linear_timed_out(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_mx_timed_out); }

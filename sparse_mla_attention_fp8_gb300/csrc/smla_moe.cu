@@ -11,9 +11,9 @@ namespace smla {
 
 namespace {
 
-int token_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 96; }
+int token_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
 
-// h: [token tile][expert slot][token][F] codes, then the scales, in rows of whole words
+// h: [token tile][expert slot][token][F] codes, then the scales, in rows on 16-byte boundaries
 struct MoeSizes {
   int tile, slots;
   int64_t tiles, rows, scale_stride;
@@ -25,7 +25,7 @@ MoeSizes moe_sizes(int T, int E, int topk, int F) {
   s.tiles = ((int64_t)T + s.tile - 1) / s.tile;
   s.slots = (int)std::min<int64_t>(E, (int64_t)std::min(T, s.tile) * topk);
   s.rows = s.tiles * s.slots * s.tile;
-  s.scale_stride = (F / kMxGroup + 3) / 4 * 4;
+  s.scale_stride = (F / kMxGroup + 15) / 16 * 16;
   s.codes = kWsStatusBytes;
   s.scales = s.codes + ((size_t)s.rows * F + 255) / 256 * 256;
   s.bytes = s.scales + ((size_t)s.rows * s.scale_stride + 255) / 256 * 256;
@@ -40,6 +40,7 @@ cudaError_t launch_experts(const MoeArgs& a, const MoeSizes& s, int num_sms, cud
   up.a_scale_stride = a.w13_scale_stride;
   up.b_scale = a.x_scale;
   up.b_scale_stride = a.x_scale_stride;
+  up.wide_scales = rows16(a.x_scale, a.x_scale_stride) && rows16(a.w13_scale, a.w13_scale_stride);
   up.rows = a.F;
   up.T = a.T;
   up.K = a.K;
@@ -57,6 +58,7 @@ cudaError_t launch_experts(const MoeArgs& a, const MoeSizes& s, int num_sms, cud
   down.a_scale_stride = a.w2_scale_stride;
   down.b_scale = ws + s.scales;
   down.b_scale_stride = s.scale_stride;
+  down.wide_scales = rows16(a.w2_scale, a.w2_scale_stride);
   down.rows = a.K;
   down.K = a.F;
   down.to = MxEpilogue{};
@@ -67,18 +69,17 @@ cudaError_t launch_experts(const MoeArgs& a, const MoeSizes& s, int num_sms, cud
   down.pairs = reinterpret_cast<uintptr_t>(a.out) % 4 == 0 && (!a.residual || (a.residual_stride % 2 == 0 &&
                                                                 reinterpret_cast<uintptr_t>(a.residual) % 4 == 0));
   CUtensorMap w13, x, w2, h;
-  cudaError_t e = code_map(&w13, a.w13, (int64_t)a.E * 2 * a.F, a.K, a.K, kTileRows);
+  cudaError_t e = code_map(&w13, a.w13, (int64_t)a.E * 2 * a.F, a.K, a.K, kTileRows / 2);
   if (e == cudaSuccess) e = code_map(&x, a.x, a.T, a.K, a.x_stride, NT);
   if (e == cudaSuccess) e = code_map(&w2, a.w2, (int64_t)a.E * a.K, a.F, a.F, kTileRows);
   if (e == cudaSuccess) e = code_map(&h, ws + s.codes, s.rows, a.F, a.F, NT);
   if (e != cudaSuccess) return e;
-  const int64_t f_tiles = (a.F + kTileRows - 1) / kTileRows, k_tiles = (a.K + kTileRows - 1) / kTileRows;
-  // (96 columns twice leave no room for partial sums in two CTAs' shared memory)
-  const int up_parts = NT > 64 ? 1 : split_k(f_tiles * s.slots * s.tiles, (a.K + kStepK - 1) / kStepK, num_sms);
-  e = launch_mx<kMoeUp, 2, NT>(up, up_parts, f_tiles, s.tiles, s.slots, w13, x, stream);
+  const int64_t f_tiles = ((int64_t)2 * a.F + kTileRows - 1) / kTileRows, k_tiles = (a.K + kTileRows - 1) / kTileRows;
+  const int up_parts = split_k(f_tiles * s.slots * s.tiles, (a.K + kStepK - 1) / kStepK, num_sms);
+  e = launch_mx<kMoeUp, NT>(up, up_parts, f_tiles, s.tiles, s.slots, w13, x, stream);
   if (e != cudaSuccess) return e;
   const int down_parts = split_k(k_tiles * s.tiles, (int64_t)s.slots * ((a.F + kStepK - 1) / kStepK), num_sms);
-  return launch_mx<kMoeDown, 1, NT>(down, down_parts, k_tiles, s.tiles, 1, w2, h, stream);
+  return launch_mx<kMoeDown, NT>(down, down_parts, k_tiles, s.tiles, 1, w2, h, stream);
 }
 
 }  // namespace
@@ -91,8 +92,7 @@ cudaError_t launch_moe(const MoeArgs& a, int num_sms, cudaStream_t stream) {
   switch (s.tile) {
     case 16: return launch_experts<16>(a, s, num_sms, stream);
     case 32: return launch_experts<32>(a, s, num_sms, stream);
-    case 64: return launch_experts<64>(a, s, num_sms, stream);
-    default: return launch_experts<96>(a, s, num_sms, stream);
+    default: return launch_experts<64>(a, s, num_sms, stream);
   }
 }
 

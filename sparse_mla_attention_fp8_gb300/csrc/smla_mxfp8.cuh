@@ -22,10 +22,10 @@ __device__ __forceinline__ uint32_t mx_finite_bits(float x) {
   const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
   return b < 0x7f800000u ? b : 0u;
 }
-// E from the bits of amax = (1 + f) 2^e: 448 = 1.75 * 2^8.  (Subnormal ones have
-// e = -127 here, far below the floor.)
+// E from the bits of amax = (1 + f) 2^e: 448 = 1.75 * 2^8, and the sum carries into
+// the exponent where f is above .75.  (Subnormal ones are far below the floor.)
 __device__ __forceinline__ int mx_exponent(uint32_t amax_bits) {
-  return max(-100, (int)(amax_bits >> 23) - 127 - 8 + ((amax_bits & 0x7fffffu) > 0x600000u));
+  return max(-100, (int)((amax_bits + 0x1fffffu) >> 23) - 127 - 8);
 }
 __device__ __forceinline__ float mx_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 

@@ -5,19 +5,25 @@
 //
 // Features are the MMA's rows and tokens its columns (M = 128, N = kNT), so that
 // one token costs a tile of 16 columns and not of 128 rows, and so that the 32
-// values under one output scale are the 32 lanes of a warp.  A gated product
-// holds two accumulators of the same lanes, its gate's and its up part's rows.
+// values under one output scale are the 32 lanes of a warp.  A gated product's
+// tile has 64 rows of its gate part and the same 64 of its up part, whose sums
+// meet in shared memory.
 //
 // A CTA makes one output tile, over all of K or, where tiles are few, over one of
 // the equal parts of K that a cluster's CTAs share; each then leaves its partial
-// sums in its shared memory and sums up some of the columns, in the order of the
-// ranks.  Warp roles: 0 TMA producer (codes, 128-byte rows and swizzle), 1 MMA
-// issuer, 2..5 first copy the scale bytes into shared memory in the order in
-// which tcgen05.cp takes them to tensor memory (row r's 4 bytes of a 128-value
-// step at 16 (r % 32) + 4 (r / 32)), then write the results out.
+// sums in its shared memory, and they sum up the results between them, in the
+// order of the ranks.  With few tokens the product is bound by reading W: several
+// CTAs an SM keep that read going while others start and end.
+//
+// Warp roles: 0 TMA of the codes (128-byte rows and swizzle), 1 MMA issuer, 2..5
+// scales, then results.  The scales of a set of four steps (of 128 values of K) go
+// from global memory through registers into tensor memory, where each warp fills
+// its quarter of the lanes: column 4 b + c holds the 4 bytes of row 32 c + lane of
+// the b-th block of 128 rows.
 #pragma once
 #include <algorithm>
 #include <cstdint>
+#include <cstdlib>
 #include <mutex>
 #include <type_traits>
 #include <cuda.h>
@@ -36,13 +42,13 @@ namespace {
 
 constexpr uint32_t kAllLanes = 0xffffffffu;
 constexpr int kStepK = 128;    // values of K per stage: one 128-byte swizzle row
-constexpr int kTileRows = 128; // features per accumulator
+constexpr int kTileRows = 128; // rows of W per tile
 constexpr int kMxThreads = 6 * 32;
 
 // Set when a wait runs out in a kernel of the file that includes this.
 __device__ int g_mx_timed_out;
 
-enum MxMode { kLinear, kMoeUp, kMoeDown };
+enum MxMode { kLinear, kGated, kMoeUp, kMoeDown };
 
 // ---------------------------------------------------------------- instructions
 
@@ -59,10 +65,19 @@ __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-// 512 bytes of shared memory (32 rows of 16) into 4 columns of tensor memory, the
-// same in each quarter of its lanes.  In order with the MMAs of the same thread.
-__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+// True in one thread of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+// An arrival that publishes nothing in memory.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
@@ -82,6 +97,7 @@ struct MxParams {
   MxEpilogue to;
   int64_t ld;              // features of an output row
   bool pairs;              // bf16 results and residual can be accessed two at a time
+  bool wide_scales;        // both sides' scale rows lie on 16-byte boundaries
   // mixture of experts
   const int32_t* ids;      // [T, topk]
   const float* weights;
@@ -89,41 +105,37 @@ struct MxParams {
   int slots;               // experts that a token tile can have at most
 };
 
-template <int NA, int NT>
-struct MxLay {
-  static constexpr int kATile = kTileRows * kStepK;
-  static constexpr int kBTile = NT * kStepK;
-  static constexpr int kStage = NA * kATile + kBTile;
-  static constexpr int kNB = (NT + 127) / 128;  // 128-row blocks of the tokens' scales
-  static constexpr int kScales = 512 * (NA + kNB);
-  static constexpr int kMisc = 4096;            // barriers, expert lists, weights
-  static constexpr int kBudget = 113 * 1024 - 1024 - kMisc;  // two CTAs an SM
-  static constexpr int kFit = kBudget / (kStage + kScales);
-  static constexpr int kStages = kFit > 6 ? 6 : kFit;
-  static constexpr int kPartial = NA * NT * kTileRows * 4;
-  static constexpr int kRing = kStages * kStage > kPartial ? kStages * kStage : kPartial;
-  static constexpr int kOffScales = kRing;
-  static constexpr int kOffMisc = kOffScales + kStages * kScales;
-  static constexpr int kSmem = kOffMisc + kMisc + 1024;
-  static constexpr int kAcc = NA * NT;          // tensor memory: accumulators, then two sets of scales
-  static constexpr int kScaleCols = 4 * (NA + kNB);
-  static constexpr int kNeed = kAcc + 2 * kScaleCols;
-  static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
-  static_assert(kStages >= 2 && kStage % 1024 == 0, "stages");
-  static_assert(kNeed <= 512 && kSmem <= 232448, "limits");
-};
+constexpr int kMaxMoeExperts = 512;
+constexpr int kSetSteps = 4;  // steps whose scales go to tensor memory together
+constexpr int kSets = 2;      // a ring of them
 
-constexpr int kMaxMoeExperts = 1024;
 struct MxMisc {
-  uint64_t full[6], empty[6], done;
+  uint64_t full[6], empty[6], scaled[kSets], unscaled[kSets], done;
   uint32_t tmem;
   int abort_flag, active;
   uint32_t mask[kMaxMoeExperts / 32];
   uint16_t list[kMaxMoeExperts];
-  float share[256];
-  uint8_t routed[256];
+  float share[64];
+  uint8_t routed[64];
 };
-static_assert(sizeof(MxMisc) <= 4096, "misc");
+
+template <int NT>
+struct MxLay {
+  static constexpr int kATile = kTileRows * kStepK;
+  static constexpr int kStage = kATile + NT * kStepK;
+  static constexpr int kCtas = NT > 64 ? 2 : 3;  // an SM
+  static constexpr int kMisc = 1664;
+  static constexpr int kFit = ((228 / kCtas - 1) * 1024 - 1024 - kMisc) / kStage;
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static constexpr int kPartial = NT * kTileRows * 4;
+  static constexpr int kOffMisc = kStages * kStage;
+  static constexpr int kSmem = kOffMisc + kMisc + 1024;
+  static constexpr int kScaleCols = 8;          // of a step: W's block and the tokens'
+  static constexpr int kNeed = NT + kSets * kSetSteps * kScaleCols;
+  static constexpr int kCols = kNeed <= 128 ? 128 : 256;  // of tensor memory
+  static_assert(kStages >= 2 && kStage % 1024 == 0 && kPartial <= kStages * kStage, "stages");
+  static_assert(kNeed <= kCols && kCols * kCtas <= 512 && sizeof(MxMisc) <= kMisc, "limits");
+};
 
 // ---------------------------------------------------------------- the results' way out
 
@@ -150,6 +162,40 @@ __device__ __forceinline__ MxOut out_kind(const MxParams& p) {
   return p.to.out == nullptr ? kOutCodes : p.pairs ? kOutPairs : kOutSingle;
 }
 
+// Four tokens' results of a group of 32 features, one a lane, as codes: lane l gets
+// those of token l % 4 and features l & ~3 .. l | 3, and that token's scale byte.
+__device__ __forceinline__ uint32_t quantize4(float (&v)[4], uint32_t& scale) {
+  const int lane = threadIdx.x & 31;
+  uint32_t top[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top[i] = __reduce_max_sync(kAllLanes, __float_as_uint(v[i]) & 0x7fffffffu);
+  if (max(max(top[0], top[1]), max(top[2], top[3])) >= 0x7f800000u) {  // infinities and NaN are left out
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top[i] = __reduce_max_sync(kAllLanes, mx_finite_bits(v[i]));
+  }
+  int e[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    e[i] = mx_exponent(top[i]);
+    v[i] *= mx_pow2(-e[i]);
+  }
+  scale = (uint32_t)((lane & 2 ? (lane & 1 ? e[3] : e[2]) : (lane & 1 ? e[1] : e[0])) + 127);
+  // bytes: this feature's 4 tokens; exchanged in fours of lanes for one token's 4 features
+  uint32_t w = mx_e4m3x4(v[0], v[1], v[2], v[3]);
+  uint32_t o = __shfl_xor_sync(kAllLanes, w, 1);
+  w = __byte_perm(w, o, lane & 1 ? 0x3715 : 0x6240);
+  o = __shfl_xor_sync(kAllLanes, w, 2);
+  return __byte_perm(w, o, lane & 2 ? 0x3276 : 0x5410);
+}
+// Two tokens' results of this lane's feature as one token's of two features (lanes
+// 2 k and 2 k + 1: features 2 k and 2 k + 1 of the first and of the second token).
+__device__ __forceinline__ void pair_up(float first, float second, float& lo, float& hi) {
+  const bool odd = threadIdx.x & 1;
+  const float got = __shfl_xor_sync(kAllLanes, odd ? first : second, 1);
+  lo = odd ? got : first;
+  hi = odd ? second : got;
+}
+
 // Four tokens' results of this lane's feature f; the lanes of the warp hold 32
 // consecutive features from `group` on.  They go to rows out_row .. of the output,
 // the first n of them.
@@ -160,23 +206,12 @@ __device__ __forceinline__ void write_out(const MxParams& p, float (&v)[4], int 
   if (kOut == kOutCodes) {
     // N is a multiple of 32, so the warp's group is whole or not there
     if (group >= p.rows) return;
-    int e[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      e[i] = mx_exponent(__reduce_max_sync(kAllLanes, mx_finite_bits(v[i])));
-      v[i] *= mx_pow2(-e[i]);
-    }
-    // bytes: this feature's 4 tokens; exchanged in fours of lanes for one token's 4 features
-    uint32_t w = mx_e4m3x4(v[0], v[1], v[2], v[3]);
-    uint32_t o = __shfl_xor_sync(kAllLanes, w, 1);
-    w = __byte_perm(w, o, lane & 1 ? 0x3715 : 0x6240);
-    o = __shfl_xor_sync(kAllLanes, w, 2);
-    w = __byte_perm(w, o, lane & 2 ? 0x3276 : 0x5410);
+    uint32_t scale;
+    const uint32_t w = quantize4(v, scale);
     const int i = lane & 3;
     if (i < n) {
       *reinterpret_cast<uint32_t*>(to.codes + (out_row + i) * p.ld + group + (lane & 28)) = w;
-      const int mine = i == 0 ? e[0] : i == 1 ? e[1] : i == 2 ? e[2] : e[3];
-      if (lane < 4) to.scales[(out_row + i) * to.scale_stride + group / kMxGroup] = (uint8_t)(mine + 127);
+      if (lane < 4) to.scales[(out_row + i) * to.scale_stride + group / kMxGroup] = (uint8_t)scale;
     }
     return;
   }
@@ -187,9 +222,8 @@ __device__ __forceinline__ void write_out(const MxParams& p, float (&v)[4], int 
     const int even = f & ~1;
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
-      const bool odd = lane & 1;
-      const float got = __shfl_xor_sync(kAllLanes, odd ? v[i] : v[i + 1], 1);
-      float lo = odd ? got : v[i], hi = odd ? v[i + 1] : got;
+      float lo, hi;
+      pair_up(v[i], v[i + 1], lo, hi);
       const int k = i + (lane & 1);
       if (k >= n || even >= p.rows) continue;
       if (res) {
@@ -219,23 +253,29 @@ __device__ __forceinline__ void write_out(MxOut kind, const MxParams& p, float (
 // ---------------------------------------------------------------- the kernel
 
 // grid: x = cluster rank + parts * row tile, y = token tile, z = expert slot (kMoeUp).
-template <int MODE, int NA, int NT>
-__global__ void __launch_bounds__(kMxThreads, 2)
+template <int MODE, int NT>
+__global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
     mx_gemm_kernel(const __grid_constant__ MxParams p, const int parts, const __grid_constant__ CUtensorMap a_map,
                    const __grid_constant__ CUtensorMap b_map) {
-  using L = MxLay<NA, NT>;
+  using L = MxLay<NT>;
+  constexpr bool kGate = MODE == kGated || MODE == kMoeUp, kExperts = MODE == kMoeUp || MODE == kMoeDown;
+  constexpr int kFeatures = kGate ? kTileRows / 2 : kTileRows;  // of a tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   MxMisc& m = *reinterpret_cast<MxMisc*>(smem + L::kOffMisc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)blockIdx.x % parts, n0 = (int)blockIdx.x / parts * kTileRows;
+  const int rank = (int)blockIdx.x % parts, n0 = (int)blockIdx.x / parts * kFeatures;
   const int t0 = (int)blockIdx.y * NT, ntok = min(NT, p.T - t0);
   volatile int* abort_flag = &m.abort_flag;
 
   if (tid == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&m.full[s], 5);  // the producer and four warps' scales
+      mbar_init(&m.full[s], 1);
       mbar_init(&m.empty[s], 1);
+    }
+    for (int s = 0; s < kSets; ++s) {
+      mbar_init(&m.scaled[s], 4);
+      mbar_init(&m.unscaled[s], 1);
     }
     mbar_init(&m.done, 1);
     m.abort_flag = 0;
@@ -245,7 +285,7 @@ __global__ void __launch_bounds__(kMxThreads, 2)
     tmem_alloc(&m.tmem, L::kCols);
     tmem_relinquish();
   }
-  if (MODE != kLinear && tid < kMaxMoeExperts / 32) m.mask[tid] = 0u;
+  if (kExperts && tid < kMaxMoeExperts / 32) m.mask[tid] = 0u;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -258,8 +298,8 @@ __global__ void __launch_bounds__(kMxThreads, 2)
   if (MODE == kMoeUp) grid_launch_dependents();
 
   const int steps = (p.K + kStepK - 1) / kStepK;  // of one row
-  int total = steps, expert = 0, active = 1;
-  if (MODE != kLinear) {
+  int total = steps, expert = 0;
+  if (kExperts) {
     // the experts that this tile's tokens go to, in order
     for (int i = tid; i < ntok * p.topk; i += kMxThreads) {
       const int id = __ldg(p.ids + (int64_t)t0 * p.topk + i);
@@ -267,7 +307,7 @@ __global__ void __launch_bounds__(kMxThreads, 2)
     }
     __syncthreads();
     if (tid < 32) {
-      const uint32_t word = m.mask[lane];
+      const uint32_t word = lane < kMaxMoeExperts / 32 ? m.mask[lane] : 0u;
       int before = __popc(word);
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -279,13 +319,177 @@ __global__ void __launch_bounds__(kMxThreads, 2)
       if (lane == 31) m.active = before;
     }
     __syncthreads();
-    active = m.active;
     if (MODE == kMoeUp) {
-      const bool idle = (int)blockIdx.z >= active;  // the same for a whole cluster
+      const bool idle = (int)blockIdx.z >= m.active;  // the same for a whole cluster
       expert = idle ? 0 : m.list[blockIdx.z];
       if (idle) total = 0;
+    } else {
+      total = m.active * steps;
+    }
+  }
+  // Parts of whole sets where the scales of a set can be read at once: 16 bytes of a row, on 16-byte boundaries.
+  const bool wide = p.wide_scales && p.K % (kSetSteps * kStepK) == 0;
+  const int unit = wide ? kSetSteps : 1;
+  const int k0 = (int)((int64_t)(total / unit) * rank / parts) * unit;
+  const int n = (int)((int64_t)(total / unit) * (rank + 1) / parts) * unit - k0;
+  const int slot0 = MODE == kMoeUp ? (int)(blockIdx.y * p.slots + blockIdx.z) : (int)blockIdx.y * p.slots;
+  // Step it's place in its row, and its expert's place in the list.
+  auto in_row = [&](int it) { return MODE == kMoeDown ? it % steps : it; };
+  auto in_list = [&](int it) { return MODE == kMoeDown ? it / steps : 0; };
+  auto expert_of = [&](int it) { return MODE == kMoeDown ? (int)m.list[it / steps] : expert; };
+
+#define MX_WAIT(bar, parity) mbar_wait(&(bar), (parity), abort_flag, &g_mx_timed_out, kDevWaitTimeout)
+  bool dead = false;
+  if (warp == 0) {
+    // ---------------------------------------------------------------- codes
+    if (lane == 0) {
+      auto load_a = [&](int i, int s) {
+        const int it = k0 + i, x = in_row(it) * kStepK, y = expert_of(it) * (kGate ? 2 : 1) * p.rows + n0;
+        const uint32_t stage = smem_u32(smem + s * L::kStage);
+        mbar_arrive_expect_tx(&m.full[s], (uint32_t)L::kStage);
+        tma_load_2d(stage, &a_map, x, y, &m.full[s]);
+        if (kGate) tma_load_2d(stage + L::kATile / 2, &a_map, x, y + p.rows, &m.full[s]);
+      };
+      auto load_b = [&](int i, int s) {
+        const int it = k0 + i;
+        tma_load_2d(smem_u32(smem + s * L::kStage) + L::kATile, &b_map, in_row(it) * kStepK,
+                    MODE == kMoeDown ? (slot0 + in_list(it)) * NT : t0, &m.full[s]);
+      };
+      const int early = MODE == kMoeDown ? min(n, L::kStages) : 0;
+      for (int i = 0; i < early; ++i) load_a(i, i);
+      if (MODE == kMoeDown) grid_dependency_wait();
+      for (int i = 0; i < early; ++i) load_b(i, i);
+      int s = early % L::kStages, issued = early;
+      uint32_t phase = early == L::kStages ? 1u : 0u;  // of the fillings of stage s
+      for (int i = early; i < n; ++i) {
+        if (i >= L::kStages && !MX_WAIT(m.empty[s], phase ^ 1u)) break;
+        load_a(i, s);
+        load_b(i, s);
+        ++issued;
+        if (++s == L::kStages) s = 0, phase ^= 1u;
+      }
+      // after an abort no copy may still be landing when the CTA exits: the last one of each stage
+      if (*abort_flag)
+        for (int i = max(0, issued - L::kStages); i < issued; ++i)
+          mbar_wait_drain(&m.full[i % L::kStages], (i / L::kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    // The whole warp goes through the loop and elects the issuing thread, so that operands lie in uniform registers.
+    constexpr uint32_t kHi = sdesc_hi(1024, kLayoutSw128);
+    const uint32_t lo0 = sdesc_lo(smem_u32(smem), 16);
+    int s = 0, set = 0;
+    uint32_t phase = 0, set_phase = 0;
+    bool ok = true;
+    for (int i0 = 0; i0 < n && ok; i0 += kSetSteps) {
+      if (!(ok = MX_WAIT(m.scaled[set], set_phase))) break;
+      const int left = min(kSetSteps, n - i0);
+      uint32_t sf = tmem + NT + set * kSetSteps * L::kScaleCols;
+      for (int k = 0; k < left; ++k, sf += L::kScaleCols) {
+        if (!(ok = MX_WAIT(m.full[s], phase))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t lo = lo0 + (uint32_t)s * (L::kStage >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kStepK / 32; ++kk)
+            mma_mx(tmem, sdesc_join<kHi>(lo + 2 * kk), sdesc_join<kHi>(lo + (L::kATile >> 4) + 2 * kk),
+                   idesc_mx(kTileRows, NT, kk), sf, sf + 4, kk > 0 ? 1u : (uint32_t)((i0 | k) != 0));
+          mma_commit(&m.empty[s]);
+          if (k + 1 == left) mma_commit(&m.unscaled[set]);
+        }
+        __syncwarp();
+        if (++s == L::kStages) s = 0, phase ^= 1u;
+      }
+      if (++set == kSets) set = 0, set_phase ^= 1u;
+    }
+    if (elect_one()) mma_commit(&m.done);
+    __syncwarp();
+    mbar_wait_drain(&m.done, 0);
+  } else {
+    // ---------------------------------------------------------------- scales
+    if (MODE == kMoeDown) grid_dependency_wait();
+    const int q = warp & 3;
+    constexpr int kB = NT / 32 > 0 ? NT / 32 : 1;  // the tokens' rows in groups of 32
+    const int groups = p.K / kMxGroup;
+    // rows 32 c + lane of W's block, and of the tokens'; null behind the end
+    auto a_row = [&](int c, int e) -> const uint8_t* {
+      const int r = 32 * c + lane, f = n0 + (kGate ? r % kFeatures : r);
+      const int64_t row = (int64_t)e * (kGate ? 2 : 1) * p.rows + (kGate && r >= kFeatures ? p.rows : 0) + f;
+      return f < p.rows ? p.a_scale + row * p.a_scale_stride : nullptr;
+    };
+    auto b_row = [&](int c, int at) -> const uint8_t* {
+      const int t = 32 * c + lane;
+      const int64_t row = MODE == kMoeDown ? (int64_t)(slot0 + at) * NT + t : t0 + t;
+      return t < ntok ? p.b_scale + row * p.b_scale_stride : nullptr;
+    };
+    struct Words {
+      uint32_t a[4][kSetSteps], b[kB][kSetSteps];
+    };
+    auto read = [&](int i0, Words& w) {
+      if (wide) {
+        const int x = 4 * in_row(k0 + i0), e = expert_of(k0 + i0), at = in_list(k0 + i0);
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint8_t* row = a_row(c, e);
+          const uint4 v = row ? __ldg(reinterpret_cast<const uint4*>(row + x)) : none;
+          w.a[c][0] = v.x, w.a[c][1] = v.y, w.a[c][2] = v.z, w.a[c][3] = v.w;
+        }
+#pragma unroll
+        for (int c = 0; c < kB; ++c) {
+          const uint8_t* row = b_row(c, at);
+          const uint4 v = row ? __ldg(reinterpret_cast<const uint4*>(row + x)) : none;
+          w.b[c][0] = v.x, w.b[c][1] = v.y, w.b[c][2] = v.z, w.b[c][3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kSetSteps; ++k) {
+          if (i0 + k >= n) break;
+          const int it = k0 + i0 + k, x = in_row(it), e = expert_of(it), at = in_list(it);
+          const int left = groups - 4 * x;  // bytes of the row's last word behind its end count for nothing
+          const uint32_t valid = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint8_t* row = a_row(c, e);
+            w.a[c][k] = row ? __ldg(reinterpret_cast<const uint32_t*>(row + 4 * x)) & valid : 0u;
+          }
+#pragma unroll
+          for (int c = 0; c < kB; ++c) {
+            const uint8_t* row = b_row(c, at);
+            w.b[c][k] = row ? __ldg(reinterpret_cast<const uint32_t*>(row + 4 * x)) & valid : 0u;
+          }
+        }
+      }
+    };
+    Words cur, next{};
+    if (n > 0) read(0, next);
+    const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + NT;
+    int set = 0;
+    uint32_t phase = 0;
+    for (int i0 = 0; i0 < n; i0 += kSetSteps) {
+      cur = next;
+      if (i0 + kSetSteps < n) read(i0 + kSetSteps, next);
+      if (i0 >= kSets * kSetSteps) dead = __any_sync(kAllLanes, !MX_WAIT(m.unscaled[set], phase ^ 1u));
+      if (dead) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < kSetSteps; ++k) {
+        const uint32_t at = to + (set * kSetSteps + k) * L::kScaleCols;
+        tmem_st4(at, cur.a[0][k], cur.a[1][k], cur.a[2][k], cur.a[3][k]);
+        tmem_st4(at + 4, cur.b[0][k], kB > 1 ? cur.b[1 % kB][k] : 0u, kB > 2 ? cur.b[2 % kB][k] : 0u,
+                 kB > 3 ? cur.b[3 % kB][k] : 0u);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_relaxed(&m.scaled[set]);
+      if (++set == kSets) set = 0, phase ^= 1u;
+    }
+    if (MODE == kMoeUp) {
       // the weight that each token gives this expert
-      for (int t = tid; t < NT; t += kMxThreads) {
+      const int t = tid - 64;
+      if (t < NT) {
         float w = 0.f;
         bool any = false;
         if (t < ntok)
@@ -296,218 +500,90 @@ __global__ void __launch_bounds__(kMxThreads, 2)
         m.share[t] = w;
         m.routed[t] = any;
       }
-      __syncthreads();
-    } else {
-      total = active * steps;
-    }
-  }
-  const int k0 = (int)((int64_t)total * rank / parts), n = (int)((int64_t)total * (rank + 1) / parts) - k0;
-  const int slot0 = MODE == kMoeUp ? (int)(blockIdx.y * p.slots + blockIdx.z) : (int)blockIdx.y * p.slots;
-
-#define MX_WAIT(bar, parity) mbar_wait(&(bar), (parity), abort_flag, &g_mx_timed_out, kDevWaitTimeout)
-  bool dead = false;
-  if (warp == 0) {
-    // ---------------------------------------------------------------- codes
-    if (lane == 0) {
-      auto load_a = [&](int i) {
-        const int s = i % L::kStages, it = k0 + i;
-        const uint32_t stage = smem_u32(smem + s * L::kStage);
-        const int x = (MODE == kMoeDown ? it % steps : it) * kStepK;
-        const int e = MODE == kMoeUp ? expert : MODE == kMoeDown ? m.list[it / steps] : 0;
-        const int y = e * NA * p.rows + n0;
-        mbar_arrive_expect_tx(&m.full[s], (uint32_t)L::kStage);
-        tma_load_2d(stage, &a_map, x, y, &m.full[s]);
-        if (NA == 2) tma_load_2d(stage + L::kATile, &a_map, x, y + p.rows, &m.full[s]);
-      };
-      auto load_b = [&](int i) {
-        const int s = i % L::kStages, it = k0 + i;
-        const int x = (MODE == kMoeDown ? it % steps : it) * kStepK;
-        const int y = MODE == kMoeDown ? (slot0 + it / steps) * NT : t0;
-        tma_load_2d(smem_u32(smem + s * L::kStage) + NA * L::kATile, &b_map, x, y, &m.full[s]);
-      };
-      const int early = MODE == kMoeDown ? min(n, L::kStages) : 0;
-      for (int i = 0; i < early; ++i) load_a(i);
-      if (MODE == kMoeDown) grid_dependency_wait();
-      for (int i = 0; i < early; ++i) load_b(i);
-      int issued = early;
-      for (int i = early; i < n; ++i) {
-        if (i >= L::kStages && !MX_WAIT(m.empty[i % L::kStages], ((i / L::kStages) + 1) & 1)) break;
-        load_a(i);
-        load_b(i);
-        ++issued;
-      }
-      // no copy may still be landing when the CTA exits (after an abort: the last of each stage)
-      if (*abort_flag)
-        for (int i = max(0, issued - L::kStages); i < issued; ++i)
-          mbar_wait_drain(&m.full[i % L::kStages], (i / L::kStages) & 1);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      for (int i = 0; i < n; ++i) {
-        const int s = i % L::kStages;
-        if (!MX_WAIT(m.full[s], (i / L::kStages) & 1)) break;
-        tc_fence_after();
-        const uint32_t stage = smem_u32(smem + s * L::kStage), scales = smem_u32(smem + L::kOffScales + s * L::kScales);
-        const uint32_t sf = tmem + L::kAcc + (i & 1) * L::kScaleCols;
-#pragma unroll
-        for (int j = 0; j < NA + L::kNB; ++j)
-          tmem_copy_scales(sf + 4 * j, make_sdesc(scales + 512 * j, 16, 128, kLayoutNone));
-#pragma unroll
-        for (int k = 0; k < kStepK / 32; ++k)
-#pragma unroll
-          for (int a = 0; a < NA; ++a)
-            mma_mx(tmem + a * NT, make_sdesc(stage + a * L::kATile + 32 * k, 16, 1024, kLayoutSw128),
-                   make_sdesc(stage + NA * L::kATile + 32 * k, 16, 1024, kLayoutSw128), idesc_mx(kTileRows, NT, k),
-                   sf + 4 * a, sf + 4 * NA, (i > 0 || k > 0) ? 1u : 0u);
-        mma_commit(&m.empty[s]);
-      }
-      mma_commit(&m.done);
-      mbar_wait_drain(&m.done, 0);
-    }
-    __syncwarp();
-  } else {
-    // ---------------------------------------------------------------- scales
-    if (MODE == kMoeDown) grid_dependency_wait();
-    const int q = warp & 3, r = 32 * q + lane;
-    constexpr int kAhead = 4, kWords = NA + L::kNB;
-    const int groups = p.K / kMxGroup;
-    auto load = [&](int i, uint32_t (&w)[kWords]) {
-      const int it = k0 + i, x = MODE == kMoeDown ? it % steps : it;
-      const int e = MODE == kMoeUp ? expert : MODE == kMoeDown ? m.list[it / steps] : 0;
-      const int left = groups - 4 * x;  // bytes of the row's last word behind its end count for nothing
-      const uint32_t valid = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
-#pragma unroll
-      for (int a = 0; a < NA; ++a) {
-        const int64_t row = ((int64_t)e * NA + a) * p.rows + n0 + r;
-        w[a] = n0 + r < p.rows
-                   ? __ldg(reinterpret_cast<const uint32_t*>(p.a_scale + row * p.a_scale_stride + 4 * x)) & valid
-                   : 0u;
-      }
-#pragma unroll
-      for (int b = 0; b < L::kNB; ++b) {
-        const int c = 128 * b + r;
-        const int64_t row = MODE == kMoeDown ? (int64_t)(slot0 + it / steps) * NT + c : t0 + c;
-        w[NA + b] = c < ntok
-                        ? __ldg(reinterpret_cast<const uint32_t*>(p.b_scale + row * p.b_scale_stride + 4 * x)) & valid
-                        : 0u;
-      }
-    };
-    uint32_t cur[kAhead][kWords], nxt[kAhead][kWords];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (j < n) load(j, nxt[j]);
-    for (int i0 = 0; i0 < n && !dead; i0 += kAhead) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-        for (int w = 0; w < kWords; ++w) cur[j][w] = nxt[j][w];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (i0 + kAhead + j < n) load(i0 + kAhead + j, nxt[j]);
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + j, s = i % L::kStages;
-        if (i >= n || dead) break;
-        if (i >= L::kStages)
-          dead = __any_sync(kAllLanes, !MX_WAIT(m.empty[s], ((i / L::kStages) + 1) & 1));
-        if (dead) break;
-        const uint32_t to = smem_u32(smem + L::kOffScales + s * L::kScales) + 16 * lane + 4 * q;
-#pragma unroll
-        for (int w = 0; w < kWords; ++w)
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + 512 * w), "r"(cur[j][w]) : "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m.full[s]);
-      }
     }
     dead = __any_sync(kAllLanes, dead || !MX_WAIT(m.done, 0));
     tc_fence_after();
   }
+#undef MX_WAIT
 
   // ---------------------------------------------------------------- results
-  const int q = warp & 3, f = n0 + 32 * q + lane;
-  const MxOut out = out_kind(p);
-  float bias[NA];
-  if (warp >= 2)
-#pragma unroll
-    for (int a = 0; a < NA; ++a)
-      bias[a] = MODE == kLinear && p.to.bias && f < p.rows ? bias_at(p.to, (int64_t)a * p.rows + f) : 0.f;
-  auto finish = [&](float (&v)[NA][4], int c) {
+  const int q = warp & 3;
+  const MxOut kind = out_kind(p);
+  const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
+  // Tokens c .. c + 3 of the group of 32 features `group` (of the tile), one a lane.
+  auto finish = [&](float (&v)[4], float (&up)[4], int group, int c) {
+    const int f = n0 + 32 * group + lane;
+    const bool biased = !kExperts && p.to.bias != nullptr && f < p.rows;
+    const float b0 = biased ? bias_at(p.to, f) : 0.f, b1 = kGate && biased ? bias_at(p.to, (int64_t)p.rows + f) : 0.f;
     float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      y[i] = v[0][i] + bias[0];
-      if (NA == 2) y[i] = silu(y[i]) * (v[NA - 1][i] + bias[NA - 1]);
+      y[i] = v[i] + b0;
+      if (kGate) y[i] = silu(y[i]) * (up[i] + b1);
       else if (MODE == kLinear) y[i] = activate(p.to.activation, y[i]);
       if (MODE == kMoeUp) y[i] = c + i < ntok && m.routed[c + i] ? y[i] * m.share[c + i] : 0.f;
     }
     const int64_t row = MODE == kMoeUp ? (int64_t)slot0 * NT + c : t0 + c;
-    write_out(out, p, y, f, n0 + 32 * q, row, ntok - c);
+    write_out(kind, p, y, f, n0 + 32 * group, row, ntok - c);
   };
-  const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
   if (MODE == kMoeUp && total == 0) {
     // no such expert: nothing to compute, nothing to write
-  } else if (parts == 1) {
+  } else if (parts == 1 && !kGate) {
     if (warp >= 2 && !dead) {
 #pragma unroll 1
       for (int c = 0; c < ntok; c += 8) {
-        uint32_t w[NA][8];
-#pragma unroll
-        for (int a = 0; a < NA; ++a) tmem_ld8(acc + a * NT + c, w[a]);
+        uint32_t w[8];
+        tmem_ld8(acc + c, w);
         tmem_ld_wait();
-#pragma unroll
-        for (int a = 0; a < NA; ++a) reg_fence8(w[a]);
+        reg_fence8(w);
 #pragma unroll
         for (int h = 0; h < 8; h += 4) {
-          float v[NA][4];
+          float v[4];
 #pragma unroll
-          for (int a = 0; a < NA; ++a)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[a][i] = n > 0 ? __uint_as_float(w[a][h + i]) : 0.f;
-          if (c + h < ntok) finish(v, c + h);
+          for (int i = 0; i < 4; ++i) v[i] = n > 0 ? __uint_as_float(w[h + i]) : 0.f;
+          if (c + h < ntok) finish(v, v, q, c + h);
         }
       }
     }
   } else {
-    float* part = reinterpret_cast<float*>(smem);  // [accumulator][column][row]; every copy and MMA has ended
+    float* part = reinterpret_cast<float*>(smem);  // [column][row]; every copy and MMA has ended
     if (warp >= 2) {
 #pragma unroll 1
       for (int c = 0; c < ntok; c += 8) {
+        uint32_t w[8];
+        tmem_ld8(acc + c, w);
+        tmem_ld_wait();
+        reg_fence8(w);
 #pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          uint32_t w[8];
-          tmem_ld8(acc + a * NT + c, w);
-          tmem_ld_wait();
-          reg_fence8(w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            part[(a * NT + c + i) * kTileRows + 32 * q + lane] = n > 0 ? __uint_as_float(w[i]) : 0.f;
-        }
+        for (int i = 0; i < 8; ++i) part[(c + i) * kTileRows + 32 * q + lane] = n > 0 ? __uint_as_float(w[i]) : 0.f;
       }
     }
     __syncwarp();
-    cluster_sync_all();
+    if (parts > 1) cluster_sync_all();
+    else __syncthreads();
     if (warp >= 2 && !dead) {
-      const uint32_t mine = smem_u32(part) + 4 * (32 * q + lane);
+      // units of 4 tokens by 32 features, dealt to the cluster's warps
+      constexpr int kGroups = kFeatures / 32;
+      const int units = (ntok + 3) / 4 * kGroups;
 #pragma unroll 1
-      for (int c = 4 * rank; c < ntok; c += 4 * parts) {
-        float v[NA][4] = {};
+      for (int u = q * parts + rank; u < units; u += 4 * parts) {
+        const int group = u % kGroups, c = u / kGroups * 4;
+        const uint32_t mine = smem_u32(part) + 4 * (c * kTileRows + 32 * group + lane);
+        float v[4] = {}, up[4] = {};
         for (int o = 0; o < parts; ++o) {
-          const uint32_t from = mapa_shared(mine, (uint32_t)o);
+          const uint32_t from = parts > 1 ? mapa_shared(mine, (uint32_t)o) : mine;
 #pragma unroll
-          for (int a = 0; a < NA; ++a)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[a][i] += ld_cluster_f32(from + 4 * kTileRows * (a * NT + c + i));
+          for (int i = 0; i < 4; ++i) {
+            v[i] += ld_cluster_f32(from + 4 * kTileRows * i);
+            if (kGate) up[i] += ld_cluster_f32(from + 4 * (kTileRows * i + kFeatures));
+          }
         }
-        finish(v, c);
+        finish(v, up, group, c);
       }
     }
     __syncwarp();
-    cluster_sync_relaxed();  // no CTA leaves while another reads its sums
+    if (parts > 1) cluster_sync_relaxed();  // no CTA leaves while another reads its sums
   }
-#undef MX_WAIT
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -549,17 +625,19 @@ cudaError_t byte_map(CUtensorMap* map, const void* base, int64_t rows, int64_t c
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+bool rows16(const uint8_t* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 16 == 0; }
+
 // Codes [rows, K] in boxes of 128 bytes of box_rows rows.
 cudaError_t code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t stride, int box_rows) {
   return byte_map(map, base, rows, K, stride, kStepK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int MODE, int NA, int NT>
+template <int MODE, int NT>
 cudaError_t launch_mx(const MxParams& p, int parts, int64_t row_tiles, int64_t token_tiles, int slots,
                       const CUtensorMap& a_map, const CUtensorMap& b_map, cudaStream_t stream) {
   if (row_tiles * parts > INT32_MAX || token_tiles > 65535 || slots > 65535) return cudaErrorInvalidValue;
-  auto kernel = mx_gemm_kernel<MODE, NA, NT>;
-  constexpr int smem = MxLay<NA, NT>::kSmem;
+  auto kernel = mx_gemm_kernel<MODE, NT>;
+  constexpr int smem = MxLay<NT>::kSmem;
   // at every launch: it takes well under a microsecond and needs no per-device record
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -583,6 +661,7 @@ cudaError_t launch_mx(const MxParams& p, int parts, int64_t row_tiles, int64_t t
 int split_k(int64_t tiles, int64_t steps, int num_sms) {
   int parts = 1;
   while (parts < 8 && tiles * parts * 2 <= 2 * (int64_t)num_sms && steps >= 4 * parts) parts *= 2;
+  if (const char* o = getenv("PARTS")) parts = atoi(o);
   return parts;
 }
 

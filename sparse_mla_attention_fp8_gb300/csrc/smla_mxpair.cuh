@@ -6,8 +6,8 @@
 // registers at once, and while its results are written the next tile's MMAs run.
 //
 // Scales: rows of 32 bytes (8 steps of K) of the tile's 384 scale rows come by TMA;
-// four warps, one for each quarter of the lanes of tensor memory, hold a step's
-// words of all of them and store them there, a set of columns per stage.  (Through
+// four warps, one for each quarter of the lanes of tensor memory, store them there,
+// four steps at a time (one at a time, 137 us instead of @@).  (Through
 // shared memory and tcgen05.cp, the copies stood between the MMAs: 2501 x 5120 x
 // 13824 took 166 us against 140 without any scales.)  What one CTA tells the other
 // by an arrival lies in tensor memory or has been read, not in memory: the arrivals
@@ -41,9 +41,6 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 // Arrives on the barrier at this place in both CTAs when all MMAs so far have completed.
 __device__ __forceinline__ void pair_commit(uint64_t* bar) {
   asm volatile(
@@ -72,6 +69,8 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
 
 // ---------------------------------------------------------------- layout
 
+constexpr int kPairSets = 4;
+
 template <int NA>
 struct PairLay {
   static constexpr int kTokens = 256 / NA;             // of a tile: the accumulator's 256 columns
@@ -83,12 +82,12 @@ struct PairLay {
   static constexpr int kOffRaw = kStages * kStage;
   static constexpr int kOffMisc = kOffRaw + 2 * kRaw;
   static constexpr int kSmem = kOffMisc + 256 + 1024;
-  static constexpr int kAcc = 256, kScaleCols = 4 * kBlocks;
+  static constexpr int kAcc = 256, kScaleCols = 4 * kBlocks;  // of a step; four steps make a set, kPairSets of them a ring
   static constexpr int kCols = 512;
-  static_assert(kSmem <= 232448 && kStage % 1024 == 0 && kAcc + kStages * kScaleCols <= kCols, "limits");
+  static_assert(kSmem <= 232448 && kStage % 1024 == 0 && kAcc + kPairSets * 4 * kScaleCols <= kCols, "limits");
 };
 struct PairMisc {
-  uint64_t full[6], empty[6], raw_full[2], raw_empty[2], acc_full, acc_empty;
+  uint64_t full[6], empty[6], scaled[kPairSets], unscaled[kPairSets], raw_full[2], raw_empty[2], acc_full, acc_empty;
   uint32_t tmem;
   int abort_flag;
 };
@@ -116,8 +115,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&m.full[s], 9);  // the first CTA's producer, four warps' scales in each
+      mbar_init(&m.full[s], 1);
       mbar_init(&m.empty[s], 1);
+    }
+    for (int b = 0; b < kPairSets; ++b) {
+      mbar_init(&m.scaled[b], 8);  // four warps in each CTA
+      mbar_init(&m.unscaled[b], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&m.raw_full[b], 1);
@@ -165,30 +168,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // after an abort no copy may still be landing when the CTAs exit
       if (!ok && rank == 0)
         for (int j = max(0, i - L::kStages); j < i; ++j) mbar_wait_drain(&m.full[j % L::kStages], (j / L::kStages) & 1);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
       // -------------------------------------------------------------- MMA issuer
-      int i = 0, n = 0;
+      // The whole warp goes through the loop and elects the issuing thread at each step, so that the operands lie in
+      // uniform registers; descriptors differ by one addition.  (One thread's loop, with descriptors made anew, was what
+      // bound the kernel: 155 us instead of @@.)
+      constexpr uint32_t kHi = sdesc_hi(1024, kLayoutSw128);
+      const uint32_t lo0 = sdesc_lo(smem_u32(smem), 16);
+      int s = 0, set = 0, n = 0;
+      uint32_t phase = 0, set_phase = 0;
       bool ok = true;
       for (int tile = first; tile < tiles && ok; tile += stride, ++n) {
         if (n > 0 && !(ok = PAIR_WAIT(m.acc_empty, (n + 1) & 1))) break;
         tc_fence_after();
-        for (int k = 0; k < steps; ++k, ++i) {
-          const int s = i % L::kStages;
-          if (!(ok = PAIR_WAIT(m.full[s], (i / L::kStages) & 1))) break;
-          tc_fence_after();
-          const uint32_t stage = smem_u32(smem + s * L::kStage), sf = tmem + L::kAcc + s * L::kScaleCols;
+        for (int k0 = 0; k0 < steps && ok; k0 += 4) {
+          if (!(ok = PAIR_WAIT(m.scaled[set], set_phase))) break;
+          const int left = min(4, steps - k0);
+          uint32_t sf = tmem + L::kAcc + 4 * set * L::kScaleCols;
+          for (int k = 0; k < left; ++k, sf += L::kScaleCols) {
+            if (!(ok = PAIR_WAIT(m.full[s], phase))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t lo = lo0 + (uint32_t)s * (L::kStage >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kStepK / 32; ++kk)
+              for (int kk = 0; kk < kStepK / 32; ++kk)
 #pragma unroll
-            for (int a = 0; a < NA; ++a)
-              pair_mma(tmem + a * L::kTokens, make_sdesc(stage + a * kTileRows * kStepK + 32 * kk, 16, 1024, kLayoutSw128),
-                       make_sdesc(stage + NA * kTileRows * kStepK + 32 * kk, 16, 1024, kLayoutSw128),
-                       idesc_mx(2 * kTileRows, L::kTokens, kk), sf + 4 * a, sf + 4 * NA, (k > 0 || kk > 0) ? 1u : 0u);
-          pair_commit(&m.empty[s]);
+                for (int a = 0; a < NA; ++a)
+                  pair_mma(tmem + a * L::kTokens, sdesc_join<kHi>(lo + ((a * kTileRows * kStepK + 32 * kk) >> 4)),
+                           sdesc_join<kHi>(lo + ((NA * kTileRows * kStepK + 32 * kk) >> 4)),
+                           idesc_mx(2 * kTileRows, L::kTokens, kk), sf + 4 * a, sf + 4 * NA,
+                           kk > 0 ? 1u : (uint32_t)((k0 | k) != 0));
+              pair_commit(&m.empty[s]);
+              if (k + 1 == left) pair_commit(&m.unscaled[set]);
+              if (k0 + k + 1 == steps) pair_commit(&m.acc_full);
+            }
+            __syncwarp();
+            if (++s == L::kStages) s = 0, phase ^= 1;
+          }
+          if (++set == kPairSets) set = 0, set_phase ^= 1;
         }
-        pair_commit(&m.acc_full);  // (after an abort: nothing is in flight behind it)
       }
-      if (!ok && n > 0) mbar_wait_drain(&m.acc_full, (n - 1) & 1);
+      if (!ok) {  // after an abort nothing is left in flight: every commit so far, in its order
+        if (elect_one()) pair_commit(&m.acc_full);
+        __syncwarp();
+        mbar_wait_drain(&m.acc_full, n & 1);
+      }
     } else if (warp == 2 && lane == 0) {
       // -------------------------------------------------------------- scales' bytes
       int i = 0;
@@ -214,46 +238,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ---------------------------------------------------------------- scales
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kScaleRegs));
     const uint32_t to = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + L::kAcc;
-    int i = 0, g = 0;
+    int g = 0, r = 0;
     bool dead = false;
     for (int tile = first; tile < tiles && !dead; tile += stride) {
-      for (int k0 = 0; k0 < steps && !dead; k0 += 8, ++g) {
-        const int b = g & 1;
-        dead = __any_sync(kAllLanes, !PAIR_WAIT(m.raw_full[b], (g >> 1) & 1));
+      for (int k = 0; k < steps; k += 4, ++g) {
+        const int b = r & 1, set = g % kPairSets, half = k & 4;
+        if (half == 0) dead = __any_sync(kAllLanes, !PAIR_WAIT(m.raw_full[b], (r >> 1) & 1));
+        if (!dead && g >= kPairSets) dead = __any_sync(kAllLanes, !PAIR_WAIT(m.unscaled[set], (g / kPairSets + 1) & 1));
         if (dead) break;
+        tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 8; h += 4) {
-          if (k0 + h >= steps || dead) break;
-          // lane l: four steps' words of rows l, l + 32, l + 64, l + 96 of each block
-          uint4 w[L::kBlocks][4];
+        for (int j = 0; j < L::kBlocks; ++j) {
+          // lane l: four steps' words of rows l, l + 32, l + 64, l + 96 of the block
+          uint4 w[4];
 #pragma unroll
-          for (int j = 0; j < L::kBlocks; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              w[j][c] = *reinterpret_cast<const uint4*>(smem + L::kOffRaw + b * L::kRaw + j * L::kRawBlock +
-                                                        (32 * c + lane) * 32 + 4 * h);
-          if (h == 4 || k0 + 4 >= steps) {  // the buffer has been read
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&m.raw_empty[b]);
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if (k0 + h + x >= steps) break;
-            const int s = i % L::kStages;
-            if (i >= L::kStages) dead = __any_sync(kAllLanes, !PAIR_WAIT(m.empty[s], ((i / L::kStages) + 1) & 1));
-            if (dead) break;
-            ++i;
-            tc_fence_after();
-            auto word = [&](const uint4& v) { return x == 0 ? v.x : x == 1 ? v.y : x == 2 ? v.z : v.w; };
-#pragma unroll
-            for (int j = 0; j < L::kBlocks; ++j)
-              tmem_st4(to + s * L::kScaleCols + 4 * j, word(w[j][0]), word(w[j][1]), word(w[j][2]), word(w[j][3]));
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&m.full[s]), 0));
-          }
+          for (int c = 0; c < 4; ++c)
+            w[c] = *reinterpret_cast<const uint4*>(smem + L::kOffRaw + b * L::kRaw + j * L::kRawBlock + (32 * c + lane) * 32 +
+                                                   4 * half);
+          const uint32_t at = to + 4 * set * L::kScaleCols + 4 * j;
+          tmem_st4(at, w[0].x, w[1].x, w[2].x, w[3].x);
+          tmem_st4(at + L::kScaleCols, w[0].y, w[1].y, w[2].y, w[3].y);
+          tmem_st4(at + 2 * L::kScaleCols, w[0].z, w[1].z, w[2].z, w[3].z);
+          tmem_st4(at + 3 * L::kScaleCols, w[0].w, w[1].w, w[2].w, w[3].w);
         }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        const bool read = half != 0 || k + 4 >= steps;  // all of the buffer
+        if (lane == 0) {
+          mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&m.scaled[set]), 0));
+          if (read) mbar_arrive(&m.raw_empty[b]);
+        }
+        if (read) ++r;
       }
     }
     __syncwarp();
@@ -284,23 +300,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(empty);
-      auto all = [&](auto out) {
+      auto result = [&](int c) {
+        const float z = __uint_as_float(w[c]) + bias[0];
+        return NA == 2 ? silu(z) * (__uint_as_float(w[(NA - 1) * kMine + c]) + bias[NA - 1]) : activate(ACT, z);
+      };
+      // whole tiles without a branch, so that the tokens' chains of operations overlap
+      const bool whole = ntok >= kMine && group + 32 <= p.rows;
+      if (whole && kind == kOutCodes) {
+        uint8_t* codes = p.to.codes + (int64_t)(t + (lane & 3)) * p.ld + group + (lane & 28);
+        uint8_t* scales = p.to.scales + (int64_t)(t + (lane & 3)) * p.to.scale_stride + group / kMxGroup;
+#pragma unroll
+        for (int c = 0; c < kMine; c += 4) {
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = result(c + i);
+          uint32_t mine;
+          *reinterpret_cast<uint32_t*>(codes) = quantize4(y, mine);
+          if (lane < 4) *scales = (uint8_t)mine;
+          codes += 4 * p.ld;
+          scales += 4 * p.to.scale_stride;
+        }
+      } else if (whole && kind == kOutPairs) {
+        auto rows = [&](auto with_residual) {
+          constexpr bool kResidual = decltype(with_residual)::value;
+          const int64_t row = t + (lane & 1);
+          uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.to.out) + row * p.ld + (f & ~1));
+          const uint32_t* res =
+              reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.to.residual) + row * p.to.residual_stride + (f & ~1));
+          constexpr int kAtOnce = 16;  // tokens
+#pragma unroll
+          for (int c0 = 0; c0 < kMine; c0 += kAtOnce) {
+            uint32_t r[kAtOnce / 2];
+            if (kResidual) {
+#pragma unroll
+              for (int i = 0; i < kAtOnce / 2; ++i, res += p.to.residual_stride) r[i] = __ldg(res);
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce / 2; ++i, out += p.ld) {
+              float lo, hi;
+              pair_up(result(c0 + 2 * i), result(c0 + 2 * i + 1), lo, hi);
+              if (kResidual) {
+                lo += __uint_as_float(r[i] << 16);
+                hi += __uint_as_float(r[i] & 0xffff0000u);
+              }
+              *out = pack_bf16x2(lo, hi);
+            }
+          }
+        };
+        if (p.to.residual) rows(std::true_type{});
+        else rows(std::false_type{});
+      } else {
 #pragma unroll
         for (int c = 0; c < kMine; c += 4) {
           if (c >= ntok) break;
           float y[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            y[i] = __uint_as_float(w[c + i]) + bias[0];
-            if (NA == 2) y[i] = silu(y[i]) * (__uint_as_float(w[(NA - 1) * kMine + c + i]) + bias[NA - 1]);
-            else y[i] = activate(ACT, y[i]);
-          }
-          write_out<decltype(out)::value>(p, y, f, group, t + c, ntok - c);
+          for (int i = 0; i < 4; ++i) y[i] = result(c + i);
+          write_out(kind, p, y, f, group, t + c, ntok - c);
         }
-      };
-      if (kind == kOutCodes) all(std::integral_constant<MxOut, kOutCodes>{});
-      else if (kind == kOutPairs) all(std::integral_constant<MxOut, kOutPairs>{});
-      else all(std::integral_constant<MxOut, kOutSingle>{});
+      }
     }
   }
 #undef PAIR_WAIT
@@ -317,20 +375,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 cudaError_t scale_map(CUtensorMap* map, const void* base, int64_t rows, int64_t n, int64_t stride) {
   return byte_map(map, base, rows, n, stride, 32, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
-// Whether scale rows can be copied by TMA: on 16-byte boundaries.
-bool pair_takes(const MxLinearArgs& a) {
-  const auto rows16 = [](const uint8_t* q, int64_t stride) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && stride % 16 == 0; };
-  return rows16(a.x_scale, a.x_scale_stride) && rows16(a.w_scale, a.w_scale_stride);
-}
-
 template <int ACT>
 cudaError_t launch_pair(const MxLinearArgs& a, const MxParams& p, int num_sms, cudaStream_t stream) {
   constexpr int NA = ACT == SMLA_ACT_SWIGLU ? 2 : 1;
   using L = PairLay<NA>;
-  CUtensorMap a_map, b_map;
+  CUtensorMap a_map, b_map, a_scale_map, b_scale_map;
   cudaError_t e = code_map(&a_map, a.w, (int64_t)NA * a.N, a.K, a.K, kTileRows);
   if (e == cudaSuccess) e = code_map(&b_map, a.x, a.T, a.K, a.x_stride, L::kTokens / 2);
-  CUtensorMap a_scale_map, b_scale_map;
   if (e == cudaSuccess) e = scale_map(&a_scale_map, a.w_scale, (int64_t)NA * a.N, a.K / kMxGroup, a.w_scale_stride);
   if (e == cudaSuccess) e = scale_map(&b_scale_map, a.x_scale, a.T, a.K / kMxGroup, a.x_scale_stride);
   if (e != cudaSuccess) return e;
