@@ -937,7 +937,10 @@ int rms_norm_mxfp8(const void* x, int64_t x_stride, const void* residual, int64_
   if (!codes && !normed && !residual_out) return fail(SMLA_ERR_INVALID_ARG, "no output is asked for");
   const smla::MxNormArgs a{x,     x_stride, residual,     residual_stride, weight, weight_type == SMLA_F32, eps, codes,
                            scales, scale_stride, normed, residual_out,    T,      K};
-  cudaError_t e = smla::launch_mx_norm(a, static_cast<cudaStream_t>(stream));
+  int sms = 0;
+  rc = num_sms(&sms);
+  if (rc != SMLA_OK) return rc;
+  cudaError_t e = smla::launch_mx_norm(a, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rms_norm_mxfp8 launch");
   return SMLA_OK;
 }

@@ -218,7 +218,7 @@ struct MxNormArgs {
 constexpr int kMaxNormK = 65536;  // a row is held in one CTA's registers
 // (smla_mxnorm.cu)
 cudaError_t launch_mx_quantize(const MxQuantizeArgs& a, cudaStream_t stream);
-cudaError_t launch_mx_norm(const MxNormArgs& a, cudaStream_t stream);
+cudaError_t launch_mx_norm(const MxNormArgs& a, int num_sms, cudaStream_t stream);
 
 // What a product's results go through and where they go.
 struct MxEpilogue {

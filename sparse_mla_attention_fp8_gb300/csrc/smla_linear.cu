@@ -42,7 +42,12 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t st
   const auto even = [](const void* q, int64_t stride) { return stride % 2 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0; };
   p.pairs = even(a.to.out, a.N) && (!a.to.residual || even(a.to.residual, a.to.residual_stride));
   p.wide_scales = rows16(a.x_scale, a.x_scale_stride) && rows16(a.w_scale, a.w_scale_stride);
-  if (a.T > (getenv("PAIRT") ? atoi(getenv("PAIRT")) : 256) && p.wide_scales) {  // (scale rows that TMA can copy)
+  // Pairs of CTAs where they have 24 tiles or more (and TMA can copy the scale rows): with K = 4096 and N = 4096, 16 tiles
+  // (256 tokens) take 14.8 us and the other kernel 15.8, 32 (300 tokens) 15.0 and 22.4; with K = 8192 and N = 1024, 16
+  // (800 tokens) 23.5 and 21.0; up to 64 tokens the other kernel's tiles of fewer columns have less to do.
+  const int64_t columns = a.to.activation == SMLA_ACT_SWIGLU ? 128 : 256;
+  const int64_t pair_tiles = ((int64_t)a.N + 255) / 256 * ((a.T + columns - 1) / columns);
+  if (p.wide_scales && a.T > 64 && pair_tiles >= 24) {
     switch (a.to.activation) {
       case SMLA_ACT_NONE: return launch_pair<SMLA_ACT_NONE>(a, p, num_sms, stream);
       case SMLA_ACT_RELU: return launch_pair<SMLA_ACT_RELU>(a, p, num_sms, stream);

@@ -23,7 +23,6 @@
 #pragma once
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 #include <mutex>
 #include <type_traits>
 #include <cuda.h>
@@ -661,7 +660,6 @@ cudaError_t launch_mx(const MxParams& p, int parts, int64_t row_tiles, int64_t t
 int split_k(int64_t tiles, int64_t steps, int num_sms) {
   int parts = 1;
   while (parts < 8 && tiles * parts * 2 <= 2 * (int64_t)num_sms && steps >= 4 * parts) parts *= 2;
-  if (const char* o = getenv("PARTS")) parts = atoi(o);
   return parts;
 }
 

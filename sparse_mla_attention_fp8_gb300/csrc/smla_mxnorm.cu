@@ -39,16 +39,30 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// The codes of 8 of a group's 32 values, its other 24 in the other lanes of this
-// four (all of them active); the first of them writes the scale.
-__device__ __forceinline__ void store_codes(const float (&v)[8], uint8_t* codes, uint8_t* scale) {
+// The scale's exponent of a group of 32 values, kCount of them here and the others in the other lanes of these
+// 32 / kCount (all of them active).
+template <int kCount>
+__device__ __forceinline__ int group_exponent(const float (&v)[kCount]) {
+  constexpr int kLanes = 32 / kCount;
+  const uint32_t lanes = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
   uint32_t top = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, mx_finite_bits(v[i]));
-  const uint32_t quad = 0xfu << (threadIdx.x & 28u);
-  top = max(top, __shfl_xor_sync(quad, top, 1));
-  top = max(top, __shfl_xor_sync(quad, top, 2));
-  const int e = mx_exponent(top);
+  for (int i = 0; i < kCount; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+  for (int d = 1; d < kLanes; d *= 2) top = max(top, __shfl_xor_sync(lanes, top, d));
+  if (top >= 0x7f800000u) {  // infinities and NaN are left out
+    top = 0u;
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) top = max(top, mx_finite_bits(v[i]));
+#pragma unroll
+    for (int d = 1; d < kLanes; d *= 2) top = max(top, __shfl_xor_sync(lanes, top, d));
+  }
+  return mx_exponent(top);
+}
+
+// The codes of 8 of a group's values; the first of its four threads writes the scale.
+__device__ __forceinline__ void store_codes(const float (&v)[8], uint8_t* codes, uint8_t* scale) {
+  const int e = group_exponent(v);
   const float inv = mx_pow2(-e);
   *reinterpret_cast<uint2*>(codes) = make_uint2(mx_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
                                                 mx_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
@@ -57,87 +71,110 @@ __device__ __forceinline__ void store_codes(const float (&v)[8], uint8_t* codes,
 
 constexpr int kQuantThreads = 256;
 
+// 16 values a thread, two threads a group.
 template <typename X>
 __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_constant__ MxQuantizeArgs a) {
   grid_dependency_wait();
-  const uint32_t per_row = (uint32_t)a.K / 8;
-  const uint64_t i = (uint64_t)blockIdx.x * kQuantThreads + threadIdx.x;
-  if (i >= (uint64_t)a.T * per_row) return;  // (a group's four threads go together)
-  const uint32_t row = (uint32_t)(i / per_row), col = (uint32_t)(i - (uint64_t)row * per_row) * 8;
-  float v[8];
-  load8(static_cast<const X*>(a.x) + row * a.x_stride + col, v);
-  store_codes(v, a.codes + (int64_t)row * a.K + col, a.scales + row * a.scale_stride + col / kMxGroup);
+  const uint32_t per_row = (uint32_t)a.K / 16, count = (uint32_t)a.T * per_row;  // (below 2^32 by the launch)
+  const uint32_t i = blockIdx.x * kQuantThreads + threadIdx.x;
+  if (i >= count) return;  // (a group's two threads go together)
+  const uint32_t row = i / per_row, col = (i - row * per_row) * 16;
+  const X* x = static_cast<const X*>(a.x) + row * a.x_stride + col;
+  float lo[8], hi[8], v[16];
+  load8(x, lo);
+  load8(x + 8, hi);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = lo[k], v[8 + k] = hi[k];
+  const int e = group_exponent(v);
+  const float inv = mx_pow2(-e);
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = mx_e4m3x4(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
+  *reinterpret_cast<uint4*>(a.codes + (int64_t)row * a.K + col) = make_uint4(w[0], w[1], w[2], w[3]);
+  if ((threadIdx.x & 1) == 0) a.scales[row * a.scale_stride + col / kMxGroup] = (uint8_t)(e + 127);
 }
 
-// One row by kWarps warps, kChunks groups of 8 values a thread; a CTA has
-// kRows rows.
-template <int kWarps, int kChunks, int kRows, typename W>
-__global__ void __launch_bounds__(32 * kWarps * kRows) norm_kernel(const __grid_constant__ MxNormArgs a) {
-  __shared__ float part[kRows][kWarps];
-  constexpr int kThreads = 32 * kWarps;
-  const int r = (int)threadIdx.x / kThreads, t = (int)threadIdx.x % kThreads;
-  const int64_t row = (int64_t)blockIdx.x * kRows + r;
-  const bool mine = row < a.T;
+// Rows by CTAs of whole warps, kChunks groups of 8 values a thread.  A CTA takes every gridDim-th row and (where
+// registers allow) loads the next one before it has the sum of the present one.
+template <int kChunks, typename W>
+__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ MxNormArgs a) {
+  constexpr bool kAhead = kChunks <= 2;
+  __shared__ float part[2][32];
+  const int t = (int)threadIdx.x, threads = (int)blockDim.x, warps = threads / 32;
+  const int col0 = 8 * t;
   grid_dependency_wait();
-  uint4 h[kChunks];
-  float sum = 0.f;
+  uint4 x[kAhead ? kChunks : 1], r[kAhead ? kChunks : 1];
+  auto load = [&](int64_t row, int c, uint4& x, uint4& r) {
+    const int col = col0 + 8 * threads * c;
+    x = r = make_uint4(0u, 0u, 0u, 0u);
+    if (row >= a.T || col >= a.K) return;
+    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + row * a.x_stride + col));
+    if (a.residual)
+      r = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.residual) + row * a.residual_stride + col));
+  };
+  if (kAhead)
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const int col = 8 * (c * kThreads + t);
-    h[c] = make_uint4(0u, 0u, 0u, 0u);
-    if (!mine || col >= a.K) continue;
-    float v[8];
-    load8(static_cast<const __nv_bfloat16*>(a.x) + row * a.x_stride + col, v);
-    if (a.residual) {
-      float u[8];
-      load8(static_cast<const __nv_bfloat16*>(a.residual) + row * a.residual_stride + col, u);
+    for (int c = 0; c < kChunks; ++c) load(blockIdx.x, c, x[c], r[c]);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
+    uint4 h[kChunks];
+    float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += u[i];
+    for (int c = 0; c < kChunks; ++c) {
+      const int k = kAhead ? c : 0;
+      if (!kAhead) load(row, c, x[k], r[k]);
+      const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, v[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = u[i];
+        if (a.residual)
+          w[i] = pack_bf16x2(__uint_as_float(u[i] << 16) + __uint_as_float(v[i] << 16),
+                             __uint_as_float(u[i] & 0xffff0000u) + __uint_as_float(v[i] & 0xffff0000u));
+        const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+        sum = fmaf(lo, lo, fmaf(hi, hi, sum));
+      }
+      h[c] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    h[c] = pack8(v);
-  }
+    if (kAhead)
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const int col = 8 * (c * kThreads + t);
-    if (a.residual_out && mine && col < a.K)
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.residual_out) + row * a.K + col) = h[c];
-    const uint32_t u[4] = {h[c].x, h[c].y, h[c].z, h[c].w};
+      for (int c = 0; c < kChunks; ++c) load(row + gridDim.x, c, x[c], r[c]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float lo = __uint_as_float(u[i] << 16), hi = __uint_as_float(u[i] & 0xffff0000u);
-      sum = fmaf(lo, lo, fmaf(hi, hi, sum));
+    for (int c = 0; c < kChunks; ++c) {
+      const int col = col0 + 8 * threads * c;
+      if (a.residual_out && col < a.K)
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.residual_out) + row * a.K + col) = h[c];
     }
-  }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
-  if (kWarps > 1) {
-    if ((t & 31) == 0) part[r][t >> 5] = sum;
-    __syncthreads();
-    sum = 0.f;
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+    if (warps > 1) {
+      if ((t & 31) == 0) part[turn][t >> 5] = sum;
+      __syncthreads();
+      sum = (t & 31) < warps ? part[turn][t & 31] : 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += part[r][w];
-  }
-  if (!mine) return;
-  const float f = rsqrtf(sum / (float)a.K + a.eps);
-#pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    const int col = 8 * (c * kThreads + t);
-    if (col >= a.K) break;
-    float y[8];
-    const uint32_t u[4] = {h[c].x, h[c].y, h[c].z, h[c].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[2 * i] = __uint_as_float(u[i] << 16) * f;
-      y[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * f;
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
     }
-    if (a.weight) {
-      float w[8];
-      load8(static_cast<const W*>(a.weight) + col, w);
+    const float f = rsqrtf(sum / (float)a.K + a.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= w[i];
+    for (int c = 0; c < kChunks; ++c) {
+      const int col = col0 + 8 * threads * c;
+      if (col >= a.K) break;
+      float y[8];
+      const uint32_t u[4] = {h[c].x, h[c].y, h[c].z, h[c].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[2 * i] = __uint_as_float(u[i] << 16) * f;
+        y[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u) * f;
+      }
+      if (a.weight) {
+        float w[8];
+        load8(static_cast<const W*>(a.weight) + col, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] *= w[i];
+      }
+      if (a.normed) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.normed) + row * a.K + col) = pack8(y);
+      if (a.codes) store_codes(y, a.codes + row * a.K + col, a.scales + row * a.scale_stride + col / kMxGroup);
     }
-    if (a.normed) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.normed) + row * a.K + col) = pack8(y);
-    if (a.codes) store_codes(y, a.codes + row * a.K + col, a.scales + row * a.scale_stride + col / kMxGroup);
   }
 }
 
@@ -156,30 +193,44 @@ cudaError_t launch(void (*kernel)(Params...), int64_t ctas, int threads, cudaStr
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// As many CTAs as the SMs hold at once (by their registers: 64 a thread).
+template <int kChunks, typename W>
+cudaError_t launch_rows(const MxNormArgs& a, int num_sms, cudaStream_t stream) {
+  const int threads = (a.K / 8 + kChunks * 32 - 1) / (kChunks * 32) * 32;
+  const int64_t ctas = std::min<int64_t>(a.T, (int64_t)num_sms * std::min(32, 1024 / threads));
+  return launch(norm_kernel<kChunks, W>, ctas, threads, stream, a);
+}
 template <typename W>
-cudaError_t launch_norm(const MxNormArgs& a, cudaStream_t stream) {
-  auto go = [&](auto kernel, int warps, int rows) {
-    return launch(kernel, ((int64_t)a.T + rows - 1) / rows, 32 * warps * rows, stream, a);
-  };
-  if (a.K <= 256) return go(norm_kernel<1, 1, 8, W>, 1, 8);
-  if (a.K <= 1024) return go(norm_kernel<4, 1, 2, W>, 4, 2);
-  if (a.K <= 2048) return go(norm_kernel<8, 1, 1, W>, 8, 1);
-  if (a.K <= 4096) return go(norm_kernel<16, 1, 1, W>, 16, 1);
-  if (a.K <= 8192) return go(norm_kernel<16, 2, 1, W>, 16, 1);
-  if (a.K <= 16384) return go(norm_kernel<16, 4, 1, W>, 16, 1);
-  return go(norm_kernel<32, 8, 1, W>, 32, 1);
+cudaError_t launch_norm(const MxNormArgs& a, int num_sms, cudaStream_t stream) {
+  // For many rows two groups a thread: more rows are in flight on an SM (7000 x 5120 without the bf16 norm 40.9 us, with
+  // one group 53.0; 400 x 4096 3.6 and 3.8; one row is better off with one).
+  const bool many = a.T > 2 * num_sms;
+  if (a.K <= 8 * 1024) return many ? launch_rows<2, W>(a, num_sms, stream) : launch_rows<1, W>(a, num_sms, stream);
+  if (a.K <= 16 * 1024) return launch_rows<2, W>(a, num_sms, stream);
+  if (a.K <= 32 * 1024) return launch_rows<4, W>(a, num_sms, stream);
+  return launch_rows<8, W>(a, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_mx_quantize(const MxQuantizeArgs& a, cudaStream_t stream) {
-  const int64_t ctas = ((int64_t)a.T * (a.K / 8) + kQuantThreads - 1) / kQuantThreads;
-  return a.x_f32 ? launch(quantize_kernel<float>, ctas, kQuantThreads, stream, a)
-                 : launch(quantize_kernel<__nv_bfloat16>, ctas, kQuantThreads, stream, a);
+cudaError_t launch_mx_quantize(const MxQuantizeArgs& all, cudaStream_t stream) {
+  MxQuantizeArgs a = all;
+  const int64_t most = (int64_t{1} << 31) / (a.K / 16) - 1;  // rows a launch
+  cudaError_t e = cudaSuccess;
+  for (int64_t done = 0; done < all.T && e == cudaSuccess; done += a.T) {
+    a.T = (int)std::min<int64_t>(most, all.T - done);
+    a.x = static_cast<const char*>(all.x) + done * all.x_stride * (all.x_f32 ? 4 : 2);
+    a.codes = all.codes + done * all.K;
+    a.scales = all.scales + done * all.scale_stride;
+    const int64_t ctas = ((int64_t)a.T * (a.K / 16) + kQuantThreads - 1) / kQuantThreads;
+    e = a.x_f32 ? launch(quantize_kernel<float>, ctas, kQuantThreads, stream, a)
+                : launch(quantize_kernel<__nv_bfloat16>, ctas, kQuantThreads, stream, a);
+  }
+  return e;
 }
 
-cudaError_t launch_mx_norm(const MxNormArgs& a, cudaStream_t stream) {
-  return a.weight_f32 ? launch_norm<float>(a, stream) : launch_norm<__nv_bfloat16>(a, stream);
+cudaError_t launch_mx_norm(const MxNormArgs& a, int num_sms, cudaStream_t stream) {
+  return a.weight_f32 ? launch_norm<float>(a, num_sms, stream) : launch_norm<__nv_bfloat16>(a, num_sms, stream);
 }
 
 }  // namespace smla

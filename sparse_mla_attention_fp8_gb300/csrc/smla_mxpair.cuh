@@ -304,36 +304,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const float z = __uint_as_float(w[c]) + bias[0];
         return NA == 2 ? silu(z) * (__uint_as_float(w[(NA - 1) * kMine + c]) + bias[NA - 1]) : activate(ACT, z);
       };
-      // whole tiles without a branch, so that the tokens' chains of operations overlap
-      const bool whole = ntok >= kMine && group + 32 <= p.rows;
-      if (whole && kind == kOutCodes) {
+      // 16 tokens at a time without a branch, so that their chains of operations overlap
+      constexpr int kAtOnce = 16;
+      if (kind == kOutCodes && group < p.rows) {
         uint8_t* codes = p.to.codes + (int64_t)(t + (lane & 3)) * p.ld + group + (lane & 28);
         uint8_t* scales = p.to.scales + (int64_t)(t + (lane & 3)) * p.to.scale_stride + group / kMxGroup;
 #pragma unroll
-        for (int c = 0; c < kMine; c += 4) {
-          float y[4];
+        for (int c0 = 0; c0 < kMine; c0 += kAtOnce) {
+          if (c0 >= ntok) break;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = result(c + i);
-          uint32_t mine;
-          *reinterpret_cast<uint32_t*>(codes) = quantize4(y, mine);
-          if (lane < 4) *scales = (uint8_t)mine;
-          codes += 4 * p.ld;
-          scales += 4 * p.to.scale_stride;
+          for (int c = c0; c < c0 + kAtOnce; c += 4) {
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = result(c + i);
+            uint32_t scale;
+            const uint32_t v = quantize4(y, scale);
+            if (c + (lane & 3) < ntok) {
+              *reinterpret_cast<uint32_t*>(codes) = v;
+              if (lane < 4) *scales = (uint8_t)scale;
+            }
+            codes += 4 * p.ld;
+            scales += 4 * p.to.scale_stride;
+          }
         }
-      } else if (whole && kind == kOutPairs) {
+      } else if (kind == kOutPairs) {
+        const int64_t row = t + (lane & 1);
+        const int even = f & ~1, last = even < p.rows ? ntok : 0;  // this lane's tokens
+        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.to.out) + row * p.ld + even);
+        const uint32_t* res = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.to.residual) +
+                                                                row * p.to.residual_stride + even);
         auto rows = [&](auto with_residual) {
           constexpr bool kResidual = decltype(with_residual)::value;
-          const int64_t row = t + (lane & 1);
-          uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.to.out) + row * p.ld + (f & ~1));
-          const uint32_t* res =
-              reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.to.residual) + row * p.to.residual_stride + (f & ~1));
-          constexpr int kAtOnce = 16;  // tokens
 #pragma unroll
           for (int c0 = 0; c0 < kMine; c0 += kAtOnce) {
+            if (c0 >= ntok) break;
             uint32_t r[kAtOnce / 2];
             if (kResidual) {
 #pragma unroll
-              for (int i = 0; i < kAtOnce / 2; ++i, res += p.to.residual_stride) r[i] = __ldg(res);
+              for (int i = 0; i < kAtOnce / 2; ++i, res += p.to.residual_stride)
+                r[i] = c0 + 2 * i + (lane & 1) < last ? __ldg(res) : 0u;
             }
 #pragma unroll
             for (int i = 0; i < kAtOnce / 2; ++i, out += p.ld) {
@@ -343,20 +352,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 lo += __uint_as_float(r[i] << 16);
                 hi += __uint_as_float(r[i] & 0xffff0000u);
               }
-              *out = pack_bf16x2(lo, hi);
+              if (c0 + 2 * i + (lane & 1) < last) *out = pack_bf16x2(lo, hi);
             }
           }
         };
         if (p.to.residual) rows(std::true_type{});
         else rows(std::false_type{});
-      } else {
+      } else if (kind == kOutSingle) {
 #pragma unroll
         for (int c = 0; c < kMine; c += 4) {
           if (c >= ntok) break;
           float y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) y[i] = result(c + i);
-          write_out(kind, p, y, f, group, t + c, ntok - c);
+          write_out<kOutSingle>(p, y, f, group, t + c, ntok - c);
         }
       }
     }

@@ -53,11 +53,12 @@ __device__ __forceinline__ float score_of(bool sigmoid, float x, float top, floa
   return sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) * inv_sum;
 }
 
-// How far a float32 score plus bias may be from the exact one, in units of 2^-24:
-// of the score (at most 1) 2 for the exponential, 1 for its argument's rounding
-// (s |x - top| < 1/2), up to 21 for the sum of 512 of them and 1 for the quotient;
-// and half of one of the sum with the bias.  32 are taken.
-__device__ __forceinline__ float slack(float x) { return 0x1p-19f * (1.f + fabsf(x)); }
+// How far a float32 score plus bias may be from the exact one, in units of 2^-24 of
+// the score (at most 1): 2 for the exponential, 1 for the quotient and one of the
+// sum with the bias; by sigmoid 1 more for the sum with 1 (6 in all, 8 are taken), by
+// softmax 1 for the argument's rounding (s |x - top| < 1/2) and up to 21 for the sum
+// of 512 exponentials (32 are taken).
+__device__ __forceinline__ float slack(bool sigmoid, float x) { return (sigmoid ? 0x1p-21f : 0x1p-19f) * (1.f + fabsf(x)); }
 
 // Ranks a token's experts (keys[i]: of expert 32 i + lane) and takes topk of
 // them, lane k the k-th (-1: there was none).  `near_tie` reports two neighbours
@@ -90,7 +91,7 @@ __device__ __forceinline__ int take(const MoeRouteArgs& a, Bits (&keys)[R], Bits
       const Bits top = warp_max(group);
       if (check && r == a.topk_groups && top) {
         const float lo = (float)value_of(top), hi = (float)value_of(last);
-        near_tie |= hi - lo <= 2.f * (slack(lo) + slack(hi));
+        near_tie |= hi - lo <= 2.f * (slack(a.sigmoid, lo) + slack(a.sigmoid, hi));
       }
       if (r == a.topk_groups || !top) break;
       const int g = __ffs(__ballot_sync(kLanes, group == top)) - 1;
@@ -111,7 +112,7 @@ __device__ __forceinline__ int take(const MoeRouteArgs& a, Bits (&keys)[R], Bits
     const Bits top = warp_max(best);
     if (check && r > 0 && top) {
       const float lo = (float)value_of(top), hi = (float)value_of(last);
-      near_tie |= hi - lo <= slack(lo) + slack(hi);
+      near_tie |= hi - lo <= slack(a.sigmoid, lo) + slack(a.sigmoid, hi);
     }
     if (r == a.topk || !top) break;
     uint32_t at = 0xffffffffu;
