@@ -17,9 +17,9 @@
 //
 // Warp roles: 0 TMA of the codes (128-byte rows and swizzle), 1 MMA issuer, 2..5
 // scales, then results.  The scales of a set of four steps (of 128 values of K) go
-// from global memory through registers into tensor memory, where each warp fills
-// its quarter of the lanes: column 4 b + c holds the 4 bytes of row 32 c + lane of
-// the b-th block of 128 rows.
+// by asynchronous copies into shared memory and from there into tensor memory,
+// where each warp fills its quarter of the lanes: of a step's 8 columns the c-th
+// holds the 4 bytes of W's row 32 c + lane, the (4 + c)-th those of that token.
 #pragma once
 #include <algorithm>
 #include <cstdint>
@@ -43,6 +43,7 @@ constexpr uint32_t kAllLanes = 0xffffffffu;
 constexpr int kStepK = 128;    // values of K per stage: one 128-byte swizzle row
 constexpr int kTileRows = 128; // rows of W per tile
 constexpr int kMxThreads = 6 * 32;
+constexpr int kMaxParts = 8;    // of K: CTAs of a (portable) cluster
 
 // Set when a wait runs out in a kernel of the file that includes this.
 __device__ int g_mx_timed_out;
@@ -73,6 +74,23 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
   return r != 0;
+}
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+// Asynchronous copy of `bytes` (up to 4) bytes, zeros behind them.
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 // An arrival that publishes nothing in memory.
 __device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
@@ -122,12 +140,15 @@ template <int NT>
 struct MxLay {
   static constexpr int kATile = kTileRows * kStepK;
   static constexpr int kStage = kATile + NT * kStepK;
-  static constexpr int kCtas = NT > 64 ? 2 : 3;  // an SM
+  static constexpr int kCtas = 2;  // an SM
   static constexpr int kMisc = 1664;
-  static constexpr int kFit = ((228 / kCtas - 1) * 1024 - 1024 - kMisc) / kStage;
+  static constexpr int kRawSets = NT > 64 ? 3 : 4;  // sets of scales on their way
+  static constexpr int kRaw = kRawSets * (kTileRows + NT) * 16;
+  static constexpr int kFit = ((228 / kCtas - 1) * 1024 - 1024 - kMisc - kRaw) / kStage;
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kPartial = NT * kTileRows * 4;
-  static constexpr int kOffMisc = kStages * kStage;
+  static constexpr int kOffRaw = kStages * kStage;
+  static constexpr int kOffMisc = kOffRaw + kRaw;
   static constexpr int kSmem = kOffMisc + kMisc + 1024;
   static constexpr int kScaleCols = 8;          // of a step: W's block and the tokens'
   static constexpr int kNeed = NT + kSets * kSetSteps * kScaleCols;
@@ -242,13 +263,6 @@ __device__ __forceinline__ void write_out(const MxParams& p, float (&v)[4], int 
     out[(out_row + i) * p.ld + f] = __float2bfloat16_rn(v[i]);
   }
 }
-__device__ __forceinline__ void write_out(MxOut kind, const MxParams& p, float (&v)[4], int f, int group, int64_t out_row,
-                                          int n) {
-  if (kind == kOutCodes) write_out<kOutCodes>(p, v, f, group, out_row, n);
-  else if (kind == kOutPairs) write_out<kOutPairs>(p, v, f, group, out_row, n);
-  else write_out<kOutSingle>(p, v, f, group, out_row, n);
-}
-
 // ---------------------------------------------------------------- the kernel
 
 // grid: x = cluster rank + parts * row tile, y = token tile, z = expert slot (kMoeUp).
@@ -280,6 +294,10 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
     m.abort_flag = 0;
     mbar_fence_init();
   }
+  if (tid == 96) {
+    prefetch_map(&a_map);
+    prefetch_map(&b_map);
+  }
   if (warp == 1) {
     tmem_alloc(&m.tmem, L::kCols);
     tmem_relinquish();
@@ -305,17 +323,17 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
       if (id >= 0 && id < p.E) atomicOr(&m.mask[id >> 5], 1u << (id & 31));
     }
     __syncthreads();
-    if (tid < 32) {
-      const uint32_t word = lane < kMaxMoeExperts / 32 ? m.mask[lane] : 0u;
-      int before = __popc(word);
+    for (int e = tid; e < kMaxMoeExperts; e += kMxThreads) {
+      int before = 0, all = 0;  // experts taken of the words before e's, and of all
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(kAllLanes, before, d);
-        if (lane >= d) before += o;
+      for (int w = 0; w < kMaxMoeExperts / 32; ++w) {
+        const int count = __popc(m.mask[w]);
+        before += w < e / 32 ? count : 0;
+        all += count;
       }
-      int at = before - __popc(word);
-      for (uint32_t w = word; w; w &= w - 1) m.list[at++] = (uint16_t)(32 * lane + __ffs(w) - 1);
-      if (lane == 31) m.active = before;
+      const uint32_t word = m.mask[e / 32], bit = 1u << (e % 32);
+      if (word & bit) m.list[before + __popc(word & (bit - 1u))] = (uint16_t)e;
+      if (e == 0) m.active = all;
     }
     __syncthreads();
     if (MODE == kMoeUp) {
@@ -326,11 +344,12 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
       total = m.active * steps;
     }
   }
-  // Parts of whole sets where the scales of a set can be read at once: 16 bytes of a row, on 16-byte boundaries.
-  const bool wide = p.wide_scales && p.K % (kSetSteps * kStepK) == 0;
+  // Parts of whole sets where the scales of a set can be copied at once: 16 bytes of a row, on 16-byte boundaries.
+  const bool wide = p.wide_scales && (MODE != kMoeDown || steps % kSetSteps == 0);
   const int unit = wide ? kSetSteps : 1;
-  const int k0 = (int)((int64_t)(total / unit) * rank / parts) * unit;
-  const int n = (int)((int64_t)(total / unit) * (rank + 1) / parts) * unit - k0;
+  const int units = (total + unit - 1) / unit;
+  const int k0 = (int)((int64_t)units * rank / parts) * unit;
+  const int n = min(total, (int)((int64_t)units * (rank + 1) / parts) * unit) - k0;
   const int slot0 = MODE == kMoeUp ? (int)(blockIdx.y * p.slots + blockIdx.z) : (int)blockIdx.y * p.slots;
   // Step it's place in its row, and its expert's place in the list.
   auto in_row = [&](int it) { return MODE == kMoeDown ? it % steps : it; };
@@ -341,37 +360,46 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
   bool dead = false;
   if (warp == 0) {
     // ---------------------------------------------------------------- codes
-    if (lane == 0) {
-      auto load_a = [&](int i, int s) {
-        const int it = k0 + i, x = in_row(it) * kStepK, y = expert_of(it) * (kGate ? 2 : 1) * p.rows + n0;
-        const uint32_t stage = smem_u32(smem + s * L::kStage);
-        mbar_arrive_expect_tx(&m.full[s], (uint32_t)L::kStage);
-        tma_load_2d(stage, &a_map, x, y, &m.full[s]);
-        if (kGate) tma_load_2d(stage + L::kATile / 2, &a_map, x, y + p.rows, &m.full[s]);
-      };
-      auto load_b = [&](int i, int s) {
-        const int it = k0 + i;
-        tma_load_2d(smem_u32(smem + s * L::kStage) + L::kATile, &b_map, in_row(it) * kStepK,
-                    MODE == kMoeDown ? (slot0 + in_list(it)) * NT : t0, &m.full[s]);
-      };
-      const int early = MODE == kMoeDown ? min(n, L::kStages) : 0;
-      for (int i = 0; i < early; ++i) load_a(i, i);
-      if (MODE == kMoeDown) grid_dependency_wait();
-      for (int i = 0; i < early; ++i) load_b(i, i);
-      int s = early % L::kStages, issued = early;
-      uint32_t phase = early == L::kStages ? 1u : 0u;  // of the fillings of stage s
-      for (int i = early; i < n; ++i) {
-        if (i >= L::kStages && !MX_WAIT(m.empty[s], phase ^ 1u)) break;
+    auto load_a = [&](int i, int s) {
+      const int it = k0 + i, x = in_row(it) * kStepK, y = expert_of(it) * (kGate ? 2 : 1) * p.rows + n0;
+      const uint32_t stage = smem_u32(smem + s * L::kStage);
+      mbar_arrive_expect_tx(&m.full[s], (uint32_t)L::kStage);
+      tma_load_2d(stage, &a_map, x, y, &m.full[s]);
+      if (kGate) tma_load_2d(stage + L::kATile / 2, &a_map, x, y + p.rows, &m.full[s]);
+    };
+    auto load_b = [&](int i, int s) {
+      const int it = k0 + i;
+      tma_load_2d(smem_u32(smem + s * L::kStage) + L::kATile, &b_map, in_row(it) * kStepK,
+                  MODE == kMoeDown ? (slot0 + in_list(it)) * NT : t0, &m.full[s]);
+    };
+    const int early = MODE == kMoeDown ? min(n, L::kStages) : 0;
+    if (MODE == kMoeDown) {
+      if (lane == 0)
+        for (int i = 0; i < early; ++i) load_a(i, i);
+      __syncwarp();
+      grid_dependency_wait();
+      if (lane == 0)
+        for (int i = 0; i < early; ++i) load_b(i, i);
+    }
+    int s = early % L::kStages, issued = early;
+    uint32_t phase = early == L::kStages ? 1u : 0u;  // of the fillings of stage s
+    bool ok = true;
+    for (int i = early; i < n && ok; ++i) {
+      if (i >= L::kStages) ok = MX_WAIT(m.empty[s], phase ^ 1u);
+      ok = __all_sync(kAllLanes, ok);
+      if (!ok) break;
+      if (lane == 0) {
         load_a(i, s);
         load_b(i, s);
-        ++issued;
-        if (++s == L::kStages) s = 0, phase ^= 1u;
       }
-      // after an abort no copy may still be landing when the CTA exits: the last one of each stage
-      if (*abort_flag)
-        for (int i = max(0, issued - L::kStages); i < issued; ++i)
-          mbar_wait_drain(&m.full[i % L::kStages], (i / L::kStages) & 1);
+      __syncwarp();
+      ++issued;
+      if (++s == L::kStages) s = 0, phase ^= 1u;
     }
+    // after an abort no copy may still be landing when the CTA exits: the last one of each stage
+    if (!ok)
+      for (int i = max(0, issued - L::kStages); i < issued; ++i)
+        mbar_wait_drain(&m.full[i % L::kStages], (i / L::kStages) & 1);
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
@@ -407,99 +435,94 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
     mbar_wait_drain(&m.done, 0);
   } else {
     // ---------------------------------------------------------------- scales
-    if (MODE == kMoeDown) grid_dependency_wait();
-    const int q = warp & 3;
-    constexpr int kB = NT / 32 > 0 ? NT / 32 : 1;  // the tokens' rows in groups of 32
+    // Thread r copies row r of W's 128 and, below NT, of the tokens', a set's 16 bytes, into a ring of kRawSets, all but
+    // one of them under way: behind the codes' copies a load takes microseconds.
+    const int q = warp & 3, r = 32 * q + lane;
     const int groups = p.K / kMxGroup;
-    // rows 32 c + lane of W's block, and of the tokens'; null behind the end
-    auto a_row = [&](int c, int e) -> const uint8_t* {
-      const int r = 32 * c + lane, f = n0 + (kGate ? r % kFeatures : r);
-      const int64_t row = (int64_t)e * (kGate ? 2 : 1) * p.rows + (kGate && r >= kFeatures ? p.rows : 0) + f;
-      return f < p.rows ? p.a_scale + row * p.a_scale_stride : nullptr;
+    constexpr int kRaw = (kTileRows + NT) * 16, kRawSets = L::kRawSets;
+    const uint32_t raw = smem_u32(smem + L::kOffRaw);
+    const int f = n0 + (kGate ? r % kFeatures : r);
+    const int64_t a_row = (kGate && r >= kFeatures ? p.rows : 0) + f, per_expert = (int64_t)(kGate ? 2 : 1) * p.rows;
+    auto copy = [&](uint32_t dst, const uint8_t* row, int x, bool there) {  // from step x of a row on; behind its end zeros
+      const int left = there ? groups - 4 * x : 0;
+      if (wide) cp_async16_zfill(dst, there ? row + 4 * x : p.a_scale, (uint32_t)min(max(left, 0), 16));
+      else cp_async4_zfill(dst, there ? row + 4 * x : p.a_scale, (uint32_t)min(max(left, 0), 4));
     };
-    auto b_row = [&](int c, int at) -> const uint8_t* {
-      const int t = 32 * c + lane;
-      const int64_t row = MODE == kMoeDown ? (int64_t)(slot0 + at) * NT + t : t0 + t;
-      return t < ntok ? p.b_scale + row * p.b_scale_stride : nullptr;
-    };
-    struct Words {
-      uint32_t a[4][kSetSteps], b[kB][kSetSteps];
-    };
-    auto read = [&](int i0, Words& w) {
-      if (wide) {
-        const int x = 4 * in_row(k0 + i0), e = expert_of(k0 + i0), at = in_list(k0 + i0);
-        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint8_t* row = a_row(c, e);
-          const uint4 v = row ? __ldg(reinterpret_cast<const uint4*>(row + x)) : none;
-          w.a[c][0] = v.x, w.a[c][1] = v.y, w.a[c][2] = v.z, w.a[c][3] = v.w;
-        }
-#pragma unroll
-        for (int c = 0; c < kB; ++c) {
-          const uint8_t* row = b_row(c, at);
-          const uint4 v = row ? __ldg(reinterpret_cast<const uint4*>(row + x)) : none;
-          w.b[c][0] = v.x, w.b[c][1] = v.y, w.b[c][2] = v.z, w.b[c][3] = v.w;
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < kSetSteps; ++k) {
-          if (i0 + k >= n) break;
-          const int it = k0 + i0 + k, x = in_row(it), e = expert_of(it), at = in_list(it);
-          const int left = groups - 4 * x;  // bytes of the row's last word behind its end count for nothing
-          const uint32_t valid = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint8_t* row = a_row(c, e);
-            w.a[c][k] = row ? __ldg(reinterpret_cast<const uint32_t*>(row + 4 * x)) & valid : 0u;
-          }
-#pragma unroll
-          for (int c = 0; c < kB; ++c) {
-            const uint8_t* row = b_row(c, at);
-            w.b[c][k] = row ? __ldg(reinterpret_cast<const uint32_t*>(row + 4 * x)) & valid : 0u;
-          }
-        }
+    auto copy_a = [&](int i0, int slot) {
+      for (int k = 0; k < kSetSteps && i0 + k < n; k += wide ? kSetSteps : 1) {
+        const int it = k0 + i0 + k;
+        copy(raw + slot * kRaw + 16 * r + 4 * k, p.a_scale + (expert_of(it) * per_expert + a_row) * p.a_scale_stride, in_row(it),
+             f < p.rows);
       }
     };
-    Words cur, next{};
-    if (n > 0) read(0, next);
+    auto copy_b = [&](int i0, int slot) {
+      if (r >= NT) return;
+      for (int k = 0; k < kSetSteps && i0 + k < n; k += wide ? kSetSteps : 1) {
+        const int it = k0 + i0 + k;
+        const int64_t row = MODE == kMoeDown ? (int64_t)(slot0 + in_list(it)) * NT + r : t0 + r;
+        copy(raw + slot * kRaw + 16 * (kTileRows + r) + 4 * k, p.b_scale + row * p.b_scale_stride, in_row(it), r < ntok);
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < kRawSets - 1; ++j) copy_a(j * kSetSteps, j);
+    if (MODE == kMoeDown) grid_dependency_wait();
+#pragma unroll
+    for (int j = 0; j < kRawSets - 1; ++j) {
+      copy_b(j * kSetSteps, j);
+      cp_async_commit();  // (the first one's group has all of W's scales)
+    }
+    if (MODE == kMoeUp && r < NT) {
+      // the weight that this thread's token gives the expert, while the first copies are under way
+      float w = 0.f;
+      bool any = false;
+      const int64_t first = (int64_t)(t0 + r) * p.topk;
+#pragma unroll 8
+      for (int k = 0; k < (r < ntok ? p.topk : 0); ++k) {
+        const int id = __ldg(p.ids + first + k);
+        const float x = __ldg(p.weights + first + k);
+        if (id == expert) w += x, any = true;
+      }
+      m.share[r] = w;
+      m.routed[r] = any;
+    }
     const uint32_t to = tmem + ((uint32_t)(32 * q) << 16) + NT;
-    int set = 0;
+    int set = 0, slot = 0;
     uint32_t phase = 0;
     for (int i0 = 0; i0 < n; i0 += kSetSteps) {
-      cur = next;
-      if (i0 + kSetSteps < n) read(i0 + kSetSteps, next);
-      if (i0 >= kSets * kSetSteps) dead = __any_sync(kAllLanes, !MX_WAIT(m.unscaled[set], phase ^ 1u));
-      if (dead) break;
+      cp_async_wait<kRawSets - 2>();
+      named_bar_sync(1, 128);  // everyone's copies of this set are there, and everyone has read the one before
+      const int before = slot == 0 ? kRawSets - 1 : slot - 1;
+      copy_a(i0 + (kRawSets - 1) * kSetSteps, before);
+      copy_b(i0 + (kRawSets - 1) * kSetSteps, before);
+      cp_async_commit();
+      if (!dead && i0 >= kSets * kSetSteps) dead = __any_sync(kAllLanes, !MX_WAIT(m.unscaled[set], phase ^ 1u));
       tc_fence_after();
+      // lane l: four steps' words of rows l, l + 32, .. of W's block and of the tokens'
+      constexpr int kB = NT / 32 > 0 ? NT / 32 : 1;
+      uint4 w[4], x[4] = {};
 #pragma unroll
-      for (int k = 0; k < kSetSteps; ++k) {
-        const uint32_t at = to + (set * kSetSteps + k) * L::kScaleCols;
-        tmem_st4(at, cur.a[0][k], cur.a[1][k], cur.a[2][k], cur.a[3][k]);
-        tmem_st4(at + 4, cur.b[0][k], kB > 1 ? cur.b[1 % kB][k] : 0u, kB > 2 ? cur.b[2 % kB][k] : 0u,
-                 kB > 3 ? cur.b[3 % kB][k] : 0u);
+      for (int c = 0; c < 4; ++c) w[c] = ld_shared_v4(raw + slot * kRaw + 16 * (32 * c + lane));
+#pragma unroll
+      for (int c = 0; c < kB; ++c) x[c] = ld_shared_v4(raw + slot * kRaw + 16 * (kTileRows + (NT < 32 ? lane % NT : 32 * c + lane)));
+      if (!dead) {
+        const uint32_t at = to + set * kSetSteps * L::kScaleCols;
+        tmem_st4(at, w[0].x, w[1].x, w[2].x, w[3].x);
+        tmem_st4(at + 4, x[0].x, x[1].x, x[2].x, x[3].x);
+        tmem_st4(at + 8, w[0].y, w[1].y, w[2].y, w[3].y);
+        tmem_st4(at + 12, x[0].y, x[1].y, x[2].y, x[3].y);
+        tmem_st4(at + 16, w[0].z, w[1].z, w[2].z, w[3].z);
+        tmem_st4(at + 20, x[0].z, x[1].z, x[2].z, x[3].z);
+        tmem_st4(at + 24, w[0].w, w[1].w, w[2].w, w[3].w);
+        tmem_st4(at + 28, x[0].w, x[1].w, x[2].w, x[3].w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(&m.scaled[set]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed(&m.scaled[set]);
       if (++set == kSets) set = 0, phase ^= 1u;
+      if (++slot == kRawSets) slot = 0;
     }
-    if (MODE == kMoeUp) {
-      // the weight that each token gives this expert
-      const int t = tid - 64;
-      if (t < NT) {
-        float w = 0.f;
-        bool any = false;
-        if (t < ntok)
-          for (int k = 0; k < p.topk; ++k) {
-            const int64_t i = (int64_t)(t0 + t) * p.topk + k;
-            if (__ldg(p.ids + i) == expert) w += __ldg(p.weights + i), any = true;
-          }
-        m.share[t] = w;
-        m.routed[t] = any;
-      }
-    }
+    cp_async_wait<0>();  // none may land later, in what is then something else
     dead = __any_sync(kAllLanes, dead || !MX_WAIT(m.done, 0));
     tc_fence_after();
   }
@@ -507,78 +530,117 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
 
   // ---------------------------------------------------------------- results
   const int q = warp & 3;
-  const MxOut kind = out_kind(p);
-  const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
-  // Tokens c .. c + 3 of the group of 32 features `group` (of the tile), one a lane.
-  auto finish = [&](float (&v)[4], float (&up)[4], int group, int c) {
-    const int f = n0 + 32 * group + lane;
-    const bool biased = !kExperts && p.to.bias != nullptr && f < p.rows;
-    const float b0 = biased ? bias_at(p.to, f) : 0.f, b1 = kGate && biased ? bias_at(p.to, (int64_t)p.rows + f) : 0.f;
+  const MxOut kind = MODE == kMoeUp ? kOutCodes : out_kind(p);
+  // Tokens c .. c + 3 of the group of 32 features `group` (of the tile), one a lane; biases b0, b1.
+  auto finish = [&](auto out, const float (&v)[4], const float (&up)[4], float b0, float b1, int group, int c) {
     float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       y[i] = v[i] + b0;
       if (kGate) y[i] = silu(y[i]) * (up[i] + b1);
       else if (MODE == kLinear) y[i] = activate(p.to.activation, y[i]);
-      if (MODE == kMoeUp) y[i] = c + i < ntok && m.routed[c + i] ? y[i] * m.share[c + i] : 0.f;
+      if (MODE == kMoeUp) y[i] = m.routed[c + i] ? y[i] * m.share[c + i] : 0.f;  // (tokens behind the last are not routed)
     }
     const int64_t row = MODE == kMoeUp ? (int64_t)slot0 * NT + c : t0 + c;
-    write_out(kind, p, y, f, n0 + 32 * group, row, ntok - c);
+    write_out<decltype(out)::value>(p, y, n0 + 32 * group + lane, n0 + 32 * group, row, ntok - c);
+  };
+  auto biases = [&](int group, float& b0, float& b1) {
+    const int f = n0 + 32 * group + lane;
+    const bool biased = !kExperts && p.to.bias != nullptr && f < p.rows;
+    b0 = biased ? bias_at(p.to, f) : 0.f;
+    b1 = kGate && biased ? bias_at(p.to, (int64_t)p.rows + f) : 0.f;
+  };
+  // body(out) for the way that results go
+  auto by_kind = [&](auto body) {
+    if (kind == kOutCodes) body(std::integral_constant<MxOut, kOutCodes>{});
+    else if (kind == kOutPairs) body(std::integral_constant<MxOut, kOutPairs>{});
+    else body(std::integral_constant<MxOut, kOutSingle>{});
+  };
+  // 16 columns of this warp's lanes
+  auto columns = [&](int c, uint32_t (&w)[16]) {
+    tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + c, w);
+    tmem_ld_wait();
+    reg_fence16(w);
+    if (n == 0)  // no part of K: nothing has been summed
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = 0u;
   };
   if (MODE == kMoeUp && total == 0) {
     // no such expert: nothing to compute, nothing to write
   } else if (parts == 1 && !kGate) {
     if (warp >= 2 && !dead) {
+      float b0, b1;
+      biases(q, b0, b1);
+      by_kind([&](auto out) {
 #pragma unroll 1
-      for (int c = 0; c < ntok; c += 8) {
-        uint32_t w[8];
-        tmem_ld8(acc + c, w);
-        tmem_ld_wait();
-        reg_fence8(w);
+        for (int c = 0; c < ntok; c += 16) {
+          uint32_t w[16];
+          columns(c, w);
 #pragma unroll
-        for (int h = 0; h < 8; h += 4) {
-          float v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = n > 0 ? __uint_as_float(w[h + i]) : 0.f;
-          if (c + h < ntok) finish(v, v, q, c + h);
+          for (int h = 0; h < 16; h += 4) {
+            const float v[4] = {__uint_as_float(w[h]), __uint_as_float(w[h + 1]), __uint_as_float(w[h + 2]),
+                                __uint_as_float(w[h + 3])};
+            if (c + h < ntok) finish(out, v, v, b0, b1, q, c + h);
+          }
         }
-      }
+      });
     }
   } else {
     float* part = reinterpret_cast<float*>(smem);  // [column][row]; every copy and MMA has ended
     if (warp >= 2) {
 #pragma unroll 1
-      for (int c = 0; c < ntok; c += 8) {
-        uint32_t w[8];
-        tmem_ld8(acc + c, w);
-        tmem_ld_wait();
-        reg_fence8(w);
+      for (int c = 0; c < ntok; c += 16) {
+        uint32_t w[16];
+        columns(c, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part[(c + i) * kTileRows + 32 * q + lane] = n > 0 ? __uint_as_float(w[i]) : 0.f;
+        for (int i = 0; i < 16; ++i) part[(c + i) * kTileRows + 32 * q + lane] = __uint_as_float(w[i]);
       }
     }
     __syncwarp();
     if (parts > 1) cluster_sync_all();
     else __syncthreads();
     if (warp >= 2 && !dead) {
-      // units of 4 tokens by 32 features, dealt to the cluster's warps
-      constexpr int kGroups = kFeatures / 32;
-      const int units = (ntok + 3) / 4 * kGroups;
+      // Blocks of kBlock tokens by 32 features, dealt to the cluster's warps.  The gated ones are large, so that their
+      // longer chains of operations overlap; without a branch but for tokens behind the last.
+      constexpr int kGroups = kFeatures / 32, kBlock = 4;
+      const int blocks = (ntok + kBlock - 1) / kBlock * kGroups;
+      by_kind([&](auto out) {
 #pragma unroll 1
-      for (int u = q * parts + rank; u < units; u += 4 * parts) {
-        const int group = u % kGroups, c = u / kGroups * 4;
-        const uint32_t mine = smem_u32(part) + 4 * (c * kTileRows + 32 * group + lane);
-        float v[4] = {}, up[4] = {};
-        for (int o = 0; o < parts; ++o) {
-          const uint32_t from = parts > 1 ? mapa_shared(mine, (uint32_t)o) : mine;
+        for (int u = q * parts + rank; u < blocks; u += 4 * parts) {
+          const int group = u % kGroups, c0 = u / kGroups * kBlock;
+          float b0, b1;
+          biases(group, b0, b1);
+          float v[kBlock], up[kBlock];
+          auto sum = [&](float (&to)[kBlock], uint32_t at) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] += ld_cluster_f32(from + 4 * kTileRows * i);
-            if (kGate) up[i] += ld_cluster_f32(from + 4 * (kTileRows * i + kFeatures));
+            for (int i = 0; i < kBlock; ++i) to[i] = 0.f;
+            for (int o = 0; o < parts; o += 4) {
+              float x[4][kBlock];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)  // all loads before the first sum
+                if (o + k < parts) {
+                  const uint32_t from = parts > 1 ? mapa_shared(at, (uint32_t)(o + k)) : at;
+#pragma unroll
+                  for (int i = 0; i < kBlock; ++i) x[k][i] = ld_cluster_f32(from + 4 * kTileRows * i);
+                }
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (o + k < parts)
+#pragma unroll
+                  for (int i = 0; i < kBlock; ++i) to[i] += x[k][i];
+            }
+          };
+          const uint32_t mine = smem_u32(part) + 4 * (c0 * kTileRows + 32 * group + lane);
+          sum(v, mine);
+          if (kGate) sum(up, mine + 4 * kFeatures);
+#pragma unroll
+          for (int h = 0; h < kBlock; h += 4) {
+            const float a[4] = {v[h], v[h + 1], v[h + 2], v[h + 3]};
+            const float g[4] = {kGate ? up[h] : 0.f, kGate ? up[h + 1] : 0.f, kGate ? up[h + 2] : 0.f, kGate ? up[h + 3] : 0.f};
+            if (c0 + h < ntok) finish(out, a, g, b0, b1, group, c0 + h);
           }
         }
-        finish(v, up, group, c);
-      }
+      });
     }
     __syncwarp();
     if (parts > 1) cluster_sync_relaxed();  // no CTA leaves while another reads its sums
@@ -659,7 +721,7 @@ cudaError_t launch_mx(const MxParams& p, int parts, int64_t row_tiles, int64_t t
 // Parts of K: as many as give every SM two CTAs, each with two steps or more.
 int split_k(int64_t tiles, int64_t steps, int num_sms) {
   int parts = 1;
-  while (parts < 8 && tiles * parts * 2 <= 2 * (int64_t)num_sms && steps >= 4 * parts) parts *= 2;
+  while (parts < kMaxParts && tiles * parts * 2 <= 2 * (int64_t)num_sms && steps >= 4 * parts) parts *= 2;
   return parts;
 }
 
