@@ -7,10 +7,12 @@
 // bits, then the lowest index that has it.  Without bias and groups the logits
 // themselves are ranked, so float32 decides exactly.  With them what is ranked is
 // computed, and near ties could fall either way: where two neighbours of the
-// ranking, or the last taken and the first left, are nearer than the computation's
-// error, the token is ranked again in 64 bits.  (All of them in 64 bits would take
-// an exponential of 64 bits per expert, at a sixtieth of the rate.)  The call is
-// bound by its launch for decode batches and by reading the logits beyond.
+// ranking, as far as it decides, are nearer than the computation's error, those
+// taken (and those that follow as closely) are ordered by scores of 64 bits, one a
+// lane; near ties of groups and of softmax scores rank the token again in 64 bits.
+// (All scores in 64 bits would take an exponential of 64 bits per expert, at a
+// sixtieth of the rate.)  The call is bound by its launch for decode batches and by
+// latency and reading the logits beyond.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -60,30 +62,42 @@ __device__ __forceinline__ float score_of(bool sigmoid, float x, float top, floa
 // of 512 exponentials (32 are taken).
 __device__ __forceinline__ float slack(bool sigmoid, float x) { return (sigmoid ? 0x1p-21f : 0x1p-19f) * (1.f + fabsf(x)); }
 
+struct Taken {
+  int id;            // lane k: the k-th expert, -1: there was none
+  int count;         // how many there are: topk, and those that follow by less than their error
+  bool near;         // two neighbours of them are nearer than that
+  bool groups_near;  // as are the last group kept and the first left
+};
+
 // Ranks a token's experts (keys[i]: of expert 32 i + lane) and takes topk of
-// them, lane k the k-th (-1: there was none).  `near_tie` reports two neighbours
-// nearer than their error.  `scratch`: E keys of shared memory, used with groups.
+// them, and with `check` also those that follow too closely.  `scratch`: E keys of
+// shared memory, used with groups.
 template <int R, typename Bits>
-__device__ __forceinline__ int take(const MoeRouteArgs& a, Bits (&keys)[R], Bits* scratch, bool check, bool& near_tie) {
+__device__ __forceinline__ Taken take(const MoeRouteArgs& a, Bits (&keys)[R], Bits* scratch, bool check) {
   const int lane = threadIdx.x & 31;
-  near_tie = false;
+  Taken got{-1, 0, false, false};
   if (a.groups > 1) {
     const int size = a.E / a.groups;
 #pragma unroll
     for (int i = 0; i < R; ++i)
       if (32 * i + lane < a.E) scratch[32 * i + lane] = keys[i];
     __syncwarp();
-    // lane g: group g's two largest; their sum's key
-    Bits group = 0;
-    if (lane < a.groups) {
-      Bits first = 0, second = 0;
-      for (int i = 0; i < size; ++i) {
-        const Bits k = scratch[lane * size + i];
+    // each group's two largest, by as many lanes as there are for it (a power of two); their sum's key
+    const int share = 32 - __clz(32 / a.groups) - 1, lanes = 1 << share, mine = lane >> share;
+    Bits first = 0, second = 0;
+    if (mine < a.groups)
+      for (int i = lane & (lanes - 1); i < size; i += lanes) {
+        const Bits k = scratch[mine * size + i];
         second = k > first ? first : k > second ? k : second;
         first = k > first ? k : first;
       }
-      if (second) group = order_bits(value_of(first) + value_of(second));
+    for (int d = 1; d < lanes; d *= 2) {
+      const Bits f = __shfl_xor_sync(kLanes, first, d), g = __shfl_xor_sync(kLanes, second, d);
+      const Bits less = f < first ? f : first, other = g > second ? g : second;
+      first = f > first ? f : first;
+      second = less > other ? less : other;
     }
+    Bits group = second ? order_bits(value_of(first) + value_of(second)) : 0;
     __syncwarp();
     uint32_t kept = 0u;
     Bits last = 0;
@@ -91,42 +105,66 @@ __device__ __forceinline__ int take(const MoeRouteArgs& a, Bits (&keys)[R], Bits
       const Bits top = warp_max(group);
       if (check && r == a.topk_groups && top) {
         const float lo = (float)value_of(top), hi = (float)value_of(last);
-        near_tie |= hi - lo <= 2.f * (slack(a.sigmoid, lo) + slack(a.sigmoid, hi));
+        got.groups_near = hi - lo <= 2.f * (slack(a.sigmoid, lo) + slack(a.sigmoid, hi));
       }
       if (r == a.topk_groups || !top) break;
-      const int g = __ffs(__ballot_sync(kLanes, group == top)) - 1;
+      const int g = (__ffs(__ballot_sync(kLanes, group == top)) - 1) >> share;
       kept |= 1u << g;
-      if (lane == g) group = 0;
+      if (mine == g) group = 0;
       last = top;
     }
 #pragma unroll
     for (int i = 0; i < R; ++i)
       if (32 * i + lane < a.E && !(kept >> ((32 * i + lane) / size) & 1u)) keys[i] = 0;
   }
-  int mine = -1;
   Bits last = 0;
-  for (int r = 0; r <= a.topk; ++r) {
+  for (int r = 0; r < 32; ++r) {
+    if (r >= a.topk && !check) break;
     Bits best = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) best = keys[i] > best ? keys[i] : best;
     const Bits top = warp_max(best);
-    if (check && r > 0 && top) {
+    if (!top) break;
+    if (check && r > 0) {
       const float lo = (float)value_of(top), hi = (float)value_of(last);
-      near_tie |= hi - lo <= slack(a.sigmoid, lo) + slack(a.sigmoid, hi);
+      const bool near = hi - lo <= slack(a.sigmoid, lo) + slack(a.sigmoid, hi);
+      if (r >= a.topk && !near) break;
+      got.near |= near;
     }
-    if (r == a.topk || !top) break;
     uint32_t at = 0xffffffffu;
 #pragma unroll
     for (int i = R - 1; i >= 0; --i)
       if (keys[i] == top) at = (uint32_t)(32 * i + lane);
     const int e = (int)__reduce_min_sync(kLanes, at);
-    if (lane == r) mine = e;
+    if (lane == r) got.id = e;
+    got.count = r + 1;
 #pragma unroll
     for (int i = 0; i < R; ++i)
       if (32 * i + lane == e) keys[i] = 0;
     last = top;
   }
-  return mine;
+  return got;
+}
+
+// The order of the taken ones in 64 bits, by sigmoid: each lane its own expert's score, and its place among the others.
+template <typename X>
+__device__ __noinline__ int order_64(const MoeRouteArgs& a, const X* logits, int id, uint64_t* scratch) {
+  const int lane = threadIdx.x & 31;
+  uint64_t key = 0;
+  if (id >= 0) key = order_bits(1. / (1. + exp(-(double)(float)logits[id])) + (a.bias ? (double)a.bias[id] : 0.));
+  int place = 0;
+  for (int i = 0; i < 32; ++i) {
+    const uint64_t k = __shfl_sync(kLanes, key, i);
+    const int other = __shfl_sync(kLanes, id, i);
+    place += k > key || (k == key && other >= 0 && other < id);
+  }
+  __syncwarp();
+  int* ids = reinterpret_cast<int*>(scratch);
+  ids[lane] = -1;
+  __syncwarp();
+  if (id >= 0) ids[place] = id;
+  __syncwarp();
+  return ids[lane];
 }
 
 // The same in 64 bits, from the logits on.
@@ -155,8 +193,7 @@ __device__ __noinline__ int take_64(const MoeRouteArgs& a, const X* logits, uint
     if (e < a.E && x[i] > -INFINITY)
       keys[i] = order_bits((a.sigmoid ? 1. / (1. + exp(-x[i])) : exp(x[i] - top) / sum) + (a.bias ? (double)a.bias[e] : 0.));
   }
-  bool unused;
-  return take<R, uint64_t>(a, keys, scratch, false, unused);
+  return take<R, uint64_t>(a, keys, scratch, false).id;
 }
 
 template <int R, typename X>
@@ -193,12 +230,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
     if (computed && x[i] > -INFINITY) rank = score_of(a.sigmoid, x[i], top, inv) + (a.bias && e < a.E ? __ldg(a.bias + e) : 0.f);
     keys[i] = e < a.E && x[i] > -INFINITY ? order_bits(rank) : 0u;
   }
-  bool near_tie;
-  int id = take<R, uint32_t>(a, keys, reinterpret_cast<uint32_t*>(scratch[warp]), computed, near_tie);
-  if (near_tie) {
+  const Taken got = take<R, uint32_t>(a, keys, reinterpret_cast<uint32_t*>(scratch[warp]), computed);
+  int id = got.id;
+  if (got.groups_near || (got.near && (!a.sigmoid || got.count == 32))) {
     __syncwarp();
     id = take_64<R, X>(a, logits, scratch[warp]);
+  } else if (got.near) {
+    id = order_64<X>(a, logits, id, scratch[warp]);
   }
+  if (lane >= a.topk) id = -1;
   // lane k: the k-th expert's weight
   float w = id >= 0 ? score_of(a.sigmoid, (float)logits[id], top, inv) : 0.f;
   if (a.renormalize) {
