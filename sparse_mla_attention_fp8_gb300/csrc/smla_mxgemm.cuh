@@ -16,7 +16,7 @@
 // CTAs an SM keep that read going while others start and end.
 //
 // Warp roles: 0 TMA of the codes (128-byte rows and swizzle), 1 MMA issuer, 2..5
-// scales, then results.  The scales of a set of four steps (of 128 values of K) go
+// scales, 2..9 results.  The scales of a set of four steps (of 128 values of K) go
 // by asynchronous copies into shared memory and from there into tensor memory,
 // where each warp fills its quarter of the lanes: of a step's 8 columns the c-th
 // holds the 4 bytes of W's row 32 c + lane, the (4 + c)-th those of that token.
@@ -42,7 +42,8 @@ namespace {
 constexpr uint32_t kAllLanes = 0xffffffffu;
 constexpr int kStepK = 128;    // values of K per stage: one 128-byte swizzle row
 constexpr int kTileRows = 128; // rows of W per tile
-constexpr int kMxThreads = 6 * 32;
+constexpr int kResultWarps = 8;
+constexpr int kMxThreads = (2 + kResultWarps) * 32;
 constexpr int kMaxParts = 8;    // of K: CTAs of a (portable) cluster
 
 // Set when a wait runs out in a kernel of the file that includes this.
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
     if (elect_one()) mma_commit(&m.done);
     __syncwarp();
     mbar_wait_drain(&m.done, 0);
-  } else {
+  } else if (warp < 6) {
     // ---------------------------------------------------------------- scales
     // Thread r copies row r of W's 128 and, below NT, of the tokens', a set's 16 bytes, into a ring of kRawSets, all but
     // one of them under way: behind the codes' copies a load takes microseconds.
@@ -523,13 +524,15 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
       if (++slot == kRawSets) slot = 0;
     }
     cp_async_wait<0>();  // none may land later, in what is then something else
+  }
+  if (warp >= 2) {
     dead = __any_sync(kAllLanes, dead || !MX_WAIT(m.done, 0));
     tc_fence_after();
   }
 #undef MX_WAIT
 
   // ---------------------------------------------------------------- results
-  const int q = warp & 3;
+  const int q = warp & 3, half = (warp - 2) >> 2;  // two warps have the same lanes of tensor memory
   const MxOut kind = MODE == kMoeUp ? kOutCodes : out_kind(p);
   // Tokens c .. c + 3 of the group of 32 features `group` (of the tile), one a lane; biases b0, b1.
   auto finish = [&](auto out, const float (&v)[4], const float (&up)[4], float b0, float b1, int group, int c) {
@@ -573,7 +576,7 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
       biases(q, b0, b1);
       by_kind([&](auto out) {
 #pragma unroll 1
-        for (int c = 0; c < ntok; c += 16) {
+        for (int c = 16 * half; c < ntok; c += 32) {
           uint32_t w[16];
           columns(c, w);
 #pragma unroll
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
     float* part = reinterpret_cast<float*>(smem);  // [column][row]; every copy and MMA has ended
     if (warp >= 2) {
 #pragma unroll 1
-      for (int c = 0; c < ntok; c += 16) {
+      for (int c = 16 * half; c < ntok; c += 32) {
         uint32_t w[16];
         columns(c, w);
 #pragma unroll
@@ -600,13 +603,13 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
     if (parts > 1) cluster_sync_all();
     else __syncthreads();
     if (warp >= 2 && !dead) {
-      // Blocks of kBlock tokens by 32 features, dealt to the cluster's warps.  The gated ones are large, so that their
-      // longer chains of operations overlap; without a branch but for tokens behind the last.
+      // Blocks of kBlock tokens by 32 features, dealt to the cluster's warps.  (Blocks of 16, with more chains of
+      // operations at once, are more code that each CTA runs once, and took longer: 4.9 us against 3.9 for 48 tokens.)
       constexpr int kGroups = kFeatures / 32, kBlock = 4;
       const int blocks = (ntok + kBlock - 1) / kBlock * kGroups;
       by_kind([&](auto out) {
 #pragma unroll 1
-        for (int u = q * parts + rank; u < blocks; u += 4 * parts) {
+        for (int u = (warp - 2) * parts + rank; u < blocks; u += kResultWarps * parts) {
           const int group = u % kGroups, c0 = u / kGroups * kBlock;
           float b0, b1;
           biases(group, b0, b1);
