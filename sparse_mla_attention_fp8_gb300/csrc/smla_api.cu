@@ -868,6 +868,7 @@ int check_type(const char* name, int type) {
 }
 int check_groups(const char* name, int v) {
   if (v <= 0 || v % 32 != 0) return fail(SMLA_ERR_INVALID_ARG, "%s=%d must be a positive multiple of 32", name, v);
+  if (v > (1 << 30)) return fail(SMLA_ERR_UNSUPPORTED, "%s=%d unsupported: at most 2^30", name, v);
   return SMLA_OK;
 }
 // Rows of `least` elements, 16-byte aligned, `size` bytes an element.

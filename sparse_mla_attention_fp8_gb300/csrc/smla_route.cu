@@ -143,6 +143,14 @@ __device__ __forceinline__ Taken take(const MoeRouteArgs& a, Bits (&keys)[R], Bi
       if (32 * i + lane == e) keys[i] = 0;
     last = top;
   }
+  if (check && got.count == 32) {  // whether one more follows as closely
+    Bits best = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) best = keys[i] > best ? keys[i] : best;
+    const Bits top = warp_max(best);
+    const float lo = top ? (float)value_of(top) : 0.f, hi = (float)value_of(last);
+    got.near |= top && hi - lo <= slack(a.sigmoid, lo) + slack(a.sigmoid, hi);
+  }
   return got;
 }
 

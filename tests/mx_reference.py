@@ -56,11 +56,11 @@ def quantized_bound(y, off):
     return off + torch.maximum(2.0 ** -4 * (y.abs() + off), 2.0 ** -10 * p)
 
 
-def quantize(x, padded=True):
-    """MXFP8 of float64 values as the operators take it: scale rows a multiple of 4 bytes apart."""
+def quantize(x, apart=16):
+    """MXFP8 of float64 values as the operators take it: scale rows a multiple of `apart` (4 or more) bytes apart."""
     codes, scales = bytes_of(x)
     rows, n = scales.shape
-    held = torch.full((rows, -(-n // 4) * 4), 255, dtype=torch.uint8, device=x.device)  # (what is behind a row counts for nothing)
+    held = torch.full((rows, -(-n // apart) * apart), 255, dtype=torch.uint8, device=x.device)  # (what is behind a row counts for nothing)
     held[:, :n] = scales
     return codes, held[:, :n]
 

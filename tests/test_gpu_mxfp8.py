@@ -35,9 +35,9 @@ def within(got, want, bound):
         f"{int(bad.sum())} of {bad.numel()} outside, worst {worst:.3g} of the bound"
 
 
-def matrix(g, rows, K, scale=1.0):
+def matrix(g, rows, K, scale=1.0, apart=16):
     """A quantized matrix and its values."""
-    codes, scales = ref.quantize(activations(g, rows, K).double() * scale)
+    codes, scales = ref.quantize(activations(g, rows, K).double() * scale, apart)
     return codes, scales, ref.values(codes, scales)
 
 
@@ -172,11 +172,11 @@ def test_norm_of_zero_rows_and_specials(smla):
 
 # ---------------------------------------------------------------- linear product
 
-def check_linear(smla, T, N, K, act="none", bias=None, residual=False, quantized=False, seed=0):
+def check_linear(smla, T, N, K, act="none", bias=None, residual=False, quantized=False, seed=0, apart=16):
     g = gen(seed + T + N + K)
-    x, xs, xv = matrix(g, T, K)
+    x, xs, xv = matrix(g, T, K, apart=apart)
     rows = 2 * N if act == "swiglu" else N
-    w, ws, wv = matrix(g, rows, K, scale=0.3 * K ** -0.5)
+    w, ws, wv = matrix(g, rows, K, scale=0.3 * K ** -0.5, apart=apart)
     b = None if bias is None else normal(g, rows, dtype=bias)
     r = normal(g, T, N, dtype=torch.bfloat16) if residual else None
     y, off = ref.linear(xv, wv, b, act, r)
@@ -194,9 +194,19 @@ def test_linear_smallest(smla):
     check_linear(smla, 1, 128, 128)
 
 
-@pytest.mark.parametrize("K", [32, 64, 96, 160, 1024, 4096])
-def test_linear_lengths(smla, K):
-    check_linear(smla, 5, 128, K)
+@pytest.mark.parametrize("apart", [4, 16])
+@pytest.mark.parametrize("K", [32, 64, 96, 160, 480, 544, 1024, 1056, 4096])
+def test_linear_lengths(smla, K, apart):
+    """Rows of scales that end inside a word, a step and a set of steps, on 16-byte boundaries and not."""
+    check_linear(smla, 5, 128, K, apart=apart)
+    check_linear(smla, 70, 96, K, act="swiglu", apart=apart)
+
+
+@pytest.mark.parametrize("apart", [4, 16])
+@pytest.mark.parametrize("K", [32, 96, 160, 480, 544, 1056, 2080])
+def test_linear_lengths_many_tokens(smla, K, apart):
+    check_linear(smla, 1500, 1040, K, apart=apart)
+    check_linear(smla, 1400, 600, K, act="swiglu", apart=apart)
 
 
 @pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 31, 33, 48, 64, 65, 96, 97, 128, 129, 300])
@@ -227,7 +237,8 @@ def test_linear_quantized(smla, T, N, K, act):
 
 
 @pytest.mark.parametrize("T,N,K", [(257, 32, 32), (300, 256, 128), (383, 130, 4096), (512, 257, 96), (640, 1000, 256),
-                                   (257, 1, 544), (1111, 2080, 1056), (2000, 4096, 512), (5000, 96, 128), (1024, 5120, 64)])
+                                   (257, 1, 544), (1111, 2080, 1056), (2000, 4096, 512), (5000, 96, 128), (1024, 5120, 64),
+                                   (65, 8200, 512), (6001, 33, 256), (100, 6500, 1024)])
 @pytest.mark.parametrize("act", ["none", "swiglu"])
 def test_linear_many_tokens(smla, T, N, K, act):
     check_linear(smla, T, N, K, act=act)
@@ -240,7 +251,7 @@ def test_linear_many_tokens(smla, T, N, K, act):
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh", "swiglu"])
 @pytest.mark.parametrize("out", ["bf16", "residual", "mxfp8"])
 def test_linear_epilogues_many_tokens(smla, act, out):
-    check_linear(smla, 500, 352, 384, act=act, bias=torch.float32, residual=out == "residual", quantized=out == "mxfp8")
+    check_linear(smla, 1300, 1120, 384, act=act, bias=torch.float32, residual=out == "residual", quantized=out == "mxfp8")
 
 
 def test_linear_many_tiles(smla):
@@ -326,6 +337,19 @@ def test_route_near_ties(smla):
     check_route(smla, near.contiguous(), 8, "softmax", bias=1e-7 * normal(g, 64), groups=4, topk_groups=2)
 
 
+def test_route_near_ties_of_many(smla):
+    """More near ties than a warp has lanes; the last taken and the first left among them."""
+    g = gen(2)
+    near = normal(g, 100, 1).expand(100, 96) + 1e-7 * torch.randint(-3, 4, (100, 96), generator=g, device="cuda")
+    bias = torch.full((96,), 0.25, device="cuda")
+    for topk in (1, 8, 31, 32):
+        check_route(smla, near.contiguous(), topk, "sigmoid", bias=bias)
+    few = 3 * normal(g, 200, 40)
+    few[:, 33] = few.sort(dim=1, descending=True).values[:, 31] * (1 + 2.0 ** -23)  # the 32nd's neighbour
+    check_route(smla, few, 32, "sigmoid", bias=torch.zeros(40, device="cuda"))
+    check_route(smla, few, 32, "softmax", bias=torch.zeros(40, device="cuda"))
+
+
 def test_route_masked_experts(smla):
     """Masked experts are not taken; where too few are left, id -1 and weight 0."""
     g = gen(4)
@@ -353,14 +377,14 @@ def test_route_many_tokens(smla):
 
 # ---------------------------------------------------------------- mixture of experts
 
-def experts(g, E, K, F):
+def experts(g, E, K, F, apart=16):
     w13 = [matrix(g, 2 * F, K, 0.3 * K ** -0.5) for _ in range(E)]
     w2 = [matrix(g, K, F, 0.3 * F ** -0.5) for _ in range(E)]
 
     def stacked(ws):
         codes = torch.stack([w[0] for w in ws])
         n = ws[0][1].shape[1]
-        held = torch.full((E, codes.shape[1], -(-n // 4) * 4), 255, dtype=torch.uint8, device="cuda")
+        held = torch.full((E, codes.shape[1], -(-n // apart) * apart), 255, dtype=torch.uint8, device="cuda")
         for e in range(E):
             held[e, :, :n] = ws[e][1]
         return codes, held[:, :, :n]
@@ -368,10 +392,10 @@ def experts(g, E, K, F):
     return stacked(w13), stacked(w2), [w[2] for w in w13], [w[2] for w in w2]
 
 
-def check_moe(smla, T, E, topk, K, F, residual=False, ids=None, seed=0, **kw):
+def check_moe(smla, T, E, topk, K, F, residual=False, ids=None, seed=0, apart=16, **kw):
     g = gen(seed + T + E + K + F)
-    x, xs, xv = matrix(g, T, K)
-    (w13, s13), (w2, s2), v13, v2 = experts(g, E, K, F)
+    x, xs, xv = matrix(g, T, K, apart=apart)
+    (w13, s13), (w2, s2), v13, v2 = experts(g, E, K, F, apart)
     if ids is None:
         ids = torch.stack([torch.randperm(E, generator=g, device="cuda")[:topk] for _ in range(T)]).int()
     w = torch.rand(ids.shape, generator=g, device="cuda")
@@ -392,10 +416,11 @@ def test_moe_tokens(smla, T):
     check_moe(smla, T, 8, 2, 256, 128, residual=T % 2 == 1)
 
 
-@pytest.mark.parametrize("K,F", [(32, 32), (96, 160), (1024, 32), (160, 544), (2048, 512)])
-def test_moe_sizes(smla, K, F):
-    check_moe(smla, 5, 6, 3, K, F)
-    check_moe(smla, 50, 6, 3, K, F, residual=True)
+@pytest.mark.parametrize("apart", [4, 16])
+@pytest.mark.parametrize("K,F", [(32, 32), (96, 160), (1024, 32), (160, 544), (480, 1024), (2048, 512), (2080, 480)])
+def test_moe_sizes(smla, K, F, apart):
+    check_moe(smla, 5, 6, 3, K, F, apart=apart)
+    check_moe(smla, 50, 6, 3, K, F, residual=True, apart=apart)
 
 
 @pytest.mark.parametrize("E,topk", [(1, 1), (3, 3), (40, 1), (64, 8), (130, 32)])
@@ -515,6 +540,48 @@ def test_layer_captured(smla):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(buf, want_stream)
+
+
+def test_refused_tensors(smla):
+    """What the binding refuses before the call: shapes, types, strides, devices."""
+    g = gen(0)
+    x, xs, _ = matrix(g, 4, 64)
+    w, ws, _ = matrix(g, 96, 64)
+    b = x.new_zeros((4, 64), dtype=torch.bfloat16)
+    bad = [
+        lambda: smla.mxfp8_quantize(b.half()), lambda: smla.mxfp8_quantize(b[0]), lambda: smla.mxfp8_quantize(b[:, ::2]),
+        lambda: smla.mxfp8_quantize(b[:, :40]), lambda: smla.mxfp8_quantize(b[:, 4:36]), lambda: smla.mxfp8_quantize(b[:1].expand(4, 64)),
+        lambda: smla.mxfp8_quantize(b, codes=x[:3]), lambda: smla.mxfp8_quantize(b, scales=xs[:, :1]),
+        lambda: smla.mxfp8_quantize(b, scales=xs.contiguous()),
+        lambda: smla.rms_norm_mxfp8(b.float()), lambda: smla.rms_norm_mxfp8(b, weight=b[0, :32]),
+        lambda: smla.rms_norm_mxfp8(b, residual=b[:3]), lambda: smla.rms_norm_mxfp8(b, normed=b[:3]),
+        lambda: smla.rms_norm_mxfp8(b, quantized=False),
+        lambda: smla.linear_mxfp8(b, xs, w, ws), lambda: smla.linear_mxfp8(x, xs, w[:, :32], ws),
+        lambda: smla.linear_mxfp8(x, xs[:3], w, ws), lambda: smla.linear_mxfp8(x, xs, w, ws[:, :1]),
+        lambda: smla.linear_mxfp8(x, xs, w[::2], ws[::2]), lambda: smla.linear_mxfp8(x, xs.float(), w, ws),
+        lambda: smla.linear_mxfp8(x, xs, w, ws, bias=b[0]), lambda: smla.linear_mxfp8(x, xs, w[:95], ws[:95], activation="swiglu"),
+        lambda: smla.linear_mxfp8(x, xs, w, ws, residual=b), lambda: smla.linear_mxfp8(x, xs, w, ws, out=b),
+        lambda: smla.linear_mxfp8(x, xs, w[:95], ws[:95], quantized=True),
+        lambda: smla.linear_mxfp8(x, xs, w, ws, residual=b.new_zeros((4, 96)), quantized=True),
+        lambda: smla.moe_route(b.half(), 2), lambda: smla.moe_route(b, 0), lambda: smla.moe_route(b, 65),
+        lambda: smla.moe_route(b.t(), 2), lambda: smla.moe_route(b, 2, bias=b[0]), lambda: smla.moe_route(b, 2, num_groups=3),
+        lambda: smla.moe_route(b, 2, ids=torch.zeros((4, 3), dtype=torch.int32, device="cuda")),
+    ]
+    (w13, s13), (w2, s2), _, _ = experts(g, 3, 64, 32)
+    ids, p = torch.zeros((4, 2), dtype=torch.int32, device="cuda"), torch.ones((4, 2), device="cuda")
+    ok = (x, xs, ids, p, w13, s13, w2, s2)
+    for i, v in [(0, b), (1, xs[:2]), (2, ids.long()), (2, ids[:3]), (3, p[:, :1]), (3, p.double()), (4, w13[:, :, :32]),
+                 (4, w13[0]), (4, w13.transpose(0, 1)), (5, s13[:2]), (5, s13.transpose(0, 1)), (6, w13), (7, s13), (6, w2[:2])]:
+        bad.append(lambda i=i, v=v: smla.moe_mxfp8(*ok[:i], v, *ok[i + 1:]))
+    bad += [lambda: smla.moe_mxfp8(*ok, residual=b[:2]), lambda: smla.moe_mxfp8(*ok, out=x),
+            lambda: smla.moe_mxfp8(*ok, workspace=torch.empty(0, dtype=torch.uint8, device="cuda")),
+            lambda: smla.moe_mxfp8(*[v.cpu() for v in ok])]
+    for k, call in enumerate(bad):
+        with pytest.raises(smla.SmlaError):
+            call()
+            pytest.fail(f"call {k} was not refused")
+    smla.moe_mxfp8(*ok)
+    torch.cuda.synchronize()
 
 
 def test_streams(smla):
