@@ -66,10 +66,6 @@ __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
-}
 // True in one thread of the (whole) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -507,14 +503,12 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
       for (int c = 0; c < kB; ++c) x[c] = ld_shared_v4(raw + slot * kRaw + 16 * (kTileRows + (NT < 32 ? lane % NT : 32 * c + lane)));
       if (!dead) {
         const uint32_t at = to + set * kSetSteps * L::kScaleCols;
-        tmem_st4(at, w[0].x, w[1].x, w[2].x, w[3].x);
-        tmem_st4(at + 4, x[0].x, x[1].x, x[2].x, x[3].x);
-        tmem_st4(at + 8, w[0].y, w[1].y, w[2].y, w[3].y);
-        tmem_st4(at + 12, x[0].y, x[1].y, x[2].y, x[3].y);
-        tmem_st4(at + 16, w[0].z, w[1].z, w[2].z, w[3].z);
-        tmem_st4(at + 20, x[0].z, x[1].z, x[2].z, x[3].z);
-        tmem_st4(at + 24, w[0].w, w[1].w, w[2].w, w[3].w);
-        tmem_st4(at + 28, x[0].w, x[1].w, x[2].w, x[3].w);
+        const uint32_t first[16] = {w[0].x, w[1].x, w[2].x, w[3].x, x[0].x, x[1].x, x[2].x, x[3].x,
+                                    w[0].y, w[1].y, w[2].y, w[3].y, x[0].y, x[1].y, x[2].y, x[3].y};
+        const uint32_t second[16] = {w[0].z, w[1].z, w[2].z, w[3].z, x[0].z, x[1].z, x[2].z, x[3].z,
+                                     w[0].w, w[1].w, w[2].w, w[3].w, x[0].w, x[1].w, x[2].w, x[3].w};
+        tmem_st16(at, first);
+        tmem_st16(at + 16, second);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();

@@ -247,20 +247,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (!dead && g >= kPairSets) dead = __any_sync(kAllLanes, !PAIR_WAIT(m.unscaled[set], (g / kPairSets + 1) & 1));
         if (dead) break;
         tc_fence_after();
+        // lane l: four steps' words of rows l, l + 32, l + 64, l + 96 of each block; column 4 j + c of a step is block j's c-th
+        uint4 w[L::kBlocks][4];
 #pragma unroll
-        for (int j = 0; j < L::kBlocks; ++j) {
-          // lane l: four steps' words of rows l, l + 32, l + 64, l + 96 of the block
-          uint4 w[4];
+        for (int j = 0; j < L::kBlocks; ++j)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            w[c] = *reinterpret_cast<const uint4*>(smem + L::kOffRaw + b * L::kRaw + j * L::kRawBlock + (32 * c + lane) * 32 +
-                                                   4 * half);
-          const uint32_t at = to + 4 * set * L::kScaleCols + 4 * j;
-          tmem_st4(at, w[0].x, w[1].x, w[2].x, w[3].x);
-          tmem_st4(at + L::kScaleCols, w[0].y, w[1].y, w[2].y, w[3].y);
-          tmem_st4(at + 2 * L::kScaleCols, w[0].z, w[1].z, w[2].z, w[3].z);
-          tmem_st4(at + 3 * L::kScaleCols, w[0].w, w[1].w, w[2].w, w[3].w);
-        }
+            w[j][c] = *reinterpret_cast<const uint4*>(smem + L::kOffRaw + b * L::kRaw + j * L::kRawBlock + (32 * c + lane) * 32 +
+                                                      4 * half);
+        uint32_t v[4 * L::kScaleCols];
+#pragma unroll
+        for (int j = 0; j < L::kBlocks; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4& u = w[j][c];
+            v[4 * j + c] = u.x;
+            v[L::kScaleCols + 4 * j + c] = u.y;
+            v[2 * L::kScaleCols + 4 * j + c] = u.z;
+            v[3 * L::kScaleCols + 4 * j + c] = u.w;
+          }
+        static_assert(L::kScaleCols == 12, "48 columns");
+#pragma unroll
+        for (int c = 0; c < 48; c += 16)
+          tmem_st16(to + 4 * set * L::kScaleCols + c, *reinterpret_cast<const uint32_t(*)[16]>(v + c));
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
