@@ -55,8 +55,9 @@ enum MxMode { kLinear, kGated, kMoeUp, kMoeDown };
 
 // Instruction descriptor of kind::mxf8f6f4: e4m3 times e4m3, both K-major, scales
 // as exponent bytes; sf: which of the 4 bytes of the scales' columns.
+__host__ __device__ constexpr uint32_t idesc_sf(uint32_t sf) { return (sf << 4) | (sf << 29); }
 __host__ __device__ constexpr uint32_t idesc_mx(uint32_t M, uint32_t N, uint32_t sf) {
-  return (sf << 4) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24) | (sf << 29);
+  return ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24) | idesc_sf(sf);
 }
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                        uint32_t accumulate) {

@@ -101,7 +101,7 @@ constexpr int kRoleRegs = 64, kScaleRegs = 96, kResultRegs = 176;
 
 template <int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    mx_pair_kernel(const __grid_constant__ MxParams p, const __grid_constant__ CUtensorMap a_map,
+    mx_pair_kernel(const __grid_constant__ MxParams p, const int whole, const int cut, const __grid_constant__ CUtensorMap a_map,
                    const __grid_constant__ CUtensorMap b_map, const __grid_constant__ CUtensorMap a_scale_map,
                    const __grid_constant__ CUtensorMap b_scale_map) {
   constexpr int NA = ACT == SMLA_ACT_SWIGLU ? 2 : 1;
@@ -141,9 +141,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   const int steps = (p.K + kStepK - 1) / kStepK;
   const int token_tiles = (p.T + L::kTokens - 1) / L::kTokens, row_tiles = (p.rows + 2 * kTileRows - 1) / (2 * kTileRows);
-  const int tiles = token_tiles * row_tiles, first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
-  auto token0 = [&](int tile) { return tile % token_tiles * L::kTokens; };
-  auto row0 = [&](int tile) { return tile / token_tiles * (2 * kTileRows) + rank * kTileRows; };
+  // Units: the whole tiles, then those that are cut into `cut` parts of fewer tokens.
+  const int first = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
+  struct Unit {
+    int row, token, tokens;  // this CTA's first feature; the first token and how many columns
+  };
+  auto unit_at = [&](int u) {
+    const int v = u - whole, tile = v < 0 ? u : whole + v / cut;
+    Unit x;
+    x.row = tile / token_tiles * (2 * kTileRows) + rank * kTileRows;
+    x.tokens = v < 0 ? L::kTokens : L::kTokens / cut;
+    x.token = tile % token_tiles * L::kTokens + (v < 0 ? 0 : v % cut * x.tokens);
+    return x;
+  };
+  const int units = whole + (token_tiles * row_tiles - whole) * cut;
+  // The next unit that has tokens, from u on.
+  auto next_unit = [&](int u, Unit& x) {
+    for (; u < units; u += stride) {
+      x = unit_at(u);
+      if (x.token < p.T) break;
+    }
+    return u;
+  };
 
 #define PAIR_WAIT(bar, parity) mbar_wait(&(bar), (parity), abort_flag, &g_mx_timed_out, kDevWaitTimeout)
   if (warp < 4) {
@@ -152,8 +171,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // -------------------------------------------------------------- codes
       int i = 0;
       bool ok = true;
-      for (int tile = first; tile < tiles && ok; tile += stride) {
-        const int y = row0(tile), t = token0(tile) + rank * (L::kTokens / 2);
+      Unit x;
+      for (int u = next_unit(first, x); u < units && ok; u = next_unit(u + stride, x)) {
+        const int y = x.row, t = x.token + rank * (x.tokens / 2);
         for (int k = 0; k < steps; ++k, ++i) {
           const int s = i % L::kStages, use = i / L::kStages;
           if (use > 0 && !(ok = PAIR_WAIT(m.empty[s], (use + 1) & 1))) break;
@@ -178,9 +198,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int s = 0, set = 0, n = 0;
       uint32_t phase = 0, set_phase = 0;
       bool ok = true;
-      for (int tile = first; tile < tiles && ok; tile += stride, ++n) {
+      Unit x;
+      for (int u = next_unit(first, x); u < units && ok; u = next_unit(u + stride, x), ++n) {
         if (n > 0 && !(ok = PAIR_WAIT(m.acc_empty, (n + 1) & 1))) break;
         tc_fence_after();
+        const uint32_t idesc = idesc_mx(2 * kTileRows, (uint32_t)x.tokens, 0);
         for (int k0 = 0; k0 < steps && ok; k0 += 4) {
           if (!(ok = PAIR_WAIT(m.scaled[set], set_phase))) break;
           const int left = min(4, steps - k0);
@@ -196,7 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 for (int a = 0; a < NA; ++a)
                   pair_mma(tmem + a * L::kTokens, sdesc_join<kHi>(lo + ((a * kTileRows * kStepK + 32 * kk) >> 4)),
                            sdesc_join<kHi>(lo + ((NA * kTileRows * kStepK + 32 * kk) >> 4)),
-                           idesc_mx(2 * kTileRows, L::kTokens, kk), sf + 4 * a, sf + 4 * NA,
+                           idesc | idesc_sf(kk), sf + 4 * a, sf + 4 * NA,
                            kk > 0 ? 1u : (uint32_t)((k0 | k) != 0));
               pair_commit(&m.empty[s]);
               if (k + 1 == left) pair_commit(&m.unscaled[set]);
@@ -217,8 +239,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // -------------------------------------------------------------- scales' bytes
       int i = 0;
       bool ok = true;
-      for (int tile = first; tile < tiles && ok; tile += stride) {
-        const int y = row0(tile), t = token0(tile);
+      Unit x;
+      for (int u = next_unit(first, x); u < units && ok; u = next_unit(u + stride, x)) {
+        const int y = x.row, t = x.token;
         for (int k = 0; k < steps; k += 8, ++i) {
           const int b = i & 1;
           if (i >= 2 && !(ok = PAIR_WAIT(m.raw_empty[b], ((i >> 1) + 1) & 1))) break;
@@ -240,7 +263,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t to = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + L::kAcc;
     int g = 0, r = 0;
     bool dead = false;
-    for (int tile = first; tile < tiles && !dead; tile += stride) {
+    Unit x;
+    for (int u = next_unit(first, x); u < units && !dead; u = next_unit(u + stride, x)) {
       for (int k = 0; k < steps; k += 4, ++g) {
         const int b = r & 1, set = g % kPairSets, half = k & 4;
         if (half == 0) dead = __any_sync(kAllLanes, !PAIR_WAIT(m.raw_full[b], (r >> 1) & 1));
@@ -286,13 +310,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ---------------------------------------------------------------- results
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kResultRegs));
     const int q = warp & 3, half = (warp - 8) >> 2;
-    constexpr int kMine = L::kTokens / 2;  // tokens of this warp
-    const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + half * kMine;
+    constexpr int kMine = L::kTokens / 2;  // tokens of this warp, at most
     const uint32_t empty = mapa_shared(smem_u32(&m.acc_empty), 0);
     const MxOut kind = out_kind(p);
     int n = 0;
-    for (int tile = first; tile < tiles; tile += stride, ++n) {
-      const int group = row0(tile) + 32 * q, f = group + lane, t = token0(tile) + half * kMine, ntok = p.T - t;
+    Unit x;
+    for (int u = next_unit(first, x); u < units; u = next_unit(u + stride, x), ++n) {
+      const int group = x.row + 32 * q, f = group + lane, t = x.token + half * (x.tokens / 2);
+      const int ntok = min(p.T - t, x.tokens / 2);
+      const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + half * (x.tokens / 2);
       float bias[NA];
 #pragma unroll
       for (int a = 0; a < NA; ++a) bias[a] = p.to.bias && f < p.rows ? bias_at(p.to, (int64_t)a * p.rows + f) : 0.f;
@@ -411,13 +437,20 @@ cudaError_t launch_pair(const MxLinearArgs& a, const MxParams& p, int num_sms, c
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, num_sms / 2)));
+  // The tiles that do not fill the pairs a last time are cut into parts of fewer tokens where that makes a last turn of
+  // parts: a turn of half the columns takes 0.6 of the time, of a quarter or an eighth half of it.
+  constexpr int kMaxCut = L::kTokens / 32;
+  const int64_t pairs = std::max(1, num_sms / 2), left = tiles % pairs;
+  int cut = 1;
+  while (left > 0 && cut < kMaxCut && left * cut * 2 <= pairs) cut *= 2;
+  const int64_t whole = cut > 1 ? tiles - left : tiles, units = whole + (tiles - whole) * cut;
+  cfg.gridDim = dim3((unsigned)(2 * std::min(units, pairs)));
   cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mx_pair_kernel<ACT>, p, a_map, b_map, a_scale_map, b_scale_map);
+  return cudaLaunchKernelEx(&cfg, mx_pair_kernel<ACT>, p, (int)whole, cut, a_map, b_map, a_scale_map, b_scale_map);
 }
 
 }  // namespace

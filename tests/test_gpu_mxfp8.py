@@ -254,6 +254,15 @@ def test_linear_epilogues_many_tokens(smla, act, out):
     check_linear(smla, 1300, 1120, 384, act=act, bias=torch.float32, residual=out == "residual", quantized=out == "mxfp8")
 
 
+@pytest.mark.parametrize("T,N", [(1277, 4090), (2039, 2816), (1280, 3840), (1019, 2560), (900, 5000), (3400, 2048)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_linear_last_tiles(smla, T, N, act):
+    """Tiles beside those that fill the SMs, whole and in parts of fewer tokens, the last ones ragged."""
+    check_linear(smla, T, N, 96, act=act, bias=torch.bfloat16, residual=True)
+    if N % 32 == 0:
+        check_linear(smla, T, N, 64, act=act, quantized=True)
+
+
 def test_linear_many_tiles(smla):
     check_linear(smla, 1100, 1300, 640, act="gelu", bias=torch.float32)
     check_linear(smla, 1000, 1056, 640, act="swiglu", quantized=True)
