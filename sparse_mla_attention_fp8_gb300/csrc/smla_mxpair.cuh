@@ -7,9 +7,9 @@
 //
 // Scales: rows of 32 bytes (8 steps of K) of the tile's 384 scale rows come by TMA;
 // four warps, one for each quarter of the lanes of tensor memory, store them there,
-// four steps at a time (one at a time, 137 us instead of @@).  (Through
-// shared memory and tcgen05.cp, the copies stood between the MMAs: 2501 x 5120 x
-// 13824 took 166 us against 140 without any scales.)  What one CTA tells the other
+// four steps at a time.  (Through shared memory and tcgen05.cp, the copies stood
+// between the MMAs: 2501 x 5120 x 13824 took 166 us where it took 140 without any
+// scales.)  What one CTA tells the other
 // by an arrival lies in tensor memory or has been read, not in memory: the arrivals
 // are relaxed.  (One that releases at cluster scope waits for the SM's stores in
 // flight: 301 us against 153.)
@@ -17,6 +17,16 @@
 // Warp roles: 0 TMA of the codes (each CTA loads its halves, both count on the
 // first one's barriers), 1 MMA issuer (in the first CTA), 2 TMA of the scales,
 // 4..7 scales, 8..15 results.
+//
+// Measured, alone and (at the power limit, 1.4 kW) in a row: 2501 x 5120 x 13824
+// with gelu 114 and 134 us (3.1 and 2.6 PFLOP/s), 6000 x 4096 x 2 * 8192 gated to
+// MXFP8 238 and 282 us (3.4 and 2.9); the MMAs alone, without copies and results,
+// take 91 and 179.  Between them and the whole lie the switch of a tile (the
+// accumulator of 256 columns has no second place beside the scales), results that
+// share tensor memory and issue slots with the MMAs, and with few turns of tiles
+// the last one.  Copies of the features' codes shared by two pairs (multicast in a
+// cluster of four) changed nothing and left 8 SMs idle; asking for them early, into
+// L2, neither.
 #pragma once
 #include "smla_mxgemm.cuh"
 
@@ -192,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // -------------------------------------------------------------- MMA issuer
       // The whole warp goes through the loop and elects the issuing thread at each step, so that the operands lie in
       // uniform registers; descriptors differ by one addition.  (One thread's loop, with descriptors made anew, was what
-      // bound the kernel: 155 us instead of @@.)
+      // bound the kernel: 155 us instead of 122.)
       constexpr uint32_t kHi = sdesc_hi(1024, kLayoutSw128);
       const uint32_t lo0 = sdesc_lo(smem_u32(smem), 16);
       int s = 0, set = 0, n = 0;

@@ -11,8 +11,9 @@
 // taken (and those that follow as closely) are ordered by scores of 64 bits, one a
 // lane; near ties of groups and of softmax scores rank the token again in 64 bits.
 // (All scores in 64 bits would take an exponential of 64 bits per expert, at a
-// sixtieth of the rate.)  The call is bound by its launch for decode batches and by
-// latency and reading the logits beyond.
+// sixtieth of the rate: 48 tokens with one near tie took 19 us so.)  The call is
+// bound by the launch and the chain of rounds: 48 tokens x 256 experts in 8 groups
+// 7 us (9 with near ties), 9000 x 64 6.4 us, 9000 x 256 in groups 26 us.
 #include <algorithm>
 #include <cstdint>
 #include <cuda_bf16.h>
