@@ -513,6 +513,9 @@ int smla_read_device_status(void* workspace, int* status_out, void* stream);
  * failure handling.  workspace: at least 256 bytes, 256-byte aligned. */
 int smla_paged_wait_check(int many_rows, void* workspace, void* stream);
 
+/* The same as linear_mxfp8 (experts = 0) or moe_mxfp8 reports it. */
+int smla_mxfp8_wait_check(int experts, void* stream);
+
 /* smla_read_device_status for the fixed scratch of
  * sparse_mla_decode_fp8_noalloc on the current device: synchronizes
  * `stream`, then reads and clears the status word (0 = no fault; 1 = a kernel

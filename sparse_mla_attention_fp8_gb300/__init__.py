@@ -227,6 +227,8 @@ def lib():
             L.moe_mxfp8_workspace_bytes.restype = sz
             L.smla_paged_wait_check.argtypes = [i32, P, P]
             L.smla_paged_wait_check.restype = i32
+            L.smla_mxfp8_wait_check.argtypes = [i32, P]
+            L.smla_mxfp8_wait_check.restype = i32
             L.smla_read_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_int), P]
             L.smla_read_noalloc_status.restype = i32
             L.smla_last_error.argtypes = []
@@ -807,6 +809,14 @@ def paged_wait_check(workspace, many_rows: bool = False, stream=None) -> None:
     with torch.cuda.device(dev):
         _check(lib().smla_paged_wait_check(int(many_rows), _ptr(workspace), _stream_ptr(stream, dev)),
                "smla_paged_wait_check")
+
+
+def mxfp8_wait_check(experts: bool = False, stream=None) -> None:
+    """The same on the current device, as linear_mxfp8 or moe_mxfp8 reports it
+    (to read_device_status())."""
+    import torch
+    dev = torch.device("cuda", torch.cuda.current_device())
+    _check(lib().smla_mxfp8_wait_check(int(experts), _stream_ptr(stream, dev)), "smla_mxfp8_wait_check")
 
 
 def read_device_status(workspace=None, stream=None) -> int:

@@ -1105,6 +1105,12 @@ int moe_mxfp8(const uint8_t* x, int64_t x_stride, const uint8_t* x_scale, int64_
   return SMLA_OK;
 }
 
+int smla_mxfp8_wait_check(int experts, void* stream) {
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = experts ? smla::moe_wait_check(s) : smla::mx_linear_wait_check(s);
+  return e == cudaSuccess ? SMLA_OK : cuda_fail(e, "smla_mxfp8_wait_check launch");
+}
+
 const char* smla_last_error(void) { return g_err; }
 
 int smla_version(void) { return 100; }

@@ -515,6 +515,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Matrix res{};
     if (a[3] != Py_None) res = matrix_of(a[3], "residual", at::kBFloat16, T, K, dev);
     const bool codes_too = PyObject_IsTrue(a[5]) == 1;
+    if (!codes_too && (a[7] != Py_None || a[8] != Py_None)) refuse("codes and scales: given, but not asked for (quantized)");
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index);
     Quantized q{};
     if (codes_too) q = quantized(a[7], a[8], "codes", "scales", T, K, dev);
@@ -569,6 +570,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Quantized q{};
     at::Tensor out;
     const bool coded = PyObject_IsTrue(a[7]) == 1;
+    if (!coded && a[9] != Py_None) refuse("out_scale: given, but not asked for (quantized)");
     if (coded)
       q = quantized(a[8], a[9], "out", "out_scale", T, N, dev);
     else

@@ -245,7 +245,9 @@ struct MxLinearArgs {
 };
 // (smla_linear.cu)
 cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t stream);
+// The current device's word that a wait which ran out in the products' kernels sets, and a kernel whose only wait does.
 cudaError_t mx_linear_timed_out(int** word);
+cudaError_t mx_linear_wait_check(cudaStream_t stream);
 
 struct MoeRouteArgs {
   const void* logits;  // bf16 or float32 [T, E]
@@ -286,6 +288,7 @@ struct MoeArgs {
 size_t moe_workspace(int T, int E, int topk, int F);
 cudaError_t launch_moe(const MoeArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t moe_timed_out(int** word);
+cudaError_t moe_wait_check(cudaStream_t stream);
 
 // Offsets inside the workspace.
 constexpr size_t kWsStatusBytes = 256;

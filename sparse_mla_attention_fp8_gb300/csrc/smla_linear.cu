@@ -62,6 +62,7 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t st
                                             : launch_few<kLinear>(a, p, num_sms, stream);
 }
 
+cudaError_t mx_linear_wait_check(cudaStream_t stream) { return mx_wait_check(stream); }
 cudaError_t mx_linear_timed_out(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_mx_timed_out); }
 
 }  // namespace smla

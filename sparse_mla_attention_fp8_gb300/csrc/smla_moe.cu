@@ -102,6 +102,7 @@ cudaError_t launch_moe(const MoeArgs& a, int num_sms, cudaStream_t stream) {
   }
 }
 
+cudaError_t moe_wait_check(cudaStream_t stream) { return mx_wait_check(stream); }
 cudaError_t moe_timed_out(int** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_mx_timed_out); }
 
 }  // namespace smla

@@ -56,6 +56,20 @@ constexpr int kMaxParts = 8;    // of K: CTAs of a (portable) cluster
 // Set when a wait runs out in a kernel of the file that includes this.
 __device__ int g_mx_timed_out;
 
+// One thread that waits for what never comes, and so reports a wait that ran out.
+__global__ void mx_wait_check_kernel() {
+  __shared__ uint64_t bar;
+  __shared__ int abort_flag;
+  abort_flag = 0;
+  mbar_init(&bar, 1);
+  mbar_fence_init();
+  mbar_wait(&bar, 0, &abort_flag, &g_mx_timed_out, kDevWaitTimeout);
+}
+cudaError_t mx_wait_check(cudaStream_t stream) {
+  mx_wait_check_kernel<<<1, 1, 0, stream>>>();
+  return cudaGetLastError();
+}
+
 enum MxMode { kLinear, kGated, kMoeUp, kMoeDown };
 
 // ---------------------------------------------------------------- instructions
@@ -268,6 +282,7 @@ __device__ __forceinline__ void write_out(const MxParams& p, float (&v)[4], int 
     out[(out_row + i) * p.ld + f] = __float2bfloat16_rn(v[i]);
   }
 }
+
 // ---------------------------------------------------------------- the kernel
 
 // grid: x = cluster rank + parts * row tile, y = token tile, z = expert slot (kMoeUp).

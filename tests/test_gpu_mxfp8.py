@@ -572,6 +572,7 @@ def test_refused_tensors(smla):
         lambda: smla.linear_mxfp8(x, xs, w, ws, residual=b), lambda: smla.linear_mxfp8(x, xs, w, ws, out=b),
         lambda: smla.linear_mxfp8(x, xs, w[:95], ws[:95], quantized=True),
         lambda: smla.linear_mxfp8(x, xs, w, ws, residual=b.new_zeros((4, 96)), quantized=True),
+        lambda: smla.linear_mxfp8(x, xs, w, ws, out_scale=xs), lambda: smla.rms_norm_mxfp8(b, normed=True, quantized=False, codes=x),
         lambda: smla.moe_route(b.half(), 2), lambda: smla.moe_route(b, 0), lambda: smla.moe_route(b, 65),
         lambda: smla.moe_route(b.t(), 2), lambda: smla.moe_route(b, 2, bias=b[0]), lambda: smla.moe_route(b, 2, num_groups=3),
         lambda: smla.moe_route(b, 2, ids=torch.zeros((4, 3), dtype=torch.int32, device="cuda")),
@@ -591,6 +592,14 @@ def test_refused_tensors(smla):
             pytest.fail(f"call {k} was not refused")
     smla.moe_mxfp8(*ok)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("experts", [False, True])
+def test_a_wait_that_runs_out_is_reported_once(smla, experts):
+    assert smla.read_device_status() == 0
+    smla.mxfp8_wait_check(experts)
+    assert smla.read_device_status() == 1
+    assert smla.read_device_status() == 0
 
 
 def test_streams(smla):
