@@ -472,6 +472,60 @@ def test_moe_unused_experts_are_not_read(smla):
     assert torch.equal(smla.moe_mxfp8(x, xs, ids, w, w13, s13, w2, s2), clean)
 
 
+# ---------------------------------------------------------------- offsets beyond 32 bits
+
+def coded(g, *shape):
+    """Codes and scale bytes that are drawn as such (no NaN)."""
+    codes = torch.randint(0, 120, shape, generator=g, device="cuda", dtype=torch.uint8)
+    codes |= torch.randint(0, 2, shape, generator=g, device="cuda", dtype=torch.uint8) << 7
+    n = shape[-1] // 32
+    scales = torch.randint(116, 122, shape[:-1] + (-(-n // 16) * 16,), generator=g, device="cuda", dtype=torch.uint8)
+    return codes, scales[..., :n]
+
+
+def test_quantize_beyond_32_bits(smla):
+    T, K = 1_100_001, 2048  # 2.25e9 values
+    x = torch.randn((T, K), generator=gen(1), device="cuda", dtype=torch.bfloat16)
+    codes, scales = smla.mxfp8_quantize(x)
+    for rows in (slice(0, 3), slice(1_048_570, 1_048_580), slice(T - 3, T)):
+        want = ref.bytes_of(x[rows].double())
+        assert torch.equal(codes[rows], want[0]) and torch.equal(scales[rows], want[1])
+    got = smla.rms_norm_mxfp8(x, residual=x, residual_out=x)
+    rows = slice(T - 3, T)
+    check_norm(smla.MxNorm(got.codes[rows], got.scales[rows], None, None), x[rows], None, None, 1e-6)
+
+
+@pytest.mark.parametrize("N", [8, 256])
+def test_linear_beyond_32_bits(smla, N):
+    T, K = 1_100_001, 2048
+    g = gen(2)
+    x, xs = coded(g, T, K)
+    w, ws = coded(g, N, K)
+    got = smla.linear_mxfp8(x, xs, w, ws)
+    for rows in (slice(0, 3), slice(1_048_570, 1_048_580), slice(T - 3, T)):
+        y, off = ref.linear(ref.values(x[rows], xs[rows]), ref.values(w, ws), None, "none", None)
+        within(got[rows], y, off + 2.0 ** -8 * (y.abs() + off))
+
+
+def test_moe_beyond_32_bits(smla):
+    E, K, F = 512, 2048, 1056
+    g = gen(3)
+    w13, s13 = coded(g, E, 2 * F, K)  # 2.2e9 codes
+    w2, s2 = coded(g, E, K, F)
+    x, xs = coded(g, 3, K)
+    ids = torch.tensor([[0, 511], [510, 256], [511, 509]], dtype=torch.int32, device="cuda")
+    w = torch.rand((3, 2), generator=g, device="cuda")
+    s13, s2 = s13 - 4, s2 - 4  # (activations of ordinary sizes)
+    s13, s2 = ([torch.nn.functional.pad(v, (0, -v.shape[2] % 16))[..., :v.shape[2]] for v in (s13, s2)])
+    got = smla.moe_mxfp8(x, xs, ids, w, w13, s13, w2, s2)
+    used = sorted(set(ids.flatten().tolist()))
+    place = torch.full((E,), -1, dtype=torch.int32, device="cuda")
+    place[used] = torch.arange(len(used), dtype=torch.int32, device="cuda")
+    y, off = ref.moe(ref.values(x, xs), place[ids.long()], w, [ref.values(w13[e], s13[e]) for e in used],
+                     [ref.values(w2[e], s2[e]) for e in used], None)
+    within(got, y, off + 2.0 ** -8 * (y.abs() + off))
+
+
 # ---------------------------------------------------------------- together, and how they are called
 
 def layer(smla, t, stream):
