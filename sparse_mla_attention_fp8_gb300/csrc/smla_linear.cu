@@ -42,13 +42,13 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t st
   const auto even = [](const void* q, int64_t stride) { return stride % 2 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0; };
   p.pairs = even(a.to.out, a.N) && (!a.to.residual || even(a.to.residual, a.to.residual_stride));
   p.wide_scales = rows16(a.x_scale, a.x_scale_stride) && rows16(a.w_scale, a.w_scale_stride);
-  // Pairs of CTAs where they have enough tiles, 24, or 8 with a short K (and TMA can copy the scale rows).  Pairs | the
-  // other kernel: K = N = 4096: 16 tiles (256 tokens) 12.8 | 12.3 us, 32 (400) 13.6 | 16.9; K = 8192, N = 1024: 12 tiles
-  // (700) 19.9 | 15.1, 24 (1500) 20.7 | 22.2; K = N = 2048: 8 tiles (128) 8.7 | 9.9, 24 (700) 9.3 | 12.7.  Up to 64 tokens
-  // the other kernel's tiles have fewer columns.
+  // Pairs of CTAs where they have enough tiles, 24, or 8 with a short K.  Pairs | the other kernel: K = N = 4096: 16 tiles
+  // (256 tokens) 12.8 | 12.3 us, 32 (400) 13.6 | 16.9; K = 8192, N = 1024: 12 tiles (700) 19.9 | 15.1, 24 (1500) 20.7 |
+  // 22.2; K = N = 2048: 8 tiles (128) 8.7 | 9.9, 24 (700) 9.3 | 12.7.  Up to 64 tokens the other kernel's tiles have
+  // fewer columns.
   const int64_t columns = a.to.activation == SMLA_ACT_SWIGLU ? 128 : 256;
   const int64_t pair_tiles = ((int64_t)a.N + 255) / 256 * ((a.T + columns - 1) / columns);
-  if (p.wide_scales && a.T > 64 && pair_tiles >= (a.K <= 2048 ? 8 : 24)) {
+  if (a.T > 64 && pair_tiles >= (a.K <= 2048 ? 8 : 24)) {
     switch (a.to.activation) {
       case SMLA_ACT_NONE: return launch_pair<SMLA_ACT_NONE>(a, p, num_sms, stream);
       case SMLA_ACT_RELU: return launch_pair<SMLA_ACT_RELU>(a, p, num_sms, stream);

@@ -5,7 +5,8 @@
 // pairs are persistent; a tile's accumulator (256 columns) is emptied into
 // registers at once, and while its results are written the next tile's MMAs run.
 //
-// Scales: rows of 32 bytes (8 steps of K) of the tile's 384 scale rows come by TMA;
+// Scales: rows of 32 bytes (8 steps of K) of the tile's 384 scale rows come by TMA
+// (where they lie on 16-byte boundaries, otherwise word by word);
 // four warps, one for each quarter of the lanes of tensor memory, store them there,
 // four steps at a time.  (Through shared memory and tcgen05.cp, the copies stood
 // between the MMAs: 2501 x 5120 x 13824 took 166 us where it took 140 without any
@@ -75,6 +76,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
         "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+// True in the four warps of the scales if it is in any of their threads.
+__device__ __forceinline__ bool scale_warps_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
 }
 
 // ---------------------------------------------------------------- layout
@@ -245,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
         mbar_wait_drain(&m.acc_full, n & 1);
       }
-    } else if (warp == 2 && lane == 0) {
+    } else if (warp == 2 && lane == 0 && p.wide_scales) {
       // -------------------------------------------------------------- scales' bytes
       int i = 0;
       bool ok = true;
@@ -271,15 +283,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ---------------------------------------------------------------- scales
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kScaleRegs));
     const uint32_t to = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + L::kAcc;
+    // Scale rows that TMA cannot copy: thread t copies word by word the t-th row of each block, eight steps ahead.
+    const int thread = 32 * (warp - 4) + lane;
+    int next_u = 0, next_k = 0, next_b = 0;
+    Unit next{};
+    auto copy_next = [&]() {
+      if (next_u < units) {
+        const uint32_t raw = smem_u32(smem + L::kOffRaw + next_b * L::kRaw) + 32 * thread;
+#pragma unroll
+        for (int j = 0; j < L::kBlocks; ++j) {
+          const bool features = j < NA;
+          const int at = features ? next.row + thread : next.token + 128 * (j - NA) + thread;
+          const bool there = at < (features ? p.rows : p.T);
+          const uint8_t* row = features ? p.a_scale + ((int64_t)j * p.rows + at) * p.a_scale_stride
+                                        : p.b_scale + (int64_t)at * p.b_scale_stride;
+          for (int k = 0; k < 8 && next_k + k < steps; ++k)
+            cp_async4_zfill(raw + j * L::kRawBlock + 4 * k, there ? row + 4 * (next_k + k) : p.a_scale,
+                            there ? (uint32_t)min(p.K / kMxGroup - 4 * (next_k + k), 4) : 0u);
+        }
+        next_k += 8;
+        if (next_k >= steps) next_k = 0, next_u = next_unit(next_u + stride, next);
+      }
+      next_b ^= 1;
+    };
+    if (!p.wide_scales) {
+      next_u = next_unit(first, next);
+      copy_next();
+    }
     int g = 0, r = 0;
-    bool dead = false;
+    bool dead = false, stop = false;  // (without TMA a warp that gives up goes on to the next meeting with the others)
     Unit x;
-    for (int u = next_unit(first, x); u < units && !dead; u = next_unit(u + stride, x)) {
+    for (int u = next_unit(first, x); u < units && !stop; u = next_unit(u + stride, x)) {
       for (int k = 0; k < steps; k += 4, ++g) {
         const int b = r & 1, set = g % kPairSets, half = k & 4;
-        if (half == 0) dead = __any_sync(kAllLanes, !PAIR_WAIT(m.raw_full[b], (r >> 1) & 1));
+        const bool read = half != 0 || k + 4 >= steps;  // the buffer is done with behind this
+        if (half == 0 && p.wide_scales) dead = __any_sync(kAllLanes, !PAIR_WAIT(m.raw_full[b], (r >> 1) & 1));
+        if (half == 0 && !p.wide_scales) {
+          cp_async_commit();
+          cp_async_wait<0>();
+          stop = scale_warps_any(dead);  // everyone's copies are there, and everyone has read the other buffer
+          if (stop) break;
+          copy_next();
+        }
         if (!dead && g >= kPairSets) dead = __any_sync(kAllLanes, !PAIR_WAIT(m.unscaled[set], (g / kPairSets + 1) & 1));
-        if (dead) break;
+        if (dead) {
+          stop = p.wide_scales;
+          if (stop) break;
+          r += read;
+          continue;
+        }
         tc_fence_after();
         // lane l: four steps' words of rows l, l + 32, l + 64, l + 96 of each block; column 4 j + c of a step is block j's c-th
         uint4 w[L::kBlocks][4];
@@ -307,14 +359,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        const bool read = half != 0 || k + 4 >= steps;  // all of the buffer
         if (lane == 0) {
           mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&m.scaled[set]), 0));
-          if (read) mbar_arrive(&m.raw_empty[b]);
+          if (read && p.wide_scales) mbar_arrive(&m.raw_empty[b]);
         }
-        if (read) ++r;
+        r += read;
       }
     }
+    cp_async_wait<0>();
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- results
@@ -436,8 +488,10 @@ cudaError_t launch_pair(const MxLinearArgs& a, const MxParams& p, int num_sms, c
   CUtensorMap a_map, b_map, a_scale_map, b_scale_map;
   cudaError_t e = code_map(&a_map, a.w, (int64_t)NA * a.N, a.K, a.K, kTileRows);
   if (e == cudaSuccess) e = code_map(&b_map, a.x, a.T, a.K, a.x_stride, L::kTokens / 2);
-  if (e == cudaSuccess) e = scale_map(&a_scale_map, a.w_scale, (int64_t)NA * a.N, a.K / kMxGroup, a.w_scale_stride);
-  if (e == cudaSuccess) e = scale_map(&b_scale_map, a.x_scale, a.T, a.K / kMxGroup, a.x_scale_stride);
+  a_scale_map = b_scale_map = a_map;  // (unused without 16-byte boundaries)
+  if (e == cudaSuccess && p.wide_scales)
+    e = scale_map(&a_scale_map, a.w_scale, (int64_t)NA * a.N, a.K / kMxGroup, a.w_scale_stride);
+  if (e == cudaSuccess && p.wide_scales) e = scale_map(&b_scale_map, a.x_scale, a.T, a.K / kMxGroup, a.x_scale_stride);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (((int64_t)a.T + L::kTokens - 1) / L::kTokens) * (((int64_t)a.N + 2 * kTileRows - 1) / (2 * kTileRows));
   if (tiles > INT32_MAX / 4) return cudaErrorInvalidValue;
