@@ -486,7 +486,7 @@ int moe_route(const void* logits, int logits_type, const float* bias, int scorin
  *   residual        bf16 [T, K] or NULL;  out bf16 [T, K], may be residual
  * K and F multiples of 32; E at most 512; topk at most 32.  The products are exact and summed in float32, over
  * all of a token's experts.  A NaN in an expert's weights reaches the tokens of its tile that do not go to it
- * (tiles of up to 64 tokens); weights of experts that no token of a tile goes to are not read.
+ * (tiles of up to 128 tokens); weights of experts that no token of a tile goes to are not read.
  *   workspace  at least moe_mxfp8_workspace_bytes(...) bytes, 256-byte aligned; NULL = library-cached.  Calls
  *              that may overlap need one each */
 int moe_mxfp8(const uint8_t* x, int64_t x_stride, const uint8_t* x_scale, int64_t x_scale_stride,

@@ -17,7 +17,7 @@ namespace smla {
 
 namespace {
 
-int token_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+int token_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
 
 // h: [token tile][expert slot][token][F] codes, then the scales, in rows on 16-byte boundaries
 struct MoeSizes {
@@ -98,7 +98,8 @@ cudaError_t launch_moe(const MoeArgs& a, int num_sms, cudaStream_t stream) {
   switch (s.tile) {
     case 16: return launch_experts<16>(a, s, num_sms, stream);
     case 32: return launch_experts<32>(a, s, num_sms, stream);
-    default: return launch_experts<64>(a, s, num_sms, stream);
+    case 64: return launch_experts<64>(a, s, num_sms, stream);
+    default: return launch_experts<128>(a, s, num_sms, stream);
   }
 }
 

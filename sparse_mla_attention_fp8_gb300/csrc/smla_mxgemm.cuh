@@ -151,8 +151,8 @@ struct MxMisc {
   int abort_flag, active;
   uint32_t mask[kMaxMoeExperts / 32];
   uint16_t list[kMaxMoeExperts];
-  float share[64];
-  uint8_t routed[64];
+  float share[128];
+  uint8_t routed[128];
 };
 
 template <int NT>
@@ -160,7 +160,7 @@ struct MxLay {
   static constexpr int kATile = kTileRows * kStepK;
   static constexpr int kStage = kATile + NT * kStepK;
   static constexpr int kCtas = 2;  // an SM
-  static constexpr int kMisc = 1664;
+  static constexpr int kMisc = 1920;
   static constexpr int kRawSets = NT > 64 ? 3 : 4;  // sets of scales on their way
   static constexpr int kRaw = kRawSets * (kTileRows + NT) * 16;
   static constexpr int kFit = ((228 / kCtas - 1) * 1024 - 1024 - kMisc - kRaw) / kStage;

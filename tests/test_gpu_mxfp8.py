@@ -420,7 +420,7 @@ def test_moe_smallest(smla):
     check_moe(smla, 1, 1, 1, 128, 128)
 
 
-@pytest.mark.parametrize("T", [1, 2, 16, 17, 33, 64, 65, 97, 200])
+@pytest.mark.parametrize("T", [1, 2, 16, 17, 33, 64, 65, 97, 128, 129, 200])
 def test_moe_tokens(smla, T):
     check_moe(smla, T, 8, 2, 256, 128, residual=T % 2 == 1)
 
@@ -430,6 +430,7 @@ def test_moe_tokens(smla, T):
 def test_moe_sizes(smla, K, F, apart):
     check_moe(smla, 5, 6, 3, K, F, apart=apart)
     check_moe(smla, 50, 6, 3, K, F, residual=True, apart=apart)
+    check_moe(smla, 100, 6, 3, K, F, apart=apart)
 
 
 @pytest.mark.parametrize("E,topk", [(1, 1), (3, 3), (40, 1), (64, 8), (130, 32)])
