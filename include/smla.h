@@ -417,7 +417,9 @@ size_t paged_attention_fp8_workspace_bytes(int T, int H, int HK, int D, int R, i
  * given in elements, and with it every row must be aligned as the first.
  * Every call begins behind the preceding work on `stream`: the launches may
  * overlap its end, but read and write no memory before it has completed; and no
- * call of these signals its dependents early.  A wait in the products that runs
+ * call of these signals its dependents early.  (What the decodes and the latent
+ * stores say of inputs that a kernel of this library writes directly before them
+ * holds for these too.)  A wait in the products that runs
  * past its time limit is reported by smla_read_device_status(NULL, ...). */
 
 #define SMLA_BF16 0
