@@ -29,6 +29,7 @@
 // L2), was slower: 31 to 45 us for 48 gated tokens x 4096 x 2 * 12288, 22.3 without.
 #pragma once
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
@@ -713,14 +714,26 @@ cudaError_t code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K
   return byte_map(map, base, rows, K, stride, kStepK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// The kernel's shared memory, once per device (a fifth of a microsecond, where a small call takes five); `done`: which.
+template <typename F>
+cudaError_t allow_smem(F* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (e != cudaSuccess || (done.load(std::memory_order_relaxed) & bit)) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 template <int MODE, int NT>
 cudaError_t launch_mx(const MxParams& p, int parts, int64_t row_tiles, int64_t token_tiles, int slots,
                       const CUtensorMap& a_map, const CUtensorMap& b_map, cudaStream_t stream) {
   if (row_tiles * parts > INT32_MAX || token_tiles > 65535 || slots > 65535) return cudaErrorInvalidValue;
   auto kernel = mx_gemm_kernel<MODE, NT>;
   constexpr int smem = MxLay<NT>::kSmem;
-  // at every launch: it takes well under a microsecond and needs no per-device record
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(kernel, smem, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -495,7 +495,8 @@ cudaError_t launch_pair(const MxLinearArgs& a, const MxParams& p, int num_sms, c
   if (e != cudaSuccess) return e;
   const int64_t tiles = (((int64_t)a.T + L::kTokens - 1) / L::kTokens) * (((int64_t)a.N + 2 * kTileRows - 1) / (2 * kTileRows));
   if (tiles > INT32_MAX / 4) return cudaErrorInvalidValue;
-  e = cudaFuncSetAttribute(mx_pair_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  static std::atomic<uint64_t> allowed{0};
+  e = allow_smem(mx_pair_kernel<ACT>, L::kSmem, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
