@@ -181,11 +181,28 @@ struct MxLay {
 
 __device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
 
+// x Phi(x), Phi the normal distribution, with the error of Phi's own value also where Phi is small (x (1 + erf(x / sqrt 2)) / 2
+// is 4 % off at -5 in float32 and 0 below -5.6): with a = |x| and s = 1 / (1 + 0.26 a),
+//   1 - Phi(a) = e^(-a^2 / 2) s P(s),
+// as 1 / s times the rest is smooth from a = 0 to infinity.  P: least squares on 0 <= a <= 14, reweighted until the largest
+// relative error, 2^-25, was least; in all within (x^2 + 6) 2^-23 of the value.  (2501 x 5120 x 13824 takes 120 us; by
+// erfcf, whose branches the results' loop takes one after the other, 200, by 1 + erff 127.)
+__device__ __forceinline__ float gelu(float x) {
+  const float a = fabsf(x), s = __fdividef(1.f, fmaf(0.26f, a, 1.f));
+  constexpr float kP[9] = {0.103759058f, 0.103016756f, 0.103030212f, 0.0510278568f, 0.160947397f,
+                           -0.150948226f, 0.251490563f, -0.15282844f, 0.0305047967f};
+  float r = kP[8];
+#pragma unroll
+  for (int k = 7; k >= 0; --k) r = fmaf(r, s, kP[k]);
+  const float q = ex2_approx(a * a * -0.72134752f) * s * r;  // log2(e) / 2
+  return x * (x < 0.f ? q : 1.f - q);
+}
+
 __device__ __forceinline__ float activate(int kind, float x) {
   switch (kind) {
     case SMLA_ACT_RELU: return x < 0.f ? 0.f : x;  // (a NaN stays)
     case SMLA_ACT_SILU: return silu(x);
-    case SMLA_ACT_GELU: return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
+    case SMLA_ACT_GELU: return gelu(x);
     // x (1 + tanh u) / 2 = x / (1 + e^(-2 u))
     case SMLA_ACT_GELU_TANH: return __fdividef(x, 1.f + __expf(-1.5957691216057308f * fmaf(0.044715f * x * x, x, x)));
     default: return x;

@@ -1,0 +1,62 @@
+"""GPU: the MXFP8 operators where float32 runs out, in place, and directly before the library's other calls."""
+import pytest
+import torch
+
+import mx_reference as ref
+
+pytestmark = pytest.mark.gpu
+F64 = torch.float64
+
+
+@pytest.fixture(scope="module")
+def smla():
+    import sparse_mla_attention_fp8_gb300 as m
+    m.build()
+    return m
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def within(got, want, bound):
+    bad = ~((got.double() - want).abs() <= bound)
+    worst = ((got.double() - want).abs() / bound.clamp(min=1e-300)).amax().item()
+    assert not bad.any().item(), f"{int(bad.sum())} of {bad.numel()} outside, worst {worst:.3g} of the bound"
+
+
+# ---------------------------------------------------------------- activations
+
+@pytest.mark.parametrize("T,N", [(5, 192), (37, 256), (1500, 1056)])
+@pytest.mark.parametrize("quantized", [False, True])
+def test_gelu_of_negative_values(smla, T, N, quantized):
+    """Between -9 and -4 gelu is small beside its argument; what is rounded is to be its own value, not the argument's.
+    Every sum is exact: one value of x, 0 or 1, times one of w, -4 to -9, plus a bias of few bits."""
+    K = 64
+    g = gen(T)
+    xv = torch.zeros((T, K), dtype=F64, device="cuda")
+    xv[:, 3] = torch.randint(0, 2, (T,), generator=g, device="cuda").double()
+    xv[0, 3] = 1
+    wv = torch.zeros((N, K), dtype=F64, device="cuda")
+    wv[:, 3] = -(torch.randint(8, 18, (N,), generator=g, device="cuda") / 2).double()
+    wv[32:64, 3] = -6 - torch.arange(32, device="cuda") % 3  # a group beyond -5.6 alone
+    bias = (torch.randint(-15, 16, (N,), generator=g, device="cuda") / 32).float()
+    x, w = ref.quantize(xv), ref.quantize(wv)
+    z = ref.values(*x) @ ref.values(*w).T + bias.double()
+    y = ref.activation("gelu", z)
+    # the exponent, z^2 / 2, is off by two or three roundings of 2^-24 and erfc's argument in another form by as much, which
+    # z^2 2^-23 covers; exponential, quotient, sum and products by 6 steps of 2^-23
+    off = y.abs() * (z * z + 6) * 2.0 ** -23
+    got = smla.linear_mxfp8(*x, *w, bias=bias, activation="gelu", quantized=quantized)
+    if quantized:
+        within(ref.values(*got), y, ref.quantized_bound(y, off))
+    else:
+        within(got, y, off + 2.0 ** -8 * (y.abs() + off))
+
+
+def test_gelu_of_infinite_and_large_values(smla):
+    z = torch.tensor([float("inf"), 1e30, 100.0, 0.0, -0.0, -20.0, -1e30, float("nan")], device="cuda")
+    x, w = (ref.quantize(torch.zeros((rows, 32), dtype=F64, device="cuda")) for rows in (2, 8))
+    got = smla.linear_mxfp8(*x, *w, bias=z, activation="gelu")
+    want = torch.tensor([float("inf"), 1e30, 100.0, 0.0, 0.0, 0.0, 0.0], device="cuda").to(torch.bfloat16)
+    assert torch.equal(got[:, :7], want.expand(2, 7)) and torch.isnan(got[:, 7]).all()
