@@ -191,7 +191,7 @@ __device__ __noinline__ int take_64(const MoeRouteArgs& a, const X* logits, uint
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmax(top, __shfl_xor_sync(kLanes, top, d));
 #pragma unroll
-    for (int i = 0; i < R; ++i) sum += 32 * i + lane < a.E ? exp(x[i] - top) : 0.;
+    for (int i = 0; i < R; ++i) sum += x[i] > -INFINITY ? exp(x[i] - top) : 0.;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kLanes, sum, d);
   }

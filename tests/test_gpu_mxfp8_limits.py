@@ -1,4 +1,5 @@
 """GPU: the MXFP8 operators where float32 runs out, in place, and directly before the library's other calls."""
+import numpy as np
 import pytest
 import torch
 
@@ -60,3 +61,33 @@ def test_gelu_of_infinite_and_large_values(smla):
     got = smla.linear_mxfp8(*x, *w, bias=z, activation="gelu")
     want = torch.tensor([float("inf"), 1e30, 100.0, 0.0, 0.0, 0.0, 0.0], device="cuda").to(torch.bfloat16)
     assert torch.equal(got[:, :7], want.expand(2, 7)) and torch.isnan(got[:, 7]).all()
+
+
+# ---------------------------------------------------------------- routing
+
+def check_route(smla, x, topk, scoring="softmax", bias=None, groups=1, topk_groups=1, masked=None):
+    """ids equal; normalized weights off by the exponentials' arguments (2^-24 of their distance from the largest taken
+    logit), 32 steps of 2^-24 for exponentials, quotients and sums of up to 32, and three times float32's
+    smallest number (two by the exponential, one by the quotient)."""
+    ids, w = smla.moe_route(x, topk, scoring=scoring, bias=bias, num_groups=groups, topk_groups=topk_groups)
+    known = (x if masked is None else torch.where(masked, float("-inf"), x)).double().cpu().numpy()
+    want, ww = ref.route(known, topk, scoring, None if bias is None else bias.double().cpu().numpy(), True, 1.0, groups,
+                         topk_groups)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    taken = np.where(want >= 0, np.take_along_axis(known, want.clip(0), 1), -np.inf)
+    top = taken.max(1, keepdims=True)
+    far = np.where(want >= 0, top - np.where(want >= 0, taken, top), 0)
+    bound = ww * (np.minimum(far, 150) + 32) * 2.0 ** -24 + 3 * 2.0 ** -149
+    bad = np.abs(w.double().cpu().numpy() - ww) > bound
+    assert not bad.any(), (w.cpu().numpy()[bad.any(1)][:2], ww[bad.any(1)][:2])
+
+
+@pytest.mark.parametrize("groups", [1, 4])
+def test_route_near_ties_beside_a_nan(smla, groups):
+    """NaN masks its expert also where near ties are ranked in 64 bits."""
+    g = gen(4)
+    x = torch.randn((50, 1), generator=g, device="cuda") + 1e-7 * torch.randint(-3, 4, (50, 32), generator=g, device="cuda")
+    masked = torch.rand((50, 32), generator=g, device="cuda") < 0.1
+    x = torch.where(masked, float("nan"), x)
+    for scoring in ("softmax", "sigmoid"):
+        check_route(smla, x, 6, scoring, torch.full((32,), 0.25, device="cuda"), groups, 2 if groups > 1 else 1, masked)
