@@ -99,14 +99,16 @@ __device__ __forceinline__ Taken take(const MoeRouteArgs& a, Bits (&keys)[R], Bi
       second = less > other ? less : other;
     }
     Bits group = second ? order_bits(value_of(first) + value_of(second)) : 0;
+    // The error of a group's sum is its two addends', which may be far larger than it; the largest of all groups' counts.
+    float error = check && second ? slack(a.sigmoid, (float)value_of(first)) + slack(a.sigmoid, (float)value_of(second)) : 0.f;
+    if (check) error = __uint_as_float(__reduce_max_sync(kLanes, __float_as_uint(error)));
     __syncwarp();
     uint32_t kept = 0u;
     Bits last = 0;
     for (int r = 0; r <= a.topk_groups; ++r) {  // one more, to see how near it is
       const Bits top = warp_max(group);
       if (check && r == a.topk_groups && top) {
-        const float lo = (float)value_of(top), hi = (float)value_of(last);
-        got.groups_near = hi - lo <= 2.f * (slack(a.sigmoid, lo) + slack(a.sigmoid, hi));
+        got.groups_near = (float)value_of(last) - (float)value_of(top) <= 2.f * error;
       }
       if (r == a.topk_groups || !top) break;
       const int g = (__ffs(__ballot_sync(kLanes, group == top)) - 1) >> share;

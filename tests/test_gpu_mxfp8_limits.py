@@ -82,6 +82,18 @@ def check_route(smla, x, topk, scoring="softmax", bias=None, groups=1, topk_grou
     assert not bad.any(), (w.cpu().numpy()[bad.any(1)][:2], ww[bad.any(1)][:2])
 
 
+def test_route_groups_of_large_biases(smla):
+    """Groups whose two scores and biases nearly cancel: their sums are off by far more than their size says."""
+    g = gen(3)
+    x = torch.randn((200, 1), generator=g, device="cuda") + 1e-5 * torch.randn((200, 16), generator=g, device="cuda")
+    bias = torch.tensor([1000.0, -1000.0], device="cuda").repeat(8)
+    check_route(smla, x.contiguous(), 2, "sigmoid", bias, groups=8, topk_groups=3)
+    check_route(smla, x.contiguous(), 2, "softmax", bias, groups=8, topk_groups=3)
+    # and only some of them
+    few = torch.where(torch.arange(16, device="cuda") < 12, 0.0, bias)
+    check_route(smla, x.contiguous(), 2, "sigmoid", few, groups=8, topk_groups=5)
+
+
 @pytest.mark.parametrize("groups", [1, 4])
 def test_route_near_ties_beside_a_nan(smla, groups):
     """NaN masks its expert also where near ties are ranked in 64 bits."""
