@@ -63,6 +63,10 @@ __device__ __forceinline__ float score_of(bool sigmoid, float x, float top, floa
 // of 512 exponentials (32 are taken).
 __device__ __forceinline__ float slack(bool sigmoid, float x) { return (sigmoid ? 0x1p-21f : 0x1p-19f) * (1.f + fabsf(x)); }
 
+// Below this, in logits from 0 or from the largest, float32 may hold a score with fewer bits than normal numbers have:
+// e^-87.3 is the smallest of these, and a sum of 512 divides by up to e^6.3.
+constexpr float kSmallScore = -80.f;
+
 struct Taken {
   int id;            // lane k: the k-th expert, -1: there was none
   int count;         // how many there are: topk, and those that follow by less than their error
@@ -251,8 +255,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
   }
   if (lane >= a.topk) id = -1;
   // lane k: the k-th expert's weight
-  float w = id >= 0 ? score_of(a.sigmoid, (float)logits[id], top, inv) : 0.f;
+  const float logit = id >= 0 ? (float)logits[id] : -INFINITY;
+  float w = id >= 0 ? score_of(a.sigmoid, logit, top, inv) : 0.f;
   if (a.renormalize) {
+    if (__any_sync(kLanes, id >= 0 && (a.sigmoid ? logit : logit - top) < kSmallScore)) {
+      // Shares are ratios, whatever the scores' size: all times what makes the largest taken one about 1.
+      float most = logit;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kLanes, most, d));
+      if (a.sigmoid) most = fminf(most, 0.f);
+      w = 0.f;
+      if (id >= 0) w = !a.sigmoid ? expf(logit - most) : logit < 0.f ? expf(logit - most) / (1.f + expf(logit)) : 1.f / (1.f + expf(-logit));
+    }
     float all = w;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(kLanes, all, d);

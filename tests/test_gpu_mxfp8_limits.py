@@ -82,6 +82,36 @@ def check_route(smla, x, topk, scoring="softmax", bias=None, groups=1, topk_grou
     assert not bad.any(), (w.cpu().numpy()[bad.any(1)][:2], ww[bad.any(1)][:2])
 
 
+@pytest.mark.parametrize("E,groups", [(16, 1), (64, 1), (64, 8), (256, 8)])
+@pytest.mark.parametrize("at", [-75.0, -86.0, -90.0, -100.0, -300.0])
+def test_route_of_small_sigmoid_scores(smla, at, E, groups):
+    """Logits whose float32 scores are 0 or nearly so: their shares are ordinary numbers."""
+    x = at + 3 * torch.randn((40, E), generator=gen(E), device="cuda")
+    x[20:] *= 1 + 0.1 * torch.rand((20, 1), generator=gen(1), device="cuda")
+    for bias in (None, torch.zeros(E, device="cuda")):
+        check_route(smla, x, 6, "sigmoid", bias, groups, max(1, groups // 2))
+
+
+def test_route_of_scores_far_apart(smla):
+    """A large score beside ones that float32 holds with few bits or not at all."""
+    x = torch.tensor([[-20.0, -84.0, -95.0, -104.0, -200.0], [-60.0, -90.0, -100.0, -110.0, -130.0],
+                      [3.0, -90.0, -101.0, -200.0, -60.0], [-100.0, -100.0, -100.0, -100.0, -100.0]], device="cuda")
+    for topk in (1, 2, 5):
+        check_route(smla, x, topk, "sigmoid")
+        check_route(smla, x, topk, "softmax")
+
+
+def test_route_of_small_softmax_scores(smla):
+    """A bias that takes experts whose scores are 0 in float32."""
+    g = gen(7)
+    x = 2 * torch.randn((30, 32), generator=g, device="cuda")
+    x[:, :8] += 150
+    bias = torch.where(torch.arange(32, device="cuda") < 8, 0.0, 2.0) + torch.arange(32, device="cuda") / 64
+    check_route(smla, x, 4, "softmax", bias)
+    check_route(smla, x, 12, "softmax", bias)
+    check_route(smla, x, 4, "softmax", bias, groups=4, topk_groups=2)
+
+
 def test_route_groups_of_large_biases(smla):
     """Groups whose two scores and biases nearly cancel: their sums are off by far more than their size says."""
     g = gen(3)
