@@ -451,7 +451,7 @@ int rms_norm_mxfp8(const void* x, int64_t x_stride, const void* residual, int64_
  *   w, w_scale   MXFP8, codes contiguous
  *   bias         bias_type, or NULL;  residual  bf16 [T, N] or NULL
  *   out          bf16 [T, N]; or NULL, and codes, scales = MXFP8 of y (N a multiple of 32; 4-byte aligned)
- * out may be residual.  The products are exact and summed in float32. */
+ * out may be residual.  T at most 2^31 - 257.  The products are exact and summed in float32. */
 #define SMLA_ACT_NONE 0
 #define SMLA_ACT_RELU 1
 #define SMLA_ACT_SILU 2

@@ -960,6 +960,8 @@ int linear_mxfp8(const uint8_t* x, int64_t x_stride, const uint8_t* x_scale, int
   if (!out && N % 32 != 0) return fail(SMLA_ERR_INVALID_ARG, "N=%d must be a multiple of 32 for MXFP8 results", N);
   if (!out && residual) return fail(SMLA_ERR_UNSUPPORTED, "a residual with MXFP8 results is unsupported");
   if (N > INT32_MAX / 2 - 128) return fail(SMLA_ERR_UNSUPPORTED, "N=%d unsupported", N);
+  // (the last tile's tokens are counted in 32 bits)
+  if (T > INT32_MAX - 256) return fail(SMLA_ERR_UNSUPPORTED, "T=%d unsupported: at most %d", T, INT32_MAX - 256);
   if (T == 0) return SMLA_OK;
   rc = check_aligned_rows("x", x, x_stride, K, 1);
   if (rc == SMLA_OK) rc = check_scales("x_scale", x_scale, x_scale_stride, K);
