@@ -518,6 +518,11 @@ int smla_paged_wait_check(int many_rows, void* workspace, void* stream);
 /* The same as linear_mxfp8 (experts = 0) or moe_mxfp8 reports it. */
 int smla_mxfp8_wait_check(int experts, void* stream);
 
+/* For tests of failure handling, too: while on (1) for this thread, the kernels
+ * of its linear_mxfp8 and moe_mxfp8 calls unwind as if their waits ran past the
+ * time limit at once: they report it, and their outputs are not valid. */
+void smla_mxfp8_give_up(int on);
+
 /* smla_read_device_status for the fixed scratch of
  * sparse_mla_decode_fp8_noalloc on the current device: synchronizes
  * `stream`, then reads and clears the status word (0 = no fault; 1 = a kernel

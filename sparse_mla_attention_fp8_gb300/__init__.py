@@ -229,6 +229,8 @@ def lib():
             L.smla_paged_wait_check.restype = i32
             L.smla_mxfp8_wait_check.argtypes = [i32, P]
             L.smla_mxfp8_wait_check.restype = i32
+            L.smla_mxfp8_give_up.argtypes = [i32]
+            L.smla_mxfp8_give_up.restype = None
             L.smla_read_noalloc_status.argtypes = [ctypes.POINTER(ctypes.c_int), P]
             L.smla_read_noalloc_status.restype = i32
             L.smla_last_error.argtypes = []
@@ -817,6 +819,13 @@ def mxfp8_wait_check(experts: bool = False, stream=None) -> None:
     import torch
     dev = torch.device("cuda", torch.cuda.current_device())
     _check(lib().smla_mxfp8_wait_check(int(experts), _stream_ptr(stream, dev)), "smla_mxfp8_wait_check")
+
+
+def mxfp8_give_up(on: bool) -> None:
+    """While on, this thread's linear_mxfp8 and moe_mxfp8 calls unwind as if
+    their kernels' waits ran out at once, and report it: for tests of a caller's
+    failure handling."""
+    lib().smla_mxfp8_give_up(int(on))
 
 
 def read_device_status(workspace=None, stream=None) -> int:

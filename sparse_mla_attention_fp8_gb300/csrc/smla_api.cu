@@ -861,6 +861,8 @@ int paged_attention_fp8(const void* q, int64_t q_stride, const uint8_t* k_cache,
 // ---- MXFP8 operators
 
 namespace {
+thread_local bool g_give_up = false;  // (smla_mxfp8_give_up)
+
 int check_type(const char* name, int type) {
   if (type != SMLA_BF16 && type != SMLA_F32)
     return fail(SMLA_ERR_INVALID_ARG, "%s: %d is no type (SMLA_BF16 or SMLA_F32)", name, type);
@@ -998,6 +1000,7 @@ int linear_mxfp8(const uint8_t* x, int64_t x_stride, const uint8_t* x_scale, int
   a.T = T;
   a.N = N;
   a.K = K;
+  a.give_up = g_give_up;
   cudaError_t e = smla::launch_mx_linear(a, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "linear_mxfp8 launch");
   return SMLA_OK;
@@ -1102,6 +1105,7 @@ int moe_mxfp8(const uint8_t* x, int64_t x_stride, const uint8_t* x_scale, int64_
   a.topk = topk;
   a.K = K;
   a.F = F;
+  a.give_up = g_give_up;
   cudaError_t e = smla::launch_moe(a, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "moe_mxfp8 launch");
   return SMLA_OK;
@@ -1112,6 +1116,8 @@ int smla_mxfp8_wait_check(int experts, void* stream) {
   const cudaError_t e = experts ? smla::moe_wait_check(s) : smla::mx_linear_wait_check(s);
   return e == cudaSuccess ? SMLA_OK : cuda_fail(e, "smla_mxfp8_wait_check launch");
 }
+
+void smla_mxfp8_give_up(int on) { g_give_up = on != 0; }
 
 const char* smla_last_error(void) { return g_err; }
 

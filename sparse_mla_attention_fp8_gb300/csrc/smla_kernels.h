@@ -242,6 +242,7 @@ struct MxLinearArgs {
   int64_t w_scale_stride;
   MxEpilogue to;
   int T, N, K;
+  bool give_up;  // for tests: the kernels' waits run out at once
 };
 // (smla_linear.cu)
 cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t stream);
@@ -283,6 +284,7 @@ struct MoeArgs {
   void* out;             // bf16 [T, K]
   void* workspace;
   int T, E, topk, K, F;
+  bool give_up;  // as for the linear product
 };
 // (smla_moe.cu)
 size_t moe_workspace(int T, int E, int topk, int F);

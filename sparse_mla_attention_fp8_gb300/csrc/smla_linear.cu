@@ -37,6 +37,7 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t st
   p.rows = a.N;
   p.T = a.T;
   p.K = a.K;
+  p.give_up = a.give_up;
   p.to = a.to;
   p.ld = a.N;
   const auto even = [](const void* q, int64_t stride) { return stride % 2 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0; };

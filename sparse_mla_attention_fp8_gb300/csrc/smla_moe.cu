@@ -50,6 +50,7 @@ cudaError_t launch_experts(const MoeArgs& a, const MoeSizes& s, int num_sms, cud
   up.rows = a.F;
   up.T = a.T;
   up.K = a.K;
+  up.give_up = a.give_up;
   up.to.codes = ws + s.codes;
   up.to.scales = ws + s.scales;
   up.to.scale_stride = s.scale_stride;

@@ -116,6 +116,18 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
 __device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
   asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// As if `bytes` bytes had arrived in the barrier's present phase.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -131,6 +143,7 @@ struct MxParams {
   int64_t b_scale_stride;
   int rows;                // features (of a gated product: the gate's; the up part's rows follow them)
   int T, K;                // tokens; values of a row
+  bool give_up;            // for tests: every wait that is not over at once has run out
   MxEpilogue to;
   int64_t ld;              // features of an output row
   bool pairs;              // bf16 results and residual can be accessed two at a time
@@ -329,7 +342,7 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
       mbar_init(&m.unscaled[s], 1);
     }
     mbar_init(&m.done, 1);
-    m.abort_flag = 0;
+    m.abort_flag = p.give_up;
     mbar_fence_init();
   }
   if (tid == 96) {
@@ -396,6 +409,7 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
 
 #define MX_WAIT(bar, parity) mbar_wait(&(bar), (parity), abort_flag, &g_mx_timed_out, kDevWaitTimeout)
   bool dead = false;
+  int issued = 0;  // copies of codes (warp 0)
   if (warp == 0) {
     // ---------------------------------------------------------------- codes
     auto load_a = [&](int i, int s) {
@@ -419,7 +433,8 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
       if (lane == 0)
         for (int i = 0; i < early; ++i) load_b(i, i);
     }
-    int s = early % L::kStages, issued = early;
+    int s = early % L::kStages;
+    issued = early;
     uint32_t phase = early == L::kStages ? 1u : 0u;  // of the fillings of stage s
     bool ok = true;
     for (int i = early; i < n && ok; ++i) {
@@ -434,11 +449,6 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
       ++issued;
       if (++s == L::kStages) s = 0, phase ^= 1u;
     }
-    // after an abort no copy may still be landing when the CTA exits: the last one of each stage
-    if (!ok)
-      for (int i = max(0, issued - L::kStages); i < issued; ++i)
-        mbar_wait_drain(&m.full[i % L::kStages], (i / L::kStages) & 1);
-    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     // The whole warp goes through the loop and elects the issuing thread, so that operands lie in uniform registers.
@@ -625,7 +635,7 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
     }
   } else {
     float* part = reinterpret_cast<float*>(smem);  // [column][row]; every copy and MMA has ended
-    if (warp >= 2) {
+    if (warp >= 2 && !dead) {
 #pragma unroll 1
       for (int c = 16 * half; c < ntok; c += 32) {
         uint32_t w[16];
@@ -688,6 +698,14 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kCols);
+  }
+  if (*abort_flag) {
+    // A wait ran out, and what it was for may still be under way: no copy may land once this CTA's shared memory is
+    // another's.  (The MMAs have been waited for, and the scales' copies.)
+    if (warp == 0)
+      for (int i = max(0, issued - L::kStages); i < issued; ++i)
+        mbar_wait_drain(&m.full[i % L::kStages], (i / L::kStages) & 1);
+    if (tid == 0) atomicExch(&g_mx_timed_out, kDevWaitTimeout);
   }
 }
 

@@ -109,9 +109,10 @@ struct PairLay {
   static_assert(kSmem <= 232448 && kStage % 1024 == 0 && kAcc + kPairSets * 4 * kScaleCols <= kCols, "limits");
 };
 struct PairMisc {
-  uint64_t full[6], empty[6], scaled[kPairSets], unscaled[kPairSets], raw_full[2], raw_empty[2], acc_full, acc_empty;
+  uint64_t full[6], empty[6], scaled[kPairSets], unscaled[kPairSets], raw_full[2], raw_empty[2], acc_full, acc_empty, idle;
   uint32_t tmem;
   int abort_flag;
+  int codes, scales;  // copies that this CTA has issued: of codes (a stage each), of scales (a buffer each)
 };
 static_assert(sizeof(PairMisc) <= 256, "misc");
 
@@ -150,7 +151,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     mbar_init(&m.acc_full, 1);
     mbar_init(&m.acc_empty, 16);
-    m.abort_flag = 0;
+    mbar_init(&m.idle, 1);
+    m.abort_flag = p.give_up;
+    m.codes = m.scales = 0;
     mbar_fence_init();
   }
   if (warp == 1) pair_alloc(&m.tmem, L::kCols);
@@ -207,9 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           pair_load_2d(stage + NA * kTileRows * kStepK, &b_map, k * kStepK, t, bar);
         }
       }
-      // after an abort no copy may still be landing when the CTAs exit
-      if (!ok && rank == 0)
-        for (int j = max(0, i - L::kStages); j < i; ++j) mbar_wait_drain(&m.full[j % L::kStages], (j / L::kStages) & 1);
+      m.codes = i;
     } else if (warp == 1 && rank == 0) {
       // -------------------------------------------------------------- MMA issuer
       // The whole warp goes through the loop and elects the issuing thread at each step, so that the operands lie in
@@ -252,11 +253,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (++set == kPairSets) set = 0, set_phase ^= 1;
         }
       }
-      if (!ok) {  // after an abort nothing is left in flight: every commit so far, in its order
-        if (elect_one()) pair_commit(&m.acc_full);
-        __syncwarp();
-        mbar_wait_drain(&m.acc_full, n & 1);
-      }
     } else if (warp == 2 && lane == 0 && p.wide_scales) {
       // -------------------------------------------------------------- scales' bytes
       int i = 0;
@@ -275,8 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         j < NA ? y + j * p.rows : t + 128 * (j - NA), &m.raw_full[b]);
         }
       }
-      if (!ok)
-        for (int j = max(0, i - 2); j < i; ++j) mbar_wait_drain(&m.raw_full[j & 1], (j >> 1) & 1);
+      m.scales = i;
     }
     __syncwarp();
   } else if (warp < 8) {
@@ -470,7 +465,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #undef PAIR_WAIT
   tc_fence_before();
   __syncwarp();
+  // Where a wait ran out both CTAs unwind: whose warp raised the flag raises the other CTA's.
+  if (lane == 0 && *abort_flag) st_cluster_u32(mapa_shared(smem_u32(&m.abort_flag), (uint32_t)rank ^ 1u), 1u);
+  __syncwarp();
   cluster_sync_all();
+  if (*abort_flag) {
+    // Nothing may be under way any more when the CTAs end: MMAs read both CTAs' memory, copies land in it.
+    if (warp == 1) {
+      if (rank == 0 && elect_one()) pair_commit(&m.idle);
+      __syncwarp();
+      mbar_wait_drain(&m.idle, 0);
+    } else if (tid == 0 && rank == 0) {
+      // both CTAs' copies count on the barriers here, and one may have issued up to kStages more than the other
+      const int mine = m.codes, other = (int)ld_cluster_u32(mapa_shared(smem_u32(&m.codes), 1)), most = max(mine, other);
+      for (int j = max(0, most - L::kStages); j < most; ++j) {
+        const int s = j % L::kStages;
+        if (j >= mine) mbar_arrive_expect_tx(&m.full[s], L::kStage);
+        if (j >= other) mbar_complete_tx(&m.full[s], L::kStage);
+        mbar_wait_drain(&m.full[s], (j / L::kStages) & 1);
+      }
+    } else if (warp == 2) {
+      for (int j = max(0, m.scales - 2); j < m.scales; ++j) mbar_wait_drain(&m.raw_full[j & 1], (j >> 1) & 1);
+    }
+    if (tid == 0) atomicExch(&g_mx_timed_out, kDevWaitTimeout);
+    __syncwarp();
+    cluster_sync_all();
+  }
   if (warp == 1) {
     tc_fence_after();
     pair_dealloc(tmem, L::kCols);

@@ -133,3 +133,51 @@ def test_route_near_ties_beside_a_nan(smla, groups):
     x = torch.where(masked, float("nan"), x)
     for scoring in ("softmax", "sigmoid"):
         check_route(smla, x, 6, scoring, torch.full((32,), 0.25, device="cuda"), groups, 2 if groups > 1 else 1, masked)
+
+
+# ---------------------------------------------------------------- waits that run out
+
+def matrix(g, *shape, apart=16):
+    """Codes and scale bytes that are drawn as such (no NaN)."""
+    codes = torch.randint(0, 120, shape, generator=g, device="cuda", dtype=torch.uint8)
+    codes |= torch.randint(0, 2, shape, generator=g, device="cuda", dtype=torch.uint8) << 7
+    n = shape[-1] // 32
+    scales = torch.randint(112, 118, shape[:-1] + (-(-n // apart) * apart,), generator=g, device="cuda", dtype=torch.uint8)
+    return codes, scales[..., :n]
+
+
+def gives_up_and_recovers(smla, call):
+    """Calls that unwind, one alone and several in a row, each time with a right one behind them."""
+    want = call()
+    assert smla.read_device_status() == 0
+    for calls in (1, 1, 4):
+        smla.mxfp8_give_up(True)
+        try:
+            for _ in range(calls):
+                call()
+        finally:
+            smla.mxfp8_give_up(False)
+        assert smla.read_device_status() == 1
+        got = call()
+        assert smla.read_device_status() == 0
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("apart", [4, 16])
+@pytest.mark.parametrize("T,N,K,act", [(5, 128, 4096, "none"), (70, 96, 544, "swiglu"), (100, 4096, 2080, "none"),
+                                       (1500, 1040, 1056, "none"), (1400, 600, 2080, "swiglu"), (5000, 8192, 512, "gelu")])
+def test_linear_unwinds(smla, T, N, K, act, apart):
+    """Every form of the product, where copies and products are under way when the waits run out."""
+    g = gen(T)
+    x, w = matrix(g, T, K, apart=apart), matrix(g, 2 * N if act == "swiglu" else N, K, apart=apart)
+    gives_up_and_recovers(smla, lambda: smla.linear_mxfp8(*x, *w, activation=act))
+
+
+@pytest.mark.parametrize("T", [1, 20, 50, 300])
+def test_experts_unwind(smla, T):
+    E, topk, K, F = 6, 2, 1056, 544
+    g = gen(T)
+    x, w13, w2 = matrix(g, T, K), matrix(g, E, 2 * F, K), matrix(g, E, K, F)
+    ids = torch.randint(0, E, (T, topk), generator=g, device="cuda").int()
+    p = torch.rand((T, topk), generator=g, device="cuda")
+    gives_up_and_recovers(smla, lambda: smla.moe_mxfp8(*x, ids, p, *w13, *w2))
