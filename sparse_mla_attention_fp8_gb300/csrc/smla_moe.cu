@@ -19,7 +19,7 @@ namespace {
 
 int token_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
 
-// h: [token tile][expert slot][token][F] codes, then the scales, in rows on 16-byte boundaries
+// behind the status word h: [token tile][expert slot][token][F] codes, then the scales, in rows on 16-byte boundaries
 struct MoeSizes {
   int tile, slots;
   int64_t tiles, rows, scale_stride;
@@ -51,6 +51,7 @@ cudaError_t launch_experts(const MoeArgs& a, const MoeSizes& s, int num_sms, cud
   up.T = a.T;
   up.K = a.K;
   up.give_up = a.give_up;
+  up.status = reinterpret_cast<int*>(ws);
   up.to.codes = ws + s.codes;
   up.to.scales = ws + s.scales;
   up.to.scale_stride = s.scale_stride;

@@ -144,6 +144,7 @@ struct MxParams {
   int rows;                // features (of a gated product: the gate's; the up part's rows follow them)
   int T, K;                // tokens; values of a row
   bool give_up;            // for tests: every wait that is not over at once has run out
+  int* status;             // of the call's workspace, or null: set when a wait runs out, as g_mx_timed_out
   MxEpilogue to;
   int64_t ld;              // features of an output row
   bool pairs;              // bf16 results and residual can be accessed two at a time
@@ -717,7 +718,10 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
     if (warp == 0)
       for (int i = max(0, issued - L::kStages); i < issued; ++i)
         mbar_wait_drain(&m.full[i % L::kStages], (i / L::kStages) & 1);
-    if (tid == 0) atomicExch(&g_mx_timed_out, kDevWaitTimeout);
+    if (tid == 0) {
+      atomicExch(&g_mx_timed_out, kDevWaitTimeout);
+      if (p.status) atomicExch(p.status, kDevWaitTimeout);  // (whatever an uninitialised workspace held)
+    }
   }
 }
 

@@ -181,3 +181,27 @@ def test_experts_unwind(smla, T):
     ids = torch.randint(0, E, (T, topk), generator=g, device="cuda").int()
     p = torch.rand((T, topk), generator=g, device="cuda")
     gives_up_and_recovers(smla, lambda: smla.moe_mxfp8(*x, ids, p, *w13, *w2))
+
+
+@pytest.mark.parametrize("T", [1, 50, 130])
+def test_experts_report_in_their_workspace(smla, T):
+    """Once in the workspace that the call had, once for the device; another workspace's word stays as it is."""
+    E, topk, K, F = 6, 2, 512, 256
+    g = gen(T)
+    x, w13, w2 = matrix(g, T, K), matrix(g, E, 2 * F, K), matrix(g, E, K, F)
+    ids = torch.randint(0, E, (T, topk), generator=g, device="cuda").int()
+    p = torch.rand((T, topk), generator=g, device="cuda")
+    ws, other = (torch.zeros(smla.moe_mxfp8_workspace_bytes(T, E, topk, F), dtype=torch.uint8, device="cuda") for _ in range(2))
+    for held in (0, 119):  # zeroed, and what an uninitialised workspace held
+        ws[:4] = held
+        smla.mxfp8_give_up(True)
+        try:
+            smla.moe_mxfp8(*x, ids, p, *w13, *w2, workspace=ws)
+        finally:
+            smla.mxfp8_give_up(False)
+        smla.moe_mxfp8(*x, ids, p, *w13, *w2, workspace=other)
+        assert smla.read_device_status(other) == 0
+        assert smla.read_device_status(ws) == 1 and smla.read_device_status(ws) == 0
+        assert smla.read_device_status() == 1 and smla.read_device_status() == 0
+        smla.moe_mxfp8(*x, ids, p, *w13, *w2, workspace=ws)
+        assert smla.read_device_status(ws) == 0
