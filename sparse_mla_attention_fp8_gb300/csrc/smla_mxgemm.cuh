@@ -310,7 +310,8 @@ __device__ __forceinline__ void write_out(const MxParams& p, float (&v)[4], int 
       const int k = i + (lane & 1);
       if (k >= n || even >= p.rows) continue;
       if (res) {
-        const uint32_t r = __ldg(reinterpret_cast<const uint32_t*>(res + (out_row + k) * to.residual_stride + even));
+        // (a plain load: out may be the residual)
+        const uint32_t r = *reinterpret_cast<const uint32_t*>(res + (out_row + k) * to.residual_stride + even);
         lo += __uint_as_float(r << 16);
         hi += __uint_as_float(r & 0xffff0000u);
       }

@@ -107,13 +107,14 @@ __global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ MxNo
   const int col0 = 8 * t;
   grid_dependency_wait();
   uint4 x[kAhead ? kChunks : 1], r[kAhead ? kChunks : 1];
+  // (plain loads: the sum may go back to where x or the residual lies)
   auto load = [&](int64_t row, int c, uint4& x, uint4& r) {
     const int col = col0 + 8 * threads * c;
     x = r = make_uint4(0u, 0u, 0u, 0u);
     if (row >= a.T || col >= a.K) return;
-    x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + row * a.x_stride + col));
+    x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + row * a.x_stride + col);
     if (a.residual)
-      r = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.residual) + row * a.residual_stride + col));
+      r = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.residual) + row * a.residual_stride + col);
   };
   if (kAhead)
 #pragma unroll

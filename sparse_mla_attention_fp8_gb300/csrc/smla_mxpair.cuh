@@ -433,8 +433,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             uint32_t r[kAtOnce / 2];
             if (kResidual) {
 #pragma unroll
-              for (int i = 0; i < kAtOnce / 2; ++i, res += p.to.residual_stride)
-                r[i] = c0 + 2 * i + (lane & 1) < last ? __ldg(res) : 0u;
+              for (int i = 0; i < kAtOnce / 2; ++i, res += p.to.residual_stride)  // (plain loads: out may be the residual)
+                r[i] = c0 + 2 * i + (lane & 1) < last ? *res : 0u;
             }
 #pragma unroll
             for (int i = 0; i < kAtOnce / 2; ++i, out += p.ld) {

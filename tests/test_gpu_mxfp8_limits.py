@@ -205,3 +205,36 @@ def test_experts_report_in_their_workspace(smla, T):
         assert smla.read_device_status() == 1 and smla.read_device_status() == 0
         smla.moe_mxfp8(*x, ids, p, *w13, *w2, workspace=ws)
         assert smla.read_device_status(ws) == 0
+
+
+# ---------------------------------------------------------------- in place
+
+@pytest.mark.parametrize("T,K", [(1, 512), (6000, 512), (3001, 4096), (2000, 16416), (700, 65536)])
+@pytest.mark.parametrize("over", ["x", "residual"])
+def test_norm_over_its_inputs(smla, T, K, over):
+    """Many rows for each CTA, the sum written over what is read: the same bits as apart."""
+    g = gen(K)
+    x, r = (torch.randn((T, K), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    w = torch.rand(K, generator=g, device="cuda")
+    want = smla.rms_norm_mxfp8(x, w, residual=r, normed=True)
+    assert torch.equal(want.residual, (x.float() + r.float()).to(torch.bfloat16))
+    held = dict(x=x, residual=r)[over].clone()
+    a, b = (held, r) if over == "x" else (x, held)
+    for _ in range(3):
+        held.copy_(dict(x=x, residual=r)[over])
+        got = smla.rms_norm_mxfp8(a, w, residual=b, normed=True, residual_out=held)
+        assert got.residual.data_ptr() == held.data_ptr()
+        assert all(torch.equal(u, v) for u, v in zip(got, want))
+
+
+@pytest.mark.parametrize("T,N,K,act", [(3, 512, 4096, "none"), (100, 515, 512, "none"), (1500, 2048, 512, "gelu_tanh"),
+                                       (1500, 1041, 512, "none"), (1400, 1200, 512, "swiglu")])
+def test_linear_over_its_residual(smla, T, N, K, act):
+    g = gen(N)
+    x, w = matrix(g, T, K), matrix(g, 2 * N if act == "swiglu" else N, K)
+    r = torch.randn((T, N), generator=g, device="cuda", dtype=torch.bfloat16)
+    want = smla.linear_mxfp8(*x, *w, activation=act, residual=r)
+    for _ in range(3):
+        held = r.clone()
+        assert smla.linear_mxfp8(*x, *w, activation=act, residual=held, out=held).data_ptr() == held.data_ptr()
+        assert torch.equal(held, want)
