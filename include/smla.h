@@ -66,7 +66,8 @@ extern "C" {
  * attention kernels do; ordinary kernels do not), the decode's index translation and Q split may read
  * q, indices, block_table and req_id_per_token before it has finished.  Everything that reads kv_cache
  * or writes out, lse or the workspace waits for it.  So write those four inputs with other kernels,
- * not with a kernel of this library (but paged_blocks_extend) launched directly before the call. */
+ * not with a kernel of this library (but paged_blocks_extend, and linear_mxfp8 with bf16 rows of a
+ * multiple of 576 values) launched directly before the call. */
 int sparse_mla_decode_fp8(const void* q, const uint8_t* kv_cache, const int32_t* indices,
                           const int32_t* block_table, const int32_t* req_id_per_token, float sm_scale,
                           int num_splits, void* out, float* lse, int T, int H, int K, int R, int MB, int NB,
@@ -254,7 +255,8 @@ int sparse_mla_attention_plan(int fp8, int T, int H, int K, int num_splits, int*
  * completed, so a decode running before it still reads the old rows.  If that kernel signals its
  * dependents early (this library's decode and attention kernels do; ordinary kernels do not),
  * kv_new and slot_mapping may be read before it has finished: write those two with other kernels,
- * not with a kernel of this library (but paged_blocks_extend) launched directly before the call. */
+ * not with a kernel of this library (but paged_blocks_extend, and linear_mxfp8 with bf16 rows of a
+ * multiple of 576 values) launched directly before the call. */
 int mla_cache_store_fp8(const void* kv_new, const int64_t* slot_mapping, uint8_t* kv_cache, int T, int NB,
                         void* stream);
 
@@ -417,10 +419,14 @@ size_t paged_attention_fp8_workspace_bytes(int T, int H, int HK, int D, int R, i
  * given in elements, and with it every row must be aligned as the first.
  * Every call begins behind the preceding work on `stream`: the launches may
  * overlap its end, but read and write no memory before it has completed; and no
- * call of these signals its dependents early.  (What the decodes and the latent
- * stores say of inputs that a kernel of this library writes directly before them
- * holds for these too.)  A wait in the products that runs
- * past its time limit is reported by smla_read_device_status(NULL, ...). */
+ * call of these signals its dependents early.  So they may follow each other and
+ * every other call here in any order, and every other call may follow them, but
+ * for one case: the latent cache's decodes and stores read some inputs before they
+ * wait for the preceding kernel.  Directly before them only linear_mxfp8 may write
+ * these, in bf16 rows of a multiple of 576 values (kv_new, q): these are visible on
+ * the device before the kernel's blocks end.
+ * A wait in the products that runs past its time limit is reported by
+ * smla_read_device_status(NULL, ...). */
 
 #define SMLA_BF16 0
 #define SMLA_F32 1

@@ -306,7 +306,11 @@ def sparse_mla_decode_fp8(q, kv_cache, indices, block_table, req_id_per_token, s
                           num_splits: int = 0, out=None, lse=None, workspace=None, stream=None):
     """FP8 sparse decode.  q bf16 [T,H,576]; kv_cache uint8 [NB,64,656];
     indices int32 [T,K] (logical, <0 = none); block_table int32 [R,MB];
-    req_id_per_token int32 [T].  Returns (out bf16 [T,H,512], lse fp32 [T,H])."""
+    req_id_per_token int32 [T].  Returns (out bf16 [T,H,512], lse fp32 [T,H]).
+    With H < 128, q, indices, block_table and req_id_per_token must not be
+    written by a kernel of this library directly before the call, but by
+    paged_blocks_extend, or by linear_mxfp8 in bf16 rows of a multiple of 576
+    values (so q may be)."""
     return _decode("sparse_mla_decode_fp8", q, kv_cache, indices, block_table, req_id_per_token, sm_scale,
                    num_splits, out, lse, workspace, stream)
 
@@ -551,7 +555,10 @@ def mla_v_up_proj(attn_out, w_uv, out=None, workspace=None, stream=None):
 
 def mla_cache_store_fp8(kv_new, slot_mapping, kv_cache, stream=None):
     """Quantize bf16 [T,576] rows into kv_cache uint8 [NB,64,656] at
-    slot_mapping int64 [T] (<0 skips).  Modifies kv_cache in place."""
+    slot_mapping int64 [T] (<0 skips).  Modifies kv_cache in place.  kv_new and
+    slot_mapping must not be written by a kernel of this library directly before
+    the call, but by paged_blocks_extend, or by linear_mxfp8 in bf16 rows of a
+    multiple of 576 values (so kv_new may be)."""
     import torch
     dev = _dev(kv_new, slot_mapping, kv_cache)
     T = kv_new.shape[0]
@@ -751,7 +758,10 @@ def linear_mxfp8(x, x_scale, weight, weight_scale, bias=None, activation: str = 
     [T,N].  activation: "none", "relu", "silu", "gelu", "gelu_tanh", or "swiglu":
     silu(first half) * second half of a product with 2 N rows.  Returns y in bf16
     [T,N], or, if `quantized` (N a multiple of 32, no residual), its codes and
-    scales as mxfp8_quantize's.  out may be the residual."""
+    scales as mxfp8_quantize's.  out may be the residual.  Rows of a multiple of
+    576 values in bf16 (q, kv_new) may go directly to the latent cache's decode
+    and store; what the other MXFP8 operators write may not be these calls' q,
+    kv_new, indices, tables or slots without another kernel between."""
     args = (x, x_scale, weight, weight_scale, bias, _choice(_ACTIVATIONS, activation, "activation"), residual, quantized,
             out, out_scale)
     call = (_binding or _bound()).linear

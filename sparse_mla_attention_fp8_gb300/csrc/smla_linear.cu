@@ -42,6 +42,9 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t st
   p.ld = a.N;
   const auto even = [](const void* q, int64_t stride) { return stride % 2 == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0; };
   p.pairs = even(a.to.out, a.N) && (!a.to.residual || even(a.to.residual, a.to.residual_stride));
+  // Rows of the latent cache's tokens and of its queries: mla_cache_store_fp8 and sparse_mla_decode_fp8 read these before they
+  // wait for this grid, and begin once its CTAs have ended.  (The fence behind the results takes 0.4 us of a token's 6.0.)
+  p.publish = a.to.out != nullptr && a.N % kDqk == 0;
   p.wide_scales = rows16(a.x_scale, a.x_scale_stride) && rows16(a.w_scale, a.w_scale_stride);
   // Pairs of CTAs where they have enough tiles, 24, or 8 with a short K.  Pairs | the other kernel: K = N = 4096: 16 tiles
   // (256 tokens) 12.8 | 12.3 us, 32 (400) 13.6 | 16.9; K = 8192, N = 1024: 12 tiles (700) 19.9 | 15.1, 24 (1500) 20.7 |

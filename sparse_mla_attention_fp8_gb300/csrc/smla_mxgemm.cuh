@@ -148,6 +148,7 @@ struct MxParams {
   MxEpilogue to;
   int64_t ld;              // features of an output row
   bool pairs;              // bf16 results and residual can be accessed two at a time
+  bool publish;            // results are visible on the device before the CTAs end
   bool wide_scales;        // both sides' scale rows lie on 16-byte boundaries
   // mixture of experts
   const int32_t* ids;      // [T, topk]
@@ -707,6 +708,7 @@ __global__ void __launch_bounds__(kMxThreads, MxLay<NT>::kCtas)
     __syncwarp();
     if (parts > 1) cluster_sync_relaxed();  // no CTA leaves while another reads its sums
   }
+  if (!kExperts && p.publish && warp >= 2) __threadfence();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -461,6 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
     }
+    if (p.publish) __threadfence();
   }
 #undef PAIR_WAIT
   tc_fence_before();

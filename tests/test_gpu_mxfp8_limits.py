@@ -238,3 +238,138 @@ def test_linear_over_its_residual(smla, T, N, K, act):
         held = r.clone()
         assert smla.linear_mxfp8(*x, *w, activation=act, residual=held, out=held).data_ptr() == held.data_ptr()
         assert torch.equal(held, want)
+
+
+# ---------------------------------------------------------------- behind calls that let theirs start early
+
+def behind_early_signals(smla, payloads, shape, dtype, call, rounds=8):
+    """`call(input)` launched directly behind a store that lets its dependents start while a decode before it still runs, and
+    then writes the input: two contents in turn, each with the result it has when it lies there."""
+    def bf16(*s):
+        return torch.randn(s, generator=gen(sum(s)), device="cuda").to(torch.bfloat16)
+
+    T, K, NB = 128, 2048, 64
+    q, read = bf16(T, 16, 576), torch.zeros((NB, 64, 656), dtype=torch.uint8, device="cuda")
+    indices = torch.randint(0, NB * 64, (T, K), generator=gen(1), device="cuda", dtype=torch.int32)
+    table = torch.arange(NB, device="cuda", dtype=torch.int32)[None]
+    request = torch.zeros(T, dtype=torch.int32, device="cuda")
+    cache = torch.zeros((1, 64, 656), dtype=torch.uint8, device="cuda")
+    at = cache[0, 17, 528:656].view(dtype).reshape(shape)  # the position part of a row, which a store copies as it is
+    slots, rows, want = torch.full((1,), 17, device="cuda"), [], []
+    for p in payloads:
+        row = bf16(1, 576)
+        row[0, 512:] = p.contiguous().reshape(-1).view(torch.uint8).view(torch.bfloat16)
+        rows.append(row)
+        got = call(p.contiguous())
+        want.append([t.clone() for t in (got if isinstance(got, (tuple, list)) else [got]) if t is not None])
+    smla.sparse_mla_decode_fp8(q, read, indices, table, request, 0.1)
+    torch.cuda.synchronize()
+    for i in range(2 * rounds):
+        smla.sparse_mla_decode_fp8(q, read, indices, table, request, 0.1)
+        smla.mla_cache_store_fp8(rows[i % 2], slots, cache)
+        got = call(at)
+        got = [t for t in (got if isinstance(got, (tuple, list)) else [got]) if t is not None]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i % 2], strict=True)), i
+
+
+def floats(n, dtype, seed):
+    return [torch.randn(n, generator=gen(seed + i), device="cuda").to(dtype) for i in range(2)]
+
+
+def test_quantize_and_norm_wait_for_their_inputs(smla):
+    bf = torch.bfloat16
+    other, w = floats(64, bf, 1)[0][None], floats(64, bf, 3)[0]
+    behind_early_signals(smla, floats(64, bf, 5), (1, 64), bf, lambda x: smla.mxfp8_quantize(x.reshape(1, 64)))
+    behind_early_signals(smla, floats(32, torch.float32, 5), (1, 32), torch.float32,
+                         lambda x: smla.mxfp8_quantize(x.reshape(1, 32)))
+    behind_early_signals(smla, floats(64, bf, 5), (1, 64), bf,
+                         lambda x: smla.rms_norm_mxfp8(x.reshape(1, 64), w, residual=other, normed=True))
+    behind_early_signals(smla, floats(64, bf, 5), (1, 64), bf,
+                         lambda r: smla.rms_norm_mxfp8(other, w, residual=r.reshape(1, 64)))
+    behind_early_signals(smla, floats(64, bf, 5), (64,), bf, lambda v: smla.rms_norm_mxfp8(other, v, normed=True))
+    behind_early_signals(smla, floats(32, torch.float32, 5), (32,), torch.float32,
+                         lambda v: smla.rms_norm_mxfp8(other[:, :32].contiguous(), v, normed=True))
+
+
+@pytest.mark.parametrize("T,K", [(1, 128), (2500, 128)])
+def test_linear_waits_for_its_inputs(smla, T, K):
+    """Both kernels: the one of few tokens and the pairs."""
+    g = gen(T)
+    x, w = matrix(g, T, K), matrix(g, 64, K)
+    for bias in (torch.bfloat16, torch.float32):
+        N = 64 if bias == torch.bfloat16 else 32
+        part = (w[0][:N], w[1][:N])
+        behind_early_signals(smla, floats(N, bias, 1), (N,), bias, lambda b: smla.linear_mxfp8(*x, *part, bias=b))
+    codes = [matrix(g, 1, 128)[0] for _ in range(2)]
+    behind_early_signals(smla, codes, (1, 128), torch.uint8, lambda c: smla.linear_mxfp8(c.reshape(1, 128), x[1][:1], *w))
+    scales = [torch.randint(112, 118, (32, 4), generator=g, device="cuda", dtype=torch.uint8) for _ in range(2)]
+    some = matrix(g, 32, 128)[0]
+    behind_early_signals(smla, scales, (32, 4), torch.uint8, lambda s: smla.linear_mxfp8(some, s, *w))
+    behind_early_signals(smla, scales, (32, 4), torch.uint8, lambda s: smla.linear_mxfp8(*x, some, s))
+    behind_early_signals(smla, floats(64, torch.bfloat16, 3), (1, 64), torch.bfloat16,
+                         lambda r: smla.linear_mxfp8(x[0][:1], x[1][:1], *w, residual=r.reshape(1, 64)))
+
+
+def test_route_and_experts_wait_for_their_inputs(smla):
+    g = gen(2)
+    f32, E = torch.float32, 32
+    logits = torch.randn((3, E), generator=g, device="cuda")
+    behind_early_signals(smla, floats(E, f32, 1), (1, E), f32, lambda v: smla.moe_route(v.reshape(1, E), 6))
+    behind_early_signals(smla, floats(E, f32, 1), (E,), f32, lambda b: smla.moe_route(logits, 6, scoring="sigmoid", bias=b))
+    x, w13, w2 = matrix(g, 4, 128), matrix(g, E, 128, 128), matrix(g, E, 128, 64)
+    ids = [torch.randint(0, E, (4, 8), generator=g, device="cuda").int() for _ in range(2)]
+    share = [torch.rand((4, 8), generator=g, device="cuda") for _ in range(2)]
+    behind_early_signals(smla, ids, (4, 8), torch.int32, lambda i: smla.moe_mxfp8(*x, i.reshape(4, 8), share[0], *w13, *w2))
+    behind_early_signals(smla, share, (4, 8), f32, lambda p: smla.moe_mxfp8(*x, ids[0], p.reshape(4, 8), *w13, *w2))
+
+
+# ---------------------------------------------------------------- with the latent cache's attention
+
+@pytest.mark.parametrize("T,hidden", [(3, 512), (40, 1024), (1500, 256)])
+def test_products_around_the_latent_attention(smla, T, hidden):
+    """kv_new and q by products, directly followed by the store and the decode that read them early, whose results are
+    quantized for the output projection; step after step into the same buffers.  The same bits as with the device idle
+    between the calls, and every product within its bound."""
+    g = gen(T)
+    H, K, NB = 16, 64, 40
+    w_kv, w_q, w_o = matrix(g, 576, hidden), matrix(g, H * 576, hidden), matrix(g, hidden, H * 512)
+    steps = [torch.randn((T, hidden), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(4)]
+    table = torch.arange(NB, device="cuda", dtype=torch.int32)[None]
+    request = torch.zeros(T, dtype=torch.int32, device="cuda")
+    slots = torch.randperm(NB * 64, generator=g, device="cuda")[:T]
+    indices = slots[torch.randint(0, T, (T, K), generator=g, device="cuda")].int()
+
+    def run(between):
+        cache = torch.zeros((NB, 64, 656), dtype=torch.uint8, device="cuda")
+        kv, q = (torch.full(s, float("nan"), dtype=torch.bfloat16, device="cuda") for s in ((T, 576), (T, H * 576)))
+        got = []
+        torch.cuda.synchronize()
+        for s in steps:
+            x = smla.mxfp8_quantize(s)
+            between()
+            smla.linear_mxfp8(*x, *w_kv, out=kv)
+            between()
+            smla.mla_cache_store_fp8(kv, slots, cache)
+            between()
+            smla.linear_mxfp8(*x, *w_q, out=q)
+            between()
+            out, lse = smla.sparse_mla_decode_fp8(q.view(T, H, 576), cache, indices, table, request, 0.002)
+            between()
+            a = smla.mxfp8_quantize(out.view(T, H * 512))
+            between()
+            smla.linear_mxfp8(*a, *w_o, residual=s)
+            got += [cache.clone(), out, lse, *a]
+        torch.cuda.synchronize()
+        assert smla.read_device_status() == 0
+        # the last step's products
+        for y, xv, w in ((kv, x, w_kv), (q, x, w_q)):
+            z, off = ref.linear(ref.values(*xv), ref.values(*w), None, "none", None)
+            within(y, z, off + 2.0 ** -8 * (z.abs() + off))
+        assert torch.equal(ref.values(*a), ref.rounded(out.view(T, H * 512).double()))
+        return got
+
+    want = run(torch.cuda.synchronize)
+    assert all(torch.isfinite(t.float()).all() for t in want[1::5])
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want, strict=True))
