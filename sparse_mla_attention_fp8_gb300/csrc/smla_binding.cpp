@@ -135,6 +135,12 @@ float number(PyObject* o) {
   return (float)v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused();
+  return v == 1;
+}
+
 int size(int64_t v, const char* name) {
   if (v > INT_MAX) refuse("%s: %lld is out of range", name, (long long)v);
   return (int)v;
@@ -514,7 +520,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     Matrix res{};
     if (a[3] != Py_None) res = matrix_of(a[3], "residual", at::kBFloat16, T, K, dev);
-    const bool codes_too = PyObject_IsTrue(a[5]) == 1;
+    const bool codes_too = truth(a[5]);
     if (!codes_too && (a[7] != Py_None || a[8] != Py_None)) refuse("codes and scales: given, but not asked for (quantized)");
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index);
     Quantized q{};
@@ -569,7 +575,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index);
     Quantized q{};
     at::Tensor out;
-    const bool coded = PyObject_IsTrue(a[7]) == 1;
+    const bool coded = truth(a[7]);
     if (!coded && a[9] != Py_None) refuse("out_scale: given, but not asked for (quantized)");
     if (coded)
       q = quantized(a[8], a[9], "out", "out_scale", T, N, dev);
@@ -599,7 +605,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor ids = a[8] == Py_None ? made({T, topk}, at::kInt, dev) : arg(a[8], "ids", at::kInt, {2, {T, topk}}, dev);
     const at::Tensor w =
         a[9] == Py_None ? made({T, topk}, at::kFloat, dev) : arg(a[9], "weights", at::kFloat, {2, {T, topk}}, dev);
-    check(g_route(x.data_ptr(), type, bias, integer(a[2], "scoring"), PyObject_IsTrue(a[4]) == 1, number(a[5]),
+    check(g_route(x.data_ptr(), type, bias, integer(a[2], "scoring"), truth(a[4]), number(a[5]),
                   integer(a[6], "num_groups"), integer(a[7], "topk_groups"), data<int32_t>(ids), data<float>(w), T, E, topk,
                   stream_of(dev)),
           "moe_route");

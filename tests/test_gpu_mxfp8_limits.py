@@ -373,3 +373,17 @@ def test_products_around_the_latent_attention(smla, T, hidden):
     assert all(torch.isfinite(t.float()).all() for t in want[1::5])
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want, strict=True))
+
+
+# ---------------------------------------------------------------- refusals
+
+def test_flags_without_a_truth_value(smla):
+    """The error of asking for it is the call's."""
+    g, both = gen(0), torch.tensor([True, False])
+    x, w = matrix(g, 2, 64), matrix(g, 32, 64)
+    calls = [lambda: smla.linear_mxfp8(*x, *w, quantized=both), lambda: smla.moe_route(torch.zeros((2, 8), device="cuda"), 2, renormalize=both),
+             lambda: smla.rms_norm_mxfp8(torch.zeros((2, 64), device="cuda", dtype=torch.bfloat16), quantized=both)]
+    for call in calls:
+        with pytest.raises(RuntimeError, match="ambiguous") as e:
+            call()
+        assert e.type is RuntimeError
