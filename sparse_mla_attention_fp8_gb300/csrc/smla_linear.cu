@@ -62,8 +62,11 @@ cudaError_t launch_mx_linear(const MxLinearArgs& a, int num_sms, cudaStream_t st
       default: return launch_pair<SMLA_ACT_SWIGLU>(a, p, num_sms, stream);
     }
   }
-  return a.to.activation == SMLA_ACT_SWIGLU ? launch_few<kGated>(a, p, num_sms, stream)
-                                            : launch_few<kLinear>(a, p, num_sms, stream);
+  switch (a.to.activation) {
+    case SMLA_ACT_SWIGLU: return launch_few<kGated>(a, p, num_sms, stream);
+    case SMLA_ACT_GELU: return launch_few<kGelu>(a, p, num_sms, stream);
+    default: return launch_few<kLinear>(a, p, num_sms, stream);
+  }
 }
 
 cudaError_t mx_linear_wait_check(cudaStream_t stream) { return mx_wait_check(stream); }

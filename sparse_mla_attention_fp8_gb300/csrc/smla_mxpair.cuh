@@ -394,7 +394,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (lane == 0) mbar_arrive_cluster_relaxed(empty);
       auto result = [&](int c) {
         const float z = __uint_as_float(w[c]) + bias[0];
-        return NA == 2 ? silu(z) * (__uint_as_float(w[(NA - 1) * kMine + c]) + bias[NA - 1]) : activate(ACT, z);
+        return NA == 2 ? silu(z) * (__uint_as_float(w[(NA - 1) * kMine + c]) + bias[NA - 1])
+                       : ACT == SMLA_ACT_GELU ? gelu(z) : activate(ACT, z);
       };
       // 16 tokens at a time without a branch, so that their chains of operations overlap
       constexpr int kAtOnce = 16;
