@@ -473,7 +473,8 @@ int linear_mxfp8(const uint8_t* x, int64_t x_stride, const uint8_t* x_scale, int
  *   s = softmax over the E logits, or sigmoid of each
  *   the topk experts with the largest s + bias are taken, in that order, equal ones by their index; with
  *   num_groups > 1 only those of the topk_groups groups (of E / num_groups consecutive experts, 2 or more)
- *   whose two largest s + bias have the largest sums, equal ones by their index
+ *   whose two largest s + bias have the largest sums, equal ones by their index (a group in which fewer than
+ *   two experts are unmasked is not kept)
  *   ids     int32 [T, topk]
  *   weights fp32 [T, topk]: s of each, divided by their sum if renormalize, times scale
  * bias (fp32 [E], finite) may be NULL.  Without bias and groups experts are ordered by their logits.  A logit

@@ -7,9 +7,9 @@
 // more cost little beside that read, which bounds both products.  The second one is
 // launched while the first runs and copies its first weights meanwhile.
 //
-// Measured, 64 experts of 3 x 4096 x 1024, 8 a token: one token 25.2 us (104 MB;
-// the first product's last CTA ends after 15.5 us, the second's after 24), 48 tokens
-// 145 us (805 MB, 5.5 TB/s).  The one token is bound by what follows one another:
+// Measured, 64 experts of 3 x 4096 x 1024, 8 a token: one token 25.3 us (104 MB;
+// the first product's last CTA ends after 15.4 us, the second's after 24.5), 48 tokens
+// 143 to 146 us (805 MB, 5.5 TB/s).  The one token is bound by what follows one another:
 // ids, weights, sums of a cluster, the launch's dependency, h, sums.
 #include "smla_mxgemm.cuh"
 
